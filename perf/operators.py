@@ -26,7 +26,7 @@ own = False
 
 EPS = 1e-6
 E4M3_MAX = 448.0
-MIN_EXP, MAX_EXP = -64, 120  # range of a cached row's scale exponent
+MIN_EXP, MAX_EXP = -63, 63  # range of a cached row's scale exponent
 
 _DT = {"bf16": torch.bfloat16, "f32": torch.float32}
 
