@@ -58,6 +58,8 @@ typedef enum { KDA_DTYPE_F32 = 0, KDA_DTYPE_BF16 = 1 } kda_dtype;
 #define KDA_DEV_SEQ_OOB 2    /* cu_seqlens not non-decreasing within [0, T], or a sequence longer than max_seqlen */
 #define KDA_DEV_TIMEOUT 4    /* a bounded wait inside a kernel gave up */
 #define KDA_DEV_ACCEPT_OOB 8 /* an accepted length outside [0, W] */
+#define KDA_DEV_POS_OOB 16   /* a token position outside the rotation table */
+#define KDA_DEV_PAGE_OOB 32  /* a page id or a token slot outside the paged cache */
 
 /* Human-readable name of a status code (static storage). */
 const char* kda_status_string(kda_status s);
@@ -92,10 +94,11 @@ kda_status kda_set_test_fault(int fault);
  * kda_set_debug_checks(on) / kda_debug_checks() -- switch / read the debug mode (process-wide; initially on
  *   when the environment variable KDA_DEBUG_CHECKS is set to a value other than 0).  In debug mode the calls
  *   that take slot ids (kda_state_copy, kda_decode_step, kda_verify_replay, kda_prefill_varlen,
- *   kda_prefill_segmented, kda_cfbi_prefill, kda_cfbi_decode, kda_fused_decode) copy their ids to the host
- *   on their stream, wait for the copy (so the call is no longer asynchronous and cannot be captured in a
+ *   kda_prefill_segmented, kda_cfbi_prefill, kda_cfbi_decode, kda_fused_decode, kda_kv_write) copy their ids to
+ *   the host on their stream, wait for the copy (so the call is no longer asynchronous and cannot be captured in a
  *   CUDA graph), and return KDA_ERR_INVALID_ARG with nothing enqueued when:
- *     - two ids of the call are equal (kda_state_copy: two destination ids; a source may feed several);
+ *     - two ids of the call are equal (kda_state_copy: two destination ids; a source may feed several;
+ *       kda_kv_write: two token slots that are not negative);
  *     - kda_state_copy with src_pool == dst_pool: a destination id is also a source id;
  *     - a prefill with snapshots: two extra_slot_ids are equal, or (extra_pool == pool) an extra slot is
  *       also one of the sequences' slots.
@@ -494,6 +497,163 @@ kda_status kda_kcp_scan(const float* frags, int32_t P, int H, int dk, int dv, co
                         int32_t* dev_status, kda_stream_t stream);
 kda_status kda_kcp_outputs(const kda_prefill_args* a, int32_t segment_len, const float* entries,
                            kda_stream_t stream);
+
+/*
+ * Softmax-attention layers beside the KDA layers
+ * ----------------------------------------------
+ * A hybrid model interleaves KDA layers with layers that attend over a key/value cache ("Kimi K3:
+ * Architecture and SGLang Day-0 Support", layer layout: 69 KDA and 24 full-attention layers).  These calls are
+ * what such a layer does to a token between its projections: the per-head norm of queries and keys (with a
+ * position rotation where the model has one), the write into a paged cache, and the attention of the newest
+ * tokens over that cache.  Queries have Hq heads, keys and values Hkv, and query head h attends with
+ * key/value head h / (Hq / Hkv).  Head sizes d in {16, 32, 64, 128}.  In these calls index arrays (positions,
+ * slots, block_table, seq_lens) need their natural alignment only; everything else keeps the 16-byte rule,
+ * token strides included (in elements, and at least the size of the token's row).
+ */
+
+/*
+ * kda_qk_norm_rope -- per-head RMS norm of queries and keys and their position rotation, in one pass.
+ * Per row x of d channels with weight w:  y = R(p) (x * r * w),  r = 1 / sqrt(mean_c x_c^2 + eps).
+ * R(p) turns channel pairs (a, b) of the first `rot` channels by the token's angles,
+ *   (a, b) -> (a cos - b sin, a sin + b cos), pair i with cos[p][i], sin[p][i], i < rot / 2;
+ * pair i is channels (i, i + rot / 2), or (2i, 2i + 1) when `interleaved`.  rot = 0: no rotation (cos, sin and
+ * positions unused).  With w = 1 / sqrt(d) and eps = 1e-6 / d this is the unit-length normalisation of the KDA
+ * layers' queries and keys.
+ */
+typedef struct {
+  const void* q;            /* [T][Hq][d] in_dtype, tokens q_stride elements apart */
+  const void* k;            /* [T][Hkv][d] in_dtype, tokens k_stride elements apart */
+  int64_t q_stride, k_stride;
+  kda_dtype in_dtype;
+  const float* q_weight;    /* [d] */
+  const float* k_weight;    /* [d] */
+  const float* cos;         /* [num_positions][rot / 2], NULL when rot = 0 */
+  const float* sin;         /* [num_positions][rot / 2], NULL when rot = 0 */
+  const int32_t* positions; /* int32[T], NULL when rot = 0 */
+  int32_t num_positions;
+  int rot;                  /* channels rotated: a multiple of 16 in [0, d] */
+  int interleaved;
+  float eps;                /* >= 0 */
+  int64_t T;
+  int Hq, Hkv, d;
+  void* q_out;              /* [T][Hq][d] out_dtype; may be q itself (same type and stride) */
+  void* k_out;              /* [T][Hkv][d] out_dtype; may be k itself */
+  int64_t q_out_stride, k_out_stride;
+  kda_dtype out_dtype;
+  int32_t* dev_status;      /* optional int32[2]; the work counter counts (token x head) rows */
+} kda_qk_norm_rope_args;
+
+/* sizeof(kda_qk_norm_rope_args), so a binding can check its mirror of the struct. */
+size_t kda_qk_norm_rope_args_bytes(void);
+
+/* kda_qk_norm_rope -- enqueue the forward.  A position outside [0, num_positions) sets KDA_DEV_POS_OOB and
+ * that token's rows are not written. */
+kda_status kda_qk_norm_rope(const kda_qk_norm_rope_args* a, kda_stream_t stream);
+
+/* Workspace of kda_qk_norm_rope_backward: 608 * 2 * d * 4 bytes of partial weight gradients. */
+size_t kda_qk_norm_rope_backward_workspace_size(int64_t T, int Hq, int Hkv, int d);
+
+/*
+ * kda_qk_norm_rope_backward -- gradients of sum <d_q_out, q_out> + <d_k_out, k_out>.  With the row's
+ * g = R(p)^T dy:  dw = sum over rows of g * x * r,   dx = r (g w - x r^2 mean_c(g w x)).
+ * `a` describes the forward (q, k, weights, rotation); a->q_out, a->k_out, their strides and a->out_dtype
+ * describe dq and dk here (in place over the incoming gradients is allowed where type and stride agree).
+ *   d_q_out [T][Hq][d], d_k_out [T][Hkv][d] in grad_dtype, contiguous;
+ *   dq_weight, dk_weight [d] fp32, overwritten (not accumulated into); summed in a fixed order;
+ *   workspace: kda_qk_norm_rope_backward_workspace_size bytes of device scratch.
+ * A token whose position is out of range is flagged as in the forward: its gradients are not written and it
+ * adds nothing to the weights' gradients.
+ */
+kda_status kda_qk_norm_rope_backward(const kda_qk_norm_rope_args* a, const void* d_q_out, const void* d_k_out,
+                                     kda_dtype grad_dtype, float* dq_weight, float* dk_weight, void* workspace,
+                                     size_t workspace_bytes, kda_stream_t stream);
+
+/*
+ * The paged key/value cache
+ * -------------------------
+ * k_pages, v_pages [num_pages][Hkv][page_size][d] in a cache type; page_size a positive multiple of 16.  A
+ * token's slot is page * page_size + offset.
+ *   KDA_CACHE_BF16: rows held as bf16 (fp32 inputs round to nearest even); no scales (NULL).
+ *   KDA_CACHE_E4M3: rows held as 8-bit e4m3 codes c with one fp32 scale per (token, head),
+ *     k_scales, v_scales [num_pages][Hkv][page_size]; the row stands for c * scale.  kda_kv_write takes
+ *     scale = 2^e with the least e in [-63, 63] for which max|x| <= 448 * 2^e (a zero row: scale 1), so scaling
+ *     is exact and the only rounding is the one to e4m3 (nearest even); a row read back and written again
+ *     keeps its values.  NaN stays NaN and is left out of the maximum; an infinity, or a value beyond
+ *     448 * 2^63, becomes 448 * 2^63.  Scales written by other code must be positive, within [2^-63, 2^63].
+ */
+typedef enum { KDA_CACHE_BF16 = 0, KDA_CACHE_E4M3 = 1 } kda_cache_type;
+
+typedef struct {
+  void* k_pages;
+  void* v_pages;
+  float* k_scales; /* NULL for KDA_CACHE_BF16 */
+  float* v_scales;
+  kda_cache_type type;
+  int32_t num_pages;
+  int page_size;
+  int Hkv, d;
+} kda_kv_cache;
+
+/* sizeof(kda_kv_cache), so a binding can check its mirror of the struct. */
+size_t kda_kv_cache_bytes(void);
+
+/*
+ * kda_kv_write -- cache row slots[t] receives token t.
+ *   k, v [T][Hkv][d] in_dtype, tokens k_stride / v_stride elements apart; slots int64[T], distinct.
+ * A negative slot skips its token; a slot >= num_pages * page_size sets KDA_DEV_PAGE_OOB and skips it.  The
+ * debug checks (kda_set_debug_checks) cover the slots being distinct.  The work counter counts (token x
+ * key/value head) rows written.
+ */
+kda_status kda_kv_write(const void* k, const void* v, int64_t k_stride, int64_t v_stride, kda_dtype in_dtype,
+                        int64_t T, const int64_t* slots, const kda_kv_cache* cache, int32_t* dev_status,
+                        kda_stream_t stream);
+
+/*
+ * kda_kv_read -- token t of k_out, v_out receives cache row slots[t] (a shared prefix brought back for a chunk of
+ * prefill).  k_out, v_out [T][Hkv][d] out_dtype, contiguous; slots int64[T], repeats allowed.  A negative slot
+ * gives a zero row; a slot >= num_pages * page_size sets KDA_DEV_PAGE_OOB and gives a zero row.
+ */
+kda_status kda_kv_read(const kda_kv_cache* cache, const int64_t* slots, int64_t T, void* k_out, void* v_out,
+                       kda_dtype out_dtype, int32_t* dev_status, kda_stream_t stream);
+
+/*
+ * kda_paged_attention -- attention of the W newest tokens of each request over its cached tokens.
+ * Request b has seq_lens[b] = L tokens in the cache (the W new ones included: write them first), at pages
+ * block_table[b][0 .. ceil(L / page_size)).  Query w of the window sits at position p = L - W + w and sees
+ * positions max(0, p - window + 1) .. p (window = 0: 0 .. p).  Per query head, with x = scale * q.k
+ * (softcap > 0: softcap * tanh(x / softcap)):
+ *   out = sum_j exp(x_j - m) v_j / sum_j exp(x_j - m),   lse = m + log sum_j exp(x_j - m).
+ * W = 1 is a decode step, W > 1 the draft window of kda_verify.  A query that sees nothing (L = 0, or p < 0)
+ * gives a zero row and lse = -infinity.  What unseen cache rows hold does not matter, NaN included.
+ */
+typedef struct {
+  const void* q;              /* [B][W][Hq][d] q_dtype */
+  kda_dtype q_dtype;
+  int B, W, Hq;
+  kda_kv_cache cache;         /* read only here */
+  const int32_t* block_table; /* int32[B][max_pages] */
+  int32_t max_pages;          /* pages a request may have: the table's row length */
+  const int32_t* seq_lens;    /* int32[B] */
+  float scale;                /* finite; 1 / sqrt(d) in most models */
+  float softcap;              /* 0: none */
+  int32_t window;             /* 0: everything before the query */
+  void* out;                  /* [B][W][Hq][d] out_dtype */
+  kda_dtype out_dtype;
+  float* lse;                 /* [B][W][Hq] fp32, or NULL */
+  void* workspace;            /* >= kda_paged_attention_workspace_size bytes of device scratch */
+  size_t workspace_bytes;
+  int32_t* dev_status;        /* optional int32[2]; the work counter counts query rows (request x token x head) */
+} kda_paged_attention_args;
+
+/* sizeof(kda_paged_attention_args), so a binding can check its mirror of the struct. */
+size_t kda_paged_attention_args_bytes(void);
+
+/* Scratch for the partial results of requests whose cache is split; its size does not depend on the lengths. */
+size_t kda_paged_attention_workspace_size(int B, int W, int Hq, int Hkv, int d);
+
+/* kda_paged_attention -- enqueue it.  A length outside [0, max_pages * page_size] sets KDA_DEV_SEQ_OOB and counts
+ * as 0; a page id outside [0, num_pages) sets KDA_DEV_PAGE_OOB and its tokens are seen by no query. */
+kda_status kda_paged_attention(const kda_paged_attention_args* a, kda_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -16,7 +16,7 @@ from . import _build
 
 __all__ = [
     "KdaError", "load", "lib_path", "KDA_OK", "KDA_DEV_SLOT_OOB", "KDA_DEV_SEQ_OOB", "KDA_DEV_TIMEOUT",
-    "KDA_DEV_ACCEPT_OOB", "kda_status_string", "kda_version", "kda_state_bytes_per_head", "kda_state_copy",
+    "KDA_DEV_ACCEPT_OOB", "KDA_DEV_POS_OOB", "KDA_DEV_PAGE_OOB", "kda_status_string", "kda_version", "kda_state_bytes_per_head", "kda_state_copy",
     "kda_decode_step", "kda_replay_bytes", "kda_verify", "kda_verify_replay", "kda_prefill_varlen",
     "kda_prefill_workspace_size", "kda_prefill_segmented", "kda_segmented_workspace_size",
     "kda_segment_fragments", "kda_fragment_scan", "kda_segment_outputs", "kda_prefill_segmented_noalloc",
@@ -24,12 +24,15 @@ __all__ = [
     "kda_cfbi_prefill_chunked_workspace_size", "kda_cfbi_prefill_chunked",
     "kda_cfbi_decode", "kda_backward_workspace_size", "kda_prefill_backward", "kda_fused_decode",
     "kda_kcp_fragments", "kda_kcp_scan", "kda_kcp_outputs", "kda_check_slot_ids", "kda_set_debug_checks",
+    "kda_qk_norm_rope", "kda_qk_norm_rope_backward", "kda_qk_norm_rope_backward_workspace_size", "kda_kv_write",
+    "kda_kv_read", "kda_paged_attention", "kda_paged_attention_workspace_size",
     "kda_debug_checks", "kda_set_test_fault", "KDA_TEST_FAULT_NONE", "KDA_TEST_FAULT_STALL_RECORD_INPUTS", "CFBI_CHUNK", "CFBI_ROW_FLOATS", "EXPORTED_SYMBOLS",
 ]
 
 KDA_OK = 0
 KDA_TEST_FAULT_NONE, KDA_TEST_FAULT_STALL_RECORD_INPUTS = 0, 1
 KDA_DEV_SLOT_OOB, KDA_DEV_SEQ_OOB, KDA_DEV_TIMEOUT, KDA_DEV_ACCEPT_OOB = 1, 2, 4, 8
+KDA_DEV_POS_OOB, KDA_DEV_PAGE_OOB = 16, 32
 F32, BF16 = 0, 1
 CFBI_CHUNK, CFBI_ROW_FLOATS = 16, 420  # KDA_CFBI_CHUNK, KDA_CFBI_ROW_FLOATS
 
@@ -44,6 +47,9 @@ EXPORTED_SYMBOLS = (
     "kda_cfbi_decode", "kda_backward_args_bytes", "kda_backward_workspace_size", "kda_prefill_backward",
     "kda_fused_decode_args_bytes", "kda_fused_decode", "kda_kcp_fragments", "kda_kcp_scan", "kda_kcp_outputs",
     "kda_check_slot_ids", "kda_set_debug_checks", "kda_debug_checks", "kda_set_test_fault",
+    "kda_qk_norm_rope_args_bytes", "kda_qk_norm_rope", "kda_qk_norm_rope_backward_workspace_size",
+    "kda_qk_norm_rope_backward", "kda_kv_cache_bytes", "kda_kv_write", "kda_kv_read",
+    "kda_paged_attention_args_bytes", "kda_paged_attention_workspace_size", "kda_paged_attention",
 )
 
 
@@ -91,6 +97,40 @@ class FusedDecodeArgs(ctypes.Structure):
         ("num_slots", ctypes.c_int32), ("slot_ids", ctypes.c_void_p), ("conv_state", ctypes.c_void_p),
         ("conv_w", ctypes.c_void_p), ("norm_w", ctypes.c_void_p), ("norm_eps", ctypes.c_float),
         ("out", ctypes.c_void_p), ("out_dtype", ctypes.c_int), ("dev_status", ctypes.c_void_p),
+    ]
+
+
+class QkNormRopeArgs(ctypes.Structure):
+    """Mirror of kda_qk_norm_rope_args."""
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+        ("in_dtype", ctypes.c_int), ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+        ("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+        ("num_positions", ctypes.c_int32), ("rot", ctypes.c_int), ("interleaved", ctypes.c_int),
+        ("eps", ctypes.c_float), ("T", ctypes.c_int64), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int),
+        ("d", ctypes.c_int), ("q_out", ctypes.c_void_p), ("k_out", ctypes.c_void_p),
+        ("q_out_stride", ctypes.c_int64), ("k_out_stride", ctypes.c_int64), ("out_dtype", ctypes.c_int),
+        ("dev_status", ctypes.c_void_p),
+    ]
+
+
+class KvCache(ctypes.Structure):
+    """Mirror of kda_kv_cache."""
+    _fields_ = [
+        ("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+        ("v_scales", ctypes.c_void_p), ("type", ctypes.c_int), ("num_pages", ctypes.c_int32),
+        ("page_size", ctypes.c_int), ("Hkv", ctypes.c_int), ("d", ctypes.c_int),
+    ]
+
+
+class PagedAttentionArgs(ctypes.Structure):
+    """Mirror of kda_paged_attention_args."""
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("q_dtype", ctypes.c_int), ("B", ctypes.c_int), ("W", ctypes.c_int),
+        ("Hq", ctypes.c_int), ("cache", KvCache), ("block_table", ctypes.c_void_p), ("max_pages", ctypes.c_int32),
+        ("seq_lens", ctypes.c_void_p), ("scale", ctypes.c_float), ("softcap", ctypes.c_float),
+        ("window", ctypes.c_int32), ("out", ctypes.c_void_p), ("out_dtype", ctypes.c_int), ("lse", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t), ("dev_status", ctypes.c_void_p),
     ]
 
 
@@ -154,6 +194,16 @@ def load(build_if_missing: bool = False):
         "kda_set_debug_checks": (None, [c_int]),
         "kda_debug_checks": (c_int, []),
         "kda_set_test_fault": (c_int, [c_int]),
+        "kda_qk_norm_rope_args_bytes": (sz, []),
+        "kda_qk_norm_rope": (c_int, [ctypes.POINTER(QkNormRopeArgs), vp]),
+        "kda_qk_norm_rope_backward_workspace_size": (sz, [i64, c_int, c_int, c_int]),
+        "kda_qk_norm_rope_backward": (c_int, [ctypes.POINTER(QkNormRopeArgs), vp, vp, c_int, vp, vp, vp, sz, vp]),
+        "kda_kv_cache_bytes": (sz, []),
+        "kda_kv_write": (c_int, [vp, vp, i64, i64, c_int, i64, vp, ctypes.POINTER(KvCache), vp, vp]),
+        "kda_kv_read": (c_int, [ctypes.POINTER(KvCache), vp, i64, vp, vp, c_int, vp, vp]),
+        "kda_paged_attention_args_bytes": (sz, []),
+        "kda_paged_attention_workspace_size": (sz, [c_int, c_int, c_int, c_int, c_int]),
+        "kda_paged_attention": (c_int, [ctypes.POINTER(PagedAttentionArgs), vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -165,6 +215,10 @@ def load(build_if_missing: bool = False):
         raise RuntimeError("kda_backward_args layout mismatch between include/kda.h and the binding")
     if lib.kda_fused_decode_args_bytes() != ctypes.sizeof(FusedDecodeArgs):
         raise RuntimeError("kda_fused_decode_args layout mismatch between include/kda.h and the binding")
+    for name, mirror in (("kda_qk_norm_rope_args", QkNormRopeArgs), ("kda_kv_cache", KvCache),
+                         ("kda_paged_attention_args", PagedAttentionArgs)):
+        if getattr(lib, name + "_bytes")() != ctypes.sizeof(mirror):
+            raise RuntimeError(f"{name} layout mismatch between include/kda.h and the binding")
     _lib = lib
     return lib
 
@@ -673,3 +727,176 @@ def kda_kcp_outputs(q, k, v, g, beta, cu_seqlens, max_seqlen, pool, slot_ids, ou
     a = _prefill_struct(q, k, v, g, beta, cu_seqlens, max_seqlen, pool, slot_ids, out, workspace=workspace,
                         dev_status=dev_status)
     _ok("kda_kcp_outputs", load().kda_kcp_outputs(ctypes.byref(a), int(segment_len), _p(entries), _stream(stream)))
+
+
+# ---------------------------------------------------------------- softmax-attention layers
+
+_I64 = (torch.int64,)
+_CACHE_TYPES = {torch.bfloat16: 0, torch.float8_e4m3fn: 1}  # KDA_CACHE_BF16, KDA_CACHE_E4M3
+
+
+def _row_stride(name, t):
+    """Elements between the tokens of t [T, H, d], whose heads and channels must be contiguous: a tensor of its own
+    or a column block of a fused projection's output."""
+    T, H, d = t.shape
+    st, sh, sc = t.stride()
+    if not t.is_cuda or (sc != 1 and d > 1) or (sh != d and H > 1):
+        raise ValueError(f"{name}: expected contiguous CUDA tensors, or heads and channels contiguous within a token")
+    return st if T > 1 else H * d
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _qk_norm_args(q, k, q_weight, k_weight, q_out, k_out, out_names, cos, sin, positions, eps, interleaved, dev_status,
+                  grads=(), weight_grads=()):
+    T, Hq, d = _rank("q", q, 3)
+    _need("q", q, (T, Hq, d), _IN)
+    _need("k", k, (T, None, d), (q.dtype,))
+    Hkv = k.shape[1]
+    _need("q_weight", q_weight, (d,), _FP)
+    _need("k_weight", k_weight, (d,), _FP)
+    _need(out_names[0], q_out, (T, Hq, d), _IN)
+    _need(out_names[1], k_out, (T, Hkv, d), (q_out.dtype,))
+    n = rot = 0
+    if cos is not None or sin is not None or positions is not None:
+        if cos is None or sin is None or positions is None:
+            raise ValueError("cos, sin and positions go together (all None: no rotation)")
+        n, half = _rank("cos", cos, 2)
+        rot = 2 * half
+        _need("cos", cos, (n, half), _FP)
+        _need("sin", sin, (n, half), _FP)
+        _need("positions", positions, (T,), _I32)
+        if rot > d or rot % 16:
+            raise ValueError(f"cos: expected angles of a multiple of 8 channel pairs within d = {d}, got {half}")
+    if grads:
+        d_q_out, d_k_out = grads
+        _need("d_q_out", d_q_out, (T, Hq, d), _IN)
+        _need("d_k_out", d_k_out, (T, Hkv, d), (d_q_out.dtype,))
+        _need("dq_weight", weight_grads[0], (d,), _FP)
+        _need("dk_weight", weight_grads[1], (d,), _FP)
+    _need_status(dev_status)
+    _check(q_weight, k_weight, cos, sin, positions, dev_status, *grads, *weight_grads)
+    return QkNormRopeArgs(q.data_ptr(), k.data_ptr(), _row_stride("q", q), _row_stride("k", k), _dt(q),
+                          q_weight.data_ptr(), k_weight.data_ptr(), _ptr(cos), _ptr(sin), _ptr(positions), n, rot,
+                          bool(interleaved), eps, T, Hq, Hkv, d, q_out.data_ptr(), k_out.data_ptr(),
+                          _row_stride(out_names[0], q_out), _row_stride(out_names[1], k_out), _dt(q_out),
+                          _ptr(dev_status))
+
+
+def kda_qk_norm_rope(q, k, q_weight, k_weight, q_out, k_out, cos=None, sin=None, positions=None, eps=1e-6,
+                     interleaved=False, dev_status=None, stream=None):
+    """RMS norm of every query and key head and their position rotation, in one pass.
+
+    q, q_out [T, Hq, d]; k, k_out [T, Hkv, d], each with any distance between tokens (column blocks of a fused
+    projection's output, say), q_out and k_out may be q and k; weights [d] fp32; cos, sin [positions, rot / 2] fp32
+    and positions int32 [T], or all None for no rotation.
+    """
+    a = _qk_norm_args(q, k, q_weight, k_weight, q_out, k_out, ("q_out", "k_out"), cos, sin, positions, eps, interleaved,
+                      dev_status)
+    _ok("kda_qk_norm_rope", load().kda_qk_norm_rope(a, _stream(stream)))
+
+
+def kda_qk_norm_rope_backward_workspace_size(T: int, Hq: int, Hkv: int, d: int) -> int:
+    return load().kda_qk_norm_rope_backward_workspace_size(T, Hq, Hkv, d)
+
+
+def kda_qk_norm_rope_backward(d_q_out, d_k_out, q, k, q_weight, k_weight, dq, dk, dq_weight, dk_weight, workspace,
+                              cos=None, sin=None, positions=None, eps=1e-6, interleaved=False, dev_status=None,
+                              stream=None):
+    """Gradients of sum <d_q_out, q_out> + <d_k_out, k_out> through kda_qk_norm_rope of (q, k, weights).
+
+    d_q_out, dq [T, Hq, d]; d_k_out, dk [T, Hkv, d]; dq_weight, dk_weight [d] fp32 (overwritten); workspace: at least
+    kda_qk_norm_rope_backward_workspace_size(T, Hq, Hkv, d) bytes.
+    """
+    a = _qk_norm_args(q, k, q_weight, k_weight, dq, dk, ("dq", "dk"), cos, sin, positions, eps, interleaved, dev_status,
+                      (d_q_out, d_k_out), (dq_weight, dk_weight))
+    _check(workspace)
+    _ok("kda_qk_norm_rope_backward",
+        load().kda_qk_norm_rope_backward(a, d_q_out.data_ptr(), d_k_out.data_ptr(), _dt(d_q_out), dq_weight.data_ptr(),
+                                         dk_weight.data_ptr(), workspace.data_ptr(),
+                                         workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def _kv_cache(k_pages, v_pages, k_scales, v_scales):
+    pages, Hkv, page_size, d = _rank("k_pages", k_pages, 4)
+    if k_pages.dtype not in _CACHE_TYPES:
+        raise TypeError(f"k_pages: expected dtype torch.bfloat16 or torch.float8_e4m3fn, got {k_pages.dtype}")
+    _need("v_pages", v_pages, (pages, Hkv, page_size, d), (k_pages.dtype,))
+    if page_size <= 0 or page_size % 16:
+        raise ValueError(f"k_pages: expected pages of a positive multiple of 16 tokens, got {page_size}")
+    kind = _CACHE_TYPES[k_pages.dtype]
+    if kind == 1:
+        if k_scales is None or v_scales is None:
+            raise ValueError("k_scales and v_scales: an e4m3 cache needs both")
+        _need("k_scales", k_scales, (pages, Hkv, page_size), _FP)
+        _need("v_scales", v_scales, (pages, Hkv, page_size), _FP)
+    elif k_scales is not None or v_scales is not None:
+        raise ValueError("k_scales and v_scales: a bfloat16 cache has none")
+    _check(k_pages, v_pages, k_scales, v_scales)
+    return KvCache(k_pages.data_ptr(), v_pages.data_ptr(), _ptr(k_scales), _ptr(v_scales), kind, pages, page_size, Hkv,
+                   d)
+
+
+def kda_kv_write(k, v, k_pages, v_pages, slots, k_scales=None, v_scales=None, dev_status=None, stream=None):
+    """Token t of k, v [T, Hkv, d] goes to cache slot slots[t] = page * page_size + offset (int64, distinct; negative:
+    skipped).  k_pages, v_pages [pages, Hkv, page_size, d] bfloat16, or float8_e4m3fn with k_scales, v_scales
+    [pages, Hkv, page_size] fp32: each row quantised with a power-of-two scale of its own."""
+    T = _rank("k", k, 3)[0]
+    Hkv, d = _rank("k_pages", k_pages, 4)[1::2]
+    _need("k", k, (T, Hkv, d), _IN)
+    _need("v", v, (T, Hkv, d), (k.dtype,))
+    _need("slots", slots, (T,), _I64)
+    _need_status(dev_status)
+    c = _kv_cache(k_pages, v_pages, k_scales, v_scales)
+    _check(slots, dev_status)
+    _ok("kda_kv_write", load().kda_kv_write(k.data_ptr(), v.data_ptr(), _row_stride("k", k), _row_stride("v", v), _dt(k),
+                                            T, slots.data_ptr(), c, _ptr(dev_status), _stream(stream)))
+
+
+def kda_kv_read(k_pages, v_pages, slots, k_out, v_out, k_scales=None, v_scales=None, dev_status=None, stream=None):
+    """Token t of k_out, v_out [T, Hkv, d] receives cache slot slots[t] (int64; negative: a zero row)."""
+    Hkv, d = _rank("k_pages", k_pages, 4)[1::2]
+    _need("slots", slots, (None,), _I64)
+    T = slots.numel()
+    _need("k_out", k_out, (T, Hkv, d), _IN)
+    _need("v_out", v_out, (T, Hkv, d), (k_out.dtype,))
+    _need_status(dev_status)
+    c = _kv_cache(k_pages, v_pages, k_scales, v_scales)
+    _check(slots, k_out, v_out, dev_status)
+    _ok("kda_kv_read", load().kda_kv_read(c, slots.data_ptr(), T, k_out.data_ptr(), v_out.data_ptr(), _dt(k_out),
+                                          _ptr(dev_status), _stream(stream)))
+
+
+def kda_paged_attention_workspace_size(B: int, W: int, Hq: int, Hkv: int, d: int) -> int:
+    return load().kda_paged_attention_workspace_size(B, W, Hq, Hkv, d)
+
+
+def kda_paged_attention(q, k_pages, v_pages, block_table, seq_lens, out, workspace, k_scales=None, v_scales=None,
+                        scale=None, softcap=0.0, window=0, lse=None, dev_status=None, stream=None):
+    """Attention of the W newest tokens of each request over its cached tokens (the new ones written first).
+
+    q, out [B, W, Hq, d]; pages and scales as kda_kv_write; block_table int32 [B, max_pages]; seq_lens int32 [B], the
+    tokens in the cache; scale: 1 / sqrt(d) unless given; softcap > 0: scores softcap * tanh(x / softcap);
+    window > 0: a query sees that many positions, its own included; lse [B, W, Hq] fp32 or None; workspace: at least
+    kda_paged_attention_workspace_size(B, W, Hq, Hkv, d) bytes.
+    """
+    B, W, Hq, d = _rank("q", q, 4)
+    Hkv = _rank("k_pages", k_pages, 4)[1]
+    _need("q", q, (B, W, Hq, d), _IN)
+    _need("k_pages", k_pages, (None, Hkv, None, d), (k_pages.dtype,))
+    _need("block_table", block_table, (B, None), _I32)
+    _need("seq_lens", seq_lens, (B,), _I32)
+    _need("out", out, (B, W, Hq, d), _IN)
+    _need("lse", lse, (B, W, Hq), _FP)
+    if Hkv == 0 or Hq % Hkv:
+        raise ValueError(f"q: expected a multiple of the cache's {Hkv} heads, got {Hq}")
+    _need_status(dev_status)
+    c = _kv_cache(k_pages, v_pages, k_scales, v_scales)
+    _check(q, block_table, seq_lens, out, lse, workspace, dev_status)
+    a = PagedAttentionArgs(q.data_ptr(), _dt(q), B, W, Hq, c, block_table.data_ptr(), block_table.shape[1],
+                           seq_lens.data_ptr(), d ** -0.5 if scale is None else scale, softcap, window, out.data_ptr(),
+                           _dt(out), _ptr(lse), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                           _ptr(dev_status))
+    _ok("kda_paged_attention", load().kda_paged_attention(a, _stream(stream)))

@@ -598,3 +598,209 @@ kda_status kda_kcp_outputs(const kda_prefill_args* a, int32_t segment_len, const
 }
 
 }  // extern "C"
+
+// ---- softmax-attention layers: norm and rotation, paged cache, attention over it
+namespace {
+
+// A token-strided array: 16-byte rows, tokens at least a row apart.
+bool strided_ok(const void* p, int64_t stride, int64_t row, kda_dtype t) {
+  return p && aligned16(p) && stride >= row && (stride * (int64_t)esize(t)) % 16 == 0;
+}
+bool natural(const void* p, unsigned bytes) { return p && (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+bool d_ok(int d) { return head_ok(d, d); }
+// fits the kernels' 32-bit row-group counters
+bool rows_ok(int64_t T, int64_t heads) { return T <= 0x7fffffff && T * heads <= 0x7fffffff - 1024; }
+
+kda_status check_norm(const kda_qk_norm_rope_args* a) {
+  if (!a) return KDA_ERR_INVALID_ARG;
+  if (!dtype_ok(a->in_dtype) || !dtype_ok(a->out_dtype)) return KDA_ERR_INVALID_ARG;
+  if (a->T < 0 || a->Hq <= 0 || a->Hkv <= 0 || a->Hq > 65535 || a->Hkv > 65535 || !(a->eps >= 0.f))
+    return KDA_ERR_INVALID_ARG;
+  if (!d_ok(a->d)) return KDA_ERR_UNSUPPORTED;
+  if (a->rot < 0 || a->rot > a->d || a->rot % 16 != 0) return KDA_ERR_INVALID_ARG;
+  return KDA_OK;
+}
+
+// the pointers of a call with tokens
+kda_status check_norm_arrays(const kda_qk_norm_rope_args* a) {
+  if (!rows_ok(a->T, a->Hq + a->Hkv)) return KDA_ERR_INVALID_ARG;
+  const int64_t rq = (int64_t)a->Hq * a->d, rk = (int64_t)a->Hkv * a->d;
+  if (!strided_ok(a->q, a->q_stride, rq, a->in_dtype) || !strided_ok(a->k, a->k_stride, rk, a->in_dtype) ||
+      !strided_ok(a->q_out, a->q_out_stride, rq, a->out_dtype) ||
+      !strided_ok(a->k_out, a->k_out_stride, rk, a->out_dtype))
+    return KDA_ERR_INVALID_ARG;
+  if (!a->q_weight || !a->k_weight || !aligned16(a->q_weight) || !aligned16(a->k_weight)) return KDA_ERR_INVALID_ARG;
+  if (a->rot > 0) {
+    if (!a->cos || !a->sin || !aligned16(a->cos) || !aligned16(a->sin)) return KDA_ERR_INVALID_ARG;
+    if (!natural(a->positions, 4) || a->num_positions < 0) return KDA_ERR_INVALID_ARG;
+  }
+  return KDA_OK;
+}
+
+kda::NormArgs norm_args(const kda_qk_norm_rope_args* a) {
+  kda::NormArgs n{};
+  n.q = a->q;
+  n.k = a->k;
+  n.q_stride = a->q_stride;
+  n.k_stride = a->k_stride;
+  n.in_bf16 = a->in_dtype == KDA_DTYPE_BF16;
+  n.out_bf16 = a->out_dtype == KDA_DTYPE_BF16;
+  n.wq = a->q_weight;
+  n.wk = a->k_weight;
+  n.cos = a->cos;
+  n.sin = a->sin;
+  n.positions = a->positions;
+  n.num_positions = a->num_positions;
+  n.rot = a->rot;
+  n.interleaved = a->interleaved != 0;
+  n.eps = a->eps;
+  n.T = a->T;
+  n.Hq = a->Hq;
+  n.Hkv = a->Hkv;
+  n.d = a->d;
+  n.q_out = a->q_out;
+  n.k_out = a->k_out;
+  n.q_out_stride = a->q_out_stride;
+  n.k_out_stride = a->k_out_stride;
+  n.status = a->dev_status;
+  return n;
+}
+
+kda_status check_cache(const kda_kv_cache* c, bool arrays) {
+  if (!c) return KDA_ERR_INVALID_ARG;
+  if (c->type != KDA_CACHE_BF16 && c->type != KDA_CACHE_E4M3) return KDA_ERR_INVALID_ARG;
+  if (c->num_pages < 0 || c->page_size <= 0 || c->page_size % 16 != 0 || c->Hkv <= 0 || c->Hkv > 65535)
+    return KDA_ERR_INVALID_ARG;
+  if (!d_ok(c->d)) return KDA_ERR_UNSUPPORTED;
+  if (!arrays) return KDA_OK;
+  if (!c->k_pages || !c->v_pages || !aligned16(c->k_pages) || !aligned16(c->v_pages)) return KDA_ERR_INVALID_ARG;
+  if (c->type == KDA_CACHE_E4M3 &&
+      (!c->k_scales || !c->v_scales || !aligned16(c->k_scales) || !aligned16(c->v_scales)))
+    return KDA_ERR_INVALID_ARG;
+  return KDA_OK;
+}
+
+kda::KvCacheArgs cache_args(const kda_kv_cache* c) {
+  return kda::KvCacheArgs{c->k_pages,   c->v_pages,   c->k_scales, c->v_scales, c->type == KDA_CACHE_E4M3,
+                          c->num_pages, c->page_size, c->Hkv,      c->d};
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t kda_qk_norm_rope_args_bytes(void) { return sizeof(kda_qk_norm_rope_args); }
+size_t kda_kv_cache_bytes(void) { return sizeof(kda_kv_cache); }
+size_t kda_paged_attention_args_bytes(void) { return sizeof(kda_paged_attention_args); }
+
+kda_status kda_qk_norm_rope(const kda_qk_norm_rope_args* a, kda_stream_t stream) {
+  kda_status st = check_norm(a);
+  if (st != KDA_OK || a->T == 0) return st;
+  st = check_norm_arrays(a);
+  if (st != KDA_OK) return st;
+  return from_cuda(kda::launch_qk_norm_rope(norm_args(a), reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t kda_qk_norm_rope_backward_workspace_size(int64_t T, int Hq, int Hkv, int d) {
+  if (T < 0 || Hq <= 0 || Hkv <= 0 || !d_ok(d)) return 0;
+  return (size_t)kda::NORM_BWD_CTAS * 2 * d * 4;
+}
+
+kda_status kda_qk_norm_rope_backward(const kda_qk_norm_rope_args* a, const void* d_q_out, const void* d_k_out,
+                                     kda_dtype grad_dtype, float* dq_weight, float* dk_weight, void* workspace,
+                                     size_t workspace_bytes, kda_stream_t stream) {
+  kda_status st = check_norm(a);
+  if (st != KDA_OK) return st;
+  if (!dtype_ok(grad_dtype)) return KDA_ERR_INVALID_ARG;
+  if (!dq_weight || !dk_weight || !aligned16(dq_weight) || !aligned16(dk_weight)) return KDA_ERR_INVALID_ARG;
+  if (a->T > 0) {
+    st = check_norm_arrays(a);
+    if (st != KDA_OK) return st;
+    if (!d_q_out || !d_k_out || !aligned16(d_q_out) || !aligned16(d_k_out)) return KDA_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < kda_qk_norm_rope_backward_workspace_size(a->T, a->Hq, a->Hkv, a->d))
+      return KDA_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return KDA_ERR_INVALID_ARG;
+  }
+  return from_cuda(kda::launch_qk_norm_rope_backward(norm_args(a), d_q_out, d_k_out, grad_dtype == KDA_DTYPE_BF16,
+                                                     dq_weight, dk_weight, static_cast<float*>(workspace),
+                                                     reinterpret_cast<cudaStream_t>(stream)));
+}
+
+kda_status kda_kv_write(const void* k, const void* v, int64_t k_stride, int64_t v_stride, kda_dtype in_dtype,
+                        int64_t T, const int64_t* slots, const kda_kv_cache* cache, int32_t* dev_status,
+                        kda_stream_t stream) {
+  if (!dtype_ok(in_dtype) || T < 0) return KDA_ERR_INVALID_ARG;
+  kda_status st = check_cache(cache, T > 0);
+  if (st != KDA_OK || T == 0) return st;
+  const int64_t row = (int64_t)cache->Hkv * cache->d;
+  if (!rows_ok(T, 2 * (int64_t)cache->Hkv) || !strided_ok(k, k_stride, row, in_dtype) ||
+      !strided_ok(v, v_stride, row, in_dtype) || !natural(slots, 8))
+    return KDA_ERR_INVALID_ARG;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  st = kda::debug_check_tokens(slots, T, s);
+  if (st != KDA_OK) return st;
+  kda::KvWriteArgs w{k, v, k_stride, v_stride, in_dtype == KDA_DTYPE_BF16, T, slots, cache_args(cache), dev_status};
+  return from_cuda(kda::launch_kv_write(w, s));
+}
+
+kda_status kda_kv_read(const kda_kv_cache* cache, const int64_t* slots, int64_t T, void* k_out, void* v_out,
+                       kda_dtype out_dtype, int32_t* dev_status, kda_stream_t stream) {
+  if (!dtype_ok(out_dtype) || T < 0) return KDA_ERR_INVALID_ARG;
+  kda_status st = check_cache(cache, T > 0);
+  if (st != KDA_OK || T == 0) return st;
+  if (!rows_ok(T, 2 * (int64_t)cache->Hkv) || !k_out || !v_out || !aligned16(k_out) || !aligned16(v_out) ||
+      !natural(slots, 8))
+    return KDA_ERR_INVALID_ARG;
+  kda::KvReadArgs r{cache_args(cache), slots, T, k_out, v_out, out_dtype == KDA_DTYPE_BF16, dev_status};
+  return from_cuda(kda::launch_kv_read(r, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t kda_paged_attention_workspace_size(int B, int W, int Hq, int Hkv, int d) {
+  if (B < 0 || W <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || !d_ok(d)) return 0;
+  if ((int64_t)W * (Hq / Hkv) > 0x7fffffff) return 0;
+  return kda::paged_attention_ws_bytes(W, Hq, Hkv, d);
+}
+
+kda_status kda_paged_attention(const kda_paged_attention_args* a, kda_stream_t stream) {
+  if (!a || !dtype_ok(a->q_dtype) || !dtype_ok(a->out_dtype)) return KDA_ERR_INVALID_ARG;
+  if (a->B < 0 || a->W <= 0 || a->Hq <= 0 || a->max_pages < 0 || a->window < 0) return KDA_ERR_INVALID_ARG;
+  if (!(a->softcap >= 0.f) || a->softcap > 3e38f || !(a->scale >= -3e38f && a->scale <= 3e38f))
+    return KDA_ERR_INVALID_ARG;
+  kda_status st = check_cache(&a->cache, a->B > 0 && a->max_pages > 0);
+  if (st != KDA_OK) return st;
+  if (a->Hq % a->cache.Hkv != 0) return KDA_ERR_INVALID_ARG;
+  if (a->B == 0) return KDA_OK;
+  // request x query row counts and the (unit, row block) numbers of the kernel stay within 32 bits
+  if ((int64_t)a->W * a->Hq > 0x7fffffff / 2 || (int64_t)a->B * a->W * a->Hq > 0x7fffffff / 2)
+    return KDA_ERR_INVALID_ARG;
+  const void* ptrs[] = {a->q, a->out};
+  for (const void* p : ptrs)
+    if (!p || !aligned16(p)) return KDA_ERR_INVALID_ARG;
+  if (a->lse && !natural(a->lse, 4)) return KDA_ERR_INVALID_ARG;
+  if ((a->max_pages > 0 && !natural(a->block_table, 4)) || !natural(a->seq_lens, 4)) return KDA_ERR_INVALID_ARG;
+  if (!a->workspace || a->workspace_bytes < kda_paged_attention_workspace_size(a->B, a->W, a->Hq, a->cache.Hkv,
+                                                                               a->cache.d))
+    return KDA_ERR_WORKSPACE;
+  if (!aligned16(a->workspace)) return KDA_ERR_INVALID_ARG;
+  kda::PagedAttnArgs p{};
+  p.q = a->q;
+  p.q_bf16 = a->q_dtype == KDA_DTYPE_BF16;
+  p.out_bf16 = a->out_dtype == KDA_DTYPE_BF16;
+  p.B = a->B;
+  p.W = a->W;
+  p.Hq = a->Hq;
+  p.c = cache_args(&a->cache);
+  p.block_table = a->block_table;
+  p.max_pages = a->max_pages;
+  p.seq_lens = a->seq_lens;
+  p.scale = a->scale;
+  p.softcap = a->softcap;
+  p.window = a->window;
+  p.out = a->out;
+  p.lse = a->lse;
+  p.ws = static_cast<float*>(a->workspace);
+  p.status = a->dev_status;
+  return from_cuda(kda::launch_paged_attention(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

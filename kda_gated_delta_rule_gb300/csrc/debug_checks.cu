@@ -82,4 +82,19 @@ kda_status debug_check_slots(const int32_t* dev_ids, int32_t n, const int32_t* d
   return kda_check_slot_ids(a.data(), n, dev_other ? b.data() : nullptr, dev_other ? n_other : 0);
 }
 
+kda_status debug_check_tokens(const int64_t* dev_slots, int64_t n, cudaStream_t s) {
+  if (!kda_debug_checks() || n <= 0) return KDA_OK;
+  try {
+    std::vector<int64_t> a(n);
+    if (cudaMemcpyAsync(a.data(), dev_slots, (size_t)n * sizeof(int64_t), cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+        cudaStreamSynchronize(s) != cudaSuccess)
+      return KDA_ERR_CUDA;
+    a.erase(std::remove_if(a.begin(), a.end(), [](int64_t v) { return v < 0; }), a.end());  // skipped tokens
+    std::sort(a.begin(), a.end());
+    return std::adjacent_find(a.begin(), a.end()) == a.end() ? KDA_OK : KDA_ERR_INVALID_ARG;
+  } catch (...) {  // no host memory for the ids: nothing leaves a C entry point but a status
+    return KDA_ERR_CUDA;
+  }
+}
+
 }  // namespace kda

@@ -199,6 +199,75 @@ struct FusedDecodeArgs {
 cudaError_t launch_fused_decode(const FusedDecodeArgs& a, cudaStream_t s);
 cudaError_t launch_backward(const BackwardArgs& a, cudaStream_t s);
 
+// Per-head norm of queries and keys with the position rotation (see kda_qk_norm_rope_args in include/kda.h).
+struct NormArgs {
+  const void *q, *k;
+  int64_t q_stride, k_stride;
+  bool in_bf16, out_bf16;
+  const float *wq, *wk, *cos, *sin;
+  const int32_t* positions;
+  int num_positions, rot;
+  bool interleaved;
+  float eps;
+  int64_t T;
+  int Hq, Hkv, d;
+  void *q_out, *k_out;
+  int64_t q_out_stride, k_out_stride;
+  int32_t* status;
+};
+// CTAs of the backward at most, one row of partial weight gradients each: four per SM
+constexpr int NORM_BWD_CTAS = 608;
+cudaError_t launch_qk_norm_rope(const NormArgs& a, cudaStream_t s);
+// q_out, k_out receive dq, dk; partial: NORM_BWD_CTAS * 2 * d floats
+cudaError_t launch_qk_norm_rope_backward(const NormArgs& a, const void* dyq, const void* dyk, bool g_bf16, float* dwq,
+                                         float* dwk, float* partial, cudaStream_t s);
+
+// The paged key/value cache (see kda_kv_cache in include/kda.h).
+struct KvCacheArgs {
+  void *k_pages, *v_pages;
+  float *k_scales, *v_scales;
+  bool e4m3;
+  int num_pages, page_size, Hkv, d;
+};
+struct KvWriteArgs {
+  const void *k, *v;
+  int64_t k_stride, v_stride;
+  bool in_bf16;
+  int64_t T;
+  const int64_t* slots;
+  KvCacheArgs c;
+  int32_t* status;
+};
+struct KvReadArgs {
+  KvCacheArgs c;
+  const int64_t* slots;
+  int64_t T;
+  void *k_out, *v_out;
+  bool out_bf16;
+  int32_t* status;
+};
+cudaError_t launch_kv_write(const KvWriteArgs& a, cudaStream_t s);
+cudaError_t launch_kv_read(const KvReadArgs& a, cudaStream_t s);
+
+// Attention of the newest tokens over the paged cache (see kda_paged_attention_args in include/kda.h).
+struct PagedAttnArgs {
+  const void* q;
+  bool q_bf16, out_bf16;
+  int B, W, Hq;
+  KvCacheArgs c;
+  const int32_t* block_table;
+  int max_pages;
+  const int32_t* seq_lens;
+  float scale, softcap;
+  int window;
+  void* out;
+  float* lse;
+  float* ws;  // paged_attention_ws_bytes
+  int32_t* status;
+};
+size_t paged_attention_ws_bytes(int W, int Hq, int Hkv, int d);
+cudaError_t launch_paged_attention(const PagedAttnArgs& a, cudaStream_t s);
+
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t s);
 cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t s);
 // Tensor-core verify (bf16 inputs, d = 128, W <= 16, no per-token snapshots).
