@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -134,6 +135,21 @@ class PagedAttentionArgs(ctypes.Structure):
     ]
 
 
+def _packer(mirror):
+    """struct.Struct.pack for a mirror's fields in their native layout, a nested struct's fields in its place."""
+    codes = {ctypes.c_void_p: "P", ctypes.c_int: "i", ctypes.c_int32: "i", ctypes.c_int64: "q", ctypes.c_size_t: "N",
+             ctypes.c_float: "f"}
+
+    def fields(m):
+        return "".join(codes[t] if t in codes else fields(t) for _, t in m._fields_) + "0P"  # structs end on a pointer's
+    packed = struct.Struct("@" + fields(mirror))
+    if packed.size != ctypes.sizeof(mirror):
+        raise RuntimeError(f"{mirror.__name__}: the packed layout differs from the mirror's")
+    return packed.pack
+
+
+_pack_norm, _pack_cache, _pack_attention = map(_packer, (QkNormRopeArgs, KvCache, PagedAttentionArgs))
+_packed = {}
 _lib = None
 
 
@@ -152,6 +168,7 @@ def load(build_if_missing: bool = False):
         _build.build()
     lib = ctypes.CDLL(_build.LIB)
     vp, i32, i64, sz, c_int = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
+    st = ctypes.c_char_p  # a packed argument struct
     sig = {
         "kda_status_string": (ctypes.c_char_p, [c_int]),
         "kda_version": (c_int, []),
@@ -219,6 +236,13 @@ def load(build_if_missing: bool = False):
                          ("kda_paged_attention_args", PagedAttentionArgs)):
         if getattr(lib, name + "_bytes")() != ctypes.sizeof(mirror):
             raise RuntimeError(f"{name} layout mismatch between include/kda.h and the binding")
+    # The attention calls' argument structs go over as packed bytes (their mirrors cost a microsecond to fill, more than
+    # the rest of such a call's marshalling); function objects of their own, since the pointer type differs.
+    for name, args in (("kda_qk_norm_rope", [st, vp]), ("kda_qk_norm_rope_backward", [st, vp, vp, c_int, vp, vp, vp, sz, vp]),
+                       ("kda_kv_write", [vp, vp, i64, i64, c_int, i64, vp, st, vp, vp]),
+                       ("kda_kv_read", [st, vp, i64, vp, vp, c_int, vp, vp]), ("kda_paged_attention", [st, vp])):
+        _packed[name] = lib[name]
+        _packed[name].restype, _packed[name].argtypes = c_int, args
     _lib = lib
     return lib
 
@@ -229,18 +253,26 @@ def _p(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+_DTYPE_CODES = {torch.float32: F32, torch.bfloat16: BF16}
+
+
 def _dt(t: torch.Tensor) -> int:
-    if t.dtype == torch.float32:
-        return F32
-    if t.dtype == torch.bfloat16:
-        return BF16
-    raise TypeError(f"unsupported dtype {t.dtype}")
+    code = _DTYPE_CODES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    return code
+
+
+# torch.cuda.current_stream() builds a Stream object (3 us on the host); this returns its handle alone
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    return stream.cuda_stream
 
 
 def _check(*ts):
@@ -260,7 +292,7 @@ _I32 = (torch.int32,)
 
 
 def _need(name, t, shape, dtypes):
-    if t is None:
+    if t is None or (t.shape == shape and t.dtype in dtypes):  # the common case first: None entries fail it
         return
     if t.dim() != len(shape) or any(s is not None and t.shape[i] != s for i, s in enumerate(shape)):
         want = ", ".join("*" if s is None else str(s) for s in shape)
@@ -746,43 +778,51 @@ def _row_stride(name, t):
 
 
 def _ptr(t):
-    return None if t is None else t.data_ptr()
+    return 0 if t is None else t.data_ptr()
+
+
+def _call(name, *args):
+    if not _packed:
+        load()
+    code = _packed[name](*args)
+    if code != KDA_OK:
+        raise KdaError(name, code)
 
 
 def _qk_norm_args(q, k, q_weight, k_weight, q_out, k_out, out_names, cos, sin, positions, eps, interleaved, dev_status,
                   grads=(), weight_grads=()):
     T, Hq, d = _rank("q", q, 3)
-    _need("q", q, (T, Hq, d), _IN)
-    _need("k", k, (T, None, d), (q.dtype,))
+    _need("q", q, q.shape, _IN)
+    dtype = (q.dtype,)
+    _need("k", k, (T, k.shape[1] if k.dim() == 3 else None, d), dtype)
     Hkv = k.shape[1]
     _need("q_weight", q_weight, (d,), _FP)
     _need("k_weight", k_weight, (d,), _FP)
-    _need(out_names[0], q_out, (T, Hq, d), _IN)
-    _need(out_names[1], k_out, (T, Hkv, d), (q_out.dtype,))
+    _need(out_names[0], q_out, q.shape, _IN)
+    _need(out_names[1], k_out, k.shape, (q_out.dtype,))
     n = rot = 0
     if cos is not None or sin is not None or positions is not None:
         if cos is None or sin is None or positions is None:
             raise ValueError("cos, sin and positions go together (all None: no rotation)")
         n, half = _rank("cos", cos, 2)
         rot = 2 * half
-        _need("cos", cos, (n, half), _FP)
-        _need("sin", sin, (n, half), _FP)
+        _need("cos", cos, cos.shape, _FP)
+        _need("sin", sin, cos.shape, _FP)
         _need("positions", positions, (T,), _I32)
         if rot > d or rot % 16:
             raise ValueError(f"cos: expected angles of a multiple of 8 channel pairs within d = {d}, got {half}")
     if grads:
         d_q_out, d_k_out = grads
-        _need("d_q_out", d_q_out, (T, Hq, d), _IN)
-        _need("d_k_out", d_k_out, (T, Hkv, d), (d_q_out.dtype,))
+        _need("d_q_out", d_q_out, q.shape, _IN)
+        _need("d_k_out", d_k_out, k.shape, (d_q_out.dtype,))
         _need("dq_weight", weight_grads[0], (d,), _FP)
         _need("dk_weight", weight_grads[1], (d,), _FP)
     _need_status(dev_status)
-    _check(q_weight, k_weight, cos, sin, positions, dev_status, *grads, *weight_grads)
-    return QkNormRopeArgs(q.data_ptr(), k.data_ptr(), _row_stride("q", q), _row_stride("k", k), _dt(q),
-                          q_weight.data_ptr(), k_weight.data_ptr(), _ptr(cos), _ptr(sin), _ptr(positions), n, rot,
-                          bool(interleaved), eps, T, Hq, Hkv, d, q_out.data_ptr(), k_out.data_ptr(),
-                          _row_stride(out_names[0], q_out), _row_stride(out_names[1], k_out), _dt(q_out),
-                          _ptr(dev_status))
+    _check(q_weight, k_weight, dev_status, cos, sin, positions, *grads, *weight_grads)
+    return _pack_norm(q.data_ptr(), k.data_ptr(), _row_stride("q", q), _row_stride("k", k), _dt(q),
+                      q_weight.data_ptr(), k_weight.data_ptr(), _ptr(cos), _ptr(sin), _ptr(positions), n, rot,
+                      bool(interleaved), eps, T, Hq, Hkv, d, q_out.data_ptr(), k_out.data_ptr(),
+                      _row_stride(out_names[0], q_out), _row_stride(out_names[1], k_out), _dt(q_out), _ptr(dev_status))
 
 
 def kda_qk_norm_rope(q, k, q_weight, k_weight, q_out, k_out, cos=None, sin=None, positions=None, eps=1e-6,
@@ -795,7 +835,7 @@ def kda_qk_norm_rope(q, k, q_weight, k_weight, q_out, k_out, cos=None, sin=None,
     """
     a = _qk_norm_args(q, k, q_weight, k_weight, q_out, k_out, ("q_out", "k_out"), cos, sin, positions, eps, interleaved,
                       dev_status)
-    _ok("kda_qk_norm_rope", load().kda_qk_norm_rope(a, _stream(stream)))
+    _call("kda_qk_norm_rope", a, _stream(stream))
 
 
 def kda_qk_norm_rope_backward_workspace_size(T: int, Hq: int, Hkv: int, d: int) -> int:
@@ -813,30 +853,29 @@ def kda_qk_norm_rope_backward(d_q_out, d_k_out, q, k, q_weight, k_weight, dq, dk
     a = _qk_norm_args(q, k, q_weight, k_weight, dq, dk, ("dq", "dk"), cos, sin, positions, eps, interleaved, dev_status,
                       (d_q_out, d_k_out), (dq_weight, dk_weight))
     _check(workspace)
-    _ok("kda_qk_norm_rope_backward",
-        load().kda_qk_norm_rope_backward(a, d_q_out.data_ptr(), d_k_out.data_ptr(), _dt(d_q_out), dq_weight.data_ptr(),
-                                         dk_weight.data_ptr(), workspace.data_ptr(),
-                                         workspace.numel() * workspace.element_size(), _stream(stream)))
+    _call("kda_qk_norm_rope_backward", a, d_q_out.data_ptr(), d_k_out.data_ptr(), _dt(d_q_out), dq_weight.data_ptr(),
+          dk_weight.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream))
 
 
 def _kv_cache(k_pages, v_pages, k_scales, v_scales):
-    pages, Hkv, page_size, d = _rank("k_pages", k_pages, 4)
-    if k_pages.dtype not in _CACHE_TYPES:
+    """The fields of kda_kv_cache."""
+    shape = k_pages.shape
+    kind = _CACHE_TYPES.get(k_pages.dtype)
+    if kind is None:
         raise TypeError(f"k_pages: expected dtype torch.bfloat16 or torch.float8_e4m3fn, got {k_pages.dtype}")
-    _need("v_pages", v_pages, (pages, Hkv, page_size, d), (k_pages.dtype,))
+    _need("v_pages", v_pages, shape, (k_pages.dtype,))
+    pages, Hkv, page_size, d = shape
     if page_size <= 0 or page_size % 16:
         raise ValueError(f"k_pages: expected pages of a positive multiple of 16 tokens, got {page_size}")
-    kind = _CACHE_TYPES[k_pages.dtype]
     if kind == 1:
         if k_scales is None or v_scales is None:
             raise ValueError("k_scales and v_scales: an e4m3 cache needs both")
-        _need("k_scales", k_scales, (pages, Hkv, page_size), _FP)
-        _need("v_scales", v_scales, (pages, Hkv, page_size), _FP)
+        _need("k_scales", k_scales, shape[:3], _FP)
+        _need("v_scales", v_scales, shape[:3], _FP)
     elif k_scales is not None or v_scales is not None:
         raise ValueError("k_scales and v_scales: a bfloat16 cache has none")
     _check(k_pages, v_pages, k_scales, v_scales)
-    return KvCache(k_pages.data_ptr(), v_pages.data_ptr(), _ptr(k_scales), _ptr(v_scales), kind, pages, page_size, Hkv,
-                   d)
+    return (k_pages.data_ptr(), v_pages.data_ptr(), _ptr(k_scales), _ptr(v_scales), kind, pages, page_size, Hkv, d)
 
 
 def kda_kv_write(k, v, k_pages, v_pages, slots, k_scales=None, v_scales=None, dev_status=None, stream=None):
@@ -844,29 +883,29 @@ def kda_kv_write(k, v, k_pages, v_pages, slots, k_scales=None, v_scales=None, de
     skipped).  k_pages, v_pages [pages, Hkv, page_size, d] bfloat16, or float8_e4m3fn with k_scales, v_scales
     [pages, Hkv, page_size] fp32: each row quantised with a power-of-two scale of its own."""
     T = _rank("k", k, 3)[0]
-    Hkv, d = _rank("k_pages", k_pages, 4)[1::2]
+    _, Hkv, _, d = _rank("k_pages", k_pages, 4)
     _need("k", k, (T, Hkv, d), _IN)
-    _need("v", v, (T, Hkv, d), (k.dtype,))
+    _need("v", v, k.shape, (k.dtype,))
     _need("slots", slots, (T,), _I64)
     _need_status(dev_status)
-    c = _kv_cache(k_pages, v_pages, k_scales, v_scales)
+    c = _pack_cache(*_kv_cache(k_pages, v_pages, k_scales, v_scales))
     _check(slots, dev_status)
-    _ok("kda_kv_write", load().kda_kv_write(k.data_ptr(), v.data_ptr(), _row_stride("k", k), _row_stride("v", v), _dt(k),
-                                            T, slots.data_ptr(), c, _ptr(dev_status), _stream(stream)))
+    _call("kda_kv_write", k.data_ptr(), v.data_ptr(), _row_stride("k", k), _row_stride("v", v), _dt(k), T,
+          slots.data_ptr(), c, _ptr(dev_status), _stream(stream))
 
 
 def kda_kv_read(k_pages, v_pages, slots, k_out, v_out, k_scales=None, v_scales=None, dev_status=None, stream=None):
     """Token t of k_out, v_out [T, Hkv, d] receives cache slot slots[t] (int64; negative: a zero row)."""
-    Hkv, d = _rank("k_pages", k_pages, 4)[1::2]
-    _need("slots", slots, (None,), _I64)
-    T = slots.numel()
+    _, Hkv, _, d = _rank("k_pages", k_pages, 4)
+    T = _rank("slots", slots, 1)[0]
+    _need("slots", slots, (T,), _I64)
     _need("k_out", k_out, (T, Hkv, d), _IN)
-    _need("v_out", v_out, (T, Hkv, d), (k_out.dtype,))
+    _need("v_out", v_out, k_out.shape, (k_out.dtype,))
     _need_status(dev_status)
-    c = _kv_cache(k_pages, v_pages, k_scales, v_scales)
+    c = _pack_cache(*_kv_cache(k_pages, v_pages, k_scales, v_scales))
     _check(slots, k_out, v_out, dev_status)
-    _ok("kda_kv_read", load().kda_kv_read(c, slots.data_ptr(), T, k_out.data_ptr(), v_out.data_ptr(), _dt(k_out),
-                                          _ptr(dev_status), _stream(stream)))
+    _call("kda_kv_read", c, slots.data_ptr(), T, k_out.data_ptr(), v_out.data_ptr(), _dt(k_out), _ptr(dev_status),
+          _stream(stream))
 
 
 def kda_paged_attention_workspace_size(B: int, W: int, Hq: int, Hkv: int, d: int) -> int:
@@ -883,20 +922,21 @@ def kda_paged_attention(q, k_pages, v_pages, block_table, seq_lens, out, workspa
     kda_paged_attention_workspace_size(B, W, Hq, Hkv, d) bytes.
     """
     B, W, Hq, d = _rank("q", q, 4)
-    Hkv = _rank("k_pages", k_pages, 4)[1]
-    _need("q", q, (B, W, Hq, d), _IN)
-    _need("k_pages", k_pages, (None, Hkv, None, d), (k_pages.dtype,))
-    _need("block_table", block_table, (B, None), _I32)
+    pages, Hkv, page_size, dc = _rank("k_pages", k_pages, 4)
+    _need("q", q, q.shape, _IN)
+    if dc != d:
+        _need("k_pages", k_pages, (pages, Hkv, page_size, d), (k_pages.dtype,))
+    max_pages = _rank("block_table", block_table, 2)[1]
+    _need("block_table", block_table, (B, max_pages), _I32)
     _need("seq_lens", seq_lens, (B,), _I32)
-    _need("out", out, (B, W, Hq, d), _IN)
-    _need("lse", lse, (B, W, Hq), _FP)
+    _need("out", out, q.shape, _IN)
+    _need("lse", lse, q.shape[:3], _FP)
     if Hkv == 0 or Hq % Hkv:
         raise ValueError(f"q: expected a multiple of the cache's {Hkv} heads, got {Hq}")
     _need_status(dev_status)
     c = _kv_cache(k_pages, v_pages, k_scales, v_scales)
     _check(q, block_table, seq_lens, out, lse, workspace, dev_status)
-    a = PagedAttentionArgs(q.data_ptr(), _dt(q), B, W, Hq, c, block_table.data_ptr(), block_table.shape[1],
-                           seq_lens.data_ptr(), d ** -0.5 if scale is None else scale, softcap, window, out.data_ptr(),
-                           _dt(out), _ptr(lse), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                           _ptr(dev_status))
-    _ok("kda_paged_attention", load().kda_paged_attention(a, _stream(stream)))
+    a = _pack_attention(q.data_ptr(), _dt(q), B, W, Hq, *c, block_table.data_ptr(), max_pages, seq_lens.data_ptr(),
+                        d ** -0.5 if scale is None else scale, softcap, window, out.data_ptr(), _dt(out), _ptr(lse),
+                        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _ptr(dev_status))
+    _call("kda_paged_attention", a, _stream(stream))
