@@ -651,8 +651,8 @@ size_t kda_paged_attention_args_bytes(void);
 /* Scratch for the partial results of requests whose cache is split; its size does not depend on the lengths. */
 size_t kda_paged_attention_workspace_size(int B, int W, int Hq, int Hkv, int d);
 
-/* kda_paged_attention -- enqueue it.  A length outside [0, max_pages * page_size] sets KDA_DEV_SEQ_OOB and counts
- * as 0; a page id outside [0, num_pages) sets KDA_DEV_PAGE_OOB and its tokens are seen by no query. */
+/* kda_paged_attention -- enqueue it.  A length outside [0, max_pages * page_size], or above 2^31 - 256, sets
+ * KDA_DEV_SEQ_OOB and counts as 0; a page id outside [0, num_pages) sets KDA_DEV_PAGE_OOB and its tokens are seen by no query. */
 kda_status kda_paged_attention(const kda_paged_attention_args* a, kda_stream_t stream);
 
 #ifdef __cplusplus

@@ -7,19 +7,19 @@
 // so each K or V element is read once and used for 2 multiplications per query row.
 //
 // Work.  A unit is one request, key/value head and block of RB = 8 NT query rows.  All units' caches, cut into tiles
-// of TILE tokens, form one line of tiles; the CTAs take equal consecutive shares of it, so ragged lengths balance
-// without the host knowing them, and a single long request spreads over the whole GPU.  A CTA that has a whole unit
-// writes its output; the parts of a unit cut across CTAs go to the workspace (each CTA has at most one part that
-// continues a unit and one that starts one) and a second, small kernel joins them in order.
+// of TILE tokens, form one line; the warps take equal consecutive shares of it, so ragged lengths balance without
+// the host knowing them, and a single long request spreads over the whole GPU.  A unit counts PA_UNIT_COST tiles more
+// than it has, for its queries, first loads and output.  A warp that has a whole unit writes its output; the parts of a
+// unit cut across warps go to the workspace (each warp has at most one part that continues a unit and one that
+// starts one) and a second, small kernel joins them in order.  Warps never wait on one another after the share-out:
+// the other warps of the SM cover one's latencies.
 //
-// Inside a CTA four warps take the 16-token groups of a tile in turn, each with its own running maximum, sum and
-// accumulators, joined at the end of the unit.  K and V go from global memory straight into the operand registers of
-// mma.m16n8k16 (no shared memory, no transposes): the products are S^T = K Q^T and O^T = V^T P^T with the tokens
-// resp. channels as the 16-row side and 8 query rows as columns.  The channel order inside a product's K steps is
-// free as long as Q follows it, so a lane's operands for consecutive steps are one 16-byte piece of its token's row;
-// V's pairs of tokens are put together from two such pieces by byte permutes.  The 5th-generation tensor instructions
-// want 64 or 128 rows and both operands in shared or tensor memory; with 1 to 32 query rows they would sit idle
-// behind the same loads.
+// K and V go from global memory straight into the operand registers of mma.m16n8k16 (no transposes, no shared memory
+// for them): the products are S^T = K Q^T and O^T = V^T P^T with the tokens resp. channels as the 16-row side and 8
+// query rows as columns.  The channel order inside a product's K steps is free as long as Q follows it, so a lane's
+// operands for consecutive steps are one 16-byte piece of its token's row; V's pairs of tokens are put together from two
+// such pieces by byte permutes.  The 5th-generation tensor instructions want 64 or 128 rows and both operands in shared
+// or tensor memory; with 1 to 32 query rows they would sit idle behind the same loads.
 //
 // e4m3 caches: codes become fp16 (exact), q is scaled per row by a power of two into fp16's range (exact for bf16 q
 // down to 2^-31 of the row's maximum), the key's scale multiplies the score and the value's scale the
@@ -39,27 +39,30 @@
 namespace kda {
 
 constexpr int PA_NT = 128, PA_WARPS = 4;
-constexpr int PA_MAX_CTAS = 608;  // four per SM
+constexpr int PA_UNIT_COST = 2;
+constexpr int PA_MAX_LEN = 0x7fffff00;  // token positions and the next tile's stay within 32 bits
 constexpr float PA_LOG2E = 1.4426950408889634f, PA_LN2 = 0.6931471805599453f;
 // how far (in powers of two) scores may run above the softmax reference before it is moved
 constexpr float PA_SLACK = 6.f;
 
-// What the main kernel leaves for the join, per CTA.
+// What the main kernel leaves for the join, per warp.
 struct PaMeta {
-  int64_t tiles;  // tiles of all units
-  int unit;       // the unit whose first part is this CTA's last, -1 if none
-  int end_cta;    // the CTA with that unit's last part
+  int unit;  // the unit whose first part is this warp's last, -1 if none
+  int end;   // the warp with that unit's last part
 };
 
-__host__ __device__ constexpr int pa_nt(int rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
+// 8-row column blocks of a unit, and the CTAs per SM its kernel is built for
+__host__ __device__ constexpr int pa_nt(int rows, bool fine) { return rows <= 8 ? 1 : rows <= 16 || fine ? 2 : 4; }
+__host__ __device__ constexpr int pa_resident(int nt) { return nt == 1 ? 3 : 2; }
+constexpr int PA_SMS = 152;
 
 struct PaPlan {  // derived on the host
   int G;         // query heads per key/value head
   int rows;      // query rows per key/value head: W * G
   int blocks;    // row blocks of RB per key/value head
-  float* part_o;   // [CTA][2][RB][D]
-  float* part_ml;  // [CTA][2][RB][2]
-  PaMeta* meta;    // [CTA]
+  float* part_o;   // [warp][2][RB][D]
+  float* part_ml;  // [warp][2][RB][2]
+  PaMeta* meta;    // [warp]
 };
 
 // ---------------------------------------------------------------- instructions
@@ -132,6 +135,17 @@ struct Piece {
   }
 };
 
+// cap * tanh(x / cap) in powers of two, given y = x / cap and cap2 = cap * log2(e).  1 - 2 / (1 + e^2y) is within 1.2e-7
+// of tanh absolutely; below 0.15 the odd series to y^7 (next term 6e-9 relative there) keeps the small scores' relative
+// precision.
+__device__ __forceinline__ float capped(float y, float cap2) {
+  const float y2 = y * y;
+  const float series = y * fmaf(y2, fmaf(y2, fmaf(y2, -17.f / 315.f, 2.f / 15.f), -1.f / 3.f), 1.f);
+  const float yc = y > 40.f ? 40.f : y;  // 2 / (1 + e^80) is still a plain division; NaN passes
+  const float whole = 1.f - __fdividef(2.f, 1.f + ex2(yc * (2.f * PA_LOG2E)));
+  return cap2 * (y2 < 0.0225f ? series : whole);
+}
+
 // ---------------------------------------------------------------- the line of tiles
 
 // Tokens a request's window sees: first seen position rounded down to 16, and the tiles from there to its length.
@@ -142,7 +156,7 @@ template <int TILE>
 __device__ __forceinline__ PaSpan pa_span(const PagedAttnArgs& a, int b, bool flag) {
   PaSpan s;
   s.len = __ldg(a.seq_lens + b);
-  if (s.len < 0 || s.len > (int64_t)a.max_pages * a.c.page_size) {
+  if (s.len < 0 || s.len > (int64_t)a.max_pages * a.c.page_size || s.len > PA_MAX_LEN) {
     if (flag) flag_status(a.status, KDA_DEV_SEQ_OOB);
     s.len = 0;
   }
@@ -159,9 +173,10 @@ __device__ __forceinline__ PaSpan pa_span(const PagedAttnArgs& a, int b, bool fl
 template <int D, bool F8, int NT, bool FINE>
 struct PaCfg {
   static constexpr int ES = F8 ? 1 : 2;
+  static constexpr int RS = D * ES;                      // bytes of a cached row
   static constexpr int RB = 8 * NT;
-  static constexpr int GPI = F8 ? 2 : 1;                 // 16-token groups a warp works on at once
-  static constexpr int TILE = 16 * GPI * PA_WARPS;       // tokens
+  static constexpr int GPI = F8 && NT < 4 ? 2 : 1;       // 16-token groups a warp works on at once
+  static constexpr int TILE = 16 * GPI;                  // tokens
   static constexpr int KC = D / 4 < 16 / ES ? D / 4 : 16 / ES;  // channels of a key piece
   static constexpr int KL = D / (4 * KC);                // key pieces per lane and token
   static constexpr int VC = D / 8 < 16 / ES ? D / 8 : 16 / ES;  // channels of a value piece
@@ -169,26 +184,27 @@ struct PaCfg {
   static constexpr int KS = D / 16;                      // K steps of the first product, 16-channel tiles of the second
   static constexpr int QP = FINE ? (F8 ? 2 : 3) : 1;     // 16-bit parts of a query
   static constexpr int PP = FINE ? (F8 ? 2 : 3) : (F8 ? 1 : 2);  // and of a probability
+  static constexpr size_t SMEM = sizeof(uint2) * QP * NT * KS * 32 * PA_WARPS;
 };
 
 template <int D, bool F8, int NT, bool FINE>
-__global__ void __launch_bounds__(PA_NT) paged_attention_kernel(const PagedAttnArgs a, const PaPlan p) {
+__global__ void __launch_bounds__(PA_NT, pa_resident(NT)) paged_attention_kernel(const PagedAttnArgs a,
+                                                                                 const PaPlan p) {
   using C = PaCfg<D, F8, NT, FINE>;
   constexpr int RB = C::RB, TILE = C::TILE, GPI = C::GPI, KS = C::KS;
-  __shared__ uint2 qs[C::QP][NT][KS][32];    // Q in the operand order of the first product
-  __shared__ float qscale[RB];               // per row: score in powers of two per unit of the first product
-  __shared__ float red[RB][D + 4];           // a unit's accumulators, warps joined
-  __shared__ float red_m[PA_WARPS][RB], red_l[PA_WARPS][RB];
+  extern __shared__ uint2 q_operands[];  // [warp][part][NT][KS][lane]: Q as the first product takes it
   __shared__ int64_t scan[PA_NT];
-  __shared__ int64_t where[2];
+  __shared__ int64_t where[PA_WARPS][2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n = lane >> 2, j = lane & 3;
   const int Hkv = a.c.Hkv, per_b = Hkv * p.blocks;  // units per request
+  uint2* qs = q_operands + warp * (C::QP * NT * KS * 32) + lane;
 
-  // ---- this CTA's share of the line: each thread sums the tiles of a run of requests, then the sums are scanned
+  // ---- the warps' shares of the line: each thread adds up the cost of a run of requests, then the sums are scanned
   const int run = (a.B + PA_NT - 1) / PA_NT;
   int64_t mine = 0;
-  for (int b = tid * run; b < min(a.B, (tid + 1) * run); ++b) mine += pa_span<TILE>(a, b, blockIdx.x == 0).tiles;
+  for (int b = tid * run; b < min(a.B, (tid + 1) * run); ++b)
+    mine += pa_span<TILE>(a, b, blockIdx.x == 0).tiles + PA_UNIT_COST;
   scan[tid] = mine;
   __syncthreads();
   for (int o = 1; o < PA_NT; o <<= 1) {
@@ -198,171 +214,189 @@ __global__ void __launch_bounds__(PA_NT) paged_attention_kernel(const PagedAttnA
     __syncthreads();
   }
   const int64_t total = scan[PA_NT - 1] * per_b;
-  const int64_t ctas = total < gridDim.x ? total : (int64_t)gridDim.x;
-  if (blockIdx.x >= ctas) {
-    if (tid == 0) p.meta[blockIdx.x] = PaMeta{total, -1, 0};
-    return;
-  }
-  int64_t at = blockIdx.x * total / ctas;  // tile on the line
-  const int64_t end = (blockIdx.x + 1) * total / ctas;
-  // the request of `at`, and its first tile on the line
+  const int64_t all = (int64_t)gridDim.x * PA_WARPS, workers = total < all ? total : all;
+  // the request in which each of this CTA's shares begins, and that request's first position
   const int64_t before = scan[tid] - mine;
-  if (at >= before * per_b && at < scan[tid] * per_b) {
+  for (int w = 0; w < PA_WARPS; ++w) {
+    const int64_t x = (int64_t)blockIdx.x * PA_WARPS + w, from = x * total / workers;
+    if (x >= workers || from < before * per_b || from >= scan[tid] * per_b) continue;
     int64_t f = before;
     for (int b = tid * run;; ++b) {
-      const int t = pa_span<TILE>(a, b, false).tiles;
-      if (at < (f + t) * per_b) {
-        where[0] = b;
-        where[1] = f * per_b;
+      const int t = pa_span<TILE>(a, b, false).tiles + PA_UNIT_COST;
+      if (from < (f + t) * per_b) {
+        where[w][0] = b;
+        where[w][1] = f * per_b;
         break;
       }
       f += t;
     }
   }
   __syncthreads();
-  int b = (int)where[0];
-  int64_t first_of_b = where[1];
-  PaMeta meta{total, -1, 0};
+  const int64_t me = (int64_t)blockIdx.x * PA_WARPS + warp;
+  PaMeta meta{-1, 0};
+  if (me >= workers) {
+    if (lane == 0) p.meta[me] = meta;
+    return;
+  }
+  int64_t at = me * total / workers;
+  const int64_t end = (me + 1) * total / workers;
+  int b = (int)where[warp][0];
+  int64_t first_of_b = where[warp][1];
   int rows_done = 0;
+  const int window = a.window > 0 ? a.window : 0x7fffffff;
+  const float cap_inv = a.softcap > 0.f ? 1.f / a.softcap : 0.f, cap2 = a.softcap * PA_LOG2E;
 
   while (at < end) {
     const PaSpan span = pa_span<TILE>(a, b, false);
-    const int in_b = (int)((at - first_of_b) / span.tiles);  // unit within the request
+    const int cost = span.tiles + PA_UNIT_COST;
+    const int in_b = (int)((at - first_of_b) / cost);  // unit within the request
+    const int64_t unit_first = first_of_b + (int64_t)in_b * cost, unit_end = unit_first + cost;
+    // the unit's overhead comes first on the line: a share that ends within it has no tile of the unit
+    const int t0 = max(0, (int)(at - unit_first) - PA_UNIT_COST);
+    const int t1 = (int)((end < unit_end ? end : unit_end) - unit_first) - PA_UNIT_COST;
     const int h = in_b / p.blocks, rb = in_b - h * p.blocks;
-    const int64_t unit_first = first_of_b + (int64_t)in_b * span.tiles, unit_end = unit_first + span.tiles;
-    const int t0 = (int)(at - unit_first), t1 = (int)((end < unit_end ? end : unit_end) - unit_first);
+    const int this_b = b;
+    at = end < unit_end ? end : unit_end;
+    if (in_b == per_b - 1 && at == unit_end) {
+      first_of_b = at;
+      ++b;
+    }
+    if (t1 <= t0) continue;
     const int row0 = rb * RB;
 
-    // ---- queries of the unit, RB rows of D channels, into operand order
-    __syncthreads();
-    for (int r = warp; r < RB; r += PA_WARPS) {
-      const int row = row0 + r, w = row / p.G, g = row - w * p.G;
-      float x[D < 32 ? 1 : D / 32];
-      float amax = 0.f;
-      const int64_t base = (((int64_t)b * a.W + w) * a.Hq + (int64_t)h * p.G + g) * D;
-#pragma unroll
-      for (int i = 0; i < (D < 32 ? 1 : D / 32); ++i) {
-        const int c = i * 32 + lane;
-        x[i] = 0.f;
-        if (row < p.rows && c < D)
-          x[i] = a.q_bf16 ? to_f32(static_cast<const bf16*>(a.q)[base + c]) : static_cast<const float*>(a.q)[base + c];
-        amax = fmaxf(amax, fabsf(x[i]));
+    // ---- where the part's tokens are: a cursor over its 16-token groups, the next page's id asked for ahead
+    const int32_t* table = a.block_table + (int64_t)this_b * a.max_pages;
+    int tok_next = span.start + t0 * TILE;  // of the next group to place
+    const int tok_end = (int)min((int64_t)span.len, (int64_t)span.start + (int64_t)t1 * TILE);
+    int page_at = tok_next / a.c.page_size, off = tok_next - page_at * a.c.page_size;
+    const int page_last = span.len > 0 ? (span.len - 1) / a.c.page_size : -1;
+    int page = page_at <= page_last ? __ldg(table + page_at) : -1;
+    int page_next = page_at < page_last ? __ldg(table + page_at + 1) : -1;
+    // Places the next group: its first token's cache row, -1 where there is nothing to read.
+    auto place = [&]() -> int64_t {
+      int64_t row = -1;
+      if (tok_next < tok_end) {
+        if ((unsigned)page < (unsigned)a.c.num_pages) row = ((int64_t)page * Hkv + h) * a.c.page_size + off;
+        else if (lane == 0) flag_status(a.status, KDA_DEV_PAGE_OOB);
       }
+      tok_next = min(tok_next, 0x7fffffff - 64) + 16;
+      off += 16;
+      if (off == a.c.page_size) {
+        off = 0;
+        ++page_at;
+        page = page_next;
+        page_next = page_at < page_last ? __ldg(table + page_at + 1) : -1;
+      }
+      return row;
+    };
+    const int page_at0 = page_at, off0 = off, page0 = page, page_next0 = page_next;  // to walk again
+
+    // ---- queries of the unit in the first product's operand order: row n of each column block, this lane's pieces
+    float f[NT][2];   // per query row of this lane's results: score in powers of two per unit of the product
+    int last[NT][2];  // and its last seen position
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int row = row0 + t * 8 + n, w = row / p.G, g = row - w * p.G;
+      const int64_t base = (((int64_t)this_b * a.W + w) * a.Hq + (int64_t)h * p.G + g) * D + j * C::KC;
+      float x[C::KL][C::KC];
+      float amax = 0.f;
+#pragma unroll
+      for (int u = 0; u < C::KL; ++u)
+#pragma unroll
+        for (int c = 0; c < C::KC; c += 4) {
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (row < p.rows) {
+            const int64_t e = base + u * 4 * C::KC + c;
+            if (a.q_bf16) {
+              const uint2 r = __ldg(reinterpret_cast<const uint2*>(static_cast<const bf16*>(a.q) + e));
+              v = make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u),
+                              __uint_as_float(r.y << 16), __uint_as_float(r.y & 0xffff0000u));
+            } else {
+              v = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + e));
+            }
+          }
+          x[u][c] = v.x, x[u][c + 1] = v.y, x[u][c + 2] = v.z, x[u][c + 3] = v.w;
+          amax = fmaxf(amax, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
+        }
       float up = 1.f, down = 1.f;
       if constexpr (F8) {  // the row's maximum to [2^14, 2^15)
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
         int e = amax > 0.f ? 14 - ((int)(__float_as_uint(amax) >> 23) - 127) : 0;
         e = max(-100, min(100, e));
         up = __uint_as_float((uint32_t)(e + 127) << 23);
         down = __uint_as_float((uint32_t)(127 - e) << 23);
       }
-      if (lane == 0) qscale[r] = down * a.scale;
 #pragma unroll
-      for (int i = 0; i < (D < 32 ? 1 : D / 32); ++i) {
-        const int c = i * 32 + lane;
-        if (c >= D) break;
-        float v = x[i] * up;
-        // channel c belongs to key piece c / (4 KC), lane quarter jj, step s of the piece, place e of the step
-        const int l = c / (4 * C::KC), jj = c / C::KC % 4, in = c % C::KC, s = l * (C::KC / 4) + in / 4, e = in % 4;
+      for (int u = 0; u < C::KL; ++u)
 #pragma unroll
-        for (int part = 0; part < C::QP; ++part) {
-          uint16_t bits;
-          if constexpr (F8) {
-            const __half hv = __float2half_rn(v);
-            v -= __half2float(hv);
-            bits = __half_as_ushort(hv);
-          } else {
-            const bf16 bv = __float2bfloat16_rn(v);
-            v -= __bfloat162float(bv);
-            bits = __bfloat16_as_ushort(bv);
+        for (int c = 0; c < C::KC; c += 4) {
+          float v0 = x[u][c] * up, v1 = x[u][c + 1] * up, v2 = x[u][c + 2] * up, v3 = x[u][c + 3] * up;
+#pragma unroll
+          for (int part = 0; part < C::QP; ++part) {
+            uint2 r;
+            r.x = split_pair<F8>(v0, v1);
+            r.y = split_pair<F8>(v2, v3);
+            qs[((part * NT + t) * KS + u * (C::KC / 4) + c / 4) * 32] = r;
           }
-          reinterpret_cast<uint16_t*>(&qs[part][r / 8][s][(r % 8) * 4 + jj])[e] = bits;
         }
-      }
-    }
-    __syncthreads();
-
-    // per lane: the two query rows of each 8-row column block, their last seen position and score factor
-    int last[NT][2];
-    float f[NT][2], m[NT][2], l[NT][2];
-    float o[NT][KS][4];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
+      const float own = down * a.scale * (a.softcap > 0.f ? cap_inv : PA_LOG2E);
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const int row = row0 + t * 8 + 2 * j + c;
-        last[t][c] = row < p.rows ? span.len - a.W + row / p.G : -1;
-        f[t][c] = qscale[t * 8 + 2 * j + c] * (a.softcap > 0.f ? 1.f : PA_LOG2E);
+        f[t][c] = __shfl_sync(0xffffffffu, own, (2 * j + c) * 4);
+        const int r = row0 + t * 8 + 2 * j + c;
+        last[t][c] = r < p.rows ? span.len - a.W + r / p.G : -1;
       }
     }
-    const int window = a.window > 0 ? a.window : 0x7fffffff;
     // tokens every row of the unit sees: [all_from, all_to]
-    const int w_lo = row0 / p.G, w_hi = min(p.rows - 1, row0 + RB - 1) / p.G;
-    const int all_to = span.len - a.W + w_lo;
-    const int64_t all_from = (int64_t)span.len - a.W + w_hi - window + 1;
+    const int all_to = span.len - a.W + row0 / p.G;
+    const int64_t all_from = (int64_t)span.len - a.W + min(p.rows - 1, row0 + RB - 1) / p.G - window + 1;
 
-    // ---- walk of the 16-token groups: this warp's group q of tile t is number (t * WARPS + warp) * GPI + q
+    float m[NT][2], mu[NT][2], l[NT][2];  // softmax reference, the same with 0 for -infinity, sum
+    float o[NT][KS][4];
     Piece<C::KC * C::ES> k[GPI][2][C::KL];
     Piece<C::VC * C::ES> v[GPI][4][C::VL];
     float ks[GPI][2], vs[GPI][2];
-    int64_t row_of[GPI], next_row[GPI];  // cache row of the group's first token, -1: nothing to read
-    const int32_t* table = a.block_table + (int64_t)b * a.max_pages;
-    auto locate = [&](int tile, int64_t (&row)[GPI]) {
-#pragma unroll
-      for (int q = 0; q < GPI; ++q) {
-        const int64_t tok = (int64_t)span.start + ((int64_t)(tile * PA_WARPS + warp) * GPI + q) * 16;
-        row[q] = -1;
-        if (tile < t1 && tok < span.len) {
-          const int pg = (int)tok / a.c.page_size, off = (int)tok - pg * a.c.page_size;
-          const int page = __ldg(table + pg);
-          if ((unsigned)page < (unsigned)a.c.num_pages)
-            row[q] = ((int64_t)page * Hkv + h) * a.c.page_size + off;
-          else if (lane == 0)
-            flag_status(a.status, KDA_DEV_PAGE_OOB);
-        }
-      }
-    };
-    // tokens of a group that exist: 16, fewer at the end of the request
-    auto count = [&](int tile, int q) {
-      const int64_t tok = (int64_t)span.start + ((int64_t)(tile * PA_WARPS + warp) * GPI + q) * 16;
-      const int64_t c = span.len - tok;
-      return c < 16 ? (int)c : 16;
-    };
-    auto load_k = [&](int tile, const int64_t (&row)[GPI]) {
-#pragma unroll
-      for (int q = 0; q < GPI; ++q) {
-        const int cnt = row[q] < 0 ? 0 : count(tile, q);
+
+    // Loads of one group whose first token is tok0.  Past the request's end the last token is read again (unseen).
+    auto load_k = [&](int q, int64_t row, int tok0) {
+      if (row < 0) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int tok = n + 8 * i;
-          const uint8_t* at_k = static_cast<const uint8_t*>(a.c.k_pages) + (row[q] + tok) * (D * C::ES);
 #pragma unroll
-          for (int u = 0; u < C::KL; ++u) {
-            if (tok < cnt) k[q][i][u].load(at_k + (u * 4 + j) * (C::KC * C::ES));
-            else k[q][i][u].clear();
-          }
-          if constexpr (F8) {
-            ks[q][i] = tok < cnt ? __ldg(a.c.k_scales + row[q] + tok) : 0.f;
-            vs[q][i] = tok < cnt ? __ldg(a.c.v_scales + row[q] + tok) : 0.f;
-          }
+          for (int u = 0; u < C::KL; ++u) k[q][i][u].clear();
+          ks[q][i] = vs[q][i] = 0.f;
+        }
+        return;
+      }
+      const int over = span.len - 1 - tok0;  // last token there is, within the group
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int64_t r = row + min(n + 8 * i, over);
+        const uint8_t* at_k = static_cast<const uint8_t*>(a.c.k_pages) + r * C::RS + j * (C::KC * C::ES);
+#pragma unroll
+        for (int u = 0; u < C::KL; ++u) k[q][i][u].load(at_k + u * (4 * C::KC * C::ES));
+        if constexpr (F8) {
+          ks[q][i] = __ldg(a.c.k_scales + r);
+          vs[q][i] = __ldg(a.c.v_scales + r);
         }
       }
     };
-    auto load_v = [&](int tile, const int64_t (&row)[GPI]) {
+    auto load_v = [&](int q, int64_t row, int tok0) {
+      if (row < 0) {
 #pragma unroll
-      for (int q = 0; q < GPI; ++q) {
-        const int cnt = row[q] < 0 ? 0 : count(tile, q);
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int tok = 2 * j + (i & 1) + 8 * (i >> 1);
-          const uint8_t* at_v = static_cast<const uint8_t*>(a.c.v_pages) + (row[q] + tok) * (D * C::ES);
+          for (int u = 0; u < C::VL; ++u) v[q][i][u].clear();
+        return;
+      }
+      const int over = span.len - 1 - tok0;
 #pragma unroll
-          for (int u = 0; u < C::VL; ++u) {
-            if (tok < cnt) v[q][i][u].load(at_v + (u * 8 + n) * (C::VC * C::ES));
-            else v[q][i][u].clear();
-          }
-        }
+      for (int i = 0; i < 4; ++i) {
+        const int64_t r = row + min(2 * j + (i & 1) + 8 * (i >> 1), over);
+        const uint8_t* at_v = static_cast<const uint8_t*>(a.c.v_pages) + r * C::RS + n * (C::VC * C::ES);
+#pragma unroll
+        for (int u = 0; u < C::VL; ++u) v[q][i][u].load(at_v + u * (8 * C::VC * C::ES));
       }
     };
     // O^T += V^T P^T for one group; pr[t]: this lane's probabilities (tokens n, n + 8; rows 2j, 2j + 1), times the
@@ -409,17 +443,21 @@ __global__ void __launch_bounds__(PA_NT) paged_attention_kernel(const PagedAttnA
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) m[t][c] = -INFINITY, l[t][c] = 0.f;
+        for (int c = 0; c < 2; ++c) m[t][c] = -INFINITY, mu[t][c] = 0.f, l[t][c] = 0.f;
 #pragma unroll
         for (int s = 0; s < KS; ++s)
 #pragma unroll
           for (int i = 0; i < 4; ++i) o[t][s][i] = 0.f;
       }
-      locate(t0, row_of);
-      load_k(t0, row_of);
-      load_v(t0, row_of);
-      locate(t0 + 1, next_row);
-      for (int tile = t0; tile < t1; ++tile) {
+      int64_t row[GPI];
+      int tok0 = span.start + t0 * TILE;  // of the tile's first group
+#pragma unroll
+      for (int q = 0; q < GPI; ++q) {
+        row[q] = place();
+        load_k(q, row[q], tok0 + 16 * q);
+        load_v(q, row[q], tok0 + 16 * q);
+      }
+      for (int tile = t0; tile < t1; ++tile, tok0 += TILE) {
         // ---- S^T = K Q^T
         float s[GPI][NT][4];
 #pragma unroll
@@ -436,8 +474,10 @@ __global__ void __launch_bounds__(PA_NT) paged_attention_kernel(const PagedAttnA
 #pragma unroll
             for (int q = 0; q < GPI; ++q) {
               if constexpr (F8) {
-                ka[q][0] = half2_of_codes(k[q][0][u].w[st] & 0xffffu), ka[q][2] = half2_of_codes(k[q][0][u].w[st] >> 16);
-                ka[q][1] = half2_of_codes(k[q][1][u].w[st] & 0xffffu), ka[q][3] = half2_of_codes(k[q][1][u].w[st] >> 16);
+                ka[q][0] = half2_of_codes(k[q][0][u].w[st] & 0xffffu);
+                ka[q][1] = half2_of_codes(k[q][1][u].w[st] & 0xffffu);
+                ka[q][2] = half2_of_codes(k[q][0][u].w[st] >> 16);
+                ka[q][3] = half2_of_codes(k[q][1][u].w[st] >> 16);
               } else {
                 ka[q][0] = k[q][0][u].w[2 * st], ka[q][2] = k[q][0][u].w[2 * st + 1];
                 ka[q][1] = k[q][1][u].w[2 * st], ka[q][3] = k[q][1][u].w[2 * st + 1];
@@ -447,35 +487,32 @@ __global__ void __launch_bounds__(PA_NT) paged_attention_kernel(const PagedAttnA
             for (int t = 0; t < NT; ++t)
 #pragma unroll
               for (int part = C::QP - 1; part >= 0; --part) {
-                const uint2 qb = qs[part][t][u * (C::KC / 4) + st][lane];
+                const uint2 qb = qs[((part * NT + t) * KS + u * (C::KC / 4) + st) * 32];
 #pragma unroll
                 for (int q = 0; q < GPI; ++q)
                   mma16816<F8>(s[q][t], ka[q][0], ka[q][1], ka[q][2], ka[q][3], qb.x, qb.y);
               }
           }
         float ksn[GPI][2], vsn[GPI][2];
-        if constexpr (F8) {
-#pragma unroll
-          for (int q = 0; q < GPI; ++q)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) ksn[q][i] = ks[q][i], vsn[q][i] = vs[q][i];
-        }
         int64_t this_row[GPI];
 #pragma unroll
-        for (int q = 0; q < GPI; ++q) this_row[q] = row_of[q], row_of[q] = next_row[q];
-        load_k(tile + 1, row_of);
-        locate(tile + 2, next_row);
+        for (int q = 0; q < GPI; ++q) {
+          this_row[q] = row[q];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) ksn[q][i] = F8 ? ks[q][i] : 1.f, vsn[q][i] = F8 ? vs[q][i] : 1.f;
+          row[q] = place();
+          load_k(q, row[q], tok0 + TILE + 16 * q);
+        }
 
         // ---- scores in powers of two; unseen ones are -infinity
         float top[NT][2];
 #pragma unroll
         for (int t = 0; t < NT; ++t) top[t][0] = top[t][1] = -INFINITY;
-        bool partly[GPI];
 #pragma unroll
         for (int q = 0; q < GPI; ++q) {
-          const int64_t tok0 = (int64_t)span.start + ((int64_t)(tile * PA_WARPS + warp) * GPI + q) * 16;
+          const int tq = tok0 + 16 * q;
           const bool none = this_row[q] < 0;
-          partly[q] = none || tok0 + 15 > all_to || tok0 < all_from;
+          const bool partly = none || tq > all_to - 15 || tq < all_from;
           float lift[2] = {0.f, 0.f};  // about log2 of the value scale
           if constexpr (F8) {
 #pragma unroll
@@ -487,15 +524,29 @@ __global__ void __launch_bounds__(PA_NT) paged_attention_kernel(const PagedAttnA
             for (int i = 0; i < 4; ++i) {
               float x = s[q][t][i] * f[t][i & 1];
               if constexpr (F8) x *= ksn[q][i >> 1];
-              if (a.softcap > 0.f) x = a.softcap * PA_LOG2E * tanhf(x / a.softcap);
-              if (partly[q]) {
-                const int64_t tok = tok0 + n + 8 * (i >> 1);
-                const bool seen = !none && tok <= last[t][i & 1] && tok > (int64_t)last[t][i & 1] - window;
-                x = seen ? x : -INFINITY;
-              }
               s[q][t][i] = x;
-              top[t][i & 1] = fmaxf(top[t][i & 1], F8 ? x + lift[i >> 1] : x);
             }
+          if (a.softcap > 0.f) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) s[q][t][i] = capped(s[q][t][i], cap2);
+          }
+          if (partly) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int tok = tq + n + 8 * (i >> 1);
+                const bool seen = !none && tok <= last[t][i & 1] && tok > (int64_t)last[t][i & 1] - window;
+                s[q][t][i] = seen ? s[q][t][i] : -INFINITY;
+              }
+          }
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              top[t][i & 1] = fmaxf(top[t][i & 1], F8 ? s[q][t][i] + lift[i >> 1] : s[q][t][i]);
         }
         // ---- the reference moves only when a score is far above it (always on the first seen token)
         bool move = false;
@@ -515,6 +566,7 @@ __global__ void __launch_bounds__(PA_NT) paged_attention_kernel(const PagedAttnA
               const float mn = fmaxf(m[t][c], x);
               const float by = m[t][c] == mn ? 1.f : ex2(m[t][c] - mn);  // 0 from -infinity
               m[t][c] = mn;
+              mu[t][c] = mn == -INFINITY ? 0.f : mn;
               l[t][c] *= by;
 #pragma unroll
               for (int st = 0; st < KS; ++st) o[t][st][c] *= by, o[t][st][c + 2] *= by;
@@ -528,8 +580,7 @@ __global__ void __launch_bounds__(PA_NT) paged_attention_kernel(const PagedAttnA
           for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const float mr = m[t][i & 1] == -INFINITY ? 0.f : m[t][i & 1];
-              const float e = ex2(s[q][t][i] - mr);
+              const float e = ex2(s[q][t][i] - mu[t][i & 1]);
               l[t][i & 1] += e;
               pr[t][i] = F8 ? e * vsn[q][i >> 1] : e;
             }
@@ -546,8 +597,8 @@ __global__ void __launch_bounds__(PA_NT) paged_attention_kernel(const PagedAttnA
                 for (int part = 0; part < C::PP; ++part) split_pair<F8>(r0, r1);
                 pr[t][i] -= r0, pr[t][i + 1] -= r1;
               }
-            const int64_t tok0 = (int64_t)span.start + ((int64_t)(tile * PA_WARPS + warp) * GPI + q) * 16;
-            const int cnt = this_row[q] < 0 ? 0 : count(tile, q);
+            const int tq = tok0 + 16 * q;
+            const int cnt = this_row[q] < 0 ? 0 : min(16, span.len - tq);
 #pragma unroll 1
             for (int tk = 0; tk < cnt; ++tk) {
               float pt[NT][2];
@@ -556,7 +607,7 @@ __global__ void __launch_bounds__(PA_NT) paged_attention_kernel(const PagedAttnA
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                   pt[t][c] = __shfl_sync(0xffffffffu, tk < 8 ? pr[t][c] : pr[t][2 + c], (tk & 7) * 4 + j);
-                  const int64_t tok = tok0 + tk;
+                  const int tok = tq + tk;
                   if (!(tok <= last[t][c] && tok > (int64_t)last[t][c] - window)) pt[t][c] = -1.f;  // not seen
                 }
 #pragma unroll
@@ -579,8 +630,8 @@ __global__ void __launch_bounds__(PA_NT) paged_attention_kernel(const PagedAttnA
                 }
             }
           }
+          load_v(q, row[q], tok0 + TILE + 16 * q);
         }
-        load_v(tile + 1, row_of);
       }
       bool nan = false;
 #pragma unroll
@@ -591,9 +642,13 @@ __global__ void __launch_bounds__(PA_NT) paged_attention_kernel(const PagedAttnA
           for (int i = 0; i < 4; ++i) nan |= isnan(o[t][s][i]);
       if (careful || !__any_sync(0xffffffffu, nan)) break;
       careful = true;
+      tok_next = span.start + t0 * TILE;
+      page_at = page_at0, off = off0, page = page0, page_next = page_next0;
     }
 
-    // ---- join the four warps
+    // ---- the part's sums, and its rows: this lane has channels (8 u + n) VC .. of rows 2j and 2j + 1 of each block
+    const bool whole = t0 == 0 && t1 == span.tiles;
+    const int64_t part = (me * 2 + (t0 == 0 ? 1 : 0)) * RB;  // second place: the part that starts its unit
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -603,114 +658,154 @@ __global__ void __launch_bounds__(PA_NT) paged_attention_kernel(const PagedAttnA
         x += __shfl_xor_sync(0xffffffffu, x, 8);
         x += __shfl_xor_sync(0xffffffffu, x, 16);
         if (m[t][c] == -INFINITY && !(x == 0.f)) m[t][c] = 0.f;  // nothing but NaN scores: let them through
-        if (n == 0) red_l[warp][t * 8 + 2 * j + c] = x, red_m[warp][t * 8 + 2 * j + c] = m[t][c];
-      }
-    __syncthreads();
-#pragma unroll 1
-    for (int w = 0; w < PA_WARPS; ++w) {
-      if (warp == w) {
+        const bool none = m[t][c] == -INFINITY;
+        const int r = t * 8 + 2 * j + c, qrow = row0 + r;
+        const float by = whole ? (none ? 0.f : 1.f / x) : 1.f;
+        if (whole && qrow >= p.rows) continue;
+        const int w = qrow / p.G, g = qrow - w * p.G;
+        const int64_t head = ((int64_t)this_b * a.W + w) * a.Hq + (int64_t)h * p.G + g;
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int u = 0; u < C::VL; ++u) {
+          float y[C::VC];
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int r = t * 8 + 2 * j + c;
-            const float mt = fmaxf(fmaxf(red_m[0][r], red_m[1][r]), fmaxf(red_m[2][r], red_m[3][r]));
-            const float by = m[t][c] == -INFINITY ? 0.f : ex2(m[t][c] - mt);
+          for (int i = 0; i < C::VC; ++i) y[i] = o[t][u * (C::VC / 2) + i / 2][c + 2 * (i & 1)] * by;
+          const int ch = (u * 8 + n) * C::VC;
+          if (whole && a.out_bf16) {
+            bf16* out = static_cast<bf16*>(a.out) + head * D + ch;
 #pragma unroll
-            for (int u = 0; u < C::VL; ++u)
+            for (int i = 0; i < C::VC; i += 2) {
+              const __nv_bfloat162 z = __floats2bfloat162_rn(y[i], y[i + 1]);
+              reinterpret_cast<__nv_bfloat162*>(out)[i / 2] = z;
+            }
+          } else {
+            float* out = whole ? static_cast<float*>(a.out) + head * D + ch : p.part_o + (part + r) * D + ch;
 #pragma unroll
-              for (int mt2 = 0; mt2 < C::VC / 2; ++mt2)
-#pragma unroll
-                for (int hh = 0; hh < 2; ++hh) {
-                  const int ch = (u * 8 + n) * C::VC + 2 * mt2 + hh;
-                  const float x = m[t][c] == -INFINITY ? 0.f : o[t][u * (C::VC / 2) + mt2][c + 2 * hh] * by;
-                  red[r][ch] = w == 0 ? x : red[r][ch] + x;
-                }
+            for (int i = 0; i < C::VC; i += 2) reinterpret_cast<float2*>(out)[i / 2] = make_float2(y[i], y[i + 1]);
           }
-      }
-      __syncthreads();
-    }
-    const bool whole = t0 == 0 && t1 == span.tiles;
-    const int slot = t0 == 0 ? 1 : 0;  // 1: this part starts its unit
-    for (int e = tid; e < RB * D; e += PA_NT) {
-      const int r = e / D, c = e - r * D, row = row0 + r;
-      float mt = -INFINITY, lt = 0.f;
-#pragma unroll
-      for (int w = 0; w < PA_WARPS; ++w) mt = fmaxf(mt, red_m[w][r]);
-#pragma unroll
-      for (int w = 0; w < PA_WARPS; ++w) lt += red_m[w][r] == -INFINITY ? 0.f : red_l[w][r] * ex2(red_m[w][r] - mt);
-      if (whole) {
-        if (row < p.rows) {
-          const int w = row / p.G, g = row - w * p.G;
-          const int64_t head = ((int64_t)b * a.W + w) * a.Hq + (int64_t)h * p.G + g;
-          const float x = mt == -INFINITY ? 0.f : red[r][c] / lt;
-          if (a.out_bf16) static_cast<bf16*>(a.out)[head * D + c] = __float2bfloat16_rn(x);
-          else static_cast<float*>(a.out)[head * D + c] = x;
-          if (c == 0 && a.lse) a.lse[head] = mt == -INFINITY ? -INFINITY : (mt + log2f(lt)) * PA_LN2;
         }
-      } else {
-        const int64_t base = ((int64_t)blockIdx.x * 2 + slot) * RB + r;
-        p.part_o[base * D + c] = red[r][c];
-        if (c == 0) p.part_ml[base * 2] = mt, p.part_ml[base * 2 + 1] = lt;
+        if (n == 0) {
+          if (!whole) *reinterpret_cast<float2*>(p.part_ml + (part + r) * 2) = make_float2(m[t][c], x);
+          else if (a.lse) a.lse[head] = none ? -INFINITY : (m[t][c] + log2f(x)) * PA_LN2;
+        }
       }
-    }
-    if (whole) rows_done += min(RB, p.rows - row0);
-    if (t0 == 0 && !whole) {
-      // the unit goes on in the following CTAs; its last tile is in the CTA whose share holds it
-      meta.unit = (b * Hkv + h) * p.blocks + rb;
-      int64_t e = (unit_end - 1) * ctas / total;  // share boundaries are floors: at most one off
-      while (e * total / ctas > unit_end - 1) --e;
-      while ((e + 1) * total / ctas <= unit_end - 1) ++e;
-      meta.end_cta = (int)e;
-    }
-    at = first_of_b + (int64_t)in_b * span.tiles + t1;
-    if (in_b == per_b - 1 && t1 == span.tiles) {
-      first_of_b = at;
-      ++b;
+    if (whole) {
+      rows_done += min(RB, p.rows - row0);
+    } else if (t0 == 0) {
+      // the unit goes on in the following shares; its last tile is at unit_end - 1 on the line
+      meta.unit = (this_b * Hkv + h) * p.blocks + rb;
+      int64_t e = (unit_end - 1) * workers / total;  // share boundaries are floors: at most one off
+      while (e * total / workers > unit_end - 1) --e;
+      while ((e + 1) * total / workers <= unit_end - 1) ++e;
+      meta.end = (int)e;
     }
   }
-  if (tid == 0) {
-    p.meta[blockIdx.x] = meta;
+  if (lane == 0) {
+    p.meta[me] = meta;
     add_work(a.status, rows_done);
   }
 }
 
 // ---------------------------------------------------------------- join
 
-// CTA (x, y) joins query rows y of the unit that main CTA x starts and others go on with: the parts' maxima and sums
-// first, then their accumulators in CTA order.
+constexpr int PA_JOIN_NT = 512, PA_JOIN_ROWS = 4;
+
+// CTA (x, y) joins rows 4 y .. 4 y + 3 of the units that the warps of main CTA x start and others go on with.  Its 16
+// warps take the parts in turn (a long request has over a hundred, and one warp's loads would wait for one another),
+// every one weighted by its maximum against the rows' overall one; then the warps' sums are added in warp order.
 template <int D, int RB>
-__global__ void __launch_bounds__(128) paged_attention_join_kernel(const PagedAttnArgs a, const PaPlan p) {
+__global__ void __launch_bounds__(PA_JOIN_NT) paged_attention_join_kernel(const PagedAttnArgs a, const PaPlan p) {
+  constexpr int JW = PA_JOIN_NT / 32, JR = PA_JOIN_ROWS;
+  constexpr int LANES = JR * D / 4 < 32 ? JR * D / 4 : 32;  // lanes with a float4 of the JR x D block
+  constexpr int VEC = JR * D / 4 / LANES;                   // float4 per lane
+  __shared__ float4 sum_o[JW][VEC][LANES];
+  __shared__ float sum_l[JW][JR], top[JW][JR];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const PaMeta meta = p.meta[blockIdx.x];
-  if (meta.unit < 0) return;
-  const int rb = meta.unit % p.blocks, bh = meta.unit / p.blocks, h = bh % a.c.Hkv, b = bh / a.c.Hkv;
-  constexpr int ROWS = 128 / D;  // rows of a CTA
-  const int r = blockIdx.y * ROWS + threadIdx.x / D, c = threadIdx.x % D, row = rb * RB + r;
-  if (row >= p.rows) return;
-  const int x0 = blockIdx.x, x1 = meta.end_cta;
-  auto at = [&](int x) { return ((int64_t)x * 2 + (x == x0 ? 1 : 0)) * RB + r; };
-  float m = -INFINITY;
-  for (int x = x0; x <= x1; ++x) m = fmaxf(m, p.part_ml[at(x) * 2]);
-  float l = 0.f, o = 0.f;
-  if (m != -INFINITY) {
-#pragma unroll 4
-    for (int x = x0; x <= x1; ++x) {
-      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + at(x) * 2);
-      const float v = p.part_o[at(x) * D + c];
-      const float by = ml.x == -INFINITY ? 0.f : ex2(ml.x - m);
-      l += ml.y * by;
-      o += v * by;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r0 = blockIdx.y * JR;
+  for (int w = 0; w < PA_WARPS; ++w) {
+    const int x0 = blockIdx.x * PA_WARPS + w;
+    const PaMeta meta = p.meta[x0];
+    if (meta.unit < 0) continue;
+    const int rb = meta.unit % p.blocks, bh = meta.unit / p.blocks, h = bh % a.c.Hkv, b = bh / a.c.Hkv;
+    const int row0 = rb * RB + r0;
+    if (row0 >= p.rows) continue;
+    const int parts = meta.end - x0 + 1;
+    auto at = [&](int i) { return ((int64_t)(x0 + i) * 2 + (i == 0 ? 1 : 0)) * RB + r0; };
+    // the rows' overall maxima: 8 parts of 4 rows at a time
+    float m = -INFINITY;
+    for (int i = threadIdx.x / JR; i < parts; i += PA_JOIN_NT / JR)
+      m = fmaxf(m, p.part_ml[(at(i) + threadIdx.x % JR) * 2]);
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+    if (lane < JR) top[warp][lane] = m;
+    __syncthreads();
+    float mr[JR], l[JR];
+#pragma unroll
+    for (int r = 0; r < JR; ++r) {
+      mr[r] = -INFINITY;
+      l[r] = 0.f;
+#pragma unroll
+      for (int i = 0; i < JW; ++i) mr[r] = fmaxf(mr[r], top[i][r]);
     }
-    o /= l;
-  }
-  const int w = row / p.G, g = row - w * p.G;
-  const int64_t head = ((int64_t)b * a.W + w) * a.Hq + (int64_t)h * p.G + g;
-  if (a.out_bf16) static_cast<bf16*>(a.out)[head * D + c] = __float2bfloat16_rn(o);
-  else static_cast<float*>(a.out)[head * D + c] = o;
-  if (c == 0) {
-    if (a.lse) a.lse[head] = m == -INFINITY ? -INFINITY : (m + log2f(l)) * PA_LN2;
-    add_work(a.status, 1);
+    float4 o[VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) o[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int li = lane < LANES ? lane : 0;
+#pragma unroll 2
+    for (int i = warp; i < parts; i += JW) {
+      float by[JR];
+      float4 x[VEC];
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) x[v] = *reinterpret_cast<const float4*>(p.part_o + at(i) * D + (v * LANES + li) * 4);
+#pragma unroll
+      for (int r = 0; r < JR; ++r) {
+        const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (at(i) + r) * 2);
+        by[r] = ml.x == -INFINITY ? 0.f : ex2(ml.x - mr[r]);
+        l[r] += ml.y * by[r];
+      }
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) {
+        const int r = (v * LANES + li) * 4 / D;
+        float b_r = by[0];
+#pragma unroll
+        for (int q = 1; q < JR; ++q) b_r = r == q ? by[q] : b_r;
+        if (b_r != 0.f)  // a part that saw nothing holds zeros
+          o[v].x += x[v].x * b_r, o[v].y += x[v].y * b_r, o[v].z += x[v].z * b_r, o[v].w += x[v].w * b_r;
+      }
+    }
+    if (lane < LANES) {
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) sum_o[warp][v][lane] = o[v];
+    }
+    if (lane < JR) {
+      float own = l[0];
+#pragma unroll
+      for (int r = 1; r < JR; ++r) own = lane == r ? l[r] : own;
+      sum_l[warp][lane] = own;
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < JR * D; e += PA_JOIN_NT) {
+      const int r = e / D, c = e - r * D, row = row0 + r;
+      if (row < p.rows && r0 + r < RB) {
+        float x = 0.f, lr = 0.f;
+#pragma unroll
+        for (int i = 0; i < JW; ++i) x += reinterpret_cast<const float*>(sum_o[i])[e], lr += sum_l[i][r];
+        float m_r = mr[0];
+#pragma unroll
+        for (int q = 1; q < JR; ++q) m_r = r == q ? mr[q] : m_r;
+        const bool none = m_r == -INFINITY;
+        const int wt = row / p.G, g = row - wt * p.G;
+        const int64_t head = ((int64_t)b * a.W + wt) * a.Hq + (int64_t)h * p.G + g;
+        x = none ? 0.f : x / lr;
+        if (a.out_bf16) static_cast<bf16*>(a.out)[head * D + c] = __float2bfloat16_rn(x);
+        else static_cast<float*>(a.out)[head * D + c] = x;
+        if (c == 0) {
+          if (a.lse) a.lse[head] = none ? -INFINITY : (m_r + log2f(lr)) * PA_LN2;
+          add_work(a.status, 1);
+        }
+      }
+    }
+    __syncthreads();
   }
 }
 
@@ -719,34 +814,32 @@ __global__ void __launch_bounds__(128) paged_attention_join_kernel(const PagedAt
 template <int D, bool F8, int NT, bool FINE>
 cudaError_t pa_launch(const PagedAttnArgs& a, const PaPlan& p, int sms, cudaStream_t s) {
   using C = PaCfg<D, F8, NT, FINE>;
-  static int resident = 0;  // CTAs of this kernel per SM
-  if (!resident) {
-    int n = 0;
-    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, paged_attention_kernel<D, F8, NT, FINE>,
-                                                                        PA_NT, 0);
+  auto kernel = paged_attention_kernel<D, F8, NT, FINE>;
+  if (C::SMEM > 40 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
     if (e != cudaSuccess) return e;
-    resident = n < 1 ? 1 : n > 4 ? 4 : n;
   }
-  // no more CTAs than tiles the longest possible lengths could give
-  const int64_t most = (int64_t)a.B * a.c.Hkv * p.blocks * (((int64_t)a.max_pages * a.c.page_size) / C::TILE + 1);
-  int64_t ctas = (int64_t)resident * sms;
-  if (ctas > PA_MAX_CTAS) ctas = PA_MAX_CTAS;
-  if (ctas > most) ctas = most;
-  paged_attention_kernel<D, F8, NT, FINE><<<(unsigned)ctas, PA_NT, 0, s>>>(a, p);
-  cudaError_t e = cudaGetLastError();
+  // no more warps than positions on the longest possible line
+  const int64_t tiles = (int64_t)a.max_pages * a.c.page_size / C::TILE + 1 + PA_UNIT_COST;
+  int64_t ctas = pa_resident(NT) * (sms < PA_SMS ? sms : PA_SMS);
+  const int64_t units = (int64_t)a.B * a.c.Hkv * p.blocks;
+  if (tiles < ctas * PA_WARPS && units * tiles < ctas * PA_WARPS) ctas = (units * tiles + PA_WARPS - 1) / PA_WARPS;
+  kernel<<<(unsigned)ctas, PA_NT, C::SMEM, s>>>(a, p);
+  const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  constexpr int ROWS = 128 / D;
-  return launch_pdl(paged_attention_join_kernel<D, C::RB>, dim3((unsigned)ctas, (C::RB + ROWS - 1) / ROWS), dim3(128), 0,
-                    s, a, p);
+  const int rows = p.rows < C::RB ? p.rows : C::RB;
+  return launch_pdl(paged_attention_join_kernel<D, C::RB>, dim3((unsigned)ctas, (rows + PA_JOIN_ROWS - 1) / PA_JOIN_ROWS),
+                    dim3(PA_JOIN_NT), 0, s, a, p);
 }
 
 template <int D, bool F8, bool FINE>
 cudaError_t pa_rows(const PagedAttnArgs& a, const PaPlan& p, int sms, cudaStream_t s) {
-  switch (pa_nt(p.rows)) {
-    case 1: return pa_launch<D, F8, 1, FINE>(a, p, sms, s);
-    case 2: return pa_launch<D, F8, 2, FINE>(a, p, sms, s);
-    default: return pa_launch<D, F8, 4, FINE>(a, p, sms, s);
+  const int nt = pa_nt(p.rows, FINE);
+  if (nt == 1) return pa_launch<D, F8, 1, FINE>(a, p, sms, s);
+  if constexpr (!FINE) {
+    if (nt == 4) return pa_launch<D, F8, 4, FINE>(a, p, sms, s);
   }
+  return pa_launch<D, F8, 2, FINE>(a, p, sms, s);
 }
 
 template <bool F8, bool FINE>
