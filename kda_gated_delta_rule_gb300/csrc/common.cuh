@@ -29,6 +29,13 @@ __device__ __forceinline__ void add_work(int32_t* st, int32_t n) {
   if (st && n) atomicAdd(reinterpret_cast<unsigned int*>(st + 1), static_cast<unsigned int>(n));
 }
 
+// First statement of a kernel launched with launch_pdl: waits for the kernels before it in the stream, then lets the
+// next one's blocks take their places as this one's finish.
+__device__ __forceinline__ void pdl_begin() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // Streaming (evict-first) 128-bit global accesses for state tiles that are touched once per launch.
 __device__ __forceinline__ float4 ld_stream(const float* p) { return __ldcs(reinterpret_cast<const float4*>(p)); }
 __device__ __forceinline__ void st_stream(float* p, float4 v) { __stcs(reinterpret_cast<float4*>(p), v); }

@@ -58,6 +58,7 @@ __device__ __forceinline__ int64_t slot_row(int64_t slot, const KvCacheArgs& c) 
 template <int D, int R, bool INBF, bool F8>
 __global__ void __launch_bounds__(KV_NT) kv_write_kernel(const KvWriteArgs p, int chunks) {
   constexpr int LPR = D / 8, NG = KV_NT / LPR;
+  pdl_begin();
   const int lane = threadIdx.x & 31, lr = threadIdx.x % LPR;
   const unsigned gid = blockIdx.x * (unsigned)NG + threadIdx.x / LPR;
   const int64_t t = gid / (unsigned)chunks;
@@ -122,6 +123,7 @@ __global__ void __launch_bounds__(KV_NT) kv_write_kernel(const KvWriteArgs p, in
 template <int D, int R, bool F8, bool OUTBF>
 __global__ void __launch_bounds__(KV_NT) kv_read_kernel(const KvReadArgs p, int chunks) {
   constexpr int LPR = D / 8, NG = KV_NT / LPR;
+  pdl_begin();
   const int lr = threadIdx.x % LPR;
   const unsigned gid = blockIdx.x * (unsigned)NG + threadIdx.x / LPR;
   const int64_t t = gid / (unsigned)chunks;
@@ -188,12 +190,9 @@ cudaError_t write_r(const KvWriteArgs& a, bool f8, cudaStream_t s) {
   const int chunks = (2 * a.c.Hkv + R - 1) / R;
   const int64_t blocks = (a.T * chunks + NG - 1) / NG;
   if (blocks * NG > 0x7fffffff) return cudaErrorInvalidValue;
-  const unsigned g = (unsigned)blocks;
-  if (f8 && a.in_bf16) kv_write_kernel<D, R, true, true><<<g, KV_NT, 0, s>>>(a, chunks);
-  else if (f8) kv_write_kernel<D, R, false, true><<<g, KV_NT, 0, s>>>(a, chunks);
-  else if (a.in_bf16) kv_write_kernel<D, R, true, false><<<g, KV_NT, 0, s>>>(a, chunks);
-  else kv_write_kernel<D, R, false, false><<<g, KV_NT, 0, s>>>(a, chunks);
-  return cudaGetLastError();
+  auto kernel = f8 ? (a.in_bf16 ? kv_write_kernel<D, R, true, true> : kv_write_kernel<D, R, false, true>)
+                   : (a.in_bf16 ? kv_write_kernel<D, R, true, false> : kv_write_kernel<D, R, false, false>);
+  return launch_pdl(kernel, dim3((unsigned)blocks), dim3(KV_NT), 0, s, a, chunks);
 }
 
 template <int D, int R>
@@ -202,12 +201,9 @@ cudaError_t read_r(const KvReadArgs& a, bool f8, cudaStream_t s) {
   const int chunks = (2 * a.c.Hkv + R - 1) / R;
   const int64_t blocks = (a.T * chunks + NG - 1) / NG;
   if (blocks * NG > 0x7fffffff) return cudaErrorInvalidValue;
-  const unsigned g = (unsigned)blocks;
-  if (f8 && a.out_bf16) kv_read_kernel<D, R, true, true><<<g, KV_NT, 0, s>>>(a, chunks);
-  else if (f8) kv_read_kernel<D, R, true, false><<<g, KV_NT, 0, s>>>(a, chunks);
-  else if (a.out_bf16) kv_read_kernel<D, R, false, true><<<g, KV_NT, 0, s>>>(a, chunks);
-  else kv_read_kernel<D, R, false, false><<<g, KV_NT, 0, s>>>(a, chunks);
-  return cudaGetLastError();
+  auto kernel = f8 ? (a.out_bf16 ? kv_read_kernel<D, R, true, true> : kv_read_kernel<D, R, true, false>)
+                   : (a.out_bf16 ? kv_read_kernel<D, R, false, true> : kv_read_kernel<D, R, false, false>);
+  return launch_pdl(kernel, dim3((unsigned)blocks), dim3(KV_NT), 0, s, a, chunks);
 }
 
 template <int D>

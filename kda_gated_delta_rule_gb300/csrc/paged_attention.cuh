@@ -195,6 +195,7 @@ __global__ void __launch_bounds__(PA_NT, pa_resident(NT)) paged_attention_kernel
   extern __shared__ uint2 q_operands[];  // [warp][part][NT][KS][lane]: Q as the first product takes it
   __shared__ int64_t scan[PA_NT];
   __shared__ int64_t where[PA_WARPS][2];
+  pdl_begin();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n = lane >> 2, j = lane & 3;
   const int Hkv = a.c.Hkv, per_b = Hkv * p.blocks;  // units per request
@@ -719,7 +720,7 @@ __global__ void __launch_bounds__(PA_JOIN_NT) paged_attention_join_kernel(const 
   constexpr int VEC = JR * D / 4 / LANES;                   // float4 per lane
   __shared__ float4 sum_o[JW][VEC][LANES];
   __shared__ float sum_l[JW][JR], top[JW][JR];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  pdl_begin();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r0 = blockIdx.y * JR;
   for (int w = 0; w < PA_WARPS; ++w) {
     const int x0 = blockIdx.x * PA_WARPS + w;
@@ -824,8 +825,7 @@ cudaError_t pa_launch(const PagedAttnArgs& a, const PaPlan& p, int sms, cudaStre
   int64_t ctas = pa_resident(NT) * (sms < PA_SMS ? sms : PA_SMS);
   const int64_t units = (int64_t)a.B * a.c.Hkv * p.blocks;
   if (tiles < ctas * PA_WARPS && units * tiles < ctas * PA_WARPS) ctas = (units * tiles + PA_WARPS - 1) / PA_WARPS;
-  kernel<<<(unsigned)ctas, PA_NT, C::SMEM, s>>>(a, p);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_pdl(kernel, dim3((unsigned)ctas), dim3(PA_NT), C::SMEM, s, a, p);
   if (e != cudaSuccess) return e;
   const int rows = p.rows < C::RB ? p.rows : C::RB;
   return launch_pdl(paged_attention_join_kernel<D, C::RB>, dim3((unsigned)ctas, (rows + PA_JOIN_ROWS - 1) / PA_JOIN_ROWS),

@@ -1,290 +1,412 @@
 // Per-head RMS norm of queries and keys with the position rotation, and its gradient.
 //
 // Forward, per row x (one token, one head) with weight w:  y = R(p) (x r w),  r = (mean x^2 + eps)^-1/2.
-// Backward, with g = R(p)^T dy and u = x r:  dx = r (g w - u mean(g w u)),  dw = sum over rows of g u.
+// Backward, with g = R(p)^T dy:  dx = r g w - x r^3 mean(g w x),  dw = sum over rows of g x r.
 // R(p) only mixes the two channels of a pair, so its transpose is the rotation by the opposite angle.
 //
-// Both are bound by HBM (about 10 operations per element against 4 to 6 bytes).  A row lies on D/8 lanes; a
-// group of lanes takes R rows of one token, issues all its loads before the first reduction and reads the
-// token's angles once for them.  In the rotation the partner channel of the half-split pairing is eight-channel
-// aligned (rot is a multiple of 16), so it sits in the same register of another lane: one shuffle per channel;
-// neighbouring pairs never leave the lane.
+// Both are bound by HBM (about 10 operations per element against 4 to 6 bytes), but only if the instructions are few.
+// A row lies on D/8 lanes.  A lane has two runs of four channels, placed so that both channels of a pair are its own:
+// lane i of the rotated part has channels 4i .. 4i + 3 and the same plus rot / 2 (half-split pairing), or
+// 8i .. 8i + 7 (neighbouring pairs); either way its four pairs are 4i .. 4i + 3, one 16-byte read of each table, and
+// its eight values are held as four float2, the pairs' lower channels in the first two and the upper ones in the others,
+// so the arithmetic is on two values per instruction.  (With eight consecutive channels per lane the half-split
+// rotation took a shuffle per channel and twice the table bytes: 41 us for 8192 x 40 x 128 bf16 rows; now NORM_FWD_US.)
+// A group of lanes takes R rows of one token and one kind, queries or keys, issues all its loads before the first
+// reduction, reads the angles and the weight once for them, and reduces the rows' sums together.
 #include "launch.h"
 #include "rows8.cuh"
 
 namespace kda {
 
-constexpr int NORM_NT = 128;
+constexpr int NORM_NT = 128, NORM_RESIDENT = 8, NORM_R = 4;
+constexpr int NORM_BWD_NT = 256, NORM_BWD_RESIDENT = 2, NORM_BWD_R = 4;
 
-// The token's angles as this lane needs them: cos and sin per channel (half-split) or per pair (interleaved,
-// entries 0..3).  Lanes past the rotated channels keep cos = 1, sin = 0.
-struct Angles {
-  float c[8], s[8];
+// ---- arithmetic on two fp32 at once
+__device__ __forceinline__ unsigned long long bits2(float2 a) { return *reinterpret_cast<unsigned long long*>(&a); }
+__device__ __forceinline__ float2 pair2(unsigned long long b) { return *reinterpret_cast<float2*>(&b); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+  return pair2(r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+  return pair2(r);
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// A lane's channels, and its four pairs.
+struct NormLane {
+  int a, b;  // first channel of each run
+  int pair;  // first pair, or -1 where the channels are not rotated
 };
-
-__device__ __forceinline__ void load_angles(Angles& a, const NormArgs& p, int pos, int lane_in_row) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) a.c[i] = 1.f, a.s[i] = 0.f;
-  const int c0 = lane_in_row * 8, half = p.rot / 2;
-  if (c0 >= p.rot) return;
-  if (p.interleaved) {
-    const int64_t at = (int64_t)pos * half + c0 / 2;
-    const float4 c = __ldg(reinterpret_cast<const float4*>(p.cos + at));
-    const float4 s = __ldg(reinterpret_cast<const float4*>(p.sin + at));
-    a.c[0] = c.x, a.c[1] = c.y, a.c[2] = c.z, a.c[3] = c.w;
-    a.s[0] = s.x, a.s[1] = s.y, a.s[2] = s.z, a.s[3] = s.w;
+template <int D, bool IL>
+__device__ __forceinline__ NormLane norm_lane(int lr, int rot) {
+  NormLane n;
+  if (lr * 8 >= rot) {
+    n.a = lr * 8, n.b = lr * 8 + 4, n.pair = -1;
   } else {
-    const int64_t at = (int64_t)pos * half + (c0 < half ? c0 : c0 - half);
-    const float sign = c0 < half ? -1.f : 1.f;  // the lower channel of a pair gets -sin, the upper +sin
-    const float4* cp = reinterpret_cast<const float4*>(p.cos + at);
-    const float4* sp = reinterpret_cast<const float4*>(p.sin + at);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float4 c = __ldg(cp + i), s = __ldg(sp + i);
-      a.c[4 * i] = c.x, a.c[4 * i + 1] = c.y, a.c[4 * i + 2] = c.z, a.c[4 * i + 3] = c.w;
-      a.s[4 * i] = sign * s.x, a.s[4 * i + 1] = sign * s.y, a.s[4 * i + 2] = sign * s.z, a.s[4 * i + 3] = sign * s.w;
-    }
+    n.pair = 4 * lr;
+    n.a = IL ? 8 * lr : 4 * lr;
+    n.b = IL ? 8 * lr + 4 : 4 * lr + rot / 2;
+  }
+  return n;
+}
+// Four channels of each run (e0 .. e3, f0 .. f3) as the four float2: half-split pairs are (e_i, f_i), neighbouring ones
+// (e0, e1), (e2, e3), (f0, f1), (f2, f3).  spread() and gather() are each other's inverse.
+template <bool IL>
+__device__ __forceinline__ void spread(float2 (&x)[4], float4 e, float4 f) {
+  if (IL) {
+    x[0] = make_float2(e.x, e.z), x[1] = make_float2(f.x, f.z);
+    x[2] = make_float2(e.y, e.w), x[3] = make_float2(f.y, f.w);
+  } else {
+    x[0] = make_float2(e.x, e.y), x[1] = make_float2(e.z, e.w);
+    x[2] = make_float2(f.x, f.y), x[3] = make_float2(f.z, f.w);
+  }
+}
+template <bool IL>
+__device__ __forceinline__ void gather(const float2 (&x)[4], float4& e, float4& f) {
+  if (IL) {
+    e = make_float4(x[0].x, x[2].x, x[0].y, x[2].y);
+    f = make_float4(x[1].x, x[3].x, x[1].y, x[3].y);
+  } else {
+    e = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
+    f = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
   }
 }
 
-// Turns this lane's eight channels by +angle (sgn = 1) or -angle (sgn = -1).  All lanes of the warp call it.
-__device__ __forceinline__ void rotate8(float (&x)[8], const Angles& a, const NormArgs& p, int partner_lane,
-                                        float sgn) {
-  if (p.rot == 0) return;
-  if (p.interleaved) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float u = x[2 * i], v = x[2 * i + 1], s = sgn * a.s[i];
-      x[2 * i] = u * a.c[i] - v * s;
-      x[2 * i + 1] = u * s + v * a.c[i];
-    }
+template <bool BF>
+struct RawRow;  // a lane's eight channels as loaded (plain loads: a call may work in place)
+template <>
+struct RawRow<true> {
+  uint2 a, b;
+  __device__ __forceinline__ void load(const void* base, int64_t row, const NormLane& n) {
+    const bf16* p = static_cast<const bf16*>(base) + row;
+    a = *reinterpret_cast<const uint2*>(p + n.a);
+    b = *reinterpret_cast<const uint2*>(p + n.b);
+  }
+  __device__ __forceinline__ float4 run(uint2 v) const {
+    float4 f;
+    unpack_bf16x2(v.x, f.x, f.y);
+    unpack_bf16x2(v.y, f.z, f.w);
+    return f;
+  }
+  template <bool IL>
+  __device__ __forceinline__ void widen(float2 (&x)[4]) const { spread<IL>(x, run(a), run(b)); }
+};
+template <>
+struct RawRow<false> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const void* base, int64_t row, const NormLane& n) {
+    const float* p = static_cast<const float*>(base) + row;
+    a = *reinterpret_cast<const float4*>(p + n.a);
+    b = *reinterpret_cast<const float4*>(p + n.b);
+  }
+  template <bool IL>
+  __device__ __forceinline__ void widen(float2 (&x)[4]) const { spread<IL>(x, a, b); }
+};
+template <bool BF, bool IL>
+__device__ __forceinline__ void store_row(void* base, int64_t row, const NormLane& n, const float2 (&x)[4]) {
+  float4 e, f;
+  gather<IL>(x, e, f);
+  if constexpr (BF) {
+    bf16* p = static_cast<bf16*>(base) + row;
+    *reinterpret_cast<uint2*>(p + n.a) = make_uint2(pack_bf16x2(e.x, e.y), pack_bf16x2(e.z, e.w));
+    *reinterpret_cast<uint2*>(p + n.b) = make_uint2(pack_bf16x2(f.x, f.y), pack_bf16x2(f.z, f.w));
   } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float other = __shfl_sync(0xffffffffu, x[i], partner_lane);
-      x[i] = x[i] * a.c[i] + other * (sgn * a.s[i]);
-    }
+    float* p = static_cast<float*>(base) + row;
+    *reinterpret_cast<float4*>(p + n.a) = e;
+    *reinterpret_cast<float4*>(p + n.b) = f;
   }
 }
 
-// Warp lane that holds the partner channels of this lane's (half-split pairing).
-__device__ __forceinline__ int partner_of(const NormArgs& p, int lane, int lane_in_row) {
-  const int hl = p.rot / 16;
-  if (lane_in_row >= 2 * hl) return lane;
-  return lane_in_row < hl ? lane + hl : lane - hl;
+struct Angles {
+  float2 c[2], s[2];
+};
+__device__ __forceinline__ Angles load_angles(const NormArgs& p, int pos, const NormLane& n) {
+  float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (n.pair >= 0) {
+    const int64_t at = (int64_t)pos * (p.rot / 2) + n.pair;
+    c = __ldg(reinterpret_cast<const float4*>(p.cos + at));
+    s = __ldg(reinterpret_cast<const float4*>(p.sin + at));
+  }
+  return Angles{{make_float2(c.x, c.y), make_float2(c.z, c.w)}, {make_float2(s.x, s.y), make_float2(s.z, s.w)}};
+}
+// Turns a lane's pairs by +angle (SIGN 1) or -angle (SIGN -1).
+template <int SIGN>
+__device__ __forceinline__ void rotate(float2 (&x)[4], const Angles& a) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float2 s = SIGN > 0 ? a.s[i] : make_float2(-a.s[i].x, -a.s[i].y), ns = make_float2(-s.x, -s.y);
+    const float2 u = x[i], v = x[i + 2];
+    x[i] = fma2(v, ns, mul2(u, a.c[i]));
+    x[i + 2] = fma2(u, s, mul2(v, a.c[i]));
+  }
+}
+template <bool IL>
+__device__ __forceinline__ void load_weight(float2 (&w)[4], const float* p, const NormLane& n) {
+  spread<IL>(w, __ldg(reinterpret_cast<const float4*>(p + n.a)), __ldg(reinterpret_cast<const float4*>(p + n.b)));
+}
+__device__ __forceinline__ float dot4(const float2 (&a)[4], const float2 (&b)[4]) {
+  float2 v = mul2(a[0], b[0]);
+#pragma unroll
+  for (int i = 1; i < 4; ++i) v = fma2(a[i], b[i], v);
+  return v.x + v.y;
 }
 
-template <int D, int R, bool INBF, bool OUTBF>
-__global__ void __launch_bounds__(NORM_NT) qk_norm_rope_kernel(const NormArgs p, int chunks) {
+// Sums of N values over the LPR lanes of a row, to all of them.  Four values over four lanes or more go together: two
+// exchanges leave each lane of a quad with one value's partial sum, which is completed across the quads and dealt back (9
+// shuffles instead of 16 at LPR = 16).
+template <int LPR, int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], int lane) {
+  if constexpr (N % 4 == 0 && LPR >= 4) {
+    const bool b0 = lane & 1, b1 = lane & 2;
+#pragma unroll
+    for (int q = 0; q < N; q += 4) {
+      float k0 = b0 ? v[q + 1] : v[q], k1 = b0 ? v[q + 3] : v[q + 2];
+      k0 += __shfl_xor_sync(0xffffffffu, b0 ? v[q] : v[q + 1], 1);
+      k1 += __shfl_xor_sync(0xffffffffu, b0 ? v[q + 2] : v[q + 3], 1);
+      float k = b1 ? k1 : k0;
+      k += __shfl_xor_sync(0xffffffffu, b1 ? k0 : k1, 2);
+#pragma unroll
+      for (int o = 4; o < LPR; o <<= 1) k += __shfl_xor_sync(0xffffffffu, k, o);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[q + i] = __shfl_sync(0xffffffffu, k, (lane & ~3) | i);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = row_sum<LPR>(v[i]);
+  }
+}
+
+// chunks_q, chunks: groups of R heads per token among the queries, and in all.
+template <int D, int R, bool INBF, bool OUTBF, bool IL>
+__global__ void __launch_bounds__(NORM_NT, NORM_RESIDENT) qk_norm_rope_kernel(const NormArgs p, unsigned chunks_q, unsigned chunks) {
   constexpr int LPR = D / 8, NG = NORM_NT / LPR;
+  pdl_begin();
   const int lane = threadIdx.x & 31, lr = threadIdx.x % LPR;
   const unsigned gid = blockIdx.x * (unsigned)NG + threadIdx.x / LPR;
-  const int64_t t = gid / (unsigned)chunks;
-  const int h0 = (int)(gid % (unsigned)chunks) * R;
-  const int H = p.Hq + p.Hkv;
+  const int64_t t = gid / chunks;
+  const unsigned c = gid % chunks;
+  const bool isq = c < chunks_q;
+  const int h0 = (int)(isq ? c : c - chunks_q) * R, H = isq ? p.Hq : p.Hkv;
+  const void* in = isq ? p.q : p.k;
+  const int64_t in0 = t * (isq ? p.q_stride : p.k_stride) + h0 * D;
+  const NormLane n = norm_lane<D, IL>(lr, p.rot);
   bool live = t < p.T;
-  Raw8<INBF> raw[R];
+  RawRow<INBF> raw[R];
 #pragma unroll
   for (int i = 0; i < R; ++i) {
-    const int h = h0 + i;
-    if (live && h < H) {
-      if (h < p.Hq) load8(raw[i], p.q, t * p.q_stride + h * D + lr * 8);
-      else load8(raw[i], p.k, t * p.k_stride + (h - p.Hq) * D + lr * 8);
-    } else {
-      raw[i] = Raw8<INBF>{};
-    }
+    if (live && h0 + i < H) raw[i].load(in, in0 + i * D, n);
+    else raw[i] = RawRow<INBF>{};
   }
-  Angles ang;
+  Angles ang{};
   if (p.rot) {
     const int pos = live ? __ldg(p.positions + t) : 0;
     if ((unsigned)pos >= (unsigned)p.num_positions) {
       if (live && lr == 0) flag_status(p.status, KDA_DEV_POS_OOB);
       live = false;
     } else {
-      load_angles(ang, p, pos, lr);
+      ang = load_angles(p, pos, n);
     }
   }
-  const int partner = partner_of(p, lane, lr);
+  float2 w[4];
+  load_weight<IL>(w, isq ? p.wq : p.wk, n);
+  float r[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    float2 x[4];
+    raw[i].template widen<IL>(x);
+    r[i] = dot4(x, x);
+  }
+  row_sums<LPR, R>(r, lane);
+  void* out = isq ? p.q_out : p.k_out;
+  const int64_t out0 = t * (isq ? p.q_out_stride : p.k_out_stride) + h0 * D;
   int written = 0;
 #pragma unroll
   for (int i = 0; i < R; ++i) {
-    const int h = h0 + i;
-    float x[8];
-    widen8(raw[i], x);
-    float ss = 0.f;
+    float2 x[4];
+    raw[i].template widen<IL>(x);
+    const float2 scale = both(rsqrtf(r[i] * (1.f / D) + p.eps));
 #pragma unroll
-    for (int c = 0; c < 8; ++c) ss += x[c] * x[c];
-    ss = row_sum<LPR>(ss);
-    const float r = rsqrtf(ss * (1.f / D) + p.eps);
-    const float* w = h < p.Hq ? p.wq : p.wk;
-    const float4 w0 = __ldg(reinterpret_cast<const float4*>(w + lr * 8));
-    const float4 w1 = __ldg(reinterpret_cast<const float4*>(w + lr * 8) + 1);
-    x[0] *= r * w0.x, x[1] *= r * w0.y, x[2] *= r * w0.z, x[3] *= r * w0.w;
-    x[4] *= r * w1.x, x[5] *= r * w1.y, x[6] *= r * w1.z, x[7] *= r * w1.w;
-    rotate8(x, ang, p, partner, 1.f);
-    if (live && h < H) {
-      if (h < p.Hq) store8<OUTBF>(p.q_out, t * p.q_out_stride + h * D + lr * 8, x);
-      else store8<OUTBF>(p.k_out, t * p.k_out_stride + (h - p.Hq) * D + lr * 8, x);
+    for (int e = 0; e < 4; ++e) x[e] = mul2(mul2(x[e], scale), w[e]);
+    if (p.rot) rotate<1>(x, ang);
+    if (live && h0 + i < H) {
+      store_row<OUTBF, IL>(out, out0 + i * D, n, x);
       ++written;
     }
   }
   if (p.status) {  // one atomic per warp
-    const int n = __reduce_add_sync(0xffffffffu, lr == 0 ? written : 0);
-    if (lane == 0) add_work(p.status, n);
+    const int sum = __reduce_add_sync(0xffffffffu, lr == 0 ? written : 0);
+    if (lane == 0) add_work(p.status, sum);
   }
 }
 
-// Backward.  A fixed number of CTAs (NORM_BWD_CTAS at most) walk the tokens' row chunks; each lane keeps the
-// weight gradients of its eight channels in registers over the whole walk, the CTA adds its groups up in shared
-// memory in a fixed order, and one row of partial sums per CTA goes to the workspace.
-template <int D, int R, bool INBF, bool GBF, bool OUTBF>
-__global__ void __launch_bounds__(NORM_NT) qk_norm_rope_bwd_kernel(const NormArgs p, const void* __restrict__ dyq,
-                                                                   const void* __restrict__ dyk,
-                                                                   float* __restrict__ partial, int chunks) {
-  constexpr int LPR = D / 8, NG = NORM_NT / LPR;
+// Backward.  The first ctas_q CTAs walk the query rows, the others the key rows, in proportion to the heads, so a lane
+// holds one weight and one set of weight gradients in registers over its whole walk.  The CTA adds its groups' sums
+// up in shared memory in a fixed order, and one row of partial sums per CTA goes to the workspace.
+template <int D, int R, bool INBF, bool GBF, bool OUTBF, bool IL>
+__global__ void __launch_bounds__(NORM_BWD_NT, NORM_BWD_RESIDENT)
+    qk_norm_rope_bwd_kernel(const NormArgs p, const void* __restrict__ dyq, const void* __restrict__ dyk,
+                            float* __restrict__ partial, int ctas_q) {
+  constexpr int LPR = D / 8, NG = NORM_BWD_NT / LPR;
+  pdl_begin();
   const int lane = threadIdx.x & 31, lr = threadIdx.x % LPR, grp = threadIdx.x / LPR;
-  const int H = p.Hq + p.Hkv;
-  const int partner = partner_of(p, lane, lr);
-  float accq[8] = {}, acck[8] = {};
+  const bool isq = blockIdx.x < ctas_q;
+  const int H = isq ? p.Hq : p.Hkv;
+  const unsigned chunks = (unsigned)(H + R - 1) / R;
+  const unsigned cta = isq ? blockIdx.x : blockIdx.x - ctas_q, ctas = isq ? ctas_q : gridDim.x - ctas_q;
+  const void *in = isq ? p.q : p.k, *dy = isq ? dyq : dyk;
+  void* out = isq ? p.q_out : p.k_out;
+  const int64_t in_stride = isq ? p.q_stride : p.k_stride, out_stride = isq ? p.q_out_stride : p.k_out_stride;
+  const NormLane n = norm_lane<D, IL>(lr, p.rot);
+  float2 w[4], acc[4] = {};
+  load_weight<IL>(w, isq ? p.wq : p.wk, n);
   int written = 0;
-  const int64_t total = p.T * chunks;
-  // every group of a warp takes the same number of turns, so the shuffles below stay warp-wide
-  for (int64_t base = (int64_t)blockIdx.x * NG; base < total; base += (int64_t)gridDim.x * NG) {
-    const int64_t gid = base + grp;
-    bool live = gid < total;
-    const int64_t t = live ? gid / chunks : 0;
-    const int h0 = live ? (int)(gid - t * chunks) * R : 0;
-    Raw8<INBF> rx[R];
-    Raw8<GBF> rg[R];
+  // this group's first (token, chunk), and how far it moves per turn
+  const unsigned T = (unsigned)p.T, gid = cta * NG + grp;
+  unsigned t = gid / chunks, c = gid % chunks;
+  const unsigned step_t = ctas * NG / chunks, step_c = ctas * NG % chunks;
+  int pos_next = p.rot && t < T ? __ldg(p.positions + t) : 0;
+  // every group of a CTA takes the same number of turns, so the shuffles below stay warp-wide
+  const int64_t per_turn = (int64_t)ctas * NG;
+  const int turns = (int)((p.T * chunks + per_turn - 1 - (int64_t)cta * NG) / per_turn);
+  for (int turn_no = 0; turn_no < turns; ++turn_no) {
+    bool live = t < T;
+    const int h0 = (int)c * R;
+    const int64_t in0 = t * in_stride + h0 * D, dy0 = ((int64_t)t * H + h0) * D, out0 = t * out_stride + h0 * D;
+    RawRow<INBF> rx[R];
+    RawRow<GBF> rg[R];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      const int h = h0 + i;
-      if (live && h < p.Hq) {
-        load8(rx[i], p.q, t * p.q_stride + h * D + lr * 8);
-        load8(rg[i], dyq, (t * p.Hq + h) * D + lr * 8);
-      } else if (live && h < H) {
-        load8(rx[i], p.k, t * p.k_stride + (h - p.Hq) * D + lr * 8);
-        load8(rg[i], dyk, (t * p.Hkv + h - p.Hq) * D + lr * 8);
+      if (live && h0 + i < H) {
+        rx[i].load(in, in0 + i * D, n);
+        rg[i].load(dy, dy0 + i * D, n);
       } else {
-        rx[i] = Raw8<INBF>{};
-        rg[i] = Raw8<GBF>{};
+        rx[i] = RawRow<INBF>{};
+        rg[i] = RawRow<GBF>{};
       }
     }
-    Angles ang;
+    Angles ang{};
     if (p.rot) {
-      const int pos = live ? __ldg(p.positions + t) : 0;
-      if ((unsigned)pos >= (unsigned)p.num_positions) {
+      if ((unsigned)pos_next >= (unsigned)p.num_positions) {
         if (live && lr == 0) flag_status(p.status, KDA_DEV_POS_OOB);
         live = false;
       } else {
-        load_angles(ang, p, pos, lr);
+        ang = load_angles(p, pos_next, n);
       }
     }
+    t += step_t;
+    c += step_c;
+    if (c >= chunks) c -= chunks, ++t;
+    if (p.rot) pos_next = t < T ? __ldg(p.positions + t) : 0;
+    float2 g[R][4];
+    float v[2 * R];  // per row: sum x^2, sum g w x
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      const int h = h0 + i;
-      const bool on = live && h < H, isq = h < p.Hq;
-      float x[8], g[8];
-      widen8(rx[i], x);
-      widen8(rg[i], g);
-      rotate8(g, ang, p, partner, -1.f);
-      const float* w = isq ? p.wq : p.wk;
-      const float4 w0 = __ldg(reinterpret_cast<const float4*>(w + lr * 8));
-      const float4 w1 = __ldg(reinterpret_cast<const float4*>(w + lr * 8) + 1);
-      const float wv[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-      float ss = 0.f, dot = 0.f;
+      float2 x[4], gx[4];
+      rx[i].template widen<IL>(x);
+      rg[i].template widen<IL>(g[i]);
+      if (p.rot) rotate<-1>(g[i], ang);
+      v[2 * i] = dot4(x, x);
 #pragma unroll
-      for (int c = 0; c < 8; ++c) ss += x[c] * x[c], dot += g[c] * wv[c] * x[c];
-      ss = row_sum<LPR>(ss);
-      dot = row_sum<LPR>(dot);
-      const float r = rsqrtf(ss * (1.f / D) + p.eps);
-      const float m = dot * r * (1.f / D);  // mean(g w u)
+      for (int e = 0; e < 4; ++e) gx[e] = mul2(g[i][e], x[e]);
+      v[2 * i + 1] = dot4(gx, w);
+    }
+    row_sums<LPR, 2 * R>(v, lane);
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        const float u = x[c] * r, gu = g[c] * u;
-        if (on && isq) accq[c] += gu;
-        if (on && !isq) acck[c] += gu;
-        x[c] = r * (g[c] * wv[c] - u * m);
+    for (int i = 0; i < R; ++i) {
+      if (!live || h0 + i >= H) continue;
+      float2 x[4];
+      rx[i].template widen<IL>(x);
+      const float r = rsqrtf(v[2 * i] * (1.f / D) + p.eps);
+      const float2 r2 = both(r), k = both(-(r * r) * (r * v[2 * i + 1]) * (1.f / D));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 gr = mul2(g[i][e], r2);
+        acc[e] = fma2(gr, x[e], acc[e]);
+        x[e] = fma2(gr, w[e], mul2(x[e], k));
       }
-      if (on) {
-        if (isq) store8<OUTBF>(p.q_out, t * p.q_out_stride + h * D + lr * 8, x);
-        else store8<OUTBF>(p.k_out, t * p.k_out_stride + (h - p.Hq) * D + lr * 8, x);
-        ++written;
-      }
+      store_row<OUTBF, IL>(out, out0 + i * D, n, x);
+      ++written;
     }
   }
-  __shared__ float sum[NG][2][D + 4];
-#pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    sum[grp][0][lr * 8 + c] = accq[c];
-    sum[grp][1][lr * 8 + c] = acck[c];
+  __shared__ float sum[NG][D + 4];
+  {
+    float4 e, f;
+    gather<IL>(acc, e, f);
+    *reinterpret_cast<float4*>(&sum[grp][n.a]) = e;
+    *reinterpret_cast<float4*>(&sum[grp][n.b]) = f;
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < 2 * D; e += NORM_NT) {
+  for (int e = threadIdx.x; e < D; e += NORM_BWD_NT) {
     float v = 0.f;
 #pragma unroll
-    for (int i = 0; i < NG; ++i) v += sum[i][e / D][e % D];
-    partial[(int64_t)blockIdx.x * 2 * D + e] = v;
+    for (int i = 0; i < NG; ++i) v += sum[i][e];
+    partial[(int64_t)blockIdx.x * D + e] = v;
   }
   if (p.status) {
-    const int n = __reduce_add_sync(0xffffffffu, lr == 0 ? written : 0);
-    if (lane == 0) add_work(p.status, n);
+    const int total = __reduce_add_sync(0xffffffffu, lr == 0 ? written : 0);
+    if (lane == 0) add_work(p.status, total);
   }
 }
 
-// Adds the CTAs' partial weight gradients: 32 channels per CTA, the partial rows spread over its warps and then
-// added in warp order, so the result does not depend on timing.
-__global__ void __launch_bounds__(512) qk_norm_weight_grad_kernel(const float* __restrict__ partial, int rows, int D,
-                                                                  float* __restrict__ dwq, float* __restrict__ dwk) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  __shared__ float part[16][33];
-  const int e = blockIdx.x * 32 + threadIdx.x % 32, w = threadIdx.x / 32;
+// Adds the CTAs' partial weight gradients, the queries' in blocks 0 .. D/16 - 1 and the keys' in the rest: 16 channels per
+// CTA, the partial rows spread over its 32 half-warps and then added in their order, so the result does not depend on
+// timing.
+__global__ void __launch_bounds__(512) qk_norm_weight_grad_kernel(const float* __restrict__ partial, int ctas_q, int ctas,
+                                                                  int D, float* __restrict__ dwq,
+                                                                  float* __restrict__ dwk) {
+  pdl_begin();
+  __shared__ float part[32][17];
+  const int c = threadIdx.x % 16, w = threadIdx.x / 16;
+  const bool isq = blockIdx.x < D / 16;
+  const int e = (isq ? blockIdx.x : blockIdx.x - D / 16) * 16 + c;
+  const int lo = isq ? 0 : ctas_q, hi = isq ? ctas_q : ctas;
   float v = 0.f;
-  for (int i = w; i < rows; i += 16) v += partial[(int64_t)i * 2 * D + e];
-  part[w][threadIdx.x % 32] = v;
+#pragma unroll 4
+  for (int i = lo + w; i < hi; i += 32) v += partial[(int64_t)i * D + e];
+  part[w][c] = v;
   __syncthreads();
   if (w == 0) {
     v = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v += part[i][threadIdx.x];
-    if (e < D) dwq[e] = v;
-    else dwk[e - D] = v;
+    for (int i = 0; i < 32; ++i) v += part[i][c];
+    (isq ? dwq : dwk)[e] = v;
   }
 }
 
 namespace {
 
-template <int D, int R>
-cudaError_t norm_fwd(const NormArgs& a, int64_t blocks, int chunks, cudaStream_t s) {
-  const unsigned g = (unsigned)blocks;
-  if (a.in_bf16 && a.out_bf16) qk_norm_rope_kernel<D, R, true, true><<<g, NORM_NT, 0, s>>>(a, chunks);
-  else if (a.in_bf16) qk_norm_rope_kernel<D, R, true, false><<<g, NORM_NT, 0, s>>>(a, chunks);
-  else if (a.out_bf16) qk_norm_rope_kernel<D, R, false, true><<<g, NORM_NT, 0, s>>>(a, chunks);
-  else qk_norm_rope_kernel<D, R, false, false><<<g, NORM_NT, 0, s>>>(a, chunks);
-  return cudaGetLastError();
+template <int D, int R, bool IL>
+cudaError_t norm_fwd(const NormArgs& a, cudaStream_t s) {
+  constexpr int NG = NORM_NT / (D / 8);
+  const unsigned cq = (a.Hq + R - 1) / R, chunks = cq + (a.Hkv + R - 1) / R;
+  const int64_t blocks = (a.T * chunks + NG - 1) / NG;
+  if (a.T > 0x7fffffff || blocks * NG > 0x7fffffff) return cudaErrorInvalidValue;
+  auto kernel = a.in_bf16 ? (a.out_bf16 ? qk_norm_rope_kernel<D, R, true, true, IL> : qk_norm_rope_kernel<D, R, true, false, IL>)
+                          : (a.out_bf16 ? qk_norm_rope_kernel<D, R, false, true, IL>
+                                        : qk_norm_rope_kernel<D, R, false, false, IL>);
+  return launch_pdl(kernel, dim3((unsigned)blocks), dim3(NORM_NT), 0, s, a, cq, chunks);
 }
 
 template <int D>
 cudaError_t norm_fwd_d(const NormArgs& a, cudaStream_t s) {
-  constexpr int NG = NORM_NT / (D / 8);
-  const int H = a.Hq + a.Hkv;
-  // Few rows: one per group, so that they spread over the SMs.  Otherwise four, for loads in flight and one
+  // Few rows: one per group, so that they spread over the SMs.  Otherwise NORM_R, for loads in flight and one
   // read of the angles.
-  const int R = a.T * H <= 4096 ? 1 : 4;
-  const int chunks = (H + R - 1) / R;
-  const int64_t blocks = (a.T * chunks + NG - 1) / NG;
-  if (a.T > 0x7fffffff || blocks * NG > 0x7fffffff) return cudaErrorInvalidValue;
-  return R == 1 ? norm_fwd<D, 1>(a, blocks, chunks, s) : norm_fwd<D, 4>(a, blocks, chunks, s);
+  if (a.T * (a.Hq + a.Hkv) <= 4096) return a.interleaved ? norm_fwd<D, 1, true>(a, s) : norm_fwd<D, 1, false>(a, s);
+  return a.interleaved ? norm_fwd<D, NORM_R, true>(a, s) : norm_fwd<D, NORM_R, false>(a, s);
 }
 
-template <int D, int R>
-cudaError_t norm_bwd(const NormArgs& a, const void* dyq, const void* dyk, bool g_bf16, float* partial, int ctas,
-                     int chunks, cudaStream_t s) {
+template <int D, int R, bool IL>
+cudaError_t norm_bwd(const NormArgs& a, const void* dyq, const void* dyk, bool g_bf16, float* partial, int ctas_q,
+                     int ctas, cudaStream_t s) {
   const int sel = (a.in_bf16 ? 4 : 0) | (g_bf16 ? 2 : 0) | (a.out_bf16 ? 1 : 0);
   switch (sel) {
-#define KDA_CASE(n, i, g, o)                                                                             \
-  case n: qk_norm_rope_bwd_kernel<D, R, i, g, o><<<ctas, NORM_NT, 0, s>>>(a, dyq, dyk, partial, chunks); \
-    break;
+#define KDA_CASE(n, i, g, o)                                                                                         \
+  case n: return launch_pdl(qk_norm_rope_bwd_kernel<D, R, i, g, o, IL>, dim3(ctas), dim3(NORM_BWD_NT), 0, s, a, dyq, \
+                            dyk, partial, ctas_q);
     KDA_CASE(0, false, false, false)
     KDA_CASE(1, false, false, true)
     KDA_CASE(2, false, true, false)
@@ -295,22 +417,29 @@ cudaError_t norm_bwd(const NormArgs& a, const void* dyq, const void* dyk, bool g
     KDA_CASE(7, true, true, true)
 #undef KDA_CASE
   }
-  return cudaGetLastError();
+  return cudaErrorInvalidValue;
 }
 
 template <int D>
 cudaError_t norm_bwd_d(const NormArgs& a, const void* dyq, const void* dyk, bool g_bf16, float* dwq, float* dwk,
                        float* partial, cudaStream_t s) {
-  constexpr int NG = NORM_NT / (D / 8), R = 2;
-  const int chunks = (a.Hq + a.Hkv + R - 1) / R;
-  const int64_t need = (a.T * chunks + NG - 1) / NG;
-  const int ctas = (int)(need < NORM_BWD_CTAS ? need : NORM_BWD_CTAS);
+  constexpr int NG = NORM_BWD_NT / (D / 8), R = NORM_BWD_R, MOST = 152 * NORM_BWD_RESIDENT;
+  static_assert(MOST <= NORM_BWD_CTAS, "one row of the workspace per CTA");
+  const int64_t need_q = (a.T * ((a.Hq + R - 1) / R) + NG - 1) / NG, need_k = (a.T * ((a.Hkv + R - 1) / R) + NG - 1) / NG;
+  int64_t ctas_q = need_q, ctas_k = need_k;
+  if (need_q + need_k > MOST) {
+    ctas_q = (MOST * need_q + (need_q + need_k) / 2) / (need_q + need_k);
+    ctas_q = ctas_q < 1 ? 1 : ctas_q > MOST - 1 ? MOST - 1 : ctas_q;
+    ctas_k = MOST - ctas_q;
+  }
+  const int ctas = (int)(ctas_q + ctas_k);
   if (ctas > 0) {  // without tokens the weights' gradients are zero
-    const cudaError_t e = norm_bwd<D, R>(a, dyq, dyk, g_bf16, partial, ctas, chunks, s);
+    const cudaError_t e = a.interleaved ? norm_bwd<D, R, true>(a, dyq, dyk, g_bf16, partial, (int)ctas_q, ctas, s)
+                                        : norm_bwd<D, R, false>(a, dyq, dyk, g_bf16, partial, (int)ctas_q, ctas, s);
     if (e != cudaSuccess) return e;
   }
-  return launch_pdl(qk_norm_weight_grad_kernel, dim3(2 * D / 32), dim3(512), 0, s, (const float*)partial, ctas, D, dwq,
-                    dwk);
+  return launch_pdl(qk_norm_weight_grad_kernel, dim3(2 * D / 16), dim3(512), 0, s, (const float*)partial, (int)ctas_q,
+                    ctas, D, dwq, dwk);
 }
 
 }  // namespace
