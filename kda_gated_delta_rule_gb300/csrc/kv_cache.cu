@@ -8,7 +8,9 @@
 // wherever in [224, 448] the largest channel lands.
 //
 // Bound by HBM: each row is read once and written once.  A row lies on D/8 lanes (rows8.cuh); a group of lanes takes
-// R of the token's 2 Hkv rows (keys, then values) and issues all its loads before the first reduction.
+// R of the token's key rows, or value rows, and issues all its loads before the first reduction.  The groups of a
+// CTA take the same rows of consecutive tokens, which lie next to one another in a page: whole sectors of scales and
+// runs of 1 KB of codes at D = 128.
 #include "launch.h"
 #include <cuda_fp16.h>
 
@@ -55,61 +57,75 @@ __device__ __forceinline__ int64_t slot_row(int64_t slot, const KvCacheArgs& c) 
   return page * c.Hkv * c.page_size + off;
 }
 
+// Largest magnitude of a row, over its lanes; NaN left out.  bf16 rows compare as bf16 pairs.
+template <int LPR>
+__device__ __forceinline__ float row_amax(const Raw8<true>& r) {
+  auto mag = [](uint32_t v) {
+    v &= 0x7fff7fffu;
+    return *reinterpret_cast<__nv_bfloat162*>(&v);
+  };
+  __nv_bfloat162 m = __hmax2(__hmax2(mag(r.v.x), mag(r.v.y)), __hmax2(mag(r.v.z), mag(r.v.w)));
+#pragma unroll
+  for (int o = LPR / 2; o > 0; o >>= 1) m = __hmax2(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float lo = __low2float(m), hi = __high2float(m);
+  return fmaxf(fmaxf(lo, hi), 0.f);  // a row of NaN only: 0
+}
+template <int LPR>
+__device__ __forceinline__ float row_amax(const Raw8<false>& r) {
+  float m = fmaxf(fmaxf(fabsf(r.a.x), fabsf(r.a.y)), fmaxf(fabsf(r.a.z), fabsf(r.a.w)));
+  m = fmaxf(m, fmaxf(fmaxf(fabsf(r.b.x), fabsf(r.b.y)), fmaxf(fabsf(r.b.z), fabsf(r.b.w))));
+  return fmaxf(row_max<LPR>(m), 0.f);
+}
+
+// chunks: groups of R heads among the keys, as many again among the values.
 template <int D, int R, bool INBF, bool F8>
-__global__ void __launch_bounds__(KV_NT) kv_write_kernel(const KvWriteArgs p, int chunks) {
+__global__ void __launch_bounds__(KV_NT) kv_write_kernel(const KvWriteArgs p, unsigned chunks) {
   constexpr int LPR = D / 8, NG = KV_NT / LPR;
   pdl_begin();
   const int lane = threadIdx.x & 31, lr = threadIdx.x % LPR;
-  const unsigned gid = blockIdx.x * (unsigned)NG + threadIdx.x / LPR;
-  const int64_t t = gid / (unsigned)chunks;
-  const int r0 = (int)(gid % (unsigned)chunks) * R;
-  const int rows = 2 * p.c.Hkv;
+  const int64_t t = (int64_t)(blockIdx.x / (2 * chunks)) * NG + threadIdx.x / LPR;
+  const unsigned c = blockIdx.x % (2 * chunks);
+  const bool isk = c < chunks;
+  const int h0 = (int)(isk ? c : c - chunks) * R, H = p.c.Hkv;
+  const void* in = isk ? p.k : p.v;
+  const int64_t in0 = t * (isk ? p.k_stride : p.v_stride) + h0 * D + lr * 8;
   Raw8<INBF> raw[R];
 #pragma unroll
   for (int i = 0; i < R; ++i) {
-    const int r = r0 + i;
-    if (t < p.T && r < rows) {
-      if (r < p.c.Hkv) load8(raw[i], p.k, t * p.k_stride + r * D + lr * 8);
-      else load8(raw[i], p.v, t * p.v_stride + (r - p.c.Hkv) * D + lr * 8);
-    } else {
-      raw[i] = Raw8<INBF>{};
-    }
+    if (t < p.T && h0 + i < H) load8(raw[i], in, in0 + i * D);
+    else raw[i] = Raw8<INBF>{};
   }
   const int64_t slot = t < p.T ? __ldg(p.slots + t) : -1;
   const bool beyond = slot >= (int64_t)p.c.num_pages * p.c.page_size;
   if (beyond && lr == 0) flag_status(p.status, KDA_DEV_PAGE_OOB);
   const bool live = slot >= 0 && !beyond;
-  const int64_t row0 = live ? slot_row(slot, p.c) : 0;
+  const int64_t row0 = (live ? slot_row(slot, p.c) : 0) + (int64_t)h0 * p.c.page_size;
+  void* pages = isk ? p.c.k_pages : p.c.v_pages;
+  float* scales = isk ? p.c.k_scales : p.c.v_scales;
   int written = 0;
 #pragma unroll
   for (int i = 0; i < R; ++i) {
-    const int r = r0 + i;
-    const bool isk = r < p.c.Hkv, on = live && r < rows;
-    const int64_t row = row0 + (int64_t)(isk ? r : r - p.c.Hkv) * p.c.page_size;
-    void* pages = isk ? p.c.k_pages : p.c.v_pages;
-    float x[8];
+    const bool on = live && h0 + i < H;
+    const int64_t row = row0 + (int64_t)i * p.c.page_size;
     if constexpr (F8) {
-      widen8(raw[i], x);
-      float amax = 0.f;
-#pragma unroll
-      for (int c = 0; c < 8; ++c) amax = fmaxf(amax, fabsf(x[c]));  // fmaxf drops NaN
-      const int e = scale_exponent(row_max<LPR>(amax));
+      const int e = scale_exponent(row_amax<LPR>(raw[i]));
       const float inv = exp2_int(-e);
+      float x[8];
+      widen8(raw[i], x);
       uint2 codes;
       codes.x = e4m3x2(x[0] * inv, x[1] * inv) | e4m3x2(x[2] * inv, x[3] * inv) << 16;
       codes.y = e4m3x2(x[4] * inv, x[5] * inv) | e4m3x2(x[6] * inv, x[7] * inv) << 16;
       if (on) {
         *reinterpret_cast<uint2*>(static_cast<uint8_t*>(pages) + row * D + lr * 8) = codes;
-        if (lr == 0) (isk ? p.c.k_scales : p.c.v_scales)[row] = exp2_int(e);
+        if (lr == 0) scales[row] = exp2_int(e);
       }
-    } else {
-      if (on) {
-        if constexpr (INBF) {
-          *reinterpret_cast<uint4*>(static_cast<bf16*>(pages) + row * D + lr * 8) = raw[i].v;
-        } else {
-          widen8(raw[i], x);
-          store8<true>(pages, row * D + lr * 8, x);
-        }
+    } else if (on) {
+      if constexpr (INBF) {
+        *reinterpret_cast<uint4*>(static_cast<bf16*>(pages) + row * D + lr * 8) = raw[i].v;
+      } else {
+        float x[8];
+        widen8(raw[i], x);
+        store8<true>(pages, row * D + lr * 8, x);
       }
     }
     written += on && isk;
@@ -121,60 +137,57 @@ __global__ void __launch_bounds__(KV_NT) kv_write_kernel(const KvWriteArgs p, in
 }
 
 template <int D, int R, bool F8, bool OUTBF>
-__global__ void __launch_bounds__(KV_NT) kv_read_kernel(const KvReadArgs p, int chunks) {
+__global__ void __launch_bounds__(KV_NT) kv_read_kernel(const KvReadArgs p, unsigned chunks) {
   constexpr int LPR = D / 8, NG = KV_NT / LPR;
   pdl_begin();
   const int lr = threadIdx.x % LPR;
-  const unsigned gid = blockIdx.x * (unsigned)NG + threadIdx.x / LPR;
-  const int64_t t = gid / (unsigned)chunks;
-  const int r0 = (int)(gid % (unsigned)chunks) * R;
-  const int rows = 2 * p.c.Hkv;
+  const int64_t t = (int64_t)(blockIdx.x / (2 * chunks)) * NG + threadIdx.x / LPR;
+  const unsigned c = blockIdx.x % (2 * chunks);
+  const bool isk = c < chunks;
+  const int h0 = (int)(isk ? c : c - chunks) * R, H = p.c.Hkv;
   if (t >= p.T) return;
   const int64_t slot = __ldg(p.slots + t);
   const bool beyond = slot >= (int64_t)p.c.num_pages * p.c.page_size;
   if (beyond && lr == 0) flag_status(p.status, KDA_DEV_PAGE_OOB);
   const bool live = slot >= 0 && !beyond;
-  const int64_t row0 = live ? slot_row(slot, p.c) : 0;
+  const int64_t row0 = (live ? slot_row(slot, p.c) : 0) + (int64_t)h0 * p.c.page_size;
+  const void* pages = isk ? p.c.k_pages : p.c.v_pages;
+  const float* scales = isk ? p.c.k_scales : p.c.v_scales;
   uint2 codes[R];
-  uint4 bits[R];
+  Raw8<true> bits[R];
   float scale[R];
 #pragma unroll
   for (int i = 0; i < R; ++i) {
-    const int r = r0 + i;
-    const bool isk = r < p.c.Hkv;
-    const int64_t row = row0 + (int64_t)(isk ? r : r - p.c.Hkv) * p.c.page_size;
-    const void* pages = isk ? p.c.k_pages : p.c.v_pages;
+    const int64_t row = row0 + (int64_t)i * p.c.page_size;
     codes[i] = make_uint2(0, 0);
-    bits[i] = make_uint4(0, 0, 0, 0);
+    bits[i] = Raw8<true>{};
     scale[i] = 0.f;
-    if (live && r < rows) {
+    if (live && h0 + i < H) {
       if constexpr (F8) {
         codes[i] = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(pages) + row * D + lr * 8);
-        scale[i] = (isk ? p.c.k_scales : p.c.v_scales)[row];
+        scale[i] = scales[row];
       } else {
-        bits[i] = *reinterpret_cast<const uint4*>(static_cast<const bf16*>(pages) + row * D + lr * 8);
+        load8(bits[i], pages, row * D + lr * 8);
       }
     }
   }
+  void* out = isk ? p.k_out : p.v_out;
+  const int64_t out0 = (t * H + h0) * D + lr * 8;
 #pragma unroll
   for (int i = 0; i < R; ++i) {
-    const int r = r0 + i;
-    if (r >= rows) break;
-    const bool isk = r < p.c.Hkv;
-    void* out = isk ? p.k_out : p.v_out;
-    const int64_t at = (t * p.c.Hkv + (isk ? r : r - p.c.Hkv)) * D + lr * 8;
+    if (h0 + i >= H) break;
     float x[8];
     if constexpr (F8) {
       const float2 a = from_e4m3x2(codes[i].x & 0xffffu), b = from_e4m3x2(codes[i].x >> 16);
-      const float2 c = from_e4m3x2(codes[i].y & 0xffffu), d = from_e4m3x2(codes[i].y >> 16);
+      const float2 cc = from_e4m3x2(codes[i].y & 0xffffu), d = from_e4m3x2(codes[i].y >> 16);
       x[0] = a.x * scale[i], x[1] = a.y * scale[i], x[2] = b.x * scale[i], x[3] = b.y * scale[i];
-      x[4] = c.x * scale[i], x[5] = c.y * scale[i], x[6] = d.x * scale[i], x[7] = d.y * scale[i];
-      store8<OUTBF>(out, at, x);
+      x[4] = cc.x * scale[i], x[5] = cc.y * scale[i], x[6] = d.x * scale[i], x[7] = d.y * scale[i];
+      store8<OUTBF>(out, out0 + i * D, x);
     } else if constexpr (OUTBF) {
-      *reinterpret_cast<uint4*>(static_cast<bf16*>(out) + at) = bits[i];
+      *reinterpret_cast<uint4*>(static_cast<bf16*>(out) + out0 + i * D) = bits[i].v;
     } else {
-      widen8(Raw8<true>{bits[i]}, x);
-      store8<false>(out, at, x);
+      widen8(bits[i], x);
+      store8<false>(out, out0 + i * D, x);
     }
   }
 }
@@ -187,9 +200,9 @@ inline int kv_rows(int64_t T, int Hkv) { return T * Hkv <= 2048 ? 1 : 4; }
 template <int D, int R>
 cudaError_t write_r(const KvWriteArgs& a, bool f8, cudaStream_t s) {
   constexpr int NG = KV_NT / (D / 8);
-  const int chunks = (2 * a.c.Hkv + R - 1) / R;
-  const int64_t blocks = (a.T * chunks + NG - 1) / NG;
-  if (blocks * NG > 0x7fffffff) return cudaErrorInvalidValue;
+  const unsigned chunks = (a.c.Hkv + R - 1) / R;
+  const int64_t blocks = (a.T + NG - 1) / NG * 2 * chunks;
+  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
   auto kernel = f8 ? (a.in_bf16 ? kv_write_kernel<D, R, true, true> : kv_write_kernel<D, R, false, true>)
                    : (a.in_bf16 ? kv_write_kernel<D, R, true, false> : kv_write_kernel<D, R, false, false>);
   return launch_pdl(kernel, dim3((unsigned)blocks), dim3(KV_NT), 0, s, a, chunks);
@@ -198,9 +211,9 @@ cudaError_t write_r(const KvWriteArgs& a, bool f8, cudaStream_t s) {
 template <int D, int R>
 cudaError_t read_r(const KvReadArgs& a, bool f8, cudaStream_t s) {
   constexpr int NG = KV_NT / (D / 8);
-  const int chunks = (2 * a.c.Hkv + R - 1) / R;
-  const int64_t blocks = (a.T * chunks + NG - 1) / NG;
-  if (blocks * NG > 0x7fffffff) return cudaErrorInvalidValue;
+  const unsigned chunks = (a.c.Hkv + R - 1) / R;
+  const int64_t blocks = (a.T + NG - 1) / NG * 2 * chunks;
+  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
   auto kernel = f8 ? (a.out_bf16 ? kv_read_kernel<D, R, true, true> : kv_read_kernel<D, R, true, false>)
                    : (a.out_bf16 ? kv_read_kernel<D, R, false, true> : kv_read_kernel<D, R, false, false>);
   return launch_pdl(kernel, dim3((unsigned)blocks), dim3(KV_NT), 0, s, a, chunks);

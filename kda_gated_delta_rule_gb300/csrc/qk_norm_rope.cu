@@ -180,61 +180,77 @@ __device__ __forceinline__ void row_sums(float (&v)[N], int lane) {
   }
 }
 
-// chunks_q, chunks: groups of R heads per token among the queries, and in all.
+// A group's place among the (token, chunk) pairs, chunk by chunk within a token, and how far it moves per turn.
+struct NormCursor {
+  unsigned t, c, step_t, step_c, chunks;
+  __device__ __forceinline__ NormCursor(unsigned first, unsigned step, unsigned chunks_)
+      : t(first / chunks_), c(first % chunks_), step_t(step / chunks_), step_c(step % chunks_), chunks(chunks_) {}
+  __device__ __forceinline__ void advance() {
+    t += step_t;
+    c += step_c;
+    if (c >= chunks) c -= chunks, ++t;
+  }
+};
+
+// chunks_q, chunks: groups of R heads per token among the queries, and in all.  The CTAs walk the pairs; the next turn's
+// position is read a turn ahead, so that rows and angles are asked for together.
 template <int D, int R, bool INBF, bool OUTBF, bool IL>
-__global__ void __launch_bounds__(NORM_NT, NORM_RESIDENT) qk_norm_rope_kernel(const NormArgs p, unsigned chunks_q, unsigned chunks) {
+__global__ void __launch_bounds__(NORM_NT, NORM_RESIDENT) qk_norm_rope_kernel(const NormArgs p, unsigned chunks_q,
+                                                                              unsigned chunks, int turns) {
   constexpr int LPR = D / 8, NG = NORM_NT / LPR;
   pdl_begin();
   const int lane = threadIdx.x & 31, lr = threadIdx.x % LPR;
-  const unsigned gid = blockIdx.x * (unsigned)NG + threadIdx.x / LPR;
-  const int64_t t = gid / chunks;
-  const unsigned c = gid % chunks;
-  const bool isq = c < chunks_q;
-  const int h0 = (int)(isq ? c : c - chunks_q) * R, H = isq ? p.Hq : p.Hkv;
-  const void* in = isq ? p.q : p.k;
-  const int64_t in0 = t * (isq ? p.q_stride : p.k_stride) + h0 * D;
   const NormLane n = norm_lane<D, IL>(lr, p.rot);
-  bool live = t < p.T;
-  RawRow<INBF> raw[R];
+  const unsigned T = (unsigned)p.T;
+  NormCursor at(blockIdx.x * (unsigned)NG + threadIdx.x / LPR, gridDim.x * (unsigned)NG, chunks);
+  int pos = p.rot && at.t < T ? __ldg(p.positions + at.t) : 0, written = 0;
+  for (int turn_no = 0; turn_no < turns; ++turn_no) {
+    const bool isq = at.c < chunks_q;
+    const int h0 = (int)(isq ? at.c : at.c - chunks_q) * R, H = isq ? p.Hq : p.Hkv;
+    const void* in = isq ? p.q : p.k;
+    void* out = isq ? p.q_out : p.k_out;
+    const int64_t in0 = at.t * (isq ? p.q_stride : p.k_stride) + h0 * D;
+    const int64_t out0 = at.t * (isq ? p.q_out_stride : p.k_out_stride) + h0 * D;
+    bool live = at.t < T;
+    RawRow<INBF> raw[R];
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    if (live && h0 + i < H) raw[i].load(in, in0 + i * D, n);
-    else raw[i] = RawRow<INBF>{};
-  }
-  Angles ang{};
-  if (p.rot) {
-    const int pos = live ? __ldg(p.positions + t) : 0;
-    if ((unsigned)pos >= (unsigned)p.num_positions) {
-      if (live && lr == 0) flag_status(p.status, KDA_DEV_POS_OOB);
-      live = false;
-    } else {
-      ang = load_angles(p, pos, n);
+    for (int i = 0; i < R; ++i) {
+      if (live && h0 + i < H) raw[i].load(in, in0 + i * D, n);
+      else raw[i] = RawRow<INBF>{};
     }
-  }
-  float2 w[4];
-  load_weight<IL>(w, isq ? p.wq : p.wk, n);
-  float r[R];
+    Angles ang{};
+    if (p.rot) {
+      if ((unsigned)pos >= (unsigned)p.num_positions) {
+        if (live && lr == 0) flag_status(p.status, KDA_DEV_POS_OOB);
+        live = false;
+      } else {
+        ang = load_angles(p, pos, n);
+      }
+    }
+    at.advance();
+    if (p.rot) pos = at.t < T ? __ldg(p.positions + at.t) : 0;
+    float2 w[4];
+    load_weight<IL>(w, isq ? p.wq : p.wk, n);
+    float r[R];
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    float2 x[4];
-    raw[i].template widen<IL>(x);
-    r[i] = dot4(x, x);
-  }
-  row_sums<LPR, R>(r, lane);
-  void* out = isq ? p.q_out : p.k_out;
-  const int64_t out0 = t * (isq ? p.q_out_stride : p.k_out_stride) + h0 * D;
-  int written = 0;
+    for (int i = 0; i < R; ++i) {
+      float2 x[4];
+      raw[i].template widen<IL>(x);
+      r[i] = dot4(x, x);
+    }
+    row_sums<LPR, R>(r, lane);
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    float2 x[4];
-    raw[i].template widen<IL>(x);
-    const float2 scale = both(rsqrtf(r[i] * (1.f / D) + p.eps));
+    for (int i = 0; i < R; ++i) {
+      float2 x[4];
+      raw[i].template widen<IL>(x);
+      const float2 scale = both(rsqrtf(r[i] * (1.f / D) + p.eps));
 #pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = mul2(mul2(x[e], scale), w[e]);
-    if (p.rot) rotate<1>(x, ang);
-    if (live && h0 + i < H) {
-      store_row<OUTBF, IL>(out, out0 + i * D, n, x);
-      ++written;
+      for (int e = 0; e < 4; ++e) x[e] = mul2(mul2(x[e], scale), w[e]);
+      if (p.rot) rotate<1>(x, ang);
+      if (live && h0 + i < H) {
+        store_row<OUTBF, IL>(out, out0 + i * D, n, x);
+        ++written;
+      }
     }
   }
   if (p.status) {  // one atomic per warp
@@ -264,18 +280,16 @@ __global__ void __launch_bounds__(NORM_BWD_NT, NORM_BWD_RESIDENT)
   float2 w[4], acc[4] = {};
   load_weight<IL>(w, isq ? p.wq : p.wk, n);
   int written = 0;
-  // this group's first (token, chunk), and how far it moves per turn
-  const unsigned T = (unsigned)p.T, gid = cta * NG + grp;
-  unsigned t = gid / chunks, c = gid % chunks;
-  const unsigned step_t = ctas * NG / chunks, step_c = ctas * NG % chunks;
-  int pos_next = p.rot && t < T ? __ldg(p.positions + t) : 0;
+  const unsigned T = (unsigned)p.T;
+  NormCursor at(cta * NG + grp, ctas * NG, chunks);
+  int pos_next = p.rot && at.t < T ? __ldg(p.positions + at.t) : 0;
   // every group of a CTA takes the same number of turns, so the shuffles below stay warp-wide
   const int64_t per_turn = (int64_t)ctas * NG;
   const int turns = (int)((p.T * chunks + per_turn - 1 - (int64_t)cta * NG) / per_turn);
   for (int turn_no = 0; turn_no < turns; ++turn_no) {
-    bool live = t < T;
-    const int h0 = (int)c * R;
-    const int64_t in0 = t * in_stride + h0 * D, dy0 = ((int64_t)t * H + h0) * D, out0 = t * out_stride + h0 * D;
+    bool live = at.t < T;
+    const int h0 = (int)at.c * R;
+    const int64_t in0 = at.t * in_stride + h0 * D, dy0 = ((int64_t)at.t * H + h0) * D, out0 = at.t * out_stride + h0 * D;
     RawRow<INBF> rx[R];
     RawRow<GBF> rg[R];
 #pragma unroll
@@ -297,10 +311,8 @@ __global__ void __launch_bounds__(NORM_BWD_NT, NORM_BWD_RESIDENT)
         ang = load_angles(p, pos_next, n);
       }
     }
-    t += step_t;
-    c += step_c;
-    if (c >= chunks) c -= chunks, ++t;
-    if (p.rot) pos_next = t < T ? __ldg(p.positions + t) : 0;
+    at.advance();
+    if (p.rot) pos_next = at.t < T ? __ldg(p.positions + at.t) : 0;
     float2 g[R][4];
     float v[2 * R];  // per row: sum x^2, sum g w x
 #pragma unroll
@@ -383,12 +395,14 @@ template <int D, int R, bool IL>
 cudaError_t norm_fwd(const NormArgs& a, cudaStream_t s) {
   constexpr int NG = NORM_NT / (D / 8);
   const unsigned cq = (a.Hq + R - 1) / R, chunks = cq + (a.Hkv + R - 1) / R;
-  const int64_t blocks = (a.T * chunks + NG - 1) / NG;
+  int64_t blocks = (a.T * chunks + NG - 1) / NG;
   if (a.T > 0x7fffffff || blocks * NG > 0x7fffffff) return cudaErrorInvalidValue;
+  const int64_t turns = (blocks + 152 * NORM_RESIDENT - 1) / (152 * NORM_RESIDENT);
+  blocks = (blocks + turns - 1) / turns;  // as many as give every CTA that many turns
   auto kernel = a.in_bf16 ? (a.out_bf16 ? qk_norm_rope_kernel<D, R, true, true, IL> : qk_norm_rope_kernel<D, R, true, false, IL>)
                           : (a.out_bf16 ? qk_norm_rope_kernel<D, R, false, true, IL>
                                         : qk_norm_rope_kernel<D, R, false, false, IL>);
-  return launch_pdl(kernel, dim3((unsigned)blocks), dim3(NORM_NT), 0, s, a, cq, chunks);
+  return launch_pdl(kernel, dim3((unsigned)blocks), dim3(NORM_NT), 0, s, a, cq, chunks, (int)turns);
 }
 
 template <int D>
