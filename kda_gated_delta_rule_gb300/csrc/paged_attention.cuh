@@ -53,7 +53,13 @@ struct PaMeta {
 
 // 8-row column blocks of a unit, and the CTAs per SM its kernel is built for
 __host__ __device__ constexpr int pa_nt(int rows, bool fine) { return rows <= 8 ? 1 : rows <= 16 || fine ? 2 : 4; }
-__host__ __device__ constexpr int pa_resident(int nt) { return nt == 1 ? 3 : 2; }
+#ifndef PAG_
+#define PAG_ 4
+#endif
+#ifndef PAR1_
+#define PAR1_ 3
+#endif
+__host__ __device__ constexpr int pa_resident(int nt) { return nt == 1 ? PAR1_ : 2; }
 constexpr int PA_SMS = 152;
 
 struct PaPlan {  // derived on the host
@@ -119,6 +125,7 @@ struct Piece {
 #pragma unroll
     for (int i = 0; i < (BYTES < 4 ? 1 : BYTES / 4); ++i) w[i] = 0;
   }
+  // Read once: not kept in L1 (174 us against 180 for one request of 262144 tokens).
   __device__ __forceinline__ void load(const uint8_t* p) {
     if constexpr (BYTES == 16) {
       asm("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
@@ -135,15 +142,18 @@ struct Piece {
   }
 };
 
-// cap * tanh(x / cap) in powers of two, given y = x / cap and cap2 = cap * log2(e).  1 - 2 / (1 + e^2y) is within 1.2e-7
-// of tanh absolutely; below 0.15 the odd series to y^7 (next term 6e-9 relative there) keeps the small scores' relative
-// precision.
-__device__ __forceinline__ float capped(float y, float cap2) {
-  const float y2 = y * y;
-  const float series = y * fmaf(y2, fmaf(y2, fmaf(y2, -17.f / 315.f, 2.f / 15.f), -1.f / 3.f), 1.f);
-  const float yc = y > 40.f ? 40.f : y;  // 2 / (1 + e^80) is still a plain division; NaN passes
-  const float whole = 1.f - __fdividef(2.f, 1.f + ex2(yc * (2.f * PA_LOG2E)));
-  return cap2 * (y2 < 0.0225f ? series : whole);
+// cap2 * tanh(y) given z = 2 log2(e) y, with cap2 = cap * log2(e): 1 - 2 / (1 + 2^z), within 1.2e-7 of tanh absolutely.
+// That is the score's precision up to caps of PA_NEAR_CAP; above, scores much smaller than the cap keep theirs by
+// the odd series to y^7 below |y| = 0.15 (next term 6e-9 relative there).
+constexpr float PA_NEAR_CAP = 64.f;
+__device__ __forceinline__ float capped(float z, float cap2) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(z)));
+  return fmaf(-2.f * cap2, r, cap2);
+}
+__device__ __forceinline__ float capped_series(float z, float cap2) {
+  const float y = z * (0.5f * PA_LN2), y2 = y * y;
+  return cap2 * y * fmaf(y2, fmaf(y2, fmaf(y2, -17.f / 315.f, 2.f / 15.f), -1.f / 3.f), 1.f);
 }
 
 // ---------------------------------------------------------------- the line of tiles
@@ -158,6 +168,10 @@ __device__ __forceinline__ PaSpan pa_span(const PagedAttnArgs& a, int b, bool fl
   s.len = __ldg(a.seq_lens + b);
   if (s.len < 0 || s.len > (int64_t)a.max_pages * a.c.page_size || s.len > PA_MAX_LEN) {
     if (flag) flag_status(a.status, KDA_DEV_SEQ_OOB);
+    s.len = 0;
+  }
+  if (a.c.num_pages == 0 && s.len > 0) {
+    if (flag) flag_status(a.status, KDA_DEV_PAGE_OOB);
     s.len = 0;
   }
   int64_t first = a.window > 0 ? (int64_t)s.len - a.W - a.window + 1 : 0;  // of the window's first query
@@ -175,7 +189,7 @@ struct PaCfg {
   static constexpr int ES = F8 ? 1 : 2;
   static constexpr int RS = D * ES;                      // bytes of a cached row
   static constexpr int RB = 8 * NT;
-  static constexpr int GPI = F8 && NT < 4 ? 2 : 1;       // 16-token groups a warp works on at once
+  static constexpr int GPI = F8 && NT < PAG_ ? 2 : 1;       // 16-token groups a warp works on at once
   static constexpr int TILE = 16 * GPI;                  // tokens
   static constexpr int KC = D / 4 < 16 / ES ? D / 4 : 16 / ES;  // channels of a key piece
   static constexpr int KL = D / (4 * KC);                // key pieces per lane and token
@@ -245,7 +259,7 @@ __global__ void __launch_bounds__(PA_NT, pa_resident(NT)) paged_attention_kernel
   int64_t first_of_b = where[warp][1];
   int rows_done = 0;
   const int window = a.window > 0 ? a.window : 0x7fffffff;
-  const float cap_inv = a.softcap > 0.f ? 1.f / a.softcap : 0.f, cap2 = a.softcap * PA_LOG2E;
+  const float cap2 = a.softcap * PA_LOG2E;
 
   while (at < end) {
     const PaSpan span = pa_span<TILE>(a, b, false);
@@ -341,7 +355,7 @@ __global__ void __launch_bounds__(PA_NT, pa_resident(NT)) paged_attention_kernel
             qs[((part * NT + t) * KS + u * (C::KC / 4) + c / 4) * 32] = r;
           }
         }
-      const float own = down * a.scale * (a.softcap > 0.f ? cap_inv : PA_LOG2E);
+      const float own = down * a.scale * (a.softcap > 0.f ? 2.f * PA_LOG2E / a.softcap : PA_LOG2E);
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         f[t][c] = __shfl_sync(0xffffffffu, own, (2 * j + c) * 4);
@@ -359,21 +373,14 @@ __global__ void __launch_bounds__(PA_NT, pa_resident(NT)) paged_attention_kernel
     Piece<C::VC * C::ES> v[GPI][4][C::VL];
     float ks[GPI][2], vs[GPI][2];
 
-    // Loads of one group whose first token is tok0.  Past the request's end the last token is read again (unseen).
+    // Loads of one group whose first token is tok0, without branches: past the request's end its last token is read
+    // again, and a group that is not there reads the pool's first rows (both unseen).
     auto load_k = [&](int q, int64_t row, int tok0) {
-      if (row < 0) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-#pragma unroll
-          for (int u = 0; u < C::KL; ++u) k[q][i][u].clear();
-          ks[q][i] = vs[q][i] = 0.f;
-        }
-        return;
-      }
-      const int over = span.len - 1 - tok0;  // last token there is, within the group
+      const int over = row < 0 ? 15 : span.len - 1 - tok0;
+      const int64_t first = row < 0 ? 0 : row;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int64_t r = row + min(n + 8 * i, over);
+        const int64_t r = first + min(n + 8 * i, over);
         const uint8_t* at_k = static_cast<const uint8_t*>(a.c.k_pages) + r * C::RS + j * (C::KC * C::ES);
 #pragma unroll
         for (int u = 0; u < C::KL; ++u) k[q][i][u].load(at_k + u * (4 * C::KC * C::ES));
@@ -384,17 +391,11 @@ __global__ void __launch_bounds__(PA_NT, pa_resident(NT)) paged_attention_kernel
       }
     };
     auto load_v = [&](int q, int64_t row, int tok0) {
-      if (row < 0) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int u = 0; u < C::VL; ++u) v[q][i][u].clear();
-        return;
-      }
-      const int over = span.len - 1 - tok0;
+      const int over = row < 0 ? 15 : span.len - 1 - tok0;
+      const int64_t first = row < 0 ? 0 : row;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int64_t r = row + min(2 * j + (i & 1) + 8 * (i >> 1), over);
+        const int64_t r = first + min(2 * j + (i & 1) + 8 * (i >> 1), over);
         const uint8_t* at_v = static_cast<const uint8_t*>(a.c.v_pages) + r * C::RS + n * (C::VC * C::ES);
 #pragma unroll
         for (int u = 0; u < C::VL; ++u) v[q][i][u].load(at_v + u * (8 * C::VC * C::ES));
@@ -452,13 +453,15 @@ __global__ void __launch_bounds__(PA_NT, pa_resident(NT)) paged_attention_kernel
       }
       int64_t row[GPI];
       int tok0 = span.start + t0 * TILE;  // of the tile's first group
+      if (span.len > 0) {
 #pragma unroll
-      for (int q = 0; q < GPI; ++q) {
-        row[q] = place();
-        load_k(q, row[q], tok0 + 16 * q);
-        load_v(q, row[q], tok0 + 16 * q);
+        for (int q = 0; q < GPI; ++q) {
+          row[q] = place();
+          load_k(q, row[q], tok0 + 16 * q);
+          load_v(q, row[q], tok0 + 16 * q);
+        }
       }
-      for (int tile = t0; tile < t1; ++tile, tok0 += TILE) {
+      for (int tile = span.len > 0 ? t0 : t1; tile < t1; ++tile, tok0 += TILE) {
         // ---- S^T = K Q^T
         float s[GPI][NT][4];
 #pragma unroll
@@ -531,7 +534,11 @@ __global__ void __launch_bounds__(PA_NT, pa_resident(NT)) paged_attention_kernel
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) s[q][t][i] = capped(s[q][t][i], cap2);
+              for (int i = 0; i < 4; ++i) {
+                const float z = s[q][t][i];
+                s[q][t][i] = capped(z, cap2);
+                if (a.softcap > PA_NEAR_CAP && fabsf(z) < 0.3f * PA_LOG2E) s[q][t][i] = capped_series(z, cap2);
+              }
           }
           if (partly) {
 #pragma unroll
