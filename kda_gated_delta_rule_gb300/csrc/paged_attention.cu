@@ -2,19 +2,39 @@
 #include "device.h"
 #include "paged_attention.cuh"
 
+#ifndef PA_TC_RULE
+#define PA_TC_RULE
+#endif
+
 namespace kda {
 
 namespace {
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 }  // namespace
 
+namespace {
+
+// The workspace's places for `workers` warps or CTAs with row blocks of rb.
+size_t lay_out(PaPlan& p, char* w, int workers, int rb, int d) {
+  const size_t parts = (size_t)workers * 2 * rb;
+  p.part_o = reinterpret_cast<float*>(w);
+  w += up256(parts * d * 4);
+  p.part_ml = reinterpret_cast<float*>(w);
+  w += up256(parts * 8);
+  p.meta = reinterpret_cast<PaMeta*>(w);
+  return up256(parts * d * 4) + up256(parts * 8) + up256(workers * sizeof(PaMeta));
+}
+
+}  // namespace
+
 size_t paged_attention_ws_bytes(int W, int Hq, int Hkv, int d) {
-  // the larger of the forms that a call's types may choose
-  size_t most = 0;
+  // the largest of the forms that a call's types may choose
+  const int rows = W * (Hq / Hkv);
+  PaPlan p;
+  size_t most = lay_out(p, nullptr, PA_SMS, pa_tc_row_block(rows), d);
   for (int fine = 0; fine < 2; ++fine) {
-    const int nt = pa_nt(W * (Hq / Hkv), fine != 0);
-    const size_t parts = (size_t)PA_SMS * pa_resident(nt) * PA_WARPS * 2 * 8 * nt;
-    const size_t n = up256(parts * d * 4) + up256(parts * 8) + up256(parts / (16 * nt) * sizeof(PaMeta));
+    const int nt = pa_nt(rows, fine != 0);
+    const size_t n = lay_out(p, nullptr, PA_SMS * pa_resident(nt) * PA_WARPS, 8 * nt, d);
     most = n > most ? n : most;
   }
   return most;
@@ -27,15 +47,15 @@ cudaError_t launch_paged_attention(const PagedAttnArgs& a, cudaStream_t s) {
   PaPlan p;
   p.G = a.Hq / a.c.Hkv;
   p.rows = a.W * p.G;
+  if (pa_tc_supported(a) PA_TC_RULE) {
+    const int rb = pa_tc_row_block(p.rows);
+    p.blocks = (p.rows + rb - 1) / rb;
+    lay_out(p, reinterpret_cast<char*>(a.ws), PA_SMS, rb, a.c.d);
+    return pa_tc(a, p, sms, s);
+  }
   const int nt = pa_nt(p.rows, fine), rb = 8 * nt;
   p.blocks = (p.rows + rb - 1) / rb;
-  const size_t parts = (size_t)PA_SMS * pa_resident(nt) * PA_WARPS * 2 * rb;
-  char* w = reinterpret_cast<char*>(a.ws);
-  p.part_o = reinterpret_cast<float*>(w);
-  w += up256(parts * a.c.d * 4);
-  p.part_ml = reinterpret_cast<float*>(w);
-  w += up256(parts * 8);
-  p.meta = reinterpret_cast<PaMeta*>(w);
+  lay_out(p, reinterpret_cast<char*>(a.ws), PA_SMS * pa_resident(nt) * PA_WARPS, rb, a.c.d);
   if (a.c.e4m3) return fine ? pa_e4m3_fine(a, p, sms, s) : pa_e4m3(a, p, sms, s);
   return fine ? pa_bf16_fine(a, p, sms, s) : pa_bf16(a, p, sms, s);
 }

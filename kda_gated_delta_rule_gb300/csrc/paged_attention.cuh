@@ -69,6 +69,7 @@ struct PaPlan {  // derived on the host
   float* part_o;   // [warp][2][RB][D]
   float* part_ml;  // [warp][2][RB][2]
   PaMeta* meta;    // [warp]
+  int workers;     // warps launched (entries of meta)
 };
 
 // ---------------------------------------------------------------- instructions
@@ -158,12 +159,13 @@ __device__ __forceinline__ float capped_series(float z, float cap2) {
 
 // ---------------------------------------------------------------- the line of tiles
 
-// Tokens a request's window sees: first seen position rounded down to 16, and the tiles from there to its length.
+// Tokens a request's window sees: first seen position rounded down to `align` (a power of two that divides the page),
+// and the tiles from there to its length.
 struct PaSpan {
   int len, start, tiles;
 };
 template <int TILE>
-__device__ __forceinline__ PaSpan pa_span(const PagedAttnArgs& a, int b, bool flag) {
+__device__ __forceinline__ PaSpan pa_span(const PagedAttnArgs& a, int b, bool flag, int align = 16) {
   PaSpan s;
   s.len = __ldg(a.seq_lens + b);
   if (s.len < 0 || s.len > (int64_t)a.max_pages * a.c.page_size || s.len > PA_MAX_LEN) {
@@ -176,7 +178,7 @@ __device__ __forceinline__ PaSpan pa_span(const PagedAttnArgs& a, int b, bool fl
   }
   int64_t first = a.window > 0 ? (int64_t)s.len - a.W - a.window + 1 : 0;  // of the window's first query
   if (first < 0) first = 0;
-  s.start = (int)first & ~15;
+  s.start = (int)first & -align;
   const int64_t n = (int64_t)s.len - s.start;
   s.tiles = n > 0 ? (int)((n + TILE - 1) / TILE) : 1;  // a unit with nothing to see still writes its rows
   return s;
@@ -731,6 +733,7 @@ __global__ void __launch_bounds__(PA_JOIN_NT) paged_attention_join_kernel(const 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r0 = blockIdx.y * JR;
   for (int w = 0; w < PA_WARPS; ++w) {
     const int x0 = blockIdx.x * PA_WARPS + w;
+    if (x0 >= p.workers) break;
     const PaMeta meta = p.meta[x0];
     if (meta.unit < 0) continue;
     const int rb = meta.unit % p.blocks, bh = meta.unit / p.blocks, h = bh % a.c.Hkv, b = bh / a.c.Hkv;
@@ -819,6 +822,14 @@ __global__ void __launch_bounds__(PA_JOIN_NT) paged_attention_join_kernel(const 
 
 // ---------------------------------------------------------------- launch
 
+template <int D, int RB>
+cudaError_t pa_join(const PagedAttnArgs& a, const PaPlan& p, cudaStream_t s) {
+  const int rows = p.rows < RB ? p.rows : RB;
+  return launch_pdl(paged_attention_join_kernel<D, RB>,
+                    dim3((p.workers + PA_WARPS - 1) / PA_WARPS, (rows + PA_JOIN_ROWS - 1) / PA_JOIN_ROWS),
+                    dim3(PA_JOIN_NT), 0, s, a, p);
+}
+
 template <int D, bool F8, int NT, bool FINE>
 cudaError_t pa_launch(const PagedAttnArgs& a, const PaPlan& p, int sms, cudaStream_t s) {
   using C = PaCfg<D, F8, NT, FINE>;
@@ -832,11 +843,11 @@ cudaError_t pa_launch(const PagedAttnArgs& a, const PaPlan& p, int sms, cudaStre
   int64_t ctas = pa_resident(NT) * (sms < PA_SMS ? sms : PA_SMS);
   const int64_t units = (int64_t)a.B * a.c.Hkv * p.blocks;
   if (tiles < ctas * PA_WARPS && units * tiles < ctas * PA_WARPS) ctas = (units * tiles + PA_WARPS - 1) / PA_WARPS;
-  const cudaError_t e = launch_pdl(kernel, dim3((unsigned)ctas), dim3(PA_NT), C::SMEM, s, a, p);
+  PaPlan plan = p;
+  plan.workers = (int)ctas * PA_WARPS;
+  const cudaError_t e = launch_pdl(kernel, dim3((unsigned)ctas), dim3(PA_NT), C::SMEM, s, a, plan);
   if (e != cudaSuccess) return e;
-  const int rows = p.rows < C::RB ? p.rows : C::RB;
-  return launch_pdl(paged_attention_join_kernel<D, C::RB>, dim3((unsigned)ctas, (rows + PA_JOIN_ROWS - 1) / PA_JOIN_ROWS),
-                    dim3(PA_JOIN_NT), 0, s, a, p);
+  return pa_join<D, C::RB>(a, plan, s);
 }
 
 template <int D, bool F8, bool FINE>
@@ -864,5 +875,9 @@ cudaError_t pa_bf16(const PagedAttnArgs& a, const PaPlan& p, int sms, cudaStream
 cudaError_t pa_bf16_fine(const PagedAttnArgs& a, const PaPlan& p, int sms, cudaStream_t s);
 cudaError_t pa_e4m3(const PagedAttnArgs& a, const PaPlan& p, int sms, cudaStream_t s);
 cudaError_t pa_e4m3_fine(const PagedAttnArgs& a, const PaPlan& p, int sms, cudaStream_t s);
+// the tensor-memory form (paged_attention_tc.cu), for d = 128 with bf16 queries and outputs
+bool pa_tc_supported(const PagedAttnArgs& a);
+int pa_tc_row_block(int rows);
+cudaError_t pa_tc(const PagedAttnArgs& a, const PaPlan& p, int sms, cudaStream_t s);
 
 }  // namespace kda

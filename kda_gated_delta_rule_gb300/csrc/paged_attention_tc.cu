@@ -1,0 +1,870 @@
+// Attention over the paged cache on the 5th-generation tensor cores: d = 128, bf16 queries and outputs.
+//
+// The mathematics, the line of tiles, the parts and their join are those of paged_attention.cuh; what differs is that
+// cached rows never pass through registers.  One CTA per SM walks its share of the line in tiles of 128 tokens:
+//   warp 0   copies the tile's K and V from their pages into a ring of shared-memory slots (TMA, 128-byte swizzle, one box
+//            of consecutive page rows per copy), running ahead of the others by the depth of the ring;
+//   warp 1   issues S^T = K Q^T (128 tokens x the unit's query rows) and O^T += V^T P^T (128 channels x rows): K is the
+//            row operand as it lies, V the same read along its channels;
+//   warp 2   puts the next unit's queries into operand order;
+//   warps 4-7 hold one token per thread: scores from tensor memory, their cap, mask and softmax, and the probabilities to
+//            shared memory as the second product's column operand.
+// An 8-bit cache is multiplied as e4m3: no conversion touches K or V.  The 16-bit side is split into e4m3 parts that
+// take columns of their own: q into 2 (exact for bf16 within 2^-14 of the row's maximum, 2^-22 of it below), p into 3
+// (12 bits, 2^-20 of the reference below).  With a bf16 cache q is one part and p the sum of two (16 bits).
+//
+// Bound by HBM: a tile's copies (32 or 64 KB) take 1400 or 2800 cycles of the SM's share of it, its two products at 16 to
+// 96 columns a few hundred, and its softmax about 13 instructions per score and thread (25 with e4m3 parts).
+//
+// Waits are bounded: one that gives up sets KDA_DEV_TIMEOUT and a flag on which every role leaves.
+#include <stddef.h>
+
+#include "device.h"
+#include "paged_attention.cuh"
+#include "tc_ptx.cuh"
+#include "tmap.h"
+
+namespace kda {
+
+namespace {
+
+constexpr int TC_TILE = 128, TC_D = 128;
+constexpr int TC_SOFT0 = 128;          // first thread of the softmax warps
+#ifndef TCU_
+#define TCU_ 2
+#endif
+constexpr int TC_UNIT_COST = TCU_;     // tiles a unit counts beyond its own
+constexpr float TC_NONE = -1e30f;      // a softmax reference that has seen nothing (finite: no -inf - -inf)
+constexpr float TC_SLACK = 6.f;        // powers of two a score may run above its reference
+constexpr float TC_P_UNIT = 4.f;       // e4m3: probability parts are of p * 4 < 256
+
+#ifndef TC4_
+#define TC4_ 4
+#endif
+#ifndef TC8_
+#define TC8_ 2
+#endif
+#ifndef TC16_
+#define TC16_ 1
+#endif
+template <bool F8, int RB>
+struct TcCfg {
+  static constexpr int ES = F8 ? 1 : 2;
+  static constexpr int QP = F8 ? 2 : 1, PP = F8 ? 3 : 2;  // parts of a query, of a probability
+  static constexpr int N1 = QP * RB < 16 ? 16 : QP * RB;  // columns of the products (multiples of 16)
+  static constexpr int N2 = (PP * RB + 15) / 16 * 16;
+  // softmax groups of four warps: TG of them take tiles in turn (each with accumulators of its own, joined at the end of
+  // the unit), so that one's latencies are covered by the others'; RS of them share a tile's rows
+  static constexpr int TG = RB == 4 ? TC4_ : RB == 8 ? TC8_ : RB == 16 ? TC16_ : 1, RS = RB >= 16 ? 2 : 1;
+  static constexpr int RG = RB / RS;                      // rows of a group
+  static constexpr int NT = TC_SOFT0 + TG * RS * 128;
+  static constexpr int S_COLS = (N1 + 31) / 32 * 32;      // tensor-memory columns of a score buffer
+  static constexpr int SB = TG < 2 ? 2 : TG;              // score and probability buffers
+  static constexpr int O_COL = SB * S_COLS, COLS = O_COL + TG * N2;
+  static constexpr int TMEM_COLS = COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
+  static constexpr int SLOT = TC_TILE * TC_D * ES;        // bytes of a K or V tile
+  static constexpr int Q_BYTES = N1 * TC_D * ES, P_BYTES = N2 * TC_TILE * ES;
+  static constexpr int JOIN = TG > 1 ? 2 * TG * RB * TC_D * 4 : 0;  // the groups' accumulators, two units' worth
+  static constexpr int FIXED = 1024 + SB * P_BYTES + 2 * Q_BYTES + JOIN + 4096;
+  static constexpr int SLOTS_FIT = (227 * 1024 - FIXED) / (SLOT + (F8 ? 1024 : 0));
+  static constexpr int SLOTS = SLOTS_FIT > 10 ? 10 : SLOTS_FIT;
+};
+
+struct TcMaps {
+  CUtensorMap k, v;
+};
+
+template <bool F8, int RB>
+struct TcShared {
+  using C = TcCfg<F8, RB>;
+  uint64_t full[C::SLOTS], empty[C::SLOTS];
+  uint64_t s_full[C::SB], s_free[C::SB], p_full[C::SB], p_free[C::SB], q_full[2], q_free[2], o_full[C::TG], drain;
+  alignas(16) float scales[F8 ? C::SLOTS : 1][2][TC_TILE];  // by V's slot: key and value scales of its tokens
+  int there[C::SLOTS];                                      // by V's slot: boxes copied
+  alignas(16) float factor[2][RB];  // per query row: score in powers of two per unit of the product
+  int last[2][RB];                  // last seen position
+  int head[2][RB];                  // place among the request's W x Hq output rows, -1 past the unit's rows
+  float red[C::TG][4][RB];
+  float jm[2][C::TG][RB], jl[2][C::TG][RB];  // the groups' references and sums
+  int64_t scan[C::NT];
+  int64_t where[2];
+  uint32_t tmem;
+  int dead;
+};
+
+// ---- the share of this CTA, unit by unit and tile by tile; every role walks it on its own
+
+struct TcUnit {
+  int b, h, rb, row0, len, start, tiles, t0, t1;
+};
+struct TcWalk {
+  int64_t at, end, first_of_b;
+  int b;
+};
+__device__ __forceinline__ bool next_unit(const PagedAttnArgs& a, const PaPlan& p, int align, TcWalk& w, TcUnit& u) {
+  const int per_b = a.c.Hkv * p.blocks;
+  while (w.at < w.end) {
+    const PaSpan span = pa_span<TC_TILE>(a, w.b, false, align);
+    const int cost = span.tiles + TC_UNIT_COST;
+    const int in_b = (int)((w.at - w.first_of_b) / cost);
+    const int64_t first = w.first_of_b + (int64_t)in_b * cost, last = first + cost;
+    u.b = w.b;
+    u.h = in_b / p.blocks;
+    u.rb = in_b - u.h * p.blocks;
+    u.len = span.len, u.start = span.start, u.tiles = span.tiles;
+    u.t0 = max(0, (int)(w.at - first) - TC_UNIT_COST);
+    u.t1 = (int)((w.end < last ? w.end : last) - first) - TC_UNIT_COST;
+    w.at = w.end < last ? w.end : last;
+    if (in_b == per_b - 1 && w.at == last) {
+      w.first_of_b = last;
+      ++w.b;
+    }
+    if (u.t1 > u.t0) return true;
+  }
+  return false;
+}
+struct TcTiles {
+  TcWalk w;
+  TcUnit u;
+  int tile, unit_no;
+  __device__ __forceinline__ explicit TcTiles(const TcWalk& from) : w(from), tile(0), unit_no(-1) { u.t1 = 0; }
+  __device__ __forceinline__ bool next(const PagedAttnArgs& a, const PaPlan& p, int align) {
+    if (unit_no >= 0 && ++tile < u.t1) return true;
+    if (!next_unit(a, p, align, w, u)) return false;
+    tile = u.t0;
+    ++unit_no;
+    return true;
+  }
+  __device__ __forceinline__ bool first() const { return tile == u.t0; }
+  __device__ __forceinline__ bool last() const { return tile + 1 == u.t1; }
+};
+
+__device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float2 of_e4m3_pair(uint32_t two) {
+  const uint32_t h = half2_of_codes(two);
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+__device__ __forceinline__ void st_shared_u8(uint32_t at, uint32_t v) {
+  asm volatile("st.shared.u8 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
+__device__ __forceinline__ void st_shared_u16(uint32_t at, uint32_t v) {
+  asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"((uint16_t)v) : "memory");
+}
+
+// A thread's raw scores of a group's RG rows, parts put together; `at`: the first part's first column.
+template <bool F8, int RB, int RG>
+__device__ __forceinline__ void load_scores(uint32_t at, float (&x)[RG]) {
+  if constexpr (F8 && RB == 4) {
+    float s[8];
+    tc::tmem_ld8(at, s);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = fmaf(s[4 + i], 1.f / 16.f, s[i]);
+  } else if constexpr (F8) {
+#pragma unroll
+    for (int r0 = 0; r0 < RG; r0 += 8) {
+      float s[16];
+      tc::tmem_ld8x2(at + r0, at + RB + r0, s);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[r0 + i] = fmaf(s[8 + i], 1.f / 16.f, s[i]);
+    }
+  } else if constexpr (RG <= 8) {
+    float s[8];
+    tc::tmem_ld8(at, s);
+#pragma unroll
+    for (int i = 0; i < RG; ++i) x[i] = s[i];
+  } else {
+    static_assert(RG % 16 == 0, "groups of at most 8 rows, or of 16");
+#pragma unroll
+    for (int r0 = 0; r0 < RG; r0 += 16) tc::tmem_ld16(at + r0, x + r0);
+  }
+}
+
+// A bounded wait that also ends when another role has given up.
+__device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, int* dead) {
+  for (int i = 0; i < 1 << 12; ++i) {
+    if (*reinterpret_cast<volatile int*>(dead)) return false;
+    if (tc::bar_wait(bar, parity, 1u << 10)) return true;
+  }
+  *reinterpret_cast<volatile int*>(dead) = 1;
+  return false;
+}
+
+// One row of a part by one warp, token by token in fp32: the way out when the accumulators hold a NaN, which may come from
+// a query that meets a token it does not see (0 * NaN) or from an infinity meeting a split probability.  A lane has
+// channels 4 lane .. 4 lane + 3.
+template <bool F8>
+__device__ __noinline__ void careful_row(const PagedAttnArgs& a, const PaPlan& p, const TcUnit& u, int qrow, float4& o,
+                                         float& m, float& l) {
+  const int lane = threadIdx.x & 31, w = qrow / p.G, g = qrow - w * p.G;
+  const int64_t head = ((int64_t)u.b * a.W + w) * a.Hq + (int64_t)u.h * p.G + g;
+  const bf16* q = static_cast<const bf16*>(a.q) + head * TC_D + 4 * lane;
+  const float q0 = to_f32(q[0]), q1 = to_f32(q[1]), q2 = to_f32(q[2]), q3 = to_f32(q[3]);
+  const int last = u.len - a.W + w, window = a.window > 0 ? a.window : 0x7fffffff;
+  const int64_t lo = max((int64_t)u.start + (int64_t)u.t0 * TC_TILE, (int64_t)last - window + 1);
+  const int64_t hi = min(min((int64_t)u.len, (int64_t)u.start + (int64_t)u.t1 * TC_TILE), (int64_t)last + 1);
+  o = make_float4(0.f, 0.f, 0.f, 0.f);
+  m = TC_NONE;
+  l = 0.f;
+  for (int64_t tok = lo < 0 ? 0 : lo; tok < hi; ++tok) {
+    const int pg = (int)(tok / a.c.page_size), page = __ldg(a.block_table + (int64_t)u.b * a.max_pages + pg);
+    if ((unsigned)page >= (unsigned)a.c.num_pages) continue;
+    const int64_t row = ((int64_t)page * a.c.Hkv + u.h) * a.c.page_size + (tok - (int64_t)pg * a.c.page_size);
+    float k[4], v[4];
+    if constexpr (F8) {
+      const uint32_t kc = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.c.k_pages) + row * TC_D + 4 * lane);
+      const uint32_t vc = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.c.v_pages) + row * TC_D + 4 * lane);
+      const float2 k0 = of_e4m3_pair(kc & 0xffffu), k1 = of_e4m3_pair(kc >> 16);
+      const float2 v0 = of_e4m3_pair(vc & 0xffffu), v1 = of_e4m3_pair(vc >> 16);
+      const float ks = a.c.k_scales[row], vs = a.c.v_scales[row];
+      k[0] = k0.x * ks, k[1] = k0.y * ks, k[2] = k1.x * ks, k[3] = k1.y * ks;
+      v[0] = v0.x * vs, v[1] = v0.y * vs, v[2] = v1.x * vs, v[3] = v1.y * vs;
+    } else {
+      const bf16* kp = static_cast<const bf16*>(a.c.k_pages) + row * TC_D + 4 * lane;
+      const bf16* vp = static_cast<const bf16*>(a.c.v_pages) + row * TC_D + 4 * lane;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) k[i] = to_f32(kp[i]), v[i] = to_f32(vp[i]);
+    }
+    float s = q0 * k[0] + q1 * k[1] + q2 * k[2] + q3 * k[3];
+#pragma unroll
+    for (int i = 16; i > 0; i >>= 1) s += __shfl_xor_sync(0xffffffffu, s, i);
+    s *= a.scale;
+    s = a.softcap > 0.f ? a.softcap * tanhf(s / a.softcap) * PA_LOG2E : s * PA_LOG2E;
+    const float mn = fmaxf(m, s), by = ex2(m - mn), e = ex2(s - mn);
+    m = mn;
+    l = l * by + e;
+    o.x = o.x * by + e * v[0], o.y = o.y * by + e * v[1], o.z = o.z * by + e * v[2], o.w = o.w * by + e * v[3];
+  }
+}
+
+template <bool F8, int RB>
+__global__ void __launch_bounds__(TcCfg<F8, RB>::NT, 1)
+    paged_attention_tc_kernel(const __grid_constant__ TcMaps maps, const PagedAttnArgs a, const PaPlan p, const int box) {
+  using C = TcCfg<F8, RB>;
+  using Sh = TcShared<F8, RB>;
+  constexpr int ES = C::ES, N1 = C::N1, N2 = C::N2, SLOT = C::SLOT, SLOTS = C::SLOTS, QP = C::QP, PP = C::PP;
+  constexpr int TG = C::TG, RS = C::RS, RG = C::RG, SB = C::SB, TC_NT = C::NT;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  unsigned char* slots = base;
+  unsigned char* pbuf = slots + SLOTS * SLOT;
+  unsigned char* qbuf = pbuf + SB * C::P_BYTES;
+  float* join = reinterpret_cast<float*>(qbuf + 2 * C::Q_BYTES);  // [2][TG][RB][128]
+  Sh& sh = *reinterpret_cast<Sh*>(qbuf + 2 * C::Q_BYTES + C::JOIN);
+  pdl_begin();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int Hkv = a.c.Hkv, per_b = Hkv * p.blocks;
+
+  if (tid == 0) {
+    for (int i = 0; i < SLOTS; ++i) tc::bar_init(&sh.full[i], 1), tc::bar_init(&sh.empty[i], 1);
+    for (int i = 0; i < SB; ++i) {
+      tc::bar_init(&sh.s_full[i], 1), tc::bar_init(&sh.s_free[i], 4 * RS);
+      tc::bar_init(&sh.p_full[i], 4 * RS), tc::bar_init(&sh.p_free[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) tc::bar_init(&sh.q_full[i], 1), tc::bar_init(&sh.q_free[i], 1 + 4 * TG * RS);
+    for (int i = 0; i < TG; ++i) tc::bar_init(&sh.o_full[i], 1);
+    tc::bar_init(&sh.drain, 1);
+    tc::bar_fence_init();
+    sh.dead = 0;
+  }
+  if (warp == 1) tc::tmem_alloc(&sh.tmem, C::TMEM_COLS);
+
+  // ---- this CTA's share of the line (see paged_attention.cuh)
+  const int run = (a.B + TC_NT - 1) / TC_NT;
+  int64_t mine = 0;
+  for (int b = tid * run; b < min(a.B, (tid + 1) * run); ++b)
+    mine += pa_span<TC_TILE>(a, b, blockIdx.x == 0, box).tiles + TC_UNIT_COST;
+  sh.scan[tid] = mine;
+  __syncthreads();
+  for (int o = 1; o < TC_NT; o <<= 1) {
+    const int64_t v = tid >= o ? sh.scan[tid - o] : 0;
+    __syncthreads();
+    sh.scan[tid] += v;
+    __syncthreads();
+  }
+  const int64_t total = sh.scan[TC_NT - 1] * per_b;
+  const int64_t workers = total < gridDim.x ? total : (int64_t)gridDim.x;
+  const int64_t me = blockIdx.x;
+  TcWalk walk;
+  walk.at = me < workers ? me * total / workers : 0;
+  walk.end = me < workers ? (me + 1) * total / workers : 0;
+  const int64_t before = sh.scan[tid] - mine;
+  if (me < workers && walk.at >= before * per_b && walk.at < sh.scan[tid] * per_b) {
+    int64_t f = before;
+    for (int b = tid * run;; ++b) {
+      const int t = pa_span<TC_TILE>(a, b, false, box).tiles + TC_UNIT_COST;
+      if (walk.at < (f + t) * per_b) {
+        sh.where[0] = b;
+        sh.where[1] = f * per_b;
+        break;
+      }
+      f += t;
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  walk.b = me < workers ? (int)sh.where[0] : 0;
+  walk.first_of_b = me < workers ? sh.where[1] : 0;
+  const uint32_t tmem = sh.tmem, tmem_o = tmem + C::O_COL;
+  const int window = a.window > 0 ? a.window : 0x7fffffff;
+
+  if (warp == 0) {
+    // ---- copies
+    TcTiles it(walk);
+    const int boxes = TC_TILE / box;
+    bool ok = true;
+    unsigned half = 0;  // K tiles are the even ones, V tiles the odd
+    while (ok && it.next(a, p, box)) {
+      const int64_t tok = (int64_t)it.u.start + (int64_t)it.tile * TC_TILE + lane * box;
+      bool there = lane < boxes && tok < it.u.len;
+      int row = 0;
+      if (there) {
+        const int pg = (int)tok / a.c.page_size, page = __ldg(a.block_table + (int64_t)it.u.b * a.max_pages + pg);
+        there = (unsigned)page < (unsigned)a.c.num_pages;
+        if (there) row = (page * Hkv + it.u.h) * a.c.page_size + ((int)tok - pg * a.c.page_size);
+        else flag_status(a.status, KDA_DEV_PAGE_OOB);
+      }
+      const unsigned mask = __ballot_sync(0xffffffffu, there);
+      const uint32_t bytes = __popc(mask) * box * TC_D * ES;
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv, ++half) {
+        const unsigned slot = half % SLOTS;
+        if (half >= (unsigned)SLOTS) ok = tc_wait(&sh.empty[slot], (half / SLOTS - 1) & 1, &sh.dead);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (lane == 0) {
+          if (kv) sh.there[slot] = (int)mask;
+          tc::bar_arrive_expect_tx(&sh.full[slot], bytes + (F8 && kv ? __popc(mask) * box * 8 : 0));
+        }
+        __syncwarp();
+        if (there) {
+          unsigned char* dst = slots + slot * SLOT + lane * box * 128;
+          const CUtensorMap* map = kv ? &maps.v : &maps.k;
+          tc::tma_load_2d(dst, map, 0, row, &sh.full[slot]);
+          if constexpr (!F8) tc::tma_load_2d(dst + TC_TILE * 128, map, 64, row, &sh.full[slot]);
+          if constexpr (F8) {
+            if (kv) {
+              tc::bulk_g2s(&sh.scales[slot][0][lane * box], a.c.k_scales + row, box * 4, &sh.full[slot]);
+              tc::bulk_g2s(&sh.scales[slot][1][lane * box], a.c.v_scales + row, box * 4, &sh.full[slot]);
+            }
+          }
+        }
+        __syncwarp();
+      }
+    }
+    if (!ok) {  // let what is on its way arrive before the CTA ends
+      if (lane == 0) {
+        flag_status(a.status, KDA_DEV_TIMEOUT);
+        for (unsigned i = half > (unsigned)SLOTS ? half - SLOTS : 0; i < half; ++i)
+          tc::bar_wait(&sh.full[i % SLOTS], (i / SLOTS) & 1, 1u << 16);
+      }
+      __syncwarp();
+    }
+  } else if (warp == 1) {
+    // ---- products, one thread
+    if (lane == 0) {
+      constexpr uint32_t id1 = F8 ? tc::idesc_e4m3(128, N1) : tc::idesc_bf16(128, N1);
+      constexpr uint32_t id2 = (F8 ? tc::idesc_e4m3(128, N2) : tc::idesc_bf16(128, N2)) | tc::IDESC_A_MN;
+      // Two places on the line of tiles: the next first product, up to AHEAD tiles before the next second one (so that
+      // every group has scores to work on; the ring has room for that).  Whichever has its operands is issued.
+      constexpr unsigned AHEAD = SB < SLOTS / 2 ? SB : SLOTS / 2;
+      TcTiles ahead(walk), now(walk);
+      unsigned ga = 0, gn = 0;  // tiles numbered over the CTA's whole share; tile g has buffers g % SB, group g % TG
+      bool has_a = ahead.next(a, p, box), has_n = now.next(a, p, box), ok = true;
+      unsigned idle = 0;
+      while (has_n) {
+        bool done = false;
+        if (has_a && ga < gn + AHEAD) {
+          const unsigned slot = 2 * ga % SLOTS, buf = ga % SB;
+          if (tc::bar_test(&sh.full[slot], (2 * ga / SLOTS) & 1) &&
+              (!ahead.first() || tc::bar_test(&sh.q_full[ahead.unit_no & 1], (ahead.unit_no >> 1) & 1)) &&
+              (ga < SB || tc::bar_test(&sh.s_free[buf], (ga / SB - 1) & 1))) {
+            tc::fence_after_sync();
+            const uint32_t kb = tc::smem_u32(slots + slot * SLOT);
+            const uint32_t qb = tc::smem_u32(qbuf + (ahead.unit_no & 1) * C::Q_BYTES);
+#pragma unroll
+            for (int kk = 0; kk < 4 * ES; ++kk) {  // 32 bytes of each row per step
+              const uint32_t blk = kk / 4, in = (kk % 4) * 32;
+              const uint64_t da = tc::sdesc(kb + blk * (TC_TILE * 128) + in), db = tc::sdesc(qb + blk * (N1 * 128) + in);
+              if constexpr (F8) tc::mma_ss_f8(tmem + buf * C::S_COLS, da, db, id1, kk > 0);
+              else tc::mma_ss(tmem + buf * C::S_COLS, da, db, id1, kk > 0);
+            }
+            tc::commit(&sh.empty[slot]);
+            tc::commit(&sh.s_full[buf]);
+            if (ahead.last()) tc::commit(&sh.q_free[ahead.unit_no & 1]);
+            ++ga;
+            has_a = ahead.next(a, p, box);
+            done = true;
+          }
+        }
+        const unsigned slot = (2 * gn + 1) % SLOTS, buf = gn % SB, grp = gn % TG;
+        if (gn < ga && tc::bar_test(&sh.p_full[buf], (gn / SB) & 1) &&
+            tc::bar_test(&sh.full[slot], ((2 * gn + 1) / SLOTS) & 1)) {
+          tc::fence_after_sync();
+          const uint32_t vb = tc::smem_u32(slots + slot * SLOT), pb = tc::smem_u32(pbuf + buf * C::P_BYTES);
+          const bool begins = now.tile - TG < now.u.t0;  // the group's first tile of the unit
+#pragma unroll
+          for (int kk = 0; kk < 4 * ES; ++kk) {  // 32 (e4m3) or 16 tokens per step
+            const uint32_t blk = kk / 4, in = (kk % 4) * 32;
+            const uint64_t da = tc::sdesc_mn(vb + kk * (F8 ? 4096 : 2048), TC_TILE * 128);
+            const uint64_t db = tc::sdesc(pb + blk * (N2 * 128) + in);
+            const uint32_t add = !(begins && kk == 0);
+            if constexpr (F8) tc::mma_ss_f8(tmem_o + grp * N2, da, db, id2, add);
+            else tc::mma_ss(tmem_o + grp * N2, da, db, id2, add);
+          }
+          tc::commit(&sh.empty[slot]);
+          tc::commit(&sh.p_free[buf]);
+          if (now.tile + TG >= now.u.t1) tc::commit(&sh.o_full[grp]);  // the group's last tile of the unit
+          ++gn;
+          has_n = now.next(a, p, box);
+          done = true;
+        }
+        if (done) {
+          idle = 0;
+        } else if (++idle > 1u << 24 || *reinterpret_cast<volatile int*>(&sh.dead)) {
+          *reinterpret_cast<volatile int*>(&sh.dead) = 1;
+          ok = false;
+          break;
+        }
+      }
+      if (!ok) {
+        flag_status(a.status, KDA_DEV_TIMEOUT);
+        tc::commit(&sh.drain);
+        tc::bar_wait(&sh.drain, 0, 1u << 16);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // ---- queries of each unit, a row of 128 channels at a time, four channels a lane
+    TcWalk w = walk;
+    TcUnit u;
+    bool ok = true;
+    for (int un = 0; ok && next_unit(a, p, box, w, u); ++un) {
+      const int buf = un & 1, row0 = u.rb * RB;
+      if (un >= 2) ok = tc_wait(&sh.q_free[buf], ((un >> 1) - 1) & 1, &sh.dead);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const uint32_t qb = tc::smem_u32(qbuf + buf * C::Q_BYTES);
+      constexpr int QCH = RB < 8 ? RB : 8;
+#pragma unroll 1
+      for (int r0 = 0; r0 < RB; r0 += QCH) {
+        uint2 raw[QCH];
+#pragma unroll
+        for (int i = 0; i < QCH; ++i) {
+          const int row = row0 + r0 + i, wt = row / p.G, g = row - wt * p.G;
+          const int64_t head = ((int64_t)u.b * a.W + wt) * a.Hq + (int64_t)u.h * p.G + g;
+          raw[i] = row < p.rows
+                       ? __ldg(reinterpret_cast<const uint2*>(static_cast<const bf16*>(a.q) + head * TC_D + 4 * lane))
+                       : make_uint2(0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < QCH; ++i) {
+          const int r = r0 + i, row = row0 + r;
+          float down = 1.f;
+          if constexpr (F8) {
+            const float x0 = __uint_as_float(raw[i].x << 16), x1 = __uint_as_float(raw[i].x & 0xffff0000u);
+            const float x2 = __uint_as_float(raw[i].y << 16), x3 = __uint_as_float(raw[i].y & 0xffff0000u);
+            float amax = fmaxf(fmaxf(fabsf(x0), fabsf(x1)), fmaxf(fabsf(x2), fabsf(x3)));
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            int e = amax > 0.f ? 7 - ((int)(__float_as_uint(amax) >> 23) - 127) : 0;  // the maximum to [2^7, 2^8)
+            e = max(-120, min(120, e));
+            const float up = __uint_as_float((uint32_t)(e + 127) << 23);
+            down = __uint_as_float((uint32_t)(127 - e) << 23);
+            float v0 = x0 * up, v1 = x1 * up, v2 = x2 * up, v3 = x3 * up;
+#pragma unroll
+            for (int part = 0; part < QP; ++part) {
+              const uint32_t c0 = e4m3_pair(v0, v1), c1 = e4m3_pair(v2, v3);
+              const float2 f0 = of_e4m3_pair(c0), f1 = of_e4m3_pair(c1);
+              const int nrow = part * RB + r;
+              const uint32_t at = qb + nrow * 128 + (((lane >> 2) ^ (nrow & 7)) << 4) + (lane & 3) * 4;
+              asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(c0 | c1 << 16) : "memory");
+              v0 = (v0 - f0.x) * 16.f, v1 = (v1 - f0.y) * 16.f, v2 = (v2 - f1.x) * 16.f, v3 = (v3 - f1.y) * 16.f;
+            }
+          } else {
+            // channels 4 lane ..: block of 64 channels, 16-byte chunk of 8
+            const uint32_t at = qb + (lane >> 4) * (N1 * 128) + r * 128 + ((((lane & 15) >> 1) ^ (r & 7)) << 4) + (lane & 1) * 8;
+            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(raw[i].x), "r"(raw[i].y) : "memory");
+          }
+          if (lane == 0) {
+            const int wt = row / p.G, g = row - wt * p.G;
+            sh.factor[buf][r] = down * a.scale * (a.softcap > 0.f ? 2.f * PA_LOG2E / a.softcap : PA_LOG2E);
+            sh.last[buf][r] = row < p.rows ? u.len - a.W + wt : -1;
+            sh.head[buf][r] = row < p.rows ? wt * a.Hq + u.h * p.G + g : -1;
+          }
+        }
+      }
+      tc::fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) tc::bar_arrive(&sh.q_full[buf]);
+    }
+    if (!ok && lane == 0) flag_status(a.status, KDA_DEV_TIMEOUT);
+  } else if (warp >= 4) {
+    // ---- softmax: thread = token of the tile, then channel of the output.  A role that gives up a wait goes on through
+    // its tiles without results (no later wait holds it), so that the barriers between groups are always met.
+    const int tk = (tid - TC_SOFT0) & 127, quarter = warp & 3, sg = (warp - 4) >> 2, tg = sg / RS, rs = sg % RS;
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    const float cap2 = a.softcap * PA_LOG2E;
+    const int bar_id = 1 + sg, rfirst = rs * RG;  // this group's rows of the unit
+    float m[RG], l[RG];
+    TcTiles it(walk);
+    unsigned g = 0;
+    int units = -1;
+    unsigned o_uses = 0;  // of this group's accumulators
+    bool bad = false, mine_any = false;
+    PaMeta meta{-1, 0};
+    int rows_done = 0;
+    // where this thread's element of an operand row lies in a probability buffer: (place ^ (row % 8) * 16) + row * 128
+    const uint32_t place = F8 ? ((uint32_t)(tk >> 4) << 4) + (tk & 15)
+                              : (uint32_t)(tk >> 6) * (N2 * 128) + ((uint32_t)((tk & 63) >> 3) << 4) + (tk & 7) * 2;
+    for (; it.next(a, p, box); ++g) {
+      const TcUnit& u = it.u;
+      const int qb = it.unit_no & 1, row0 = u.rb * RB, nrows = min(RB, p.rows - row0);
+      if (it.unit_no != units) {
+        units = it.unit_no;
+        mine_any = false;
+        bad |= !tc_wait(&sh.q_full[qb], (it.unit_no >> 1) & 1, &sh.dead);
+#pragma unroll
+        for (int r = 0; r < RG; ++r) m[r] = TC_NONE, l[r] = 0.f;
+      }
+      if (TG == 1 || (int)(g % TG) == tg) {
+        const bool begins = !mine_any;
+        mine_any = true;
+        const unsigned vslot = (2 * g + 1) % SLOTS, buf = g % SB;
+        bad |= !tc_wait(&sh.full[vslot], ((2 * g + 1) / SLOTS) & 1, &sh.dead);
+        const int64_t tok0 = (int64_t)u.start + (int64_t)it.tile * TC_TILE;
+        const int tok = (int)tok0 + tk;
+        const bool there = tok < u.len && (sh.there[vslot] >> (tk / box) & 1);
+        float ks = 1.f, vs = 1.f, lift = 0.f;
+        if constexpr (F8) {
+          ks = there ? sh.scales[vslot][0][tk] : 0.f;
+          vs = there ? sh.scales[vslot][1][tk] : 0.f;
+          lift = (float)((int)(__float_as_uint(vs) >> 23) - 126);  // just above log2 of the value scale
+        }
+        const int all_to = u.len - a.W + row0 / p.G;
+        const int64_t all_from = (int64_t)u.len - a.W + (row0 + nrows - 1) / p.G - window + 1;
+        const bool masked = !there || tok0 + TC_TILE - 1 > all_to || tok0 < all_from;
+
+        bad |= !tc_wait(&sh.s_full[buf], (g / SB) & 1, &sh.dead);
+        tc::fence_after_sync();
+        float x[RG];
+        load_scores<F8, RB, RG>(tmem + buf * C::S_COLS + lanes + rfirst, x);
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::bar_arrive(&sh.s_free[buf]);
+#pragma unroll
+        for (int r = 0; r < RG; r += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(&sh.factor[qb][rfirst + r]);
+          x[r] *= f.x * ks, x[r + 1] *= f.y * ks, x[r + 2] *= f.z * ks, x[r + 3] *= f.w * ks;
+        }
+        if (a.softcap > 0.f) {
+          if (a.softcap <= PA_NEAR_CAP) {
+#pragma unroll
+            for (int r = 0; r < RG; ++r) x[r] = capped(x[r], cap2);
+          } else {
+#pragma unroll
+            for (int r = 0; r < RG; ++r)
+              x[r] = fabsf(x[r]) < 0.3f * PA_LOG2E ? capped_series(x[r], cap2) : capped(x[r], cap2);
+          }
+        }
+        if (masked) {
+#pragma unroll
+          for (int r = 0; r < RG; ++r) {
+            const int last = sh.last[qb][rfirst + r];
+            x[r] = there && tok <= last && tok > (int64_t)last - window ? x[r] : -INFINITY;
+          }
+        }
+        float over = -INFINITY;
+#pragma unroll
+        for (int r = 0; r < RG; ++r) over = fmaxf(over, x[r] - m[r]);
+        if (tc::named_bar_or(bar_id, 128, over + lift > TC_SLACK)) {
+          // ---- references move: the rows' maxima over the 128 tokens, then sums and accumulators follow
+#pragma unroll
+          for (int r = 0; r < RG; ++r) {
+            float t = x[r] + lift;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
+            if (lane == 0) sh.red[tg][quarter][rfirst + r] = t;
+          }
+          // the group's last product into its accumulators is through
+          if (!begins) bad |= !tc_wait(&sh.p_free[(g - TG) % SB], ((g - TG) / SB) & 1, &sh.dead);
+          tc::fence_after_sync();
+          tc::named_bar(bar_id, 128);
+          float by[RG];
+#pragma unroll
+          for (int r = 0; r < RG; ++r) {
+            const float(&red)[4][RB] = sh.red[tg];
+            const int q = rfirst + r;
+            const float mn = fmaxf(fmaxf(fmaxf(red[0][q], red[1][q]), fmaxf(red[2][q], red[3][q])), m[r]);
+            by[r] = ex2(m[r] - mn);
+            m[r] = mn;
+            l[r] *= by[r];
+          }
+          if (!begins) {
+            if constexpr (RG < 8) {  // column c is row c % RB's; the group has all rows
+#pragma unroll
+              for (int c = 0; c < PP * RB; c += 8) {
+                float v[8];
+                tc::tmem_ld8(tmem_o + tg * N2 + lanes + c, v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] *= by[(c + i) % RB];
+                tc::tmem_st8f(tmem_o + tg * N2 + lanes + c, v);
+              }
+            } else {
+#pragma unroll
+              for (int part = 0; part < PP; ++part)
+#pragma unroll
+                for (int c = 0; c < RG; c += 8) {
+                  float v[8];
+                  const uint32_t at = tmem_o + tg * N2 + lanes + part * RB + rfirst + c;
+                  tc::tmem_ld8(at, v);
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) v[i] *= by[c + i];
+                  tc::tmem_st8f(at, v);
+                }
+            }
+            tc::tmem_wait_st();
+          }
+          tc::named_bar(bar_id, 128);  // red may be written again
+        }
+
+        // ---- probabilities and their parts
+        if (g >= SB) bad |= !tc_wait(&sh.p_free[buf], (g / SB - 1) & 1, &sh.dead);
+        const uint32_t pb = tc::smem_u32(pbuf + buf * C::P_BYTES) + place;
+        const float pv = F8 ? vs * TC_P_UNIT : 1.f;
+#pragma unroll
+        for (int r = 0; r < RG; r += 2) {
+          float p0 = ex2(x[r] - m[r]), p1 = ex2(x[r + 1] - m[r + 1]);
+          l[r] += p0;
+          l[r + 1] += p1;
+          __half2 h;
+          if constexpr (F8) h = __floats2half2_rn(p0 * pv, p1 * pv);  // 11 bits, which the three parts hold
+#pragma unroll
+          for (int part = 0; part < PP; ++part) {
+            const int c0 = part * RB + r;  // the operand's row is this plus rfirst (a multiple of 8, or 0)
+            const uint32_t a0 = (pb ^ ((c0 & 7) << 4)) + (rfirst + c0) * 128;
+            const uint32_t a1 = (pb ^ (((c0 + 1) & 7) << 4)) + (rfirst + c0 + 1) * 128;
+            uint32_t c;
+            if constexpr (F8) {
+              uint16_t c16;
+              asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c16) : "r"(*reinterpret_cast<const uint32_t*>(&h)));
+              c = c16;
+              st_shared_u8(a0, c & 0xffu);
+              st_shared_u8(a1, c >> 8);
+              if (part + 1 < PP) {
+                const uint32_t back = half2_of_codes(c);
+                h = __hmul2(__hsub2(h, *reinterpret_cast<const __half2*>(&back)), __float2half2_rn(16.f));
+              }
+            } else {
+              c = split_pair<false>(p0, p1);
+              st_shared_u16(a0, c & 0xffffu);
+              st_shared_u16(a1, c >> 16);
+            }
+          }
+        }
+        if (!there && rs == 0) {  // what lies in the slot for a token that is not there must not be a NaN
+          unsigned char* vrow = slots + vslot * SLOT + tk * 128;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            reinterpret_cast<uint4*>(vrow)[i] = make_uint4(0, 0, 0, 0);
+            if constexpr (!F8) reinterpret_cast<uint4*>(vrow + TC_TILE * 128)[i] = make_uint4(0, 0, 0, 0);
+          }
+        }
+        tc::fence_proxy_async();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::bar_arrive(&sh.p_full[buf]);
+      }
+      if (!it.last()) continue;
+
+      // ---- end of the unit's part
+      __syncwarp();
+      const int jb = it.unit_no & 1;
+      const bool whole = u.t0 == 0 && u.t1 == u.tiles;
+      const int64_t part_at = (me * 2 + (u.t0 == 0 ? 1 : 0)) * RB;
+      bool nan = false;
+      // writes row r (of the unit) of the result: accumulator y of channel tk, reference mr, sum lr
+      auto put = [&](int r, float y, float mr, float lr) {
+        const bool none = mr == TC_NONE && lr == 0.f;
+        if (mr == TC_NONE) mr = none ? -INFINITY : 0.f;  // nothing but NaN scores: let them through
+        if (none) y = 0.f;
+        const int hd = sh.head[qb][r];
+        if (hd < 0 || bad) return;
+        nan |= isnan(y);
+        if (whole) {
+          const int64_t head = (int64_t)u.b * a.W * a.Hq + hd;
+          static_cast<bf16*>(a.out)[head * TC_D + tk] = __float2bfloat16_rn(none ? 0.f : y / lr);
+          if (tk == 0 && a.lse) a.lse[head] = none ? -INFINITY : (mr + log2f(lr)) * PA_LN2;
+        } else {
+          p.part_o[(part_at + r) * TC_D + tk] = y;
+          if (tk == 0) *reinterpret_cast<float2*>(p.part_ml + (part_at + r) * 2) = make_float2(mr, lr);
+        }
+      };
+      if (mine_any) {
+#pragma unroll
+        for (int r = 0; r < RG; ++r) {
+          float t = l[r];
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+          if (lane == 0) sh.red[tg][quarter][rfirst + r] = t;
+        }
+        bad |= !tc_wait(&sh.o_full[tg], o_uses & 1, &sh.dead);
+        ++o_uses;
+        tc::fence_after_sync();
+        tc::named_bar(bar_id, 128);
+        constexpr int CH = RG < 8 ? RG : 8;
+#pragma unroll
+        for (int r0 = 0; r0 < RG; r0 += CH) {
+          float o[PP * CH];
+          if constexpr (RG < 8) {
+            float t[16];
+            tc::tmem_ld16(tmem_o + tg * N2 + lanes, t);
+#pragma unroll
+            for (int i = 0; i < PP * CH; ++i) o[i] = t[i];
+          } else {
+#pragma unroll
+            for (int part = 0; part < PP; ++part)
+              tc::tmem_ld8(tmem_o + tg * N2 + lanes + part * RB + rfirst + r0, o + part * CH);
+          }
+#pragma unroll
+          for (int i = 0; i < CH; ++i) {
+            const int r = rfirst + r0 + i;
+            float y;
+            if constexpr (F8) y = fmaf(o[2 * CH + i], 1.f / 256.f, fmaf(o[CH + i], 1.f / 16.f, o[i])) * (1.f / TC_P_UNIT);
+            else y = o[i] + o[CH + i];
+            const float lr = sh.red[tg][0][r] + sh.red[tg][1][r] + sh.red[tg][2][r] + sh.red[tg][3][r];
+            if constexpr (TG == 1) {
+              put(r, y, m[r0 + i], lr);
+            } else {
+              join[((jb * TG + tg) * RB + r) * TC_D + tk] = y;
+              if (tk == 0) sh.jm[jb][tg][r] = m[r0 + i], sh.jl[jb][tg][r] = lr;
+            }
+          }
+        }
+        tc::fence_before_sync();
+      } else if (TG > 1 && tk < RB) {
+        sh.jm[jb][tg][tk] = TC_NONE, sh.jl[jb][tg][tk] = 0.f;  // a unit of fewer tiles than groups
+      }
+      if constexpr (TG > 1) {
+        // the groups' results together, rows dealt out to them.  The other unit's half of `join` takes the next results,
+        // so this barrier is also what frees this half for the one after.
+        tc::named_bar(15, TG * RS * 128);
+        for (int r = tg; r < nrows; r += TG) {
+          float mr = TC_NONE, lr = 0.f, y = 0.f;
+#pragma unroll
+          for (int i = 0; i < TG; ++i) mr = fmaxf(mr, sh.jm[jb][i][r]);
+#pragma unroll
+          for (int i = 0; i < TG; ++i) {
+            const float mi = sh.jm[jb][i][r], li = sh.jl[jb][i][r];
+            if (mi == TC_NONE && li == 0.f) continue;  // saw nothing: its accumulators may never have been written
+            const float by = ex2(mi - mr);
+            lr += li * by;
+            y += join[((jb * TG + i) * RB + r) * TC_D + tk] * by;
+          }
+          put(r, y, mr, lr);
+        }
+      }
+      if (tc::named_bar_or(bar_id, 128, nan)) {  // also: red may be written again
+        // rows this group wrote: all of its rows (TG = 1), or every TG-th
+        for (int i = quarter; i < RG; i += 4) {
+          const int r = TG == 1 ? rfirst + i : tg + i * TG;
+          if (r >= nrows || bad) continue;
+          float4 o;
+          float mr, lr;
+          careful_row<F8>(a, p, u, row0 + r, o, mr, lr);
+          const bool none = mr == TC_NONE && lr == 0.f;
+          if (mr == TC_NONE) mr = none ? -INFINITY : 0.f;
+          if (whole) {
+            const int64_t head = (int64_t)u.b * a.W * a.Hq + sh.head[qb][r];
+            const float by = none ? 0.f : 1.f / lr;
+            uint2 y;
+            y.x = tc::pack2(__float2bfloat16_rn(o.x * by), __float2bfloat16_rn(o.y * by));
+            y.y = tc::pack2(__float2bfloat16_rn(o.z * by), __float2bfloat16_rn(o.w * by));
+            *reinterpret_cast<uint2*>(static_cast<bf16*>(a.out) + head * TC_D + 4 * lane) = y;
+            if (lane == 0 && a.lse) a.lse[head] = none ? -INFINITY : (mr + log2f(lr)) * PA_LN2;
+          } else {
+            *reinterpret_cast<float4*>(p.part_o + (part_at + r) * TC_D + 4 * lane) = o;
+            if (lane == 0) *reinterpret_cast<float2*>(p.part_ml + (part_at + r) * 2) = make_float2(mr, lr);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) tc::bar_arrive(&sh.q_free[qb]);  // the unit's row table has been read
+      if (whole) {
+        rows_done += nrows;
+      } else if (u.t0 == 0) {
+        // the unit goes on in the following shares: this one ends t1 tiles into it
+        const int cost = u.tiles + TC_UNIT_COST;
+        const int64_t unit_end = walk.end - (u.t1 + TC_UNIT_COST) + cost;
+        meta.unit = (u.b * Hkv + u.h) * p.blocks + u.rb;
+        int64_t e = (unit_end - 1) * workers / total;
+        while (e * total / workers > unit_end - 1) --e;
+        while ((e + 1) * total / workers <= unit_end - 1) ++e;
+        meta.end = (int)e;
+      }
+    }
+    if (bad && tk == 0) flag_status(a.status, KDA_DEV_TIMEOUT);
+    if (tid == TC_SOFT0) {
+      p.meta[me] = bad ? PaMeta{-1, 0} : meta;
+      add_work(a.status, rows_done);
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (warp == 1) tc::tmem_dealloc(tmem, C::TMEM_COLS);
+}
+
+int page_box(int page_size) {  // largest power of two that divides the page, at most a tile
+  const int b = page_size & -page_size;
+  return b < TC_TILE ? b : TC_TILE;
+}
+
+template <bool F8, int RB>
+cudaError_t tc_launch(const PagedAttnArgs& a, const PaPlan& p, int sms, cudaStream_t s) {
+  using C = TcCfg<F8, RB>;
+  auto kernel = paged_attention_tc_kernel<F8, RB>;
+  constexpr int bytes = 1024 + C::SLOTS * C::SLOT + C::SB * C::P_BYTES + 2 * C::Q_BYTES + C::JOIN +
+                        (int)sizeof(TcShared<F8, RB>);
+  static_assert(bytes <= 227 * 1024 && C::SLOTS >= 5, "shared memory of one SM");
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  const int box = page_box(a.c.page_size);
+  const long long rows = (long long)a.c.num_pages * a.c.Hkv * a.c.page_size;
+  TcMaps maps;
+  if (!encode_cache_map(&maps.k, a.c.k_pages, F8, rows, box) || !encode_cache_map(&maps.v, a.c.v_pages, F8, rows, box))
+    return cudaErrorInvalidValue;
+  int64_t ctas = sms < PA_SMS ? sms : PA_SMS;
+  const int64_t tiles = (int64_t)a.max_pages * a.c.page_size / TC_TILE + 2 + TC_UNIT_COST;
+  const int64_t units = (int64_t)a.B * a.c.Hkv * p.blocks;
+  if (tiles < ctas && units * tiles < ctas) ctas = units * tiles;
+  PaPlan plan = p;
+  plan.workers = (int)ctas;
+  e = launch_pdl(kernel, dim3((unsigned)ctas), dim3(C::NT), bytes, s, maps, a, plan, box);
+  if (e != cudaSuccess) return e;
+  return pa_join<TC_D, RB>(a, plan, s);
+}
+
+}  // namespace
+
+bool pa_tc_supported(const PagedAttnArgs& a) {
+  return a.c.d == TC_D && a.q_bf16 && a.out_bf16 && a.c.num_pages > 0 &&
+         (int64_t)a.c.num_pages * a.c.Hkv * a.c.page_size <= 0x7fffffff;
+}
+
+int pa_tc_row_block(int rows) { return rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
+
+cudaError_t pa_tc(const PagedAttnArgs& a, const PaPlan& p, int sms, cudaStream_t s) {
+  switch (pa_tc_row_block(p.rows)) {
+    case 4: return a.c.e4m3 ? tc_launch<true, 4>(a, p, sms, s) : tc_launch<false, 4>(a, p, sms, s);
+    case 8: return a.c.e4m3 ? tc_launch<true, 8>(a, p, sms, s) : tc_launch<false, 8>(a, p, sms, s);
+    case 16: return a.c.e4m3 ? tc_launch<true, 16>(a, p, sms, s) : tc_launch<false, 16>(a, p, sms, s);
+    default: return a.c.e4m3 ? tc_launch<true, 32>(a, p, sms, s) : tc_launch<false, 32>(a, p, sms, s);
+  }
+}
+
+}  // namespace kda
