@@ -4,8 +4,8 @@
 // cached rows never pass through registers.  One CTA per SM walks its share of the line in tiles of 128 tokens:
 //   warp 0   copies the tile's K and V from their pages into a ring of shared-memory slots (TMA, 128-byte swizzle, one box
 //            of consecutive page rows per copy), running ahead of the others by the depth of the ring;
-//   warp 1   issues S^T = K Q^T (128 tokens x the unit's query rows) and O^T += V^T P^T (128 channels x rows): K is the
-//            row operand as it lies, V the same read along its channels;
+//   warps 1 and 3   issue S^T = K Q^T (128 tokens x the unit's query rows) and O^T += V^T P^T (128 channels x rows): K
+//            is the row operand as it lies, V the same read along its channels;
 //   warp 2   puts the next unit's queries into operand order;
 //   warps 4-7 hold one token per thread: scores from tensor memory, their cap, mask and softmax, and the probabilities to
 //            shared memory as the second product's column operand.
@@ -65,9 +65,23 @@ struct TcCfg {
   static constexpr int SLOT = TC_TILE * TC_D * ES;        // bytes of a K or V tile
   static constexpr int Q_BYTES = N1 * TC_D * ES, P_BYTES = N2 * TC_TILE * ES;
   static constexpr int JOIN = TG > 1 ? 2 * TG * RB * TC_D * 4 : 0;  // the groups' accumulators, two units' worth
-  static constexpr int FIXED = 1024 + SB * P_BYTES + 2 * Q_BYTES + JOIN + 4096;
-  static constexpr int SLOTS_FIT = (227 * 1024 - FIXED) / (SLOT + (F8 ? 1024 : 0));
+  static constexpr int FIXED = 1024 + SB * P_BYTES + 2 * Q_BYTES + JOIN + 2560 + 8 * NT;
+  static constexpr int INFO = 8;  // tiles whose scales and boxes are kept: more than VS (see the copies)
+  static constexpr int SLOTS_FIT = (227 * 1024 - FIXED - (F8 ? INFO * 1024 : 0)) / SLOT;
   static constexpr int SLOTS = SLOTS_FIT > 10 ? 10 : SLOTS_FIT;
+  static constexpr int KS = SLOTS / 2, VS = SLOTS - KS;  // slots of the two rings
+};
+
+// A place in a ring of N with the parity of its current round.
+template <int N>
+struct TcRing {
+  int at = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ explicit TcRing(int first = 0) : at(first) {}
+  __device__ __forceinline__ void step(int by = 1) {
+    at += by;
+    if (at >= N) at -= N, parity ^= 1;
+  }
 };
 
 struct TcMaps {
@@ -77,10 +91,11 @@ struct TcMaps {
 template <bool F8, int RB>
 struct TcShared {
   using C = TcCfg<F8, RB>;
-  uint64_t full[C::SLOTS], empty[C::SLOTS];
-  uint64_t s_full[C::SB], s_free[C::SB], p_full[C::SB], p_free[C::SB], q_full[2], q_free[2], o_full[C::TG], drain;
-  alignas(16) float scales[F8 ? C::SLOTS : 1][2][TC_TILE];  // by V's slot: key and value scales of its tokens
-  int there[C::SLOTS];                                      // by V's slot: boxes copied
+  // Every barrier is waited on only by roles that see each of its rounds: a parity tells rounds apart no further.
+  uint64_t k_full[C::KS], k_empty[C::KS], v_full[C::VS], v_empty[C::VS];
+  uint64_t s_full[C::SB], s_free[C::SB], p_full[C::SB], p_free[C::SB], q_full[2], q_free[2], o_full[C::TG], drain[2];
+  alignas(16) float scales[F8 ? C::INFO : 1][2][TC_TILE];  // by tile: key and value scales of its tokens
+  int there[C::INFO];                                      // by tile: the boxes that were copied
   alignas(16) float factor[2][RB];  // per query row: score in powers of two per unit of the product
   int last[2][RB];                  // last seen position
   int head[2][RB];                  // place among the request's W x Hq output rows, -1 past the unit's rows
@@ -185,6 +200,7 @@ __device__ __forceinline__ void load_scores(uint32_t at, float (&x)[RG]) {
 
 // A bounded wait that also ends when another role has given up.
 __device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, int* dead) {
+  if (tc::bar_test(bar, parity)) return true;
   for (int i = 0; i < 1 << 12; ++i) {
     if (*reinterpret_cast<volatile int*>(dead)) return false;
     if (tc::bar_wait(bar, parity, 1u << 10)) return true;
@@ -245,12 +261,13 @@ __global__ void __launch_bounds__(TcCfg<F8, RB>::NT, 1)
     paged_attention_tc_kernel(const __grid_constant__ TcMaps maps, const PagedAttnArgs a, const PaPlan p, const int box) {
   using C = TcCfg<F8, RB>;
   using Sh = TcShared<F8, RB>;
-  constexpr int ES = C::ES, N1 = C::N1, N2 = C::N2, SLOT = C::SLOT, SLOTS = C::SLOTS, QP = C::QP, PP = C::PP;
+  constexpr int ES = C::ES, N1 = C::N1, N2 = C::N2, SLOT = C::SLOT, KS = C::KS, VS = C::VS, QP = C::QP, PP = C::PP;
   constexpr int TG = C::TG, RS = C::RS, RG = C::RG, SB = C::SB, TC_NT = C::NT;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   unsigned char* slots = base;
-  unsigned char* pbuf = slots + SLOTS * SLOT;
+  unsigned char* vslots = slots + KS * SLOT;
+  unsigned char* pbuf = vslots + VS * SLOT;
   unsigned char* qbuf = pbuf + SB * C::P_BYTES;
   float* join = reinterpret_cast<float*>(qbuf + 2 * C::Q_BYTES);  // [2][TG][RB][128]
   Sh& sh = *reinterpret_cast<Sh*>(qbuf + 2 * C::Q_BYTES + C::JOIN);
@@ -259,14 +276,15 @@ __global__ void __launch_bounds__(TcCfg<F8, RB>::NT, 1)
   const int Hkv = a.c.Hkv, per_b = Hkv * p.blocks;
 
   if (tid == 0) {
-    for (int i = 0; i < SLOTS; ++i) tc::bar_init(&sh.full[i], 1), tc::bar_init(&sh.empty[i], 1);
+    for (int i = 0; i < KS; ++i) tc::bar_init(&sh.k_full[i], 1), tc::bar_init(&sh.k_empty[i], 1);
+    for (int i = 0; i < VS; ++i) tc::bar_init(&sh.v_full[i], 1), tc::bar_init(&sh.v_empty[i], 1);
     for (int i = 0; i < SB; ++i) {
-      tc::bar_init(&sh.s_full[i], 1), tc::bar_init(&sh.s_free[i], 4 * RS);
+      tc::bar_init(&sh.s_full[i], 2), tc::bar_init(&sh.s_free[i], 4 * RS);
       tc::bar_init(&sh.p_full[i], 4 * RS), tc::bar_init(&sh.p_free[i], 1);
     }
     for (int i = 0; i < 2; ++i) tc::bar_init(&sh.q_full[i], 1), tc::bar_init(&sh.q_free[i], 1 + 4 * TG * RS);
     for (int i = 0; i < TG; ++i) tc::bar_init(&sh.o_full[i], 1);
-    tc::bar_init(&sh.drain, 1);
+    for (int i = 0; i < 2; ++i) tc::bar_init(&sh.drain[i], 1);
     tc::bar_fence_init();
     sh.dead = 0;
   }
@@ -317,125 +335,176 @@ __global__ void __launch_bounds__(TcCfg<F8, RB>::NT, 1)
     TcTiles it(walk);
     const int boxes = TC_TILE / box;
     bool ok = true;
-    unsigned half = 0;  // K tiles are the even ones, V tiles the odd
-    while (ok && it.next(a, p, box)) {
+    TcRing<KS> kr;
+    TcRing<VS> vr;
+    TcRing<C::INFO> info;
+    // this lane's box of the next tile: its page's id is asked for a tile ahead (waiting for it tile by tile took longer
+    // than an 8-bit tile's copy)
+    bool more = it.next(a, p, box), next_there = false;
+    int next_page = 0, next_off = 0, next_h = 0;
+    auto look_up = [&]() {
       const int64_t tok = (int64_t)it.u.start + (int64_t)it.tile * TC_TILE + lane * box;
-      bool there = lane < boxes && tok < it.u.len;
+      next_there = lane < boxes && tok < it.u.len;
+      if (next_there) {
+        const int pg = (int)tok / a.c.page_size;
+        next_off = (int)tok - pg * a.c.page_size;
+        next_h = it.u.h;
+        next_page = __ldg(a.block_table + (int64_t)it.u.b * a.max_pages + pg);
+      }
+    };
+    if (more) look_up();
+    while (more) {
+      bool there = next_there;
+      const int page = next_page, off = next_off, h = next_h;
+      more = it.next(a, p, box);
+      if (more) look_up();
       int row = 0;
       if (there) {
-        const int pg = (int)tok / a.c.page_size, page = __ldg(a.block_table + (int64_t)it.u.b * a.max_pages + pg);
         there = (unsigned)page < (unsigned)a.c.num_pages;
-        if (there) row = (page * Hkv + it.u.h) * a.c.page_size + ((int)tok - pg * a.c.page_size);
+        if (there) row = (page * Hkv + h) * a.c.page_size + off;
         else flag_status(a.status, KDA_DEV_PAGE_OOB);
       }
       const unsigned mask = __ballot_sync(0xffffffffu, there);
-      const uint32_t bytes = __popc(mask) * box * TC_D * ES;
-#pragma unroll
-      for (int kv = 0; kv < 2; ++kv, ++half) {
-        const unsigned slot = half % SLOTS;
-        if (half >= (unsigned)SLOTS) ok = tc_wait(&sh.empty[slot], (half / SLOTS - 1) & 1, &sh.dead);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        if (lane == 0) {
-          if (kv) sh.there[slot] = (int)mask;
-          tc::bar_arrive_expect_tx(&sh.full[slot], bytes + (F8 && kv ? __popc(mask) * box * 8 : 0));
-        }
-        __syncwarp();
-        if (there) {
-          unsigned char* dst = slots + slot * SLOT + lane * box * 128;
-          const CUtensorMap* map = kv ? &maps.v : &maps.k;
-          tc::tma_load_2d(dst, map, 0, row, &sh.full[slot]);
-          if constexpr (!F8) tc::tma_load_2d(dst + TC_TILE * 128, map, 64, row, &sh.full[slot]);
-          if constexpr (F8) {
-            if (kv) {
-              tc::bulk_g2s(&sh.scales[slot][0][lane * box], a.c.k_scales + row, box * 4, &sh.full[slot]);
-              tc::bulk_g2s(&sh.scales[slot][1][lane * box], a.c.v_scales + row, box * 4, &sh.full[slot]);
-            }
-          }
-        }
-        __syncwarp();
-      }
-    }
-    if (!ok) {  // let what is on its way arrive before the CTA ends
-      if (lane == 0) {
-        flag_status(a.status, KDA_DEV_TIMEOUT);
-        for (unsigned i = half > (unsigned)SLOTS ? half - SLOTS : 0; i < half; ++i)
-          tc::bar_wait(&sh.full[i % SLOTS], (i / SLOTS) & 1, 1u << 16);
+      const int count = __popc(mask);
+      const uint32_t bytes = count * box * TC_D * ES;
+      // A slot's n-th use waits for the release of the one before (the first finds the round before the first over).
+      // The tile's scales and list of boxes go by its number: they have been read when its V is released, which the
+      // copies of VS tiles later wait for.
+      ok = ok && tc_wait(&sh.k_empty[kr.at], kr.parity ^ 1, &sh.dead);
+      if (lane == 0 && ok) {
+        sh.there[info.at] = (int)mask;
+        tc::bar_arrive_expect_tx(&sh.k_full[kr.at], bytes + (F8 ? count * box * 8 : 0));
       }
       __syncwarp();
+      if (there && ok) {
+        unsigned char* dst = slots + kr.at * SLOT + lane * box * 128;
+        tc::tma_load_2d(dst, &maps.k, 0, row, &sh.k_full[kr.at]);
+        if constexpr (F8) {
+          tc::bulk_g2s(&sh.scales[info.at][0][lane * box], a.c.k_scales + row, box * 4, &sh.k_full[kr.at]);
+          tc::bulk_g2s(&sh.scales[info.at][1][lane * box], a.c.v_scales + row, box * 4, &sh.k_full[kr.at]);
+        } else {
+          tc::tma_load_2d(dst + TC_TILE * 128, &maps.k, 64, row, &sh.k_full[kr.at]);
+        }
+      }
+      const bool k_sent = ok;
+      ok = ok && tc_wait(&sh.v_empty[vr.at], vr.parity ^ 1, &sh.dead);
+      if (lane == 0 && ok) tc::bar_arrive_expect_tx(&sh.v_full[vr.at], bytes);
+      __syncwarp();
+      if (there && ok) {
+        unsigned char* dst = vslots + vr.at * SLOT + lane * box * 128;
+        tc::tma_load_2d(dst, &maps.v, 0, row, &sh.v_full[vr.at]);
+        if constexpr (!F8) tc::tma_load_2d(dst + TC_TILE * 128, &maps.v, 64, row, &sh.v_full[vr.at]);
+      }
+      if (!__all_sync(0xffffffffu, ok)) {
+        // let what is on its way arrive before the CTA ends: this round's copies and those of the rounds just before
+        if (lane == 0) {
+          flag_status(a.status, KDA_DEV_TIMEOUT);
+          for (int i = 0; i < KS; ++i) {
+            const bool this_round = i < kr.at || (i == kr.at && k_sent);
+            tc::bar_wait(&sh.k_full[i], this_round ? kr.parity : kr.parity ^ 1, 1u << 16);
+          }
+          for (int i = 0; i < VS; ++i)
+            tc::bar_wait(&sh.v_full[i], i < vr.at || (i == vr.at && ok) ? vr.parity : vr.parity ^ 1, 1u << 16);
+        }
+        __syncwarp();
+        break;
+      }
+      kr.step();
+      vr.step();
+      info.step();
     }
-  } else if (warp == 1) {
-    // ---- products, one thread
-    if (lane == 0) {
-      constexpr uint32_t id1 = F8 ? tc::idesc_e4m3(128, N1) : tc::idesc_bf16(128, N1);
-      constexpr uint32_t id2 = (F8 ? tc::idesc_e4m3(128, N2) : tc::idesc_bf16(128, N2)) | tc::IDESC_A_MN;
-      // Two places on the line of tiles: the next first product, up to AHEAD tiles before the next second one (so that
-      // every group has scores to work on; the ring has room for that).  Whichever has its operands is issued.
-      constexpr unsigned AHEAD = SB < SLOTS / 2 ? SB : SLOTS / 2;
-      TcTiles ahead(walk), now(walk);
-      unsigned ga = 0, gn = 0;  // tiles numbered over the CTA's whole share; tile g has buffers g % SB, group g % TG
-      bool has_a = ahead.next(a, p, box), has_n = now.next(a, p, box), ok = true;
-      unsigned idle = 0;
-      while (has_n) {
-        bool done = false;
-        if (has_a && ga < gn + AHEAD) {
-          const unsigned slot = 2 * ga % SLOTS, buf = ga % SB;
-          if (tc::bar_test(&sh.full[slot], (2 * ga / SLOTS) & 1) &&
-              (!ahead.first() || tc::bar_test(&sh.q_full[ahead.unit_no & 1], (ahead.unit_no >> 1) & 1)) &&
-              (ga < SB || tc::bar_test(&sh.s_free[buf], (ga / SB - 1) & 1))) {
-            tc::fence_after_sync();
-            const uint32_t kb = tc::smem_u32(slots + slot * SLOT);
-            const uint32_t qb = tc::smem_u32(qbuf + (ahead.unit_no & 1) * C::Q_BYTES);
-#pragma unroll
-            for (int kk = 0; kk < 4 * ES; ++kk) {  // 32 bytes of each row per step
-              const uint32_t blk = kk / 4, in = (kk % 4) * 32;
-              const uint64_t da = tc::sdesc(kb + blk * (TC_TILE * 128) + in), db = tc::sdesc(qb + blk * (N1 * 128) + in);
-              if constexpr (F8) tc::mma_ss_f8(tmem + buf * C::S_COLS, da, db, id1, kk > 0);
-              else tc::mma_ss(tmem + buf * C::S_COLS, da, db, id1, kk > 0);
-            }
-            tc::commit(&sh.empty[slot]);
-            tc::commit(&sh.s_full[buf]);
-            if (ahead.last()) tc::commit(&sh.q_free[ahead.unit_no & 1]);
-            ++ga;
-            has_a = ahead.next(a, p, box);
-            done = true;
-          }
-        }
-        const unsigned slot = (2 * gn + 1) % SLOTS, buf = gn % SB, grp = gn % TG;
-        if (gn < ga && tc::bar_test(&sh.p_full[buf], (gn / SB) & 1) &&
-            tc::bar_test(&sh.full[slot], ((2 * gn + 1) / SLOTS) & 1)) {
+  } else if (warp == 1 || warp == 3) {
+    // ---- products, one thread each: tiles numbered over the CTA's whole share, tile g has buffers g % SB and group
+    // g % TG.  (One thread for both took 1700 cycles a tile, most of it its own instructions' latency.)
+    bool ok = true;
+    TcTiles it(walk);
+    TcRing<SB> buf;
+    if (warp == 1) {
+      if (lane == 0) {
+        constexpr uint32_t id = F8 ? tc::idesc_e4m3(128, N1) : tc::idesc_bf16(128, N1);
+        const uint64_t k0 = tc::sdesc(tc::smem_u32(slots)), q0 = tc::sdesc(tc::smem_u32(qbuf));
+        TcRing<KS> ring;
+        while (it.next(a, p, box)) {
+          if (it.first()) ok = ok && tc_wait(&sh.q_full[it.unit_no & 1], (it.unit_no >> 1) & 1, &sh.dead);
+          ok = ok && tc_wait(&sh.s_free[buf.at], buf.parity ^ 1, &sh.dead);
+          ok = ok && tc_wait(&sh.k_full[ring.at], ring.parity, &sh.dead);
+          if (!ok) break;
+          tc::bar_arrive(&sh.s_full[buf.at]);  // hands on what came with K: the scales and the list of boxes
           tc::fence_after_sync();
-          const uint32_t vb = tc::smem_u32(slots + slot * SLOT), pb = tc::smem_u32(pbuf + buf * C::P_BYTES);
-          const bool begins = now.tile - TG < now.u.t0;  // the group's first tile of the unit
+          const uint64_t kd = k0 + ring.at * (SLOT / 16), qd = q0 + (it.unit_no & 1) * (C::Q_BYTES / 16);
+          const uint32_t d = tmem + buf.at * C::S_COLS;
 #pragma unroll
-          for (int kk = 0; kk < 4 * ES; ++kk) {  // 32 (e4m3) or 16 tokens per step
-            const uint32_t blk = kk / 4, in = (kk % 4) * 32;
-            const uint64_t da = tc::sdesc_mn(vb + kk * (F8 ? 4096 : 2048), TC_TILE * 128);
-            const uint64_t db = tc::sdesc(pb + blk * (N2 * 128) + in);
-            const uint32_t add = !(begins && kk == 0);
-            if constexpr (F8) tc::mma_ss_f8(tmem_o + grp * N2, da, db, id2, add);
-            else tc::mma_ss(tmem_o + grp * N2, da, db, id2, add);
+          for (int kk = 0; kk < 4 * ES; ++kk) {  // 32 bytes of each row per step
+            const uint64_t da = kd + (kk / 4 * (TC_TILE * 128) + kk % 4 * 32) / 16;
+            const uint64_t db = qd + (kk / 4 * (N1 * 128) + kk % 4 * 32) / 16;
+            if constexpr (F8) tc::mma_ss_f8(d, da, db, id, kk > 0);
+            else tc::mma_ss(d, da, db, id, kk > 0);
           }
-          tc::commit(&sh.empty[slot]);
-          tc::commit(&sh.p_free[buf]);
-          if (now.tile + TG >= now.u.t1) tc::commit(&sh.o_full[grp]);  // the group's last tile of the unit
-          ++gn;
-          has_n = now.next(a, p, box);
-          done = true;
-        }
-        if (done) {
-          idle = 0;
-        } else if (++idle > 1u << 24 || *reinterpret_cast<volatile int*>(&sh.dead)) {
-          *reinterpret_cast<volatile int*>(&sh.dead) = 1;
-          ok = false;
-          break;
+          tc::commit(&sh.s_full[buf.at]);
+          tc::commit(&sh.k_empty[ring.at]);
+          if (it.last()) tc::commit(&sh.q_free[it.unit_no & 1]);
+          ring.step();
+          buf.step();
         }
       }
-      if (!ok) {
-        flag_status(a.status, KDA_DEV_TIMEOUT);
-        tc::commit(&sh.drain);
-        tc::bar_wait(&sh.drain, 0, 1u << 16);
+    } else {
+      constexpr uint32_t id = (F8 ? tc::idesc_e4m3(128, N2) : tc::idesc_bf16(128, N2)) | tc::IDESC_A_MN;
+      const uint64_t v0 = tc::sdesc_mn(tc::smem_u32(vslots), TC_TILE * 128), p0 = tc::sdesc(tc::smem_u32(pbuf));
+      TcRing<VS> ring;
+      TcRing<TG> grp;
+      TcRing<C::INFO> info;
+      const int all_boxes = (int)((1u << (TC_TILE / box)) - 1);
+      while (it.next(a, p, box)) {
+        ok = ok && tc_wait(&sh.v_full[ring.at], ring.parity, &sh.dead);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const int64_t left = (int64_t)it.u.len - it.u.start - (int64_t)it.tile * TC_TILE;  // tokens from the tile's first on
+        const int mask = sh.there[info.at];
+        if (left < TC_TILE || mask != all_boxes) {
+          // what lies in the slot for tokens that are not there must not be a NaN
+          for (int t = lane; t < TC_TILE; t += 32)
+            if (t >= left || !(mask >> (t / box) & 1)) {
+              unsigned char* vrow = vslots + ring.at * SLOT + t * 128;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                reinterpret_cast<uint4*>(vrow)[i] = make_uint4(0, 0, 0, 0);
+                if constexpr (!F8) reinterpret_cast<uint4*>(vrow + TC_TILE * 128)[i] = make_uint4(0, 0, 0, 0);
+              }
+            }
+          tc::fence_proxy_async();
+          __syncwarp();
+        }
+        if (lane == 0) {
+          ok = tc_wait(&sh.p_full[buf.at], buf.parity, &sh.dead);
+          if (ok) {
+            tc::fence_after_sync();
+            const uint64_t vd = v0 + ring.at * (SLOT / 16), pd = p0 + buf.at * (C::P_BYTES / 16);
+            const uint32_t d = tmem_o + grp.at * N2;
+            const bool begins = it.tile - TG < it.u.t0;  // the group's first tile of the unit
+#pragma unroll
+            for (int kk = 0; kk < 4 * ES; ++kk) {  // 32 (e4m3) or 16 tokens per step
+              const uint64_t da = vd + kk * (F8 ? 4096 : 2048) / 16;
+              const uint64_t db = pd + (kk / 4 * (N2 * 128) + kk % 4 * 32) / 16;
+              const uint32_t add = !(begins && kk == 0);
+              if constexpr (F8) tc::mma_ss_f8(d, da, db, id, add);
+              else tc::mma_ss(d, da, db, id, add);
+            }
+            tc::commit(&sh.p_free[buf.at]);
+            tc::commit(&sh.v_empty[ring.at]);
+            if (it.tile + TG >= it.u.t1) tc::commit(&sh.o_full[grp.at]);  // the group's last tile of the unit
+          }
+        }
+        ring.step();
+        buf.step();
+        grp.step();
+        info.step();
       }
+    }
+    if (lane == 0) {  // nothing of this thread's is on its way when the CTA ends
+      if (!ok) flag_status(a.status, KDA_DEV_TIMEOUT);
+      uint64_t* drain = &sh.drain[warp >> 1];
+      tc::commit(drain);
+      tc::bar_wait(drain, 0);
     }
     __syncwarp();
   } else if (warp == 2) {
@@ -512,50 +581,55 @@ __global__ void __launch_bounds__(TcCfg<F8, RB>::NT, 1)
     const int bar_id = 1 + sg, rfirst = rs * RG;  // this group's rows of the unit
     float m[RG], l[RG];
     TcTiles it(walk);
-    unsigned g = 0;
-    int units = -1;
+    TcRing<SB> buf, before(SB - TG);  // this tile's buffers, and those of the group's tile before
+    before.parity = 1;
+    TcRing<C::INFO> info;
+    TcRing<TG> turn;
+    int units = -1, row0 = 0, nrows = 0, all_to = 0;
+    int64_t all_from = 0;
     unsigned o_uses = 0;  // of this group's accumulators
     bool bad = false, mine_any = false;
+    const int box_bit = tk / box;
     PaMeta meta{-1, 0};
     int rows_done = 0;
     // where this thread's element of an operand row lies in a probability buffer: (place ^ (row % 8) * 16) + row * 128
     const uint32_t place = F8 ? ((uint32_t)(tk >> 4) << 4) + (tk & 15)
                               : (uint32_t)(tk >> 6) * (N2 * 128) + ((uint32_t)((tk & 63) >> 3) << 4) + (tk & 7) * 2;
-    for (; it.next(a, p, box); ++g) {
+    for (; it.next(a, p, box); buf.step(), before.step(), info.step(), turn.step()) {
       const TcUnit& u = it.u;
-      const int qb = it.unit_no & 1, row0 = u.rb * RB, nrows = min(RB, p.rows - row0);
+      const int qb = it.unit_no & 1;
       if (it.unit_no != units) {
         units = it.unit_no;
         mine_any = false;
+        row0 = u.rb * RB;
+        nrows = min(RB, p.rows - row0);
+        // tokens that every row of the unit sees
+        all_to = u.len - a.W + row0 / p.G;
+        all_from = (int64_t)u.len - a.W + (row0 + nrows - 1) / p.G - window + 1;
         bad |= !tc_wait(&sh.q_full[qb], (it.unit_no >> 1) & 1, &sh.dead);
 #pragma unroll
         for (int r = 0; r < RG; ++r) m[r] = TC_NONE, l[r] = 0.f;
       }
-      if (TG == 1 || (int)(g % TG) == tg) {
+      if (TG == 1 || turn.at == tg) {
         const bool begins = !mine_any;
         mine_any = true;
-        const unsigned vslot = (2 * g + 1) % SLOTS, buf = g % SB;
-        bad |= !tc_wait(&sh.full[vslot], ((2 * g + 1) / SLOTS) & 1, &sh.dead);
+        bad |= !tc_wait(&sh.s_full[buf.at], buf.parity, &sh.dead);
+        tc::fence_after_sync();
         const int64_t tok0 = (int64_t)u.start + (int64_t)it.tile * TC_TILE;
         const int tok = (int)tok0 + tk;
-        const bool there = tok < u.len && (sh.there[vslot] >> (tk / box) & 1);
+        const bool there = tok < u.len && (sh.there[info.at] >> box_bit & 1);
         float ks = 1.f, vs = 1.f, lift = 0.f;
         if constexpr (F8) {
-          ks = there ? sh.scales[vslot][0][tk] : 0.f;
-          vs = there ? sh.scales[vslot][1][tk] : 0.f;
+          ks = there ? sh.scales[info.at][0][tk] : 0.f;
+          vs = there ? sh.scales[info.at][1][tk] : 0.f;
           lift = (float)((int)(__float_as_uint(vs) >> 23) - 126);  // just above log2 of the value scale
         }
-        const int all_to = u.len - a.W + row0 / p.G;
-        const int64_t all_from = (int64_t)u.len - a.W + (row0 + nrows - 1) / p.G - window + 1;
         const bool masked = !there || tok0 + TC_TILE - 1 > all_to || tok0 < all_from;
-
-        bad |= !tc_wait(&sh.s_full[buf], (g / SB) & 1, &sh.dead);
-        tc::fence_after_sync();
         float x[RG];
-        load_scores<F8, RB, RG>(tmem + buf * C::S_COLS + lanes + rfirst, x);
+        load_scores<F8, RB, RG>(tmem + buf.at * C::S_COLS + lanes + rfirst, x);
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) tc::bar_arrive(&sh.s_free[buf]);
+        if (lane == 0) tc::bar_arrive(&sh.s_free[buf.at]);
 #pragma unroll
         for (int r = 0; r < RG; r += 4) {
           const float4 f = *reinterpret_cast<const float4*>(&sh.factor[qb][rfirst + r]);
@@ -591,7 +665,7 @@ __global__ void __launch_bounds__(TcCfg<F8, RB>::NT, 1)
             if (lane == 0) sh.red[tg][quarter][rfirst + r] = t;
           }
           // the group's last product into its accumulators is through
-          if (!begins) bad |= !tc_wait(&sh.p_free[(g - TG) % SB], ((g - TG) / SB) & 1, &sh.dead);
+          if (!begins) bad |= !tc_wait(&sh.p_free[before.at], before.parity, &sh.dead);
           tc::fence_after_sync();
           tc::named_bar(bar_id, 128);
           float by[RG];
@@ -633,8 +707,8 @@ __global__ void __launch_bounds__(TcCfg<F8, RB>::NT, 1)
         }
 
         // ---- probabilities and their parts
-        if (g >= SB) bad |= !tc_wait(&sh.p_free[buf], (g / SB - 1) & 1, &sh.dead);
-        const uint32_t pb = tc::smem_u32(pbuf + buf * C::P_BYTES) + place;
+        bad |= !tc_wait(&sh.p_free[buf.at], buf.parity ^ 1, &sh.dead);
+        const uint32_t pb = tc::smem_u32(pbuf + buf.at * C::P_BYTES) + place;
         const float pv = F8 ? vs * TC_P_UNIT : 1.f;
 #pragma unroll
         for (int r = 0; r < RG; r += 2) {
@@ -666,18 +740,10 @@ __global__ void __launch_bounds__(TcCfg<F8, RB>::NT, 1)
             }
           }
         }
-        if (!there && rs == 0) {  // what lies in the slot for a token that is not there must not be a NaN
-          unsigned char* vrow = slots + vslot * SLOT + tk * 128;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            reinterpret_cast<uint4*>(vrow)[i] = make_uint4(0, 0, 0, 0);
-            if constexpr (!F8) reinterpret_cast<uint4*>(vrow + TC_TILE * 128)[i] = make_uint4(0, 0, 0, 0);
-          }
-        }
         tc::fence_proxy_async();
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) tc::bar_arrive(&sh.p_full[buf]);
+        if (lane == 0) tc::bar_arrive(&sh.p_full[buf.at]);
       }
       if (!it.last()) continue;
 
@@ -828,9 +894,10 @@ template <bool F8, int RB>
 cudaError_t tc_launch(const PagedAttnArgs& a, const PaPlan& p, int sms, cudaStream_t s) {
   using C = TcCfg<F8, RB>;
   auto kernel = paged_attention_tc_kernel<F8, RB>;
+  static_assert(C::INFO > C::VS, "scales kept until they are read");
   constexpr int bytes = 1024 + C::SLOTS * C::SLOT + C::SB * C::P_BYTES + 2 * C::Q_BYTES + C::JOIN +
                         (int)sizeof(TcShared<F8, RB>);
-  static_assert(bytes <= 227 * 1024 && C::SLOTS >= 5, "shared memory of one SM");
+  static_assert(bytes <= 227 * 1024 && C::KS >= 2, "shared memory of one SM");
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
   const int box = page_box(a.c.page_size);
