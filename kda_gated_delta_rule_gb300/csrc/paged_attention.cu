@@ -2,10 +2,6 @@
 #include "device.h"
 #include "paged_attention.cuh"
 
-#ifndef PA_TC_RULE
-#define PA_TC_RULE
-#endif
-
 namespace kda {
 
 namespace {
@@ -47,9 +43,14 @@ cudaError_t launch_paged_attention(const PagedAttnArgs& a, cudaStream_t s) {
   PaPlan p;
   p.G = a.Hq / a.c.Hkv;
   p.rows = a.W * p.G;
-  if (pa_tc_supported(a) PA_TC_RULE) {
-    const int rb = pa_tc_row_block(p.rows);
-    p.blocks = (p.rows + rb - 1) / rb;
+  const int tc_rb = pa_tc_row_block(p.rows), tc_blocks = (p.rows + tc_rb - 1) / tc_rb;
+  // The tensor-memory form is ahead with many query rows per cached row (96 rows: 88 against 119 us; 24: 43 against 57), and
+  // with fewer units than CTAs, where its larger and so fewer parts join faster (one request of 4096 tokens and 8 heads: 15
+  // against 26 us, of 262144: 167 against 175); with many units of few rows their starts and ends cost it more (16 requests
+  // of 4096 tokens, 128 units: 64 against 56 us).
+  if (pa_tc_supported(a) && (p.rows > 16 || (int64_t)a.B * a.c.Hkv * tc_blocks <= 64)) {
+    const int rb = tc_rb;
+    p.blocks = tc_blocks;
     lay_out(p, reinterpret_cast<char*>(a.ws), PA_SMS, rb, a.c.d);
     return pa_tc(a, p, sms, s);
   }

@@ -40,6 +40,7 @@ namespace kda {
 
 constexpr int PA_NT = 128, PA_WARPS = 4;
 constexpr int PA_UNIT_COST = 2;
+constexpr int PA_SHARE = 2;  // positions on the line that a warp takes at least
 constexpr int PA_MAX_LEN = 0x7fffff00;  // token positions and the next tile's stay within 32 bits
 constexpr float PA_LOG2E = 1.4426950408889634f, PA_LN2 = 0.6931471805599453f;
 // how far (in powers of two) scores may run above the softmax reference before it is moved
@@ -231,7 +232,8 @@ __global__ void __launch_bounds__(PA_NT, pa_resident(NT)) paged_attention_kernel
     __syncthreads();
   }
   const int64_t total = scan[PA_NT - 1] * per_b;
-  const int64_t all = (int64_t)gridDim.x * PA_WARPS, workers = total < all ? total : all;
+  const int64_t all = (int64_t)gridDim.x * PA_WARPS, few = (total + PA_SHARE - 1) / PA_SHARE;
+  const int64_t workers = few < all ? few : all;
   // the request in which each of this CTA's shares begins, and that request's first position
   const int64_t before = scan[tid] - mine;
   for (int w = 0; w < PA_WARPS; ++w) {

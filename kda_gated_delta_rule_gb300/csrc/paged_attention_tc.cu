@@ -1,20 +1,20 @@
-// Attention over the paged cache on the 5th-generation tensor cores: d = 128, bf16 queries and outputs.
+// Attention over a bf16 paged cache on the 5th-generation tensor cores: d = 128, bf16 queries and outputs.
 //
 // The mathematics, the line of tiles, the parts and their join are those of paged_attention.cuh; what differs is that
 // cached rows never pass through registers.  One CTA per SM walks its share of the line in tiles of 128 tokens:
-//   warp 0   copies the tile's K and V from their pages into a ring of shared-memory slots (TMA, 128-byte swizzle, one box
-//            of consecutive page rows per copy), running ahead of the others by the depth of the ring;
+//   warp 0   copies the tile's K and V from their pages into rings of shared-memory slots (TMA, 128-byte swizzle, one box
+//            of consecutive page rows per copy), running ahead of the others by the depth of the rings;
 //   warps 1 and 3   issue S^T = K Q^T (128 tokens x the unit's query rows) and O^T += V^T P^T (128 channels x rows): K
 //            is the row operand as it lies, V the same read along its channels;
 //   warp 2   puts the next unit's queries into operand order;
-//   warps 4-7 hold one token per thread: scores from tensor memory, their cap, mask and softmax, and the probabilities to
-//            shared memory as the second product's column operand.
-// An 8-bit cache is multiplied as e4m3: no conversion touches K or V.  The 16-bit side is split into e4m3 parts that
-// take columns of their own: q into 2 (exact for bf16 within 2^-14 of the row's maximum, 2^-22 of it below), p into 3
-// (12 bits, 2^-20 of the reference below).  With a bf16 cache q is one part and p the sum of two (16 bits).
+//   warps 4 on   hold one token per thread: scores from tensor memory, their cap, mask and softmax, and the probabilities,
+//            each as the sum of two bf16, to shared memory as the second product's column operand.
 //
-// Bound by HBM: a tile's copies (32 or 64 KB) take 1400 or 2800 cycles of the SM's share of it, its two products at 16 to
-// 96 columns a few hundred, and its softmax about 13 instructions per score and thread (25 with e4m3 parts).
+// Bound by HBM for few query rows: a tile's copies (64 KB) take 2800 cycles of the SM's share of it.  Every role is one
+// warp or four, each passing through its code once per tile, so a role's time per tile is its instructions' latency (5
+// to 10 cycles each): that is what was shortened (look-ups without divisions, roles on warps of their own).  With an 8-bit
+// cache (1400 cycles a tile) the same roles were slower than the register form of paged_attention.cuh, multiplied as
+// e4m3 with the 16-bit side in parts (125 against 119 us at 262144 tokens): that cache keeps the register form.
 //
 // Waits are bounded: one that gives up sets KDA_DEV_TIMEOUT and a flag on which every role leaves.
 #include <stddef.h>
@@ -30,44 +30,26 @@ namespace {
 
 constexpr int TC_TILE = 128, TC_D = 128;
 constexpr int TC_SOFT0 = 128;          // first thread of the softmax warps
-#ifndef TCU_
-#define TCU_ 2
-#endif
-constexpr int TC_UNIT_COST = TCU_;     // tiles a unit counts beyond its own
+constexpr int TC_UNIT_COST = 4;        // tiles a unit counts beyond its own
 constexpr float TC_NONE = -1e30f;      // a softmax reference that has seen nothing (finite: no -inf - -inf)
 constexpr float TC_SLACK = 6.f;        // powers of two a score may run above its reference
-constexpr float TC_P_UNIT = 4.f;       // e4m3: probability parts are of p * 4 < 256
 
-#ifndef TC4_
-#define TC4_ 4
-#endif
-#ifndef TC8_
-#define TC8_ 2
-#endif
-#ifndef TC16_
-#define TC16_ 1
-#endif
-template <bool F8, int RB>
+template <int RB>
 struct TcCfg {
-  static constexpr int ES = F8 ? 1 : 2;
-  static constexpr int QP = F8 ? 2 : 1, PP = F8 ? 3 : 2;  // parts of a query, of a probability
-  static constexpr int N1 = QP * RB < 16 ? 16 : QP * RB;  // columns of the products (multiples of 16)
+  static constexpr int PP = 2;                            // parts of a probability
+  static constexpr int N1 = RB < 16 ? 16 : RB;            // columns of the products (multiples of 16)
   static constexpr int N2 = (PP * RB + 15) / 16 * 16;
-  // softmax groups of four warps: TG of them take tiles in turn (each with accumulators of its own, joined at the end of
-  // the unit), so that one's latencies are covered by the others'; RS of them share a tile's rows
-  static constexpr int TG = RB == 4 ? TC4_ : RB == 8 ? TC8_ : RB == 16 ? TC16_ : 1, RS = RB >= 16 ? 2 : 1;
-  static constexpr int RG = RB / RS;                      // rows of a group
-  static constexpr int NT = TC_SOFT0 + TG * RS * 128;
+  // softmax groups of four warps, each with RG of a tile's rows: several cover one another's latencies
+  static constexpr int RG = RB < 8 ? RB : 8, RS = RB / RG;
+  static constexpr int NT = TC_SOFT0 + RS * 128;
   static constexpr int S_COLS = (N1 + 31) / 32 * 32;      // tensor-memory columns of a score buffer
-  static constexpr int SB = TG < 2 ? 2 : TG;              // score and probability buffers
-  static constexpr int O_COL = SB * S_COLS, COLS = O_COL + TG * N2;
-  static constexpr int TMEM_COLS = COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
-  static constexpr int SLOT = TC_TILE * TC_D * ES;        // bytes of a K or V tile
-  static constexpr int Q_BYTES = N1 * TC_D * ES, P_BYTES = N2 * TC_TILE * ES;
-  static constexpr int JOIN = TG > 1 ? 2 * TG * RB * TC_D * 4 : 0;  // the groups' accumulators, two units' worth
-  static constexpr int FIXED = 1024 + SB * P_BYTES + 2 * Q_BYTES + JOIN + 2560 + 8 * NT;
-  static constexpr int INFO = 8;  // tiles whose scales and boxes are kept: more than VS (see the copies)
-  static constexpr int SLOTS_FIT = (227 * 1024 - FIXED - (F8 ? INFO * 1024 : 0)) / SLOT;
+  static constexpr int SB = 2;                            // score and probability buffers
+  static constexpr int O_COL = SB * S_COLS, TMEM_COLS = 128;
+  static constexpr int SLOT = TC_TILE * TC_D * 2;        // bytes of a K or V tile
+  static constexpr int Q_BYTES = N1 * TC_D * 2, P_BYTES = N2 * TC_TILE * 2;
+  static constexpr int FIXED = 1024 + SB * P_BYTES + 2 * Q_BYTES + 2560 + 8 * NT;
+  static constexpr int INFO = 8;  // tiles whose lists of boxes are kept: more than VS (see the copies)
+  static constexpr int SLOTS_FIT = (227 * 1024 - FIXED) / SLOT;
   static constexpr int SLOTS = SLOTS_FIT > 10 ? 10 : SLOTS_FIT;
   static constexpr int KS = SLOTS / 2, VS = SLOTS - KS;  // slots of the two rings
 };
@@ -88,19 +70,17 @@ struct TcMaps {
   CUtensorMap k, v;
 };
 
-template <bool F8, int RB>
+template <int RB>
 struct TcShared {
-  using C = TcCfg<F8, RB>;
+  using C = TcCfg<RB>;
   // Every barrier is waited on only by roles that see each of its rounds: a parity tells rounds apart no further.
   uint64_t k_full[C::KS], k_empty[C::KS], v_full[C::VS], v_empty[C::VS];
-  uint64_t s_full[C::SB], s_free[C::SB], p_full[C::SB], p_free[C::SB], q_full[2], q_free[2], o_full[C::TG], drain[2];
-  alignas(16) float scales[F8 ? C::INFO : 1][2][TC_TILE];  // by tile: key and value scales of its tokens
+  uint64_t s_full[C::SB], s_free[C::SB], p_full[C::SB], p_free[C::SB], q_full[2], q_free[2], o_full, drain[2];
   int there[C::INFO];                                      // by tile: the boxes that were copied
   alignas(16) float factor[2][RB];  // per query row: score in powers of two per unit of the product
   int last[2][RB];                  // last seen position
   int head[2][RB];                  // place among the request's W x Hq output rows, -1 past the unit's rows
-  float red[C::TG][4][RB];
-  float jm[2][C::TG][RB], jl[2][C::TG][RB];  // the groups' references and sums
+  float red[4][RB];
   int64_t scan[C::NT];
   int64_t where[2];
   uint32_t tmem;
@@ -154,48 +134,18 @@ struct TcTiles {
   __device__ __forceinline__ bool last() const { return tile + 1 == u.t1; }
 };
 
-__device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ float2 of_e4m3_pair(uint32_t two) {
-  const uint32_t h = half2_of_codes(two);
-  return __half22float2(*reinterpret_cast<const __half2*>(&h));
-}
-__device__ __forceinline__ void st_shared_u8(uint32_t at, uint32_t v) {
-  asm volatile("st.shared.u8 [%0], %1;" ::"r"(at), "r"(v) : "memory");
-}
 __device__ __forceinline__ void st_shared_u16(uint32_t at, uint32_t v) {
   asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"((uint16_t)v) : "memory");
 }
 
-// A thread's raw scores of a group's RG rows, parts put together; `at`: the first part's first column.
-template <bool F8, int RB, int RG>
+// A thread's raw scores of a group's RG rows; `at`: their first column.
+template <int RG>
 __device__ __forceinline__ void load_scores(uint32_t at, float (&x)[RG]) {
-  if constexpr (F8 && RB == 4) {
-    float s[8];
-    tc::tmem_ld8(at, s);
+  static_assert(RG <= 8, "one load");
+  float s[8];
+  tc::tmem_ld8(at, s);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = fmaf(s[4 + i], 1.f / 16.f, s[i]);
-  } else if constexpr (F8) {
-#pragma unroll
-    for (int r0 = 0; r0 < RG; r0 += 8) {
-      float s[16];
-      tc::tmem_ld8x2(at + r0, at + RB + r0, s);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[r0 + i] = fmaf(s[8 + i], 1.f / 16.f, s[i]);
-    }
-  } else if constexpr (RG <= 8) {
-    float s[8];
-    tc::tmem_ld8(at, s);
-#pragma unroll
-    for (int i = 0; i < RG; ++i) x[i] = s[i];
-  } else {
-    static_assert(RG % 16 == 0, "groups of at most 8 rows, or of 16");
-#pragma unroll
-    for (int r0 = 0; r0 < RG; r0 += 16) tc::tmem_ld16(at + r0, x + r0);
-  }
+  for (int i = 0; i < RG; ++i) x[i] = s[i];
 }
 
 // A bounded wait that also ends when another role has given up.
@@ -212,7 +162,6 @@ __device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, int* dea
 // One row of a part by one warp, token by token in fp32: the way out when the accumulators hold a NaN, which may come from
 // a query that meets a token it does not see (0 * NaN) or from an infinity meeting a split probability.  A lane has
 // channels 4 lane .. 4 lane + 3.
-template <bool F8>
 __device__ __noinline__ void careful_row(const PagedAttnArgs& a, const PaPlan& p, const TcUnit& u, int qrow, float4& o,
                                          float& m, float& l) {
   const int lane = threadIdx.x & 31, w = qrow / p.G, g = qrow - w * p.G;
@@ -230,20 +179,10 @@ __device__ __noinline__ void careful_row(const PagedAttnArgs& a, const PaPlan& p
     if ((unsigned)page >= (unsigned)a.c.num_pages) continue;
     const int64_t row = ((int64_t)page * a.c.Hkv + u.h) * a.c.page_size + (tok - (int64_t)pg * a.c.page_size);
     float k[4], v[4];
-    if constexpr (F8) {
-      const uint32_t kc = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.c.k_pages) + row * TC_D + 4 * lane);
-      const uint32_t vc = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.c.v_pages) + row * TC_D + 4 * lane);
-      const float2 k0 = of_e4m3_pair(kc & 0xffffu), k1 = of_e4m3_pair(kc >> 16);
-      const float2 v0 = of_e4m3_pair(vc & 0xffffu), v1 = of_e4m3_pair(vc >> 16);
-      const float ks = a.c.k_scales[row], vs = a.c.v_scales[row];
-      k[0] = k0.x * ks, k[1] = k0.y * ks, k[2] = k1.x * ks, k[3] = k1.y * ks;
-      v[0] = v0.x * vs, v[1] = v0.y * vs, v[2] = v1.x * vs, v[3] = v1.y * vs;
-    } else {
-      const bf16* kp = static_cast<const bf16*>(a.c.k_pages) + row * TC_D + 4 * lane;
-      const bf16* vp = static_cast<const bf16*>(a.c.v_pages) + row * TC_D + 4 * lane;
+    const bf16* kp = static_cast<const bf16*>(a.c.k_pages) + row * TC_D + 4 * lane;
+    const bf16* vp = static_cast<const bf16*>(a.c.v_pages) + row * TC_D + 4 * lane;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) k[i] = to_f32(kp[i]), v[i] = to_f32(vp[i]);
-    }
+    for (int i = 0; i < 4; ++i) k[i] = to_f32(kp[i]), v[i] = to_f32(vp[i]);
     float s = q0 * k[0] + q1 * k[1] + q2 * k[2] + q3 * k[3];
 #pragma unroll
     for (int i = 16; i > 0; i >>= 1) s += __shfl_xor_sync(0xffffffffu, s, i);
@@ -256,21 +195,21 @@ __device__ __noinline__ void careful_row(const PagedAttnArgs& a, const PaPlan& p
   }
 }
 
-template <bool F8, int RB>
-__global__ void __launch_bounds__(TcCfg<F8, RB>::NT, 1)
+template <int RB>
+__global__ void __launch_bounds__(TcCfg<RB>::NT, 1)
     paged_attention_tc_kernel(const __grid_constant__ TcMaps maps, const PagedAttnArgs a, const PaPlan p, const int box) {
-  using C = TcCfg<F8, RB>;
-  using Sh = TcShared<F8, RB>;
-  constexpr int ES = C::ES, N1 = C::N1, N2 = C::N2, SLOT = C::SLOT, KS = C::KS, VS = C::VS, QP = C::QP, PP = C::PP;
-  constexpr int TG = C::TG, RS = C::RS, RG = C::RG, SB = C::SB, TC_NT = C::NT;
+  using C = TcCfg<RB>;
+  using Sh = TcShared<RB>;
+  constexpr int N1 = C::N1, N2 = C::N2, SLOT = C::SLOT, KS = C::KS, VS = C::VS, PP = C::PP;
+  constexpr int RS = C::RS, RG = C::RG, SB = C::SB, TC_NT = C::NT;
+  static_assert(SB * C::S_COLS + N2 <= C::TMEM_COLS, "tensor memory asked for");
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   unsigned char* slots = base;
   unsigned char* vslots = slots + KS * SLOT;
   unsigned char* pbuf = vslots + VS * SLOT;
   unsigned char* qbuf = pbuf + SB * C::P_BYTES;
-  float* join = reinterpret_cast<float*>(qbuf + 2 * C::Q_BYTES);  // [2][TG][RB][128]
-  Sh& sh = *reinterpret_cast<Sh*>(qbuf + 2 * C::Q_BYTES + C::JOIN);
+  Sh& sh = *reinterpret_cast<Sh*>(qbuf + 2 * C::Q_BYTES);
   pdl_begin();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int Hkv = a.c.Hkv, per_b = Hkv * p.blocks;
@@ -282,8 +221,8 @@ __global__ void __launch_bounds__(TcCfg<F8, RB>::NT, 1)
       tc::bar_init(&sh.s_full[i], 2), tc::bar_init(&sh.s_free[i], 4 * RS);
       tc::bar_init(&sh.p_full[i], 4 * RS), tc::bar_init(&sh.p_free[i], 1);
     }
-    for (int i = 0; i < 2; ++i) tc::bar_init(&sh.q_full[i], 1), tc::bar_init(&sh.q_free[i], 1 + 4 * TG * RS);
-    for (int i = 0; i < TG; ++i) tc::bar_init(&sh.o_full[i], 1);
+    for (int i = 0; i < 2; ++i) tc::bar_init(&sh.q_full[i], 1), tc::bar_init(&sh.q_free[i], 1 + 4 * RS);
+    tc::bar_init(&sh.o_full, 1);
     for (int i = 0; i < 2; ++i) tc::bar_init(&sh.drain[i], 1);
     tc::bar_fence_init();
     sh.dead = 0;
@@ -338,63 +277,60 @@ __global__ void __launch_bounds__(TcCfg<F8, RB>::NT, 1)
     TcRing<KS> kr;
     TcRing<VS> vr;
     TcRing<C::INFO> info;
-    // this lane's box of the next tile: its page's id is asked for a tile ahead (waiting for it tile by tile took longer
-    // than an 8-bit tile's copy)
+    // This lane's box of the next tile: its page's id is asked for a tile ahead, its place among the pages follows from the
+    // last tile's.
+    const int per_tile = TC_TILE / a.c.page_size, rest = TC_TILE - per_tile * a.c.page_size;
     bool more = it.next(a, p, box), next_there = false;
-    int next_page = 0, next_off = 0, next_h = 0;
+    int next_page = 0, pg = 0, off = 0;
+    const int32_t* table = nullptr;
     auto look_up = [&]() {
-      const int64_t tok = (int64_t)it.u.start + (int64_t)it.tile * TC_TILE + lane * box;
-      next_there = lane < boxes && tok < it.u.len;
-      if (next_there) {
-        const int pg = (int)tok / a.c.page_size;
-        next_off = (int)tok - pg * a.c.page_size;
-        next_h = it.u.h;
-        next_page = __ldg(a.block_table + (int64_t)it.u.b * a.max_pages + pg);
+      const int tok = it.u.start + it.tile * TC_TILE + lane * box;
+      if (it.first()) {
+        pg = tok / a.c.page_size;
+        off = tok - pg * a.c.page_size;
+        table = a.block_table + (int64_t)it.u.b * a.max_pages;
+      } else {
+        pg += per_tile;
+        off += rest;
+        if (off >= a.c.page_size) off -= a.c.page_size, ++pg;
       }
+      next_there = lane < boxes && tok < it.u.len;
+      if (next_there) next_page = __ldg(table + pg);
     };
     if (more) look_up();
     while (more) {
       bool there = next_there;
-      const int page = next_page, off = next_off, h = next_h;
+      const int page = next_page, at = off, h = it.u.h;
       more = it.next(a, p, box);
       if (more) look_up();
       int row = 0;
       if (there) {
         there = (unsigned)page < (unsigned)a.c.num_pages;
-        if (there) row = (page * Hkv + h) * a.c.page_size + off;
+        if (there) row = (page * Hkv + h) * a.c.page_size + at;
         else flag_status(a.status, KDA_DEV_PAGE_OOB);
       }
       const unsigned mask = __ballot_sync(0xffffffffu, there);
       const int count = __popc(mask);
-      const uint32_t bytes = count * box * TC_D * ES;
+      const uint32_t bytes = count * box * TC_D * 2;
       // A slot's n-th use waits for the release of the one before (the first finds the round before the first over).
-      // The tile's scales and list of boxes go by its number: they have been read when its V is released, which the
-      // copies of VS tiles later wait for.
+      // The tile's list of boxes goes by its number: it has been read when its V is released, which the copies of VS tiles
+      // later wait for.
       ok = ok && tc_wait(&sh.k_empty[kr.at], kr.parity ^ 1, &sh.dead);
       if (lane == 0 && ok) {
         sh.there[info.at] = (int)mask;
-        tc::bar_arrive_expect_tx(&sh.k_full[kr.at], bytes + (F8 ? count * box * 8 : 0));
+        tc::bar_arrive_expect_tx(&sh.k_full[kr.at], bytes);
       }
       __syncwarp();
-      if (there && ok) {
-        unsigned char* dst = slots + kr.at * SLOT + lane * box * 128;
-        tc::tma_load_2d(dst, &maps.k, 0, row, &sh.k_full[kr.at]);
-        if constexpr (F8) {
-          tc::bulk_g2s(&sh.scales[info.at][0][lane * box], a.c.k_scales + row, box * 4, &sh.k_full[kr.at]);
-          tc::bulk_g2s(&sh.scales[info.at][1][lane * box], a.c.v_scales + row, box * 4, &sh.k_full[kr.at]);
-        } else {
-          tc::tma_load_2d(dst + TC_TILE * 128, &maps.k, 64, row, &sh.k_full[kr.at]);
-        }
-      }
+      // lane i has channels 0 .. 63 or 64 .. 127 of box i / 2
+      const int two_row = __shfl_sync(0xffffffffu, row, lane >> 1), odd = lane & 1;
+      const bool two = lane < 2 * boxes && (mask >> (lane >> 1) & 1);
+      const uint32_t piece = odd * (TC_TILE * 128) + (lane >> 1) * box * 128;
+      if (two && ok) tc::tma_load_2d(slots + kr.at * SLOT + piece, &maps.k, odd * 64, two_row, &sh.k_full[kr.at]);
       const bool k_sent = ok;
       ok = ok && tc_wait(&sh.v_empty[vr.at], vr.parity ^ 1, &sh.dead);
       if (lane == 0 && ok) tc::bar_arrive_expect_tx(&sh.v_full[vr.at], bytes);
       __syncwarp();
-      if (there && ok) {
-        unsigned char* dst = vslots + vr.at * SLOT + lane * box * 128;
-        tc::tma_load_2d(dst, &maps.v, 0, row, &sh.v_full[vr.at]);
-        if constexpr (!F8) tc::tma_load_2d(dst + TC_TILE * 128, &maps.v, 64, row, &sh.v_full[vr.at]);
-      }
+      if (two && ok) tc::tma_load_2d(vslots + vr.at * SLOT + piece, &maps.v, odd * 64, two_row, &sh.v_full[vr.at]);
       if (!__all_sync(0xffffffffu, ok)) {
         // let what is on its way arrive before the CTA ends: this round's copies and those of the rounds just before
         if (lane == 0) {
@@ -414,14 +350,14 @@ __global__ void __launch_bounds__(TcCfg<F8, RB>::NT, 1)
       info.step();
     }
   } else if (warp == 1 || warp == 3) {
-    // ---- products, one thread each: tiles numbered over the CTA's whole share, tile g has buffers g % SB and group
-    // g % TG.  (One thread for both took 1700 cycles a tile, most of it its own instructions' latency.)
+    // ---- products, one thread each; the tiles of the CTA's whole share take the buffers in turn.  (One thread for both
+    // took 1700 cycles a tile, most of it its own instructions' latency.)
     bool ok = true;
     TcTiles it(walk);
     TcRing<SB> buf;
     if (warp == 1) {
       if (lane == 0) {
-        constexpr uint32_t id = F8 ? tc::idesc_e4m3(128, N1) : tc::idesc_bf16(128, N1);
+        constexpr uint32_t id = tc::idesc_bf16(128, N1);
         const uint64_t k0 = tc::sdesc(tc::smem_u32(slots)), q0 = tc::sdesc(tc::smem_u32(qbuf));
         TcRing<KS> ring;
         while (it.next(a, p, box)) {
@@ -429,16 +365,15 @@ __global__ void __launch_bounds__(TcCfg<F8, RB>::NT, 1)
           ok = ok && tc_wait(&sh.s_free[buf.at], buf.parity ^ 1, &sh.dead);
           ok = ok && tc_wait(&sh.k_full[ring.at], ring.parity, &sh.dead);
           if (!ok) break;
-          tc::bar_arrive(&sh.s_full[buf.at]);  // hands on what came with K: the scales and the list of boxes
+          tc::bar_arrive(&sh.s_full[buf.at]);  // hands on what came with K: the list of boxes
           tc::fence_after_sync();
           const uint64_t kd = k0 + ring.at * (SLOT / 16), qd = q0 + (it.unit_no & 1) * (C::Q_BYTES / 16);
           const uint32_t d = tmem + buf.at * C::S_COLS;
 #pragma unroll
-          for (int kk = 0; kk < 4 * ES; ++kk) {  // 32 bytes of each row per step
+          for (int kk = 0; kk < 8; ++kk) {  // 32 bytes of each row per step
             const uint64_t da = kd + (kk / 4 * (TC_TILE * 128) + kk % 4 * 32) / 16;
             const uint64_t db = qd + (kk / 4 * (N1 * 128) + kk % 4 * 32) / 16;
-            if constexpr (F8) tc::mma_ss_f8(d, da, db, id, kk > 0);
-            else tc::mma_ss(d, da, db, id, kk > 0);
+            tc::mma_ss(d, da, db, id, kk > 0);
           }
           tc::commit(&sh.s_full[buf.at]);
           tc::commit(&sh.k_empty[ring.at]);
@@ -448,10 +383,9 @@ __global__ void __launch_bounds__(TcCfg<F8, RB>::NT, 1)
         }
       }
     } else {
-      constexpr uint32_t id = (F8 ? tc::idesc_e4m3(128, N2) : tc::idesc_bf16(128, N2)) | tc::IDESC_A_MN;
+      constexpr uint32_t id = tc::idesc_bf16(128, N2) | tc::IDESC_A_MN;
       const uint64_t v0 = tc::sdesc_mn(tc::smem_u32(vslots), TC_TILE * 128), p0 = tc::sdesc(tc::smem_u32(pbuf));
       TcRing<VS> ring;
-      TcRing<TG> grp;
       TcRing<C::INFO> info;
       const int all_boxes = (int)((1u << (TC_TILE / box)) - 1);
       while (it.next(a, p, box)) {
@@ -468,7 +402,7 @@ __global__ void __launch_bounds__(TcCfg<F8, RB>::NT, 1)
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
                 reinterpret_cast<uint4*>(vrow)[i] = make_uint4(0, 0, 0, 0);
-                if constexpr (!F8) reinterpret_cast<uint4*>(vrow + TC_TILE * 128)[i] = make_uint4(0, 0, 0, 0);
+                reinterpret_cast<uint4*>(vrow + TC_TILE * 128)[i] = make_uint4(0, 0, 0, 0);
               }
             }
           tc::fence_proxy_async();
@@ -479,24 +413,21 @@ __global__ void __launch_bounds__(TcCfg<F8, RB>::NT, 1)
           if (ok) {
             tc::fence_after_sync();
             const uint64_t vd = v0 + ring.at * (SLOT / 16), pd = p0 + buf.at * (C::P_BYTES / 16);
-            const uint32_t d = tmem_o + grp.at * N2;
-            const bool begins = it.tile - TG < it.u.t0;  // the group's first tile of the unit
+            const uint32_t d = tmem_o;
 #pragma unroll
-            for (int kk = 0; kk < 4 * ES; ++kk) {  // 32 (e4m3) or 16 tokens per step
-              const uint64_t da = vd + kk * (F8 ? 4096 : 2048) / 16;
+            for (int kk = 0; kk < 8; ++kk) {  // 16 tokens per step
+              const uint64_t da = vd + kk * 2048 / 16;
               const uint64_t db = pd + (kk / 4 * (N2 * 128) + kk % 4 * 32) / 16;
-              const uint32_t add = !(begins && kk == 0);
-              if constexpr (F8) tc::mma_ss_f8(d, da, db, id, add);
-              else tc::mma_ss(d, da, db, id, add);
+              const uint32_t add = !(it.first() && kk == 0);
+              tc::mma_ss(d, da, db, id, add);
             }
             tc::commit(&sh.p_free[buf.at]);
             tc::commit(&sh.v_empty[ring.at]);
-            if (it.tile + TG >= it.u.t1) tc::commit(&sh.o_full[grp.at]);  // the group's last tile of the unit
+            if (it.last()) tc::commit(&sh.o_full);
           }
         }
         ring.step();
         buf.step();
-        grp.step();
         info.step();
       }
     }
@@ -533,35 +464,12 @@ __global__ void __launch_bounds__(TcCfg<F8, RB>::NT, 1)
 #pragma unroll
         for (int i = 0; i < QCH; ++i) {
           const int r = r0 + i, row = row0 + r;
-          float down = 1.f;
-          if constexpr (F8) {
-            const float x0 = __uint_as_float(raw[i].x << 16), x1 = __uint_as_float(raw[i].x & 0xffff0000u);
-            const float x2 = __uint_as_float(raw[i].y << 16), x3 = __uint_as_float(raw[i].y & 0xffff0000u);
-            float amax = fmaxf(fmaxf(fabsf(x0), fabsf(x1)), fmaxf(fabsf(x2), fabsf(x3)));
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            int e = amax > 0.f ? 7 - ((int)(__float_as_uint(amax) >> 23) - 127) : 0;  // the maximum to [2^7, 2^8)
-            e = max(-120, min(120, e));
-            const float up = __uint_as_float((uint32_t)(e + 127) << 23);
-            down = __uint_as_float((uint32_t)(127 - e) << 23);
-            float v0 = x0 * up, v1 = x1 * up, v2 = x2 * up, v3 = x3 * up;
-#pragma unroll
-            for (int part = 0; part < QP; ++part) {
-              const uint32_t c0 = e4m3_pair(v0, v1), c1 = e4m3_pair(v2, v3);
-              const float2 f0 = of_e4m3_pair(c0), f1 = of_e4m3_pair(c1);
-              const int nrow = part * RB + r;
-              const uint32_t at = qb + nrow * 128 + (((lane >> 2) ^ (nrow & 7)) << 4) + (lane & 3) * 4;
-              asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(c0 | c1 << 16) : "memory");
-              v0 = (v0 - f0.x) * 16.f, v1 = (v1 - f0.y) * 16.f, v2 = (v2 - f1.x) * 16.f, v3 = (v3 - f1.y) * 16.f;
-            }
-          } else {
-            // channels 4 lane ..: block of 64 channels, 16-byte chunk of 8
-            const uint32_t at = qb + (lane >> 4) * (N1 * 128) + r * 128 + ((((lane & 15) >> 1) ^ (r & 7)) << 4) + (lane & 1) * 8;
-            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(raw[i].x), "r"(raw[i].y) : "memory");
-          }
+          // channels 4 lane ..: block of 64 channels, 16-byte chunk of 8
+          const uint32_t at = qb + (lane >> 4) * (N1 * 128) + r * 128 + ((((lane & 15) >> 1) ^ (r & 7)) << 4) + (lane & 1) * 8;
+          asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(raw[i].x), "r"(raw[i].y) : "memory");
           if (lane == 0) {
             const int wt = row / p.G, g = row - wt * p.G;
-            sh.factor[buf][r] = down * a.scale * (a.softcap > 0.f ? 2.f * PA_LOG2E / a.softcap : PA_LOG2E);
+            sh.factor[buf][r] = a.scale * (a.softcap > 0.f ? 2.f * PA_LOG2E / a.softcap : PA_LOG2E);
             sh.last[buf][r] = row < p.rows ? u.len - a.W + wt : -1;
             sh.head[buf][r] = row < p.rows ? wt * a.Hq + u.h * p.G + g : -1;
           }
@@ -575,32 +483,27 @@ __global__ void __launch_bounds__(TcCfg<F8, RB>::NT, 1)
   } else if (warp >= 4) {
     // ---- softmax: thread = token of the tile, then channel of the output.  A role that gives up a wait goes on through
     // its tiles without results (no later wait holds it), so that the barriers between groups are always met.
-    const int tk = (tid - TC_SOFT0) & 127, quarter = warp & 3, sg = (warp - 4) >> 2, tg = sg / RS, rs = sg % RS;
+    const int tk = (tid - TC_SOFT0) & 127, quarter = warp & 3, rs = (warp - 4) >> 2;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     const float cap2 = a.softcap * PA_LOG2E;
-    const int bar_id = 1 + sg, rfirst = rs * RG;  // this group's rows of the unit
+    const int bar_id = 1 + rs, rfirst = rs * RG;  // this group's rows of the unit
     float m[RG], l[RG];
     TcTiles it(walk);
-    TcRing<SB> buf, before(SB - TG);  // this tile's buffers, and those of the group's tile before
+    TcRing<SB> buf, before(SB - 1);  // this tile's buffers, and those of the tile before
     before.parity = 1;
     TcRing<C::INFO> info;
-    TcRing<TG> turn;
-    int units = -1, row0 = 0, nrows = 0, all_to = 0;
+    int row0 = 0, nrows = 0, all_to = 0;
     int64_t all_from = 0;
-    unsigned o_uses = 0;  // of this group's accumulators
-    bool bad = false, mine_any = false;
+    bool bad = false;
     const int box_bit = tk / box;
     PaMeta meta{-1, 0};
     int rows_done = 0;
     // where this thread's element of an operand row lies in a probability buffer: (place ^ (row % 8) * 16) + row * 128
-    const uint32_t place = F8 ? ((uint32_t)(tk >> 4) << 4) + (tk & 15)
-                              : (uint32_t)(tk >> 6) * (N2 * 128) + ((uint32_t)((tk & 63) >> 3) << 4) + (tk & 7) * 2;
-    for (; it.next(a, p, box); buf.step(), before.step(), info.step(), turn.step()) {
+    const uint32_t place = (uint32_t)(tk >> 6) * (N2 * 128) + ((uint32_t)((tk & 63) >> 3) << 4) + (tk & 7) * 2;
+    for (; it.next(a, p, box); buf.step(), before.step(), info.step()) {
       const TcUnit& u = it.u;
       const int qb = it.unit_no & 1;
-      if (it.unit_no != units) {
-        units = it.unit_no;
-        mine_any = false;
+      if (it.first()) {
         row0 = u.rb * RB;
         nrows = min(RB, p.rows - row0);
         // tokens that every row of the unit sees
@@ -610,146 +513,117 @@ __global__ void __launch_bounds__(TcCfg<F8, RB>::NT, 1)
 #pragma unroll
         for (int r = 0; r < RG; ++r) m[r] = TC_NONE, l[r] = 0.f;
       }
-      if (TG == 1 || turn.at == tg) {
-        const bool begins = !mine_any;
-        mine_any = true;
-        bad |= !tc_wait(&sh.s_full[buf.at], buf.parity, &sh.dead);
+      bad |= !tc_wait(&sh.s_full[buf.at], buf.parity, &sh.dead);
+      tc::fence_after_sync();
+      const int64_t tok0 = (int64_t)u.start + (int64_t)it.tile * TC_TILE;
+      const int tok = (int)tok0 + tk;
+      const bool there = tok < u.len && (sh.there[info.at] >> box_bit & 1);
+      const bool masked = !there || tok0 + TC_TILE - 1 > all_to || tok0 < all_from;
+      float x[RG];
+      load_scores<RG>(tmem + buf.at * C::S_COLS + lanes + rfirst, x);
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) tc::bar_arrive(&sh.s_free[buf.at]);
+#pragma unroll
+      for (int r = 0; r < RG; r += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(&sh.factor[qb][rfirst + r]);
+        x[r] *= f.x, x[r + 1] *= f.y, x[r + 2] *= f.z, x[r + 3] *= f.w;
+      }
+      if (a.softcap > 0.f) {
+        if (a.softcap <= PA_NEAR_CAP) {
+#pragma unroll
+          for (int r = 0; r < RG; ++r) x[r] = capped(x[r], cap2);
+        } else {
+#pragma unroll
+          for (int r = 0; r < RG; ++r)
+            x[r] = fabsf(x[r]) < 0.3f * PA_LOG2E ? capped_series(x[r], cap2) : capped(x[r], cap2);
+        }
+      }
+      if (masked) {
+#pragma unroll
+        for (int r = 0; r < RG; ++r) {
+          const int last = sh.last[qb][rfirst + r];
+          x[r] = there && tok <= last && tok > (int64_t)last - window ? x[r] : -INFINITY;
+        }
+      }
+      float over = -INFINITY;
+#pragma unroll
+      for (int r = 0; r < RG; ++r) over = fmaxf(over, x[r] - m[r]);
+      if (tc::named_bar_or(bar_id, 128, over > TC_SLACK)) {
+        // ---- references move: the rows' maxima over the 128 tokens, then sums and accumulators follow
+#pragma unroll
+        for (int r = 0; r < RG; ++r) {
+          float t = x[r];
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
+          if (lane == 0) sh.red[quarter][rfirst + r] = t;
+        }
+        // the group's last product into its accumulators is through
+        if (!it.first()) bad |= !tc_wait(&sh.p_free[before.at], before.parity, &sh.dead);
         tc::fence_after_sync();
-        const int64_t tok0 = (int64_t)u.start + (int64_t)it.tile * TC_TILE;
-        const int tok = (int)tok0 + tk;
-        const bool there = tok < u.len && (sh.there[info.at] >> box_bit & 1);
-        float ks = 1.f, vs = 1.f, lift = 0.f;
-        if constexpr (F8) {
-          ks = there ? sh.scales[info.at][0][tk] : 0.f;
-          vs = there ? sh.scales[info.at][1][tk] : 0.f;
-          lift = (float)((int)(__float_as_uint(vs) >> 23) - 126);  // just above log2 of the value scale
-        }
-        const bool masked = !there || tok0 + TC_TILE - 1 > all_to || tok0 < all_from;
-        float x[RG];
-        load_scores<F8, RB, RG>(tmem + buf.at * C::S_COLS + lanes + rfirst, x);
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) tc::bar_arrive(&sh.s_free[buf.at]);
+        tc::named_bar(bar_id, 128);
+        float by[RG];
 #pragma unroll
-        for (int r = 0; r < RG; r += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(&sh.factor[qb][rfirst + r]);
-          x[r] *= f.x * ks, x[r + 1] *= f.y * ks, x[r + 2] *= f.z * ks, x[r + 3] *= f.w * ks;
+        for (int r = 0; r < RG; ++r) {
+          const float(&red)[4][RB] = sh.red;
+          const int q = rfirst + r;
+          const float mn = fmaxf(fmaxf(fmaxf(red[0][q], red[1][q]), fmaxf(red[2][q], red[3][q])), m[r]);
+          by[r] = ex2(m[r] - mn);
+          m[r] = mn;
+          l[r] *= by[r];
         }
-        if (a.softcap > 0.f) {
-          if (a.softcap <= PA_NEAR_CAP) {
+        if (!it.first()) {
+          if constexpr (RG < 8) {  // column c is row c % RB's; the group has all rows
 #pragma unroll
-            for (int r = 0; r < RG; ++r) x[r] = capped(x[r], cap2);
+            for (int c = 0; c < PP * RB; c += 8) {
+              float v[8];
+              tc::tmem_ld8(tmem_o + lanes + c, v);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) v[i] *= by[(c + i) % RB];
+              tc::tmem_st8f(tmem_o + lanes + c, v);
+            }
           } else {
 #pragma unroll
-            for (int r = 0; r < RG; ++r)
-              x[r] = fabsf(x[r]) < 0.3f * PA_LOG2E ? capped_series(x[r], cap2) : capped(x[r], cap2);
-          }
-        }
-        if (masked) {
+            for (int part = 0; part < PP; ++part)
 #pragma unroll
-          for (int r = 0; r < RG; ++r) {
-            const int last = sh.last[qb][rfirst + r];
-            x[r] = there && tok <= last && tok > (int64_t)last - window ? x[r] : -INFINITY;
-          }
-        }
-        float over = -INFINITY;
-#pragma unroll
-        for (int r = 0; r < RG; ++r) over = fmaxf(over, x[r] - m[r]);
-        if (tc::named_bar_or(bar_id, 128, over + lift > TC_SLACK)) {
-          // ---- references move: the rows' maxima over the 128 tokens, then sums and accumulators follow
-#pragma unroll
-          for (int r = 0; r < RG; ++r) {
-            float t = x[r] + lift;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
-            if (lane == 0) sh.red[tg][quarter][rfirst + r] = t;
-          }
-          // the group's last product into its accumulators is through
-          if (!begins) bad |= !tc_wait(&sh.p_free[before.at], before.parity, &sh.dead);
-          tc::fence_after_sync();
-          tc::named_bar(bar_id, 128);
-          float by[RG];
-#pragma unroll
-          for (int r = 0; r < RG; ++r) {
-            const float(&red)[4][RB] = sh.red[tg];
-            const int q = rfirst + r;
-            const float mn = fmaxf(fmaxf(fmaxf(red[0][q], red[1][q]), fmaxf(red[2][q], red[3][q])), m[r]);
-            by[r] = ex2(m[r] - mn);
-            m[r] = mn;
-            l[r] *= by[r];
-          }
-          if (!begins) {
-            if constexpr (RG < 8) {  // column c is row c % RB's; the group has all rows
-#pragma unroll
-              for (int c = 0; c < PP * RB; c += 8) {
+              for (int c = 0; c < RG; c += 8) {
                 float v[8];
-                tc::tmem_ld8(tmem_o + tg * N2 + lanes + c, v);
+                const uint32_t at = tmem_o + lanes + part * RB + rfirst + c;
+                tc::tmem_ld8(at, v);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] *= by[(c + i) % RB];
-                tc::tmem_st8f(tmem_o + tg * N2 + lanes + c, v);
+                for (int i = 0; i < 8; ++i) v[i] *= by[c + i];
+                tc::tmem_st8f(at, v);
               }
-            } else {
-#pragma unroll
-              for (int part = 0; part < PP; ++part)
-#pragma unroll
-                for (int c = 0; c < RG; c += 8) {
-                  float v[8];
-                  const uint32_t at = tmem_o + tg * N2 + lanes + part * RB + rfirst + c;
-                  tc::tmem_ld8(at, v);
-#pragma unroll
-                  for (int i = 0; i < 8; ++i) v[i] *= by[c + i];
-                  tc::tmem_st8f(at, v);
-                }
-            }
-            tc::tmem_wait_st();
           }
-          tc::named_bar(bar_id, 128);  // red may be written again
+          tc::tmem_wait_st();
         }
-
-        // ---- probabilities and their parts
-        bad |= !tc_wait(&sh.p_free[buf.at], buf.parity ^ 1, &sh.dead);
-        const uint32_t pb = tc::smem_u32(pbuf + buf.at * C::P_BYTES) + place;
-        const float pv = F8 ? vs * TC_P_UNIT : 1.f;
-#pragma unroll
-        for (int r = 0; r < RG; r += 2) {
-          float p0 = ex2(x[r] - m[r]), p1 = ex2(x[r + 1] - m[r + 1]);
-          l[r] += p0;
-          l[r + 1] += p1;
-          __half2 h;
-          if constexpr (F8) h = __floats2half2_rn(p0 * pv, p1 * pv);  // 11 bits, which the three parts hold
-#pragma unroll
-          for (int part = 0; part < PP; ++part) {
-            const int c0 = part * RB + r;  // the operand's row is this plus rfirst (a multiple of 8, or 0)
-            const uint32_t a0 = (pb ^ ((c0 & 7) << 4)) + (rfirst + c0) * 128;
-            const uint32_t a1 = (pb ^ (((c0 + 1) & 7) << 4)) + (rfirst + c0 + 1) * 128;
-            uint32_t c;
-            if constexpr (F8) {
-              uint16_t c16;
-              asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c16) : "r"(*reinterpret_cast<const uint32_t*>(&h)));
-              c = c16;
-              st_shared_u8(a0, c & 0xffu);
-              st_shared_u8(a1, c >> 8);
-              if (part + 1 < PP) {
-                const uint32_t back = half2_of_codes(c);
-                h = __hmul2(__hsub2(h, *reinterpret_cast<const __half2*>(&back)), __float2half2_rn(16.f));
-              }
-            } else {
-              c = split_pair<false>(p0, p1);
-              st_shared_u16(a0, c & 0xffffu);
-              st_shared_u16(a1, c >> 16);
-            }
-          }
-        }
-        tc::fence_proxy_async();
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) tc::bar_arrive(&sh.p_full[buf.at]);
+        tc::named_bar(bar_id, 128);  // red may be written again
       }
+
+      // ---- probabilities and their parts
+      bad |= !tc_wait(&sh.p_free[buf.at], buf.parity ^ 1, &sh.dead);
+      const uint32_t pb = tc::smem_u32(pbuf + buf.at * C::P_BYTES) + place;
+#pragma unroll
+      for (int r = 0; r < RG; r += 2) {
+        float p0 = ex2(x[r] - m[r]), p1 = ex2(x[r + 1] - m[r + 1]);
+        l[r] += p0;
+        l[r + 1] += p1;
+#pragma unroll
+        for (int part = 0; part < PP; ++part) {
+          const int c0 = part * RB + r;  // the operand's row is this plus rfirst (a multiple of 8, or 0)
+          const uint32_t c = split_pair<false>(p0, p1);
+          st_shared_u16((pb ^ ((c0 & 7) << 4)) + (rfirst + c0) * 128, c & 0xffffu);
+          st_shared_u16((pb ^ (((c0 + 1) & 7) << 4)) + (rfirst + c0 + 1) * 128, c >> 16);
+        }
+      }
+      tc::fence_proxy_async();
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) tc::bar_arrive(&sh.p_full[buf.at]);
       if (!it.last()) continue;
 
       // ---- end of the unit's part
       __syncwarp();
-      const int jb = it.unit_no & 1;
       const bool whole = u.t0 == 0 && u.t1 == u.tiles;
       const int64_t part_at = (me * 2 + (u.t0 == 0 ? 1 : 0)) * RB;
       bool nan = false;
@@ -770,78 +644,36 @@ __global__ void __launch_bounds__(TcCfg<F8, RB>::NT, 1)
           if (tk == 0) *reinterpret_cast<float2*>(p.part_ml + (part_at + r) * 2) = make_float2(mr, lr);
         }
       };
-      if (mine_any) {
 #pragma unroll
-        for (int r = 0; r < RG; ++r) {
-          float t = l[r];
+      for (int r = 0; r < RG; ++r) {
+        float t = l[r];
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-          if (lane == 0) sh.red[tg][quarter][rfirst + r] = t;
-        }
-        bad |= !tc_wait(&sh.o_full[tg], o_uses & 1, &sh.dead);
-        ++o_uses;
-        tc::fence_after_sync();
-        tc::named_bar(bar_id, 128);
-        constexpr int CH = RG < 8 ? RG : 8;
-#pragma unroll
-        for (int r0 = 0; r0 < RG; r0 += CH) {
-          float o[PP * CH];
-          if constexpr (RG < 8) {
-            float t[16];
-            tc::tmem_ld16(tmem_o + tg * N2 + lanes, t);
-#pragma unroll
-            for (int i = 0; i < PP * CH; ++i) o[i] = t[i];
-          } else {
-#pragma unroll
-            for (int part = 0; part < PP; ++part)
-              tc::tmem_ld8(tmem_o + tg * N2 + lanes + part * RB + rfirst + r0, o + part * CH);
-          }
-#pragma unroll
-          for (int i = 0; i < CH; ++i) {
-            const int r = rfirst + r0 + i;
-            float y;
-            if constexpr (F8) y = fmaf(o[2 * CH + i], 1.f / 256.f, fmaf(o[CH + i], 1.f / 16.f, o[i])) * (1.f / TC_P_UNIT);
-            else y = o[i] + o[CH + i];
-            const float lr = sh.red[tg][0][r] + sh.red[tg][1][r] + sh.red[tg][2][r] + sh.red[tg][3][r];
-            if constexpr (TG == 1) {
-              put(r, y, m[r0 + i], lr);
-            } else {
-              join[((jb * TG + tg) * RB + r) * TC_D + tk] = y;
-              if (tk == 0) sh.jm[jb][tg][r] = m[r0 + i], sh.jl[jb][tg][r] = lr;
-            }
-          }
-        }
-        tc::fence_before_sync();
-      } else if (TG > 1 && tk < RB) {
-        sh.jm[jb][tg][tk] = TC_NONE, sh.jl[jb][tg][tk] = 0.f;  // a unit of fewer tiles than groups
+        for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+        if (lane == 0) sh.red[quarter][rfirst + r] = t;
       }
-      if constexpr (TG > 1) {
-        // the groups' results together, rows dealt out to them.  The other unit's half of `join` takes the next results,
-        // so this barrier is also what frees this half for the one after.
-        tc::named_bar(15, TG * RS * 128);
-        for (int r = tg; r < nrows; r += TG) {
-          float mr = TC_NONE, lr = 0.f, y = 0.f;
+      bad |= !tc_wait(&sh.o_full, it.unit_no & 1, &sh.dead);
+      tc::fence_after_sync();
+      tc::named_bar(bar_id, 128);
+      float o[PP * RG];
+      if constexpr (RG < 8) {
+        tc::tmem_ld8(tmem_o + lanes, o);
+      } else {
 #pragma unroll
-          for (int i = 0; i < TG; ++i) mr = fmaxf(mr, sh.jm[jb][i][r]);
+        for (int part = 0; part < PP; ++part) tc::tmem_ld8(tmem_o + lanes + part * RB + rfirst, o + part * RG);
+      }
+      tc::fence_before_sync();
 #pragma unroll
-          for (int i = 0; i < TG; ++i) {
-            const float mi = sh.jm[jb][i][r], li = sh.jl[jb][i][r];
-            if (mi == TC_NONE && li == 0.f) continue;  // saw nothing: its accumulators may never have been written
-            const float by = ex2(mi - mr);
-            lr += li * by;
-            y += join[((jb * TG + i) * RB + r) * TC_D + tk] * by;
-          }
-          put(r, y, mr, lr);
-        }
+      for (int i = 0; i < RG; ++i) {
+        const int r = rfirst + i;
+        put(r, o[i] + o[RG + i], m[i], sh.red[0][r] + sh.red[1][r] + sh.red[2][r] + sh.red[3][r]);
       }
       if (tc::named_bar_or(bar_id, 128, nan)) {  // also: red may be written again
-        // rows this group wrote: all of its rows (TG = 1), or every TG-th
         for (int i = quarter; i < RG; i += 4) {
-          const int r = TG == 1 ? rfirst + i : tg + i * TG;
+          const int r = rfirst + i;
           if (r >= nrows || bad) continue;
           float4 o;
           float mr, lr;
-          careful_row<F8>(a, p, u, row0 + r, o, mr, lr);
+          careful_row(a, p, u, row0 + r, o, mr, lr);
           const bool none = mr == TC_NONE && lr == 0.f;
           if (mr == TC_NONE) mr = none ? -INFINITY : 0.f;
           if (whole) {
@@ -890,20 +722,20 @@ int page_box(int page_size) {  // largest power of two that divides the page, at
   return b < TC_TILE ? b : TC_TILE;
 }
 
-template <bool F8, int RB>
+template <int RB>
 cudaError_t tc_launch(const PagedAttnArgs& a, const PaPlan& p, int sms, cudaStream_t s) {
-  using C = TcCfg<F8, RB>;
-  auto kernel = paged_attention_tc_kernel<F8, RB>;
-  static_assert(C::INFO > C::VS, "scales kept until they are read");
-  constexpr int bytes = 1024 + C::SLOTS * C::SLOT + C::SB * C::P_BYTES + 2 * C::Q_BYTES + C::JOIN +
-                        (int)sizeof(TcShared<F8, RB>);
+  using C = TcCfg<RB>;
+  auto kernel = paged_attention_tc_kernel<RB>;
+  static_assert(C::INFO > C::VS, "lists of boxes kept until they are read");
+  constexpr int bytes = 1024 + C::SLOTS * C::SLOT + C::SB * C::P_BYTES + 2 * C::Q_BYTES +
+                        (int)sizeof(TcShared<RB>);
   static_assert(bytes <= 227 * 1024 && C::KS >= 2, "shared memory of one SM");
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
   const int box = page_box(a.c.page_size);
   const long long rows = (long long)a.c.num_pages * a.c.Hkv * a.c.page_size;
   TcMaps maps;
-  if (!encode_cache_map(&maps.k, a.c.k_pages, F8, rows, box) || !encode_cache_map(&maps.v, a.c.v_pages, F8, rows, box))
+  if (!encode_cache_map(&maps.k, a.c.k_pages, rows, box) || !encode_cache_map(&maps.v, a.c.v_pages, rows, box))
     return cudaErrorInvalidValue;
   int64_t ctas = sms < PA_SMS ? sms : PA_SMS;
   const int64_t tiles = (int64_t)a.max_pages * a.c.page_size / TC_TILE + 2 + TC_UNIT_COST;
@@ -919,7 +751,7 @@ cudaError_t tc_launch(const PagedAttnArgs& a, const PaPlan& p, int sms, cudaStre
 }  // namespace
 
 bool pa_tc_supported(const PagedAttnArgs& a) {
-  return a.c.d == TC_D && a.q_bf16 && a.out_bf16 && a.c.num_pages > 0 &&
+  return a.c.d == TC_D && !a.c.e4m3 && a.q_bf16 && a.out_bf16 && a.c.num_pages > 0 &&
          (int64_t)a.c.num_pages * a.c.Hkv * a.c.page_size <= 0x7fffffff;
 }
 
@@ -927,10 +759,10 @@ int pa_tc_row_block(int rows) { return rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 1
 
 cudaError_t pa_tc(const PagedAttnArgs& a, const PaPlan& p, int sms, cudaStream_t s) {
   switch (pa_tc_row_block(p.rows)) {
-    case 4: return a.c.e4m3 ? tc_launch<true, 4>(a, p, sms, s) : tc_launch<false, 4>(a, p, sms, s);
-    case 8: return a.c.e4m3 ? tc_launch<true, 8>(a, p, sms, s) : tc_launch<false, 8>(a, p, sms, s);
-    case 16: return a.c.e4m3 ? tc_launch<true, 16>(a, p, sms, s) : tc_launch<false, 16>(a, p, sms, s);
-    default: return a.c.e4m3 ? tc_launch<true, 32>(a, p, sms, s) : tc_launch<false, 32>(a, p, sms, s);
+    case 4: return tc_launch<4>(a, p, sms, s);
+    case 8: return tc_launch<8>(a, p, sms, s);
+    case 16: return tc_launch<16>(a, p, sms, s);
+    default: return tc_launch<32>(a, p, sms, s);
   }
 }
 

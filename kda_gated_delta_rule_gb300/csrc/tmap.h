@@ -54,19 +54,17 @@ inline bool encode_token_map_sw128(CUtensorMap* map, const void* base, long long
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// [rows][128] cache rows, bf16 or 8-bit codes; box = box_rows rows x 128 bytes (all of an 8-bit row, half of a bf16 one)
-// with the 128-byte swizzle, as above.
-inline bool encode_cache_map(CUtensorMap* map, const void* base, bool e4m3, long long rows, int box_rows) {
+// [rows][128] bf16 cache rows; box = box_rows rows x 64 channels with the 128-byte swizzle, as above.
+inline bool encode_cache_map(CUtensorMap* map, const void* base, long long rows, int box_rows) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
   if (!enc) return false;
-  const cuuint64_t es = e4m3 ? 1 : 2, D = 128;
-  const cuuint64_t dims[2] = {D, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {D * es};
-  const cuuint32_t box[2] = {(cuuint32_t)(128 / es), (cuuint32_t)box_rows};
+  const cuuint64_t dims[2] = {128, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {256};
+  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
   const cuuint32_t estr[2] = {1, 1};
-  return enc(map, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base),
-             dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace kda
