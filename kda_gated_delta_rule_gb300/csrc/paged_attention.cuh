@@ -377,14 +377,21 @@ __global__ void __launch_bounds__(PA_NT, pa_resident(NT)) paged_attention_kernel
     Piece<C::VC * C::ES> v[GPI][4][C::VL];
     float ks[GPI][2], vs[GPI][2];
 
-    // Loads of one group whose first token is tok0, without branches: past the request's end its last token is read
-    // again, and a group that is not there reads the pool's first rows (both unseen).
+    // Loads of one group whose first token is tok0.  Past the request's end the last token is read again (unseen).
     auto load_k = [&](int q, int64_t row, int tok0) {
-      const int over = row < 0 ? 15 : span.len - 1 - tok0;
-      const int64_t first = row < 0 ? 0 : row;
+      if (row < 0) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+          for (int u = 0; u < C::KL; ++u) k[q][i][u].clear();
+          ks[q][i] = vs[q][i] = 0.f;
+        }
+        return;
+      }
+      const int over = span.len - 1 - tok0;  // last token there is, within the group
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int64_t r = first + min(n + 8 * i, over);
+        const int64_t r = row + min(n + 8 * i, over);
         const uint8_t* at_k = static_cast<const uint8_t*>(a.c.k_pages) + r * C::RS + j * (C::KC * C::ES);
 #pragma unroll
         for (int u = 0; u < C::KL; ++u) k[q][i][u].load(at_k + u * (4 * C::KC * C::ES));
@@ -395,11 +402,17 @@ __global__ void __launch_bounds__(PA_NT, pa_resident(NT)) paged_attention_kernel
       }
     };
     auto load_v = [&](int q, int64_t row, int tok0) {
-      const int over = row < 0 ? 15 : span.len - 1 - tok0;
-      const int64_t first = row < 0 ? 0 : row;
+      if (row < 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int u = 0; u < C::VL; ++u) v[q][i][u].clear();
+        return;
+      }
+      const int over = span.len - 1 - tok0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int64_t r = first + min(2 * j + (i & 1) + 8 * (i >> 1), over);
+        const int64_t r = row + min(2 * j + (i & 1) + 8 * (i >> 1), over);
         const uint8_t* at_v = static_cast<const uint8_t*>(a.c.v_pages) + r * C::RS + n * (C::VC * C::ES);
 #pragma unroll
         for (int u = 0; u < C::VL; ++u) v[q][i][u].load(at_v + u * (8 * C::VC * C::ES));
