@@ -789,40 +789,72 @@ def _call(name, *args):
         raise KdaError(name, code)
 
 
-def _qk_norm_args(q, k, q_weight, k_weight, q_out, k_out, out_names, cos, sin, positions, eps, interleaved, dev_status,
-                  grads=(), weight_grads=()):
+# The checks of these calls are written twice: one expression that the usual call passes (a call of one token spends
+# most of its time here), and behind it the checks one by one, which name what is wrong.
+
+def _qk_norm_checks(q, k, q_weight, k_weight, q_out, k_out, out_names, cos, sin, positions, dev_status, grads,
+                    weight_grads):
     T, Hq, d = _rank("q", q, 3)
     _need("q", q, q.shape, _IN)
-    dtype = (q.dtype,)
-    _need("k", k, (T, k.shape[1] if k.dim() == 3 else None, d), dtype)
-    Hkv = k.shape[1]
+    _need("k", k, (T, k.shape[1] if k.dim() == 3 else None, d), (q.dtype,))
     _need("q_weight", q_weight, (d,), _FP)
     _need("k_weight", k_weight, (d,), _FP)
     _need(out_names[0], q_out, q.shape, _IN)
     _need(out_names[1], k_out, k.shape, (q_out.dtype,))
-    n = rot = 0
     if cos is not None or sin is not None or positions is not None:
         if cos is None or sin is None or positions is None:
             raise ValueError("cos, sin and positions go together (all None: no rotation)")
-        n, half = _rank("cos", cos, 2)
-        rot = 2 * half
+        half = _rank("cos", cos, 2)[1]
         _need("cos", cos, cos.shape, _FP)
         _need("sin", sin, cos.shape, _FP)
         _need("positions", positions, (T,), _I32)
-        if rot > d or rot % 16:
+        if 2 * half > d or half % 8:
             raise ValueError(f"cos: expected angles of a multiple of 8 channel pairs within d = {d}, got {half}")
     if grads:
-        d_q_out, d_k_out = grads
-        _need("d_q_out", d_q_out, q.shape, _IN)
-        _need("d_k_out", d_k_out, k.shape, (d_q_out.dtype,))
+        _need("d_q_out", grads[0], q.shape, _IN)
+        _need("d_k_out", grads[1], k.shape, (grads[0].dtype,))
         _need("dq_weight", weight_grads[0], (d,), _FP)
         _need("dk_weight", weight_grads[1], (d,), _FP)
     _need_status(dev_status)
     _check(q_weight, k_weight, dev_status, cos, sin, positions, *grads, *weight_grads)
-    return _pack_norm(q.data_ptr(), k.data_ptr(), _row_stride("q", q), _row_stride("k", k), _dt(q),
+
+
+def _qk_norm_args(q, k, q_weight, k_weight, q_out, k_out, out_names, cos, sin, positions, eps, interleaved, dev_status,
+                  grads=(), weight_grads=()):
+    shape, k_shape, dtype, out_dtype, f32 = q.shape, k.shape, q.dtype, q_out.dtype, torch.float32
+    w_shape, in_code, out_code = shape[2:], _DTYPE_CODES.get(dtype), _DTYPE_CODES.get(out_dtype)
+    n = rot = 0
+    usual = (len(shape) == 3 and len(k_shape) == 3 and k_shape[0] == shape[0] and k_shape[2] == shape[2]
+             and k.dtype is dtype and in_code is not None and out_code is not None and k_out.dtype is out_dtype
+             and q_out.shape == shape and k_out.shape == k_shape and q_weight.shape == w_shape
+             and k_weight.shape == w_shape and q_weight.dtype is f32 and k_weight.dtype is f32 and q_weight.is_cuda
+             and k_weight.is_cuda and q_weight.is_contiguous() and k_weight.is_contiguous() and dev_status is None)
+    if grads and usual:
+        (d_q, d_k), (w_q, w_k) = grads, weight_grads
+        usual = (d_q.shape == shape and d_k.shape == k_shape and d_q.dtype in _DTYPE_CODES and d_k.dtype is d_q.dtype
+                 and w_q.shape == w_shape and w_k.shape == w_shape and w_q.dtype is f32 and w_k.dtype is f32
+                 and d_q.is_cuda and d_k.is_cuda and w_q.is_cuda and w_k.is_cuda and d_q.is_contiguous()
+                 and d_k.is_contiguous() and w_q.is_contiguous() and w_k.is_contiguous())
+    if cos is not None and usual and sin is not None and positions is not None:
+        c_shape = cos.shape
+        usual = (len(c_shape) == 2 and c_shape[1] % 8 == 0 and 2 * c_shape[1] <= shape[2] and sin.shape == c_shape
+                 and cos.dtype is f32 and sin.dtype is f32 and positions.shape == shape[:1]
+                 and positions.dtype is torch.int32 and cos.is_cuda and sin.is_cuda and positions.is_cuda
+                 and cos.is_contiguous() and sin.is_contiguous() and positions.is_contiguous())
+    elif cos is not None or sin is not None or positions is not None:
+        usual = False
+    if not usual:
+        _qk_norm_checks(q, k, q_weight, k_weight, q_out, k_out, out_names, cos, sin, positions, dev_status, grads,
+                        weight_grads)
+    if cos is not None:
+        n, rot = cos.shape
+        rot *= 2
+    T, Hq, d = shape
+    Hkv = k_shape[1]
+    return _pack_norm(q.data_ptr(), k.data_ptr(), _row_stride("q", q), _row_stride("k", k), in_code,
                       q_weight.data_ptr(), k_weight.data_ptr(), _ptr(cos), _ptr(sin), _ptr(positions), n, rot,
                       bool(interleaved), eps, T, Hq, Hkv, d, q_out.data_ptr(), k_out.data_ptr(),
-                      _row_stride(out_names[0], q_out), _row_stride(out_names[1], k_out), _dt(q_out), _ptr(dev_status))
+                      _row_stride(out_names[0], q_out), _row_stride(out_names[1], k_out), out_code, _ptr(dev_status))
 
 
 def kda_qk_norm_rope(q, k, q_weight, k_weight, q_out, k_out, cos=None, sin=None, positions=None, eps=1e-6,
@@ -859,22 +891,28 @@ def kda_qk_norm_rope_backward(d_q_out, d_k_out, q, k, q_weight, k_weight, dq, dk
 
 def _kv_cache(k_pages, v_pages, k_scales, v_scales):
     """The fields of kda_kv_cache."""
-    shape = k_pages.shape
-    kind = _CACHE_TYPES.get(k_pages.dtype)
-    if kind is None:
-        raise TypeError(f"k_pages: expected dtype torch.bfloat16 or torch.float8_e4m3fn, got {k_pages.dtype}")
-    _need("v_pages", v_pages, shape, (k_pages.dtype,))
+    shape, dtype = k_pages.shape, k_pages.dtype
+    kind = _CACHE_TYPES.get(dtype)
+    if not (kind is not None and v_pages.shape == shape and v_pages.dtype is dtype and shape[2] > 0 and shape[2] % 16 == 0
+            and k_pages.is_cuda and v_pages.is_cuda and k_pages.is_contiguous() and v_pages.is_contiguous()
+            and (k_scales is None and v_scales is None if kind == 0 else
+                 k_scales is not None and v_scales is not None and k_scales.shape == shape[:3] == v_scales.shape
+                 and k_scales.dtype is torch.float32 and v_scales.dtype is torch.float32 and k_scales.is_cuda
+                 and v_scales.is_cuda and k_scales.is_contiguous() and v_scales.is_contiguous())):
+        if kind is None:
+            raise TypeError(f"k_pages: expected dtype torch.bfloat16 or torch.float8_e4m3fn, got {dtype}")
+        _need("v_pages", v_pages, shape, (dtype,))
+        if shape[2] <= 0 or shape[2] % 16:
+            raise ValueError(f"k_pages: expected pages of a positive multiple of 16 tokens, got {shape[2]}")
+        if kind == 1:
+            if k_scales is None or v_scales is None:
+                raise ValueError("k_scales and v_scales: an e4m3 cache needs both")
+            _need("k_scales", k_scales, shape[:3], _FP)
+            _need("v_scales", v_scales, shape[:3], _FP)
+        elif k_scales is not None or v_scales is not None:
+            raise ValueError("k_scales and v_scales: a bfloat16 cache has none")
+        _check(k_pages, v_pages, k_scales, v_scales)
     pages, Hkv, page_size, d = shape
-    if page_size <= 0 or page_size % 16:
-        raise ValueError(f"k_pages: expected pages of a positive multiple of 16 tokens, got {page_size}")
-    if kind == 1:
-        if k_scales is None or v_scales is None:
-            raise ValueError("k_scales and v_scales: an e4m3 cache needs both")
-        _need("k_scales", k_scales, shape[:3], _FP)
-        _need("v_scales", v_scales, shape[:3], _FP)
-    elif k_scales is not None or v_scales is not None:
-        raise ValueError("k_scales and v_scales: a bfloat16 cache has none")
-    _check(k_pages, v_pages, k_scales, v_scales)
     return (k_pages.data_ptr(), v_pages.data_ptr(), _ptr(k_scales), _ptr(v_scales), kind, pages, page_size, Hkv, d)
 
 
@@ -882,29 +920,42 @@ def kda_kv_write(k, v, k_pages, v_pages, slots, k_scales=None, v_scales=None, de
     """Token t of k, v [T, Hkv, d] goes to cache slot slots[t] = page * page_size + offset (int64, distinct; negative:
     skipped).  k_pages, v_pages [pages, Hkv, page_size, d] bfloat16, or float8_e4m3fn with k_scales, v_scales
     [pages, Hkv, page_size] fp32: each row quantised with a power-of-two scale of its own."""
-    T = _rank("k", k, 3)[0]
-    _, Hkv, _, d = _rank("k_pages", k_pages, 4)
-    _need("k", k, (T, Hkv, d), _IN)
-    _need("v", v, k.shape, (k.dtype,))
-    _need("slots", slots, (T,), _I64)
-    _need_status(dev_status)
+    shape, page_shape = k.shape, k_pages.shape
+    code = _DTYPE_CODES.get(k.dtype)
+    if not (len(shape) == 3 and len(page_shape) == 4 and shape[1] == page_shape[1] and shape[2] == page_shape[3]
+            and code is not None and v.shape == shape and v.dtype is k.dtype and slots.shape == shape[:1]
+            and slots.dtype is torch.int64 and slots.is_cuda and slots.is_contiguous() and dev_status is None):
+        T = _rank("k", k, 3)[0]
+        _, Hkv, _, d = _rank("k_pages", k_pages, 4)
+        _need("k", k, (T, Hkv, d), _IN)
+        _need("v", v, k.shape, (k.dtype,))
+        _need("slots", slots, (T,), _I64)
+        _need_status(dev_status)
+        _kv_cache(k_pages, v_pages, k_scales, v_scales)
+        _check(slots, dev_status)
     c = _pack_cache(*_kv_cache(k_pages, v_pages, k_scales, v_scales))
-    _check(slots, dev_status)
-    _call("kda_kv_write", k.data_ptr(), v.data_ptr(), _row_stride("k", k), _row_stride("v", v), _dt(k), T,
+    _call("kda_kv_write", k.data_ptr(), v.data_ptr(), _row_stride("k", k), _row_stride("v", v), code, shape[0],
           slots.data_ptr(), c, _ptr(dev_status), _stream(stream))
 
 
 def kda_kv_read(k_pages, v_pages, slots, k_out, v_out, k_scales=None, v_scales=None, dev_status=None, stream=None):
     """Token t of k_out, v_out [T, Hkv, d] receives cache slot slots[t] (int64; negative: a zero row)."""
-    _, Hkv, _, d = _rank("k_pages", k_pages, 4)
-    T = _rank("slots", slots, 1)[0]
-    _need("slots", slots, (T,), _I64)
-    _need("k_out", k_out, (T, Hkv, d), _IN)
-    _need("v_out", v_out, k_out.shape, (k_out.dtype,))
-    _need_status(dev_status)
+    shape, page_shape = k_out.shape, k_pages.shape
+    code = _DTYPE_CODES.get(k_out.dtype)
+    if not (len(shape) == 3 and len(page_shape) == 4 and shape[1] == page_shape[1] and shape[2] == page_shape[3]
+            and code is not None and v_out.shape == shape and v_out.dtype is k_out.dtype and slots.shape == shape[:1]
+            and slots.dtype is torch.int64 and slots.is_cuda and k_out.is_cuda and v_out.is_cuda
+            and slots.is_contiguous() and k_out.is_contiguous() and v_out.is_contiguous() and dev_status is None):
+        _, Hkv, _, d = _rank("k_pages", k_pages, 4)
+        T = _rank("slots", slots, 1)[0]
+        _need("slots", slots, (T,), _I64)
+        _need("k_out", k_out, (T, Hkv, d), _IN)
+        _need("v_out", v_out, k_out.shape, (k_out.dtype,))
+        _need_status(dev_status)
+        _kv_cache(k_pages, v_pages, k_scales, v_scales)
+        _check(slots, k_out, v_out, dev_status)
     c = _pack_cache(*_kv_cache(k_pages, v_pages, k_scales, v_scales))
-    _check(slots, k_out, v_out, dev_status)
-    _call("kda_kv_read", c, slots.data_ptr(), T, k_out.data_ptr(), v_out.data_ptr(), _dt(k_out), _ptr(dev_status),
+    _call("kda_kv_read", c, slots.data_ptr(), shape[0], k_out.data_ptr(), v_out.data_ptr(), code, _ptr(dev_status),
           _stream(stream))
 
 
@@ -921,22 +972,34 @@ def kda_paged_attention(q, k_pages, v_pages, block_table, seq_lens, out, workspa
     window > 0: a query sees that many positions, its own included; lse [B, W, Hq] fp32 or None; workspace: at least
     kda_paged_attention_workspace_size(B, W, Hq, Hkv, d) bytes.
     """
-    B, W, Hq, d = _rank("q", q, 4)
-    pages, Hkv, page_size, dc = _rank("k_pages", k_pages, 4)
-    _need("q", q, q.shape, _IN)
-    if dc != d:
-        _need("k_pages", k_pages, (pages, Hkv, page_size, d), (k_pages.dtype,))
-    max_pages = _rank("block_table", block_table, 2)[1]
-    _need("block_table", block_table, (B, max_pages), _I32)
-    _need("seq_lens", seq_lens, (B,), _I32)
-    _need("out", out, q.shape, _IN)
-    _need("lse", lse, q.shape[:3], _FP)
-    if Hkv == 0 or Hq % Hkv:
-        raise ValueError(f"q: expected a multiple of the cache's {Hkv} heads, got {Hq}")
-    _need_status(dev_status)
+    shape, page_shape, table_shape = q.shape, k_pages.shape, block_table.shape
+    code, out_code, i32 = _DTYPE_CODES.get(q.dtype), _DTYPE_CODES.get(out.dtype), torch.int32
+    if not (len(shape) == 4 and len(page_shape) == 4 and shape[3] == page_shape[3] and page_shape[1] > 0
+            and shape[2] % page_shape[1] == 0 and code is not None and out_code is not None and out.shape == shape
+            and len(table_shape) == 2 and table_shape[0] == shape[0] and block_table.dtype is i32
+            and seq_lens.shape == shape[:1] and seq_lens.dtype is i32 and q.is_cuda and out.is_cuda
+            and block_table.is_cuda and seq_lens.is_cuda and workspace.is_cuda and q.is_contiguous()
+            and out.is_contiguous() and block_table.is_contiguous() and seq_lens.is_contiguous()
+            and workspace.is_contiguous() and dev_status is None
+            and (lse is None or (lse.shape == shape[:3] and lse.dtype is torch.float32 and lse.is_cuda
+                                 and lse.is_contiguous()))):
+        B, W, Hq, d = _rank("q", q, 4)
+        pages, Hkv, page_size, dc = _rank("k_pages", k_pages, 4)
+        _need("q", q, q.shape, _IN)
+        if dc != d:
+            _need("k_pages", k_pages, (pages, Hkv, page_size, d), (k_pages.dtype,))
+        _need("block_table", block_table, (B, _rank("block_table", block_table, 2)[1]), _I32)
+        _need("seq_lens", seq_lens, (B,), _I32)
+        _need("out", out, q.shape, _IN)
+        _need("lse", lse, q.shape[:3], _FP)
+        if Hkv == 0 or Hq % Hkv:
+            raise ValueError(f"q: expected a multiple of the cache's {Hkv} heads, got {Hq}")
+        _need_status(dev_status)
+        _kv_cache(k_pages, v_pages, k_scales, v_scales)
+        _check(q, block_table, seq_lens, out, lse, workspace, dev_status)
     c = _kv_cache(k_pages, v_pages, k_scales, v_scales)
-    _check(q, block_table, seq_lens, out, lse, workspace, dev_status)
-    a = _pack_attention(q.data_ptr(), _dt(q), B, W, Hq, *c, block_table.data_ptr(), max_pages, seq_lens.data_ptr(),
-                        d ** -0.5 if scale is None else scale, softcap, window, out.data_ptr(), _dt(out), _ptr(lse),
+    B, W, Hq, d = shape
+    a = _pack_attention(q.data_ptr(), code, B, W, Hq, *c, block_table.data_ptr(), table_shape[1], seq_lens.data_ptr(),
+                        d ** -0.5 if scale is None else scale, softcap, window, out.data_ptr(), out_code, _ptr(lse),
                         workspace.data_ptr(), workspace.numel() * workspace.element_size(), _ptr(dev_status))
     _call("kda_paged_attention", a, _stream(stream))
