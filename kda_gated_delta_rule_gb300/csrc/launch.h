@@ -215,7 +215,7 @@ struct NormArgs {
   int64_t q_out_stride, k_out_stride;
   int32_t* status;
 };
-// CTAs of the backward at most, one row of partial weight gradients each: four per SM
+// Rows of partial weight gradients that a workspace holds, one per CTA of the backward (it launches half as many)
 constexpr int NORM_BWD_CTAS = 608;
 cudaError_t launch_qk_norm_rope(const NormArgs& a, cudaStream_t s);
 // q_out, k_out receive dq, dk; partial: NORM_BWD_CTAS * 2 * d floats

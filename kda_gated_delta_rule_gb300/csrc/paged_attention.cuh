@@ -54,13 +54,7 @@ struct PaMeta {
 
 // 8-row column blocks of a unit, and the CTAs per SM its kernel is built for
 __host__ __device__ constexpr int pa_nt(int rows, bool fine) { return rows <= 8 ? 1 : rows <= 16 || fine ? 2 : 4; }
-#ifndef PAG_
-#define PAG_ 4
-#endif
-#ifndef PAR1_
-#define PAR1_ 3
-#endif
-__host__ __device__ constexpr int pa_resident(int nt) { return nt == 1 ? PAR1_ : 2; }
+__host__ __device__ constexpr int pa_resident(int nt) { return nt == 1 ? 3 : 2; }
 constexpr int PA_SMS = 152;
 
 struct PaPlan {  // derived on the host
@@ -127,7 +121,7 @@ struct Piece {
 #pragma unroll
     for (int i = 0; i < (BYTES < 4 ? 1 : BYTES / 4); ++i) w[i] = 0;
   }
-  // Read once: not kept in L1 (174 us against 180 for one request of 262144 tokens).
+  // Read once: not kept in L1 (one request of 262144 tokens, bf16: 172 to 174 us against 175 to 177).
   __device__ __forceinline__ void load(const uint8_t* p) {
     if constexpr (BYTES == 16) {
       asm("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
@@ -192,7 +186,7 @@ struct PaCfg {
   static constexpr int ES = F8 ? 1 : 2;
   static constexpr int RS = D * ES;                      // bytes of a cached row
   static constexpr int RB = 8 * NT;
-  static constexpr int GPI = F8 && NT < PAG_ ? 2 : 1;       // 16-token groups a warp works on at once
+  static constexpr int GPI = F8 && NT < 4 ? 2 : 1;          // 16-token groups a warp works on at once
   static constexpr int TILE = 16 * GPI;                  // tokens
   static constexpr int KC = D / 4 < 16 / ES ? D / 4 : 16 / ES;  // channels of a key piece
   static constexpr int KL = D / (4 * KC);                // key pieces per lane and token

@@ -10,7 +10,7 @@
 // 8i .. 8i + 7 (neighbouring pairs); either way its four pairs are 4i .. 4i + 3, one 16-byte read of each table, and
 // its eight values are held as four float2, the pairs' lower channels in the first two and the upper ones in the others,
 // so the arithmetic is on two values per instruction.  (With eight consecutive channels per lane the half-split
-// rotation took a shuffle per channel and twice the table bytes: 41 us for 8192 x 40 x 128 bf16 rows; now NORM_FWD_US.)
+// rotation took a shuffle per channel and twice the table bytes: 41 us for 8192 x 40 x 128 bf16 rows; now 30.6, 83 % of the copy rate.)
 // A group of lanes takes R rows of one token and one kind, queries or keys, issues all its loads before the first
 // reduction, reads the angles and the weight once for them, and reduces the rows' sums together.
 #include "launch.h"
