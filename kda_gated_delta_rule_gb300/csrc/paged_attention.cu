@@ -10,6 +10,11 @@ size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 namespace {
 
+// More query rows per cached row than this take the many-rows form: its time hardly grows up to 128 (64 requests of 500 to 6000
+// tokens: 33 to 37 us with bf16, 42 to 45 with e4m3), where the others' grow with the rows (24 rows: 44 and 50 us; 96: 87
+// and 93); at 12 and 16 rows the register form is as fast (32 to 34 us) or faster (29 us).
+constexpr int PA_ROWS_FROM = 16;
+
 // The workspace's places for `workers` warps or CTAs with row blocks of rb.
 size_t lay_out(PaPlan& p, char* w, int workers, int rb, int d) {
   const size_t parts = (size_t)workers * 2 * rb;
@@ -28,6 +33,10 @@ size_t paged_attention_ws_bytes(int W, int Hq, int Hkv, int d) {
   const int rows = W * (Hq / Hkv);
   PaPlan p;
   size_t most = lay_out(p, nullptr, PA_SMS, pa_tc_row_block(rows), d);
+  if (rows > PA_ROWS_FROM) {
+    const size_t n = lay_out(p, nullptr, PA_SMS, PA_ROWS_BLOCK, d);
+    most = n > most ? n : most;
+  }
   for (int fine = 0; fine < 2; ++fine) {
     const int nt = pa_nt(rows, fine != 0);
     const size_t n = lay_out(p, nullptr, PA_SMS * pa_resident(nt) * PA_WARPS, 8 * nt, d);
@@ -43,14 +52,17 @@ cudaError_t launch_paged_attention(const PagedAttnArgs& a, cudaStream_t s) {
   PaPlan p;
   p.G = a.Hq / a.c.Hkv;
   p.rows = a.W * p.G;
-  const int tc_rb = pa_tc_row_block(p.rows), tc_blocks = (p.rows + tc_rb - 1) / tc_rb;
-  // The tensor-memory form is ahead with many query rows per cached row (96 rows: 88 against 119 us; 24: 43 against 57), and
-  // with fewer units than CTAs, where its larger and so fewer parts join faster (one request of 4096 tokens and 8 heads: 15
-  // against 26 us, of 262144: 167 against 175); with many units of few rows their starts and ends cost it more (16 requests
-  // of 4096 tokens, 128 units: 64 against 56 us).
-  if (pa_tc_supported(a) && (p.rows > 16 || (int64_t)a.B * a.c.Hkv * tc_blocks <= 64)) {
-    const int rb = tc_rb;
-    p.blocks = tc_blocks;
+  if (p.rows > PA_ROWS_FROM && pa_rows_supported(a)) {
+    p.blocks = (p.rows + PA_ROWS_BLOCK - 1) / PA_ROWS_BLOCK;
+    lay_out(p, reinterpret_cast<char*>(a.ws), PA_SMS, PA_ROWS_BLOCK, a.c.d);
+    return pa_rows(a, p, sms, s);
+  }
+  // With fewer units than CTAs the tensor-memory form's larger and so fewer parts join faster (one request of 4096 tokens and 8
+  // heads: 15 against 26 us, of 262144: 167 against 175); with many units of few rows their starts and ends cost it
+  // more (16 requests of 4096 tokens, 128 units: 64 against 56 us).
+  if (pa_tc_supported(a) && p.rows <= 16 && (int64_t)a.B * a.c.Hkv <= 64) {
+    const int rb = pa_tc_row_block(p.rows);
+    p.blocks = 1;
     lay_out(p, reinterpret_cast<char*>(a.ws), PA_SMS, rb, a.c.d);
     return pa_tc(a, p, sms, s);
   }

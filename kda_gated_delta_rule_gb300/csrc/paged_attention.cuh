@@ -179,6 +179,28 @@ __device__ __forceinline__ PaSpan pa_span(const PagedAttnArgs& a, int b, bool fl
   return s;
 }
 
+// Sum of `mine` over the threads up to this one, and over all; `sums`: one place per warp.
+template <int NT>
+__device__ __forceinline__ int64_t block_scan(int64_t mine, int64_t* sums, int64_t& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t x = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) sums[warp] = x;
+  __syncthreads();
+  total = 0;
+  int64_t before = 0;
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) {
+    if (w == warp) before = total;
+    total += sums[w];
+  }
+  return x + before;
+}
+
 // ---------------------------------------------------------------- main kernel
 
 template <int D, bool F8, int NT, bool FINE>
@@ -204,7 +226,7 @@ __global__ void __launch_bounds__(PA_NT, pa_resident(NT)) paged_attention_kernel
   using C = PaCfg<D, F8, NT, FINE>;
   constexpr int RB = C::RB, TILE = C::TILE, GPI = C::GPI, KS = C::KS;
   extern __shared__ uint2 q_operands[];  // [warp][part][NT][KS][lane]: Q as the first product takes it
-  __shared__ int64_t scan[PA_NT];
+  __shared__ int64_t sums[PA_WARPS];
   __shared__ int64_t where[PA_WARPS][2];
   pdl_begin();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -217,22 +239,16 @@ __global__ void __launch_bounds__(PA_NT, pa_resident(NT)) paged_attention_kernel
   int64_t mine = 0;
   for (int b = tid * run; b < min(a.B, (tid + 1) * run); ++b)
     mine += pa_span<TILE>(a, b, blockIdx.x == 0).tiles + PA_UNIT_COST;
-  scan[tid] = mine;
-  __syncthreads();
-  for (int o = 1; o < PA_NT; o <<= 1) {
-    const int64_t v = tid >= o ? scan[tid - o] : 0;
-    __syncthreads();
-    scan[tid] += v;
-    __syncthreads();
-  }
-  const int64_t total = scan[PA_NT - 1] * per_b;
+  int64_t total;
+  const int64_t upto = block_scan<PA_NT>(mine, sums, total);
+  total *= per_b;
   const int64_t all = (int64_t)gridDim.x * PA_WARPS, few = (total + PA_SHARE - 1) / PA_SHARE;
   const int64_t workers = few < all ? few : all;
   // the request in which each of this CTA's shares begins, and that request's first position
-  const int64_t before = scan[tid] - mine;
+  const int64_t before = upto - mine;
   for (int w = 0; w < PA_WARPS; ++w) {
     const int64_t x = (int64_t)blockIdx.x * PA_WARPS + w, from = x * total / workers;
-    if (x >= workers || from < before * per_b || from >= scan[tid] * per_b) continue;
+    if (x >= workers || from < before * per_b || from >= upto * per_b) continue;
     int64_t f = before;
     for (int b = tid * run;; ++b) {
       const int t = pa_span<TILE>(a, b, false).tiles + PA_UNIT_COST;
@@ -888,5 +904,8 @@ cudaError_t pa_e4m3_fine(const PagedAttnArgs& a, const PaPlan& p, int sms, cudaS
 bool pa_tc_supported(const PagedAttnArgs& a);
 int pa_tc_row_block(int rows);
 cudaError_t pa_tc(const PagedAttnArgs& a, const PaPlan& p, int sms, cudaStream_t s);
+constexpr int PA_ROWS_BLOCK = 128;  // query rows of a unit of the many-rows form
+bool pa_rows_supported(const PagedAttnArgs& a);
+cudaError_t pa_rows(const PagedAttnArgs& a, const PaPlan& p, int sms, cudaStream_t s);
 
 }  // namespace kda

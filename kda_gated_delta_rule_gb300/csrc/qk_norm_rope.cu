@@ -13,6 +13,7 @@
 // rotation took a shuffle per channel and twice the table bytes: 41 us for 8192 x 40 x 128 bf16 rows; now 30.6, 83 % of the copy rate.)
 // A group of lanes takes R rows of one token and one kind, queries or keys, issues all its loads before the first
 // reduction, reads the angles and the weight once for them, and reduces the rows' sums together.
+#include "f32x2.cuh"
 #include "launch.h"
 #include "rows8.cuh"
 
@@ -20,21 +21,6 @@ namespace kda {
 
 constexpr int NORM_NT = 128, NORM_RESIDENT = 8, NORM_R = 4;
 constexpr int NORM_BWD_NT = 256, NORM_BWD_RESIDENT = 2, NORM_BWD_R = 4;
-
-// ---- arithmetic on two fp32 at once
-__device__ __forceinline__ unsigned long long bits2(float2 a) { return *reinterpret_cast<unsigned long long*>(&a); }
-__device__ __forceinline__ float2 pair2(unsigned long long b) { return *reinterpret_cast<float2*>(&b); }
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  unsigned long long r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
-  return pair2(r);
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  unsigned long long r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
-  return pair2(r);
-}
-__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
 // A lane's channels, and its four pairs.
 struct NormLane {
