@@ -10,7 +10,8 @@
 //              codes become fp16 (exact);
 //   warps 4 to 11   softmax: two groups of four, each with 64 of a tile's tokens and an accumulator of its own, so that they
 //              meet only at a unit's end; two score buffers, so that the next tile's product runs under a tile's softmax;
-//   warps 12 and 13   issue the two products.
+//   warps 12 and 13   issue the two products;
+//   warps 14 and 15   put the next unit's queries into operand order.
 //
 // Bound by the softmax warps.  A tile's 128 x 128 scores are 128 exponentials a lane and scheduler, 1024 cycles of their unit,
 // and with cap and scales about 20 more operations each; measured, a tile takes 3500 cycles (bf16) to 6000 (e4m3 with
@@ -29,7 +30,7 @@ namespace kda {
 namespace {
 
 constexpr int RW_RB = PA_ROWS_BLOCK;
-constexpr int RW_SOFT0 = 128, RW_SOFT = 256, RW_NT = RW_SOFT0 + RW_SOFT + 64;
+constexpr int RW_SOFT0 = 128, RW_SOFT = 256, RW_NT = RW_SOFT0 + RW_SOFT + 128;
 constexpr int RW_RING = 2;                        // slots of K and of V
 constexpr int RW_INFO = 4;                        // tiles whose scales and tokens are kept: twice the ring
 constexpr int RW_SLOT = TC_TILE * TC_D * 2;       // bytes of a K, V or Q tile: two blocks of 64 channels
@@ -38,22 +39,25 @@ constexpr int RW_O = 256, RW_TMEM = 512;          // columns: two score buffers,
 
 struct RwShared {
   // Every barrier is waited on only by roles that see each of its rounds: a parity tells rounds apart no further.
-  uint64_t k_full[RW_RING], k_empty[RW_RING], v_full[RW_RING], v_empty[RW_RING];
-  uint64_t s_full[2], p_full[2], p_free[2], q_full, o_full, drain[2];
+  uint64_t k_full[RW_RING], k_empty[RW_RING], v_full[RW_RING], v_ready[RW_RING], v_empty[RW_RING];
+  uint64_t s_full[2], p_full[2], p_free[2], q_full[2], q_free[2], o_full, drain[2];
+  TcUnit unit[2];  // what the query warps walk to; t1 = 0 ends the share
   // by tile: which tokens there are, and their scales; lift is about log2 of the value's
-  uint32_t there[RW_INFO][4];
+  alignas(16) uint32_t there[RW_INFO][4];
   alignas(16) float k_scale[RW_INFO][TC_TILE], v_scale[RW_INFO][TC_TILE], lift[RW_INFO][TC_TILE];
   float lift_top[RW_INFO][4];  // largest lift of 32 tokens
   float2 ml[2][RW_RB];
-  float factor[RW_RB];  // per query row: score in powers of two per unit of the product
-  int head[RW_RB];      // place among the request's W x Hq output rows, -1 past the unit's rows
+  // per query row of a unit: score in powers of two per unit of the product, last seen position, and place among the
+  // request's W x Hq output rows (-1 past the unit's)
+  float factor[2][RW_RB];
+  int last[2][RW_RB], head[2][RW_RB];
   uint32_t nan[2][4];
   int64_t sums[RW_NT / 32];
   int64_t where[2];
   uint32_t tmem;
   int dead;
 };
-constexpr int RW_SMEM = 1024 + (2 * RW_RING + 1) * RW_SLOT + (int)sizeof(RwShared);
+constexpr int RW_SMEM = 1024 + (2 * RW_RING + 2) * RW_SLOT + (int)sizeof(RwShared);
 static_assert(RW_SMEM <= 227 * 1024, "shared memory of one SM");
 
 __host__ __device__ constexpr uint32_t rw_idesc(bool f8) {  // 128 x 128, fp16 or bf16 operands
@@ -135,7 +139,7 @@ __global__ void __launch_bounds__(RW_NT, 1)
   unsigned char* kslots = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   unsigned char* vslots = kslots + RW_RING * RW_SLOT;
   unsigned char* qbuf = vslots + RW_RING * RW_SLOT;
-  RwShared& sh = *reinterpret_cast<RwShared*>(qbuf + RW_SLOT);
+  RwShared& sh = *reinterpret_cast<RwShared*>(qbuf + 2 * RW_SLOT);
   pdl_begin();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int Hkv = a.c.Hkv, per_b = Hkv * p.blocks;
@@ -143,13 +147,13 @@ __global__ void __launch_bounds__(RW_NT, 1)
   if (tid == 0) {
     for (int i = 0; i < RW_RING; ++i) {
       tc::bar_init(&sh.k_full[i], F8 ? 4 : 1), tc::bar_init(&sh.k_empty[i], 1);
-      tc::bar_init(&sh.v_full[i], F8 ? 4 : 1), tc::bar_init(&sh.v_empty[i], 1);
+      tc::bar_init(&sh.v_full[i], F8 ? 4 : 1), tc::bar_init(&sh.v_ready[i], 3), tc::bar_init(&sh.v_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       tc::bar_init(&sh.s_full[i], 2), tc::bar_init(&sh.p_full[i], 8), tc::bar_init(&sh.p_free[i], 1);
       tc::bar_init(&sh.drain[i], 1);
+      tc::bar_init(&sh.q_full[i], 2), tc::bar_init(&sh.q_free[i], 8);
     }
-    tc::bar_init(&sh.q_full, 8);
     tc::bar_init(&sh.o_full, 1);
     tc::bar_fence_init();
     sh.dead = 0;
@@ -303,6 +307,7 @@ __global__ void __launch_bounds__(RW_NT, 1)
           if (there) row = (page * Hkv + it.u.h) * a.c.page_size + off;
           else flag_status(a.status, KDA_DEV_PAGE_OOB);
         }
+        const int left = (int)min((int64_t)TC_TILE, (int64_t)it.u.len - it.u.start - (int64_t)it.tile * TC_TILE);
         more = it.next(a, p, box);
         if (more) look_up();
         const unsigned mask = __ballot_sync(0xffffffffu, there);
@@ -312,6 +317,8 @@ __global__ void __launch_bounds__(RW_NT, 1)
           uint32_t w = 0;
           for (int s = 0; s < 2; ++s)
             if (mask >> ((lane * 32 + s * 16) / box) & 1) w |= 0xffffu << (16 * s);
+          const int n = left - lane * 32;  // of the request's tokens
+          if (n < 32) w &= n <= 0 ? 0u : (1u << n) - 1;
           sh.there[info.at][lane] = w;
         }
         __syncwarp();
@@ -343,174 +350,190 @@ __global__ void __launch_bounds__(RW_NT, 1)
         ring.step();
         info.step();
       }
+    } else {
+      // ---- bf16: what lies in a V slot for tokens that are not there must not be a NaN
+      for (; it.next(a, p, box); ring.step(), info.step()) {
+        ok = ok && tc_wait(&sh.v_full[ring.at], ring.parity, &sh.dead);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint4 there = *reinterpret_cast<const uint4*>(sh.there[info.at]);
+        if ((there.x & there.y & there.z & there.w) != 0xffffffffu) {
+          // two threads a row: the first 64 channels and the others
+          for (int i = tid - 32; i < 2 * TC_TILE; i += 96) {
+            const int t = i >> 1;
+            if (sh.there[info.at][t >> 5] >> (t & 31) & 1) continue;
+            uint4* vrow = reinterpret_cast<uint4*>(vslots + ring.at * RW_SLOT + (i & 1) * RW_BLOCK + t * 128);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) vrow[j] = make_uint4(0, 0, 0, 0);
+          }
+          tc::fence_proxy_async();
+        }
+        __syncwarp();
+        if (lane == 0) tc::bar_arrive(&sh.v_ready[ring.at]);
+      }
+      if (!ok && lane == 0) flag_status(a.status, KDA_DEV_TIMEOUT);
     }
   } else if (warp == 12 || warp == 13) {
     // ---- products, one thread each
-    bool ok = true;
-    TcTiles it(walk);
-    TcRing<2> buf;
-    TcRing<RW_RING> ring;
-    constexpr uint32_t id = rw_idesc(F8);
-    if (warp == 12) {
-      if (lane == 0) {
-        const uint64_t k0 = tc::sdesc(tc::smem_u32(kslots)), q0 = tc::sdesc(tc::smem_u32(qbuf));
-        while (it.next(a, p, box)) {
-          if (it.first()) ok = ok && tc_wait(&sh.q_full, it.unit_no & 1, &sh.dead);
-          ok = ok && tc_wait(&sh.p_free[buf.at], buf.parity ^ 1, &sh.dead);
-          ok = ok && tc_wait(&sh.k_full[ring.at], ring.parity, &sh.dead);
-          if (!ok) break;
-          tc::bar_arrive(&sh.s_full[buf.at]);  // hands on what came with K: the tokens and scales
-          tc::fence_after_sync();
-          const uint64_t kd = k0 + ring.at * (RW_SLOT / 16);
+    if (lane == 0) {
+      bool ok = true;
+      TcRing<2> buf;
+      TcRing<RW_RING> ring;
+      constexpr uint32_t id = rw_idesc(F8);
+      const uint64_t k0 = tc::sdesc(tc::smem_u32(kslots)), q0 = tc::sdesc(tc::smem_u32(qbuf));
+      const uint64_t v0 = tc::sdesc_mn(tc::smem_u32(vslots), RW_BLOCK);
+      for (int un = 0; ok; ++un) {
+        ok = tc_wait(&sh.q_full[un & 1], un >> 1 & 1, &sh.dead);
+        if (!ok) break;
+        const int t0 = sh.unit[un & 1].t0, t1 = sh.unit[un & 1].t1;
+        if (t1 == 0) break;
+        for (int t = t0; t < t1; ++t) {
+          if (warp == 12) {
+            ok = ok && tc_wait(&sh.p_free[buf.at], buf.parity ^ 1, &sh.dead);
+            ok = ok && tc_wait(&sh.k_full[ring.at], ring.parity, &sh.dead);
+            if (!ok) break;
+            tc::bar_arrive(&sh.s_full[buf.at]);  // hands on what came with K: the tokens and scales
+            tc::fence_after_sync();
+            const uint64_t kd = k0 + ring.at * (RW_SLOT / 16), qd = q0 + (un & 1) * (RW_SLOT / 16);
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {  // 16 channels per step
-            const uint32_t at = (kk / 4 * RW_BLOCK + kk % 4 * 32) / 16;
-            tc::mma_ss(tmem + buf.at * 128, q0 + at, kd + at, id, kk > 0);
+            for (int kk = 0; kk < 8; ++kk) {  // 16 channels per step
+              const uint32_t at = (kk / 4 * RW_BLOCK + kk % 4 * 32) / 16;
+              tc::mma_ss(tmem + buf.at * 128, qd + at, kd + at, id, kk > 0);
+            }
+            tc::commit(&sh.s_full[buf.at]);
+            tc::commit(&sh.k_empty[ring.at]);
+          } else {
+            ok = ok && tc_wait(F8 ? &sh.v_full[ring.at] : &sh.v_ready[ring.at], ring.parity, &sh.dead);
+            ok = ok && tc_wait(&sh.p_full[buf.at], buf.parity, &sh.dead);
+            if (!ok) break;
+            tc::fence_after_sync();
+            const uint64_t vd = v0 + ring.at * (RW_SLOT / 16);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) {  // 16 tokens per step; the first four are group 0's
+              const uint32_t d = tmem + RW_O + kk / 4 * 128, at = tmem + buf.at * 128 + kk / 2 * 32 + kk % 2 * 8;
+              const uint64_t db = vd + kk * (2048 / 16);
+              tc::mma_ts(d, at, db, id | tc::IDESC_B_MN, !(t == t0 && kk % 4 == 0));
+              if constexpr (!F8) tc::mma_ts(d, at + 16, db, id | tc::IDESC_B_MN, 1);
+            }
+            tc::commit(&sh.p_free[buf.at]);
+            tc::commit(&sh.v_empty[ring.at]);
+            if (t + 1 == t1) tc::commit(&sh.o_full);
           }
-          tc::commit(&sh.s_full[buf.at]);
-          tc::commit(&sh.k_empty[ring.at]);
           ring.step();
           buf.step();
         }
       }
-    } else {
-      const uint64_t v0 = tc::sdesc_mn(tc::smem_u32(vslots), RW_BLOCK);
-      TcRing<RW_INFO> info;
-      while (it.next(a, p, box)) {
-        ok = ok && tc_wait(&sh.v_full[ring.at], ring.parity, &sh.dead);
-        // also before the list of tokens is read: it came with K, which the scores came from
-        ok = ok && tc_wait(&sh.p_full[buf.at], buf.parity, &sh.dead);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        if constexpr (!F8) {
-          const int64_t left = (int64_t)it.u.len - it.u.start - (int64_t)it.tile * TC_TILE;  // tokens from the tile's first on
-          const uint32_t(&there)[4] = sh.there[info.at];
-          if (left < TC_TILE || (there[0] & there[1] & there[2] & there[3]) != 0xffffffffu) {
-            // what lies in the slot for tokens that are not there must not be a NaN
-            for (int t = lane; t < TC_TILE; t += 32)
-              if (t >= left || !(there[t >> 5] >> (t & 31) & 1)) {
-                unsigned char* vrow = vslots + ring.at * RW_SLOT + t * 128;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  reinterpret_cast<uint4*>(vrow)[i] = make_uint4(0, 0, 0, 0);
-                  reinterpret_cast<uint4*>(vrow + RW_BLOCK)[i] = make_uint4(0, 0, 0, 0);
-                }
-              }
-            tc::fence_proxy_async();
-            __syncwarp();
-          }
-        }
-        if (lane == 0) {
-          tc::fence_after_sync();
-          const uint64_t vd = v0 + ring.at * (RW_SLOT / 16);
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {  // 16 tokens per step; the first four are group 0's
-            const uint32_t d = tmem + RW_O + kk / 4 * 128, at = tmem + buf.at * 128 + kk / 2 * 32 + kk % 2 * 8;
-            const uint64_t db = vd + kk * (2048 / 16);
-            tc::mma_ts(d, at, db, id | tc::IDESC_B_MN, !(it.first() && kk % 4 == 0));
-            if constexpr (!F8) tc::mma_ts(d, at + 16, db, id | tc::IDESC_B_MN, 1);
-          }
-          tc::commit(&sh.p_free[buf.at]);
-          tc::commit(&sh.v_empty[ring.at]);
-          if (it.last()) tc::commit(&sh.o_full);
-        }
-        ring.step();
-        buf.step();
-        info.step();
-      }
-    }
-    if (lane == 0) {  // nothing of this thread's is on its way when the CTA ends
+      // nothing of this thread's is on its way when the CTA ends
       if (!ok) flag_status(a.status, KDA_DEV_TIMEOUT);
       uint64_t* drain = &sh.drain[warp - 12];
       tc::commit(drain);
       tc::bar_wait(drain, 0);
     }
     __syncwarp();
-  } else {
-    // ---- softmax: thread = query row; group g has tokens 64 g .. 64 g + 63 of each tile.  A role that gives up a wait goes
-    // on through its tiles without results (no later wait holds it), so that the barriers between groups are always met.
-    const int tk = (tid - RW_SOFT0) & 127, quarter = warp & 3, g = (warp - 4) >> 2;
-    const uint32_t lanes = (uint32_t)(quarter * 32) << 16, own_o = tmem + RW_O + g * 128 + lanes;
-    const float cap2 = a.softcap * PA_LOG2E;
-    const CapPoly cap_poly(cap2);
-    float m = TC_NONE, l = 0.f, factor = 0.f;
-    int last = -1, nrows = 0, all_to = 0;
-    int64_t all_from = 0;
-    bool active = false, bad = false;
-    TcTiles it(walk);
-    TcRing<2> buf, before(1);  // this tile's buffer, and that of the tile before
-    before.parity = 1;
-    TcRing<RW_INFO> info;
-    PaMeta meta{-1, 0};
-    int rows_done = 0;
-    for (; it.next(a, p, box); buf.step(), before.step(), info.step()) {
-      const TcUnit& u = it.u;
-      if (it.first()) {
-        // ---- the unit's queries to operand order: 16 rows a warp, two at a time
-        const int row0 = u.rb * RW_RB;
-        nrows = min(RW_RB, p.rows - row0);
-        active = quarter * 32 < nrows;
-        const int wt = (row0 + tk) / p.G;
-        last = tk < nrows ? u.len - a.W + wt : -1;
-        // tokens that every row of the unit sees
-        all_to = u.len - a.W + row0 / p.G;
-        all_from = (int64_t)u.len - a.W + (row0 + nrows - 1) / p.G - window + 1;
-        if (g == 0) sh.head[tk] = tk < nrows ? wt * a.Hq + u.h * p.G + (row0 + tk - wt * p.G) : -1;
-        tc::named_bar(1, RW_SOFT);
-        uint4 x[8];
-        const int r0 = (warp - 4) * 16 + (lane >> 4), c = lane & 15;
+  } else if (warp >= 14) {
+    // ---- each unit for the others, and its queries: 16 lanes a row, all rows on their way at once
+    TcWalk w = walk;
+    TcUnit u;
+    bool ok = true, more = true;
+    const int c = lane & 15;
+    const float per_unit = a.scale * (a.softcap > 0.f ? 2.f * PA_LOG2E / a.softcap : PA_LOG2E);
+    for (int un = 0; more; ++un) {
+      const int buf = un & 1;
+      more = next_unit(a, p, box, w, u);
+      if (un >= 2) ok = tc_wait(&sh.q_free[buf], ((un >> 1) - 1) & 1, &sh.dead);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      if (more) {
+        const int row0 = u.rb * RW_RB, nrows = min(RW_RB, p.rows - row0), rows32 = (nrows + 31) & ~31;
         const uint4* q = static_cast<const uint4*>(a.q) + (int64_t)u.b * a.W * a.Hq * 16 + c;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int hd = sh.head[r0 + 2 * i];
-          x[i] = hd >= 0 ? __ldg(q + (int64_t)hd * 16) : make_uint4(0, 0, 0, 0);
+        const uint32_t q_at = tc::smem_u32(qbuf + buf * RW_SLOT) + (c >> 3) * RW_BLOCK;
+        const int r0 = (warp - 14) * 2 + (lane >> 4);
+#pragma unroll 4
+        for (int r = r0; r < rows32; r += 4) {
+          const int wt = (row0 + r) / p.G, hd = r < nrows ? wt * a.Hq + u.h * p.G + (row0 + r - wt * p.G) : -1;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(q_at + tc::sw128_chunk(r, c & 7)),
+                       "l"(q + (int64_t)max(hd, 0) * 16), "r"(hd >= 0 ? 16 : 0)
+                       : "memory");
+          if (c == 0) {
+            sh.head[buf][r] = hd;
+            sh.last[buf][r] = hd >= 0 ? u.len - a.W + wt : -1;
+            if constexpr (!F8) sh.factor[buf][r] = per_unit;
+          }
         }
-        const float per_unit = a.scale * (a.softcap > 0.f ? 2.f * PA_LOG2E / a.softcap : PA_LOG2E);
-        const uint32_t q_at = tc::smem_u32(qbuf) + (c >> 3) * RW_BLOCK;
+        if (warp == 14 && lane == 0) sh.unit[buf] = u;
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        if constexpr (F8) {  // fp16: each row's maximum to [2^14, 2^15) by a power of two, exact down to 2^-31 of it
+#pragma unroll 2
+          for (int r = r0; r < rows32; r += 4) {
+            const uint32_t at = q_at + tc::sw128_chunk(r, c & 7);  // what this thread copied
+            uint32_t w4[4], top = 0;
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w4[0]), "=r"(w4[1]), "=r"(w4[2]), "=r"(w4[3])
+                         : "r"(at)
+                         : "memory");
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = r0 + 2 * i;
-          uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-          float down = 1.f;
-          if constexpr (F8) {  // fp16: the row's maximum to [2^14, 2^15) by a power of two, exact down to 2^-31 of it
-            uint32_t top = 0;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) top = max(top, max((w[j] & 0x7fffu) << 16, w[j] & 0x7fff0000u));
+            for (int j = 0; j < 4; ++j) top = max(top, max((w4[j] & 0x7fffu) << 16, w4[j] & 0x7fff0000u));
 #pragma unroll
             for (int j = 1; j < 16; j <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, j));
             int e = top > 0 && top <= 0x7f800000u ? 14 - ((int)(top >> 23) - 127) : 0;
             e = max(-100, min(100, e));
             const float up = __uint_as_float((uint32_t)(e + 127) << 23);
-            down = __uint_as_float((uint32_t)(127 - e) << 23);
+            if (c == 0) sh.factor[buf][r] = per_unit * __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const __half2 h = __floats2half2_rn(__uint_as_float(w[j] << 16) * up, __uint_as_float(w[j] & 0xffff0000u) * up);
-              w[j] = *reinterpret_cast<const uint32_t*>(&h);
-            }
+            for (int j = 0; j < 4; ++j)
+              w4[j] = pack_f16(make_float2(__uint_as_float(w4[j] << 16) * up, __uint_as_float(w4[j] & 0xffff0000u) * up));
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w4[0]), "r"(w4[1]), "r"(w4[2]), "r"(w4[3])
+                         : "memory");
           }
-          if (c == 0) sh.factor[r] = per_unit * down;
-          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(q_at + tc::sw128_chunk(r, c & 7)), "r"(w[0]),
-                       "r"(w[1]), "r"(w[2]), "r"(w[3])
-                       : "memory");
         }
         tc::fence_proxy_async();
-        tc::fence_before_sync();  // the accumulators of the unit before have been read
-        __syncwarp();
-        if (lane == 0) tc::bar_arrive(&sh.q_full);
-        m = TC_NONE;
-        l = 0.f;
-        tc::named_bar(1, RW_SOFT);
-        factor = sh.factor[tk];
+      } else if (warp == 14 && lane == 0) {
+        sh.unit[buf].t1 = 0;
       }
+      __syncwarp();
+      if (lane == 0) tc::bar_arrive(&sh.q_full[buf]);
+    }
+    if (!ok && lane == 0) flag_status(a.status, KDA_DEV_TIMEOUT);
+  } else {
+    // ---- softmax: thread = query row; group g has tokens 64 g .. 64 g + 63 of each tile.  A role that gives up a wait goes
+    // on through its unit without results (no later wait holds it), so that the barriers between groups are always met.
+    const int tk = (tid - RW_SOFT0) & 127, quarter = warp & 3, g = (warp - 4) >> 2;
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16, own_o = tmem + RW_O + g * 128 + lanes;
+    const float cap2 = a.softcap * PA_LOG2E;
+    const CapPoly cap_poly(cap2);
+    bool bad = false;
+    TcRing<2> buf, before(1);  // this tile's buffer, and that of the tile before
+    before.parity = 1;
+    TcRing<RW_INFO> info;
+    PaMeta meta{-1, 0};
+    int rows_done = 0;
+    for (int un = 0;; ++un) {
+      const int qb = un & 1;
+      bad |= !tc_wait(&sh.q_full[qb], un >> 1 & 1, &sh.dead);
+      if (tc::named_bar_or(1, RW_SOFT, bad)) {
+        bad = true;
+        break;
+      }
+      const TcUnit u = sh.unit[qb];
+      if (u.t1 == 0) break;
+      const int row0 = u.rb * RW_RB, nrows = min(RW_RB, p.rows - row0);
+      const bool active = quarter * 32 < nrows;
+      // tokens that every row of the unit sees: [all_from, all_to]; a window longer than the request is no window
+      const int width = min(window, max(u.len, 1));
+      const int all_to = u.len - a.W + row0 / p.G, all_from = u.len - a.W + (row0 + nrows - 1) / p.G - width + 1;
+      const int last = active ? sh.last[qb][tk] : -1, low = last - width + 1;
+      const float factor = active ? sh.factor[qb][tk] : 0.f;
+      float m = TC_NONE, l = 0.f;
+      for (int tile = u.t0; tile < u.t1; ++tile, buf.step(), before.step(), info.step()) {
+      const bool first_tile = tile == u.t0;
       bad |= !tc_wait(&sh.s_full[buf.at], buf.parity, &sh.dead);
       bad = __any_sync(0xffffffffu, bad);
       const uint32_t own_s = tmem + buf.at * 128 + g * 64 + lanes;
       if (active) {
         tc::fence_after_sync();
-        const int64_t tok0 = (int64_t)u.start + (int64_t)it.tile * TC_TILE;
-        const uint32_t(&there)[4] = sh.there[info.at];
-        const bool masked = tok0 + TC_TILE - 1 > all_to || tok0 < all_from ||
-                            (there[0] & there[1] & there[2] & there[3]) != 0xffffffffu;
+        const int tok0 = u.start + tile * TC_TILE;
+        const uint4 there = *reinterpret_cast<const uint4*>(sh.there[info.at]);
+        const bool masked = tok0 > all_to - (TC_TILE - 1) || tok0 < all_from || (there.x & there.y & there.z & there.w) != 0xffffffffu;
         // 32 tokens at a time: few enough instructions to stay in the instruction cache, and no spilled scores
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
@@ -557,11 +580,9 @@ __global__ void __launch_bounds__(RW_NT, 1)
             capped_yet = true;
           }
           if (masked) {
-            const int64_t first = tok0 + t0;
             // of the 32 the row sees those from `from` on, up to `to`
-            const int to = (int)max((int64_t)0, min((int64_t)32, last + 1 - first));
-            const int from = (int)max((int64_t)0, min((int64_t)32, last + 1 - first - window));
-            uint32_t seen = there[2 * g + h];
+            const int first = tok0 + t0, to = max(0, min(32, last + 1 - first)), from = max(0, min(32, low - first));
+            uint32_t seen = g == 0 ? (h == 0 ? there.x : there.y) : (h == 0 ? there.z : there.w);
             if (to < 32) seen &= (1u << to) - 1;
             seen &= from < 32 ? ~((1u << from) - 1) : 0u;
 #pragma unroll
@@ -601,7 +622,7 @@ __global__ void __launch_bounds__(RW_NT, 1)
                 tc::tmem_st8f(own_s + c, w);
               }
             }
-            if (!it.first()) {
+            if (!first_tile) {
               // the last product into this accumulator is through
               bad |= !tc_wait(&sh.p_free[before.at], before.parity, &sh.dead);
               bad = __any_sync(0xffffffffu, bad);
@@ -646,19 +667,18 @@ __global__ void __launch_bounds__(RW_NT, 1)
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) tc::bar_arrive(&sh.p_full[buf.at]);
-      if (!it.last()) continue;
+      }
 
       // ---- end of the unit's part: the groups' results joined, each writing 64 channels
       const bool whole = u.t0 == 0 && u.t1 == u.tiles;
-      const int row0 = u.rb * RW_RB;
       const int64_t part_at = (me * 2 + (u.t0 == 0 ? 1 : 0)) * RW_RB, heads = (int64_t)u.b * a.W * a.Hq;
       sh.ml[g][tk] = make_float2(m, l);
-      bad |= !tc_wait(&sh.o_full, it.unit_no & 1, &sh.dead);
+      bad |= !tc_wait(&sh.o_full, un & 1, &sh.dead);
       bad = __any_sync(0xffffffffu, bad);
       tc::fence_after_sync();
       tc::named_bar(1, RW_SOFT);
       bool nan = false;
-      const int head = sh.head[tk];
+      const int head = active ? sh.head[qb][tk] : -1;
       if (active && !bad) {
         const float2 other = sh.ml[1 - g][tk];
         float mr = fmaxf(m, other.x);
@@ -667,46 +687,51 @@ __global__ void __launch_bounds__(RW_NT, 1)
         const float by0 = g == 0 ? own : his, by1 = g == 0 ? his : own;
         const bool none = mr == TC_NONE && lr == 0.f;
         if (mr == TC_NONE) mr = none ? -INFINITY : 0.f;  // nothing but NaN scores: let them through
-        const float over_l = none ? 0.f : 1.f / lr;
-        const float out_by = whole ? over_l : 1.f;
+        float over_l = 1.f;
+        if (whole) asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(over_l) : "f"(lr));
+        const float2 f0 = both(none ? 0.f : by0 * over_l), f1 = both(none ? 0.f : by1 * over_l);
         // over the queries, which the products have read: 32 channels of each group at a time, 128 bytes a row
-        const uint32_t turn = tc::smem_u32(qbuf) + g * RW_BLOCK;
+        const uint32_t turn = tc::smem_u32(qbuf + qb * RW_SLOT) + g * RW_BLOCK;
+        float2 check = both(0.f);
+        const int r0 = quarter * 32 + (lane >> 3);
+        int hd[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) hd[i] = sh.head[qb][r0 + 4 * i];
 #pragma unroll 1
         for (int c = 0; c < 64; c += 32) {
           float o[32], o1[32];
           tc::tmem_ld32_two(tmem + RW_O + lanes + g * 64 + c, tmem + RW_O + 128 + lanes + g * 64 + c, o, o1);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            o[i] = none ? 0.f : o[i] * by0 + o1[i] * by1;
-            nan |= isnan(o[i]);
-            o[i] *= out_by;
+          for (int i = 0; i < 32; i += 4) {
+            float2 y0 = fma2(make_float2(o1[i], o1[i + 1]), f1, mul2(make_float2(o[i], o[i + 1]), f0));
+            float2 y1 = fma2(make_float2(o1[i + 2], o1[i + 3]), f1, mul2(make_float2(o[i + 2], o[i + 3]), f0));
+            check = fma2(y0, both(0.f), check), check = fma2(y1, both(0.f), check);  // NaN where one is NaN or infinite
+            if (none) y0 = y1 = both(0.f);
+            asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(turn + tc::sw128_chunk(tk, i / 4)), "f"(y0.x),
+                         "f"(y0.y), "f"(y1.x), "f"(y1.y)
+                         : "memory");
           }
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(turn + tc::sw128_chunk(tk, i)), "f"(o[4 * i]),
-                         "f"(o[4 * i + 1]), "f"(o[4 * i + 2]), "f"(o[4 * i + 3])
-                         : "memory");
           __syncwarp();
-#pragma unroll 2
-          for (int i = 0; i < 8; ++i) {
-            const int r = quarter * 32 + i * 4 + (lane >> 3), ch = g * 64 + c + (lane & 7) * 4;
-            float4 y;
-            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                         : "=f"(y.x), "=f"(y.y), "=f"(y.z), "=f"(y.w)
-                         : "r"(turn + tc::sw128_chunk(r, lane & 7))
-                         : "memory");
-            const int hd = sh.head[r];
-            if (hd >= 0 && whole) {
+          const int ch = g * 64 + c + (lane & 7) * 4;
+          float4 y[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] = ld_shared4(turn + tc::sw128_chunk(r0 + 4 * i, lane & 7));
+          if (whole) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
               uint2 w;
-              w.x = tc::pack2(__float2bfloat16_rn(y.x), __float2bfloat16_rn(y.y));
-              w.y = tc::pack2(__float2bfloat16_rn(y.z), __float2bfloat16_rn(y.w));
-              *reinterpret_cast<uint2*>(static_cast<bf16*>(a.out) + (heads + hd) * TC_D + ch) = w;
-            } else if (hd >= 0) {
-              *reinterpret_cast<float4*>(p.part_o + (part_at + r) * TC_D + ch) = y;
+              w.x = tc::pack2(__float2bfloat16_rn(y[i].x), __float2bfloat16_rn(y[i].y));
+              w.y = tc::pack2(__float2bfloat16_rn(y[i].z), __float2bfloat16_rn(y[i].w));
+              if (hd[i] >= 0) *reinterpret_cast<uint2*>(static_cast<bf16*>(a.out) + (heads + hd[i]) * TC_D + ch) = w;
             }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (hd[i] >= 0) *reinterpret_cast<float4*>(p.part_o + (part_at + r0 + 4 * i) * TC_D + ch) = y[i];
           }
           __syncwarp();
         }
+        nan = !none && isnan(check.x + check.y);
         if (head >= 0 && g == 0) {
           if (!whole) *reinterpret_cast<float2*>(p.part_ml + (part_at + tk) * 2) = make_float2(mr, lr);
           else if (a.lse) a.lse[heads + head] = none ? -INFINITY : (mr + log2f(lr)) * PA_LN2;
@@ -738,6 +763,7 @@ __global__ void __launch_bounds__(RW_NT, 1)
         }
       }
       __syncwarp();
+      if (lane == 0) tc::bar_arrive(&sh.q_free[qb]);  // the unit's rows have been read, and written from its queries' place
       if (whole) {
         rows_done += nrows;
       } else if (u.t0 == 0 && tid == RW_SOFT0) {
