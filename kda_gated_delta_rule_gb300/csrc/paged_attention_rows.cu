@@ -109,6 +109,10 @@ __device__ __forceinline__ float capped_any(float z, float cap2) {
   return fabsf(z) < 0.3f * PA_LOG2E ? capped_series(z, cap2) : capped(z, cap2);
 }
 
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
 __device__ __forceinline__ uint32_t pack_f16(float2 x) {
   const __half2 h = __floats2half2_rn(x.x, x.y);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -653,8 +657,7 @@ __global__ void __launch_bounds__(RW_NT, 1)
               hi[2 * i] = pack_f16(e0), hi[2 * i + 1] = pack_f16(e1);
             } else {
               hi[2 * i] = split_pair<false>(e0.x, e0.y), hi[2 * i + 1] = split_pair<false>(e1.x, e1.y);
-              const __nv_bfloat162 y0 = __floats2bfloat162_rn(e0.x, e0.y), y1 = __floats2bfloat162_rn(e1.x, e1.y);
-              lo[2 * i] = *reinterpret_cast<const uint32_t*>(&y0), lo[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&y1);
+              lo[2 * i] = pack_bf16(e0.x, e0.y), lo[2 * i + 1] = pack_bf16(e1.x, e1.y);
             }
           }
           sum = add2(sum, sum1);
@@ -720,8 +723,8 @@ __global__ void __launch_bounds__(RW_NT, 1)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               uint2 w;
-              w.x = tc::pack2(__float2bfloat16_rn(y[i].x), __float2bfloat16_rn(y[i].y));
-              w.y = tc::pack2(__float2bfloat16_rn(y[i].z), __float2bfloat16_rn(y[i].w));
+              w.x = pack_bf16(y[i].x, y[i].y);
+              w.y = pack_bf16(y[i].z, y[i].w);
               if (hd[i] >= 0) *reinterpret_cast<uint2*>(static_cast<bf16*>(a.out) + (heads + hd[i]) * TC_D + ch) = w;
             }
           } else {
@@ -752,8 +755,8 @@ __global__ void __launch_bounds__(RW_NT, 1)
             const int64_t at = heads + (int64_t)wt * a.Hq + u.h * p.G + (row0 + r - wt * p.G);
             const float by = none ? 0.f : 1.f / lr;
             uint2 y;
-            y.x = tc::pack2(__float2bfloat16_rn(o.x * by), __float2bfloat16_rn(o.y * by));
-            y.y = tc::pack2(__float2bfloat16_rn(o.z * by), __float2bfloat16_rn(o.w * by));
+            y.x = pack_bf16(o.x * by, o.y * by);
+            y.y = pack_bf16(o.z * by, o.w * by);
             *reinterpret_cast<uint2*>(static_cast<bf16*>(a.out) + at * TC_D + 4 * lane) = y;
             if (lane == 0 && a.lse) a.lse[at] = none ? -INFINITY : (mr + log2f(lr)) * PA_LN2;
           } else {
@@ -843,8 +846,8 @@ __global__ void __launch_bounds__(RW_JOIN_NT) paged_attention_rows_join_kernel(c
   const int64_t head = ((int64_t)b * a.W + wt) * a.Hq + (int64_t)h * p.G + g;
   const float by = none ? 0.f : 1.f / l;
   uint2 y;
-  y.x = tc::pack2(__float2bfloat16_rn(none ? 0.f : o.x * by), __float2bfloat16_rn(none ? 0.f : o.y * by));
-  y.y = tc::pack2(__float2bfloat16_rn(none ? 0.f : o.z * by), __float2bfloat16_rn(none ? 0.f : o.w * by));
+  y.x = pack_bf16(none ? 0.f : o.x * by, none ? 0.f : o.y * by);
+  y.y = pack_bf16(none ? 0.f : o.z * by, none ? 0.f : o.w * by);
   *reinterpret_cast<uint2*>(static_cast<bf16*>(a.out) + head * TC_D + lane * 4) = y;
   if (lane == 0) {
     if (a.lse) a.lse[head] = none ? -INFINITY : (m + log2f(l)) * PA_LN2;
