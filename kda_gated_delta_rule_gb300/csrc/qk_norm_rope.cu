@@ -10,7 +10,8 @@
 // 8i .. 8i + 7 (neighbouring pairs); either way its four pairs are 4i .. 4i + 3, one 16-byte read of each table, and
 // its eight values are held as four float2, the pairs' lower channels in the first two and the upper ones in the others,
 // so the arithmetic is on two values per instruction.  (With eight consecutive channels per lane the half-split
-// rotation took a shuffle per channel and twice the table bytes: 41 us for 8192 x 40 x 128 bf16 rows; now 30.6, 83 % of the copy rate.)
+// rotation took a shuffle per channel and twice the table bytes: 41 us for 8192 x 40 x 128 bf16 rows; now 28.5, 89 % of the
+// copy rate.)
 // A group of lanes takes R rows of one token and one kind, queries or keys, issues all its loads before the first
 // reduction, reads the angles and the weight once for them, and reduces the rows' sums together.
 #include "f32x2.cuh"
@@ -19,8 +20,14 @@
 
 namespace kda {
 
-constexpr int NORM_NT = 128, NORM_RESIDENT = 8, NORM_R = 4;
-constexpr int NORM_BWD_NT = 256, NORM_BWD_RESIDENT = 2, NORM_BWD_R = 4;
+constexpr int NORM_NT = 128, NORM_R = 4;
+// CTAs per SM: as many as hold their rows without spills (8192 x 40 x 128 rows, bf16: 28.6 us with 7, 30.8 with 8, 30.0
+// with 6; fp32: 55.8 with 6, 58.6 with 7, 64.9 with 8)
+constexpr int norm_resident(bool bf16_in) { return bf16_in ? 7 : 6; }
+constexpr int NORM_BWD_NT = 256, NORM_BWD_RESIDENT = 2;
+// Rows that a group of the backward takes at once: fp32 rows fill the registers with two (16384 x 40 x 128 rows, bf16: 83 us
+// with 4, 98 with 2; fp32: 150 us with 2, 163 with 4).
+constexpr int norm_bwd_rows(bool bf16_in, bool bf16_grad) { return bf16_in && bf16_grad ? 4 : 2; }
 
 // A lane's channels, and its four pairs.
 struct NormLane {
@@ -181,7 +188,7 @@ struct NormCursor {
 // chunks_q, chunks: groups of R heads per token among the queries, and in all.  The CTAs walk the pairs; the next turn's
 // position is read a turn ahead, so that rows and angles are asked for together.
 template <int D, int R, bool INBF, bool OUTBF, bool IL>
-__global__ void __launch_bounds__(NORM_NT, NORM_RESIDENT) qk_norm_rope_kernel(const NormArgs p, unsigned chunks_q,
+__global__ void __launch_bounds__(NORM_NT, norm_resident(INBF)) qk_norm_rope_kernel(const NormArgs p, unsigned chunks_q,
                                                                               unsigned chunks, int turns) {
   constexpr int LPR = D / 8, NG = NORM_NT / LPR;
   pdl_begin();
@@ -383,7 +390,7 @@ cudaError_t norm_fwd(const NormArgs& a, cudaStream_t s) {
   const unsigned cq = (a.Hq + R - 1) / R, chunks = cq + (a.Hkv + R - 1) / R;
   int64_t blocks = (a.T * chunks + NG - 1) / NG;
   if (a.T > 0x7fffffff || blocks * NG > 0x7fffffff) return cudaErrorInvalidValue;
-  const int64_t turns = (blocks + 152 * NORM_RESIDENT - 1) / (152 * NORM_RESIDENT);
+  const int64_t at_once = 152 * norm_resident(a.in_bf16), turns = (blocks + at_once - 1) / at_once;
   blocks = (blocks + turns - 1) / turns;  // as many as give every CTA that many turns
   auto kernel = a.in_bf16 ? (a.out_bf16 ? qk_norm_rope_kernel<D, R, true, true, IL> : qk_norm_rope_kernel<D, R, true, false, IL>)
                           : (a.out_bf16 ? qk_norm_rope_kernel<D, R, false, true, IL>
@@ -399,14 +406,14 @@ cudaError_t norm_fwd_d(const NormArgs& a, cudaStream_t s) {
   return a.interleaved ? norm_fwd<D, NORM_R, true>(a, s) : norm_fwd<D, NORM_R, false>(a, s);
 }
 
-template <int D, int R, bool IL>
+template <int D, bool IL>
 cudaError_t norm_bwd(const NormArgs& a, const void* dyq, const void* dyk, bool g_bf16, float* partial, int ctas_q,
                      int ctas, cudaStream_t s) {
   const int sel = (a.in_bf16 ? 4 : 0) | (g_bf16 ? 2 : 0) | (a.out_bf16 ? 1 : 0);
   switch (sel) {
 #define KDA_CASE(n, i, g, o)                                                                                         \
-  case n: return launch_pdl(qk_norm_rope_bwd_kernel<D, R, i, g, o, IL>, dim3(ctas), dim3(NORM_BWD_NT), 0, s, a, dyq, \
-                            dyk, partial, ctas_q);
+  case n: return launch_pdl(qk_norm_rope_bwd_kernel<D, norm_bwd_rows(i, g), i, g, o, IL>, dim3(ctas),                \
+                            dim3(NORM_BWD_NT), 0, s, a, dyq, dyk, partial, ctas_q);
     KDA_CASE(0, false, false, false)
     KDA_CASE(1, false, false, true)
     KDA_CASE(2, false, true, false)
@@ -423,7 +430,8 @@ cudaError_t norm_bwd(const NormArgs& a, const void* dyq, const void* dyk, bool g
 template <int D>
 cudaError_t norm_bwd_d(const NormArgs& a, const void* dyq, const void* dyk, bool g_bf16, float* dwq, float* dwk,
                        float* partial, cudaStream_t s) {
-  constexpr int NG = NORM_BWD_NT / (D / 8), R = NORM_BWD_R, MOST = 152 * NORM_BWD_RESIDENT;
+  constexpr int NG = NORM_BWD_NT / (D / 8), MOST = 152 * NORM_BWD_RESIDENT;
+  const int R = norm_bwd_rows(a.in_bf16, g_bf16);
   static_assert(MOST <= NORM_BWD_CTAS, "one row of the workspace per CTA");
   const int64_t need_q = (a.T * ((a.Hq + R - 1) / R) + NG - 1) / NG, need_k = (a.T * ((a.Hkv + R - 1) / R) + NG - 1) / NG;
   int64_t ctas_q = need_q, ctas_k = need_k;
@@ -434,8 +442,8 @@ cudaError_t norm_bwd_d(const NormArgs& a, const void* dyq, const void* dyk, bool
   }
   const int ctas = (int)(ctas_q + ctas_k);
   if (ctas > 0) {  // without tokens the weights' gradients are zero
-    const cudaError_t e = a.interleaved ? norm_bwd<D, R, true>(a, dyq, dyk, g_bf16, partial, (int)ctas_q, ctas, s)
-                                        : norm_bwd<D, R, false>(a, dyq, dyk, g_bf16, partial, (int)ctas_q, ctas, s);
+    const cudaError_t e = a.interleaved ? norm_bwd<D, true>(a, dyq, dyk, g_bf16, partial, (int)ctas_q, ctas, s)
+                                        : norm_bwd<D, false>(a, dyq, dyk, g_bf16, partial, (int)ctas_q, ctas, s);
     if (e != cudaSuccess) return e;
   }
   return launch_pdl(qk_norm_weight_grad_kernel, dim3(2 * D / 16), dim3(512), 0, s, (const float*)partial, (int)ctas_q,
