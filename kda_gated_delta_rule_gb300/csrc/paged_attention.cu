@@ -11,8 +11,9 @@ size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 namespace {
 
 // More query rows per cached row than this take the many-rows form: its time hardly grows up to 128 (64 requests of 500 to 6000
-// tokens: 33 to 37 us with bf16, 42 to 45 with e4m3), where the others' grow with the rows (24 rows: 44 and 50 us; 96: 87
-// and 93); at 12 and 16 rows the register form is as fast (32 to 34 us) or faster (29 us).
+// tokens, 24 rows and 96: 33 and 36 us with bf16, 40 and 45 with e4m3), where the register form's grows with the rows (55
+// and 108; 50 and 92).  At 12 and 16 rows that one is as fast (bf16: 35 against 32) or faster (e4m3: 29 against 40), and
+// on longer caches faster (90 requests of 2227 to 8908 tokens: 59 against 66, 48 against 88).
 constexpr int PA_ROWS_FROM = 16;
 
 // The workspace's places for `workers` warps or CTAs with row blocks of rb.
