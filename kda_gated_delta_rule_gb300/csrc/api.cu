@@ -794,7 +794,9 @@ kda_status kda_paged_attention(const kda_paged_attention_args* a, kda_stream_t s
   p.max_pages = a->max_pages;
   p.seq_lens = a->seq_lens;
   p.scale = a->scale;
-  p.softcap = a->softcap;
+  // A cap of 1e30 leaves scores below 1e26 as they are in fp32, and its multiples would leave fp32's range; one below 1e-20
+  // leaves nothing of them, and the scores' multiples of its inverse would.
+  p.softcap = a->softcap > 1e30f ? 0.f : a->softcap > 0.f && a->softcap < 1e-20f ? 1e-20f : a->softcap;
   p.window = a->window;
   p.out = a->out;
   p.lse = a->lse;

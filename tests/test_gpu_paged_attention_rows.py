@@ -167,3 +167,15 @@ def test_captured_and_on_another_stream(cuda, kind):
         out.zero_()
         graph.replay()
         assert torch.equal(out, want)
+
+
+@kinds
+@pytest.mark.parametrize("Hq,Hkv,W", [(12, 1, 8), (4, 1, 1), (200, 100, 1)])
+def test_caps_at_the_ends_of_fp32(cuda, Hq, Hkv, W, kind):
+    """The same in all three forms: a cap that no score feels, and one that leaves nothing of any score."""
+    p = Problem([9, 257], W, Hq, Hkv, 128, 16, kind)
+    want = p.run(cuda).out.clone()
+    for cap in (1e31, 1e37, 3e38):
+        assert torch.equal(p.run(cuda, softcap=cap).out, want)
+    for cap in (1e-18, 1e-30, 1e-38):
+        p.run(cuda, softcap=cap).check(softcap=cap)
