@@ -808,7 +808,7 @@ cudaError_t rows_launch(const PagedAttnArgs& a, const PaPlan& p, int sms, cudaSt
   plan.workers = (int)ctas;
   e = launch_pdl(kernel, dim3((unsigned)ctas), dim3(RW_NT), RW_SMEM, s, maps, a, plan, box);
   if (e != cudaSuccess) return e;
-  return tc_join<RW_RB>(a, plan, units, s);
+  return pa_join<TC_D, RW_RB>(a, plan, units, s);
 }
 
 }  // namespace

@@ -618,7 +618,7 @@ cudaError_t tc_launch(const PagedAttnArgs& a, const PaPlan& p, int sms, cudaStre
   plan.workers = (int)ctas;
   e = launch_pdl(kernel, dim3((unsigned)ctas), dim3(C::NT), bytes, s, maps, a, plan, box);
   if (e != cudaSuccess) return e;
-  return tc_join<RB>(a, plan, units, s);
+  return pa_join<TC_D, RB>(a, plan, units, s);
 }
 
 }  // namespace

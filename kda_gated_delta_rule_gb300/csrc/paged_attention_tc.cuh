@@ -149,78 +149,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// The cut units' parts joined: a warp has a row (32 lanes x 4 channels) and every SL-th of its parts.
-constexpr int TC_JOIN_NT = 256;
-template <int RB, int SL>
-__global__ void __launch_bounds__(TC_JOIN_NT) paged_attention_tc_join_kernel(const PagedAttnArgs a, const PaPlan p) {
-  constexpr int JR = TC_JOIN_NT / 32 / SL;  // rows of a CTA
-  __shared__ float4 sum_o[SL > 1 ? TC_JOIN_NT : 1];
-  pdl_begin();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, slice = warp % SL, x0 = blockIdx.x;
-  const PaMeta meta = p.meta[x0];
-  if (meta.unit < 0) return;
-  const int rb = meta.unit % p.blocks, bh = meta.unit / p.blocks, h = bh % a.c.Hkv, b = bh / a.c.Hkv;
-  const int r = blockIdx.y * JR + warp / SL, row = rb * RB + r, parts = meta.end - x0 + 1;
-  const bool there = row < p.rows;  // of a warp
-  auto at = [&](int i) { return ((int64_t)(x0 + i) * 2 + (i == 0 ? 1 : 0)) * RB + r; };
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  float m = -INFINITY, l = 0.f;
-  if (there) {
-    for (int i = lane; i < parts; i += 32) m = fmaxf(m, p.part_ml[at(i) * 2]);
-#pragma unroll
-    for (int j = 16; j > 0; j >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, j));
-    for (int i0 = 0; i0 < parts; i0 += 32) {
-      float by = 0.f;
-      if (i0 + lane < parts) {
-        const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + at(i0 + lane) * 2);
-        by = ml.x == -INFINITY ? 0.f : ex2(ml.x - m);
-        l += ml.y * by;
-      }
-      const int n = min(32, parts - i0);
-#pragma unroll 4
-      for (int i = slice; i < n; i += SL) {
-        const float4 x = *reinterpret_cast<const float4*>(p.part_o + at(i0 + i) * TC_D + lane * 4);
-        const float w = __shfl_sync(0xffffffffu, by, i);
-        if (w != 0.f) o.x += x.x * w, o.y += x.y * w, o.z += x.z * w, o.w += x.w * w;  // a part that saw nothing holds zeros
-      }
-    }
-#pragma unroll
-    for (int j = 16; j > 0; j >>= 1) l += __shfl_xor_sync(0xffffffffu, l, j);
-  }
-  if constexpr (SL > 1) {
-    sum_o[threadIdx.x] = o;
-    __syncthreads();
-    if (slice != 0) return;
-#pragma unroll
-    for (int i = 1; i < SL; ++i) {
-      const float4 x = sum_o[threadIdx.x + 32 * i];
-      o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
-    }
-  }
-  if (!there) return;
-  const bool none = m == -INFINITY;
-  const int wt = row / p.G, g = row - wt * p.G;
-  const int64_t head = ((int64_t)b * a.W + wt) * a.Hq + (int64_t)h * p.G + g;
-  const float by = none ? 0.f : 1.f / l;
-  uint2 y;
-  y.x = pack_bf16(none ? 0.f : o.x * by, none ? 0.f : o.y * by);
-  y.y = pack_bf16(none ? 0.f : o.z * by, none ? 0.f : o.w * by);
-  *reinterpret_cast<uint2*>(static_cast<bf16*>(a.out) + head * TC_D + lane * 4) = y;
-  if (lane == 0) {
-    if (a.lse) a.lse[head] = none ? -INFINITY : (m + log2f(l)) * PA_LN2;
-    add_work(a.status, 1);
-  }
-}
-
-template <int RB>
-cudaError_t tc_join(const PagedAttnArgs& a, const PaPlan& p, int64_t units, cudaStream_t s) {
-  const int rows = p.rows < RB ? p.rows : RB;
-  // with few units each has many parts
-  if (units * 8 < p.workers)
-    return launch_pdl(paged_attention_tc_join_kernel<RB, 8>, dim3(p.workers, rows), dim3(TC_JOIN_NT), 0, s, a, p);
-  return launch_pdl(paged_attention_tc_join_kernel<RB, 1>, dim3(p.workers, (rows + 7) / 8), dim3(TC_JOIN_NT), 0, s, a, p);
-}
-
 }  // namespace
 
 }  // namespace kda
