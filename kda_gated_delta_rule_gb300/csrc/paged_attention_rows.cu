@@ -525,147 +525,147 @@ __global__ void __launch_bounds__(RW_NT, 1)
       const float factor = active ? sh.factor[qb][tk] : 0.f;
       float m = TC_NONE, l = 0.f;
       for (int tile = u.t0; tile < u.t1; ++tile, buf.step(), before.step(), info.step()) {
-      const bool first_tile = tile == u.t0;
-      bad |= !tc_wait(&sh.s_full[buf.at], buf.parity, &sh.dead);
-      bad = __any_sync(0xffffffffu, bad);
-      const uint32_t own_s = tmem + buf.at * 128 + g * 64 + lanes;
-      if (active) {
-        tc::fence_after_sync();
-        const int tok0 = u.start + tile * TC_TILE;
-        const uint4 there = *reinterpret_cast<const uint4*>(sh.there[info.at]);
-        const bool masked = tok0 > all_to - (TC_TILE - 1) || tok0 < all_from || (there.x & there.y & there.z & there.w) != 0xffffffffu;
-        // 32 tokens at a time: few enough instructions to stay in the instruction cache, and no spilled scores
+        const bool first_tile = tile == u.t0;
+        bad |= !tc_wait(&sh.s_full[buf.at], buf.parity, &sh.dead);
+        bad = __any_sync(0xffffffffu, bad);
+        const uint32_t own_s = tmem + buf.at * 128 + g * 64 + lanes;
+        if (active) {
+          tc::fence_after_sync();
+          const int tok0 = u.start + tile * TC_TILE;
+          const uint4 there = *reinterpret_cast<const uint4*>(sh.there[info.at]);
+          const bool masked = tok0 > all_to - (TC_TILE - 1) || tok0 < all_from || (there.x & there.y & there.z & there.w) != 0xffffffffu;
+          // 32 tokens at a time: few enough instructions to stay in the instruction cache, and no spilled scores
 #pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          const int t0 = g * 64 + h * 32;  // first token within the tile
-          float2 x[16];
-          bool capped_yet = a.softcap <= 0.f;
-          for (;;) {
-            float raw[32];
-            tc::tmem_ld32(own_s + 32 * h, raw);
+          for (int h = 0; h < 2; ++h) {
+            const int t0 = g * 64 + h * 32;  // first token within the tile
+            float2 x[16];
+            bool capped_yet = a.softcap <= 0.f;
+            for (;;) {
+              float raw[32];
+              tc::tmem_ld32(own_s + 32 * h, raw);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = make_float2(raw[2 * i], raw[2 * i + 1]);
-            if (a.softcap > 0.f && capped_yet) break;  // as they come
-            if constexpr (F8) {
-              const uint32_t ks = tc::smem_u32(sh.k_scale[info.at] + t0);
+              for (int i = 0; i < 16; ++i) x[i] = make_float2(raw[2 * i], raw[2 * i + 1]);
+              if (a.softcap > 0.f && capped_yet) break;  // as they come
+              if constexpr (F8) {
+                const uint32_t ks = tc::smem_u32(sh.k_scale[info.at] + t0);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const float4 s = ld_shared4(ks + 16 * i);
+                  x[2 * i] = mul2(mul2(x[2 * i], both(factor)), make_float2(s.x, s.y));
+                  x[2 * i + 1] = mul2(mul2(x[2 * i + 1], both(factor)), make_float2(s.z, s.w));
+                }
+              } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x[i] = mul2(x[i], both(factor));
+              }
+              if (capped_yet) break;
+              float top = 0.f;
+#pragma unroll
+              for (int i = 0; i < 16; ++i) top = fmaxf(top, fmaxf(fabsf(x[i].x), fabsf(x[i].y)));
+              if (__all_sync(0xffffffffu, top <= RW_POLY)) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x[i] = cap_poly(x[i]);
+                break;
+              }
+              // scores near the cap: capped where they are, few at a time (little code for a rare case), and read again
+#pragma unroll 1
+              for (int c = 0; c < 32; c += 8) {
+                float y[8];
+                tc::tmem_ld8(own_s + 32 * h + c, y);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[i] = capped_any(y[i] * factor * (F8 ? sh.k_scale[info.at][t0 + c + i] : 1.f), cap2);
+                tc::tmem_st8f(own_s + 32 * h + c, y);
+              }
+              tc::tmem_wait_st();
+              capped_yet = true;
+            }
+            if (masked) {
+              // of the 32 the row sees those from `from` on, up to `to`
+              const int first = tok0 + t0, to = max(0, min(32, last + 1 - first)), from = max(0, min(32, low - first));
+              uint32_t seen = g == 0 ? (h == 0 ? there.x : there.y) : (h == 0 ? there.z : there.w);
+              if (to < 32) seen &= (1u << to) - 1;
+              seen &= from < 32 ? ~((1u << from) - 1) : 0u;
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                x[i].x = seen >> (2 * i) & 1 ? x[i].x : -INFINITY;
+                x[i].y = seen >> (2 * i + 1) & 1 ? x[i].y : -INFINITY;
+              }
+            }
+            // ---- the reference moves only when a score is far above it (always on the first seen token), and by whole powers
+            // of two, so that probabilities written already follow exactly
+            float over = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) over = fmaxf(over, fmaxf(x[i].x, x[i].y));
+            bool move = over + (F8 ? sh.lift_top[info.at][2 * g + h] : 0.f) > m + TC_SLACK;
+            if (F8 && __any_sync(0xffffffffu, move)) {  // so says a bound: now token by token
+              const uint32_t lift = tc::smem_u32(sh.lift[info.at] + t0);
+              over = -INFINITY;
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
-                const float4 s = ld_shared4(ks + 16 * i);
-                x[2 * i] = mul2(mul2(x[2 * i], both(factor)), make_float2(s.x, s.y));
-                x[2 * i + 1] = mul2(mul2(x[2 * i + 1], both(factor)), make_float2(s.z, s.w));
+                const float4 s = ld_shared4(lift + 16 * i);
+                const float2 y = add2(x[2 * i], make_float2(s.x, s.y)), z = add2(x[2 * i + 1], make_float2(s.z, s.w));
+                over = fmaxf(over, fmaxf(fmaxf(y.x, y.y), fmaxf(z.x, z.y)));
               }
-            } else {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) x[i] = mul2(x[i], both(factor));
+              move = over > m + TC_SLACK;
             }
-            if (capped_yet) break;
-            float top = 0.f;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) top = fmaxf(top, fmaxf(fabsf(x[i].x), fabsf(x[i].y)));
-            if (__all_sync(0xffffffffu, top <= RW_POLY)) {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) x[i] = cap_poly(x[i]);
-              break;
-            }
-            // scores near the cap: capped where they are, few at a time (little code for a rare case), and read again
+            if (__any_sync(0xffffffffu, move)) {
+              const float mn = fmaxf(m, ceilf(over)), by = mn - m > 126.f ? 0.f : __uint_as_float((uint32_t)(127 - (int)(mn - m)) << 23);
+              m = mn;
+              l *= by;
+              if (h == 1) {  // the first 32 tokens' probabilities
 #pragma unroll 1
-            for (int c = 0; c < 32; c += 8) {
-              float y[8];
-              tc::tmem_ld8(own_s + 32 * h + c, y);
+                for (int c = 0; c < (F8 ? 16 : 32); c += 8) {
+                  float w[8];
+                  tc::tmem_ld8(own_s + c, w);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) y[i] = capped_any(y[i] * factor * (F8 ? sh.k_scale[info.at][t0 + c + i] : 1.f), cap2);
-              tc::tmem_st8f(own_s + 32 * h + c, y);
+                  for (int i = 0; i < 8; ++i) w[i] = __uint_as_float(times16<F8>(__float_as_uint(w[i]), by));
+                  tc::tmem_st8f(own_s + c, w);
+                }
+              }
+              if (!first_tile) {
+                // the last product into this accumulator is through
+                bad |= !tc_wait(&sh.p_free[before.at], before.parity, &sh.dead);
+                bad = __any_sync(0xffffffffu, bad);
+                tc::fence_after_sync();
+#pragma unroll 1
+                for (int c = 0; c < 128; c += 16) {
+                  float o[16];
+                  uint32_t w[16];
+                  tc::tmem_ld16(own_o + c, o);
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[i] * by);
+                  tc::tmem_st16(own_o + c, w);
+                }
+              }
             }
-            tc::tmem_wait_st();
-            capped_yet = true;
-          }
-          if (masked) {
-            // of the 32 the row sees those from `from` on, up to `to`
-            const int first = tok0 + t0, to = max(0, min(32, last + 1 - first)), from = max(0, min(32, low - first));
-            uint32_t seen = g == 0 ? (h == 0 ? there.x : there.y) : (h == 0 ? there.z : there.w);
-            if (to < 32) seen &= (1u << to) - 1;
-            seen &= from < 32 ? ~((1u << from) - 1) : 0u;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              x[i].x = seen >> (2 * i) & 1 ? x[i].x : -INFINITY;
-              x[i].y = seen >> (2 * i + 1) & 1 ? x[i].y : -INFINITY;
-            }
-          }
-          // ---- the reference moves only when a score is far above it (always on the first seen token), and by whole powers
-          // of two, so that probabilities written already follow exactly
-          float over = -INFINITY;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) over = fmaxf(over, fmaxf(x[i].x, x[i].y));
-          bool move = over + (F8 ? sh.lift_top[info.at][2 * g + h] : 0.f) > m + TC_SLACK;
-          if (F8 && __any_sync(0xffffffffu, move)) {  // so says a bound: now token by token
-            const uint32_t lift = tc::smem_u32(sh.lift[info.at] + t0);
-            over = -INFINITY;
+            // ---- probabilities, to tensor memory over the scores: of 32 columns the first 16, for bf16 what they leave in the others
+            uint32_t hi[16], lo[16];
+            const uint32_t vs = tc::smem_u32(sh.v_scale[info.at] + t0);
+            float2 sum = make_float2(l, 0.f), sum1 = both(0.f);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              const float4 s = ld_shared4(lift + 16 * i);
-              const float2 y = add2(x[2 * i], make_float2(s.x, s.y)), z = add2(x[2 * i + 1], make_float2(s.z, s.w));
-              over = fmaxf(over, fmaxf(fmaxf(y.x, y.y), fmaxf(z.x, z.y)));
-            }
-            move = over > m + TC_SLACK;
-          }
-          if (__any_sync(0xffffffffu, move)) {
-            const float mn = fmaxf(m, ceilf(over)), by = mn - m > 126.f ? 0.f : __uint_as_float((uint32_t)(127 - (int)(mn - m)) << 23);
-            m = mn;
-            l *= by;
-            if (h == 1) {  // the first 32 tokens' probabilities
-#pragma unroll 1
-              for (int c = 0; c < (F8 ? 16 : 32); c += 8) {
-                float w[8];
-                tc::tmem_ld8(own_s + c, w);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) w[i] = __uint_as_float(times16<F8>(__float_as_uint(w[i]), by));
-                tc::tmem_st8f(own_s + c, w);
+              float2 e0 = add2(x[2 * i], both(-m)), e1 = add2(x[2 * i + 1], both(-m));
+              e0 = make_float2(ex2(e0.x), ex2(e0.y)), e1 = make_float2(ex2(e1.x), ex2(e1.y));
+              sum = add2(sum, e0), sum1 = add2(sum1, e1);
+              if constexpr (F8) {
+                const float4 s = ld_shared4(vs + 16 * i);
+                e0 = mul2(e0, make_float2(s.x, s.y)), e1 = mul2(e1, make_float2(s.z, s.w));
+                hi[2 * i] = pack_f16(e0), hi[2 * i + 1] = pack_f16(e1);
+              } else {
+                hi[2 * i] = split_pair<false>(e0.x, e0.y), hi[2 * i + 1] = split_pair<false>(e1.x, e1.y);
+                lo[2 * i] = pack_bf16(e0.x, e0.y), lo[2 * i + 1] = pack_bf16(e1.x, e1.y);
               }
             }
-            if (!first_tile) {
-              // the last product into this accumulator is through
-              bad |= !tc_wait(&sh.p_free[before.at], before.parity, &sh.dead);
-              bad = __any_sync(0xffffffffu, bad);
-              tc::fence_after_sync();
-#pragma unroll 1
-              for (int c = 0; c < 128; c += 16) {
-                float o[16];
-                uint32_t w[16];
-                tc::tmem_ld16(own_o + c, o);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[i] * by);
-                tc::tmem_st16(own_o + c, w);
-              }
-            }
+            sum = add2(sum, sum1);
+            l = sum.x + sum.y;
+            tc::tmem_st16(own_s + 32 * h, hi);
+            if constexpr (!F8) tc::tmem_st16(own_s + 32 * h + 16, lo);
           }
-          // ---- probabilities, to tensor memory over the scores: of 32 columns the first 16, for bf16 what they leave in the others
-          uint32_t hi[16], lo[16];
-          const uint32_t vs = tc::smem_u32(sh.v_scale[info.at] + t0);
-          float2 sum = make_float2(l, 0.f), sum1 = both(0.f);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            float2 e0 = add2(x[2 * i], both(-m)), e1 = add2(x[2 * i + 1], both(-m));
-            e0 = make_float2(ex2(e0.x), ex2(e0.y)), e1 = make_float2(ex2(e1.x), ex2(e1.y));
-            sum = add2(sum, e0), sum1 = add2(sum1, e1);
-            if constexpr (F8) {
-              const float4 s = ld_shared4(vs + 16 * i);
-              e0 = mul2(e0, make_float2(s.x, s.y)), e1 = mul2(e1, make_float2(s.z, s.w));
-              hi[2 * i] = pack_f16(e0), hi[2 * i + 1] = pack_f16(e1);
-            } else {
-              hi[2 * i] = split_pair<false>(e0.x, e0.y), hi[2 * i + 1] = split_pair<false>(e1.x, e1.y);
-              lo[2 * i] = pack_bf16(e0.x, e0.y), lo[2 * i + 1] = pack_bf16(e1.x, e1.y);
-            }
-          }
-          sum = add2(sum, sum1);
-          l = sum.x + sum.y;
-          tc::tmem_st16(own_s + 32 * h, hi);
-          if constexpr (!F8) tc::tmem_st16(own_s + 32 * h + 16, lo);
+          tc::tmem_wait_st();
         }
-        tc::tmem_wait_st();
-      }
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) tc::bar_arrive(&sh.p_full[buf.at]);
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::bar_arrive(&sh.p_full[buf.at]);
       }
 
       // ---- end of the unit's part: the groups' results joined, each writing 64 channels
