@@ -17,7 +17,7 @@
 // and with cap and scales about 20 more operations each; measured, a tile takes 3500 cycles (bf16) to 6000 (e4m3 with
 // cap), the products 1024 to 1536 under them.  Code that runs once is dear (a cold instruction costs about 4 cycles, and a
 // share has some ten tiles), so tiles go in two equal passes over one compact body, and rare cases in small loops.
-// 64 requests of 500 to 6000 tokens (window 4096), 8 drafts, 12 heads over 1, cap: 41 us (bf16) and 47 us (e4m3); with the
+// 64 requests of 500 to 6000 tokens (window 4096), 8 drafts, 12 heads over 1, cap: 39 us (bf16) and 44 us (e4m3); with the
 // queries as the products' column operand 88 and 100 us.
 //
 // Waits are bounded: one that gives up sets KDA_DEV_TIMEOUT and a flag on which every role leaves.
