@@ -11,7 +11,7 @@ size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 namespace {
 
 // More query rows per cached row than this take the many-rows form: its time hardly grows up to 128 (64 requests of 500 to 6000
-// tokens, 24 rows and 96: 33 and 36 us with bf16, 40 and 45 with e4m3), where the register form's grows with the rows (55
+// tokens, 24 rows and 96: 31 and 34 us with bf16, 38 and 42 with e4m3), where the register form's grows with the rows (55
 // and 108; 50 and 92).  At 12 and 16 rows that one is as fast (bf16: 35 against 32) or faster (e4m3: 29 against 40), and
 // on longer caches faster (90 requests of 2227 to 8908 tokens: 59 against 66, 48 against 88).
 constexpr int PA_ROWS_FROM = 16;
@@ -59,8 +59,8 @@ cudaError_t launch_paged_attention(const PagedAttnArgs& a, cudaStream_t s) {
     return pa_rows(a, p, sms, s);
   }
   // With few units the tensor-memory form's larger and so fewer parts join faster (one request with 8 heads, of 1000 tokens: 11
-  // against 13 us, of 4096: 13 against 17, of 262144: 165 against 168; 64 units of 100 to 30000 tokens: 46 against 55);
-  // with many units of few rows their starts and ends cost it more (64 units of 4096 tokens: 34 against 33 us, 128: 55
+  // against 13 us, of 4096: 13 against 17, of 262144: 164 against 168; 64 units of 100 to 30000 tokens: 46 against 55);
+  // with many units of few rows their starts and ends cost it more (64 units of 4096 tokens: 33 against 33 us, 128: 55
   // against 52).
   if (pa_tc_supported(a) && p.rows <= 16 && (int64_t)a.B * a.c.Hkv <= 64) {
     const int rb = pa_tc_row_block(p.rows);
