@@ -613,6 +613,7 @@ __global__ void __launch_bounds__(RW_NT, 1)
               m = mn;
               l *= by;
               if (h == 1) {  // the first 32 tokens' probabilities
+                tc::tmem_wait_st();  // what pass 0 stored, probabilities and accumulators, before it is read back
 #pragma unroll 1
                 for (int c = 0; c < (F8 ? 16 : 32); c += 8) {
                   float w[8];
