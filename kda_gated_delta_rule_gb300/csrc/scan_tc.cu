@@ -56,6 +56,15 @@ __device__ __forceinline__ void tmem_ld8_async(uint32_t taddr, uint32_t* r) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                : "r"(taddr));
 }
+// waits for this thread's loads; the registers pass through the statement, so that no use of them can precede it
+__device__ __forceinline__ void tmem_wait_ld8(uint32_t* a, uint32_t* b, uint32_t* c) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]), "+r"(a[6]), "+r"(a[7]),
+                 "+r"(b[0]), "+r"(b[1]), "+r"(b[2]), "+r"(b[3]), "+r"(b[4]), "+r"(b[5]), "+r"(b[6]), "+r"(b[7]),
+                 "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3]), "+r"(c[4]), "+r"(c[5]), "+r"(c[6]), "+r"(c[7])
+               :
+               : "memory");
+}
 
 __device__ __forceinline__ uint8_t* align_1k(uint8_t* p) {
   return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
@@ -238,7 +247,7 @@ __global__ void __launch_bounds__(SCAN_NT, 1) seg_scan_tc_kernel(const PrefillAr
         tmem_ld8_async(tm + lane_base + COL_D + ce, r0);
         tmem_ld8_async(tm + lane_base + COL_D + 16 + ce, r1);
         tmem_ld8_async(tm + lane_base + COL_D + 32 + ce, r2);
-        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+        tmem_wait_ld8(r0, r1, r2);
         tc::fence_before_sync();  // this thread's last tensor-memory access of the step
         float d[EC];
 #pragma unroll
