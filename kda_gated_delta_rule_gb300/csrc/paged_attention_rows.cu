@@ -204,22 +204,23 @@ __global__ void __launch_bounds__(RW_NT, 1)
       // so the 8 lanes of a shared-memory store have half of two neighbouring rows, whose chunks meet all banks
       const int c = (lane & 3) + (lane >> 3 & 1) * 4, r4 = (lane >> 4) * 2 + (lane >> 2 & 1), tok_own = warp * 32 + lane;
       // the page's id is asked for two tiles ahead, the tile's rows one ahead
-      int page = -2, off = 0, head = 0;
-      bool more = true;
+      int page = 0, off = 0, head = 0;
+      bool more = true, next_there = false;
       auto look_up = [&]() {
-        page = -2;  // no such token
+        next_there = false;
         more = it.next(a, p, box);
         if (!more) return;
         head = it.u.h;
         const int64_t tok = (int64_t)it.u.start + (int64_t)it.tile * TC_TILE + tok_own;
-        if (tok < it.u.len) {
+        next_there = tok < it.u.len;
+        if (next_there) {
           const int pg = (int)tok / a.c.page_size;
           off = (int)tok - pg * a.c.page_size;
           page = __ldg(a.block_table + (int64_t)it.u.b * a.max_pages + pg);
         }
       };
       auto place = [&]() -> int64_t {
-        if (page == -2) return -1;
+        if (!next_there) return -1;
         if ((unsigned)page >= (unsigned)a.c.num_pages) {
           flag_status(a.status, KDA_DEV_PAGE_OOB);
           return -1;
