@@ -92,6 +92,12 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+// v 2^d, d <= 0, where 2^d alone may be below fp32's range (ex2 gives 0 there) though the product is not: references that
+// include a value scale lie up to 126 powers of two apart at equal scores.  For d >= -64 the second factor is 1.
+__device__ __forceinline__ float times_pow2(float v, float d) {
+  const float near = fmaxf(d, -64.f);
+  return v * ex2(near) * ex2(d - near);
+}
 __device__ __forceinline__ uint32_t half2_of_codes(uint32_t two) {
   uint32_t r;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)two));
@@ -600,10 +606,10 @@ __global__ void __launch_bounds__(PA_NT, pa_resident(NT)) paged_attention_kernel
               x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
               x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
               const float mn = fmaxf(m[t][c], x);
-              const float by = m[t][c] == mn ? 1.f : ex2(m[t][c] - mn);  // 0 from -infinity
+              const float down = m[t][c] == mn ? 0.f : m[t][c] - mn, by = ex2(down);  // 0 from -infinity
               m[t][c] = mn;
               mu[t][c] = mn == -INFINITY ? 0.f : mn;
-              l[t][c] *= by;
+              l[t][c] = F8 ? times_pow2(l[t][c], down) : l[t][c] * by;
 #pragma unroll
               for (int st = 0; st < KS; ++st) o[t][st][c] *= by, o[t][st][c + 2] *= by;
             }
@@ -774,11 +780,11 @@ __global__ void __launch_bounds__(SL == 1 ? 256 : 32 * SL) paged_attention_join_
         if (top > m) {
           const float by = ex2(m - top);  // 0 from -infinity
           o.x *= by, o.y *= by, o.z *= by, o.w *= by;
-          l *= by;
+          l = times_pow2(l, m - top);
           m = top;
         }
         const float by = ml.x == -INFINITY ? 0.f : ex2(ml.x - m);
-        l += ml.y * by;
+        if (ml.x != -INFINITY) l += times_pow2(ml.y, ml.x - m);
         const int n = min(32, (parts - i0 + SL - 1) / SL);
 #pragma unroll 8
         for (int i = 0; i < n; ++i) {
@@ -802,7 +808,7 @@ __global__ void __launch_bounds__(SL == 1 ? 256 : 32 * SL) paged_attention_join_
 #pragma unroll
         for (int j = 16; j > 0; j >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, j));
         const float by = ml.x == -INFINITY ? 0.f : ex2(ml.x - m);
-        l = ml.y * by;
+        l = ml.x == -INFINITY ? 0.f : times_pow2(ml.y, ml.x - m);
         o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
         for (int i = 0; i < SL; ++i) {

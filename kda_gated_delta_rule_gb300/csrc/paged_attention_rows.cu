@@ -611,8 +611,8 @@ __global__ void __launch_bounds__(RW_NT, 1)
             }
             if (__any_sync(0xffffffffu, move)) {
               const float mn = fmaxf(m, ceilf(over)), by = mn - m > 126.f ? 0.f : __uint_as_float((uint32_t)(127 - (int)(mn - m)) << 23);
+              l = F8 && mn - m > 126.f ? times_pow2(l, m - mn) : l * by;
               m = mn;
-              l *= by;
               if (h == 1) {  // the first 32 tokens' probabilities
                 tc::tmem_wait_st();  // what pass 0 stored, probabilities and accumulators, before it is read back
 #pragma unroll 1
@@ -684,7 +684,9 @@ __global__ void __launch_bounds__(RW_NT, 1)
         const float2 other = sh.ml[1 - g][tk];
         float mr = fmaxf(m, other.x);
         const float own = ex2(m - mr), his = ex2(other.x - mr);
-        const float lr = g == 0 ? l * own + other.y * his : other.y * his + l * own;
+        float lr;
+        if constexpr (F8) lr = __fadd_rn(times_pow2(l, m - mr), times_pow2(other.y, other.x - mr));
+        else lr = g == 0 ? l * own + other.y * his : other.y * his + l * own;
         const float by0 = g == 0 ? own : his, by1 = g == 0 ? his : own;
         const bool none = mr == TC_NONE && lr == 0.f;
         if (mr == TC_NONE) mr = none ? -INFINITY : 0.f;  // nothing but NaN scores: let them through

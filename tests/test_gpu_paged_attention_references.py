@@ -38,3 +38,44 @@ def test_many_rows_move_in_every_pass(cuda, kind, step):
     p.check(scale=1.0)
     for _ in range(5):
         assert torch.equal(p.run(cuda, scale=1.0).out, first)
+
+
+F32 = torch.float32
+# Hq, Hkv, W, d, type: the register form with 8 and with 16 or more columns, with fp32, and the many-rows form
+E4_FORMS = [(4, 1, 1, 128, BF), (12, 1, 1, 64, BF), (6, 2, 2, 32, F32), (12, 1, 2, 128, BF), (130, 1, 1, 128, BF)]
+e4_forms = pytest.mark.parametrize("Hq,Hkv,W,d,dt", E4_FORMS)
+
+
+def many_times(p, times, g):
+    """The problem's one request `times` over, each with queries of its own: enough that a worker's share is whole requests."""
+    p.lens, p.table_cpu = p.lens * times, p.table_cpu.expand(times, -1)
+    p.table = p.table.expand(times, -1).contiguous()
+    p.q = (1.5 * torch.randn(times, *p.q.shape[1:], generator=g)).to(p.q.dtype).cuda()
+
+
+@e4_forms
+@pytest.mark.parametrize("n,times", [(600, 1), (320, 1500), (5000, 1)])
+@pytest.mark.parametrize("first,second", [(-63, 63), (63, -63)])
+def test_value_scales_of_both_ends_one_after_the_other(cuda, Hq, Hkv, W, d, dt, n, times, first, second):
+    """Half of a request's values with scale 2^-63, the other half with 2^63: all count alike in the sum of the softmax.  Within one
+    worker's share and across shares, in either order."""
+    g = torch.Generator().manual_seed(n)
+    p = Problem([n], W, Hq, Hkv, d, 64, E4, dt, dt)
+    scale = torch.exp2(torch.where(torch.arange(n) < n // 2, first, second).double())[:, None].expand(n, Hkv)
+    put(p, "v", 0, 100 * torch.randn(n, Hkv, d, generator=g).double() * scale[..., None], scale=scale)
+    if times > 1:
+        many_times(p, times, g)
+    p.run(cuda)
+    p.check(only=range(0, times, 499))
+
+
+@e4_forms
+def test_value_scales_that_alternate_by_tiles(cuda, Hq, Hkv, W, d, dt):
+    """Scales from one end to the other and back, in runs of 16 to 256 tokens."""
+    n = 1500
+    g = torch.Generator().manual_seed(d)
+    for run in (16, 32, 64, 128, 256):
+        p = Problem([n], W, Hq, Hkv, d, 16, E4, dt, dt)
+        scale = torch.exp2(torch.where((torch.arange(n) // run) % 2 == 0, -63, 63).double())[:, None].expand(n, Hkv)
+        put(p, "v", 0, 100 * torch.randn(n, Hkv, d, generator=g).double() * scale[..., None], scale=scale)
+        p.run(cuda).check()
