@@ -25,7 +25,9 @@
 // e4m3 caches: codes become fp16 (exact), q is scaled per row by a power of two into fp16's range (exact for bf16 q
 // down to 2^-31 of the row's maximum), the key's scale multiplies the score and the value's scale the
 // probability.  The running reference of the softmax is then the maximum of x + log2(value scale), so that the
-// scaled probabilities fit fp16 for any scales.
+// scaled probabilities fit fp16 for any scales.  A value of zeros says nothing by its scale (1 in a row that kda_kv_write
+// wrote): it counts with the least, and its probability, which multiplies zeros, is taken as 0 in the product.  Codes
+// are looked at for that only when the reference moves, so it costs nothing else (256 ragged requests: 96 us with and without).
 //
 // Rounding to fewer bits: probabilities enter the second product as 16-bit numbers.  fp16 (e4m3 cache) has 11 bits,
 // well below the bf16 output's 8; bf16 (bf16 cache) has 8, so they go in as a sum of two bf16 (16 bits), else
@@ -46,6 +48,7 @@ constexpr int PA_MAX_LEN = 0x7fffff00;  // token positions and the next tile's s
 constexpr float PA_LOG2E = 1.4426950408889634f, PA_LN2 = 0.6931471805599453f;
 // how far (in powers of two) scores may run above the softmax reference before it is moved
 constexpr float PA_SLACK = 6.f;
+constexpr float PA_LEAST_LIFT = -62.f;  // of the least value scale, 2^-63
 
 // What the main kernel leaves for the join, per warp.
 struct PaMeta {
@@ -127,6 +130,12 @@ struct Piece {
   __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int i = 0; i < (BYTES < 4 ? 1 : BYTES / 4); ++i) w[i] = 0;
+  }
+  __device__ __forceinline__ uint32_t any() const {
+    uint32_t x = w[0];
+#pragma unroll
+    for (int i = 1; i < (BYTES < 4 ? 1 : BYTES / 4); ++i) x |= w[i];
+    return x;
   }
   // Read once: not kept in L1 (one request of 262144 tokens, bf16: 172 to 174 us against 175 to 177).
   __device__ __forceinline__ void load(const uint8_t* p) {
@@ -544,6 +553,7 @@ __global__ void __launch_bounds__(PA_NT, pa_resident(NT)) paged_attention_kernel
 
         // ---- scores in powers of two; unseen ones are -infinity
         float top[NT][2];
+        float lift[GPI][2];  // about log2 of the value scale
 #pragma unroll
         for (int t = 0; t < NT; ++t) top[t][0] = top[t][1] = -INFINITY;
 #pragma unroll
@@ -551,10 +561,9 @@ __global__ void __launch_bounds__(PA_NT, pa_resident(NT)) paged_attention_kernel
           const int tq = tok0 + 16 * q;
           const bool none = this_row[q] < 0;
           const bool partly = none || tq > all_to - 15 || tq < all_from;
-          float lift[2] = {0.f, 0.f};  // about log2 of the value scale
           if constexpr (F8) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) lift[i] = (float)((int)(__float_as_uint(vsn[q][i]) >> 23) - 126);
+            for (int i = 0; i < 2; ++i) lift[q][i] = (float)((int)(__float_as_uint(vsn[q][i]) >> 23) - 126);
           }
 #pragma unroll
           for (int t = 0; t < NT; ++t)
@@ -588,7 +597,7 @@ __global__ void __launch_bounds__(PA_NT, pa_resident(NT)) paged_attention_kernel
           for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              top[t][i & 1] = fmaxf(top[t][i & 1], F8 ? s[q][t][i] + lift[i >> 1] : s[q][t][i]);
+              top[t][i & 1] = fmaxf(top[t][i & 1], F8 ? s[q][t][i] + lift[q][i >> 1] : s[q][t][i]);
         }
         // ---- the reference moves only when a score is far above it (always on the first seen token)
         bool move = false;
@@ -597,6 +606,36 @@ __global__ void __launch_bounds__(PA_NT, pa_resident(NT)) paged_attention_kernel
 #pragma unroll
           for (int c = 0; c < 2; ++c) move |= top[t][c] > m[t][c] + PA_SLACK;
         if (__any_sync(0xffffffffu, move)) {
+          if constexpr (F8) {
+            // a value of zeros has a scale all the same: it adds nothing, and lifts the reference as the least scale does
+            bool zeros = false;
+#pragma unroll
+            for (int q = 0; q < GPI; ++q) {
+              uint32_t other[4];  // bit n' 4 + j': lane's piece of token 2 j' + (i & 1) + 8 (i >> 1) has a nonzero code
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                uint32_t any = 0;
+#pragma unroll
+                for (int u = 0; u < C::VL; ++u) any |= v[q][i][u].any();
+                other[i] = __ballot_sync(0xffffffffu, any & 0x7f7f7f7fu);
+              }
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {  // this lane's tokens n and n + 8
+                const uint32_t of = (n & 1 ? other[2 * i + 1] : other[2 * i]) >> (n >> 1) & 0x11111111u;
+                if (of == 0) lift[q][i] = PA_LEAST_LIFT, vsn[q][i] = 0.f, zeros = true;
+              }
+            }
+            if (__any_sync(0xffffffffu, zeros)) {
+#pragma unroll
+              for (int t = 0; t < NT; ++t) top[t][0] = top[t][1] = -INFINITY;
+#pragma unroll
+              for (int q = 0; q < GPI; ++q)
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) top[t][i & 1] = fmaxf(top[t][i & 1], s[q][t][i] + lift[q][i >> 1]);
+            }
+          }
 #pragma unroll
           for (int t = 0; t < NT; ++t)
 #pragma unroll

@@ -46,6 +46,7 @@ struct RwShared {
   alignas(16) uint32_t there[RW_INFO][4];
   alignas(16) float k_scale[RW_INFO][TC_TILE], v_scale[RW_INFO][TC_TILE], lift[RW_INFO][TC_TILE];
   float lift_top[RW_INFO][4];  // largest lift of 32 tokens
+  uint32_t v_tile[4];  // e4m3: number of the last tile whose V rows a warp has put in their slot, from 1
   float2 ml[2][RW_RB];
   // per query row of a unit: score in powers of two per unit of the product, last seen position, and place among the
   // request's W x Hq output rows (-1 past the unit's)
@@ -119,6 +120,35 @@ __device__ __forceinline__ float4 ld_shared4(uint32_t at) {
   return x;
 }
 
+// Waits until the V rows of tile `tile_no` are in their slot (they stay there until this warp's probabilities are used); false
+// when that takes too long, or another role has given up.
+__device__ __forceinline__ bool rw_put(const volatile uint32_t* v_tile, uint32_t tile_no, int* dead) {
+  for (int i = 0; i < 1 << 22; ++i) {
+    if ((int)(*v_tile - tile_no) >= 0) {
+      __threadfence_block();
+      return true;
+    }
+    if (*reinterpret_cast<volatile int*>(dead)) return false;
+  }
+  *reinterpret_cast<volatile int*>(dead) = 1;
+  return false;
+}
+// Whether a row of a V slot, one a lane, holds anything but zeros (fp16).  Most rows show it in their first chunk.
+__device__ __forceinline__ uint32_t rw_nonzero(uint32_t slot, int row) {
+  uint32_t any = 0;
+#pragma unroll 1
+  for (int c = 0; c < 16; ++c) {
+    uint32_t x, y, z, w;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(x), "=r"(y), "=r"(z), "=r"(w)
+                 : "r"(slot + (c >> 3) * RW_BLOCK + tc::sw128_chunk(row, c & 7))
+                 : "memory");
+    any |= (x | y | z | w) & 0x7fff7fffu;
+    if (__all_sync(0xffffffffu, any != 0)) break;
+  }
+  return any;
+}
+
 // A pair of probabilities times a power of two.
 template <bool F8>
 __device__ __forceinline__ uint32_t times16(uint32_t two, float by) {
@@ -157,6 +187,7 @@ __global__ void __launch_bounds__(RW_NT, 1)
     tc::bar_init(&sh.o_full, 1);
     tc::bar_fence_init();
     sh.dead = 0;
+    for (int i = 0; i < 4; ++i) sh.v_tile[i] = 0;
   }
   if (warp == 12) tc::tmem_alloc(&sh.tmem, RW_TMEM);
 
@@ -230,6 +261,7 @@ __global__ void __launch_bounds__(RW_NT, 1)
       uint4 kw[8], vw[8];
       float ks = 0.f, vs = 0.f;
       int64_t row = -1;
+      uint32_t tile_no = 0;  // of the CTA's share, from 1
       auto load_k = [&]() {
         ks = row >= 0 ? __ldg(a.c.k_scales + row) : 0.f;
         vs = row >= 0 ? __ldg(a.c.v_scales + row) : 0.f;
@@ -265,12 +297,18 @@ __global__ void __launch_bounds__(RW_NT, 1)
         tc::fence_proxy_async();
         __syncwarp();
         if (lane == 0) tc::bar_arrive(&sh.k_full[ring.at]);
-        have = more;
-        if (have) {
-          row = place();
-          look_up();
-          load_k();
-        }
+        // the next tile's keys are asked for before this one's values are put in place, but for the first tile, whose softmax
+        // waits for them to move its reference
+        const bool first = tile_no == 0;
+        auto next_k = [&]() {
+          have = more;
+          if (have) {
+            row = place();
+            look_up();
+            load_k();
+          }
+        };
+        if (!first) next_k();
         ok = ok && tc_wait(&sh.v_empty[ring.at], ring.parity ^ 1, &sh.dead);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -278,7 +316,13 @@ __global__ void __launch_bounds__(RW_NT, 1)
         for (int i = 0; i < 8; ++i) put_codes(v_at, warp * 32 + i * 4 + r4, c, vw[i]);
         tc::fence_proxy_async();
         __syncwarp();
-        if (lane == 0) tc::bar_arrive(&sh.v_full[ring.at]);
+        ++tile_no;
+        if (lane == 0) {
+          tc::bar_arrive(&sh.v_full[ring.at]);
+          __threadfence_block();
+          *const_cast<volatile uint32_t*>(&sh.v_tile[warp]) = tile_no;
+        }
+        if (first) next_k();
         if (have) load_v();
         ring.step();
         info.step();
@@ -506,6 +550,7 @@ __global__ void __launch_bounds__(RW_NT, 1)
     TcRing<2> buf, before(1);  // this tile's buffer, and that of the tile before
     before.parity = 1;
     TcRing<RW_INFO> info;
+    uint32_t tile_no = 0;
     PaMeta meta{-1, 0};
     int rows_done = 0;
     for (int un = 0;; ++un) {
@@ -527,6 +572,7 @@ __global__ void __launch_bounds__(RW_NT, 1)
       float m = TC_NONE, l = 0.f;
       for (int tile = u.t0; tile < u.t1; ++tile, buf.step(), before.step(), info.step()) {
         const bool first_tile = tile == u.t0;
+        ++tile_no;
         bad |= !tc_wait(&sh.s_full[buf.at], buf.parity, &sh.dead);
         bad = __any_sync(0xffffffffu, bad);
         const uint32_t own_s = tmem + buf.at * 128 + g * 64 + lanes;
@@ -599,6 +645,13 @@ __global__ void __launch_bounds__(RW_NT, 1)
             for (int i = 0; i < 16; ++i) over = fmaxf(over, fmaxf(x[i].x, x[i].y));
             bool move = over + (F8 ? sh.lift_top[info.at][2 * g + h] : 0.f) > m + TC_SLACK;
             if (F8 && __any_sync(0xffffffffu, move)) {  // so says a bound: now token by token
+              // A value of zeros has a scale all the same: it adds nothing, and lifts the reference as the least scale does.  (All
+              // warps of the group write the same; to one that does not move, either scale of such a token is right.)
+              bad |= !rw_put(&sh.v_tile[2 * g + h], tile_no, &sh.dead);
+              bad = __any_sync(0xffffffffu, bad);
+              const uint32_t slot = tc::smem_u32(vslots + ((tile_no - 1) % RW_RING) * RW_SLOT);
+              if (rw_nonzero(slot, t0 + lane) == 0) sh.v_scale[info.at][t0 + lane] = 0.f, sh.lift[info.at][t0 + lane] = PA_LEAST_LIFT;
+              __syncwarp();
               const uint32_t lift = tc::smem_u32(sh.lift[info.at] + t0);
               over = -INFINITY;
 #pragma unroll

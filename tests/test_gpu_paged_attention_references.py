@@ -79,3 +79,36 @@ def test_value_scales_that_alternate_by_tiles(cuda, Hq, Hkv, W, d, dt):
         scale = torch.exp2(torch.where((torch.arange(n) // run) % 2 == 0, -63, 63).double())[:, None].expand(n, Hkv)
         put(p, "v", 0, 100 * torch.randn(n, Hkv, d, generator=g).double() * scale[..., None], scale=scale)
         p.run(cuda).check()
+
+
+@e4_forms
+@pytest.mark.parametrize("above", [0.0, 5.0, 8.0, 12.0, 15.0, 40.0])
+@pytest.mark.parametrize("where", [[0], [77], [199], list(range(64, 128)), list(range(0, 200, 3))], ids=len)
+def test_values_of_zeros_far_above_the_others(cuda, Hq, Hkv, W, d, dt, above, where):
+    """A row of zeros has scale 1 in the cache, other rows one after their size: such a token may score `above` nats more than all
+    that add something, and leaves the others' 11 (21) bits."""
+    n = 200
+    g = torch.Generator().manual_seed(len(where))
+    p = Problem([n, 300], W, Hq, Hkv, d, 16, E4, dt, dt)
+    k, v = 0.3 * torch.randn(2, n, Hkv, d, generator=g).double()
+    k[:, :, 0] = 0
+    k[where] = 0
+    k[where, :, 0] = (above + 3.0) * d ** 0.5 / 4.0
+    v[where] = 0
+    put(p, "k", 0, k)
+    put(p, "v", 0, v)
+    p.q[0, ..., 0] = 4.0
+    p.run(cuda).check()
+
+
+@e4_forms
+def test_nothing_but_values_of_zeros(cuda, Hq, Hkv, W, d, dt):
+    """All of a request's values are zeros, of scale 1 or any other."""
+    n = 150
+    g = torch.Generator().manual_seed(d)
+    for e in (0, -63, 63):
+        p = Problem([n], W, Hq, Hkv, d, 16, E4, dt, dt)
+        put(p, "v", 0, torch.zeros(n, Hkv, d).double(), scale=torch.full((n, Hkv), 2.0 ** e).double())
+        put(p, "k", 0, 30 * torch.randn(n, Hkv, d, generator=g).double())
+        p.run(cuda).check()
+        assert not p.out.any()
