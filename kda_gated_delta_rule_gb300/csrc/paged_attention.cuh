@@ -46,8 +46,12 @@ constexpr int PA_UNIT_COST = 2;
 constexpr int PA_SHARE = 2;  // positions on the line that a warp takes at least
 constexpr int PA_MAX_LEN = 0x7fffff00;  // token positions and the next tile's stay within 32 bits
 constexpr float PA_LOG2E = 1.4426950408889634f, PA_LN2 = 0.6931471805599453f;
-// how far (in powers of two) scores may run above the softmax reference before it is moved
-constexpr float PA_SLACK = 6.f;
+// How far (in powers of two) scores may run above the softmax reference before it is moved, and how far above it the largest
+// lies when it has moved.  fp16 probabilities use that type's range: up to 2^15 (the value scale's rounding to `lift` included),
+// so that they keep all their bits down to 2^-14 and are lost below 2^-25 only, 2^-34 of the largest.  fp32 calls move at
+// less, for which the second part reaches to 2^-39: below fp32's own bits over a quarter of a million tokens.
+constexpr float pa_head(bool f8, bool fine) { return f8 ? fine ? 14.f : 9.f : 0.f; }
+constexpr float pa_slack(bool f8) { return f8 ? 15.f : 6.f; }
 constexpr float PA_LEAST_LIFT = -62.f;  // of the least value scale, 2^-63
 
 // What the main kernel leaves for the join, per warp.
@@ -604,7 +608,7 @@ __global__ void __launch_bounds__(PA_NT, pa_resident(NT)) paged_attention_kernel
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int c = 0; c < 2; ++c) move |= top[t][c] > m[t][c] + PA_SLACK;
+          for (int c = 0; c < 2; ++c) move |= top[t][c] > m[t][c] + pa_slack(F8);
         if (__any_sync(0xffffffffu, move)) {
           if constexpr (F8) {
             // a value of zeros has a scale all the same: it adds nothing, and lifts the reference as the least scale does
@@ -644,7 +648,7 @@ __global__ void __launch_bounds__(PA_NT, pa_resident(NT)) paged_attention_kernel
               x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
               x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
               x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-              const float mn = fmaxf(m[t][c], x);
+              const float mn = fmaxf(m[t][c], x - pa_head(F8, FINE));
               const float down = m[t][c] == mn ? 0.f : m[t][c] - mn, by = ex2(down);  // 0 from -infinity
               m[t][c] = mn;
               mu[t][c] = mn == -INFINITY ? 0.f : mn;

@@ -643,7 +643,7 @@ __global__ void __launch_bounds__(RW_NT, 1)
             float over = -INFINITY;
 #pragma unroll
             for (int i = 0; i < 16; ++i) over = fmaxf(over, fmaxf(x[i].x, x[i].y));
-            bool move = over + (F8 ? sh.lift_top[info.at][2 * g + h] : 0.f) > m + TC_SLACK;
+            bool move = over + (F8 ? sh.lift_top[info.at][2 * g + h] : 0.f) > m + pa_slack(F8);
             if (F8 && __any_sync(0xffffffffu, move)) {  // so says a bound: now token by token
               // A value of zeros has a scale all the same: it adds nothing, and lifts the reference as the least scale does.  (All
               // warps of the group write the same; to one that does not move, either scale of such a token is right.)
@@ -660,10 +660,10 @@ __global__ void __launch_bounds__(RW_NT, 1)
                 const float2 y = add2(x[2 * i], make_float2(s.x, s.y)), z = add2(x[2 * i + 1], make_float2(s.z, s.w));
                 over = fmaxf(over, fmaxf(fmaxf(y.x, y.y), fmaxf(z.x, z.y)));
               }
-              move = over > m + TC_SLACK;
+              move = over > m + pa_slack(F8);
             }
             if (__any_sync(0xffffffffu, move)) {
-              const float mn = fmaxf(m, ceilf(over)), by = mn - m > 126.f ? 0.f : __uint_as_float((uint32_t)(127 - (int)(mn - m)) << 23);
+              const float mn = fmaxf(m, ceilf(over) - pa_head(F8, false)), by = mn - m > 126.f ? 0.f : __uint_as_float((uint32_t)(127 - (int)(mn - m)) << 23);
               l = F8 && mn - m > 126.f ? times_pow2(l, m - mn) : l * by;
               m = mn;
               if (h == 1) {  // the first 32 tokens' probabilities

@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(TcCfg<RB>::NT, 1)
       float over = -INFINITY;
 #pragma unroll
       for (int r = 0; r < RG; ++r) over = fmaxf(over, x[r] - m[r]);
-      if (tc::named_bar_or(bar_id, 128, over > TC_SLACK)) {
+      if (tc::named_bar_or(bar_id, 128, over > pa_slack(false))) {
         // ---- references move: the rows' maxima over the 128 tokens, then sums and accumulators follow
 #pragma unroll
         for (int r = 0; r < RG; ++r) {

@@ -112,3 +112,25 @@ def test_nothing_but_values_of_zeros(cuda, Hq, Hkv, W, d, dt):
         put(p, "k", 0, 30 * torch.randn(n, Hkv, d, generator=g).double())
         p.run(cuda).check()
         assert not p.out.any()
+
+
+@e4_forms
+@pytest.mark.parametrize("above", [6.0, 9.0, 12.0, 14.5])
+@pytest.mark.parametrize("at", [0, 199])
+def test_channels_of_unlikely_tokens_only(cuda, Hq, Hkv, W, d, dt, above, at):
+    """A token that scores `above` nats (up to 21 powers of two) more than all others has a value in channel 0 alone: the other
+    channels are sums of small probabilities, which have their 11 (21) bits all the same."""
+    n = 200
+    g = torch.Generator().manual_seed(at)
+    p = Problem([n, 300], W, Hq, Hkv, d, 16, E4, dt, dt)
+    k, v = 0.1 * torch.randn(2, n, Hkv, d, generator=g).double()
+    v *= 10
+    k[:, :, 0] = 0
+    k[at] = 0
+    k[at, :, 0] = above * d ** 0.5 / 4.0
+    v[at] = 0
+    v[at, :, 0] = 3.0
+    put(p, "k", 0, k)
+    put(p, "v", 0, v)
+    p.q[0, ..., 0] = 4.0
+    p.run(cuda).check()
