@@ -134,3 +134,32 @@ def test_channels_of_unlikely_tokens_only(cuda, Hq, Hkv, W, d, dt, above, at):
     put(p, "v", 0, v)
     p.q[0, ..., 0] = 4.0
     p.run(cuda).check()
+
+
+ALL_FORMS = [(BF, 4, 1, 1, 128, BF), (BF, 16, 1, 1, 128, BF), (BF, 12, 1, 2, 128, BF), (BF, 4, 2, 1, 64, BF),
+             (BF, 6, 2, 2, 32, F32)] + [(E4, *f) for f in E4_FORMS]
+all_forms = pytest.mark.parametrize("kind,Hq,Hkv,W,d,dt", ALL_FORMS)
+
+
+@all_forms
+@pytest.mark.parametrize("size", [1e16, 1e18])
+def test_scores_far_below_zero(cuda, kind, Hq, Hkv, W, d, dt, size):
+    """Equal scores of about -1e32 and -1e36: the result is the values' mean (bf16's and fp16's rounding of it at most), and its
+    log-sum-exp the score."""
+    n = 300
+    p = Problem([n, 5], W, Hq, Hkv, d, 16, kind, dt, dt)
+    for i, m in enumerate(p.lens):
+        k = torch.zeros(m, Hkv, d).double()
+        k[:, :, 0] = -size
+        put(p, "k", i, k)
+    p.q.zero_()
+    p.q[..., 0] = size
+    p.run(cuda, scale=1.0)
+    for i, m in enumerate(p.lens):
+        v = p.rows(p.vd, i)
+        score = float(p.q[0, 0, 0, 0]) * float(p.rows(p.kd, i)[0, 0, 0])
+        for w in range(W):
+            want = v[:m - W + 1 + w].mean(0).repeat_interleave(Hq // Hkv, 0)
+            got = p.out[i, w].cpu().double()
+            assert torch.all((got - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -10 * v.abs().mean(0).repeat_interleave(Hq // Hkv, 0))
+        assert torch.all((p.lse[i].cpu().double() / score - 1).abs() <= 2.0 ** -20)
