@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(PA_NT, pa_resident(NT)) paged_attention_kernel
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
         int e = amax > 0.f ? 14 - ((int)(__float_as_uint(amax) >> 23) - 127) : 0;
-        e = max(-100, min(100, e));
+        e = min(100, e);  // -114 at least
         up = __uint_as_float((uint32_t)(e + 127) << 23);
         down = __uint_as_float((uint32_t)(127 - e) << 23);
       }
@@ -573,9 +573,9 @@ __global__ void __launch_bounds__(PA_NT, pa_resident(NT)) paged_attention_kernel
           for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              float x = s[q][t][i] * f[t][i & 1];
-              if constexpr (F8) x *= ksn[q][i >> 1];
-              s[q][t][i] = x;
+              float x = s[q][t][i];
+              if constexpr (F8) x *= ksn[q][i >> 1];  // first: a large query's factor and a small key's scale make up for one another
+              s[q][t][i] = x * f[t][i & 1];
             }
           if (a.softcap > 0.f) {
 #pragma unroll

@@ -521,7 +521,7 @@ __global__ void __launch_bounds__(RW_NT, 1)
 #pragma unroll
             for (int j = 1; j < 16; j <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, j));
             int e = top > 0 && top <= 0x7f800000u ? 14 - ((int)(top >> 23) - 127) : 0;
-            e = max(-100, min(100, e));
+            e = min(100, e);  // -114 at least
             const float up = __uint_as_float((uint32_t)(e + 127) << 23);
             if (c == 0) sh.factor[buf][r] = per_unit * __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
@@ -598,8 +598,8 @@ __global__ void __launch_bounds__(RW_NT, 1)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                   const float4 s = ld_shared4(ks + 16 * i);
-                  x[2 * i] = mul2(mul2(x[2 * i], both(factor)), make_float2(s.x, s.y));
-                  x[2 * i + 1] = mul2(mul2(x[2 * i + 1], both(factor)), make_float2(s.z, s.w));
+                  x[2 * i] = mul2(mul2(x[2 * i], make_float2(s.x, s.y)), both(factor));
+                  x[2 * i + 1] = mul2(mul2(x[2 * i + 1], make_float2(s.z, s.w)), both(factor));
                 }
               } else {
 #pragma unroll
@@ -620,7 +620,7 @@ __global__ void __launch_bounds__(RW_NT, 1)
                 float y[8];
                 tc::tmem_ld8(own_s + 32 * h + c, y);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] = capped_any(y[i] * factor * (F8 ? sh.k_scale[info.at][t0 + c + i] : 1.f), cap2);
+                for (int i = 0; i < 8; ++i) y[i] = capped_any(y[i] * (F8 ? sh.k_scale[info.at][t0 + c + i] : 1.f) * factor, cap2);
                 tc::tmem_st8f(own_s + 32 * h + c, y);
               }
               tc::tmem_wait_st();

@@ -163,3 +163,12 @@ def test_scores_far_below_zero(cuda, kind, Hq, Hkv, W, d, dt, size):
             got = p.out[i, w].cpu().double()
             assert torch.all((got - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -10 * v.abs().mean(0).repeat_interleave(Hq // Hkv, 0))
         assert torch.all((p.lse[i].cpu().double() / score - 1).abs() <= 2.0 ** -20)
+
+
+@all_forms
+@pytest.mark.parametrize("qscale,kscale", [(1e36, 1e-18), (4e37, 1e-16), (1e-30, 1e17)])
+def test_queries_at_the_ends_of_fp32(cuda, kind, Hq, Hkv, W, d, dt, qscale, kscale):
+    """Ordinary scores of very large or very small queries and keys of the opposite size."""
+    scale = d ** -0.5 / (qscale * kscale)
+    p = Problem([70, 257], W, Hq, Hkv, d, 16, kind, dt, dt, qscale=qscale, kscale=kscale).run(cuda, scale=scale)
+    p.check(scale=scale)
