@@ -159,7 +159,7 @@ def lib_path() -> str:
 
 def load(build_if_missing: bool = False):
     """Loads libkda.so; raises if it is not built (no fallback path exists)."""
-    global _lib
+    global _lib, _packed
     if _lib is not None:
         return _lib
     if not os.path.exists(_build.LIB):
@@ -238,11 +238,13 @@ def load(build_if_missing: bool = False):
             raise RuntimeError(f"{name} layout mismatch between include/kda.h and the binding")
     # The attention calls' argument structs go over as packed bytes (their mirrors cost a microsecond to fill, more than
     # the rest of such a call's marshalling); function objects of their own, since the pointer type differs.
+    packed = {}
     for name, args in (("kda_qk_norm_rope", [st, vp]), ("kda_qk_norm_rope_backward", [st, vp, vp, c_int, vp, vp, vp, sz, vp]),
                        ("kda_kv_write", [vp, vp, i64, i64, c_int, i64, vp, st, vp, vp]),
                        ("kda_kv_read", [st, vp, i64, vp, vp, c_int, vp, vp]), ("kda_paged_attention", [st, vp])):
-        _packed[name] = lib[name]
-        _packed[name].restype, _packed[name].argtypes = c_int, args
+        packed[name] = lib[name]
+        packed[name].restype, packed[name].argtypes = c_int, args
+    _packed = packed  # whole: another thread's call takes a table that is there for a loaded library
     _lib = lib
     return lib
 
