@@ -159,8 +159,9 @@ struct Piece {
 };
 
 // cap2 * tanh(y) given z = 2 log2(e) y, with cap2 = cap * log2(e): 1 - 2 / (1 + 2^z), within 1.2e-7 of tanh absolutely.
-// That is the score's precision up to caps of PA_NEAR_CAP; above, scores much smaller than the cap keep theirs by
-// the odd series to y^7 below |y| = 0.15 (next term 6e-9 relative there).
+// That is up to 8e-6 of a score (and of the log-sum-exp) at the cap PA_NEAR_CAP, below the 16-bit probabilities' bits; above it, scores much smaller
+// than the cap keep theirs by the odd series to y^7 below |y| = 0.15 (next term 6e-9 relative there).  fp32 calls take
+// CUDA's tanhf, which loses nothing of small scores.
 constexpr float PA_NEAR_CAP = 64.f;
 __device__ __forceinline__ float capped(float z, float cap2) {
   float r;
@@ -341,7 +342,7 @@ __global__ void __launch_bounds__(PA_NT, pa_resident(NT)) paged_attention_kernel
     const int page_at0 = page_at, off0 = off, page0 = page, page_next0 = page_next;  // to walk again
 
     // ---- queries of the unit in the first product's operand order: row n of each column block, this lane's pieces
-    float f[NT][2];   // per query row of this lane's results: score in powers of two per unit of the product
+    float f[NT][2];   // per query row of this lane's results: score in powers of two (or the cap's argument) per unit of the product
     int last[NT][2];  // and its last seen position
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -389,7 +390,7 @@ __global__ void __launch_bounds__(PA_NT, pa_resident(NT)) paged_attention_kernel
             qs[((part * NT + t) * KS + u * (C::KC / 4) + c / 4) * 32] = r;
           }
         }
-      const float own = down * a.scale * (a.softcap > 0.f ? 2.f * PA_LOG2E / a.softcap : PA_LOG2E);
+      const float own = down * a.scale * (a.softcap > 0.f ? (FINE ? 1.f : 2.f * PA_LOG2E) / a.softcap : PA_LOG2E);
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         f[t][c] = __shfl_sync(0xffffffffu, own, (2 * j + c) * 4);
@@ -583,8 +584,12 @@ __global__ void __launch_bounds__(PA_NT, pa_resident(NT)) paged_attention_kernel
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 const float z = s[q][t][i];
-                s[q][t][i] = capped(z, cap2);
-                if (a.softcap > PA_NEAR_CAP && fabsf(z) < 0.3f * PA_LOG2E) s[q][t][i] = capped_series(z, cap2);
+                if constexpr (FINE) {
+                  s[q][t][i] = cap2 * tanhf(z);
+                } else {
+                  s[q][t][i] = capped(z, cap2);
+                  if (a.softcap > PA_NEAR_CAP && fabsf(z) < 0.3f * PA_LOG2E) s[q][t][i] = capped_series(z, cap2);
+                }
               }
           }
           if (partly) {

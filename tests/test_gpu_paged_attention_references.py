@@ -172,3 +172,21 @@ def test_queries_at_the_ends_of_fp32(cuda, kind, Hq, Hkv, W, d, dt, qscale, ksca
     scale = d ** -0.5 / (qscale * kscale)
     p = Problem([70, 257], W, Hq, Hkv, d, 16, kind, dt, dt, qscale=qscale, kscale=kscale).run(cuda, scale=scale)
     p.check(scale=scale)
+
+
+@kinds
+@pytest.mark.parametrize("softcap", [1.0, 10.0, 30.0, 64.0, 65.0, 1000.0])
+@pytest.mark.parametrize("size", [0.01, 0.5, 3.0])
+def test_small_scores_under_a_cap_in_fp32(cuda, kind, softcap, size):
+    """Scores well below the cap, with fp32 queries and outputs, have fp32's precision: their products have one term each, so
+    the bound leaves little to anything else."""
+    lens, Hq, d = [1, 2, 3, 40], 32, 16
+    g = torch.Generator().manual_seed(int(softcap))
+    p = Problem(lens, 1, Hq, 4, d, 16, kind, F32, F32)
+    for i, n in enumerate(lens):
+        k = torch.zeros(n, 4, d).double()
+        k[:, :, 0] = 1 + torch.rand(n, 4, generator=g).double()
+        put(p, "k", i, k)
+    p.q[..., 0] = size * torch.randn(len(lens), 1, Hq, generator=g).cuda()
+    p.q[..., 1:] = 0
+    p.run(cuda, scale=1.0, softcap=softcap).check(scale=1.0, softcap=softcap)
