@@ -357,7 +357,9 @@ __global__ void __launch_bounds__(RW_NT, 1)
         if (more) look_up();
         const unsigned mask = __ballot_sync(0xffffffffu, there);
         const uint32_t bytes = __popc(mask) * box * TC_D * 2;
+        // the warp goes on or leaves as one: no lane copies what another does not wait for
         ok = ok && tc_wait(&sh.k_empty[ring.at], ring.parity ^ 1, &sh.dead);
+        ok = __all_sync(0xffffffffu, ok);
         if (lane < 4 && ok) {  // 32 tokens of the tile each; a box has at least 16
           uint32_t w = 0;
           for (int s = 0; s < 2; ++s)
@@ -376,10 +378,11 @@ __global__ void __launch_bounds__(RW_NT, 1)
         if (two && ok) tc::tma_load_2d(kslots + ring.at * RW_SLOT + piece, &maps.k, odd * 64, two_row, &sh.k_full[ring.at]);
         const bool k_sent = ok;
         ok = ok && tc_wait(&sh.v_empty[ring.at], ring.parity ^ 1, &sh.dead);
+        ok = __all_sync(0xffffffffu, ok);
         if (lane == 0 && ok) tc::bar_arrive_expect_tx(&sh.v_full[ring.at], bytes);
         __syncwarp();
         if (two && ok) tc::tma_load_2d(vslots + ring.at * RW_SLOT + piece, &maps.v, odd * 64, two_row, &sh.v_full[ring.at]);
-        if (!__all_sync(0xffffffffu, ok)) {
+        if (!ok) {
           // let what is on its way arrive before the CTA ends: this round's copies and those of the rounds just before
           if (lane == 0) {
             flag_status(a.status, KDA_DEV_TIMEOUT);

@@ -196,7 +196,9 @@ __global__ void __launch_bounds__(TcCfg<RB>::NT, 1)
       // A slot's n-th use waits for the release of the one before (the first finds the round before the first over).
       // The tile's list of boxes goes by its number: it has been read when its V is released, which the copies of VS tiles
       // later wait for.
+      // The warp goes on or leaves as one: no lane copies what another does not wait for.
       ok = ok && tc_wait(&sh.k_empty[kr.at], kr.parity ^ 1, &sh.dead);
+      ok = __all_sync(0xffffffffu, ok);
       if (lane == 0 && ok) {
         sh.there[info.at] = (int)mask;
         tc::bar_arrive_expect_tx(&sh.k_full[kr.at], bytes);
@@ -209,10 +211,11 @@ __global__ void __launch_bounds__(TcCfg<RB>::NT, 1)
       if (two && ok) tc::tma_load_2d(slots + kr.at * SLOT + piece, &maps.k, odd * 64, two_row, &sh.k_full[kr.at]);
       const bool k_sent = ok;
       ok = ok && tc_wait(&sh.v_empty[vr.at], vr.parity ^ 1, &sh.dead);
+      ok = __all_sync(0xffffffffu, ok);
       if (lane == 0 && ok) tc::bar_arrive_expect_tx(&sh.v_full[vr.at], bytes);
       __syncwarp();
       if (two && ok) tc::tma_load_2d(vslots + vr.at * SLOT + piece, &maps.v, odd * 64, two_row, &sh.v_full[vr.at]);
-      if (!__all_sync(0xffffffffu, ok)) {
+      if (!ok) {
         // let what is on its way arrive before the CTA ends: this round's copies and those of the rounds just before
         if (lane == 0) {
           flag_status(a.status, KDA_DEV_TIMEOUT);
@@ -533,6 +536,7 @@ __global__ void __launch_bounds__(TcCfg<RB>::NT, 1)
         if (lane == 0) sh.red[quarter][rfirst + r] = t;
       }
       bad |= !tc_wait(&sh.o_full, it.unit_no & 1, &sh.dead);
+      bad = __any_sync(0xffffffffu, bad);  // the careful way out is a warp's
       tc::fence_after_sync();
       tc::named_bar(bar_id, 128);
       float o[PP * RG];
