@@ -77,11 +77,15 @@ size_t kda_state_bytes_per_head(int dk, int dv);
  * input copies left out: no copy is issued, so its first wait for the inputs finds nothing to wait for,
  * gives up after a short bounded poll, and every CTA flags KDA_DEV_TIMEOUT in dev_status and returns (its
  * tensor memory freed, nothing in flight).  The records are then not written; nothing else is touched.
+ * KDA_TEST_FAULT_STALL_CACHE_COPIES makes the tensor-memory forms of later kda_paged_attention calls (d = 128, bf16 queries
+ * and outputs) leave at the third tile of a worker's share (of a unit, with an e4m3 cache) as if a bounded wait had run
+ * out: the worker lets its copies arrive, flags KDA_DEV_TIMEOUT and returns; rows that it had a part of are not defined.
  * KDA_TEST_FAULT_NONE (the initial value) restores normal calls.  Process-wide, not thread-safe; for tests.
  * Returns KDA_ERR_INVALID_ARG for an unknown value.
  */
 #define KDA_TEST_FAULT_NONE 0
 #define KDA_TEST_FAULT_STALL_RECORD_INPUTS 1
+#define KDA_TEST_FAULT_STALL_CACHE_COPIES 2
 kda_status kda_set_test_fault(int fault);
 
 /*

@@ -27,11 +27,11 @@ __all__ = [
     "kda_kcp_fragments", "kda_kcp_scan", "kda_kcp_outputs", "kda_check_slot_ids", "kda_set_debug_checks",
     "kda_qk_norm_rope", "kda_qk_norm_rope_backward", "kda_qk_norm_rope_backward_workspace_size", "kda_kv_write",
     "kda_kv_read", "kda_paged_attention", "kda_paged_attention_workspace_size",
-    "kda_debug_checks", "kda_set_test_fault", "KDA_TEST_FAULT_NONE", "KDA_TEST_FAULT_STALL_RECORD_INPUTS", "CFBI_CHUNK", "CFBI_ROW_FLOATS", "EXPORTED_SYMBOLS",
+    "kda_debug_checks", "kda_set_test_fault", "KDA_TEST_FAULT_NONE", "KDA_TEST_FAULT_STALL_RECORD_INPUTS", "KDA_TEST_FAULT_STALL_CACHE_COPIES", "CFBI_CHUNK", "CFBI_ROW_FLOATS", "EXPORTED_SYMBOLS",
 ]
 
 KDA_OK = 0
-KDA_TEST_FAULT_NONE, KDA_TEST_FAULT_STALL_RECORD_INPUTS = 0, 1
+KDA_TEST_FAULT_NONE, KDA_TEST_FAULT_STALL_RECORD_INPUTS, KDA_TEST_FAULT_STALL_CACHE_COPIES = 0, 1, 2
 KDA_DEV_SLOT_OOB, KDA_DEV_SEQ_OOB, KDA_DEV_TIMEOUT, KDA_DEV_ACCEPT_OOB = 1, 2, 4, 8
 KDA_DEV_POS_OOB, KDA_DEV_PAGE_OOB = 16, 32
 F32, BF16 = 0, 1

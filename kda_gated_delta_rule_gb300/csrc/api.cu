@@ -187,7 +187,9 @@ const char* kda_status_string(kda_status s) {
 int kda_version(void) { return kVersion; }
 
 kda_status kda_set_test_fault(int fault) {
-  if (fault != KDA_TEST_FAULT_NONE && fault != KDA_TEST_FAULT_STALL_RECORD_INPUTS) return KDA_ERR_INVALID_ARG;
+  if (fault != KDA_TEST_FAULT_NONE && fault != KDA_TEST_FAULT_STALL_RECORD_INPUTS &&
+      fault != KDA_TEST_FAULT_STALL_CACHE_COPIES)
+    return KDA_ERR_INVALID_ARG;
   g_test_fault = fault;
   return KDA_OK;
 }
@@ -802,6 +804,7 @@ kda_status kda_paged_attention(const kda_paged_attention_args* a, kda_stream_t s
   p.lse = a->lse;
   p.ws = static_cast<float*>(a->workspace);
   p.status = a->dev_status;
+  p.test_stall = g_test_fault == KDA_TEST_FAULT_STALL_CACHE_COPIES;
   return from_cuda(kda::launch_paged_attention(p, reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -264,6 +264,7 @@ struct PagedAttnArgs {
   float* lse;
   float* ws;  // paged_attention_ws_bytes
   int32_t* status;
+  bool test_stall;  // test hook (kda_set_test_fault): the tensor-memory forms' copies give up
 };
 size_t paged_attention_ws_bytes(int W, int Hq, int Hkv, int d);
 cudaError_t launch_paged_attention(const PagedAttnArgs& a, cudaStream_t s);

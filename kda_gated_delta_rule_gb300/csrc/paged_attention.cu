@@ -53,6 +53,7 @@ cudaError_t launch_paged_attention(const PagedAttnArgs& a, cudaStream_t s) {
   PaPlan p;
   p.G = a.Hq / a.c.Hkv;
   p.rows = a.W * p.G;
+  p.stall = a.test_stall;
   if (p.rows > PA_ROWS_FROM && pa_rows_supported(a)) {
     p.blocks = (p.rows + PA_ROWS_BLOCK - 1) / PA_ROWS_BLOCK;
     lay_out(p, reinterpret_cast<char*>(a.ws), PA_SMS, PA_ROWS_BLOCK, a.c.d);

@@ -73,6 +73,7 @@ struct PaPlan {  // derived on the host
   float* part_ml;  // [warp][2][RB][2]
   PaMeta* meta;    // [warp]
   int workers;     // warps launched (entries of meta)
+  bool stall;      // a test of the bounded waits (tensor-memory forms)
 };
 
 // ---------------------------------------------------------------- instructions

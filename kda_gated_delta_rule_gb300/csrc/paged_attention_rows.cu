@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(RW_NT, 1)
     } else if (warp == 0) {
       // ---- bf16: lane i places box i of the next tile; its page's id is asked for a tile ahead
       const int boxes = TC_TILE / box;
-      int page = 0, off = 0;
+      int page = 0, off = 0, tile_no = 0;
       bool next_there = false;
       auto look_up = [&]() {
         const int64_t tok = (int64_t)it.u.start + (int64_t)it.tile * TC_TILE + lane * box;
@@ -377,6 +377,7 @@ __global__ void __launch_bounds__(RW_NT, 1)
         const uint32_t piece = odd * RW_BLOCK + (lane >> 1) * box * 128;
         if (two && ok) tc::tma_load_2d(kslots + ring.at * RW_SLOT + piece, &maps.k, odd * 64, two_row, &sh.k_full[ring.at]);
         const bool k_sent = ok;
+        if (p.stall && tile_no++ == TC_STALL_AT) ok = tc_give_up(&sh.dead);
         ok = ok && tc_wait(&sh.v_empty[ring.at], ring.parity ^ 1, &sh.dead);
         ok = __all_sync(0xffffffffu, ok);
         if (lane == 0 && ok) tc::bar_arrive_expect_tx(&sh.v_full[ring.at], bytes);
@@ -437,6 +438,7 @@ __global__ void __launch_bounds__(RW_NT, 1)
         if (t1 == 0) break;
         for (int t = t0; t < t1; ++t) {
           if (warp == 12) {
+            if (F8 && p.stall && t == t0 + TC_STALL_AT) ok = tc_give_up(&sh.dead);
             ok = ok && tc_wait(&sh.p_free[buf.at], buf.parity ^ 1, &sh.dead);
             ok = ok && tc_wait(&sh.k_full[ring.at], ring.parity, &sh.dead);
             if (!ok) break;

@@ -161,6 +161,7 @@ __global__ void __launch_bounds__(TcCfg<RB>::NT, 1)
     // This lane's box of the next tile: its page's id is asked for a tile ahead, its place among the pages follows from the
     // last tile's.
     const int per_tile = TC_TILE / a.c.page_size, rest = TC_TILE - per_tile * a.c.page_size;
+    int tile_no = 0;
     bool more = it.next(a, p, box), next_there = false;
     int next_page = 0, pg = 0, off = 0;
     const int32_t* table = nullptr;
@@ -210,6 +211,7 @@ __global__ void __launch_bounds__(TcCfg<RB>::NT, 1)
       const uint32_t piece = odd * (TC_TILE * 128) + (lane >> 1) * box * 128;
       if (two && ok) tc::tma_load_2d(slots + kr.at * SLOT + piece, &maps.k, odd * 64, two_row, &sh.k_full[kr.at]);
       const bool k_sent = ok;
+      if (p.stall && tile_no++ == TC_STALL_AT) ok = tc_give_up(&sh.dead);
       ok = ok && tc_wait(&sh.v_empty[vr.at], vr.parity ^ 1, &sh.dead);
       ok = __all_sync(0xffffffffu, ok);
       if (lane == 0 && ok) tc::bar_arrive_expect_tx(&sh.v_full[vr.at], bytes);

@@ -88,6 +88,15 @@ __device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, int* dea
   return false;
 }
 
+// For tests of the way out (kda_set_test_fault): the copying warp leaves as if its wait for a slot had run out, at this tile of its
+// share, with the copies of those before it and of its keys on their way.  (Of an e4m3 cache, which has no such copies, the first
+// product's warp, at this tile of a unit: any statement more in the loaders cost the calls 10 %.)
+constexpr int TC_STALL_AT = 2;
+__device__ __forceinline__ bool tc_give_up(int* dead) {
+  *reinterpret_cast<volatile int*>(dead) = 1;
+  return false;
+}
+
 // One row of a part by one warp, token by token in fp32: the way out when the accumulators hold a NaN, which may come from
 // a query that meets a token it does not see (0 * NaN) or from an infinity meeting a split probability.  A lane has
 // channels 4 lane .. 4 lane + 3.
