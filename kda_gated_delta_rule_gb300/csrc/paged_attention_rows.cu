@@ -84,19 +84,15 @@ __device__ __forceinline__ uint4 load_codes(const void* pages, int64_t row, int 
   return w;
 }
 
-// cap2 * tanh(y) as in paged_attention.cuh, for |y| <= 0.75 (|z| <= RW_POLY): y times a polynomial in y^2 for tanh(y) / y (a
-// weighted least-squares fit that levels the relative error, 1.3e-7 in fp32), its coefficients multiplied out to
-// powers of z.  Seven multiplications and additions instead of two operations of the exponential's unit, which the
-// exponentials already fill; and no cancellation below large caps.
-constexpr float RW_POLY = 1.5f * PA_LOG2E;
+// capped_near of paged_attention.cuh for two scores, its coefficients multiplied out to powers of z.  Seven multiplications and
+// additions instead of two operations of the exponential's unit.
 struct CapPoly {
   float k[6];
   __device__ __forceinline__ explicit CapPoly(float cap2) {
     constexpr float h = 0.5f * PA_LN2, h2 = h * h;
-    constexpr float c[6] = {1.f, -0.333329588f, 0.133254066f, -0.0533444285f, 0.0195829086f, -0.0047162571f};
     float w = cap2 * h;
 #pragma unroll
-    for (int i = 0; i < 6; ++i) k[i] = c[i] * w, w *= h2;
+    for (int i = 0; i < 6; ++i) k[i] = pa_tanh(i) * w, w *= h2;
   }
   __device__ __forceinline__ float2 operator()(float2 z) const {
     const float2 u = mul2(z, z);
@@ -106,10 +102,6 @@ struct CapPoly {
     return mul2(z, t);
   }
 };
-__device__ __forceinline__ float capped_any(float z, float cap2) {
-  return fabsf(z) < 0.3f * PA_LOG2E ? capped_series(z, cap2) : capped(z, cap2);
-}
-
 __device__ __forceinline__ uint32_t pack_f16(float2 x) {
   const __half2 h = __floats2half2_rn(x.x, x.y);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -614,7 +606,7 @@ __global__ void __launch_bounds__(RW_NT, 1)
               float top = 0.f;
 #pragma unroll
               for (int i = 0; i < 16; ++i) top = fmaxf(top, fmaxf(fabsf(x[i].x), fabsf(x[i].y)));
-              if (__all_sync(0xffffffffu, top <= RW_POLY)) {
+              if (__all_sync(0xffffffffu, top <= PA_NEAR)) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) x[i] = cap_poly(x[i]);
                 break;
@@ -625,7 +617,7 @@ __global__ void __launch_bounds__(RW_NT, 1)
                 float y[8];
                 tc::tmem_ld8(own_s + 32 * h + c, y);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] = capped_any(y[i] * (F8 ? sh.k_scale[info.at][t0 + c + i] : 1.f) * factor, cap2);
+                for (int i = 0; i < 8; ++i) y[i] = capped(y[i] * (F8 ? sh.k_scale[info.at][t0 + c + i] : 1.f) * factor, cap2);
                 tc::tmem_st8f(own_s + 32 * h + c, y);
               }
               tc::tmem_wait_st();

@@ -416,13 +416,15 @@ __global__ void __launch_bounds__(TcCfg<RB>::NT, 1)
         x[r] *= f.x, x[r + 1] *= f.y, x[r + 2] *= f.z, x[r + 3] *= f.w;
       }
       if (a.softcap > 0.f) {
-        if (a.softcap <= PA_NEAR_CAP) {
+        bool near = true;
 #pragma unroll
-          for (int r = 0; r < RG; ++r) x[r] = capped(x[r], cap2);
+        for (int r = 0; r < RG; ++r) near = near && fabsf(x[r]) <= PA_NEAR;
+        if (__all_sync(0xffffffffu, near)) {
+#pragma unroll
+          for (int r = 0; r < RG; ++r) x[r] = capped_near(x[r], cap2);
         } else {
 #pragma unroll
-          for (int r = 0; r < RG; ++r)
-            x[r] = fabsf(x[r]) < 0.3f * PA_LOG2E ? capped_series(x[r], cap2) : capped(x[r], cap2);
+          for (int r = 0; r < RG; ++r) x[r] = capped(x[r], cap2);
         }
       }
       if (masked) {

@@ -174,19 +174,25 @@ def test_queries_at_the_ends_of_fp32(cuda, kind, Hq, Hkv, W, d, dt, qscale, ksca
     p.check(scale=scale)
 
 
+# types, and Hq, Hkv, W: fp32 in the register form, then each form with bf16
+CAPPED = [(F32, 32, 4, 1), (BF, 32, 4, 1), (BF, 128, 128, 1), (BF, 24, 1, 1), (BF, 12, 1, 2)]
+
+
 @kinds
+@pytest.mark.parametrize("dt,Hq,Hkv,W", CAPPED)
 @pytest.mark.parametrize("softcap", [1.0, 10.0, 30.0, 64.0, 65.0, 1000.0])
 @pytest.mark.parametrize("size", [0.01, 0.5, 3.0])
-def test_small_scores_under_a_cap_in_fp32(cuda, kind, softcap, size):
-    """Scores well below the cap, with fp32 queries and outputs, have fp32's precision: their products have one term each, so
-    the bound leaves little to anything else."""
-    lens, Hq, d = [1, 2, 3, 40], 32, 16
+def test_small_scores_under_a_cap(cuda, kind, dt, Hq, Hkv, W, softcap, size):
+    """Scores well below the cap have fp32's precision: their products have one term each, so the bound (of the log-sum-exp, with
+    bf16 types) leaves little to anything else."""
+    lens = [1, 2, 3, 40]
+    d = 16 if dt == F32 else 128
     g = torch.Generator().manual_seed(int(softcap))
-    p = Problem(lens, 1, Hq, 4, d, 16, kind, F32, F32)
+    p = Problem(lens, W, Hq, Hkv, d, 16, kind, dt, dt)
     for i, n in enumerate(lens):
-        k = torch.zeros(n, 4, d).double()
-        k[:, :, 0] = 1 + torch.rand(n, 4, generator=g).double()
+        k = torch.zeros(n, Hkv, d).double()
+        k[:, :, 0] = 1 + torch.rand(n, Hkv, generator=g).double()
         put(p, "k", i, k)
-    p.q[..., 0] = size * torch.randn(len(lens), 1, Hq, generator=g).cuda()
+    p.q[..., 0] = (size * torch.randn(len(lens), W, Hq, generator=g)).to(dt).cuda()
     p.q[..., 1:] = 0
     p.run(cuda, scale=1.0, softcap=softcap).check(scale=1.0, softcap=softcap)
