@@ -52,7 +52,9 @@ constexpr float PA_LOG2E = 1.4426950408889634f, PA_LN2 = 0.6931471805599453f;
 // less, for which the second part reaches to 2^-39: below fp32's own bits over a quarter of a million tokens.
 constexpr float pa_head(bool f8, bool fine) { return f8 ? fine ? 14.f : 9.f : 0.f; }
 constexpr float pa_slack(bool f8) { return f8 ? 15.f : 6.f; }
-constexpr float PA_LEAST_LIFT = -62.f;  // of the least value scale, 2^-63
+// The lift of the least value scale, 2^-63; where nothing else counts, the sum's terms are then up to 2^62 (and the rounding of such
+// exponents, 2^-18, shows in the log-sum-exp as 1e-6).
+constexpr float PA_LEAST_LIFT = -62.f;
 
 // What the main kernel leaves for the join, per warp.
 struct PaMeta {
@@ -105,6 +107,14 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ float times_pow2(float v, float d) {
   const float near = fmaxf(d, -64.f);
   return v * ex2(near) * ex2(d - near);
+}
+// ln(l 2^m): l's power of two goes to m first, so that what is rounded has the result's size (l itself is up to 2^71 where
+// references lie that far below the scores).
+__device__ __forceinline__ float log_sum(float m, float l) {
+  const uint32_t b = __float_as_uint(l);
+  const int e = (int)(b >> 23) - 127;
+  if (e < -126 || e > 127) return (m + log2f(l)) * PA_LN2;  // 0, infinity, NaN
+  return (m + (float)e + log2f(__uint_as_float((b & 0x7fffffu) | 0x3f800000u))) * PA_LN2;
 }
 __device__ __forceinline__ uint32_t half2_of_codes(uint32_t two) {
   uint32_t r;
@@ -646,7 +656,7 @@ __global__ void __launch_bounds__(PA_NT, pa_resident(NT)) paged_attention_kernel
 #pragma unroll
               for (int i = 0; i < 2; ++i) {  // this lane's tokens n and n + 8
                 const uint32_t of = (n & 1 ? other[2 * i + 1] : other[2 * i]) >> (n >> 1) & 0x11111111u;
-                if (of == 0) lift[q][i] = PA_LEAST_LIFT, vsn[q][i] = 0.f, zeros = true;
+                if (of == 0) lift[q][i] = PA_LEAST_LIFT + pa_head(F8, FINE), vsn[q][i] = 0.f, zeros = true;
               }
             }
             if (__any_sync(0xffffffffu, zeros)) {
@@ -790,7 +800,7 @@ __global__ void __launch_bounds__(PA_NT, pa_resident(NT)) paged_attention_kernel
         }
         if (n == 0) {
           if (!whole) *reinterpret_cast<float2*>(p.part_ml + (part + r) * 2) = make_float2(m[t][c], x);
-          else if (a.lse) a.lse[head] = none ? -INFINITY : (m[t][c] + log2f(x)) * PA_LN2;
+          else if (a.lse) a.lse[head] = none ? -INFINITY : log_sum(m[t][c], x);
         }
       }
     if (whole) {
@@ -899,7 +909,7 @@ __global__ void __launch_bounds__(SL == 1 ? 256 : 32 * SL) paged_attention_join_
       }
     }
     if (lane == 0) {
-      if (a.lse) a.lse[head] = none ? -INFINITY : (m + log2f(l)) * PA_LN2;
+      if (a.lse) a.lse[head] = none ? -INFINITY : log_sum(m, l);
       add_work(a.status, 1);
     }
   };

@@ -647,7 +647,8 @@ __global__ void __launch_bounds__(RW_NT, 1)
               bad |= !rw_put(&sh.v_tile[2 * g + h], tile_no, &sh.dead);
               bad = __any_sync(0xffffffffu, bad);
               const uint32_t slot = tc::smem_u32(vslots + ((tile_no - 1) % RW_RING) * RW_SLOT);
-              if (rw_nonzero(slot, t0 + lane) == 0) sh.v_scale[info.at][t0 + lane] = 0.f, sh.lift[info.at][t0 + lane] = PA_LEAST_LIFT;
+              if (rw_nonzero(slot, t0 + lane) == 0)
+                sh.v_scale[info.at][t0 + lane] = 0.f, sh.lift[info.at][t0 + lane] = PA_LEAST_LIFT + pa_head(F8, false);
               __syncwarp();
               const uint32_t lift = tc::smem_u32(sh.lift[info.at] + t0);
               over = -INFINITY;
@@ -787,7 +788,7 @@ __global__ void __launch_bounds__(RW_NT, 1)
         nan = !none && isnan(check.x + check.y);
         if (head >= 0 && g == 0) {
           if (!whole) *reinterpret_cast<float2*>(p.part_ml + (part_at + tk) * 2) = make_float2(mr, lr);
-          else if (a.lse) a.lse[heads + head] = none ? -INFINITY : (mr + log2f(lr)) * PA_LN2;
+          else if (a.lse) a.lse[heads + head] = none ? -INFINITY : log_sum(mr, lr);
         }
       }
       const uint32_t nans = __ballot_sync(0xffffffffu, nan && head >= 0);
@@ -808,7 +809,7 @@ __global__ void __launch_bounds__(RW_NT, 1)
             y.x = pack_bf16(o.x * by, o.y * by);
             y.y = pack_bf16(o.z * by, o.w * by);
             *reinterpret_cast<uint2*>(static_cast<bf16*>(a.out) + at * TC_D + 4 * lane) = y;
-            if (lane == 0 && a.lse) a.lse[at] = none ? -INFINITY : (mr + log2f(lr)) * PA_LN2;
+            if (lane == 0 && a.lse) a.lse[at] = none ? -INFINITY : log_sum(mr, lr);
           } else {
             *reinterpret_cast<float4*>(p.part_o + (part_at + r) * TC_D + 4 * lane) = o;
             if (lane == 0) *reinterpret_cast<float2*>(p.part_ml + (part_at + r) * 2) = make_float2(mr, lr);

@@ -526,7 +526,7 @@ __global__ void __launch_bounds__(TcCfg<RB>::NT, 1)
         if (whole) {
           const int64_t head = (int64_t)u.b * a.W * a.Hq + hd;
           static_cast<bf16*>(a.out)[head * TC_D + tk] = __float2bfloat16_rn(none ? 0.f : y / lr);
-          if (tk == 0 && a.lse) a.lse[head] = none ? -INFINITY : (mr + log2f(lr)) * PA_LN2;
+          if (tk == 0 && a.lse) a.lse[head] = none ? -INFINITY : log_sum(mr, lr);
         } else {
           p.part_o[(part_at + r) * TC_D + tk] = y;
           if (tk == 0) *reinterpret_cast<float2*>(p.part_ml + (part_at + r) * 2) = make_float2(mr, lr);
@@ -572,7 +572,7 @@ __global__ void __launch_bounds__(TcCfg<RB>::NT, 1)
             y.x = tc::pack2(__float2bfloat16_rn(o.x * by), __float2bfloat16_rn(o.y * by));
             y.y = tc::pack2(__float2bfloat16_rn(o.z * by), __float2bfloat16_rn(o.w * by));
             *reinterpret_cast<uint2*>(static_cast<bf16*>(a.out) + head * TC_D + 4 * lane) = y;
-            if (lane == 0 && a.lse) a.lse[head] = none ? -INFINITY : (mr + log2f(lr)) * PA_LN2;
+            if (lane == 0 && a.lse) a.lse[head] = none ? -INFINITY : log_sum(mr, lr);
           } else {
             *reinterpret_cast<float4*>(p.part_o + (part_at + r) * TC_D + 4 * lane) = o;
             if (lane == 0) *reinterpret_cast<float2*>(p.part_ml + (part_at + r) * 2) = make_float2(mr, lr);

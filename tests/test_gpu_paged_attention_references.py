@@ -4,6 +4,7 @@ without a value, scales at both ends of their range, scores at the ends of fp32.
 import pytest
 import torch
 
+from tests import _attention as ref
 from tests._attention_rows import put
 from tests.test_gpu_paged_attention import BF, E4, Problem
 
@@ -196,3 +197,26 @@ def test_small_scores_under_a_cap(cuda, kind, dt, Hq, Hkv, W, softcap, size):
     p.q[..., 0] = (size * torch.randn(len(lens), W, Hq, generator=g)).to(dt).cuda()
     p.q[..., 1:] = 0
     p.run(cuda, scale=1.0, softcap=softcap).check(scale=1.0, softcap=softcap)
+
+
+@e4_forms
+def test_log_sum_exp_with_values_of_zeros(cuda, Hq, Hkv, W, d, dt):
+    """Values of zeros of scale 1 put the references 62 powers of two below the scores.  Scores of one term each: the bound on the
+    log-sum-exp leaves 2^-20 to the exponentials, and here 2^-19 more to the rounding of exponents up to 64."""
+    lens = [1, 2, 3, 9]
+    g = torch.Generator().manual_seed(d)
+    p = Problem(lens, W, Hq, Hkv, d, 16, E4, dt, dt)
+    for i, n in enumerate(lens):
+        k = torch.zeros(n, Hkv, d).double()
+        k[:, :, 0] = 1 + torch.rand(n, Hkv, generator=g).double()
+        put(p, "k", i, k)
+        put(p, "v", i, torch.zeros(n, Hkv, d).double(), scale=torch.ones(n, Hkv).double())
+    p.q[..., 0] = 0.3 * torch.randn(len(lens), W, Hq, generator=g).to(dt).cuda()
+    p.q[..., 1:] = 0
+    p.run(cuda, scale=1.0)
+    lse = p.lse.cpu().double()
+    for i, n in enumerate(lens):
+        want = ref.attend(p.q[i].cpu().double(), p.rows(p.kd, i), p.rows(p.vd, i), n, 1.0)
+        none = want[1] == -float("inf")
+        _, tol = ref.attend_bound(*want, d, n, dt == BF, 11)
+        assert torch.all((lse[i] - want[1])[~none].abs() <= tol[~none] + 2.0 ** -19)
