@@ -505,9 +505,10 @@ kda_status kda_kcp_outputs(const kda_prefill_args* a, int32_t segment_len, const
 /*
  * Softmax-attention layers beside the KDA layers
  * ----------------------------------------------
- * A hybrid model interleaves KDA layers with layers that attend over a key/value cache ("Kimi K3:
- * Architecture and SGLang Day-0 Support", layer layout: 69 KDA and 24 full-attention layers).  These calls are
- * what such a layer does to a token between its projections: the per-head norm of queries and keys (with a
+ * A hybrid model interleaves KDA layers with layers that attend over a key/value cache.  (In the model of "Kimi K3:
+ * Architecture and SGLang Day-0 Support" those are 24 layers of latent attention, MLA, with other row sizes and no rotation,
+ * which these calls do not serve; they are for layers of grouped-head attention with keys and values of one size.)  These
+ * calls are what such a layer does to a token between its projections: the per-head norm of queries and keys (with a
  * position rotation where the model has one), the write into a paged cache, and the attention of the newest
  * tokens over that cache.  Queries have Hq heads, keys and values Hkv, and query head h attends with
  * key/value head h / (Hq / Hkv).  Head sizes d in {16, 32, 64, 128}.  In these calls index arrays (positions,
@@ -554,7 +555,8 @@ size_t kda_qk_norm_rope_args_bytes(void);
  * that token's rows are not written. */
 kda_status kda_qk_norm_rope(const kda_qk_norm_rope_args* a, kda_stream_t stream);
 
-/* Workspace of kda_qk_norm_rope_backward: 608 * 2 * d * 4 bytes of partial weight gradients. */
+/* Workspace of kda_qk_norm_rope_backward: 608 * 2 * d * 4 bytes for partial weight gradients, d floats for each CTA that the
+ * kernel launches, of which there are at most 304 (the rest is unused). */
 size_t kda_qk_norm_rope_backward_workspace_size(int64_t T, int Hq, int Hkv, int d);
 
 /*

@@ -215,7 +215,7 @@ struct NormArgs {
   int64_t q_out_stride, k_out_stride;
   int32_t* status;
 };
-// Rows of partial weight gradients that a workspace holds, one per CTA of the backward (it launches half as many)
+// Pairs of rows of d partial weight gradients that a workspace has room for; the backward uses a row per CTA, of at most 304
 constexpr int NORM_BWD_CTAS = 608;
 cudaError_t launch_qk_norm_rope(const NormArgs& a, cudaStream_t s);
 // q_out, k_out receive dq, dk; partial: NORM_BWD_CTAS * 2 * d floats

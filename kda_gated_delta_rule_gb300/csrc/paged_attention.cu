@@ -11,9 +11,11 @@ size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 namespace {
 
 // More query rows per cached row than this take the many-rows form: its time hardly grows up to 128 (64 requests of 500 to 6000
-// tokens, 24 rows and 96: 31 and 34 us with bf16, 38 and 42 with e4m3), where the register form's grows with the rows (55
-// and 108; 50 and 92).  At 12 and 16 rows that one is as fast (bf16: 35 against 32) or faster (e4m3: 29 against 40), and
-// on longer caches faster (90 requests of 2227 to 8908 tokens: 59 against 66, 48 against 88).
+// tokens, 24 rows and 96: 29 and 33 us with bf16, 39 and 44 with e4m3), where the register form's grows with the rows (52
+// and 94; 48 and 78).  At 12 and 16 rows that one is as fast with bf16 (31 and 32 against 29; 90 requests of 2227 to 8908 tokens:
+// 57 and 58 against 57) and faster with e4m3 (28 and 29 against 38; 46 and 47 against 88).  Units of a tile or less are the
+// many-rows form's worst case (239 requests of 4 tokens, 8 drafts, 32 heads over 8: 80 against 48 us with bf16, 89 against 45 with e4m3; of
+// 64 tokens 78 against 87, 87 against 76): the host knows no lengths, and a table wide enough for long ones says nothing.
 constexpr int PA_ROWS_FROM = 16;
 
 // The workspace's places for `workers` warps or CTAs with row blocks of rb.
@@ -59,10 +61,10 @@ cudaError_t launch_paged_attention(const PagedAttnArgs& a, cudaStream_t s) {
     lay_out(p, reinterpret_cast<char*>(a.ws), PA_SMS, PA_ROWS_BLOCK, a.c.d);
     return pa_rows(a, p, sms, s);
   }
-  // With few units the tensor-memory form's larger and so fewer parts join faster (one request with 8 heads, of 1000 tokens: 11
-  // against 13 us, of 4096: 13 against 17, of 262144: 164 against 168; 64 units of 100 to 30000 tokens: 46 against 55);
-  // with many units of few rows their starts and ends cost it more (64 units of 4096 tokens: 33 against 33 us, 128: 55
-  // against 52).
+  // With few units the tensor-memory form's larger and so fewer parts join faster (one request with 8 heads, of 1000 tokens: 10.5
+  // against 12.2 us, of 4096: 13.3 against 15.7, of 262144: 164 against 167; 64 units of 100 to 30000 tokens: 43.6 against
+  // 44.0); with many units of few rows their starts and ends cost it more (64 units of 4096 tokens: 35 against 33 us, 128: 56
+  // against 53).
   if (pa_tc_supported(a) && p.rows <= 16 && (int64_t)a.B * a.c.Hkv <= 64) {
     const int rb = pa_tc_row_block(p.rows);
     p.blocks = 1;

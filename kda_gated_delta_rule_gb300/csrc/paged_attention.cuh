@@ -3,8 +3,9 @@
 // Per query row (a query head of one window token), over the positions it sees, with x = scale q.k (capped:
 // cap tanh(x / cap)):  out = sum exp(x - m) v / sum exp(x - m),  lse = m + log sum exp(x - m).
 //
-// Bound by HBM: a cached row of d channels feeds the few query rows of its head group (Hq / Hkv heads x W tokens),
-// so each K or V element is read once and used for 2 multiplications per query row.
+// Bound by HBM: a cached row of d channels feeds the few query rows of its head group (Hq / Hkv heads x W tokens), so each K
+// or V element is used for 2 multiplications per query row.  It is read once per block of query rows: once where they are
+// up to RB (8, 16 or 32; 16 at most with fp32 queries or outputs), three times for 96 bf16 rows, six times for 96 fp32 ones.
 //
 // Work.  A unit is one request, key/value head and block of RB = 8 NT query rows.  All units' caches, cut into tiles
 // of TILE tokens, form one line; the warps take equal consecutive shares of it, so ragged lengths balance without
@@ -12,15 +13,18 @@
 // than it has, for its queries, first loads and output.  A warp that has a whole unit writes its output; the parts of a
 // unit cut across warps go to the workspace (each warp has at most one part that continues a unit and one that
 // starts one) and a second, small kernel joins them in order.  Warps never wait on one another after the share-out:
-// the other warps of the SM cover one's latencies.  256 requests of 65 to 8191 tokens, 12 heads over 4: 96 us with e4m3 (4.8
-// TB/s, 70 % of the copy rate: latency of dependent instructions at 12 warps per SM), 143 us with bf16 (91 %).
+// the other warps of the SM cover one's latencies.  256 requests of 65 to 8191 tokens, 12 heads over 4: 96.5 us with e4m3 (4.8
+// TB/s, 70 % of the copy rate: latency of dependent instructions at 12 warps per SM), 142 us with bf16 (92 %); with fp32
+// queries and outputs 110 and 145 us; at d = 64 69 and 87 us (51 and 75 %: twice the rows for the same bytes).
 //
 // K and V go from global memory straight into the operand registers of mma.m16n8k16 (no transposes, no shared memory
 // for them): the products are S^T = K Q^T and O^T = V^T P^T with the tokens resp. channels as the 16-row side and 8
 // query rows as columns.  The channel order inside a product's K steps is free as long as Q follows it, so a lane's
 // operands for consecutive steps are one 16-byte piece of its token's row; V's pairs of tokens are put together from two
-// such pieces by byte permutes.  The 5th-generation tensor instructions want 64 or 128 rows and both operands in shared
-// or tensor memory; with 1 to 32 query rows they would sit idle behind the same loads.
+// such pieces by byte permutes.  The 5th-generation tensor instructions take both operands from shared or tensor memory, where a
+// bf16 cache comes by TMA as it lies: that is paged_attention_tc.cu, for few units, and paged_attention_rows.cu, for
+// many query rows.  This form has all other calls: e4m3 codes need a pass through registers to become an operand, which
+// this form makes of the operand's own load, and units that are many and short would pay those forms' starts and ends.
 //
 // e4m3 caches: codes become fp16 (exact), q is scaled per row by a power of two into fp16's range (exact for bf16 q
 // down to 2^-31 of the row's maximum), the key's scale multiplies the score and the value's scale the

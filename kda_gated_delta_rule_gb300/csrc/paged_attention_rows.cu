@@ -13,11 +13,12 @@
 //   warps 12 and 13   issue the two products;
 //   warps 14 and 15   put the next unit's queries into operand order.
 //
-// Bound by the softmax warps.  A tile's 128 x 128 scores are 128 exponentials a lane and scheduler, 1024 cycles of their unit,
+// Bound by the softmax warps, and with an e4m3 cache by the loaders next to them (forty instructions more in their loop over
+// the tiles cost 10 %, so what can be seen elsewhere is not looked at there).  A tile's 128 x 128 scores are 128 exponentials a lane and scheduler, 1024 cycles of their unit,
 // and with cap and scales about 20 more operations each; measured, a tile takes 3500 cycles (bf16) to 6000 (e4m3 with
 // cap), the products 1024 to 1536 under them.  Code that runs once is dear (a cold instruction costs about 4 cycles, and a
 // share has some ten tiles), so tiles go in two equal passes over one compact body, and rare cases in small loops.
-// 64 requests of 500 to 6000 tokens (window 4096), 8 drafts, 12 heads over 1, cap: 39 us (bf16) and 44 us (e4m3); with the
+// 64 requests of 500 to 6000 tokens (window 4096), 8 drafts, 12 heads over 1, cap: 37.5 us (bf16) and 45.5 us (e4m3); with the
 // queries as the products' column operand 88 and 100 us.
 //
 // Waits are bounded: one that gives up sets KDA_DEV_TIMEOUT and a flag on which every role leaves.

@@ -14,9 +14,9 @@
 // warp or four, each passing through its code once per tile, so a role's time per tile is its instructions' latency (5
 // to 10 cycles each): that is what was shortened (look-ups without divisions, roles on warps of their own).  With an 8-bit
 // cache (1400 cycles a tile) the same roles were slower than the register form of paged_attention.cuh, multiplied as
-// e4m3 with the 16-bit side in parts (125 against 119 us at 262144 tokens): that cache keeps the register form.
+// e4m3 with the 16-bit side in parts (125 us at 262144 tokens, where that form takes 109): that cache keeps it.
 //
-// One request with 32 heads over 8: of 262144 tokens 165 us (6.5 TB/s, 96 % of the copy rate), of 1000 tokens 10.6 us, a chain
+// One request with 32 heads over 8: of 262144 tokens 161 to 164 us (6.6 TB/s, 97 % of the copy rate), of 1000 tokens 10.7 us, a chain
 // of launches, share-out, first copies and the join.
 //
 // Waits are bounded: one that gives up sets KDA_DEV_TIMEOUT and a flag on which every role leaves.

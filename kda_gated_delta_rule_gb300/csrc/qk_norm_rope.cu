@@ -2,7 +2,9 @@
 //
 // Forward, per row x (one token, one head) with weight w:  y = R(p) (x r w),  r = (mean x^2 + eps)^-1/2.
 // Backward, with g = R(p)^T dy:  dx = r g w - x r^3 mean(g w x),  dw = sum over rows of g x r.
-// R(p) only mixes the two channels of a pair, so its transpose is the rotation by the opposite angle.
+// R(p) only mixes the two channels of a pair, so its transpose is the rotation by the opposite angle.  All sums are in fp32: with
+// fp32 rows dx is off by 6e-8 (rms) and dw, a sum over all rows, by 2e-7 (8000 tokens x 40 heads x 128: 2.5e-7), as much as
+// with one operation after the other.
 //
 // Both are bound by HBM (about 10 operations per element against 4 to 6 bytes), but only if the instructions are few.
 // A row lies on D/8 lanes.  A lane has two runs of four channels, placed so that both channels of a pair are its own:
