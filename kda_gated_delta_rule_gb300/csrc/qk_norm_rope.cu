@@ -3,8 +3,8 @@
 // Forward, per row x (one token, one head) with weight w:  y = R(p) (x r w),  r = (mean x^2 + eps)^-1/2.
 // Backward, with g = R(p)^T dy:  dx = r g w - x r^3 mean(g w x),  dw = sum over rows of g x r.
 // R(p) only mixes the two channels of a pair, so its transpose is the rotation by the opposite angle.  All sums are in fp32: with
-// fp32 rows dx is off by 6e-8 (rms) and dw, a sum over all rows, by 2e-7 (8000 tokens x 40 heads x 128: 2.5e-7), as much as
-// with one operation after the other.
+// fp32 rows dx is off by 6e-8 (rms) and dw, a sum over all rows, by 1.5e-7 (8000 tokens x 40 heads x 128: 2e-7); torch
+// operations one after the other are off by 7e-8 and 1.2e-7 (3.8e-7).
 //
 // Both are bound by HBM (about 10 operations per element against 4 to 6 bytes), but only if the instructions are few.
 // A row lies on D/8 lanes.  A lane has two runs of four channels, placed so that both channels of a pair are its own:
@@ -254,6 +254,13 @@ __global__ void __launch_bounds__(NORM_NT, norm_resident(INBF)) qk_norm_rope_ker
   }
 }
 
+// Sum of N floats (a power of two) STRIDE apart, in pairs of pairs: a few roundings instead of one per term.
+template <int N, int STRIDE>
+__device__ __forceinline__ float pair_sum(const float* p) {
+  if constexpr (N == 1) return *p;
+  else return pair_sum<N / 2, STRIDE>(p) + pair_sum<N / 2, STRIDE>(p + N / 2 * STRIDE);
+}
+
 // Backward.  The first ctas_q CTAs walk the query rows, the others the key rows, in proportion to the heads, so a lane
 // holds one weight and one set of weight gradients in registers over its whole walk.  The CTA adds its groups' sums
 // up in shared memory in a fixed order, and one row of partial sums per CTA goes to the workspace.
@@ -348,10 +355,7 @@ __global__ void __launch_bounds__(NORM_BWD_NT, NORM_BWD_RESIDENT)
   }
   __syncthreads();
   for (int e = threadIdx.x; e < D; e += NORM_BWD_NT) {
-    float v = 0.f;
-#pragma unroll
-    for (int i = 0; i < NG; ++i) v += sum[i][e];
-    partial[(int64_t)blockIdx.x * D + e] = v;
+    partial[(int64_t)blockIdx.x * D + e] = pair_sum<NG, D + 4>(&sum[0][e]);
   }
   if (p.status) {
     const int total = __reduce_add_sync(0xffffffffu, lr == 0 ? written : 0);
@@ -360,7 +364,7 @@ __global__ void __launch_bounds__(NORM_BWD_NT, NORM_BWD_RESIDENT)
 }
 
 // Adds the CTAs' partial weight gradients, the queries' in blocks 0 .. D/16 - 1 and the keys' in the rest: 16 channels per
-// CTA, the partial rows spread over its 32 half-warps and then added in their order, so the result does not depend on
+// CTA, the partial rows spread over its 32 half-warps and then added pair by pair, so the result does not depend on
 // timing.
 __global__ void __launch_bounds__(512) qk_norm_weight_grad_kernel(const float* __restrict__ partial, int ctas_q, int ctas,
                                                                   int D, float* __restrict__ dwq,
@@ -376,12 +380,7 @@ __global__ void __launch_bounds__(512) qk_norm_weight_grad_kernel(const float* _
   for (int i = lo + w; i < hi; i += 32) v += partial[(int64_t)i * D + e];
   part[w][c] = v;
   __syncthreads();
-  if (w == 0) {
-    v = 0.f;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v += part[i][c];
-    (isq ? dwq : dwk)[e] = v;
-  }
+  if (w == 0) (isq ? dwq : dwk)[e] = pair_sum<32, 17>(&part[0][c]);
 }
 
 namespace {
