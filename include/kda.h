@@ -57,9 +57,11 @@ typedef enum { KDA_DTYPE_F32 = 0, KDA_DTYPE_BF16 = 1 } kda_dtype;
 #define KDA_DEV_SLOT_OOB 1   /* a slot id outside [0, num_slots) */
 #define KDA_DEV_SEQ_OOB 2    /* cu_seqlens not non-decreasing within [0, T], or a sequence longer than max_seqlen */
 #define KDA_DEV_TIMEOUT 4    /* a bounded wait inside a kernel gave up */
-#define KDA_DEV_ACCEPT_OOB 8 /* an accepted length outside [0, W] */
+#define KDA_DEV_ACCEPT_OOB 8 /* an accepted length outside [0, W], or a number of drafts outside [0, W - 1] */
 #define KDA_DEV_POS_OOB 16   /* a token position outside the rotation table */
 #define KDA_DEV_PAGE_OOB 32  /* a page id or a token slot outside the paged cache */
+#define KDA_DEV_TOKEN_OOB 64 /* a drafted token outside [0, V) */
+#define KDA_DEV_PROB_OOB 128 /* a row of probabilities that holds no weight, or sums to 31 or more */
 
 /* Human-readable name of a status code (static storage). */
 const char* kda_status_string(kda_status s);
@@ -660,6 +662,115 @@ size_t kda_paged_attention_workspace_size(int B, int W, int Hq, int Hkv, int d);
 /* kda_paged_attention -- enqueue it.  A length outside [0, max_pages * page_size], or above 2^31 - 256, sets
  * KDA_DEV_SEQ_OOB and counts as 0; a page id outside [0, num_pages) sets KDA_DEV_PAGE_OOB and its tokens are seen by no query. */
 kda_status kda_paged_attention(const kda_paged_attention_args* a, kda_stream_t stream);
+
+/*
+ * kda_prefill_attention -- causal attention of whole prompts, packed one behind another.
+ * Sequence i is tokens cu_seqlens[i] .. cu_seqlens[i + 1] - 1.  The query of token t (position p in its sequence) sees the keys of
+ * its sequence at positions max(0, p - window + 1) .. p (window = 0: 0 .. p).  Per query head, with x = scale * q.k
+ * (softcap > 0: softcap * tanh(x / softcap)):
+ *   out = sum_j exp(x_j - m) v_j / sum_j exp(x_j - m),   lse = m + log sum_j exp(x_j - m).
+ * The head layout is kda_qk_norm_rope's (its q_out, k_out and the projection's values go in as they are), the result that of
+ * kda_paged_attention over a cache that holds the sequence, to rounding.  Sums and softmax statistics are fp32; with bf16 inputs
+ * the probabilities are rounded to bf16 for their product with the values.
+ * Rows outside every sequence are neither read into a result nor written.  What a query does not see does not matter to its row,
+ * NaN included.
+ */
+typedef struct {
+  const void* q;             /* [T][Hq][d] in_dtype, tokens q_stride elements apart */
+  const void* k;             /* [T][Hkv][d] in_dtype, tokens k_stride elements apart */
+  const void* v;             /* [T][Hkv][d] in_dtype, tokens v_stride elements apart */
+  int64_t q_stride, k_stride, v_stride;
+  kda_dtype in_dtype;
+  int64_t T;                 /* total packed tokens, at most 2^31 - 1024 */
+  int Hq, Hkv, d;            /* Hq a multiple of Hkv, at most 65535 */
+  int N;                     /* sequences, <= 65535 */
+  const int32_t* cu_seqlens; /* int32[N + 1] device, non-decreasing within [0, T] */
+  int32_t max_seqlen;        /* host: an upper bound on every sequence length */
+  float scale;               /* finite; 1 / sqrt(d) in most models */
+  float softcap;             /* 0: none */
+  int32_t window;            /* 0: everything before the query */
+  void* out;                 /* [T][Hq][d] out_dtype, tokens out_stride elements apart */
+  int64_t out_stride;
+  kda_dtype out_dtype;
+  float* lse;                /* [T][Hq] fp32, or NULL */
+  int32_t* dev_status;       /* optional int32[2]; the work counter counts query rows (token x head) */
+} kda_prefill_attention_args;
+
+/* sizeof(kda_prefill_attention_args), so a binding can check its mirror of the struct. */
+size_t kda_prefill_attention_args_bytes(void);
+
+/* kda_prefill_attention -- enqueue it.  Offsets out of order or outside [0, T], and a sequence longer than max_seqlen, set
+ * KDA_DEV_SEQ_OOB.  A sequence that is too long is not written, the others are; with offsets out of order it is not defined which
+ * sequences' rows are written. */
+kda_status kda_prefill_attention(const kda_prefill_attention_args* a, kda_stream_t stream);
+
+/*
+ * kda_prefill_attention_backward -- gradients of sum <d_out, out> through kda_prefill_attention.
+ * `a` describes the forward; a->out (of either type) and a->lse (required) are what it returned, and are read here.  With
+ * p = exp(x - lse), D = <d_out, out> and the cap's slope c = 1 - (x / softcap)^2 (1 without a cap):
+ *   dv_j = sum_i p_ij d_out_i,   dx_ij = p_ij (d_out_i . v_j - D_i) c_ij scale,   dq_i = sum_j dx_ij k_j,
+ *   dk_j = sum_i dx_ij q_i,   dk and dv summed over the query heads that share a key/value head.
+ * Every sum has one owner and a fixed order: the same call gives the same bits.  With bf16 inputs p and dx are rounded to bf16
+ * for the products that take them in.  Rows outside every sequence are not written.  A token that holds a NaN or an infinity
+ * (in q, k, v or d_out) may spread it to all gradients of its own sequence, never to another's.
+ */
+typedef struct {
+  const void* d_out;         /* [T][Hq][d] in_dtype, tokens d_out_stride elements apart */
+  int64_t d_out_stride;
+  void* dq;                  /* [T][Hq][d] grad_dtype, overwritten (not accumulated into) */
+  void* dk;                  /* [T][Hkv][d] */
+  void* dv;                  /* [T][Hkv][d] */
+  int64_t dq_stride, dk_stride, dv_stride;
+  kda_dtype grad_dtype;
+  void* workspace;           /* >= kda_prefill_attention_backward_workspace_size bytes of device scratch */
+  size_t workspace_bytes;
+} kda_prefill_attention_grads;
+
+/* sizeof(kda_prefill_attention_grads), so a binding can check its mirror of the struct. */
+size_t kda_prefill_attention_grads_bytes(void);
+
+size_t kda_prefill_attention_backward_workspace_size(int64_t T, int N, int Hq, int Hkv, int d);
+
+kda_status kda_prefill_attention_backward(const kda_prefill_attention_args* a, const kda_prefill_attention_grads* g,
+                                          kda_stream_t stream);
+
+/*
+ * kda_verify_accept -- which of a window's drafted tokens the target accepts, and the token that follows them: what stands between
+ * kda_verify (with kda_paged_attention in the attention layers) and kda_verify_replay.
+ * A window has W tokens: the first is already part of the text, the W - 1 others are drafts.  target_probs[b][i] is the target's
+ * distribution behind window token i, so it judges draft i (window token i + 1); draft_probs[b][i] is the one that draft i was
+ * drawn from.  Draft x = draft_tokens[b][i] is accepted when
+ *   uniform[b][i] * draft_probs[b][i][x] < target_probs[b][i][x]
+ * (in exact arithmetic; draft_probs NULL: the drafts were certain, its place is taken by 1), up to the first that is not; n of
+ * them are.  Then one token is drawn with r = uniform[b][W - 1]: the least v for which w(0) + .. + w(v) > r * sum w, with
+ *   w = max(target_probs[b][n] - draft_probs[b][n], 0) where draft n was refused (drafts certain: target_probs[b][n] without
+ *       that token), or target_probs[b][n] itself where that holds no weight or all drafts were accepted.
+ * Tokens so drawn have the target's distribution.  The sums are integers in units of 2^-58, so they depend on no order.
+ * NaN and negative probabilities count as zero; rows need not be normalised.
+ *   accepted[b] = n + 1: window tokens to commit, as kda_verify_replay takes it.
+ *   tokens[b] = the n accepted drafts, the drawn token, then -1.
+ * num_drafts[b] (NULL: W - 1) is how many drafts request b has; the others are not read.  A number outside [0, W - 1] sets
+ * KDA_DEV_ACCEPT_OOB and counts as 0.  A draft outside [0, V) sets KDA_DEV_TOKEN_OOB and is refused, the token then drawn from
+ * target_probs[b][n].  A row that holds no weight, or sums to 31 or more, sets KDA_DEV_PROB_OOB, and the drawn token is -1.
+ */
+typedef struct {
+  const void* target_probs;    /* [B][W][V] dtype */
+  const void* draft_probs;     /* [B][W - 1][V] dtype, or NULL */
+  kda_dtype dtype;
+  int B, W, V;                 /* W >= 1; 1 <= V <= 2^30 */
+  const int32_t* draft_tokens; /* int32[B][W - 1]; NULL when W = 1 */
+  const int32_t* num_drafts;   /* int32[B], or NULL */
+  const float* uniform;        /* [B][W] in [0, 1); other values count as the nearest within, NaN as 0 (in the draw) */
+  int32_t* accepted;           /* int32[B] */
+  int32_t* tokens;             /* int32[B][W] */
+  int32_t* dev_status;         /* optional int32[2]; the work counter counts accepted (n + 1 per request) */
+} kda_verify_accept_args;
+
+/* sizeof(kda_verify_accept_args), so a binding can check its mirror of the struct. */
+size_t kda_verify_accept_args_bytes(void);
+
+/* kda_verify_accept -- enqueue it.  Here every array needs its natural alignment only. */
+kda_status kda_verify_accept(const kda_verify_accept_args* a, kda_stream_t stream);
 
 #ifdef __cplusplus
 }

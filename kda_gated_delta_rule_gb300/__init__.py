@@ -17,7 +17,7 @@ from . import _build
 
 __all__ = [
     "KdaError", "load", "lib_path", "KDA_OK", "KDA_DEV_SLOT_OOB", "KDA_DEV_SEQ_OOB", "KDA_DEV_TIMEOUT",
-    "KDA_DEV_ACCEPT_OOB", "KDA_DEV_POS_OOB", "KDA_DEV_PAGE_OOB", "kda_status_string", "kda_version", "kda_state_bytes_per_head", "kda_state_copy",
+    "KDA_DEV_ACCEPT_OOB", "KDA_DEV_POS_OOB", "KDA_DEV_PAGE_OOB", "KDA_DEV_TOKEN_OOB", "KDA_DEV_PROB_OOB", "kda_status_string", "kda_version", "kda_state_bytes_per_head", "kda_state_copy",
     "kda_decode_step", "kda_replay_bytes", "kda_verify", "kda_verify_replay", "kda_prefill_varlen",
     "kda_prefill_workspace_size", "kda_prefill_segmented", "kda_segmented_workspace_size",
     "kda_segment_fragments", "kda_fragment_scan", "kda_segment_outputs", "kda_prefill_segmented_noalloc",
@@ -26,14 +26,15 @@ __all__ = [
     "kda_cfbi_decode", "kda_backward_workspace_size", "kda_prefill_backward", "kda_fused_decode",
     "kda_kcp_fragments", "kda_kcp_scan", "kda_kcp_outputs", "kda_check_slot_ids", "kda_set_debug_checks",
     "kda_qk_norm_rope", "kda_qk_norm_rope_backward", "kda_qk_norm_rope_backward_workspace_size", "kda_kv_write",
-    "kda_kv_read", "kda_paged_attention", "kda_paged_attention_workspace_size",
+    "kda_kv_read", "kda_paged_attention", "kda_paged_attention_workspace_size", "kda_prefill_attention",
+    "kda_prefill_attention_backward", "kda_prefill_attention_backward_workspace_size", "kda_verify_accept",
     "kda_debug_checks", "kda_set_test_fault", "KDA_TEST_FAULT_NONE", "KDA_TEST_FAULT_STALL_RECORD_INPUTS", "KDA_TEST_FAULT_STALL_CACHE_COPIES", "CFBI_CHUNK", "CFBI_ROW_FLOATS", "EXPORTED_SYMBOLS",
 ]
 
 KDA_OK = 0
 KDA_TEST_FAULT_NONE, KDA_TEST_FAULT_STALL_RECORD_INPUTS, KDA_TEST_FAULT_STALL_CACHE_COPIES = 0, 1, 2
 KDA_DEV_SLOT_OOB, KDA_DEV_SEQ_OOB, KDA_DEV_TIMEOUT, KDA_DEV_ACCEPT_OOB = 1, 2, 4, 8
-KDA_DEV_POS_OOB, KDA_DEV_PAGE_OOB = 16, 32
+KDA_DEV_POS_OOB, KDA_DEV_PAGE_OOB, KDA_DEV_TOKEN_OOB, KDA_DEV_PROB_OOB = 16, 32, 64, 128
 F32, BF16 = 0, 1
 CFBI_CHUNK, CFBI_ROW_FLOATS = 16, 420  # KDA_CFBI_CHUNK, KDA_CFBI_ROW_FLOATS
 
@@ -51,6 +52,9 @@ EXPORTED_SYMBOLS = (
     "kda_qk_norm_rope_args_bytes", "kda_qk_norm_rope", "kda_qk_norm_rope_backward_workspace_size",
     "kda_qk_norm_rope_backward", "kda_kv_cache_bytes", "kda_kv_write", "kda_kv_read",
     "kda_paged_attention_args_bytes", "kda_paged_attention_workspace_size", "kda_paged_attention",
+    "kda_prefill_attention_args_bytes", "kda_prefill_attention", "kda_prefill_attention_grads_bytes",
+    "kda_prefill_attention_backward_workspace_size", "kda_prefill_attention_backward", "kda_verify_accept_args_bytes",
+    "kda_verify_accept",
 )
 
 
@@ -135,6 +139,38 @@ class PagedAttentionArgs(ctypes.Structure):
     ]
 
 
+class PrefillAttentionArgs(ctypes.Structure):
+    """Mirror of kda_prefill_attention_args."""
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("q_stride", ctypes.c_int64),
+        ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64), ("in_dtype", ctypes.c_int), ("T", ctypes.c_int64),
+        ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int), ("d", ctypes.c_int), ("N", ctypes.c_int),
+        ("cu_seqlens", ctypes.c_void_p), ("max_seqlen", ctypes.c_int32), ("scale", ctypes.c_float),
+        ("softcap", ctypes.c_float), ("window", ctypes.c_int32), ("out", ctypes.c_void_p), ("out_stride", ctypes.c_int64),
+        ("out_dtype", ctypes.c_int), ("lse", ctypes.c_void_p), ("dev_status", ctypes.c_void_p),
+    ]
+
+
+class PrefillAttentionGrads(ctypes.Structure):
+    """Mirror of kda_prefill_attention_grads."""
+    _fields_ = [
+        ("d_out", ctypes.c_void_p), ("d_out_stride", ctypes.c_int64), ("dq", ctypes.c_void_p), ("dk", ctypes.c_void_p),
+        ("dv", ctypes.c_void_p), ("dq_stride", ctypes.c_int64), ("dk_stride", ctypes.c_int64),
+        ("dv_stride", ctypes.c_int64), ("grad_dtype", ctypes.c_int), ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class VerifyAcceptArgs(ctypes.Structure):
+    """Mirror of kda_verify_accept_args."""
+    _fields_ = [
+        ("target_probs", ctypes.c_void_p), ("draft_probs", ctypes.c_void_p), ("dtype", ctypes.c_int), ("B", ctypes.c_int),
+        ("W", ctypes.c_int), ("V", ctypes.c_int), ("draft_tokens", ctypes.c_void_p), ("num_drafts", ctypes.c_void_p),
+        ("uniform", ctypes.c_void_p), ("accepted", ctypes.c_void_p), ("tokens", ctypes.c_void_p),
+        ("dev_status", ctypes.c_void_p),
+    ]
+
+
 def _packer(mirror):
     """struct.Struct.pack for a mirror's fields in their native layout, a nested struct's fields in its place."""
     codes = {ctypes.c_void_p: "P", ctypes.c_int: "i", ctypes.c_int32: "i", ctypes.c_int64: "q", ctypes.c_size_t: "N",
@@ -149,6 +185,7 @@ def _packer(mirror):
 
 
 _pack_norm, _pack_cache, _pack_attention = map(_packer, (QkNormRopeArgs, KvCache, PagedAttentionArgs))
+_pack_prompt, _pack_grads, _pack_accept = map(_packer, (PrefillAttentionArgs, PrefillAttentionGrads, VerifyAcceptArgs))
 _packed = {}
 _lib = None
 
@@ -221,6 +258,14 @@ def load(build_if_missing: bool = False):
         "kda_paged_attention_args_bytes": (sz, []),
         "kda_paged_attention_workspace_size": (sz, [c_int, c_int, c_int, c_int, c_int]),
         "kda_paged_attention": (c_int, [ctypes.POINTER(PagedAttentionArgs), vp]),
+        "kda_prefill_attention_args_bytes": (sz, []),
+        "kda_prefill_attention": (c_int, [ctypes.POINTER(PrefillAttentionArgs), vp]),
+        "kda_prefill_attention_grads_bytes": (sz, []),
+        "kda_prefill_attention_backward_workspace_size": (sz, [i64, c_int, c_int, c_int, c_int]),
+        "kda_prefill_attention_backward": (c_int, [ctypes.POINTER(PrefillAttentionArgs),
+                                                   ctypes.POINTER(PrefillAttentionGrads), vp]),
+        "kda_verify_accept_args_bytes": (sz, []),
+        "kda_verify_accept": (c_int, [ctypes.POINTER(VerifyAcceptArgs), vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -233,7 +278,10 @@ def load(build_if_missing: bool = False):
     if lib.kda_fused_decode_args_bytes() != ctypes.sizeof(FusedDecodeArgs):
         raise RuntimeError("kda_fused_decode_args layout mismatch between include/kda.h and the binding")
     for name, mirror in (("kda_qk_norm_rope_args", QkNormRopeArgs), ("kda_kv_cache", KvCache),
-                         ("kda_paged_attention_args", PagedAttentionArgs)):
+                         ("kda_paged_attention_args", PagedAttentionArgs),
+                         ("kda_prefill_attention_args", PrefillAttentionArgs),
+                         ("kda_prefill_attention_grads", PrefillAttentionGrads),
+                         ("kda_verify_accept_args", VerifyAcceptArgs)):
         if getattr(lib, name + "_bytes")() != ctypes.sizeof(mirror):
             raise RuntimeError(f"{name} layout mismatch between include/kda.h and the binding")
     # The attention calls' argument structs go over as packed bytes (their mirrors cost a microsecond to fill, more than
@@ -241,7 +289,9 @@ def load(build_if_missing: bool = False):
     packed = {}
     for name, args in (("kda_qk_norm_rope", [st, vp]), ("kda_qk_norm_rope_backward", [st, vp, vp, c_int, vp, vp, vp, sz, vp]),
                        ("kda_kv_write", [vp, vp, i64, i64, c_int, i64, vp, st, vp, vp]),
-                       ("kda_kv_read", [st, vp, i64, vp, vp, c_int, vp, vp]), ("kda_paged_attention", [st, vp])):
+                       ("kda_kv_read", [st, vp, i64, vp, vp, c_int, vp, vp]), ("kda_paged_attention", [st, vp]),
+                       ("kda_prefill_attention", [st, vp]), ("kda_prefill_attention_backward", [st, st, vp]),
+                       ("kda_verify_accept", [st, vp])):
         packed[name] = lib[name]
         packed[name].restype, packed[name].argtypes = c_int, args
     _packed = packed  # whole: another thread's call takes a table that is there for a loaded library
@@ -1005,3 +1055,132 @@ def kda_paged_attention(q, k_pages, v_pages, block_table, seq_lens, out, workspa
                         d ** -0.5 if scale is None else scale, softcap, window, out.data_ptr(), out_code, _ptr(lse),
                         workspace.data_ptr(), workspace.numel() * workspace.element_size(), _ptr(dev_status))
     _call("kda_paged_attention", a, _stream(stream))
+
+
+# ---------------------------------------------------------------- prompts of the attention layers, and accepted drafts
+
+def _same_device(*named):
+    """Every tensor on the current device: the launches go there."""
+    here = torch.cuda.current_device()
+    for name, t in named:
+        if t is not None and t.get_device() != here:
+            raise ValueError(f"{name}: expected a tensor on the current device cuda:{here}, got {t.device}")
+
+
+def _prompt_checks(q, k, v, cu_seqlens, out, lse, dev_status, grads):
+    T, Hq, d = _rank("q", q, 3)
+    _need("q", q, q.shape, _IN)
+    Hkv = _rank("k", k, 3)[1]
+    _need("k", k, (T, Hkv, d), (q.dtype,))
+    _need("v", v, (T, Hkv, d), (q.dtype,))
+    if Hkv == 0 or Hq % Hkv:
+        raise ValueError(f"q: expected a multiple of the keys' {Hkv} heads, got {Hq}")
+    _need("cu_seqlens", cu_seqlens, (None,), _I32)
+    if cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens: expected N + 1 >= 1 offsets")
+    _need("out", out, q.shape, _IN)
+    _need("lse", lse, (T, Hq), _FP)
+    if grads:
+        d_out, dq, dk, dv = grads
+        _need("d_out", d_out, q.shape, (q.dtype,))
+        _need("dq", dq, q.shape, _IN)
+        _need("dk", dk, k.shape, (dq.dtype,))
+        _need("dv", dv, k.shape, (dq.dtype,))
+    _need_status(dev_status)
+    _check(cu_seqlens, lse, dev_status)
+
+
+def _prompt_args(q, k, v, cu_seqlens, max_seqlen, out, scale, softcap, window, lse, dev_status, grads=()):
+    shape, k_shape, dtype, lens = q.shape, k.shape, q.dtype, cu_seqlens.shape
+    code, out_code = _DTYPE_CODES.get(dtype), _DTYPE_CODES.get(out.dtype)
+    usual = (len(shape) == 3 and len(k_shape) == 3 and k_shape[0] == shape[0] and k_shape[2] == shape[2] and k_shape[1] > 0
+             and shape[1] % k_shape[1] == 0 and v.shape == k_shape and k.dtype is dtype and v.dtype is dtype
+             and code is not None and out_code is not None and out.shape == shape and len(lens) == 1 and lens[0] > 0
+             and cu_seqlens.dtype is torch.int32 and cu_seqlens.is_cuda and cu_seqlens.is_contiguous() and dev_status is None
+             and (lse is None or (lse.shape == shape[:2] and lse.dtype is torch.float32 and lse.is_cuda
+                                  and lse.is_contiguous())))
+    if grads and usual:
+        d_out, dq, dk, dv = grads
+        usual = (d_out.shape == shape and d_out.dtype is dtype and dq.shape == shape and dk.shape == k_shape
+                 and dv.shape == k_shape and dq.dtype in _DTYPE_CODES and dk.dtype is dq.dtype and dv.dtype is dq.dtype)
+    if not usual:
+        _prompt_checks(q, k, v, cu_seqlens, out, lse, dev_status, grads)
+    T, Hq, d = shape
+    strides = _row_stride("q", q), _row_stride("k", k), _row_stride("v", v)
+    out_stride = _row_stride("out", out)
+    _same_device(("q", q), ("k", k), ("v", v), ("cu_seqlens", cu_seqlens), ("out", out), ("lse", lse),
+                 ("dev_status", dev_status))
+    return _pack_prompt(q.data_ptr(), k.data_ptr(), v.data_ptr(), *strides, code, T, Hq, k_shape[1], d, lens[0] - 1,
+                        cu_seqlens.data_ptr(), max_seqlen, d ** -0.5 if scale is None else scale, softcap, window,
+                        out.data_ptr(), out_stride, out_code, _ptr(lse), _ptr(dev_status))
+
+
+def kda_prefill_attention(q, k, v, cu_seqlens, max_seqlen, out, scale=None, softcap=0.0, window=0, lse=None,
+                          dev_status=None, stream=None):
+    """Causal attention of whole prompts, packed one behind another.
+
+    q, out [T, Hq, d]; k, v [T, Hkv, d], each with any distance between tokens (column blocks of a fused projection's
+    output, say); cu_seqlens int32 [N + 1]; max_seqlen: at least the longest sequence; scale: 1 / sqrt(d) unless given;
+    softcap > 0: scores softcap * tanh(x / softcap); window > 0: a query sees that many positions, its own included;
+    lse [T, Hq] fp32 or None (the gradient needs it).
+    """
+    a = _prompt_args(q, k, v, cu_seqlens, max_seqlen, out, scale, softcap, window, lse, dev_status)
+    _call("kda_prefill_attention", a, _stream(stream))
+
+
+def kda_prefill_attention_backward_workspace_size(T: int, N: int, Hq: int, Hkv: int, d: int) -> int:
+    return load().kda_prefill_attention_backward_workspace_size(T, N, Hq, Hkv, d)
+
+
+def kda_prefill_attention_backward(d_out, q, k, v, out, lse, cu_seqlens, max_seqlen, dq, dk, dv, workspace, scale=None,
+                                   softcap=0.0, window=0, dev_status=None, stream=None):
+    """Gradients of sum <d_out, out> through kda_prefill_attention of (q, k, v), which returned out and lse.
+
+    d_out, dq [T, Hq, d]; dk, dv [T, Hkv, d] (overwritten; column blocks of one buffer are allowed); workspace: at least
+    kda_prefill_attention_backward_workspace_size(T, N, Hq, Hkv, d) bytes; the rest as in the forward call.
+    """
+    if lse is None:
+        raise ValueError("lse: the gradient needs the forward's")
+    a = _prompt_args(q, k, v, cu_seqlens, max_seqlen, out, scale, softcap, window, lse, dev_status, (d_out, dq, dk, dv))
+    strides = _row_stride("d_out", d_out), _row_stride("dq", dq), _row_stride("dk", dk), _row_stride("dv", dv)
+    _check(workspace)
+    _same_device(("d_out", d_out), ("dq", dq), ("dk", dk), ("dv", dv), ("workspace", workspace))
+    g = _pack_grads(d_out.data_ptr(), strides[0], dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), *strides[1:], _dt(dq),
+                    workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    _call("kda_prefill_attention_backward", a, g, _stream(stream))
+
+
+def kda_verify_accept(target_probs, draft_tokens, uniform, accepted, tokens, draft_probs=None, num_drafts=None,
+                      dev_status=None, stream=None):
+    """Which drafts of each request's window the target accepts, and the token drawn behind them.
+
+    target_probs [B, W, V] fp32 or bf16; draft_tokens int32 [B, W - 1] (window tokens 1 .. W - 1); uniform [B, W] fp32 in
+    [0, 1): one number per draft, the last for the draw; accepted int32 [B]: window tokens to commit, as
+    kda_verify_replay takes it (accepted drafts + 1); tokens int32 [B, W]: accepted drafts, the drawn token, then -1;
+    draft_probs [B, W - 1, V] like target_probs, or None for drafts that were certain; num_drafts int32 [B] or None.
+    """
+    shape, code, i32 = target_probs.shape, _DTYPE_CODES.get(target_probs.dtype), torch.int32
+    if not (len(shape) == 3 and shape[1] > 0 and shape[2] > 0 and code is not None
+            and draft_tokens.shape == (shape[0], shape[1] - 1) and draft_tokens.dtype is i32 and uniform.shape == shape[:2]
+            and uniform.dtype is torch.float32 and accepted.shape == shape[:1] and accepted.dtype is i32
+            and tokens.shape == shape[:2] and tokens.dtype is i32 and num_drafts is None and dev_status is None
+            and (draft_probs is None or (draft_probs.shape == (shape[0], shape[1] - 1, shape[2])
+                                         and draft_probs.dtype is target_probs.dtype))):
+        B, W, V = _rank("target_probs", target_probs, 3)
+        _need("target_probs", target_probs, target_probs.shape, _IN)
+        if W == 0 or V == 0:
+            raise ValueError(f"target_probs: expected a window and a vocabulary of at least one, got {list(shape)}")
+        _need("draft_tokens", draft_tokens, (B, W - 1), _I32)
+        _need("uniform", uniform, (B, W), _FP)
+        _need("accepted", accepted, (B,), _I32)
+        _need("tokens", tokens, (B, W), _I32)
+        _need("draft_probs", draft_probs, (B, W - 1, V), (target_probs.dtype,))
+        _need("num_drafts", num_drafts, (B,), _I32)
+        _need_status(dev_status)
+    _check(target_probs, draft_tokens, uniform, accepted, tokens, draft_probs, num_drafts, dev_status)
+    _same_device(("target_probs", target_probs), ("draft_tokens", draft_tokens), ("uniform", uniform), ("accepted", accepted),
+                 ("tokens", tokens), ("draft_probs", draft_probs), ("num_drafts", num_drafts), ("dev_status", dev_status))
+    B, W, V = shape
+    a = _pack_accept(target_probs.data_ptr(), _ptr(draft_probs), code, B, W, V, draft_tokens.data_ptr(), _ptr(num_drafts),
+                     uniform.data_ptr(), accepted.data_ptr(), tokens.data_ptr(), _ptr(dev_status))
+    _call("kda_verify_accept", a, _stream(stream))

@@ -808,4 +808,135 @@ kda_status kda_paged_attention(const kda_paged_attention_args* a, kda_stream_t s
   return from_cuda(kda::launch_paged_attention(p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+size_t kda_prefill_attention_args_bytes(void) { return sizeof(kda_prefill_attention_args); }
+size_t kda_prefill_attention_grads_bytes(void) { return sizeof(kda_prefill_attention_grads); }
+size_t kda_verify_accept_args_bytes(void) { return sizeof(kda_verify_accept_args); }
+
+}  // extern "C"
+
+namespace {
+
+// T is 0, or nothing is asked for that the arrays would have to be there for.
+kda_status check_prompt(const kda_prefill_attention_args* a) {
+  if (!a || !dtype_ok(a->in_dtype) || !dtype_ok(a->out_dtype)) return KDA_ERR_INVALID_ARG;
+  if (a->T < 0 || a->N < 0 || a->N > 65535 || a->Hq <= 0 || a->Hkv <= 0 || a->Hq > 65535 || a->Hq % a->Hkv != 0 ||
+      a->max_seqlen < 0 || a->window < 0)
+    return KDA_ERR_INVALID_ARG;
+  if (a->T > 0x7fffffff - 1023 || a->T * a->Hq > 0x3ffffffffLL) return KDA_ERR_INVALID_ARG;
+  if (!(a->softcap >= 0.f) || a->softcap > 3e38f || !(a->scale >= -3e38f && a->scale <= 3e38f)) return KDA_ERR_INVALID_ARG;
+  if (!d_ok(a->d)) return KDA_ERR_UNSUPPORTED;
+  return KDA_OK;
+}
+
+kda_status check_prompt_arrays(const kda_prefill_attention_args* a) {
+  const int64_t q = (int64_t)a->Hq * a->d, k = (int64_t)a->Hkv * a->d;
+  if (!strided_ok(a->q, a->q_stride, q, a->in_dtype) || !strided_ok(a->k, a->k_stride, k, a->in_dtype) ||
+      !strided_ok(a->v, a->v_stride, k, a->in_dtype) || !strided_ok(a->out, a->out_stride, q, a->out_dtype) ||
+      !natural(a->cu_seqlens, 4) || (a->lse && !natural(a->lse, 4)))
+    return KDA_ERR_INVALID_ARG;
+  return KDA_OK;
+}
+
+kda::PromptAttnArgs prompt_args(const kda_prefill_attention_args* a) {
+  kda::PromptAttnArgs p{};
+  p.q = a->q;
+  p.k = a->k;
+  p.v = a->v;
+  p.q_stride = a->q_stride;
+  p.k_stride = a->k_stride;
+  p.v_stride = a->v_stride;
+  p.in_bf16 = a->in_dtype == KDA_DTYPE_BF16;
+  p.T = a->T;
+  p.Hq = a->Hq;
+  p.Hkv = a->Hkv;
+  p.d = a->d;
+  p.N = a->N;
+  p.cu = a->cu_seqlens;
+  p.max_seqlen = a->max_seqlen;
+  p.scale = a->scale;
+  // see kda_paged_attention
+  p.softcap = a->softcap > 1e30f ? 0.f : a->softcap > 0.f && a->softcap < 1e-20f ? 1e-20f : a->softcap;
+  p.window = a->window;
+  p.out = a->out;
+  p.out_stride = a->out_stride;
+  p.out_bf16 = a->out_dtype == KDA_DTYPE_BF16;
+  p.lse = a->lse;
+  p.status = a->dev_status;
+  return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+kda_status kda_prefill_attention(const kda_prefill_attention_args* a, kda_stream_t stream) {
+  kda_status st = check_prompt(a);
+  if (st != KDA_OK || a->T == 0 || a->N == 0) return st;
+  st = check_prompt_arrays(a);
+  if (st != KDA_OK) return st;
+  return from_cuda(kda::launch_prefill_attention(prompt_args(a), reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t kda_prefill_attention_backward_workspace_size(int64_t T, int N, int Hq, int Hkv, int d) {
+  if (T < 0 || T > 0x7fffffff - 1023 || N < 0 || Hq <= 0 || Hkv <= 0 || Hq > 65535 || Hq % Hkv != 0 || !d_ok(d)) return 0;
+  return kda::prefill_attention_grad_ws_bytes(T, N, Hq, Hkv, d);
+}
+
+kda_status kda_prefill_attention_backward(const kda_prefill_attention_args* a, const kda_prefill_attention_grads* g,
+                                          kda_stream_t stream) {
+  kda_status st = check_prompt(a);
+  if (st != KDA_OK) return st;
+  if (!g || !dtype_ok(g->grad_dtype)) return KDA_ERR_INVALID_ARG;
+  if (a->T == 0 || a->N == 0) return KDA_OK;
+  st = check_prompt_arrays(a);
+  if (st != KDA_OK) return st;
+  const int64_t q = (int64_t)a->Hq * a->d, k = (int64_t)a->Hkv * a->d;
+  if (!a->lse || !strided_ok(g->d_out, g->d_out_stride, q, a->in_dtype) || !strided_ok(g->dq, g->dq_stride, q, g->grad_dtype) ||
+      !strided_ok(g->dk, g->dk_stride, k, g->grad_dtype) || !strided_ok(g->dv, g->dv_stride, k, g->grad_dtype))
+    return KDA_ERR_INVALID_ARG;
+  if (!g->workspace ||
+      g->workspace_bytes < kda_prefill_attention_backward_workspace_size(a->T, a->N, a->Hq, a->Hkv, a->d))
+    return KDA_ERR_WORKSPACE;
+  if (!aligned16(g->workspace)) return KDA_ERR_INVALID_ARG;
+  kda::PromptGradArgs p{};
+  p.d_out = g->d_out;
+  p.d_out_stride = g->d_out_stride;
+  p.dq = g->dq;
+  p.dk = g->dk;
+  p.dv = g->dv;
+  p.dq_stride = g->dq_stride;
+  p.dk_stride = g->dk_stride;
+  p.dv_stride = g->dv_stride;
+  p.bf16 = g->grad_dtype == KDA_DTYPE_BF16;
+  p.ws = g->workspace;
+  return from_cuda(kda::launch_prefill_attention_backward(prompt_args(a), p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+kda_status kda_verify_accept(const kda_verify_accept_args* a, kda_stream_t stream) {
+  if (!a || !dtype_ok(a->dtype)) return KDA_ERR_INVALID_ARG;
+  if (a->B < 0 || a->W <= 0 || a->V <= 0 || a->V > 1 << 30) return KDA_ERR_INVALID_ARG;
+  if (a->B == 0) return KDA_OK;
+  if ((int64_t)a->B * a->W > 0x7fffffff / 8) return KDA_ERR_INVALID_ARG;  // places, and CTAs, within 32 bits
+  const size_t es = esize(a->dtype);
+  if (!natural(a->target_probs, es) || !natural(a->uniform, 4) || !natural(a->accepted, 4) || !natural(a->tokens, 4))
+    return KDA_ERR_INVALID_ARG;
+  if (a->W > 1 && !natural(a->draft_tokens, 4)) return KDA_ERR_INVALID_ARG;
+  if ((a->draft_probs && !natural(a->draft_probs, es)) || (a->num_drafts && !natural(a->num_drafts, 4)))
+    return KDA_ERR_INVALID_ARG;
+  kda::VerifyAcceptArgs v{};
+  v.target = a->target_probs;
+  v.proposal = a->W > 1 ? a->draft_probs : nullptr;
+  v.bf16 = a->dtype == KDA_DTYPE_BF16;
+  v.B = a->B;
+  v.W = a->W;
+  v.V = a->V;
+  v.drafts = a->draft_tokens;
+  v.num_drafts = a->num_drafts;
+  v.uniform = a->uniform;
+  v.accepted = a->accepted;
+  v.tokens = a->tokens;
+  v.status = a->dev_status;
+  return from_cuda(kda::launch_verify_accept(v, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 }  // extern "C"

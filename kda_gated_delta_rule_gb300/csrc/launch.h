@@ -269,6 +269,49 @@ struct PagedAttnArgs {
 size_t paged_attention_ws_bytes(int W, int Hq, int Hkv, int d);
 cudaError_t launch_paged_attention(const PagedAttnArgs& a, cudaStream_t s);
 
+// Causal attention over packed prompts and its gradients (see kda_prefill_attention_args in include/kda.h).
+struct PromptAttnArgs {
+  const void *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride;
+  bool in_bf16;
+  int64_t T;
+  int Hq, Hkv, d, N;
+  const int32_t* cu;
+  int max_seqlen;
+  float scale, softcap;
+  int window;  // 0: none
+  void* out;   // the gradient reads it
+  int64_t out_stride;
+  bool out_bf16;
+  float* lse;  // [T][Hq], null in a forward that is not asked for it
+  int32_t* status;
+  bool test_stall;  // test hook (kda_set_test_fault): the tensor-memory forms' copies give up
+};
+struct PromptGradArgs {
+  const void* d_out;  // in dtype
+  int64_t d_out_stride;
+  void *dq, *dk, *dv;
+  int64_t dq_stride, dk_stride, dv_stride;
+  bool bf16;  // type of the gradients
+  void* ws;   // prefill_attention_grad_ws_bytes
+};
+cudaError_t launch_prefill_attention(const PromptAttnArgs& a, cudaStream_t s);
+size_t prefill_attention_grad_ws_bytes(int64_t T, int N, int Hq, int Hkv, int d);
+cudaError_t launch_prefill_attention_backward(const PromptAttnArgs& a, const PromptGradArgs& g, cudaStream_t s);
+
+// Acceptance of drafted tokens (see kda_verify_accept_args in include/kda.h).
+struct VerifyAcceptArgs {
+  const void *target, *proposal;  // proposal null: the drafts were certain
+  bool bf16;
+  int B, W, V;
+  const int32_t* drafts;      // [B][W - 1]
+  const int32_t* num_drafts;  // [B], null: W - 1 each
+  const float* uniform;       // [B][W]
+  int32_t *accepted, *tokens;
+  int32_t* status;
+};
+cudaError_t launch_verify_accept(const VerifyAcceptArgs& a, cudaStream_t s);
+
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t s);
 cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t s);
 // Tensor-core verify (bf16 inputs, d = 128, W <= 16, no per-token snapshots).

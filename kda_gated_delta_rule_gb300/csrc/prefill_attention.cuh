@@ -1,0 +1,74 @@
+// What the forms of the prompt attention share: where a block of a packed batch's tokens lies, and which keys its rows see.
+#pragma once
+
+#include "common.cuh"
+#include "launch.h"
+
+namespace kda {
+
+namespace {
+
+constexpr float PF_LOG2E = 1.4426950408889634f;
+constexpr float PF_LN2 = 0.6931471805599453f;
+constexpr float PF_NONE = -3.402823466e38f;  // a softmax reference that has seen nothing (finite: no -inf - -inf)
+
+__device__ __forceinline__ float pf_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Blocks of `rows` tokens of all sequences, without sums over their lengths: the blocks of sequence i, at most
+// ceil(length / rows) of them, lie among the places floor(start_i / rows) + i .. floor(start_i+1 / rows) + i, which
+// are its own.  So a batch has floor(T / rows) + N places, some of them empty.
+inline int64_t pf_places(int64_t T, int N, int rows) { return T / rows + N; }
+
+struct PfBlock {
+  int t0, len;  // the sequence's first token and length; len = 0: an empty place
+  int row0;     // the block's first token within the sequence
+};
+
+// The block at `place`; one whole warp asks.  A search with 32 probes at a time: N <= 32 is one load.
+__device__ __forceinline__ PfBlock pf_block(const PromptAttnArgs& a, int64_t place, int rows) {
+  const int lane = threadIdx.x & 31;
+  const int T = (int)a.T;
+  auto at = [&](int i) { return max(0, min(T, __ldg(a.cu + i))); };
+  int lo = 0, hi = a.N;
+  PfBlock b{0, 0, 0};
+  while (hi > lo) {
+    const int step = (hi - lo + 31) >> 5, i = lo + lane * step;
+    const bool ok = i < hi && (int64_t)(at(i) / rows) + i <= place;
+    const int n = __popc(__ballot_sync(0xffffffffu, ok));
+    if (n == 0) return b;
+    lo += (n - 1) * step;
+    hi = min(hi, lo + step);
+    if (step == 1) break;
+  }
+  const int c0 = __ldg(a.cu + lo), c1 = __ldg(a.cu + lo + 1);
+  if (c0 < 0 || c1 < c0 || c1 > T || c1 - c0 > a.max_seqlen) return b;
+  const int64_t row0 = (place - ((int64_t)(c0 / rows) + lo)) * rows;
+  if (row0 >= c1 - c0) return b;
+  b.t0 = c0;
+  b.len = c1 - c0;
+  b.row0 = (int)row0;
+  return b;
+}
+
+// Reports offsets that are out of order or out of range, and sequences beyond max_seqlen; one warp asks.
+__device__ __forceinline__ void pf_check_offsets(const PromptAttnArgs& a) {
+  bool bad = false;
+  for (int i = threadIdx.x & 31; i < a.N; i += 32) {
+    const int c0 = __ldg(a.cu + i), c1 = __ldg(a.cu + i + 1);
+    bad |= c0 < 0 || c1 < c0 || c1 > a.T || c1 - c0 > a.max_seqlen;
+  }
+  if (__any_sync(0xffffffffu, bad) && (threadIdx.x & 31) == 0) flag_status(a.status, KDA_DEV_SEQ_OOB);
+}
+
+}  // namespace
+
+// The register forms (any head size; prefill_attention_f32.cu) and the tensor-memory ones (prefill_attention_tc.cu,
+// prefill_attention_grad_tc.cu).
+cudaError_t pf_f32(const PromptAttnArgs& a, cudaStream_t s);
+cudaError_t pf_f32_grad(const PromptAttnArgs& a, const PromptGradArgs& g, const float2* stats, cudaStream_t s);
+
+}  // namespace kda

@@ -1,0 +1,459 @@
+// Attention over packed prompts and its gradients on the CUDA cores, in fp32.
+//
+//   x_ij = scale q_i . k_j, capped: y = cap tanh(x / cap);  p = softmax_j(y) over the keys that row i sees;  o_i = sum_j p_ij v_j
+//   dv_j = sum_i p_ij do_i,  dy = p (do_i . v_j - D_i),  D_i = do_i . o_i,  dx = dy (1 - (y / cap)^2) scale
+//   dq_i = sum_j dx_ij k_j,  dk_j = sum_i dx_ij q_i
+//
+// A CTA of 256 threads has 64 query rows of one head and walks the 64-key tiles that they see with the running maximum and sum;
+// a thread has 4 x 4 scores of a tile and the same 4 rows of the output.  The gradients take two kernels, so that each
+// output has one owner and no sum depends on an order of arrival: one CTA per 64 keys of a key/value head walks the
+// query blocks of all its query heads (dk, dv), one per 64 query rows walks the keys (dq).  Both form the scores again
+// from the log-sum-exp.  Bound by the fp32 pipe and the shared-memory loads that feed it (8 loads of 16 bytes for 32
+// two-wide multiply-adds in the scores).
+#include "f32x2.cuh"
+#include "prefill_attention.cuh"
+
+namespace kda {
+
+namespace {
+
+constexpr int PB = 64;  // rows and keys of a block
+constexpr int PNT = 256;
+
+template <int D>
+struct PfShape {
+  static constexpr int LD = D + 4;                 // floats between rows: the 16 rows a half-warp reads meet all banks
+  static constexpr int CPT = D / 16;               // channels of a thread
+  static constexpr int G = CPT < 4 ? CPT : 4;      // contiguous ones
+  static constexpr int NG = CPT / G;               // groups of them, 16 G channels apart
+  static constexpr int PLD = PB + 4;
+};
+
+template <typename T>
+__device__ __forceinline__ float4 ld4(const T* p);
+template <>
+__device__ __forceinline__ float4 ld4<float>(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
+template <>
+__device__ __forceinline__ float4 ld4<bf16>(const bf16* p) {
+  const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
+  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
+                     __uint_as_float(w.y & 0xffff0000u));
+}
+
+// Rows 0 .. 63 of `base` (tokens `stride` apart); those from `valid` on are zeros.
+template <int D, typename In>
+__device__ __forceinline__ void load_block(float* dst, const In* base, int64_t stride, int valid) {
+  constexpr int C4 = D / 4;
+  for (int i = threadIdx.x; i < PB * C4; i += PNT) {
+    const int r = i / C4, c = (i - r * C4) * 4;
+    const float4 x = r < valid ? ld4<In>(base + r * stride + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+    *reinterpret_cast<float4*>(dst + r * PfShape<D>::LD + c) = x;
+  }
+}
+
+// s[i][j] = row (ty + 16 i) of a times row (tx + 16 j) of b
+template <int D>
+__device__ __forceinline__ void dots(const float* a, const float* b, float (&s)[4][4]) {
+  constexpr int LD = PfShape<D>::LD;
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  float2 acc[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = both(0.f);
+#pragma unroll 4
+  for (int c = 0; c < D; c += 4) {
+    float4 x[4], y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4*>(a + (ty + 16 * i) * LD + c);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const float4*>(b + (tx + 16 * j) * LD + c);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        acc[i][j] = fma2(make_float2(x[i].x, x[i].y), make_float2(y[j].x, y[j].y), acc[i][j]);
+        acc[i][j] = fma2(make_float2(x[i].z, x[i].w), make_float2(y[j].z, y[j].w), acc[i][j]);
+      }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[i][j] = acc[i][j].x + acc[i][j].y;
+}
+
+// A thread's channels of a row in shared memory.
+template <int D>
+__device__ __forceinline__ void ld_channels(const float* row, float (&v)[PfShape<D>::CPT]) {
+  using S = PfShape<D>;
+  const int tx = threadIdx.x & 15;
+#pragma unroll
+  for (int n = 0; n < S::NG; ++n) {
+    const float* p = row + n * 16 * S::G + tx * S::G;
+    if constexpr (S::G == 4) {
+      const float4 x = *reinterpret_cast<const float4*>(p);
+      v[4 * n] = x.x, v[4 * n + 1] = x.y, v[4 * n + 2] = x.z, v[4 * n + 3] = x.w;
+    } else if constexpr (S::G == 2) {
+      const float2 x = *reinterpret_cast<const float2*>(p);
+      v[0] = x.x, v[1] = x.y;
+    } else {
+      v[0] = *p;
+    }
+  }
+}
+
+// acc[i] += sum_j w(i, j) row_j over 4 rows of b at j0, w given per output row
+template <int D>
+__device__ __forceinline__ void add_rows(float (&acc)[4][PfShape<D>::CPT], const float4 (&w)[4], const float* b) {
+  constexpr int CPT = PfShape<D>::CPT;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float v[CPT];
+    ld_channels<D>(b + j * PfShape<D>::LD, v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float p = j == 0 ? w[i].x : j == 1 ? w[i].y : j == 2 ? w[i].z : w[i].w;
+      if constexpr (CPT >= 2) {
+#pragma unroll
+        for (int c = 0; c < CPT; c += 2) {
+          const float2 r = fma2(both(p), make_float2(v[c], v[c + 1]), make_float2(acc[i][c], acc[i][c + 1]));
+          acc[i][c] = r.x, acc[i][c + 1] = r.y;
+        }
+      } else {
+        acc[i][0] = fmaf(p, v[0], acc[i][0]);
+      }
+    }
+  }
+}
+
+template <int D, typename Out>
+__device__ __forceinline__ void store_channels(Out* row, const float (&v)[PfShape<D>::CPT]) {
+  using S = PfShape<D>;
+  const int tx = threadIdx.x & 15;
+#pragma unroll
+  for (int n = 0; n < S::NG; ++n) {
+    Out* p = row + n * 16 * S::G + tx * S::G;
+    if constexpr (S::G == 4 && sizeof(Out) == 4) {
+      *reinterpret_cast<float4*>(p) = make_float4(v[4 * n], v[4 * n + 1], v[4 * n + 2], v[4 * n + 3]);
+    } else {
+#pragma unroll
+      for (int c = 0; c < S::G; ++c) p[c] = from_f32<Out>(v[S::G * n + c]);
+    }
+  }
+}
+template <int D>
+__device__ __forceinline__ void store_row(void* base, bool is_bf16, int64_t at, const float (&v)[PfShape<D>::CPT]) {
+  if (is_bf16) store_channels<D>(static_cast<bf16*>(base) + at, v);
+  else store_channels<D>(static_cast<float*>(base) + at, v);
+}
+
+// The score in powers of two, and the cap's slope there.
+__device__ __forceinline__ float score2(float dot, float scale, float cap, float& slope) {
+  const float x = dot * scale;
+  if (cap > 0.f) {
+    const float t = tanhf(x / cap);
+    slope = 1.f - t * t;
+    return cap * t * PF_LOG2E;
+  }
+  slope = 1.f;
+  return x * PF_LOG2E;
+}
+
+template <int D, typename In>
+__global__ void __launch_bounds__(PNT) pf_f32_kernel(const PromptAttnArgs a, const int64_t places) {
+  using S = PfShape<D>;
+  extern __shared__ __align__(16) float sm[];
+  float *sq = sm, *sk = sq + PB * S::LD, *sv = sk + PB * S::LD, *sp = sv + PB * S::LD;
+  pdl_begin();
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, h = blockIdx.y, kh = h / (a.Hq / a.Hkv);
+  if (blockIdx.x == 0 && h == 0 && tid < 32) pf_check_offsets(a);
+  // the longest rows first: a sequence's last blocks see most keys
+  const PfBlock b = pf_block(a, places - 1 - blockIdx.x, PB);
+  if (b.len == 0) return;
+  const int rows = min(PB, b.len - b.row0), window = a.window > 0 ? a.window : 0x7fffffff;
+  load_block<D>(sq, static_cast<const In*>(a.q) + (int64_t)(b.t0 + b.row0) * a.q_stride + h * D, a.q_stride, rows);
+  float o[4][S::CPT], m[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    m[i] = PF_NONE, l[i] = 0.f;
+#pragma unroll
+    for (int c = 0; c < S::CPT; ++c) o[i][c] = 0.f;
+  }
+  const int last = b.row0 + rows - 1, first = max(0, b.row0 - window + 1);
+  for (int k0 = first / PB * PB; k0 <= last; k0 += PB) {
+    const int64_t tok = b.t0 + k0;
+    __syncthreads();
+    load_block<D>(sk, static_cast<const In*>(a.k) + tok * a.k_stride + kh * D, a.k_stride, b.len - k0);
+    load_block<D>(sv, static_cast<const In*>(a.v) + tok * a.v_stride + kh * D, a.v_stride, b.len - k0);
+    __syncthreads();
+    float s[4][4];
+    dots<D>(sq, sk, s);
+    const bool masked = k0 + PB - 1 > b.row0 || k0 <= last - window;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = b.row0 + ty + 16 * i;
+      float top = m[i], slope;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int key = k0 + tx + 16 * j;
+        s[i][j] = score2(s[i][j], a.scale, a.softcap, slope);
+        if (masked && !(key <= row && key > row - window)) s[i][j] = -INFINITY;
+        top = fmaxf(top, s[i][j]);
+      }
+#pragma unroll
+      for (int n = 1; n < 16; n <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, n));
+      const float by = pf_ex2(m[i] - top);
+      m[i] = top;
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float p = pf_ex2(s[i][j] - top);
+        sum += p;
+        sp[(ty + 16 * i) * S::PLD + tx + 16 * j] = p;
+      }
+#pragma unroll
+      for (int n = 1; n < 16; n <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, n);
+      l[i] = l[i] * by + sum;
+#pragma unroll
+      for (int c = 0; c < S::CPT; ++c) o[i][c] *= by;
+    }
+    __syncwarp();  // a row's probabilities come from its own half-warp
+    if (!masked) {
+#pragma unroll 2
+      for (int j = 0; j < PB; j += 4) {
+        float4 w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float4*>(sp + (ty + 16 * i) * S::PLD + j);
+        add_rows<D>(o, w, sv + j * S::LD);
+      }
+    } else {
+      // what unseen keys' values hold does not matter, NaN included
+#pragma unroll 1
+      for (int j = 0; j < PB; ++j) {
+        float v[S::CPT];
+        ld_channels<D>(sv + j * S::LD, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = b.row0 + ty + 16 * i;
+          const bool seen = k0 + j <= row && k0 + j > row - window;
+          const float p = sp[(ty + 16 * i) * S::PLD + j];
+#pragma unroll
+          for (int c = 0; c < S::CPT; ++c) o[i][c] = seen ? fmaf(p, v[c], o[i][c]) : o[i][c];
+        }
+      }
+    }
+    __syncwarp();
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = ty + 16 * i;
+    if (r >= rows) continue;
+    const int64_t t = b.t0 + b.row0 + r;
+#pragma unroll
+    for (int c = 0; c < S::CPT; ++c) o[i][c] /= l[i];
+    store_row<D>(a.out, a.out_bf16, t * a.out_stride + h * D, o[i]);
+    if (tx == 0 && a.lse) a.lse[t * a.Hq + h] = m[i] * PF_LN2 + logf(l[i]);
+  }
+  if (tid == 0) add_work(a.status, rows);
+}
+
+// Probabilities and dy of the tile (rows: queries, columns: keys) from the scores, with the masks; also in shared memory.
+template <int D>
+__device__ __forceinline__ void tile_grads(const PromptAttnArgs& a, const float2* stats, const float* sq, const float* sk,
+                                           const float* sdo, const float* sv, int row0, int k0, int rows, int len, int window,
+                                           float* sp, float* sds) {
+  using S = PfShape<D>;
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  float s[4][4], dp[4][4];
+  dots<D>(sq, sk, s);
+  dots<D>(sdo, sv, dp);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = ty + 16 * i, row = row0 + r;
+    const float2 st = r < rows ? __ldg(stats + r) : make_float2(0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int key = k0 + tx + 16 * j;
+      const bool seen = r < rows && key < len && key <= row && key > row - window;
+      float slope;
+      const float y = score2(s[i][j], a.scale, a.softcap, slope);
+      const float p = seen ? pf_ex2(y - st.x) : 0.f;
+      if (sp) sp[r * S::PLD + tx + 16 * j] = p;
+      sds[r * S::PLD + tx + 16 * j] = seen ? p * (dp[i][j] - st.y) * slope : 0.f;
+    }
+  }
+}
+
+template <int D, typename In>
+__global__ void __launch_bounds__(PNT)
+    pf_f32_grad_kv_kernel(const PromptAttnArgs a, const PromptGradArgs g, const float2* __restrict__ stats, const int64_t places) {
+  using S = PfShape<D>;
+  extern __shared__ __align__(16) float sm[];
+  float *sk = sm, *sv = sk + PB * S::LD, *sq = sv + PB * S::LD, *sdo = sq + PB * S::LD, *sp = sdo + PB * S::LD,
+        *sds = sp + PB * S::PLD;
+  pdl_begin();
+  const int tid = threadIdx.x, ty = tid >> 4, kh = blockIdx.y, group = a.Hq / a.Hkv;
+  if (blockIdx.x == 0 && kh == 0 && tid < 32) pf_check_offsets(a);
+  const PfBlock b = pf_block(a, blockIdx.x, PB);
+  if (b.len == 0) return;
+  const int k0 = b.row0, keys = min(PB, b.len - k0), window = a.window > 0 ? a.window : 0x7fffffff;
+  const int64_t tok = b.t0 + k0;
+  load_block<D>(sk, static_cast<const In*>(a.k) + tok * a.k_stride + kh * D, a.k_stride, keys);
+  load_block<D>(sv, static_cast<const In*>(a.v) + tok * a.v_stride + kh * D, a.v_stride, keys);
+  float dk[4][S::CPT], dv[4][S::CPT];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int c = 0; c < S::CPT; ++c) dk[i][c] = dv[i][c] = 0.f;
+  const int64_t last = min((int64_t)b.len - 1, (int64_t)k0 + keys - 1 + window - 1);  // the last row that sees one of the keys
+  for (int h = kh * group; h < (kh + 1) * group; ++h)
+    for (int row0 = k0; row0 <= last; row0 += PB) {
+      const int64_t t = b.t0 + row0;
+      const int rows = min(PB, b.len - row0);
+      __syncthreads();
+      load_block<D>(sq, static_cast<const In*>(a.q) + t * a.q_stride + h * D, a.q_stride, rows);
+      load_block<D>(sdo, static_cast<const In*>(g.d_out) + t * g.d_out_stride + h * D, g.d_out_stride, rows);
+      __syncthreads();
+      tile_grads<D>(a, stats + h * a.T + t, sq, sk, sdo, sv, row0, k0, rows, b.len, window, sp, sds);
+      __syncthreads();
+#pragma unroll 2
+      for (int q = 0; q < PB; q += 1) {
+        const float4 p = *reinterpret_cast<const float4*>(sp + q * S::PLD + ty * 4);
+        const float4 ds = *reinterpret_cast<const float4*>(sds + q * S::PLD + ty * 4);
+        float x[S::CPT], y[S::CPT];
+        ld_channels<D>(sdo + q * S::LD, x);
+        ld_channels<D>(sq + q * S::LD, y);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float pi = i == 0 ? p.x : i == 1 ? p.y : i == 2 ? p.z : p.w;
+          const float di = i == 0 ? ds.x : i == 1 ? ds.y : i == 2 ? ds.z : ds.w;
+#pragma unroll
+          for (int c = 0; c < S::CPT; ++c) {
+            dv[i][c] = fmaf(pi, x[c], dv[i][c]);
+            dk[i][c] = fmaf(di, y[c], dk[i][c]);
+          }
+        }
+      }
+    }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = ty * 4 + i;
+    if (r >= keys) continue;
+#pragma unroll
+    for (int c = 0; c < S::CPT; ++c) dk[i][c] *= a.scale;
+    store_row<D>(g.dk, g.bf16, (tok + r) * g.dk_stride + kh * D, dk[i]);
+    store_row<D>(g.dv, g.bf16, (tok + r) * g.dv_stride + kh * D, dv[i]);
+  }
+}
+
+template <int D, typename In>
+__global__ void __launch_bounds__(PNT)
+    pf_f32_grad_q_kernel(const PromptAttnArgs a, const PromptGradArgs g, const float2* __restrict__ stats, const int64_t places) {
+  using S = PfShape<D>;
+  extern __shared__ __align__(16) float sm[];
+  float *sq = sm, *sdo = sq + PB * S::LD, *sk = sdo + PB * S::LD, *sv = sk + PB * S::LD, *sds = sv + PB * S::LD;
+  pdl_begin();
+  const int tid = threadIdx.x, ty = tid >> 4, h = blockIdx.y, kh = h / (a.Hq / a.Hkv);
+  const PfBlock b = pf_block(a, places - 1 - blockIdx.x, PB);
+  if (b.len == 0) return;
+  const int rows = min(PB, b.len - b.row0), window = a.window > 0 ? a.window : 0x7fffffff;
+  const int64_t t = b.t0 + b.row0;
+  load_block<D>(sq, static_cast<const In*>(a.q) + t * a.q_stride + h * D, a.q_stride, rows);
+  load_block<D>(sdo, static_cast<const In*>(g.d_out) + t * g.d_out_stride + h * D, g.d_out_stride, rows);
+  float dq[4][S::CPT];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int c = 0; c < S::CPT; ++c) dq[i][c] = 0.f;
+  const int last = b.row0 + rows - 1, first = max(0, b.row0 - window + 1);
+  for (int k0 = first / PB * PB; k0 <= last; k0 += PB) {
+    const int64_t tok = b.t0 + k0;
+    __syncthreads();
+    load_block<D>(sk, static_cast<const In*>(a.k) + tok * a.k_stride + kh * D, a.k_stride, b.len - k0);
+    load_block<D>(sv, static_cast<const In*>(a.v) + tok * a.v_stride + kh * D, a.v_stride, b.len - k0);
+    __syncthreads();
+    tile_grads<D>(a, stats + h * a.T + t, sq, sk, sdo, sv, b.row0, k0, rows, b.len, window, nullptr, sds);
+    __syncwarp();
+#pragma unroll 2
+    for (int j = 0; j < PB; j += 4) {
+      float4 w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float4*>(sds + (ty + 16 * i) * S::PLD + j);
+      add_rows<D>(dq, w, sk + j * S::LD);
+    }
+    __syncwarp();
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = ty + 16 * i;
+    if (r >= rows) continue;
+#pragma unroll
+    for (int c = 0; c < S::CPT; ++c) dq[i][c] *= a.scale;
+    store_row<D>(g.dq, g.bf16, (t + r) * g.dq_stride + h * D, dq[i]);
+  }
+  if (tid == 0) add_work(a.status, rows);
+}
+
+template <int D, typename In>
+cudaError_t forward_launch(const PromptAttnArgs& a, cudaStream_t s) {
+  using S = PfShape<D>;
+  const int smem = (3 * PB * S::LD + PB * S::PLD) * 4;
+  auto kernel = pf_f32_kernel<D, In>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const int64_t places = pf_places(a.T, a.N, PB);
+  return launch_pdl(kernel, dim3((unsigned)places, a.Hq), dim3(PNT), smem, s, a, places);
+}
+
+template <int D, typename In>
+cudaError_t grad_launch(const PromptAttnArgs& a, const PromptGradArgs& g, const float2* stats, cudaStream_t s) {
+  using S = PfShape<D>;
+  const int smem_kv = (4 * PB * S::LD + 2 * PB * S::PLD) * 4, smem_q = (4 * PB * S::LD + PB * S::PLD) * 4;
+  auto kv = pf_f32_grad_kv_kernel<D, In>;
+  auto q = pf_f32_grad_q_kernel<D, In>;
+  cudaError_t e = cudaFuncSetAttribute(kv, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_kv);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(q, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_q);
+  if (e != cudaSuccess) return e;
+  const int64_t places = pf_places(a.T, a.N, PB);
+  e = launch_pdl(kv, dim3((unsigned)places, a.Hkv), dim3(PNT), smem_kv, s, a, g, stats, places);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(q, dim3((unsigned)places, a.Hq), dim3(PNT), smem_q, s, a, g, stats, places);
+}
+
+}  // namespace
+
+cudaError_t pf_f32(const PromptAttnArgs& a, cudaStream_t s) {
+  if (a.in_bf16) {
+    switch (a.d) {
+      case 16: return forward_launch<16, bf16>(a, s);
+      case 32: return forward_launch<32, bf16>(a, s);
+      case 64: return forward_launch<64, bf16>(a, s);
+      default: return forward_launch<128, bf16>(a, s);
+    }
+  }
+  switch (a.d) {
+    case 16: return forward_launch<16, float>(a, s);
+    case 32: return forward_launch<32, float>(a, s);
+    case 64: return forward_launch<64, float>(a, s);
+    default: return forward_launch<128, float>(a, s);
+  }
+}
+
+cudaError_t pf_f32_grad(const PromptAttnArgs& a, const PromptGradArgs& g, const float2* stats, cudaStream_t s) {
+  if (a.in_bf16) {
+    switch (a.d) {
+      case 16: return grad_launch<16, bf16>(a, g, stats, s);
+      case 32: return grad_launch<32, bf16>(a, g, stats, s);
+      case 64: return grad_launch<64, bf16>(a, g, stats, s);
+      default: return grad_launch<128, bf16>(a, g, stats, s);
+    }
+  }
+  switch (a.d) {
+    case 16: return grad_launch<16, float>(a, g, stats, s);
+    case 32: return grad_launch<32, float>(a, g, stats, s);
+    case 64: return grad_launch<64, float>(a, g, stats, s);
+    default: return grad_launch<128, float>(a, g, stats, s);
+  }
+}
+
+}  // namespace kda

@@ -1,0 +1,231 @@
+// Acceptance of drafted tokens against the target's probabilities, and the token that follows the accepted ones.
+//
+// Draft i (token x, from a distribution q) is accepted when u_i q_i(x) < p_i(x), in exact arithmetic, up to the first that is not.
+// Then one token is taken with the last random number r: the least v with w(0) + .. + w(v) > r sum(w), where w is max(p - q, 0)
+// at a refused draft's place (p without x for a certain draft; p where nothing is left of it) and p behind the last accepted.
+//
+// The sums decide a whole number, so they must not depend on their order, and a place that fp32 rounds by 2^-24 would move past
+// neighbouring tokens of a large vocabulary.  Probabilities are summed as 64-bit integers, in units of 2^-58: a difference
+// p - q is exact down to that unit (truncated below it: in all V 2^-58, 6e-13 for 150001 tokens), sums up to 31 stay
+// within 63 bits, and any split gives the same result.
+//
+// One request per cluster of C CTAs of 16 warps, each warp a contiguous piece of the vocabulary.  It reads one row of p and of q
+// once, for the sums; then the CTA in whose part the threshold falls reads one warp's piece again (from L2) to find the token.
+#include <cooperative_groups.h>
+
+#include "device.h"
+#include "common.cuh"
+#include "launch.h"
+
+namespace kda {
+
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int VA_NT = 512, VA_WARPS = VA_NT / 32, VA_MOST = 8;  // threads, warps, CTAs of a cluster at most
+constexpr int VA_UNROLL = 8;
+constexpr float VA_UNIT = 288230376151711744.f;  // 2^58
+constexpr float VA_SUM = 31.f;                 // sums below it, and so differences, fit a signed 64-bit number of units
+
+__device__ __forceinline__ long long units(float p) {  // NaN and negative values count as zero
+  return p > 0.f ? __float2ll_rz(fminf(p, VA_SUM) * VA_UNIT) : 0;
+}
+
+// What a token weighs.
+template <typename In>
+struct Weights {
+  const In *p, *q;  // q null: no proposal to take off
+  int without;      // a token that weighs nothing, or -1
+  __device__ __forceinline__ unsigned long long operator()(float pv, float qv, int v) const {
+    const long long w = units(pv) - (q ? units(qv) : 0);
+    return w > 0 && v != without ? (unsigned long long)w : 0ull;
+  }
+};
+
+// Sum of v0 .. v1, a lane's tokens 32 apart; also in fp32, where it cannot wrap.
+template <typename In>
+__device__ __forceinline__ unsigned long long warp_sum(const Weights<In>& w, int v0, int v1, float& rough) {
+  const int lane = threadIdx.x & 31;
+  unsigned long long sum = 0;
+  float f = 0.f;
+  for (int v = v0 + lane; v < v1; v += 32 * VA_UNROLL) {
+    float p[VA_UNROLL], q[VA_UNROLL];
+#pragma unroll
+    for (int i = 0; i < VA_UNROLL; ++i) {
+      const int at = v + 32 * i;
+      p[i] = at < v1 ? to_f32(w.p[at]) : 0.f;
+      q[i] = w.q && at < v1 ? to_f32(w.q[at]) : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < VA_UNROLL; ++i) {
+      sum += w(p[i], q[i], v + 32 * i);
+      f += p[i] > 0.f ? p[i] : 0.f;
+    }
+  }
+#pragma unroll
+  for (int i = 16; i > 0; i >>= 1) {
+    sum += __shfl_xor_sync(0xffffffffu, sum, i);
+    f += __shfl_xor_sync(0xffffffffu, f, i);
+  }
+  rough = f;
+  return sum;
+}
+
+template <typename In>
+__global__ void __launch_bounds__(VA_NT) verify_accept_kernel(const VerifyAcceptArgs a) {
+  __shared__ unsigned long long sums[VA_WARPS], scan[VA_WARPS];
+  __shared__ float roughs[VA_WARPS];
+  __shared__ unsigned long long total_here;
+  __shared__ float rough_here;
+  __shared__ int accepted, odd;
+  pdl_begin();
+  cg::cluster_group cluster = cg::this_cluster();
+  const int C = cluster.num_blocks(), rank = cluster.block_rank(), b = blockIdx.x / C;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const In* target = static_cast<const In*>(a.target) + (int64_t)b * a.W * a.V;
+  const In* proposal = static_cast<const In*>(a.proposal) + (a.proposal ? (int64_t)b * (a.W - 1) * a.V : 0);
+  const float* u = a.uniform + (int64_t)b * a.W;
+  const int32_t* drafts = a.drafts + (int64_t)b * (a.W - 1);
+
+  int have = a.num_drafts ? __ldg(a.num_drafts + b) : a.W - 1;
+  int flags = 0;
+  if (have < 0 || have > a.W - 1) have = 0, flags |= KDA_DEV_ACCEPT_OOB;
+  if (warp == 0) {
+    // a lane tests a draft
+    int n = 0;
+    bool stray = false;
+    for (int i0 = 0; i0 < have; i0 += 32) {
+      const int i = i0 + lane;
+      bool ok = false, out = false;
+      if (i < have) {
+        const int x = __ldg(drafts + i);
+        out = (unsigned)x >= (unsigned)a.V;
+        if (!out) {
+          const int64_t at = (int64_t)i * a.V + x;
+          const double p = to_f32(target[at]), q = a.proposal ? to_f32(proposal[at]) : 1.f;
+          ok = (double)__ldg(u + i) * q < p;  // a product of two fp32 is exact in fp64
+        }
+      }
+      const unsigned not_ok = ~__ballot_sync(0xffffffffu, ok);
+      const int run = not_ok ? __ffs(not_ok) - 1 : 32;
+      n += run;
+      if (run < 32) {
+        stray = __shfl_sync(0xffffffffu, out, run);
+        break;
+      }
+    }
+    if (lane == 0) accepted = n, odd = stray;
+  }
+  __syncthreads();
+  const int n = accepted;
+  const bool refused = n < have, stray = refused && odd != 0;
+  if (stray) flags |= KDA_DEV_TOKEN_OOB;
+
+  Weights<In> w{target + (int64_t)n * a.V, nullptr, -1};
+  if (refused && !stray) {
+    if (a.proposal) w.q = proposal + (int64_t)n * a.V;
+    else w.without = __ldg(drafts + n);
+  }
+  const int piece = ((a.V + C * VA_WARPS - 1) / (C * VA_WARPS) + 31) & ~31;
+  const int64_t first = (int64_t)(rank * VA_WARPS + warp) * piece;
+  const int v0 = (int)min((int64_t)a.V, first), v1 = (int)min((int64_t)a.V, first + piece);
+  unsigned long long before = 0, total = 0;
+  float rough = 0.f;
+  for (;;) {
+    float f;
+    const unsigned long long s = warp_sum(w, v0, v1, f);
+    if (lane == 0) sums[warp] = s, roughs[warp] = f;
+    __syncthreads();
+    if (tid == 0) {
+      unsigned long long t = 0;
+      float r = 0.f;
+      for (int i = 0; i < VA_WARPS; ++i) t += sums[i], r += roughs[i];
+      total_here = t, rough_here = r;
+    }
+    cluster.sync();
+    before = total = 0, rough = 0.f;
+    for (int i = 0; i < C; ++i) {
+      const unsigned long long t = *cluster.map_shared_rank(&total_here, i);
+      rough += *cluster.map_shared_rank(&rough_here, i);
+      if (i < rank) before += t;
+      total += t;
+    }
+    cluster.sync();  // the others have read this CTA's sums
+    if (total != 0 || (!w.q && w.without < 0)) break;
+    w.q = nullptr, w.without = -1;  // nothing is left of the target there: it is taken as it stands
+  }
+
+  const bool usable = total != 0 && rough < VA_SUM;
+  if (!usable) flags |= KDA_DEV_PROB_OOB;
+  if (rank == 0 && tid == 0) {
+    a.accepted[b] = n + 1;
+    if (!usable) a.tokens[(int64_t)b * a.W + n] = -1;
+    if (flags) flag_status(a.status, flags);
+    add_work(a.status, n + 1);
+  }
+  if (rank == 0)
+    for (int i = tid; i < a.W; i += VA_NT)
+      if (i != n) a.tokens[(int64_t)b * a.W + i] = i < n ? __ldg(drafts + i) : -1;
+  if (!usable) return;
+
+  // the last random number in units of 2^-64, within [0, 1)
+  const float r = __ldg(u + a.W - 1);
+  const double r1 = r > 0.f ? fmin((double)r, 1.0 - 0x1p-53) : 0.0;
+  const unsigned long long threshold = __umul64hi((unsigned long long)(r1 * 0x1p64), total);
+  if (threshold < before || threshold - before >= total_here) return;
+  // of this CTA's pieces the one that goes beyond it
+  int at = 0;
+  unsigned long long sum = before;
+  while (at < VA_WARPS - 1 && sum + sums[at] <= threshold) sum += sums[at++];
+  // and of its tokens: a thread has a run of them
+  const int64_t p0 = (int64_t)(rank * VA_WARPS + at) * piece;
+  const int each = (piece + VA_NT - 1) / VA_NT;
+  const int t0 = (int)min((int64_t)a.V, p0 + (int64_t)tid * each), t1 = (int)min(min((int64_t)a.V, p0 + piece), p0 + (int64_t)(tid + 1) * each);
+  unsigned long long mine = 0;
+  for (int v = t0; v < t1; ++v) mine += w(to_f32(w.p[v]), w.q ? to_f32(w.q[v]) : 0.f, v);
+  unsigned long long upto = mine;
+#pragma unroll
+  for (int i = 1; i < 32; i <<= 1) {
+    const unsigned long long o = __shfl_up_sync(0xffffffffu, upto, i);
+    if (lane >= i) upto += o;
+  }
+  if (lane == 31) scan[warp] = upto;
+  __syncthreads();
+  for (int i = 0; i < warp; ++i) sum += scan[i];
+  sum += upto - mine;
+  if (threshold < sum || threshold - sum >= mine) return;
+  int v = t0;
+  for (; v < t1 - 1; ++v) {
+    sum += w(to_f32(w.p[v]), w.q ? to_f32(w.q[v]) : 0.f, v);
+    if (sum > threshold) break;
+  }
+  a.tokens[(int64_t)b * a.W + n] = v;
+}
+
+template <typename In>
+cudaError_t accept_launch(const VerifyAcceptArgs& a, int cluster, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(a.B * cluster));
+  cfg.blockDim = dim3(VA_NT);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, verify_accept_kernel<In>, a);
+}
+
+}  // namespace
+
+cudaError_t launch_verify_accept(const VerifyAcceptArgs& a, cudaStream_t s) {
+  int cluster = VA_MOST;
+  while (cluster > 1 && (int64_t)a.B * cluster > 4 * 152) cluster >>= 1;
+  return a.bf16 ? accept_launch<bf16>(a, cluster, s) : accept_launch<float>(a, cluster, s);
+}
+
+}  // namespace kda

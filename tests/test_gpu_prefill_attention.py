@@ -1,0 +1,236 @@
+"""Prompt attention and its gradients against the definitions in fp64, at the lengths, heads, types and masks where the kernels
+change course; the bounds are derived in _prompt.py."""
+import math
+
+import pytest
+import torch
+
+import _prompt as P
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+LENGTHS = [[1], [2], [63, 1, 64], [65, 0, 127, 5], [128, 129], [255, 256, 257], [300, 3, 511]]
+
+
+@pytest.mark.parametrize("lengths", LENGTHS, ids=str)
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("heads", [(2, 2), (4, 1)], ids=str)
+def test_lengths(cuda, lengths, dtype, heads):
+    P.compare(cuda, lengths, *heads, 128, dtype, seed=sum(lengths))
+
+
+@pytest.mark.parametrize("d", [16, 32, 64, 128])
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("heads", [(1, 1), (6, 2), (12, 1), (5, 5)], ids=str)
+def test_heads_and_sizes(cuda, d, dtype, heads):
+    P.compare(cuda, [70, 200, 13], *heads, d, dtype, seed=d, packed=True)
+
+
+@pytest.mark.parametrize("window", [1, 2, 64, 100, 128, 129, 300, 10000])
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (F32, 64)], ids=["bf16-128", "bf16-64", "f32-64"])
+def test_windows(cuda, window, dtype, d):
+    P.compare(cuda, [400, 37, 129], 4, 2, d, dtype, seed=window, window=window)
+
+
+@pytest.mark.parametrize("softcap,size", [(30.0, 1.0), (2.0, 1.5), (0.5, 1.0), (50.0, 4.0)])
+@pytest.mark.parametrize("dtype,d,window", [(BF, 128, 0), (BF, 64, 90), (F32, 32, 0)])
+def test_capped_scores(cuda, softcap, size, dtype, d, window):
+    P.compare(cuda, [260, 41], 4, 2, d, dtype, seed=5, softcap=softcap, size=size, window=window)
+
+
+@pytest.mark.parametrize("scale", [1.0, -0.2, 0.0, 0.01])
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_scales(cuda, scale, dtype):
+    P.compare(cuda, [200], 2, 1, 64, dtype, seed=2, scale=scale)
+
+
+@pytest.mark.parametrize("dtype,out_type,grad_type", [(BF, F32, F32), (BF, BF, F32), (F32, BF, BF), (BF, F32, BF)])
+@pytest.mark.parametrize("d", [32, 128])
+def test_types_of_the_results(cuda, dtype, out_type, grad_type, d):
+    P.compare(cuda, [130, 61], 4, 2, d, dtype, seed=3, out_type=out_type, grad_type=grad_type)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("start,tail", [(1, 0), (0, 1), (130, 77), (5, 300)])
+def test_rows_outside_the_sequences_are_left_alone(cuda, dtype, start, tail):
+    # they hold NaN in every input and are not written
+    P.compare(cuda, [129, 0, 64], 4, 2, 128, dtype, start=start, tail=tail, packed=True)
+    P.compare(cuda, [3], 2, 2, 64, dtype, start=start, tail=tail)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_large_scores(cuda, dtype):
+    # one key takes nearly everything, references move by hundreds of powers of two
+    P.compare(cuda, [300, 150], 2, 1, 128, dtype, seed=9, size=5.0)
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (F32, 64)])
+def test_many_sequences(cuda, dtype, d):
+    lengths = [(7 * i * i + 3) % 97 for i in range(200)] + [0, 0, 900] + [1] * 40
+    P.compare(cuda, lengths, 2, 1, d, dtype, seed=4)
+
+
+@pytest.mark.parametrize("dtype,d,heads", [(BF, 128, (4, 1)), (BF, 64, (3, 3)), (F32, 32, (2, 2))])
+@pytest.mark.parametrize("window", [0, 700])
+def test_longer_prompts(cuda, dtype, d, heads, window):
+    P.compare(cuda, [2500, 1100], *heads, d, dtype, seed=6, window=window)
+
+
+def test_nothing_to_do(cuda):
+    e = lambda *s: torch.zeros(*s, device="cuda")  # noqa: E731
+    cuda.kda_prefill_attention(e(0, 2, 16), e(0, 1, 16), e(0, 1, 16), P.cu([0, 0]), 0, e(0, 2, 16))
+    out = torch.full((4, 2, 16), 7.0, device="cuda")
+    cuda.kda_prefill_attention(e(4, 2, 16), e(4, 1, 16), e(4, 1, 16), P.cu([]), 4, out)
+    cuda.kda_prefill_attention(e(4, 2, 16), e(4, 1, 16), e(4, 1, 16), P.cu([0, 0, 0]), 4, out)
+    assert (out == 7.0).all()
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (F32, 64)])
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("window", [0, 50])
+def test_what_a_row_does_not_see_does_not_matter(cuda, dtype, d, value, window):
+    """Values that are no numbers at some tokens: rows that do not see them are as without, the others are no numbers
+    in those channels alone (values), or anywhere (keys)."""
+    lengths, where = [150, 200], [40, 149, 150 + 60, 150 + 129]
+    T = sum(lengths)
+    q, k, v, _ = P.inputs(T, 4, 2, d, dtype, 8)
+    seq = torch.tensor([0] * 150 + [1] * 200, device="cuda")
+    pos = torch.cat([torch.arange(n, device="cuda") for n in lengths])
+    sees = torch.zeros(T, dtype=torch.bool, device="cuda")
+    for w in where:
+        hit = (seq == seq[w]) & (pos >= pos[w])
+        if window:
+            hit &= pos < pos[w] + window
+        sees |= hit
+    args = (P.cu(lengths), 200)
+    clean = P.run(cuda, q, k, v, *args, window=window)
+    v2 = v.clone()
+    v2[where, :, 3] = value
+    got = P.run(cuda, q, k, v2, *args, window=window)
+    assert torch.equal(got["out"][~sees], clean["out"][~sees]) and torch.equal(got["lse"], clean["lse"])
+    others = [c for c in range(d) if c != 3]
+    assert torch.equal(got["out"][..., others], clean["out"][..., others])
+    assert not torch.isfinite(got["out"][sees][..., 3]).any()
+    k2 = k.clone()
+    k2[where] = math.nan
+    got = P.run(cuda, q, k2, v, *args, window=window)
+    assert torch.equal(got["out"][~sees], clean["out"][~sees]) and torch.equal(got["lse"][~sees], clean["lse"][~sees])
+    assert torch.isnan(got["out"][sees]).all() and torch.isnan(got["lse"][sees]).all()
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (F32, 64)])
+def test_a_gradient_stays_within_its_sequence(cuda, dtype, d):
+    lengths = [70, 130, 90]
+    q, k, v, d_out = P.inputs(290, 4, 2, d, dtype, 11)
+    clean = P.run(cuda, q, k, v, P.cu(lengths), 130, d_out)
+    for x in (q, k, v, d_out):
+        x[100] = math.nan
+    got = P.run(cuda, q, k, v, P.cu(lengths), 130, d_out)
+    others = torch.ones(290, dtype=torch.bool, device="cuda")
+    others[70:200] = False
+    for n in got:
+        assert torch.equal(got[n][others], clean[n][others]), n
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 32), (F32, 64)])
+def test_the_same_call_gives_the_same_bits(cuda, dtype, d):
+    lengths = [777, 5, 300]
+    q, k, v, d_out = P.inputs(sum(lengths), 6, 2, d, dtype, 12)
+    a = P.run(cuda, q, k, v, P.cu(lengths), 777, d_out)
+    b = P.run(cuda, q, k, v, P.cu(lengths), 777, d_out)
+    # and the batch around a sequence changes nothing
+    at = slice(777, 782)
+    alone = P.run(cuda, q[at], k[at], v[at], P.cu([5]), 5, d_out[at])
+    for n in a:
+        assert torch.equal(a[n], b[n]), n
+        assert torch.equal(a[n][at], alone[n]), n
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (F32, 64)])
+def test_captured_and_on_another_stream(cuda, dtype, d):
+    lengths = [140, 33]
+    q, k, v, d_out = P.inputs(173, 4, 2, d, dtype, 13)
+    want = P.run(cuda, q, k, v, P.cu(lengths), 140, d_out)
+    offsets = P.cu(lengths)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = P.run(cuda, q, k, v, offsets, 140, d_out)
+    torch.cuda.current_stream().wait_stream(side)
+    for n in want:
+        assert torch.equal(want[n], got[n]), n
+    out, lse = torch.zeros_like(want["out"]), torch.zeros_like(want["lse"])
+    grads = [torch.zeros_like(want[n]) for n in ("dq", "dk", "dv")]
+    ws = torch.empty(cuda.kda_prefill_attention_backward_workspace_size(173, 2, 4, 2, d), dtype=torch.uint8, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cuda.kda_prefill_attention(q, k, v, offsets, 140, out, lse=lse)
+        cuda.kda_prefill_attention_backward(d_out, q, k, v, out, lse, offsets, 140, *grads, ws)
+    for fresh in range(2):
+        if fresh:  # other tokens, cut elsewhere
+            new = P.inputs(173, 4, 2, d, dtype, 14)
+            for x, y in zip((q, k, v, d_out), new):
+                x.copy_(y)
+            offsets.copy_(P.cu([20, 140]))
+            want = P.run(cuda, q, k, v, offsets, 140, d_out)
+        ws.fill_(255)
+        graph.replay()
+        rows = slice(0, 160 if fresh else 173)
+        for n, x in zip(("out", "lse", "dq", "dk", "dv"), (out, lse, *grads)):
+            assert torch.equal(want[n][rows], x[rows]), n
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (F32, 64)])
+@pytest.mark.parametrize("offsets,longest,written", [([0, 100, 300, 340], 150, [(0, 100), (300, 340)]),
+                                                     ([0, 100, 341], 400, [(0, 100)]),
+                                                     ([-1, 100, 340], 400, [(100, 340)])])
+def test_offsets_out_of_range_are_flagged(cuda, dtype, d, offsets, longest, written):
+    q, k, v, d_out = P.inputs(340, 4, 2, d, dtype, 15)
+    status = torch.zeros(2, dtype=torch.int32, device="cuda")
+    at = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    got = P.run(cuda, q, k, v, at, longest, d_out, dev_status=status)
+    assert status[0].item() == cuda.KDA_DEV_SEQ_OOB
+    rows = torch.zeros(340, dtype=torch.bool, device="cuda")
+    for a, b in written:
+        rows[a:b] = True
+        alone = P.run(cuda, q[a:b], k[a:b], v[a:b], P.cu([b - a]), b - a, d_out[a:b])
+        for n in got:
+            assert torch.equal(got[n][a:b], alone[n]), n
+    for n in got:
+        assert (got[n][~rows] == 7.0).all(), n
+
+
+def test_work_is_counted(cuda):
+    for dtype in (BF, F32):
+        q, k, v, d_out = P.inputs(200, 6, 2, 64, dtype, 16)
+        status = torch.zeros(2, dtype=torch.int32, device="cuda")
+        P.run(cuda, q, k, v, P.cu([120, 50]), 120, dev_status=status)
+        assert status.tolist() == [0, 170 * 6]
+        P.run(cuda, q, k, v, P.cu([120, 50]), 120, d_out, dev_status=status)
+        assert status.tolist() == [0, 3 * 170 * 6]
+
+
+@pytest.mark.parametrize("softcap,window", [(0.0, 0), (3.0, 0), (0.0, 17)])
+def test_gradients_against_differences(cuda, softcap, window):
+    """Along a random direction: the fp32 loss's central difference and the gradient's product with the direction.  The
+    loss sums 50 x 3 x 32 outputs of size 1 in fp64 from fp32 rows (2^-22 relative each), the step is 2^-7: noise
+    sqrt(4800) 2^-22 / 2^-7 < 0.003 and a third-order term of 2^-14 times the third derivative (within 50 here)."""
+    lengths = [40, 10]
+    q, k, v, d_out = P.inputs(50, 3, 1, 32, F32, 17)
+    got = P.run(cuda, q, k, v, P.cu(lengths), 40, d_out, softcap=softcap, window=window)
+
+    def loss(*x):
+        return (P.run(cuda, *x, P.cu(lengths), 40, softcap=softcap, window=window)["out"].double() * d_out.double()).sum().item()
+
+    g = torch.Generator(device="cuda").manual_seed(18)
+    for i, name in enumerate(("dq", "dk", "dv")):
+        x = [q, k, v]
+        step = torch.randn(x[i].shape, generator=g, device="cuda")
+        step /= step.norm()
+        h = 2.0 ** -7
+        up, down = list(x), list(x)
+        up[i], down[i] = x[i] + h * step, x[i] - h * step
+        slope = (loss(*up) - loss(*down)) / (2 * h)
+        want = (got[name].double() * step.double()).sum().item()
+        assert abs(slope - want) <= 0.01, (name, slope, want)
