@@ -42,6 +42,7 @@
 
 #include "common.cuh"
 #include "launch.h"
+#include "softcap.cuh"
 
 namespace kda {
 
@@ -49,7 +50,6 @@ constexpr int PA_NT = 128, PA_WARPS = 4;
 constexpr int PA_UNIT_COST = 2;
 constexpr int PA_SHARE = 2;  // positions on the line that a warp takes at least
 constexpr int PA_MAX_LEN = 0x7fffff00;  // token positions and the next tile's stay within 32 bits
-constexpr float PA_LOG2E = 1.4426950408889634f, PA_LN2 = 0.6931471805599453f;
 // How far (in powers of two) scores may run above the softmax reference before it is moved, and how far above it the largest
 // lies when it has moved.  fp16 probabilities use that type's range: up to 2^15 (the value scale's rounding to `lift` included),
 // so that they keep all their bits down to 2^-14 and are lost below 2^-25 only, 2^-34 of the largest.  fp32 calls move at
@@ -99,11 +99,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   uint32_t r;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
-  return r;
-}
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 // v 2^d, d <= 0, where 2^d alone may be below fp32's range (ex2 gives 0 there) though the product is not: references that
@@ -172,31 +167,6 @@ struct Piece {
     }
   }
 };
-
-// cap2 * tanh(y) given z = 2 log2(e) y, with cap2 = cap * log2(e).  Where all of a warp's |y| are up to 0.75 (|z| <= PA_NEAR) it is y
-// times a polynomial in y^2 for tanh(y) / y (a weighted least-squares fit that levels the relative error, 1.3e-7 in fp32):
-// no cancellation for small scores, and no use of the exponential's unit, which the exponentials fill already (256 ragged
-// requests, e4m3 cache, cap 30: 103 us without it, 101 with).  Else 1 - 2 / (1 + 2^z), within 1.2e-7 absolutely, and below |y| = 0.15
-// the odd series to y^7 (next term 6e-9 relatively there): 8e-7 relatively at worst.  fp32 calls take CUDA's tanhf.
-constexpr float PA_NEAR = 1.5f * PA_LOG2E;
-__host__ __device__ constexpr float pa_tanh(int i) {
-  constexpr float c[6] = {1.f, -0.333329588f, 0.133254066f, -0.0533444285f, 0.0195829086f, -0.0047162571f};
-  return c[i];
-}
-__device__ __forceinline__ float capped_near(float z, float cap2) {
-  const float y = z * (0.5f * PA_LN2), u = y * y;
-  float t = pa_tanh(5);
-#pragma unroll
-  for (int i = 4; i >= 0; --i) t = fmaf(t, u, pa_tanh(i));
-  return cap2 * y * t;
-}
-__device__ __forceinline__ float capped(float z, float cap2) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(z)));
-  const float y = z * (0.5f * PA_LN2), u = y * y;
-  const float small = cap2 * y * fmaf(u, fmaf(u, fmaf(u, -17.f / 315.f, 2.f / 15.f), -1.f / 3.f), 1.f);
-  return fabsf(z) < 0.3f * PA_LOG2E ? small : fmaf(-2.f * cap2, r, cap2);
-}
 
 // ---------------------------------------------------------------- the line of tiles
 

@@ -85,24 +85,6 @@ __device__ __forceinline__ uint4 load_codes(const void* pages, int64_t row, int 
   return w;
 }
 
-// capped_near of paged_attention.cuh for two scores, its coefficients multiplied out to powers of z.  Seven multiplications and
-// additions instead of two operations of the exponential's unit.
-struct CapPoly {
-  float k[6];
-  __device__ __forceinline__ explicit CapPoly(float cap2) {
-    constexpr float h = 0.5f * PA_LN2, h2 = h * h;
-    float w = cap2 * h;
-#pragma unroll
-    for (int i = 0; i < 6; ++i) k[i] = pa_tanh(i) * w, w *= h2;
-  }
-  __device__ __forceinline__ float2 operator()(float2 z) const {
-    const float2 u = mul2(z, z);
-    float2 t = both(k[5]);
-#pragma unroll
-    for (int i = 4; i >= 0; --i) t = fma2(t, u, both(k[i]));
-    return mul2(z, t);
-  }
-};
 __device__ __forceinline__ uint32_t pack_f16(float2 x) {
   const __half2 h = __floats2half2_rn(x.x, x.y);
   return *reinterpret_cast<const uint32_t*>(&h);

@@ -4,6 +4,7 @@
 
 #include "paged_attention.cuh"
 #include "tc_ptx.cuh"
+#include "tc_roles.cuh"
 #include "tmap.h"
 
 namespace kda {
@@ -13,18 +14,6 @@ namespace {
 constexpr int TC_TILE = 128, TC_D = 128;
 constexpr int TC_UNIT_COST = 2;        // tiles a unit counts beyond its own (64 ragged requests with 96 rows: 43.8 us; 1: 44.7, 4: 46.8)
 constexpr float TC_NONE = -3.402823466e38f;  // a softmax reference that has seen nothing (finite: no -inf - -inf)
-
-// A place in a ring of N with the parity of its current round.
-template <int N>
-struct TcRing {
-  int at = 0;
-  uint32_t parity = 0;
-  __device__ __forceinline__ explicit TcRing(int first = 0) : at(first) {}
-  __device__ __forceinline__ void step(int by = 1) {
-    at += by;
-    if (at >= N) at -= N, parity ^= 1;
-  }
-};
 
 struct TcMaps {
   CUtensorMap k, v;
@@ -77,25 +66,10 @@ struct TcTiles {
   __device__ __forceinline__ bool last() const { return tile + 1 == u.t1; }
 };
 
-// A bounded wait that also ends when another role has given up.
-__device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, int* dead) {
-  if (tc::bar_test(bar, parity)) return true;
-  for (int i = 0; i < 1 << 12; ++i) {
-    if (*reinterpret_cast<volatile int*>(dead)) return false;
-    if (tc::bar_wait(bar, parity, 1u << 10)) return true;
-  }
-  *reinterpret_cast<volatile int*>(dead) = 1;
-  return false;
-}
-
 // For tests of the way out (kda_set_test_fault): the copying warp leaves as if its wait for a slot had run out, at this tile of its
 // share, with the copies of those before it and of its keys on their way.  (Of an e4m3 cache, which has no such copies, the first
 // product's warp, at this tile of a unit: any statement more in the loaders cost the calls 10 %.)
 constexpr int TC_STALL_AT = 2;
-__device__ __forceinline__ bool tc_give_up(int* dead) {
-  *reinterpret_cast<volatile int*>(dead) = 1;
-  return false;
-}
 
 // One row of a part by one warp, token by token in fp32: the way out when the accumulators hold a NaN, which may come from
 // a query that meets a token it does not see (0 * NaN) or from an infinity meeting a split probability.  A lane has
@@ -150,11 +124,6 @@ __device__ __noinline__ void careful_row(const PagedAttnArgs& a, const PaPlan& p
 inline int page_box(int page_size) {  // largest power of two that divides the page, at most a tile
   const int b = page_size & -page_size;
   return b < TC_TILE ? b : TC_TILE;
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 }  // namespace

@@ -32,7 +32,7 @@ __global__ void __launch_bounds__(256)
   const unsigned lanes = __activemask();
 #pragma unroll
   for (int i = 1; i < L; i <<= 1) sum += __shfl_xor_sync(lanes, sum, i);
-  if (c == 0) stats[h * a.T + t] = make_float2(__ldg(a.lse + row) * PF_LOG2E, sum);
+  if (c == 0) stats[h * a.T + t] = make_float2(__ldg(a.lse + row) * PA_LOG2E, sum);
 }
 
 template <typename In, typename Out>
@@ -49,7 +49,9 @@ cudaError_t stats_launch(const PromptAttnArgs& a, const PromptGradArgs& g, float
 
 }  // namespace
 
-cudaError_t launch_prefill_attention(const PromptAttnArgs& a, cudaStream_t s) { return pf_f32(a, s); }
+cudaError_t launch_prefill_attention(const PromptAttnArgs& a, cudaStream_t s) {
+  return a.in_bf16 ? pf_tc(a, s) : pf_f32(a, s);
+}
 
 size_t prefill_attention_grad_ws_bytes(int64_t T, int N, int Hq, int Hkv, int d) {
   return ((size_t)T * Hq * sizeof(float2) + 255) & ~size_t(255);

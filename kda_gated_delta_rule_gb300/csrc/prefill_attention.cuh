@@ -3,20 +3,13 @@
 
 #include "common.cuh"
 #include "launch.h"
+#include "softcap.cuh"
 
 namespace kda {
 
 namespace {
 
-constexpr float PF_LOG2E = 1.4426950408889634f;
-constexpr float PF_LN2 = 0.6931471805599453f;
 constexpr float PF_NONE = -3.402823466e38f;  // a softmax reference that has seen nothing (finite: no -inf - -inf)
-
-__device__ __forceinline__ float pf_ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 // Blocks of `rows` tokens of all sequences, without sums over their lengths: the blocks of sequence i, at most
 // ceil(length / rows) of them, lie among the places floor(start_i / rows) + i .. floor(start_i+1 / rows) + i, which
@@ -68,6 +61,7 @@ __device__ __forceinline__ void pf_check_offsets(const PromptAttnArgs& a) {
 
 // The register forms (any head size; prefill_attention_f32.cu) and the tensor-memory ones (prefill_attention_tc.cu,
 // prefill_attention_grad_tc.cu).
+cudaError_t pf_tc(const PromptAttnArgs& a, cudaStream_t s);
 cudaError_t pf_f32(const PromptAttnArgs& a, cudaStream_t s);
 cudaError_t pf_f32_grad(const PromptAttnArgs& a, const PromptGradArgs& g, const float2* stats, cudaStream_t s);
 

@@ -153,10 +153,10 @@ __device__ __forceinline__ float score2(float dot, float scale, float cap, float
   if (cap > 0.f) {
     const float t = tanhf(x / cap);
     slope = 1.f - t * t;
-    return cap * t * PF_LOG2E;
+    return cap * t * PA_LOG2E;
   }
   slope = 1.f;
-  return x * PF_LOG2E;
+  return x * PA_LOG2E;
 }
 
 template <int D, typename In>
@@ -202,12 +202,12 @@ __global__ void __launch_bounds__(PNT) pf_f32_kernel(const PromptAttnArgs a, con
       }
 #pragma unroll
       for (int n = 1; n < 16; n <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, n));
-      const float by = pf_ex2(m[i] - top);
+      const float by = ex2(m[i] - top);
       m[i] = top;
       float sum = 0.f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float p = pf_ex2(s[i][j] - top);
+        const float p = ex2(s[i][j] - top);
         sum += p;
         sp[(ty + 16 * i) * S::PLD + tx + 16 * j] = p;
       }
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(PNT) pf_f32_kernel(const PromptAttnArgs a, con
 #pragma unroll
     for (int c = 0; c < S::CPT; ++c) o[i][c] /= l[i];
     store_row<D>(a.out, a.out_bf16, t * a.out_stride + h * D, o[i]);
-    if (tx == 0 && a.lse) a.lse[t * a.Hq + h] = m[i] * PF_LN2 + logf(l[i]);
+    if (tx == 0 && a.lse) a.lse[t * a.Hq + h] = m[i] * PA_LN2 + logf(l[i]);
   }
   if (tid == 0) add_work(a.status, rows);
 }
@@ -277,7 +277,7 @@ __device__ __forceinline__ void tile_grads(const PromptAttnArgs& a, const float2
       const bool seen = r < rows && key < len && key <= row && key > row - window;
       float slope;
       const float y = score2(s[i][j], a.scale, a.softcap, slope);
-      const float p = seen ? pf_ex2(y - st.x) : 0.f;
+      const float p = seen ? ex2(y - st.x) : 0.f;
       if (sp) sp[r * S::PLD + tx + 16 * j] = p;
       sds[r * S::PLD + tx + 16 * j] = seen ? p * (dp[i][j] - st.y) * slope : 0.f;
     }
@@ -423,14 +423,6 @@ cudaError_t grad_launch(const PromptAttnArgs& a, const PromptGradArgs& g, const 
 }  // namespace
 
 cudaError_t pf_f32(const PromptAttnArgs& a, cudaStream_t s) {
-  if (a.in_bf16) {
-    switch (a.d) {
-      case 16: return forward_launch<16, bf16>(a, s);
-      case 32: return forward_launch<32, bf16>(a, s);
-      case 64: return forward_launch<64, bf16>(a, s);
-      default: return forward_launch<128, bf16>(a, s);
-    }
-  }
   switch (a.d) {
     case 16: return forward_launch<16, float>(a, s);
     case 32: return forward_launch<32, float>(a, s);

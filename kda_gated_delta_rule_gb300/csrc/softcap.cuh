@@ -1,0 +1,64 @@
+// The softmax's exponential and the scores' tanh cap, in powers of two.
+#pragma once
+
+#include "f32x2.cuh"
+
+namespace kda {
+
+namespace {
+
+constexpr float PA_LOG2E = 1.4426950408889634f, PA_LN2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// cap2 * tanh(y) given z = 2 log2(e) y, with cap2 = cap * log2(e).  Where all of a warp's |y| are up to 0.75 (|z| <= PA_NEAR) it is y
+// times a polynomial in y^2 for tanh(y) / y (a weighted least-squares fit that levels the relative error, 1.3e-7 in fp32):
+// no cancellation for small scores, and no use of the exponential's unit, which the exponentials fill already (256 ragged
+// requests, e4m3 cache, cap 30: 103 us without it, 101 with).  Else 1 - 2 / (1 + 2^z), within 1.2e-7 absolutely, and below |y| = 0.15
+// the odd series to y^7 (next term 6e-9 relatively there): 8e-7 relatively at worst.  fp32 calls take CUDA's tanhf.
+constexpr float PA_NEAR = 1.5f * PA_LOG2E;
+__host__ __device__ constexpr float pa_tanh(int i) {
+  constexpr float c[6] = {1.f, -0.333329588f, 0.133254066f, -0.0533444285f, 0.0195829086f, -0.0047162571f};
+  return c[i];
+}
+__device__ __forceinline__ float capped_near(float z, float cap2) {
+  const float y = z * (0.5f * PA_LN2), u = y * y;
+  float t = pa_tanh(5);
+#pragma unroll
+  for (int i = 4; i >= 0; --i) t = fmaf(t, u, pa_tanh(i));
+  return cap2 * y * t;
+}
+__device__ __forceinline__ float capped(float z, float cap2) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(z)));
+  const float y = z * (0.5f * PA_LN2), u = y * y;
+  const float small = cap2 * y * fmaf(u, fmaf(u, fmaf(u, -17.f / 315.f, 2.f / 15.f), -1.f / 3.f), 1.f);
+  return fabsf(z) < 0.3f * PA_LOG2E ? small : fmaf(-2.f * cap2, r, cap2);
+}
+
+// capped_near for two scores, its coefficients multiplied out to powers of z.  Seven multiplications and
+// additions instead of two operations of the exponential's unit.
+struct CapPoly {
+  float k[6];
+  __device__ __forceinline__ explicit CapPoly(float cap2) {
+    constexpr float h = 0.5f * PA_LN2, h2 = h * h;
+    float w = cap2 * h;
+#pragma unroll
+    for (int i = 0; i < 6; ++i) k[i] = pa_tanh(i) * w, w *= h2;
+  }
+  __device__ __forceinline__ float2 operator()(float2 z) const {
+    const float2 u = mul2(z, z);
+    float2 t = both(k[5]);
+#pragma unroll
+    for (int i = 4; i >= 0; --i) t = fma2(t, u, both(k[i]));
+    return mul2(z, t);
+  }
+};
+
+}  // namespace
+
+}  // namespace kda

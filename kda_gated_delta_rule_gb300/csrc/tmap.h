@@ -54,6 +54,21 @@ inline bool encode_token_map_sw128(CUtensorMap* map, const void* base, long long
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// bf16 [rows][H][d], d <= 128, rows `stride` elements apart; box = 64 channels x 1 head x box_rows rows with the 128-byte swizzle, as
+// above.  Channels beyond d read as zeros.
+inline bool encode_rows_map_sw128(CUtensorMap* map, const void* base, long long rows, int H, int d, long long stride, int box_rows) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t es = 2;
+  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)H, (cuuint64_t)rows};
+  const cuuint64_t strides[2] = {d * es, (cuuint64_t)stride * es};
+  const cuuint32_t box[3] = {64, 1, (cuuint32_t)box_rows};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // [rows][128] bf16 cache rows; box = box_rows rows x 64 channels with the 128-byte swizzle, as above.
 inline bool encode_cache_map(CUtensorMap* map, const void* base, long long rows, int box_rows) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
