@@ -82,12 +82,15 @@ size_t kda_state_bytes_per_head(int dk, int dv);
  * KDA_TEST_FAULT_STALL_CACHE_COPIES makes the tensor-memory forms of later kda_paged_attention calls (d = 128, bf16 queries
  * and outputs) leave at the third tile of a worker's share (of a unit, with an e4m3 cache) as if a bounded wait had run
  * out: the worker lets its copies arrive, flags KDA_DEV_TIMEOUT and returns; rows that it had a part of are not defined.
+ * KDA_TEST_FAULT_STALL_PROMPT_COPIES makes the tensor-memory kernels of later kda_prefill_attention and
+ * kda_prefill_attention_backward calls (bf16 inputs) do the same at the third tile that a CTA walks; rows of such CTAs are not written.
  * KDA_TEST_FAULT_NONE (the initial value) restores normal calls.  Process-wide, not thread-safe; for tests.
  * Returns KDA_ERR_INVALID_ARG for an unknown value.
  */
 #define KDA_TEST_FAULT_NONE 0
 #define KDA_TEST_FAULT_STALL_RECORD_INPUTS 1
 #define KDA_TEST_FAULT_STALL_CACHE_COPIES 2
+#define KDA_TEST_FAULT_STALL_PROMPT_COPIES 3
 kda_status kda_set_test_fault(int fault);
 
 /*

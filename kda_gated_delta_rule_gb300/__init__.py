@@ -28,11 +28,13 @@ __all__ = [
     "kda_qk_norm_rope", "kda_qk_norm_rope_backward", "kda_qk_norm_rope_backward_workspace_size", "kda_kv_write",
     "kda_kv_read", "kda_paged_attention", "kda_paged_attention_workspace_size", "kda_prefill_attention",
     "kda_prefill_attention_backward", "kda_prefill_attention_backward_workspace_size", "kda_verify_accept",
-    "kda_debug_checks", "kda_set_test_fault", "KDA_TEST_FAULT_NONE", "KDA_TEST_FAULT_STALL_RECORD_INPUTS", "KDA_TEST_FAULT_STALL_CACHE_COPIES", "CFBI_CHUNK", "CFBI_ROW_FLOATS", "EXPORTED_SYMBOLS",
+    "kda_debug_checks", "kda_set_test_fault", "KDA_TEST_FAULT_NONE", "KDA_TEST_FAULT_STALL_RECORD_INPUTS", "KDA_TEST_FAULT_STALL_CACHE_COPIES", "KDA_TEST_FAULT_STALL_PROMPT_COPIES",
+    "CFBI_CHUNK", "CFBI_ROW_FLOATS", "EXPORTED_SYMBOLS",
 ]
 
 KDA_OK = 0
 KDA_TEST_FAULT_NONE, KDA_TEST_FAULT_STALL_RECORD_INPUTS, KDA_TEST_FAULT_STALL_CACHE_COPIES = 0, 1, 2
+KDA_TEST_FAULT_STALL_PROMPT_COPIES = 3
 KDA_DEV_SLOT_OOB, KDA_DEV_SEQ_OOB, KDA_DEV_TIMEOUT, KDA_DEV_ACCEPT_OOB = 1, 2, 4, 8
 KDA_DEV_POS_OOB, KDA_DEV_PAGE_OOB, KDA_DEV_TOKEN_OOB, KDA_DEV_PROB_OOB = 16, 32, 64, 128
 F32, BF16 = 0, 1

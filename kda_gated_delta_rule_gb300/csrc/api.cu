@@ -188,7 +188,7 @@ int kda_version(void) { return kVersion; }
 
 kda_status kda_set_test_fault(int fault) {
   if (fault != KDA_TEST_FAULT_NONE && fault != KDA_TEST_FAULT_STALL_RECORD_INPUTS &&
-      fault != KDA_TEST_FAULT_STALL_CACHE_COPIES)
+      fault != KDA_TEST_FAULT_STALL_CACHE_COPIES && fault != KDA_TEST_FAULT_STALL_PROMPT_COPIES)
     return KDA_ERR_INVALID_ARG;
   g_test_fault = fault;
   return KDA_OK;
@@ -862,6 +862,7 @@ kda::PromptAttnArgs prompt_args(const kda_prefill_attention_args* a) {
   p.out_bf16 = a->out_dtype == KDA_DTYPE_BF16;
   p.lse = a->lse;
   p.status = a->dev_status;
+  p.test_stall = g_test_fault == KDA_TEST_FAULT_STALL_PROMPT_COPIES;
   return p;
 }
 

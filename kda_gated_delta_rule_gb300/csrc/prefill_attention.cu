@@ -53,8 +53,13 @@ cudaError_t launch_prefill_attention(const PromptAttnArgs& a, cudaStream_t s) {
   return a.in_bf16 ? pf_tc(a, s) : pf_f32(a, s);
 }
 
+namespace {
+size_t stats_bytes(int64_t T, int Hq) { return ((size_t)T * Hq * sizeof(float2) + 255) & ~size_t(255); }
+}  // namespace
+
 size_t prefill_attention_grad_ws_bytes(int64_t T, int N, int Hq, int Hkv, int d) {
-  return ((size_t)T * Hq * sizeof(float2) + 255) & ~size_t(255);
+  const int parts = pg_parts(T, Hq, Hkv);
+  return stats_bytes(T, Hq) + (parts > 1 ? (size_t)parts * 2 * T * Hkv * d * 4 : 0);
 }
 
 cudaError_t launch_prefill_attention_backward(const PromptAttnArgs& a, const PromptGradArgs& g, cudaStream_t s) {
@@ -62,7 +67,8 @@ cudaError_t launch_prefill_attention_backward(const PromptAttnArgs& a, const Pro
   cudaError_t e = a.in_bf16 ? (a.out_bf16 ? stats_launch<bf16, bf16>(a, g, stats, s) : stats_launch<bf16, float>(a, g, stats, s))
                             : (a.out_bf16 ? stats_launch<float, bf16>(a, g, stats, s) : stats_launch<float, float>(a, g, stats, s));
   if (e != cudaSuccess) return e;
-  return pf_f32_grad(a, g, stats, s);
+  if (!a.in_bf16) return pf_f32_grad(a, g, stats, s);
+  return pf_tc_grad(a, g, stats, reinterpret_cast<float*>(static_cast<char*>(g.ws) + stats_bytes(a.T, a.Hq)), s);
 }
 
 }  // namespace kda

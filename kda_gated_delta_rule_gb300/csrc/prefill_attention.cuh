@@ -62,6 +62,9 @@ __device__ __forceinline__ void pf_check_offsets(const PromptAttnArgs& a) {
 // The register forms (any head size; prefill_attention_f32.cu) and the tensor-memory ones (prefill_attention_tc.cu,
 // prefill_attention_grad_tc.cu).
 cudaError_t pf_tc(const PromptAttnArgs& a, cudaStream_t s);
+// How many fp32 parts of dk and dv a gradient on the tensor cores adds up (1: none are written), and the gradient.
+int pg_parts(int64_t T, int Hq, int Hkv);
+cudaError_t pf_tc_grad(const PromptAttnArgs& a, const PromptGradArgs& g, const float2* stats, float* parts, cudaStream_t s);
 cudaError_t pf_f32(const PromptAttnArgs& a, cudaStream_t s);
 cudaError_t pf_f32_grad(const PromptAttnArgs& a, const PromptGradArgs& g, const float2* stats, cudaStream_t s);
 

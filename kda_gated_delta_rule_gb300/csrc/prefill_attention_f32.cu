@@ -1,4 +1,4 @@
-// Attention over packed prompts and its gradients on the CUDA cores, in fp32.
+// Attention over packed prompts and its gradients on the CUDA cores: fp32 inputs, any head size.
 //
 //   x_ij = scale q_i . k_j, capped: y = cap tanh(x / cap);  p = softmax_j(y) over the keys that row i sees;  o_i = sum_j p_ij v_j
 //   dv_j = sum_i p_ij do_i,  dy = p (do_i . v_j - D_i),  D_i = do_i . o_i,  dx = dy (1 - (y / cap)^2) scale
@@ -29,24 +29,13 @@ struct PfShape {
   static constexpr int PLD = PB + 4;
 };
 
-template <typename T>
-__device__ __forceinline__ float4 ld4(const T* p);
-template <>
-__device__ __forceinline__ float4 ld4<float>(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
-template <>
-__device__ __forceinline__ float4 ld4<bf16>(const bf16* p) {
-  const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
-  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
-                     __uint_as_float(w.y & 0xffff0000u));
-}
-
 // Rows 0 .. 63 of `base` (tokens `stride` apart); those from `valid` on are zeros.
-template <int D, typename In>
-__device__ __forceinline__ void load_block(float* dst, const In* base, int64_t stride, int valid) {
+template <int D>
+__device__ __forceinline__ void load_block(float* dst, const float* base, int64_t stride, int valid) {
   constexpr int C4 = D / 4;
   for (int i = threadIdx.x; i < PB * C4; i += PNT) {
     const int r = i / C4, c = (i - r * C4) * 4;
-    const float4 x = r < valid ? ld4<In>(base + r * stride + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4 x = r < valid ? __ldg(reinterpret_cast<const float4*>(base + r * stride + c)) : make_float4(0.f, 0.f, 0.f, 0.f);
     *reinterpret_cast<float4*>(dst + r * PfShape<D>::LD + c) = x;
   }
 }
@@ -159,7 +148,7 @@ __device__ __forceinline__ float score2(float dot, float scale, float cap, float
   return x * PA_LOG2E;
 }
 
-template <int D, typename In>
+template <int D>
 __global__ void __launch_bounds__(PNT) pf_f32_kernel(const PromptAttnArgs a, const int64_t places) {
   using S = PfShape<D>;
   extern __shared__ __align__(16) float sm[];
@@ -171,7 +160,7 @@ __global__ void __launch_bounds__(PNT) pf_f32_kernel(const PromptAttnArgs a, con
   const PfBlock b = pf_block(a, places - 1 - blockIdx.x, PB);
   if (b.len == 0) return;
   const int rows = min(PB, b.len - b.row0), window = a.window > 0 ? a.window : 0x7fffffff;
-  load_block<D>(sq, static_cast<const In*>(a.q) + (int64_t)(b.t0 + b.row0) * a.q_stride + h * D, a.q_stride, rows);
+  load_block<D>(sq, static_cast<const float*>(a.q) + (int64_t)(b.t0 + b.row0) * a.q_stride + h * D, a.q_stride, rows);
   float o[4][S::CPT], m[4], l[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -183,8 +172,8 @@ __global__ void __launch_bounds__(PNT) pf_f32_kernel(const PromptAttnArgs a, con
   for (int k0 = first / PB * PB; k0 <= last; k0 += PB) {
     const int64_t tok = b.t0 + k0;
     __syncthreads();
-    load_block<D>(sk, static_cast<const In*>(a.k) + tok * a.k_stride + kh * D, a.k_stride, b.len - k0);
-    load_block<D>(sv, static_cast<const In*>(a.v) + tok * a.v_stride + kh * D, a.v_stride, b.len - k0);
+    load_block<D>(sk, static_cast<const float*>(a.k) + tok * a.k_stride + kh * D, a.k_stride, b.len - k0);
+    load_block<D>(sv, static_cast<const float*>(a.v) + tok * a.v_stride + kh * D, a.v_stride, b.len - k0);
     __syncthreads();
     float s[4][4];
     dots<D>(sq, sk, s);
@@ -284,7 +273,7 @@ __device__ __forceinline__ void tile_grads(const PromptAttnArgs& a, const float2
   }
 }
 
-template <int D, typename In>
+template <int D>
 __global__ void __launch_bounds__(PNT)
     pf_f32_grad_kv_kernel(const PromptAttnArgs a, const PromptGradArgs g, const float2* __restrict__ stats, const int64_t places) {
   using S = PfShape<D>;
@@ -298,8 +287,8 @@ __global__ void __launch_bounds__(PNT)
   if (b.len == 0) return;
   const int k0 = b.row0, keys = min(PB, b.len - k0), window = a.window > 0 ? a.window : 0x7fffffff;
   const int64_t tok = b.t0 + k0;
-  load_block<D>(sk, static_cast<const In*>(a.k) + tok * a.k_stride + kh * D, a.k_stride, keys);
-  load_block<D>(sv, static_cast<const In*>(a.v) + tok * a.v_stride + kh * D, a.v_stride, keys);
+  load_block<D>(sk, static_cast<const float*>(a.k) + tok * a.k_stride + kh * D, a.k_stride, keys);
+  load_block<D>(sv, static_cast<const float*>(a.v) + tok * a.v_stride + kh * D, a.v_stride, keys);
   float dk[4][S::CPT], dv[4][S::CPT];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -311,8 +300,8 @@ __global__ void __launch_bounds__(PNT)
       const int64_t t = b.t0 + row0;
       const int rows = min(PB, b.len - row0);
       __syncthreads();
-      load_block<D>(sq, static_cast<const In*>(a.q) + t * a.q_stride + h * D, a.q_stride, rows);
-      load_block<D>(sdo, static_cast<const In*>(g.d_out) + t * g.d_out_stride + h * D, g.d_out_stride, rows);
+      load_block<D>(sq, static_cast<const float*>(a.q) + t * a.q_stride + h * D, a.q_stride, rows);
+      load_block<D>(sdo, static_cast<const float*>(g.d_out) + t * g.d_out_stride + h * D, g.d_out_stride, rows);
       __syncthreads();
       tile_grads<D>(a, stats + h * a.T + t, sq, sk, sdo, sv, row0, k0, rows, b.len, window, sp, sds);
       __syncthreads();
@@ -346,7 +335,7 @@ __global__ void __launch_bounds__(PNT)
   }
 }
 
-template <int D, typename In>
+template <int D>
 __global__ void __launch_bounds__(PNT)
     pf_f32_grad_q_kernel(const PromptAttnArgs a, const PromptGradArgs g, const float2* __restrict__ stats, const int64_t places) {
   using S = PfShape<D>;
@@ -358,8 +347,8 @@ __global__ void __launch_bounds__(PNT)
   if (b.len == 0) return;
   const int rows = min(PB, b.len - b.row0), window = a.window > 0 ? a.window : 0x7fffffff;
   const int64_t t = b.t0 + b.row0;
-  load_block<D>(sq, static_cast<const In*>(a.q) + t * a.q_stride + h * D, a.q_stride, rows);
-  load_block<D>(sdo, static_cast<const In*>(g.d_out) + t * g.d_out_stride + h * D, g.d_out_stride, rows);
+  load_block<D>(sq, static_cast<const float*>(a.q) + t * a.q_stride + h * D, a.q_stride, rows);
+  load_block<D>(sdo, static_cast<const float*>(g.d_out) + t * g.d_out_stride + h * D, g.d_out_stride, rows);
   float dq[4][S::CPT];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -369,8 +358,8 @@ __global__ void __launch_bounds__(PNT)
   for (int k0 = first / PB * PB; k0 <= last; k0 += PB) {
     const int64_t tok = b.t0 + k0;
     __syncthreads();
-    load_block<D>(sk, static_cast<const In*>(a.k) + tok * a.k_stride + kh * D, a.k_stride, b.len - k0);
-    load_block<D>(sv, static_cast<const In*>(a.v) + tok * a.v_stride + kh * D, a.v_stride, b.len - k0);
+    load_block<D>(sk, static_cast<const float*>(a.k) + tok * a.k_stride + kh * D, a.k_stride, b.len - k0);
+    load_block<D>(sv, static_cast<const float*>(a.v) + tok * a.v_stride + kh * D, a.v_stride, b.len - k0);
     __syncthreads();
     tile_grads<D>(a, stats + h * a.T + t, sq, sk, sdo, sv, b.row0, k0, rows, b.len, window, nullptr, sds);
     __syncwarp();
@@ -394,23 +383,23 @@ __global__ void __launch_bounds__(PNT)
   if (tid == 0) add_work(a.status, rows);
 }
 
-template <int D, typename In>
+template <int D>
 cudaError_t forward_launch(const PromptAttnArgs& a, cudaStream_t s) {
   using S = PfShape<D>;
   const int smem = (3 * PB * S::LD + PB * S::PLD) * 4;
-  auto kernel = pf_f32_kernel<D, In>;
+  auto kernel = pf_f32_kernel<D>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int64_t places = pf_places(a.T, a.N, PB);
   return launch_pdl(kernel, dim3((unsigned)places, a.Hq), dim3(PNT), smem, s, a, places);
 }
 
-template <int D, typename In>
+template <int D>
 cudaError_t grad_launch(const PromptAttnArgs& a, const PromptGradArgs& g, const float2* stats, cudaStream_t s) {
   using S = PfShape<D>;
   const int smem_kv = (4 * PB * S::LD + 2 * PB * S::PLD) * 4, smem_q = (4 * PB * S::LD + PB * S::PLD) * 4;
-  auto kv = pf_f32_grad_kv_kernel<D, In>;
-  auto q = pf_f32_grad_q_kernel<D, In>;
+  auto kv = pf_f32_grad_kv_kernel<D>;
+  auto q = pf_f32_grad_q_kernel<D>;
   cudaError_t e = cudaFuncSetAttribute(kv, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_kv);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(q, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_q);
   if (e != cudaSuccess) return e;
@@ -424,27 +413,19 @@ cudaError_t grad_launch(const PromptAttnArgs& a, const PromptGradArgs& g, const 
 
 cudaError_t pf_f32(const PromptAttnArgs& a, cudaStream_t s) {
   switch (a.d) {
-    case 16: return forward_launch<16, float>(a, s);
-    case 32: return forward_launch<32, float>(a, s);
-    case 64: return forward_launch<64, float>(a, s);
-    default: return forward_launch<128, float>(a, s);
+    case 16: return forward_launch<16>(a, s);
+    case 32: return forward_launch<32>(a, s);
+    case 64: return forward_launch<64>(a, s);
+    default: return forward_launch<128>(a, s);
   }
 }
 
 cudaError_t pf_f32_grad(const PromptAttnArgs& a, const PromptGradArgs& g, const float2* stats, cudaStream_t s) {
-  if (a.in_bf16) {
-    switch (a.d) {
-      case 16: return grad_launch<16, bf16>(a, g, stats, s);
-      case 32: return grad_launch<32, bf16>(a, g, stats, s);
-      case 64: return grad_launch<64, bf16>(a, g, stats, s);
-      default: return grad_launch<128, bf16>(a, g, stats, s);
-    }
-  }
   switch (a.d) {
-    case 16: return grad_launch<16, float>(a, g, stats, s);
-    case 32: return grad_launch<32, float>(a, g, stats, s);
-    case 64: return grad_launch<64, float>(a, g, stats, s);
-    default: return grad_launch<128, float>(a, g, stats, s);
+    case 16: return grad_launch<16>(a, g, stats, s);
+    case 32: return grad_launch<32>(a, g, stats, s);
+    case 64: return grad_launch<64>(a, g, stats, s);
+    default: return grad_launch<128>(a, g, stats, s);
   }
 }
 

@@ -14,20 +14,14 @@
 // it, after the products that the scores' barrier already covers.  Probabilities are rounded to bf16 (2^-8) for the second
 // product, half a step like the output's own rounding; their sum is taken before that, in fp32.
 #include "device.h"
-#include "prefill_attention.cuh"
-#include "tc_roles.cuh"
-#include "tmap.h"
+#include "prefill_attention_tc.cuh"
 
 namespace kda {
 
 namespace {
 
-constexpr int PT_B = 128;                 // rows of a block, keys of a tile
-constexpr int PT_NT = 384;
-constexpr int PT_HALF = PT_B * 128;       // bytes of 64 channels of a block or tile
-constexpr int PT_O = 256, PT_TMEM = 512;  // columns: scores of the two blocks, then their accumulators
+constexpr int PT_O = 256;  // columns: scores of the two blocks, then their accumulators
 constexpr float PT_SLACK = 8.f;
-constexpr int PT_STALL_AT = 2;
 
 template <int D>
 struct PtCfg {
@@ -87,10 +81,6 @@ __device__ __forceinline__ bool pt_masked(const PtUnit& u, int tile, int window)
   return k0 + PT_B - 1 > u.row0[0] || k0 <= last - window;
 }
 
-__host__ __device__ constexpr uint32_t pt_idesc(int n) {  // 128 x n, bf16 operands
-  return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | (8u << 24);
-}
-
 __device__ __forceinline__ bool odd_bf16(uint32_t two) {  // a NaN or an infinity among the two
   return (two & 0x7f80u) == 0x7f80u || (two & 0x7f800000u) == 0x7f800000u;
 }
@@ -139,8 +129,7 @@ __global__ void __launch_bounds__(PT_NT, 1)
         const int blocks = u.rows[1] > 0 ? 2 : 1;
         tc::bar_arrive_expect_tx(&sh.q_full, blocks * C::SLOT);
         for (int s = 0; s < blocks; ++s)
-          for (int c = 0; c < C::HALVES; ++c)
-            tc::tma_load_3d(qbuf + s * C::SLOT + c * PT_HALF, &maps.q, c * 64, u.head[s], u.t0 + u.row0[s], &sh.q_full);
+          pt_load<D>(qbuf + s * C::SLOT, &maps.q, u.head[s], u.t0 + u.row0[s], &sh.q_full);
         TcRing<C::KR> kr;
         TcRing<C::VR> vr;
         for (int j = u.lo; j <= u.top; ++j) {
@@ -148,16 +137,14 @@ __global__ void __launch_bounds__(PT_NT, 1)
           ok = tc_wait(&sh.k_empty[kr.at], kr.parity ^ 1, &sh.dead);
           if (!ok) break;
           tc::bar_arrive_expect_tx(&sh.k_full[kr.at], C::SLOT);
-          for (int c = 0; c < C::HALVES; ++c)
-            tc::tma_load_3d(kslots + kr.at * C::SLOT + c * PT_HALF, &maps.k, c * 64, u.kv_head, tok, &sh.k_full[kr.at]);
+          pt_load<D>(kslots + kr.at * C::SLOT, &maps.k, u.kv_head, tok, &sh.k_full[kr.at]);
           ++sent_k;
           kr.step();
           if (a.test_stall && j == u.lo + PT_STALL_AT) ok = tc_give_up(&sh.dead);
           ok = ok && tc_wait(&sh.v_empty[vr.at], vr.parity ^ 1, &sh.dead);
           if (!ok) break;
           tc::bar_arrive_expect_tx(&sh.v_full[vr.at], C::SLOT);
-          for (int c = 0; c < C::HALVES; ++c)
-            tc::tma_load_3d(vslots + vr.at * C::SLOT + c * PT_HALF, &maps.v, c * 64, u.kv_head, tok, &sh.v_full[vr.at]);
+          pt_load<D>(vslots + vr.at * C::SLOT, &maps.v, u.kv_head, tok, &sh.v_full[vr.at]);
           ++sent_v;
           vr.step();
         }
@@ -284,22 +271,7 @@ __global__ void __launch_bounds__(PT_NT, 1)
 #pragma unroll
       for (int c = 0; c < PT_B; c += 64) tc::tmem_ld64(own_s + c, reinterpret_cast<float*>(x) + c);
       const int k0 = j * PT_B;
-      if constexpr (CAP) {
-        const CapPoly near(cap2);
-        float top = 0.f;
-#pragma unroll
-        for (int i = 0; i < PT_B / 2; ++i) {
-          x[i] = mul2(x[i], both(factor));
-          top = fmaxf(top, fmaxf(fabsf(x[i].x), fabsf(x[i].y)));
-        }
-        if (__all_sync(0xffffffffu, top <= PA_NEAR)) {
-#pragma unroll
-          for (int i = 0; i < PT_B / 2; ++i) x[i] = near(x[i]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < PT_B / 2; ++i) x[i] = make_float2(capped(x[i].x, cap2), capped(x[i].y, cap2));
-        }
-      }
+      if constexpr (CAP) pt_cap(x, factor, cap2);
       // of the tile the row sees keys from .. to - 1
       if (k0 + PT_B - 1 > u.row0[s] || k0 <= u.row0[s] + PT_B - 1 - window) {
         const int to = row + 1 - k0, from = row - k0 < window ? 0 : row - k0 - window + 1;
@@ -397,15 +369,7 @@ __global__ void __launch_bounds__(PT_NT, 1)
 #pragma unroll
             for (int i = 0; i < 16; ++i) o[i] *= by;
             if (odd) add_odd(c, o);
-            if (a.out_bf16) {
-              uint4* y = reinterpret_cast<uint4*>(static_cast<bf16*>(a.out) + t * a.out_stride + (int64_t)u.head[s] * a.d + c);
-              y[0] = make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]), pack_bf16(o[6], o[7]));
-              y[1] = make_uint4(pack_bf16(o[8], o[9]), pack_bf16(o[10], o[11]), pack_bf16(o[12], o[13]), pack_bf16(o[14], o[15]));
-            } else {
-              float4* y = reinterpret_cast<float4*>(static_cast<float*>(a.out) + t * a.out_stride + (int64_t)u.head[s] * a.d + c);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) y[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-            }
+            pt_store16(a.out, a.out_bf16, t * a.out_stride + (int64_t)u.head[s] * a.d + c, o);
           }
           __syncwarp();  // the next load is the whole warp's
         }
