@@ -21,25 +21,28 @@ struct PfBlock {
   int row0;     // the block's first token within the sequence
 };
 
-// The block at `place`; one whole warp asks.  A search with 32 probes at a time: N <= 32 is one load.
-__device__ __forceinline__ PfBlock pf_block(const PromptAttnArgs& a, int64_t place, int rows) {
+// The block of 1 << SHIFT tokens at `place`; one whole warp asks.  A search with 32 probes at a time: N <= 32 is one load.
+template <int SHIFT>
+__device__ __forceinline__ PfBlock pf_block(const PromptAttnArgs& a, int64_t place) {
   const int lane = threadIdx.x & 31;
   const int T = (int)a.T;
-  auto at = [&](int i) { return max(0, min(T, __ldg(a.cu + i))); };
-  int lo = 0, hi = a.N;
+  int lo = 0, hi = a.N, c0 = 0, c1 = -1;
   PfBlock b{0, 0, 0};
   while (hi > lo) {
     const int step = (hi - lo + 31) >> 5, i = lo + lane * step;
-    const bool ok = i < hi && (int64_t)(at(i) / rows) + i <= place;
+    if (i < hi) c0 = __ldg(a.cu + i), c1 = __ldg(a.cu + i + 1);
+    const bool ok = i < hi && (int64_t)(max(0, min(T, c0)) >> SHIFT) + i <= place;
     const int n = __popc(__ballot_sync(0xffffffffu, ok));
     if (n == 0) return b;
     lo += (n - 1) * step;
     hi = min(hi, lo + step);
-    if (step == 1) break;
+    if (step == 1) {
+      c0 = __shfl_sync(0xffffffffu, c0, n - 1), c1 = __shfl_sync(0xffffffffu, c1, n - 1);
+      break;
+    }
   }
-  const int c0 = __ldg(a.cu + lo), c1 = __ldg(a.cu + lo + 1);
   if (c0 < 0 || c1 < c0 || c1 > T || c1 - c0 > a.max_seqlen) return b;
-  const int64_t row0 = (place - ((int64_t)(c0 / rows) + lo)) * rows;
+  const int64_t row0 = (place - ((int64_t)(c0 >> SHIFT) + lo)) << SHIFT;
   if (row0 >= c1 - c0) return b;
   b.t0 = c0;
   b.len = c1 - c0;

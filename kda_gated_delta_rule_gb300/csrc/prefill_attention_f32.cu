@@ -17,7 +17,7 @@ namespace kda {
 
 namespace {
 
-constexpr int PB = 64;  // rows and keys of a block
+constexpr int PB = 64;  // rows and keys of a block (1 << 6)
 constexpr int PNT = 256;
 
 template <int D>
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(PNT) pf_f32_kernel(const PromptAttnArgs a, con
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, h = blockIdx.y, kh = h / (a.Hq / a.Hkv);
   if (blockIdx.x == 0 && h == 0 && tid < 32) pf_check_offsets(a);
   // the longest rows first: a sequence's last blocks see most keys
-  const PfBlock b = pf_block(a, places - 1 - blockIdx.x, PB);
+  const PfBlock b = pf_block<6>(a, places - 1 - blockIdx.x);
   if (b.len == 0) return;
   const int rows = min(PB, b.len - b.row0), window = a.window > 0 ? a.window : 0x7fffffff;
   load_block<D>(sq, static_cast<const float*>(a.q) + (int64_t)(b.t0 + b.row0) * a.q_stride + h * D, a.q_stride, rows);
@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(PNT)
   pdl_begin();
   const int tid = threadIdx.x, ty = tid >> 4, kh = blockIdx.y, group = a.Hq / a.Hkv;
   if (blockIdx.x == 0 && kh == 0 && tid < 32) pf_check_offsets(a);
-  const PfBlock b = pf_block(a, blockIdx.x, PB);
+  const PfBlock b = pf_block<6>(a, blockIdx.x);
   if (b.len == 0) return;
   const int k0 = b.row0, keys = min(PB, b.len - k0), window = a.window > 0 ? a.window : 0x7fffffff;
   const int64_t tok = b.t0 + k0;
@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(PNT)
   float *sq = sm, *sdo = sq + PB * S::LD, *sk = sdo + PB * S::LD, *sv = sk + PB * S::LD, *sds = sv + PB * S::LD;
   pdl_begin();
   const int tid = threadIdx.x, ty = tid >> 4, h = blockIdx.y, kh = h / (a.Hq / a.Hkv);
-  const PfBlock b = pf_block(a, places - 1 - blockIdx.x, PB);
+  const PfBlock b = pf_block<6>(a, places - 1 - blockIdx.x);
   if (b.len == 0) return;
   const int rows = min(PB, b.len - b.row0), window = a.window > 0 ? a.window : 0x7fffffff;
   const int64_t t = b.t0 + b.row0;

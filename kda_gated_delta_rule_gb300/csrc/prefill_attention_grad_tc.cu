@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(PT_NT, 1)
   if (blockIdx.x == 0 && warp == 0) pf_check_offsets(a);
   // the first keys first: most queries see them
   const int unit = blockIdx.x % (a.Hkv * nparts), kh = unit / nparts, part = unit - kh * nparts;
-  const PfBlock b = pf_block(a, blockIdx.x / (a.Hkv * nparts), PT_B);
+  const PfBlock b = pf_block<7>(a, blockIdx.x / (a.Hkv * nparts));
   if (b.len == 0) return;
   const int group = a.Hq / a.Hkv, h0 = kh * group + part * group / nparts, h1 = kh * group + (part + 1) * group / nparts;
   const int k0 = b.row0, keys = min(PT_B, b.len - k0), tile = k0 / PT_B;
@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(PT_NT, 1)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int window = a.window > 0 ? a.window : 0x7fffffff;
   const int h = blockIdx.x % a.Hq, kh = h / (a.Hq / a.Hkv);
-  const PfBlock b = pf_block(a, places - 1 - blockIdx.x / a.Hq, PT_B);  // the longest rows first
+  const PfBlock b = pf_block<7>(a, places - 1 - blockIdx.x / a.Hq);  // the longest rows first
   if (b.len == 0) return;
   const int rows = min(PT_B, b.len - b.row0);
   const int lo = max(0, b.row0 - window + 1) / PT_B, n = b.row0 / PT_B - lo + 1;
@@ -600,7 +600,7 @@ __global__ void __launch_bounds__(PT_NT, 1)
 __global__ void __launch_bounds__(256) pg_join_kernel(const PromptAttnArgs a, const PromptGradArgs g, const float* __restrict__ parts,
                                                       const int nparts) {
   pdl_begin();
-  const PfBlock b = pf_block(a, blockIdx.x, PT_B);
+  const PfBlock b = pf_block<7>(a, blockIdx.x);
   if (b.len == 0) return;
   const int per_row = a.d / 4, rows = min(PT_B, b.len - b.row0), kh = blockIdx.y >> 1, which = blockIdx.y & 1;
   const int64_t step = 2 * a.T * a.Hkv * a.d;

@@ -1,12 +1,14 @@
 // Attention over packed prompts on the 5th-generation tensor cores: bf16 inputs, any head size.
 //
-// A CTA has two blocks of 128 query rows that share their keys: the same tokens of two heads of a group where the group has an
+// A unit is two blocks of 128 query rows that share their keys: the same tokens of two heads of a group where the group has an
 // even number, else two neighbouring blocks of one head.  Per 128 keys and block, S = Q K^T (rows x keys) in tensor memory; a
 // thread has one row of it, so its maximum and sum need no exchange; P = exp2(S - reference) goes back as bf16 over the
 // scores it came from, as the row operand of O += P V.  While one block's softmax runs, the other's products do.
+// One CTA per SM walks units: the grid has a CTA for each, and one that runs takes over the next that has not started, the longest
+// rows first, so that a unit's start lies under the end of the one before.
 //   warps 0 to 3, 4 to 7   softmax of block 0, 1
 //   warp 8     issues the products (one thread)
-//   warp 9     brings Q, and K and V tiles into rings, by TMA (128-byte swizzle; channels beyond d as zeros)
+//   warp 9     takes units, and brings their Q, and K and V tiles into rings, by TMA (128-byte swizzle; channels beyond d as zeros)
 //   warps 10, 11   look at the V tiles with unseen keys: rows behind the sequence become zeros, values that are no numbers
 //              too (0 * NaN would reach rows that do not see them); rows that do see one get it at the end
 //
@@ -34,12 +36,23 @@ struct PtMaps {
   CUtensorMap q, k, v;
 };
 
+// The two blocks of a unit, and the key tiles that they walk.
+struct PtUnit {
+  int t0, len;  // len = 0: no more units
+  int row0[2], head[2], rows[2];  // rows = 0: no such block
+  int lo, hi[2], top;             // tiles lo .. hi[s]; top: the larger hi
+  int kv_head;
+};
+
 struct PtShared {
   // every barrier is waited on only by roles that see each of its rounds
+  PtFeed feed;
   uint64_t k_full[4], k_empty[4], v_full[4], v_ready[4], v_empty[4];
-  uint64_t q_full, s_full[2], p_full[2], o_full[2], drain;
+  uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], drain;
+  PtUnit unit[2];
+  int odd_v[2];  // by unit: a value that is no number was left out
   uint32_t tmem;
-  int dead, odd_v;
+  int dead;
 };
 template <int D>
 constexpr int pt_smem() {
@@ -48,25 +61,18 @@ constexpr int pt_smem() {
 }
 static_assert(pt_smem<128>() <= 227 * 1024, "shared memory of one SM");
 
-// The two blocks of a CTA, and the key tiles that they walk.
-struct PtUnit {
-  int t0, len;
-  int row0[2], head[2], rows[2];  // rows = 0: no such block
-  int lo, hi[2], top;             // tiles lo .. hi[s]; top: the larger hi
-  int kv_head;
-};
-
-__device__ __forceinline__ PtUnit pt_unit(const PromptAttnArgs& a, int64_t places, int pairs, bool by_heads, int window) {
-  const int64_t place = places - 1 - blockIdx.x / pairs;  // the longest rows first
-  const int pair = blockIdx.x % pairs;
-  const PfBlock b = pf_block(a, place, by_heads ? PT_B : 2 * PT_B);
+template <bool BY_HEADS>
+__device__ __forceinline__ PtUnit pt_unit(const PromptAttnArgs& a, int64_t places, int pairs, int id, int window) {
+  const int64_t place = places - 1 - id / pairs;  // the longest rows first
+  const int pair = id % pairs;
+  const PfBlock b = pf_block<BY_HEADS ? 7 : 8>(a, place);
   PtUnit u;
   u.t0 = b.t0, u.len = b.len;
   u.top = -1;
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
-    u.head[s] = by_heads ? 2 * pair + s : pair;
-    u.row0[s] = by_heads ? b.row0 : b.row0 + s * PT_B;
+    u.head[s] = BY_HEADS ? 2 * pair + s : pair;
+    u.row0[s] = BY_HEADS ? b.row0 : b.row0 + s * PT_B;
     u.rows[s] = max(0, min(PT_B, b.len - u.row0[s]));
     u.hi[s] = u.rows[s] > 0 ? (u.row0[s] + u.rows[s] - 1) / PT_B : -1;
     u.top = max(u.top, u.hi[s]);
@@ -75,44 +81,69 @@ __device__ __forceinline__ PtUnit pt_unit(const PromptAttnArgs& a, int64_t place
   u.kv_head = u.head[0] / (a.Hq / a.Hkv);
   return u;
 }
-// Whether some row of the CTA does not see some key of the tile.
+// Whether some row of the unit does not see some key of the tile.
 __device__ __forceinline__ bool pt_masked(const PtUnit& u, int tile, int window) {
   const int k0 = tile * PT_B, last = u.rows[1] > 0 ? u.row0[1] + u.rows[1] - 1 : u.row0[0] + u.rows[0] - 1;
   return k0 + PT_B - 1 > u.row0[0] || k0 <= last - window;
 }
 
-__device__ __forceinline__ bool odd_bf16(uint32_t two) {  // a NaN or an infinity among the two
-  return (two & 0x7f80u) == 0x7f80u || (two & 0x7f800000u) == 0x7f800000u;
+// Zeros for the rows of a V tile from `keys` on, and for what is no number in the others; true where there was such.  Two warps.
+template <int D>
+__device__ __forceinline__ bool pt_clean(unsigned char* tile, int keys, int t) {
+  constexpr int N = PT_B * 8 * (D / 64);  // pieces of 16 bytes: eight lie in a row's 128 bytes, in some order
+  bool odd = false;
+#pragma unroll 1
+  for (int i0 = t; i0 < N; i0 += 64 * 8) {
+    uint4 x[8];
+#pragma unroll
+    for (int n = 0; n < 8; ++n) x[n] = *(reinterpret_cast<uint4*>(tile) + i0 + 64 * n);
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+      uint4* at = reinterpret_cast<uint4*>(tile) + i0 + 64 * n;
+      const int row = ((i0 + 64 * n) >> 3) & (PT_B - 1);
+      // an exponent of all ones carries into the next bit
+      const uint32_t carry = ((x[n].x & 0x7f807f80u) + 0x00800080u) | ((x[n].y & 0x7f807f80u) + 0x00800080u) |
+                             ((x[n].z & 0x7f807f80u) + 0x00800080u) | ((x[n].w & 0x7f807f80u) + 0x00800080u);
+      if (row >= keys) {
+        *at = make_uint4(0, 0, 0, 0);
+      } else if (carry & 0x80008000u) {
+        odd = true;
+        uint16_t* e = reinterpret_cast<uint16_t*>(at);
+        for (int c = 0; c < 8; ++c)
+          if ((e[c] & 0x7f80) == 0x7f80) e[c] = 0;
+      }
+    }
+  }
+  tc::fence_proxy_async();
+  return odd;
 }
 
-template <int D, bool CAP>
+template <int D, bool CAP, bool BY_HEADS>
 __global__ void __launch_bounds__(PT_NT, 1)
-    prefill_attention_tc_kernel(const __grid_constant__ PtMaps maps, const PromptAttnArgs a, const int64_t places, const int pairs,
-                                const bool by_heads) {
+    prefill_attention_tc_kernel(const __grid_constant__ PtMaps maps, const PromptAttnArgs a, const int64_t places, const int pairs) {
   using C = PtCfg<D>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* qbuf = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   unsigned char* kslots = qbuf + 2 * C::SLOT;
   unsigned char* vslots = kslots + C::KR * C::SLOT;
   PtShared& sh = *reinterpret_cast<PtShared*>(vslots + C::VR * C::SLOT);
-  pdl_begin();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int window = a.window > 0 ? a.window : 0x7fffffff;
-  if (blockIdx.x == 0 && warp == 0) pf_check_offsets(a);
-  const PtUnit u = pt_unit(a, places, pairs, by_heads, window);
-  if (u.len == 0) return;
 
   if (tid == 0) {
+    sh.feed.init(8 + 1 + 2);
     for (int i = 0; i < C::KR; ++i) tc::bar_init(&sh.k_full[i], 1), tc::bar_init(&sh.k_empty[i], 1);
     for (int i = 0; i < C::VR; ++i)
       tc::bar_init(&sh.v_full[i], 1), tc::bar_init(&sh.v_ready[i], 2), tc::bar_init(&sh.v_empty[i], 1);
     for (int i = 0; i < 2; ++i)
       tc::bar_init(&sh.s_full[i], 1), tc::bar_init(&sh.p_full[i], 4), tc::bar_init(&sh.o_full[i], 1);
-    tc::bar_init(&sh.q_full, 1), tc::bar_init(&sh.drain, 1);
+    tc::bar_init(&sh.q_full, 1), tc::bar_init(&sh.q_empty, 1), tc::bar_init(&sh.drain, 1);
     tc::bar_fence_init();
-    sh.dead = sh.odd_v = 0;
+    sh.dead = 0;
   }
+  if (tid == 9 * 32) tc::prefetch_map(&maps.q), tc::prefetch_map(&maps.k), tc::prefetch_map(&maps.v);
   if (warp == 8) tc::tmem_alloc(&sh.tmem, PT_TMEM);
+  pdl_begin();
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -122,131 +153,180 @@ __global__ void __launch_bounds__(PT_NT, 1)
     // 384 threads with 168 registers each were launched: 256 x 200 + 128 x 104 is as many
     asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     if (warp == 9) {
-      // ---- loads
-      if (lane == 0) {
-        bool ok = true;
-        int sent_k = 0, sent_v = 0;
-        const int blocks = u.rows[1] > 0 ? 2 : 1;
-        tc::bar_arrive_expect_tx(&sh.q_full, blocks * C::SLOT);
-        for (int s = 0; s < blocks; ++s)
-          pt_load<D>(qbuf + s * C::SLOT, &maps.q, u.head[s], u.t0 + u.row0[s], &sh.q_full);
-        TcRing<C::KR> kr;
-        TcRing<C::VR> vr;
-        for (int j = u.lo; j <= u.top; ++j) {
-          const int tok = u.t0 + j * PT_B;
-          ok = tc_wait(&sh.k_empty[kr.at], kr.parity ^ 1, &sh.dead);
+      // ---- units, and their loads
+      bool ok = true, more = true;
+      int sent_k = 0, sent_v = 0, units = 0, id = blockIdx.x;
+      TcRing<2> un;
+      TcRing<C::KR> kr;
+      TcRing<C::VR> vr;
+      while (more) {
+        const PtUnit u = pt_unit<BY_HEADS>(a, places, pairs, id, window);
+        if (u.len > 0) {
+          ok = tc_wait(&sh.feed.empty[un.at], un.parity ^ 1, &sh.dead);
+          ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          tc::bar_arrive_expect_tx(&sh.k_full[kr.at], C::SLOT);
-          pt_load<D>(kslots + kr.at * C::SLOT, &maps.k, u.kv_head, tok, &sh.k_full[kr.at]);
-          ++sent_k;
-          kr.step();
-          if (a.test_stall && j == u.lo + PT_STALL_AT) ok = tc_give_up(&sh.dead);
-          ok = ok && tc_wait(&sh.v_empty[vr.at], vr.parity ^ 1, &sh.dead);
+          if (lane == 0) {
+            sh.unit[un.at] = u, sh.odd_v[un.at] = 0;
+            tc::bar_arrive(&sh.feed.full[un.at]);
+            for (int j = u.lo; j <= u.top; ++j) {
+              const int tok = u.t0 + j * PT_B;
+              ok = tc_wait(&sh.k_empty[kr.at], kr.parity ^ 1, &sh.dead);
+              if (!ok) break;
+              tc::bar_arrive_expect_tx(&sh.k_full[kr.at], C::SLOT);
+              pt_load<D>(kslots + kr.at * C::SLOT, &maps.k, u.kv_head, tok, &sh.k_full[kr.at]);
+              ++sent_k;
+              kr.step();
+              if (j == u.lo) {
+                ok = tc_wait(&sh.q_empty, (units & 1) ^ 1, &sh.dead);
+                if (!ok) break;
+                const int blocks = u.rows[1] > 0 ? 2 : 1;
+                tc::bar_arrive_expect_tx(&sh.q_full, blocks * C::SLOT);
+                for (int s = 0; s < blocks; ++s) pt_load<D>(qbuf + s * C::SLOT, &maps.q, u.head[s], u.t0 + u.row0[s], &sh.q_full);
+                ++units;
+              }
+              if (j == u.top) sh.feed.ask();
+              if (a.test_stall && j == u.lo + PT_STALL_AT) ok = tc_give_up(&sh.dead);
+              ok = ok && tc_wait(&sh.v_empty[vr.at], vr.parity ^ 1, &sh.dead);
+              if (!ok) break;
+              tc::bar_arrive_expect_tx(&sh.v_full[vr.at], C::SLOT);
+              pt_load<D>(vslots + vr.at * C::SLOT, &maps.v, u.kv_head, tok, &sh.v_full[vr.at]);
+              ++sent_v;
+              vr.step();
+            }
+          }
+          ok = __shfl_sync(0xffffffffu, ok, 0);
           if (!ok) break;
-          tc::bar_arrive_expect_tx(&sh.v_full[vr.at], C::SLOT);
-          pt_load<D>(vslots + vr.at * C::SLOT, &maps.v, u.kv_head, tok, &sh.v_full[vr.at]);
-          ++sent_v;
-          vr.step();
+          un.step();
+        } else if (lane == 0) {
+          sh.feed.ask();
         }
-        if (!ok) {
-          // let what is on its way arrive before the CTA ends: the last round of every slot
-          flag_status(a.status, KDA_DEV_TIMEOUT);
-          tc::bar_wait(&sh.q_full, 0, 1u << 16);
-          for (int i = max(0, sent_k - C::KR); i < sent_k; ++i) tc::bar_wait(&sh.k_full[i % C::KR], i / C::KR & 1, 1u << 16);
-          for (int i = max(0, sent_v - C::VR); i < sent_v; ++i) tc::bar_wait(&sh.v_full[i % C::VR], i / C::VR & 1, 1u << 16);
+        ok = sh.feed.answered(&sh.dead, id);
+        if (!ok) break;
+        more = id >= 0;
+      }
+      if (ok) {
+        ok = tc_wait(&sh.feed.empty[un.at], un.parity ^ 1, &sh.dead);
+        ok = __all_sync(0xffffffffu, ok);
+        if (lane == 0 && ok) {
+          sh.unit[un.at].len = 0;
+          tc::bar_arrive(&sh.feed.full[un.at]);
         }
       }
+      if (!ok && lane == 0) {
+        // let what is on its way arrive before the CTA ends: the last round of every slot
+        flag_status(a.status, KDA_DEV_TIMEOUT);
+        sh.feed.drain();
+        if (units > 0) tc::bar_wait(&sh.q_full, (units - 1) & 1, 1u << 16);
+        for (int i = max(0, sent_k - C::KR); i < sent_k; ++i) tc::bar_wait(&sh.k_full[i % C::KR], i / C::KR & 1, 1u << 16);
+        for (int i = max(0, sent_v - C::VR); i < sent_v; ++i) tc::bar_wait(&sh.v_full[i % C::VR], i / C::VR & 1, 1u << 16);
+      }
     } else if (warp == 8) {
-      // ---- products
-      if (lane == 0) {
-        bool ok = tc_wait(&sh.q_full, 0, &sh.dead);
-        TcRing<C::KR> kr;
-        TcRing<C::VR> vr;
-        const uint64_t q0 = tc::sdesc(tc::smem_u32(qbuf)), k0 = tc::sdesc(tc::smem_u32(kslots));
-        const uint64_t v0 = tc::sdesc_mn(tc::smem_u32(vslots), PT_HALF);
-        constexpr uint32_t id_s = pt_idesc(PT_B), id_o = pt_idesc(D) | tc::IDESC_B_MN;
-        auto scores = [&](int s) {
-          const uint64_t qd = q0 + s * (C::SLOT / 16), kd = k0 + kr.at * (C::SLOT / 16);
+      // ---- products: the warp waits and counts as one, one lane issues
+      bool ok = true;
+      TcRing<2> un;
+      TcRing<C::KR> kr;
+      TcRing<C::VR> vr;
+      uint32_t p_parity[2] = {0, 0};
+      const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem);
+      const uint64_t q0 = tc::sdesc(tc::smem_u32(qbuf)), k0 = tc::sdesc(tc::smem_u32(kslots));
+      const uint64_t v0 = tc::sdesc_mn(tc::smem_u32(vslots), PT_HALF);
+      constexpr uint32_t id_s = pt_idesc(PT_B), id_o = pt_idesc(D) | tc::IDESC_B_MN;
+      auto scores = [&](int s) {
+        const uint64_t qd = q0 + s * (C::SLOT / 16), kd = k0 + kr.at * (C::SLOT / 16);
+        if (tc::elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {  // 16 channels per step
             const uint32_t at = (kk / 4 * PT_HALF + kk % 4 * 32) / 16;
-            tc::mma_ss(tmem + s * PT_B, qd + at, kd + at, id_s, kk > 0);
+            tc::mma_ss(tm + s * PT_B, qd + at, kd + at, id_s, kk > 0);
           }
           tc::commit(&sh.s_full[s]);
-        };
-        // the first tile's scores
-        ok = ok && tc_wait(&sh.k_full[0], 0, &sh.dead);
-        if (ok) {
-          tc::fence_after_sync();
-          for (int s = 0; s < 2; ++s)
-            if (u.lo <= u.hi[s]) scores(s);
-          tc::commit(&sh.k_empty[0]);
-          kr.step();
         }
-        for (int j = u.lo; ok && j <= u.top; ++j) {
-          const uint32_t parity = (j - u.lo) & 1;
-          ok = tc_wait(&sh.v_ready[vr.at], vr.parity, &sh.dead);
-          if (ok && j < u.top) ok = tc_wait(&sh.k_full[kr.at], kr.parity, &sh.dead);
+      };
+      for (uint32_t q_parity = 0;; q_parity ^= 1, un.step()) {
+        ok = tc_wait_warp(&sh.feed.full[un.at], un.parity, &sh.dead);
+        if (!ok) break;
+        // numbers that are known to be the same for all lanes
+        const int lo = __reduce_max_sync(0xffffffffu, sh.unit[un.at].lo), end = __reduce_max_sync(0xffffffffu, sh.unit[un.at].len);
+        const int hi0 = __reduce_max_sync(0xffffffffu, sh.unit[un.at].hi[0]), hi1 = __reduce_max_sync(0xffffffffu, sh.unit[un.at].hi[1]);
+        const int top = max(hi0, hi1);
+        if (lane == 0) tc::bar_arrive(&sh.feed.empty[un.at]);
+        __syncwarp();
+        if (end == 0) break;
+        // the first tile's scores
+        ok = tc_wait_warp(&sh.k_full[kr.at], kr.parity, &sh.dead) && tc_wait_warp(&sh.q_full, q_parity, &sh.dead);
+        if (!ok) break;
+        tc::fence_after_sync();
+        scores(0);
+        if (hi1 >= 0) scores(1);
+        if (tc::elect_one()) {
+          tc::commit(&sh.k_empty[kr.at]);
+          if (lo == top) tc::commit(&sh.q_empty);
+        }
+        kr.step();
+        for (int j = lo; j <= top; ++j) {
+          ok = tc_wait_warp(&sh.v_ready[vr.at], vr.parity, &sh.dead);
+          if (ok && j < top) ok = tc_wait_warp(&sh.k_full[kr.at], kr.parity, &sh.dead);
 #pragma unroll
           for (int s = 0; s < 2; ++s) {
-            if (!ok || j > u.hi[s]) continue;
-            ok = tc_wait(&sh.p_full[s], parity, &sh.dead);
+            const int hi = s ? hi1 : hi0;
+            if (!ok || j > hi) continue;
+            ok = tc_wait_warp(&sh.p_full[s], p_parity[s], &sh.dead);
             if (!ok) continue;
+            p_parity[s] ^= 1;
             tc::fence_after_sync();
             const uint64_t vd = v0 + vr.at * (C::SLOT / 16);
+            if (tc::elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < PT_B / 16; ++kk)  // 16 keys per step
-              tc::mma_ts(tmem + PT_O + s * 128, tmem + s * PT_B + kk * 8, vd + kk * (2048 / 16), id_o, !(j == u.lo && kk == 0));
-            if (j == u.hi[s]) tc::commit(&sh.o_full[s]);
-            if (s == 1 || j > u.hi[1]) tc::commit(&sh.v_empty[vr.at]);
+              for (int kk = 0; kk < PT_B / 16; ++kk)  // 16 keys per step
+                tc::mma_ts(tm + PT_O + s * 128, tm + s * PT_B + kk * 8, vd + kk * (2048 / 16), id_o, !(j == lo && kk == 0));
+              if (j == hi) tc::commit(&sh.o_full[s]);
+              if (s == 1 || j > hi1) tc::commit(&sh.v_empty[vr.at]);
+            }
             // the next scores go where these probabilities lie: products run in the order of their issue
-            if (j < u.hi[s]) scores(s);
+            if (j < hi) scores(s);
           }
           if (!ok) break;
-          if (j < u.top) {
-            tc::commit(&sh.k_empty[kr.at]);
+          if (j < top) {
+            if (tc::elect_one()) {
+              tc::commit(&sh.k_empty[kr.at]);
+              if (j + 1 == top) tc::commit(&sh.q_empty);
+            }
             kr.step();
           }
           vr.step();
         }
-        // nothing of this thread's is on its way when the CTA ends
-        if (!ok) flag_status(a.status, KDA_DEV_TIMEOUT);
-        tc::commit(&sh.drain);
-        tc::bar_wait(&sh.drain, 0);
+        if (!ok) break;
       }
+      // nothing of this warp's is on its way when the CTA ends
+      if (!ok && lane == 0) flag_status(a.status, KDA_DEV_TIMEOUT);
+      __syncwarp();
+      if (tc::elect_one()) tc::commit(&sh.drain);
+      tc::bar_wait(&sh.drain, 0);
     } else {
       // ---- V tiles with keys that some row does not see
+      TcRing<2> un;
       TcRing<C::VR> vr;
       bool ok = true;
-      for (int j = u.lo; j <= u.top; ++j, vr.step()) {
-        ok = tc_wait(&sh.v_full[vr.at], vr.parity, &sh.dead);
+      if (blockIdx.x == 0 && warp == 10) pf_check_offsets(a);
+      for (;; un.step()) {
+        ok = tc_wait(&sh.feed.full[un.at], un.parity, &sh.dead);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        if (pt_masked(u, j, window)) {
-          unsigned char* tile = vslots + vr.at * C::SLOT;
-          const int keys = u.len - j * PT_B;  // of the sequence
-          bool odd = false;
-          for (int i = tid - 320; i < PT_B * 8 * C::HALVES; i += 64) {
-            const int row = (i >> 3) & (PT_B - 1);  // 16 bytes of it: eight lie in 128 bytes, in some order
-            uint4* at = reinterpret_cast<uint4*>(tile) + i;
-            if (row >= keys) {
-              *at = make_uint4(0, 0, 0, 0);
-              continue;
-            }
-            const uint4 x = *at;
-            if (odd_bf16(x.x) || odd_bf16(x.y) || odd_bf16(x.z) || odd_bf16(x.w)) {
-              odd = true;
-              uint16_t* e = reinterpret_cast<uint16_t*>(at);
-              for (int n = 0; n < 8; ++n)
-                if ((e[n] & 0x7f80) == 0x7f80) e[n] = 0;
-            }
+        const PtUnit u = sh.unit[un.at];
+        if (u.len == 0) break;
+        for (int j = u.lo; j <= u.top; ++j, vr.step()) {
+          ok = tc_wait(&sh.v_full[vr.at], vr.parity, &sh.dead);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (pt_masked(u, j, window)) {
+            if (pt_clean<D>(vslots + vr.at * C::SLOT, u.len - j * PT_B, tid - 320)) *const_cast<volatile int*>(&sh.odd_v[un.at]) = 1;
+            __threadfence_block();
           }
-          if (odd) *const_cast<volatile int*>(&sh.odd_v) = 1;
-          __threadfence_block();
-          tc::fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) tc::bar_arrive(&sh.v_ready[vr.at]);
         }
-        __syncwarp();
-        if (lane == 0) tc::bar_arrive(&sh.v_ready[vr.at]);
+        if (!ok) break;
+        if (lane == 0) tc::bar_arrive(&sh.feed.empty[un.at]);
       }
       if (!ok && lane == 0) flag_status(a.status, KDA_DEV_TIMEOUT);
     }
@@ -254,130 +334,142 @@ __global__ void __launch_bounds__(PT_NT, 1)
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     // ---- softmax: thread = row
-    const int s = warp >> 2, row = u.row0[s] + (tid & 127);
+    const int s = warp >> 2;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16, own_s = tmem + s * PT_B + lanes, own_o = tmem + PT_O + s * 128 + lanes;
     const float cap2 = a.softcap * PA_LOG2E;
     // of a product, to powers of two (or the cap's argument); not 0, which would turn an unseen key's -infinity into a NaN
     float factor = a.scale * (CAP ? 2.f * PA_LOG2E / a.softcap : PA_LOG2E);
-    if (!CAP && fabsf(factor) < 1.2e-38f) factor = 1.2e-38f;
+    const bool negative = !CAP && factor < 0.f;
+    if (!CAP) factor = fmaxf(fabsf(factor), 1.2e-38f);
     bool ok = true;
-    float m = PF_NONE, l = 0.f;
-    for (int j = u.lo; j <= u.hi[s]; ++j) {
-      ok = ok && tc_wait(&sh.s_full[s], (j - u.lo) & 1, &sh.dead);
+    uint32_t s_parity = 0, o_parity = 0;
+    int rows_done = 0;
+    for (TcRing<2> un;; un.step()) {
+      ok = tc_wait(&sh.feed.full[un.at], un.parity, &sh.dead);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      tc::fence_after_sync();
-      float2 x[PT_B / 2];
+      const PtUnit u = sh.unit[un.at];
+      if (u.len == 0) break;
+      const int row0 = u.row0[s], row = row0 + (tid & 127), hi = u.hi[s];
+      float m = PF_NONE, l = 0.f;
+      for (int j = u.lo; j <= hi; ++j) {
+        ok = tc_wait(&sh.s_full[s], s_parity, &sh.dead);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        s_parity ^= 1;
+        tc::fence_after_sync();
+        float2 x[PT_B / 2];
+        tc::tmem_ld128(own_s, reinterpret_cast<float*>(x));
+        if constexpr (CAP) pt_cap(x, factor, cap2);
+        if (negative) {
 #pragma unroll
-      for (int c = 0; c < PT_B; c += 64) tc::tmem_ld64(own_s + c, reinterpret_cast<float*>(x) + c);
-      const int k0 = j * PT_B;
-      if constexpr (CAP) pt_cap(x, factor, cap2);
-      // of the tile the row sees keys from .. to - 1
-      if (k0 + PT_B - 1 > u.row0[s] || k0 <= u.row0[s] + PT_B - 1 - window) {
-        const int to = row + 1 - k0, from = row - k0 < window ? 0 : row - k0 - window + 1;
-        const float none = !CAP && factor < 0.f ? INFINITY : -INFINITY;
-#pragma unroll
-        for (int i = 0; i < PT_B / 2; ++i) {
-          if (2 * i >= to || 2 * i < from) x[i].x = none;
-          if (2 * i + 1 >= to || 2 * i + 1 < from) x[i].y = none;
+          for (int i = 0; i < PT_B / 2; ++i) x[i] = make_float2(-x[i].x, -x[i].y);
         }
-      }
-      // the largest score in powers of two
-      float top;
-      if (CAP || factor >= 0.f) {
-        float t0 = -INFINITY, t1 = -INFINITY;
+        // of the tile the row sees keys from .. to - 1
+        const int k0 = j * PT_B;
+        if (k0 + PT_B - 1 > row0 || k0 <= row0 + PT_B - 1 - window) {
+          const int to = row + 1 - k0, from = row - k0 < window ? 0 : row - k0 - window + 1;
 #pragma unroll
-        for (int i = 0; i < PT_B / 2; ++i) t0 = fmaxf(t0, x[i].x), t1 = fmaxf(t1, x[i].y);
-        top = fmaxf(t0, t1);
-      } else {
-        float t0 = INFINITY, t1 = INFINITY;
+          for (int i = 0; i < PT_B / 2; ++i) {
+            if (2 * i >= to || 2 * i < from) x[i].x = -INFINITY;
+            if (2 * i + 1 >= to || 2 * i + 1 < from) x[i].y = -INFINITY;
+          }
+        }
+        // the largest score in powers of two
+        float t[4];
 #pragma unroll
-        for (int i = 0; i < PT_B / 2; ++i) t0 = fminf(t0, x[i].x), t1 = fminf(t1, x[i].y);
-        top = fminf(t0, t1);
-      }
-      if constexpr (!CAP) top = top == -INFINITY || top == INFINITY ? (factor >= 0.f ? top : -top) : top * factor;
-      const bool move = top > m + PT_SLACK;
-      if (__any_sync(0xffffffffu, move)) {
-        const float mn = move ? top : m, by = ex2(m - mn);
-        m = mn;
-        l *= by;
-        if (j > u.lo) {
+        for (int i = 0; i < 4; ++i) t[i] = fmaxf(x[i].x, x[i].y);
+#pragma unroll
+        for (int i = 4; i < PT_B / 2; ++i) t[i & 3] = fmaxf(fmaxf(t[i & 3], x[i].x), x[i].y);
+        float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+        if constexpr (!CAP) top *= factor;
+        const bool move = top > m + PT_SLACK;
+        if (__any_sync(0xffffffffu, move)) {
+          const float mn = move ? top : m, by = ex2(m - mn);
+          m = mn;
+          l *= by;
+          if (j > u.lo) {
 #pragma unroll 1
-          for (int c = 0; c < D; c += 16) {
-            float o[16];
-            uint32_t w[16];
-            tc::tmem_ld16(own_o + c, o);
+            for (int c = 0; c < D; c += 16) {
+              float o[16];
+              uint32_t w[16];
+              tc::tmem_ld16(own_o + c, o);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[i] * by);
-            tc::tmem_st16(own_o + c, w);
+              for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[i] * by);
+              tc::tmem_st16(own_o + c, w);
+            }
           }
         }
-      }
-      float2 sum0 = make_float2(l, 0.f), sum1 = both(0.f);
+        float2 sum0 = make_float2(l, 0.f), sum1 = both(0.f);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t w[16];
+        for (int c = 0; c < 4; ++c) {
+          uint32_t w[16];
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-          float2 e0 = x[16 * c + i], e1 = x[16 * c + i + 1];
-          if constexpr (CAP) {
-            e0 = add2(e0, both(-m)), e1 = add2(e1, both(-m));
-          } else {
-            e0 = fma2(e0, both(factor), both(-m)), e1 = fma2(e1, both(factor), both(-m));
+          for (int i = 0; i < 16; i += 2) {
+            float2 e0 = x[16 * c + i], e1 = x[16 * c + i + 1];
+            if constexpr (CAP) {
+              e0 = add2(e0, both(-m)), e1 = add2(e1, both(-m));
+            } else {
+              e0 = fma2(e0, both(factor), both(-m)), e1 = fma2(e1, both(factor), both(-m));
+            }
+            e0 = make_float2(ex2(e0.x), ex2(e0.y)), e1 = make_float2(ex2(e1.x), ex2(e1.y));
+            sum0 = add2(sum0, e0), sum1 = add2(sum1, e1);
+            w[i] = pack_bf16(e0.x, e0.y), w[i + 1] = pack_bf16(e1.x, e1.y);
           }
-          e0 = make_float2(ex2(e0.x), ex2(e0.y)), e1 = make_float2(ex2(e1.x), ex2(e1.y));
-          sum0 = add2(sum0, e0), sum1 = add2(sum1, e1);
-          w[i] = pack_bf16(e0.x, e0.y), w[i + 1] = pack_bf16(e1.x, e1.y);
+          tc::tmem_st16(own_s + 16 * c, w);
         }
-        tc::tmem_st16(own_s + 16 * c, w);
+        sum0 = add2(sum0, sum1);
+        l = sum0.x + sum0.y;
+        tc::tmem_wait_st();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::bar_arrive(&sh.p_full[s]);
       }
-      sum0 = add2(sum0, sum1);
-      l = sum0.x + sum0.y;
-      tc::tmem_wait_st();
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) tc::bar_arrive(&sh.p_full[s]);
-    }
+      if (!ok) break;
 
-    // ---- the rows' results
-    if (u.rows[s] > 0) {
-      ok = ok && tc_wait(&sh.o_full[s], 0, &sh.dead);
-      ok = __all_sync(0xffffffffu, ok);
-      tc::fence_after_sync();
-      if (ok) {
-        const bool mine = row - u.row0[s] < u.rows[s], odd = *const_cast<volatile int*>(&sh.odd_v) != 0;
+      // ---- the rows' results
+      if (u.rows[s] > 0) {
+        ok = tc_wait(&sh.o_full[s], o_parity, &sh.dead);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        o_parity ^= 1;
+        tc::fence_after_sync();
+        const bool mine = row - row0 < u.rows[s], odd = *const_cast<volatile int*>(&sh.odd_v[un.at]) != 0;
         const int64_t t = u.t0 + row;
         const float by = 1.f / l;
-        const bf16* v = static_cast<const bf16*>(a.v) + u.kv_head * a.d;
+        const bf16* v = static_cast<const bf16*>(a.v) + (int64_t)u.kv_head * a.d;
         // values that are no numbers were left out of the tiles with unseen keys
-        auto add_odd = [&](int c, float (&o)[16]) {
-          for (int j = u.lo; j <= u.hi[s]; ++j) {
+        auto add_odd = [&](int c, float (&o)[32]) {
+          for (int j = u.lo; j <= hi; ++j) {
             if (!pt_masked(u, j, window)) continue;
             for (int k = max(j * PT_B, row >= window ? row - window + 1 : 0); k <= min(j * PT_B + PT_B - 1, row); ++k)
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
+              for (int i = 0; i < 32; ++i) {
                 const float x = c + i < a.d ? to_f32(v[(int64_t)(u.t0 + k) * a.v_stride + c + i]) : 0.f;
                 if (!(fabsf(x) <= 3.4e38f)) o[i] += x;
               }
           }
         };
 #pragma unroll 1
-        for (int c = 0; c < D; c += 16) {
-          float o[16];
-          tc::tmem_ld16(own_o + c, o);
+        for (int c = 0; c < D; c += 32) {
+          float o[32];
+          tc::tmem_ld32(own_o + c, o);
           if (mine && c < a.d) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] *= by;
+            for (int i = 0; i < 32; ++i) o[i] *= by;
             if (odd) add_odd(c, o);
-            pt_store16(a.out, a.out_bf16, t * a.out_stride + (int64_t)u.head[s] * a.d + c, o);
+            pt_store32(a.out, a.out_bf16, t * a.out_stride + (int64_t)u.head[s] * a.d + c, o, a.d - c);
           }
           __syncwarp();  // the next load is the whole warp's
         }
         if (mine && a.lse) a.lse[t * a.Hq + u.head[s]] = (m + log2f(l)) * PA_LN2;
+        rows_done += u.rows[s];
       }
+      __syncwarp();
+      if (lane == 0) tc::bar_arrive(&sh.feed.empty[un.at]);
     }
     if (!ok && lane == 0) flag_status(a.status, KDA_DEV_TIMEOUT);
-    if ((tid & 127) == 0 && ok) add_work(a.status, u.rows[s]);
+    if ((tid & 127) == 0) add_work(a.status, rows_done);
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -385,9 +477,9 @@ __global__ void __launch_bounds__(PT_NT, 1)
   if (warp == 8) tc::tmem_dealloc(tmem, PT_TMEM);
 }
 
-template <int D, bool CAP>
+template <int D, bool CAP, bool BY_HEADS>
 cudaError_t tc_launch(const PromptAttnArgs& a, cudaStream_t s) {
-  auto kernel = prefill_attention_tc_kernel<D, CAP>;
+  auto kernel = prefill_attention_tc_kernel<D, CAP, BY_HEADS>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, pt_smem<D>());
   if (e != cudaSuccess) return e;
   PtMaps maps;
@@ -395,19 +487,20 @@ cudaError_t tc_launch(const PromptAttnArgs& a, cudaStream_t s) {
       !encode_rows_map_sw128(&maps.k, a.k, a.T, a.Hkv, a.d, a.k_stride, PT_B) ||
       !encode_rows_map_sw128(&maps.v, a.v, a.T, a.Hkv, a.d, a.v_stride, PT_B))
     return cudaErrorInvalidValue;
-  const bool by_heads = a.Hq / a.Hkv % 2 == 0;
-  const int pairs = by_heads ? a.Hq / 2 : a.Hq;
-  const int64_t places = pf_places(a.T, a.N, by_heads ? PT_B : 2 * PT_B);
+  const int pairs = BY_HEADS ? a.Hq / 2 : a.Hq;
+  const int64_t places = pf_places(a.T, a.N, BY_HEADS ? PT_B : 2 * PT_B);
   if (places * pairs > 0x7fffffff) return cudaErrorInvalidValue;
-  return launch_pdl(kernel, dim3((unsigned)(places * pairs)), dim3(PT_NT), pt_smem<D>(), s, maps, a, places, pairs, by_heads);
+  return launch_pdl(kernel, dim3((unsigned)(places * pairs)), dim3(PT_NT), pt_smem<D>(), s, maps, a, places, pairs);
+}
+
+template <int D>
+cudaError_t tc_launch(const PromptAttnArgs& a, cudaStream_t s) {
+  if (a.Hq / a.Hkv % 2 == 0) return a.softcap > 0.f ? tc_launch<D, true, true>(a, s) : tc_launch<D, false, true>(a, s);
+  return a.softcap > 0.f ? tc_launch<D, true, false>(a, s) : tc_launch<D, false, false>(a, s);
 }
 
 }  // namespace
 
-cudaError_t pf_tc(const PromptAttnArgs& a, cudaStream_t s) {
-  const bool cap = a.softcap > 0.f;
-  if (a.d == 128) return cap ? tc_launch<128, true>(a, s) : tc_launch<128, false>(a, s);
-  return cap ? tc_launch<64, true>(a, s) : tc_launch<64, false>(a, s);
-}
+cudaError_t pf_tc(const PromptAttnArgs& a, cudaStream_t s) { return a.d == 128 ? tc_launch<128>(a, s) : tc_launch<64>(a, s); }
 
 }  // namespace kda

@@ -26,6 +26,40 @@ __device__ __forceinline__ void pt_load(unsigned char* slot, const CUtensorMap* 
   for (int c = 0; c < D / 64; ++c) tc::tma_load_3d(slot + c * PT_HALF, map, c * 64, head, tok, bar);
 }
 
+// Units on their way to the roles of a CTA, two places, and the taking over of a CTA that has not started.
+struct PtFeed {
+  alignas(16) uint4 answer;
+  uint64_t full[2], empty[2], taken;
+  int asked, heard;
+  __device__ __forceinline__ void init(int readers) {
+    for (int i = 0; i < 2; ++i) tc::bar_init(&full[i], 1), tc::bar_init(&empty[i], readers);
+    tc::bar_init(&taken, 1);
+    asked = heard = 0;
+  }
+  // One thread asks, once before each answer; the whole warp hears it.
+  __device__ __forceinline__ void ask() {
+    tc::fence_proxy_async();  // the answer before has been read
+    tc::take_cta(&answer, &taken);
+    ++asked;
+  }
+  __device__ __forceinline__ bool answered(int* dead, int& id) {
+    __syncwarp();
+    const int n = heard;
+    bool ok = tc_wait(&taken, n & 1, dead);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) return false;
+    id = tc::taken_cta(&answer);
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) heard = n + 1;
+    __syncwarp();
+    return true;
+  }
+  // On the way out: an answer that has not been heard arrives.
+  __device__ __forceinline__ void drain() {
+    if (asked > heard) tc::bar_wait(&taken, heard & 1, 1u << 16);
+  }
+};
+
 // 16 results of a row, from channel c on.
 __device__ __forceinline__ void pt_store16(void* base, bool is_bf16, int64_t at, const float (&o)[16]) {
   if (is_bf16) {
@@ -37,6 +71,12 @@ __device__ __forceinline__ void pt_store16(void* base, bool is_bf16, int64_t at,
 #pragma unroll
     for (int i = 0; i < 4; ++i) y[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
   }
+}
+
+// The same with 32, of which there are `left` (a multiple of 16).
+__device__ __forceinline__ void pt_store32(void* base, bool is_bf16, int64_t at, const float (&o)[32], int left) {
+  pt_store16(base, is_bf16, at, reinterpret_cast<const float(&)[16]>(o[0]));
+  if (left > 16) pt_store16(base, is_bf16, at + 16, reinterpret_cast<const float(&)[16]>(o[16]));
 }
 
 // Scores in powers of two, capped; `factor` takes a product to the cap's argument.

@@ -30,6 +30,11 @@ __device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, int* dea
   return false;
 }
 
+// The same by a whole warp, which goes on or leaves as one.
+__device__ __forceinline__ bool tc_wait_warp(uint64_t* bar, uint32_t parity, int* dead) {
+  return __all_sync(0xffffffffu, tc_wait(bar, parity, dead));
+}
+
 __device__ __forceinline__ bool tc_give_up(int* dead) {
   *reinterpret_cast<volatile int*>(dead) = 1;
   return false;
