@@ -50,6 +50,78 @@ __device__ __forceinline__ PfBlock pf_block(const PromptAttnArgs& a, int64_t pla
   return b;
 }
 
+// The blocks of a batch in the order of how far they lie from their sequence's start: all sequences' last blocks of the longest
+// length first.  Where the batch has up to 32 PF_RANKED sequences a warp keeps their lengths and finds block `rank` of that order by
+// counting: level L has count(L) = sum_i max(0, blocks_i - L) blocks at L or above.  (Blocks of unlike work in the batch's own
+// order end with whatever sequence came first: 16 prompts of 250 to 8000 tokens took 375 us.)
+constexpr int PF_RANKED = 8;
+template <int SHIFT>
+struct PfRanks {
+  int t0[PF_RANKED], len[PF_RANKED];
+  __device__ __forceinline__ static bool serves(int N) { return N <= 32 * PF_RANKED; }
+  __device__ __forceinline__ explicit PfRanks(const PromptAttnArgs& a) {
+#pragma unroll
+    for (int r = 0; r < PF_RANKED; ++r) {
+      const int i = 32 * r + (int)(threadIdx.x & 31);
+      t0[r] = len[r] = 0;
+      if (32 * r < a.N && i < a.N) {
+        const int c0 = __ldg(a.cu + i), c1 = __ldg(a.cu + i + 1);
+        if (!(c0 < 0 || c1 < c0 || c1 > a.T || c1 - c0 > a.max_seqlen)) t0[r] = c0, len[r] = c1 - c0;
+      }
+    }
+  }
+  __device__ __forceinline__ int blocks(int r) const { return (int)(((unsigned)len[r] + (1u << SHIFT) - 1) >> SHIFT); }
+  __device__ __forceinline__ int64_t count(int level, int N) const {  // below 2^31 / 128 + N
+    int n = 0;
+#pragma unroll
+    for (int r = 0; r < PF_RANKED; ++r)
+      if (32 * r < N) n += max(0, blocks(r) - level);
+    return __reduce_add_sync(0xffffffffu, n);
+  }
+  // level: the block's distance from the sequence's start (its number) in `from_start` order; the caller may count from the end.
+  __device__ __forceinline__ PfBlock find(int64_t rank, int N, int& level) const {
+    PfBlock b{0, 0, 0};
+    int lo = 0, hi = 1;
+#pragma unroll
+    for (int r = 0; r < PF_RANKED; ++r) hi = max(hi, blocks(r));
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    if (count(0, N) <= rank) return b;
+    while (hi - lo > 1) {  // count(lo) > rank >= count(hi)
+      const int mid = (lo + hi) >> 1;
+      if (count(mid, N) > rank) lo = mid;
+      else hi = mid;
+    }
+    int k = (int)(rank - count(lo + 1, N));
+    level = lo;
+    bool found = false;
+#pragma unroll
+    for (int r = 0; r < PF_RANKED; ++r) {
+      if (32 * r >= N || found) continue;
+      const unsigned mask = __ballot_sync(0xffffffffu, blocks(r) > lo);
+      const int n = __popc(mask);
+      if (k < n) {
+        const unsigned lane = threadIdx.x & 31, below = mask & ((1u << lane) - 1);
+        const unsigned it = __ballot_sync(0xffffffffu, (mask >> lane & 1) && __popc(below) == k);
+        const int from = __ffs(it) - 1;
+        b.t0 = __shfl_sync(0xffffffffu, t0[r], from);
+        b.len = __shfl_sync(0xffffffffu, len[r], from);
+        found = true;
+      }
+      k -= n;
+    }
+    return b;
+  }
+};
+// Block number `rank`, the longest rows first (the farthest from their sequence's start), or, `reversed`, the farthest from its end.
+template <int SHIFT>
+__device__ __forceinline__ PfBlock pf_ranked(const PromptAttnArgs& a, const PfRanks<SHIFT>& ranks, int64_t rank, int64_t places, bool reversed) {
+  if (!PfRanks<SHIFT>::serves(a.N)) return pf_block<SHIFT>(a, reversed ? rank : places - 1 - rank);
+  int level = 0;
+  PfBlock b = ranks.find(rank, a.N, level);
+  if (b.len > 0) b.row0 = (reversed ? (int)(((unsigned)b.len + (1u << SHIFT) - 1) >> SHIFT) - 1 - level : level) << SHIFT;
+  return b;
+}
+
 // Reports offsets that are out of order or out of range, and sequences beyond max_seqlen; one warp asks.
 __device__ __forceinline__ void pf_check_offsets(const PromptAttnArgs& a) {
   bool bad = false;

@@ -62,10 +62,10 @@ constexpr int pt_smem() {
 static_assert(pt_smem<128>() <= 227 * 1024, "shared memory of one SM");
 
 template <bool BY_HEADS>
-__device__ __forceinline__ PtUnit pt_unit(const PromptAttnArgs& a, int64_t places, int pairs, int id, int window) {
-  const int64_t place = places - 1 - id / pairs;  // the longest rows first
+__device__ __forceinline__ PtUnit pt_unit(const PromptAttnArgs& a, const PfRanks<BY_HEADS ? 7 : 8>& ranks, int64_t places, int pairs, int id,
+                                          int window) {
   const int pair = id % pairs;
-  const PfBlock b = pf_block<BY_HEADS ? 7 : 8>(a, place);
+  const PfBlock b = pf_ranked(a, ranks, id / pairs, places, false);
   PtUnit u;
   u.t0 = b.t0, u.len = b.len;
   u.top = -1;
@@ -154,13 +154,14 @@ __global__ void __launch_bounds__(PT_NT, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     if (warp == 9) {
       // ---- units, and their loads
+      const PfRanks<BY_HEADS ? 7 : 8> ranks(a);
       bool ok = true, more = true;
       int sent_k = 0, sent_v = 0, units = 0, id = blockIdx.x;
       TcRing<2> un;
       TcRing<C::KR> kr;
       TcRing<C::VR> vr;
       while (more) {
-        const PtUnit u = pt_unit<BY_HEADS>(a, places, pairs, id, window);
+        const PtUnit u = pt_unit<BY_HEADS>(a, ranks, places, pairs, id, window);
         if (u.len > 0) {
           ok = tc_wait(&sh.feed.empty[un.at], un.parity ^ 1, &sh.dead);
           ok = __all_sync(0xffffffffu, ok);
@@ -339,8 +340,10 @@ __global__ void __launch_bounds__(PT_NT, 1)
     const float cap2 = a.softcap * PA_LOG2E;
     // of a product, to powers of two (or the cap's argument); not 0, which would turn an unseen key's -infinity into a NaN
     float factor = a.scale * (CAP ? 2.f * PA_LOG2E / a.softcap : PA_LOG2E);
-    const bool negative = !CAP && factor < 0.f;
-    if (!CAP) factor = fmaxf(fabsf(factor), 1.2e-38f);
+    const bool negative = factor < 0.f;
+    factor = fmaxf(fabsf(factor), 1.2e-38f);
+    const float per = factor * (0.5f * PA_LN2);  // with a cap: of a product, to tanh's argument
+    const CapNearer nearer(cap2, per);
     bool ok = true;
     uint32_t s_parity = 0, o_parity = 0;
     int rows_done = 0;
@@ -360,14 +363,25 @@ __global__ void __launch_bounds__(PT_NT, 1)
         tc::fence_after_sync();
         float2 x[PT_B / 2];
         tc::tmem_ld128(own_s, reinterpret_cast<float*>(x));
-        if constexpr (CAP) pt_cap(x, factor, cap2);
         if (negative) {
 #pragma unroll
           for (int i = 0; i < PT_B / 2; ++i) x[i] = make_float2(-x[i].x, -x[i].y);
         }
-        // of the tile the row sees keys from .. to - 1
         const int k0 = j * PT_B;
-        if (k0 + PT_B - 1 > row0 || k0 <= row0 + PT_B - 1 - window) {
+        const bool masked = k0 + PT_B - 1 > row0 || k0 <= row0 + PT_B - 1 - window;
+        bool as_products = !CAP;  // x are products still, to be capped by the short polynomial
+        if constexpr (CAP) {
+          float t[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) t[i] = fmaxf(fabsf(x[i].x), fabsf(x[i].y));
+#pragma unroll
+          for (int i = 4; i < PT_B / 2; ++i) t[i & 3] = fmaxf(fmaxf(t[i & 3], fabsf(x[i].x)), fabsf(x[i].y));
+          const float far = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+          as_products = __all_sync(0xffffffffu, far * per <= PA_NEARER) && !masked;
+          if (!as_products) pt_cap(x, factor, cap2);
+        }
+        // of the tile the row sees keys from .. to - 1
+        if (masked) {
           const int to = row + 1 - k0, from = row - k0 < window ? 0 : row - k0 - window + 1;
 #pragma unroll
           for (int i = 0; i < PT_B / 2; ++i) {
@@ -382,7 +396,7 @@ __global__ void __launch_bounds__(PT_NT, 1)
 #pragma unroll
         for (int i = 4; i < PT_B / 2; ++i) t[i & 3] = fmaxf(fmaxf(t[i & 3], x[i].x), x[i].y);
         float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
-        if constexpr (!CAP) top *= factor;
+        if (as_products) top *= CAP ? nearer(top) : factor;
         const bool move = top > m + PT_SLACK;
         if (__any_sync(0xffffffffu, move)) {
           const float mn = move ? top : m, by = ex2(m - mn);
@@ -401,23 +415,23 @@ __global__ void __launch_bounds__(PT_NT, 1)
           }
         }
         float2 sum0 = make_float2(l, 0.f), sum1 = both(0.f);
+        auto probabilities = [&](auto argument) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t w[16];
+          for (int c = 0; c < 4; ++c) {
+            uint32_t w[16];
 #pragma unroll
-          for (int i = 0; i < 16; i += 2) {
-            float2 e0 = x[16 * c + i], e1 = x[16 * c + i + 1];
-            if constexpr (CAP) {
-              e0 = add2(e0, both(-m)), e1 = add2(e1, both(-m));
-            } else {
-              e0 = fma2(e0, both(factor), both(-m)), e1 = fma2(e1, both(factor), both(-m));
+            for (int i = 0; i < 16; i += 2) {
+              float2 e0 = argument(x[16 * c + i]), e1 = argument(x[16 * c + i + 1]);
+              e0 = make_float2(ex2(e0.x), ex2(e0.y)), e1 = make_float2(ex2(e1.x), ex2(e1.y));
+              sum0 = add2(sum0, e0), sum1 = add2(sum1, e1);
+              w[i] = pack_bf16(e0.x, e0.y), w[i + 1] = pack_bf16(e1.x, e1.y);
             }
-            e0 = make_float2(ex2(e0.x), ex2(e0.y)), e1 = make_float2(ex2(e1.x), ex2(e1.y));
-            sum0 = add2(sum0, e0), sum1 = add2(sum1, e1);
-            w[i] = pack_bf16(e0.x, e0.y), w[i + 1] = pack_bf16(e1.x, e1.y);
+            tc::tmem_st16(own_s + 16 * c, w);
           }
-          tc::tmem_st16(own_s + 16 * c, w);
-        }
+        };
+        if (!CAP) probabilities([&](float2 s) { return fma2(s, both(factor), both(-m)); });
+        else if (as_products) probabilities([&](float2 s) { return fma2(s, nearer(s), both(-m)); });
+        else probabilities([&](float2 s) { return add2(s, both(-m)); });
         sum0 = add2(sum0, sum1);
         l = sum0.x + sum0.y;
         tc::tmem_wait_st();
