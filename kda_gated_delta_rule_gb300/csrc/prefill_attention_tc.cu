@@ -118,6 +118,46 @@ __device__ __forceinline__ bool pt_clean(unsigned char* tile, int keys, int t) {
   return odd;
 }
 
+// A tile's capped scores: the row's largest.  Half by half they are left in tensor memory as products where all rows of the warp see
+// all keys and the short polynomial serves, else written there as scores in powers of two, -infinity for unseen keys.
+__device__ __forceinline__ float pt_capped_top(uint32_t own_s, bool masked, int from, int to, float factor, float cap2,
+                                               const CapNearer& nearer, int& products) {
+  float top = -INFINITY;
+#pragma unroll 1
+  for (int half = 0; half < 2; ++half) {
+    float x[64], far[4], most[4];
+    tc::tmem_ld64(own_s + 64 * half, x);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) far[i] = fabsf(x[i]), most[i] = x[i];
+#pragma unroll
+    for (int i = 4; i < 64; ++i) far[i & 3] = fmaxf(far[i & 3], fabsf(x[i])), most[i & 3] = fmaxf(most[i & 3], x[i]);
+    const float all = fmaxf(fmaxf(far[0], far[1]), fmaxf(far[2], far[3]));
+    if (!masked && factor > 0.f && __all_sync(0xffffffffu, all * factor <= 2.f * PA_LOG2E * PA_NEARER)) {
+      const float s = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
+      top = fmaxf(top, s * nearer(s));
+      products |= 1 << half;
+      continue;
+    }
+#pragma unroll 1
+    for (int c = 64 * half; c < 64 * half + 64; c += 16) {
+      float2 y[8];
+      uint32_t w[16];
+      tc::tmem_ld16(own_s + c, reinterpret_cast<float*>(y));
+      pt_cap(y, factor, cap2);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (masked && (c + 2 * i >= to || c + 2 * i < from)) y[i].x = -INFINITY;
+        if (masked && (c + 2 * i + 1 >= to || c + 2 * i + 1 < from)) y[i].y = -INFINITY;
+        top = fmaxf(top, fmaxf(y[i].x, y[i].y));
+        w[2 * i] = __float_as_uint(y[i].x), w[2 * i + 1] = __float_as_uint(y[i].y);
+      }
+      tc::tmem_st16(own_s + c, w);
+    }
+    tc::tmem_wait_st();  // read back below
+  }
+  return top;
+}
+
 template <int D, bool CAP, bool BY_HEADS>
 __global__ void __launch_bounds__(PT_NT, 1)
     prefill_attention_tc_kernel(const __grid_constant__ PtMaps maps, const PromptAttnArgs a, const int64_t places, const int pairs) {
@@ -340,10 +380,9 @@ __global__ void __launch_bounds__(PT_NT, 1)
     const float cap2 = a.softcap * PA_LOG2E;
     // of a product, to powers of two (or the cap's argument); not 0, which would turn an unseen key's -infinity into a NaN
     float factor = a.scale * (CAP ? 2.f * PA_LOG2E / a.softcap : PA_LOG2E);
-    const bool negative = factor < 0.f;
-    factor = fmaxf(fabsf(factor), 1.2e-38f);
-    const float per = factor * (0.5f * PA_LN2);  // with a cap: of a product, to tanh's argument
-    const CapNearer nearer(cap2, per);
+    const bool negative = !CAP && factor < 0.f;
+    if (!CAP) factor = fmaxf(fabsf(factor), 1.2e-38f);
+    const CapNearer nearer(cap2, factor * (0.5f * PA_LN2));
     bool ok = true;
     uint32_t s_parity = 0, o_parity = 0;
     int rows_done = 0;
@@ -361,42 +400,36 @@ __global__ void __launch_bounds__(PT_NT, 1)
         if (!ok) break;
         s_parity ^= 1;
         tc::fence_after_sync();
-        float2 x[PT_B / 2];
-        tc::tmem_ld128(own_s, reinterpret_cast<float*>(x));
-        if (negative) {
-#pragma unroll
-          for (int i = 0; i < PT_B / 2; ++i) x[i] = make_float2(-x[i].x, -x[i].y);
-        }
+        // of the tile the row sees keys from .. to - 1
         const int k0 = j * PT_B;
         const bool masked = k0 + PT_B - 1 > row0 || k0 <= row0 + PT_B - 1 - window;
-        bool as_products = !CAP;  // x are products still, to be capped by the short polynomial
+        const int to = row + 1 - k0, from = row - k0 < window ? 0 : row - k0 - window + 1;
+        // the largest score in powers of two
+        float top;
+        float2 x[CAP ? 1 : PT_B / 2];
+        int products = 0;  // halves of the keys whose scores are left as products, for the short polynomial
         if constexpr (CAP) {
+          top = pt_capped_top(own_s, masked, from, to, factor, cap2, nearer, products);
+        } else {
+          tc::tmem_ld128(own_s, reinterpret_cast<float*>(x));
+          if (negative) {
+#pragma unroll
+            for (int i = 0; i < PT_B / 2; ++i) x[i] = make_float2(-x[i].x, -x[i].y);
+          }
+          if (masked) {
+#pragma unroll
+            for (int i = 0; i < PT_B / 2; ++i) {
+              if (2 * i >= to || 2 * i < from) x[i].x = -INFINITY;
+              if (2 * i + 1 >= to || 2 * i + 1 < from) x[i].y = -INFINITY;
+            }
+          }
           float t[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) t[i] = fmaxf(fabsf(x[i].x), fabsf(x[i].y));
+          for (int i = 0; i < 4; ++i) t[i] = fmaxf(x[i].x, x[i].y);
 #pragma unroll
-          for (int i = 4; i < PT_B / 2; ++i) t[i & 3] = fmaxf(fmaxf(t[i & 3], fabsf(x[i].x)), fabsf(x[i].y));
-          const float far = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
-          as_products = __all_sync(0xffffffffu, far * per <= PA_NEARER) && !masked;
-          if (!as_products) pt_cap(x, factor, cap2);
+          for (int i = 4; i < PT_B / 2; ++i) t[i & 3] = fmaxf(fmaxf(t[i & 3], x[i].x), x[i].y);
+          top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * factor;
         }
-        // of the tile the row sees keys from .. to - 1
-        if (masked) {
-          const int to = row + 1 - k0, from = row - k0 < window ? 0 : row - k0 - window + 1;
-#pragma unroll
-          for (int i = 0; i < PT_B / 2; ++i) {
-            if (2 * i >= to || 2 * i < from) x[i].x = -INFINITY;
-            if (2 * i + 1 >= to || 2 * i + 1 < from) x[i].y = -INFINITY;
-          }
-        }
-        // the largest score in powers of two
-        float t[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) t[i] = fmaxf(x[i].x, x[i].y);
-#pragma unroll
-        for (int i = 4; i < PT_B / 2; ++i) t[i & 3] = fmaxf(fmaxf(t[i & 3], x[i].x), x[i].y);
-        float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
-        if (as_products) top *= CAP ? nearer(top) : factor;
         const bool move = top > m + PT_SLACK;
         if (__any_sync(0xffffffffu, move)) {
           const float mn = move ? top : m, by = ex2(m - mn);
@@ -415,23 +448,36 @@ __global__ void __launch_bounds__(PT_NT, 1)
           }
         }
         float2 sum0 = make_float2(l, 0.f), sum1 = both(0.f);
-        auto probabilities = [&](auto argument) {
+        // 32 probabilities, to the columns of the scores that `at` counts in keys
+        auto probabilities = [&](int at, const float2* x, auto argument) {
+          uint32_t w[16];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t w[16];
-#pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-              float2 e0 = argument(x[16 * c + i]), e1 = argument(x[16 * c + i + 1]);
-              e0 = make_float2(ex2(e0.x), ex2(e0.y)), e1 = make_float2(ex2(e1.x), ex2(e1.y));
-              sum0 = add2(sum0, e0), sum1 = add2(sum1, e1);
-              w[i] = pack_bf16(e0.x, e0.y), w[i + 1] = pack_bf16(e1.x, e1.y);
-            }
-            tc::tmem_st16(own_s + 16 * c, w);
+          for (int i = 0; i < 16; i += 2) {
+            float2 e0 = argument(x[i]), e1 = argument(x[i + 1]);
+            e0 = make_float2(ex2(e0.x), ex2(e0.y)), e1 = make_float2(ex2(e1.x), ex2(e1.y));
+            sum0 = add2(sum0, e0), sum1 = add2(sum1, e1);
+            w[i] = pack_bf16(e0.x, e0.y), w[i + 1] = pack_bf16(e1.x, e1.y);
           }
+          tc::tmem_st16(own_s + at / 2, w);
         };
-        if (!CAP) probabilities([&](float2 s) { return fma2(s, both(factor), both(-m)); });
-        else if (as_products) probabilities([&](float2 s) { return fma2(s, nearer(s), both(-m)); });
-        else probabilities([&](float2 s) { return add2(s, both(-m)); });
+        if constexpr (CAP) {
+          // by halves, over scores that have been read (a shorter body than the whole row's: instructions are fetched for each tile)
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+            float2 y[32];
+            tc::tmem_ld64(own_s + 64 * half, reinterpret_cast<float*>(y));
+            if (products >> half & 1) {
+#pragma unroll
+              for (int c = 0; c < 2; ++c) probabilities(64 * half + 32 * c, y + 16 * c, [&](float2 s) { return fma2(s, nearer(s), both(-m)); });
+            } else {
+#pragma unroll
+              for (int c = 0; c < 2; ++c) probabilities(64 * half + 32 * c, y + 16 * c, [&](float2 s) { return add2(s, both(-m)); });
+            }
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) probabilities(32 * c, x + 16 * c, [&](float2 s) { return fma2(s, both(factor), both(-m)); });
+        }
         sum0 = add2(sum0, sum1);
         l = sum0.x + sum0.y;
         tc::tmem_wait_st();
