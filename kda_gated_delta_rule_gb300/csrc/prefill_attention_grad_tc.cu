@@ -12,8 +12,9 @@
 //            dO V^T (dX in its place), so that the next tile's products run under a tile's arithmetic.
 // Where keys' blocks are too few for the SMs (one key/value head for all queries), the group's heads are dealt to several CTAs, whose
 // fp32 parts a third kernel adds up in order.
-// A CTA has 12 warps: 0 to 7 the arithmetic, thread = row and half of the tile's columns; 8 the products; 9 the loads (TMA);
-// 10 and 11 clear what lies behind the sequence in tiles that are column operands (0 * NaN), and bring the queries' statistics.
+// As in the forward, one CTA per SM walks units and takes over those that have not started, the most work first.  Its warps: the
+// arithmetic's, thread = row and one of PG_GROUPS parts of the tile's columns; one for the products; one for units and loads (TMA);
+// and two that clear what lies behind the sequence in tiles that are column operands (0 * NaN), and bring the queries' statistics.
 // p and dx are rounded to bf16 (2^-8) for their products; everything else is fp32.
 #include "device.h"
 #include "prefill_attention_tc.cuh"
@@ -23,6 +24,9 @@ namespace kda {
 namespace {
 
 constexpr int PG_MOST_PARTS = 16;
+constexpr int PG_GROUPS = 4;               // (2 with twice the columns: backward of 8192 tokens, 12 heads of 128, 566 us against 548)
+constexpr int PG_COLS = PT_B / PG_GROUPS;  // columns of a thread
+constexpr int PG_SOFT = 128 * PG_GROUPS, PG_NT = PG_SOFT + 128, PG_W = PG_SOFT / 32;
 
 template <int D>
 struct PgCfg {
@@ -35,17 +39,30 @@ struct PgMaps {
   CUtensorMap q, k, v, d_out;
 };
 
+// A block of keys with query heads h0 .. h1 - 1: a round is a block of one head's queries, `blocks` of them from number `tile` on.
+struct PgKeysUnit {
+  int t0, len, k0, tile, blocks, kh, part, h0, h1;  // len = 0: no more units
+};
+// A block of a head's queries: n tiles of keys from number lo on.
+struct PgQueriesUnit {
+  int t0, len, row0, h, lo, n;
+};
+
 struct PgKeysShared {
   // every barrier is waited on only by roles that see each of its rounds
-  uint64_t kv_full, q_full[3], q_ready[3], q_empty[3], o_full[3], o_ready[3], o_empty[3], st_full[2], st_empty[2];
+  PtFeed feed;
+  uint64_t kv_full, kv_empty, q_full[3], q_ready[3], q_empty[3], o_full[3], o_ready[3], o_empty[3], st_full[2], st_empty[2];
   uint64_t s_full, p_full, dp_full, ds_full, out_full, drain;
   alignas(16) float minus_lse[2][PT_B], minus_d[2][PT_B];  // of a block's queries: log-sum-exp in powers of two, D
+  PgKeysUnit unit[2];
   uint32_t tmem;
   int dead;
 };
 struct PgQueriesShared {
-  uint64_t q_full, k_full[3], k_ready[3], k_empty[3], v_full[3], v_empty[3];
+  PtFeed feed;
+  uint64_t q_full, q_empty, k_full[3], k_ready[3], k_empty[3], v_full[3], v_empty[3];
   uint64_t s_full, s_read, dp_full[2], ds_full[2], out_full, drain;
+  PgQueriesUnit unit[2];
   uint32_t tmem;
   int dead;
 };
@@ -60,6 +77,14 @@ constexpr int pg_queries_smem() {
   return 1024 + (2 + C::KR + C::VR) * C::SLOT + (int)sizeof(PgQueriesShared);
 }
 static_assert(pg_keys_smem<128>() <= 227 * 1024 && pg_queries_smem<128>() <= 227 * 1024, "shared memory of one SM");
+
+// Registers of a thread: 640 threads with 96 each were launched; 512 x 104 + 128 x 64 is as many.
+__device__ __forceinline__ void more_registers() {
+  if constexpr (PG_GROUPS == 4) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+}
+__device__ __forceinline__ void fewer_registers() {
+  if constexpr (PG_GROUPS == 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+}
 
 // Rows from `rows` on of a tile of D / 64 halves become zeros; two warps, t = 0 .. 63.
 template <int D>
@@ -81,19 +106,20 @@ __device__ __forceinline__ void scores_mma(uint32_t to, uint64_t a, uint64_t b) 
     tc::mma_ss(to, a + at, b + at, pt_idesc(PT_B), kk > 0);
   }
 }
-// to (128 x D) += the 128 x 128 bf16 in tensor memory at `a` (each half of the columns over its own scores) times rows of b
+// to (128 x D) += the 128 x 128 bf16 in tensor memory at `a` (each thread's columns over its own scores) times rows of b
 template <int D>
 __device__ __forceinline__ void rows_mma(uint32_t to, uint32_t a, uint64_t b, bool first) {
 #pragma unroll
   for (int kk = 0; kk < PT_B / 16; ++kk)  // 16 rows per step
-    tc::mma_ts(to, a + kk / 4 * 64 + kk % 4 * 8, b + kk * (2048 / 16), pt_idesc(D) | tc::IDESC_B_MN, !(first && kk == 0));
+    tc::mma_ts(to, a + kk * 16 / PG_COLS * PG_COLS + kk * 16 % PG_COLS / 2, b + kk * (2048 / 16), pt_idesc(D) | tc::IDESC_B_MN,
+               !(first && kk == 0));
 }
 
-// Half a row of a block's result, 128 x D in tensor memory, times `by`.
-template <int D>
-__device__ __forceinline__ void store_rows(void* base, bool is_bf16, int64_t at, uint32_t from, float by, int d, bool mine) {
+// N channels from c0 on of a row of a block's result in tensor memory, times `by`.
+template <int N>
+__device__ __forceinline__ void store_rows(void* base, bool is_bf16, int64_t at, uint32_t from, int c0, float by, int d, bool mine) {
 #pragma unroll 1
-  for (int c = 0; c < D; c += 16) {
+  for (int c = c0; c < c0 + N; c += 16) {
     float o[16];
     tc::tmem_ld16(from + c, o);
     if (mine && c < d) {
@@ -105,281 +131,380 @@ __device__ __forceinline__ void store_rows(void* base, bool is_bf16, int64_t at,
   }
 }
 
+__device__ __forceinline__ void ld_columns(uint32_t at, float2 (&x)[PG_COLS / 2]) {
+  if constexpr (PG_COLS == 64) tc::tmem_ld64(at, reinterpret_cast<float*>(x));
+  else tc::tmem_ld32(at, reinterpret_cast<float*>(x));
+}
+// bf16 pairs over the columns that they come from
+__device__ __forceinline__ void st_columns(uint32_t at, const uint32_t (&w)[PG_COLS / 2]) {
+#pragma unroll
+  for (int c = 0; c < PG_COLS / 2; c += 16) tc::tmem_st16(at + c, w + c);
+  tc::tmem_wait_st();
+}
+__device__ __forceinline__ float2 only(float2 x, int i, int from, int to) {  // of columns i and i + 1 those from .. to - 1
+  return make_float2(i < from || i >= to ? 0.f : x.x, i + 1 < from || i + 1 >= to ? 0.f : x.y);
+}
+// The cap's slope at a score in powers of two.
+__device__ __forceinline__ float2 cap_slope(float2 x, float over_cap2) {
+  const float2 y = mul2(x, both(over_cap2));
+  return fma2(mul2(y, both(-1.f)), y, both(1.f));
+}
+
+struct Yes {
+  static constexpr bool value = true;
+};
+struct No {
+  static constexpr bool value = false;
+};
+
 template <int D, bool CAP>
-__global__ void __launch_bounds__(PT_NT, 1)
+__global__ void __launch_bounds__(PG_NT, 1)
     prefill_attention_grad_keys_kernel(const __grid_constant__ PgMaps maps, const PromptAttnArgs a, const PromptGradArgs g,
-                                       const float2* __restrict__ stats, float* __restrict__ parts, const int nparts) {
+                                       const float2* __restrict__ stats, float* __restrict__ parts, const int nparts, const int64_t places) {
   using C = PgCfg<D>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* kbuf = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   unsigned char *vbuf = kbuf + C::SLOT, *qslots = vbuf + C::SLOT, *oslots = qslots + C::QR * C::SLOT;
   PgKeysShared& sh = *reinterpret_cast<PgKeysShared*>(oslots + C::OR * C::SLOT);
-  pdl_begin();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int window = a.window > 0 ? a.window : 0x7fffffff;
-  if (blockIdx.x == 0 && warp == 0) pf_check_offsets(a);
-  // the first keys first: most queries see them
-  const int unit = blockIdx.x % (a.Hkv * nparts), kh = unit / nparts, part = unit - kh * nparts;
-  const PfBlock b = pf_block<7>(a, blockIdx.x / (a.Hkv * nparts));
-  if (b.len == 0) return;
-  const int group = a.Hq / a.Hkv, h0 = kh * group + part * group / nparts, h1 = kh * group + (part + 1) * group / nparts;
-  const int k0 = b.row0, keys = min(PT_B, b.len - k0), tile = k0 / PT_B;
-  const int last = (int)min((int64_t)b.len - 1, (int64_t)k0 + keys - 2 + window);  // the last query that sees one of the keys
-  const int blocks = last / PT_B - tile + 1, n = blocks * (h1 - h0);              // a round: a block of one head
 
   if (tid == 0) {
-    tc::bar_init(&sh.kv_full, 1);
+    sh.feed.init(PG_W + 1 + 2);
+    tc::bar_init(&sh.kv_full, 1), tc::bar_init(&sh.kv_empty, 1);
     for (int i = 0; i < C::QR; ++i) tc::bar_init(&sh.q_full[i], 1), tc::bar_init(&sh.q_ready[i], 2), tc::bar_init(&sh.q_empty[i], 1);
     for (int i = 0; i < C::OR; ++i) tc::bar_init(&sh.o_full[i], 1), tc::bar_init(&sh.o_ready[i], 2), tc::bar_init(&sh.o_empty[i], 1);
-    for (int i = 0; i < 2; ++i) tc::bar_init(&sh.st_full[i], 2), tc::bar_init(&sh.st_empty[i], 8);
-    tc::bar_init(&sh.s_full, 1), tc::bar_init(&sh.p_full, 8), tc::bar_init(&sh.dp_full, 1), tc::bar_init(&sh.ds_full, 8);
+    for (int i = 0; i < 2; ++i) tc::bar_init(&sh.st_full[i], 2), tc::bar_init(&sh.st_empty[i], PG_W);
+    tc::bar_init(&sh.s_full, 1), tc::bar_init(&sh.p_full, PG_W), tc::bar_init(&sh.dp_full, 1), tc::bar_init(&sh.ds_full, PG_W);
     tc::bar_init(&sh.out_full, 1), tc::bar_init(&sh.drain, 1);
     tc::bar_fence_init();
     sh.dead = 0;
   }
-  if (warp == 8) tc::tmem_alloc(&sh.tmem, PT_TMEM);
+  if (tid == PG_SOFT + 32)
+    tc::prefetch_map(&maps.q), tc::prefetch_map(&maps.k), tc::prefetch_map(&maps.v), tc::prefetch_map(&maps.d_out);
+  if (warp == PG_W) tc::tmem_alloc(&sh.tmem, PT_TMEM);
+  pdl_begin();
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tmem = sh.tmem, t_s = tmem, t_dp = tmem + 128, t_dv = tmem + 256, t_dk = tmem + 384;
+  const uint32_t tmem = sh.tmem;
 
-  if (warp == 9) {
-    // ---- loads
-    if (lane == 0) {
-      bool ok = true;
-      int sent_q = 0, sent_o = 0;
-      tc::bar_arrive_expect_tx(&sh.kv_full, 2 * C::SLOT);
-      pt_load<D>(kbuf, &maps.k, kh, b.t0 + k0, &sh.kv_full);
-      pt_load<D>(vbuf, &maps.v, kh, b.t0 + k0, &sh.kv_full);
-      TcRing<C::QR> qr;
-      TcRing<C::OR> orr;
-      int h = h0, block = tile;
-      for (int i = 0; i < n; ++i) {
-        const int tok = b.t0 + block * PT_B;
-        ok = tc_wait(&sh.q_empty[qr.at], qr.parity ^ 1, &sh.dead);
+  if (warp == PG_W + 1) {
+    // ---- units, and their loads
+    fewer_registers();
+    const PfRanks<7> ranks(a);
+    bool ok = true, more = true;
+    int sent_q = 0, sent_o = 0, units = 0, id = blockIdx.x;
+    TcRing<2> un;
+    TcRing<C::QR> qr;
+    TcRing<C::OR> orr;
+    const int group = a.Hq / a.Hkv;
+    while (more) {
+      const int col = id % (a.Hkv * nparts);
+      // the first keys first: most queries see them
+      const PfBlock b = pf_ranked(a, ranks, id / (a.Hkv * nparts), places, true);
+      if (b.len > 0) {
+        PgKeysUnit u;
+        u.t0 = b.t0, u.len = b.len, u.k0 = b.row0, u.tile = b.row0 / PT_B;
+        u.kh = col / nparts, u.part = col - u.kh * nparts;
+        u.h0 = u.kh * group + u.part * group / nparts, u.h1 = u.kh * group + (u.part + 1) * group / nparts;
+        const int keys = min(PT_B, b.len - b.row0);
+        const int last = (int)min((int64_t)b.len - 1, (int64_t)b.row0 + keys - 2 + window);  // the last query that sees one of the keys
+        u.blocks = last / PT_B - u.tile + 1;
+        ok = tc_wait_warp(&sh.feed.empty[un.at], un.parity ^ 1, &sh.dead);
         if (!ok) break;
-        tc::bar_arrive_expect_tx(&sh.q_full[qr.at], C::SLOT);
-        pt_load<D>(qslots + qr.at * C::SLOT, &maps.q, h, tok, &sh.q_full[qr.at]);
-        ++sent_q;
-        qr.step();
-        if (a.test_stall && i == PT_STALL_AT) ok = tc_give_up(&sh.dead);
-        ok = ok && tc_wait(&sh.o_empty[orr.at], orr.parity ^ 1, &sh.dead);
+        if (lane == 0) {
+          sh.unit[un.at] = u;
+          tc::bar_arrive(&sh.feed.full[un.at]);
+          ok = tc_wait(&sh.kv_empty, (units & 1) ^ 1, &sh.dead);
+          if (ok) {
+            tc::bar_arrive_expect_tx(&sh.kv_full, 2 * C::SLOT);
+            pt_load<D>(kbuf, &maps.k, u.kh, u.t0 + u.k0, &sh.kv_full);
+            pt_load<D>(vbuf, &maps.v, u.kh, u.t0 + u.k0, &sh.kv_full);
+            ++units;
+          }
+          const int n = u.blocks * (u.h1 - u.h0);
+          int h = u.h0, block = u.tile;
+          for (int i = 0; ok && i < n; ++i) {
+            const int tok = u.t0 + block * PT_B;
+            ok = tc_wait(&sh.q_empty[qr.at], qr.parity ^ 1, &sh.dead);
+            if (!ok) break;
+            tc::bar_arrive_expect_tx(&sh.q_full[qr.at], C::SLOT);
+            pt_load<D>(qslots + qr.at * C::SLOT, &maps.q, h, tok, &sh.q_full[qr.at]);
+            ++sent_q;
+            qr.step();
+            if (i + 1 == n) sh.feed.ask();
+            if (a.test_stall && i == PT_STALL_AT) ok = tc_give_up(&sh.dead);
+            ok = ok && tc_wait(&sh.o_empty[orr.at], orr.parity ^ 1, &sh.dead);
+            if (!ok) break;
+            tc::bar_arrive_expect_tx(&sh.o_full[orr.at], C::SLOT);
+            pt_load<D>(oslots + orr.at * C::SLOT, &maps.d_out, h, tok, &sh.o_full[orr.at]);
+            ++sent_o;
+            orr.step();
+            if (++block == u.tile + u.blocks) block = u.tile, ++h;
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
-        tc::bar_arrive_expect_tx(&sh.o_full[orr.at], C::SLOT);
-        pt_load<D>(oslots + orr.at * C::SLOT, &maps.d_out, h, tok, &sh.o_full[orr.at]);
-        ++sent_o;
-        orr.step();
-        if (++block == tile + blocks) block = tile, ++h;
+        un.step();
+      } else if (lane == 0) {
+        sh.feed.ask();
       }
-      if (!ok) {
-        // let what is on its way arrive before the CTA ends: the last round of every slot
-        flag_status(a.status, KDA_DEV_TIMEOUT);
-        tc::bar_wait(&sh.kv_full, 0, 1u << 16);
-        for (int i = max(0, sent_q - C::QR); i < sent_q; ++i) tc::bar_wait(&sh.q_full[i % C::QR], i / C::QR & 1, 1u << 16);
-        for (int i = max(0, sent_o - C::OR); i < sent_o; ++i) tc::bar_wait(&sh.o_full[i % C::OR], i / C::OR & 1, 1u << 16);
+      ok = sh.feed.answered(&sh.dead, id);
+      if (!ok) break;
+      more = id >= 0;
+    }
+    if (ok) {
+      ok = tc_wait_warp(&sh.feed.empty[un.at], un.parity ^ 1, &sh.dead);
+      if (lane == 0 && ok) {
+        sh.unit[un.at].len = 0;
+        tc::bar_arrive(&sh.feed.full[un.at]);
       }
     }
+    if (!ok && lane == 0) {
+      // let what is on its way arrive before the CTA ends: the last round of every slot
+      flag_status(a.status, KDA_DEV_TIMEOUT);
+      sh.feed.drain();
+      if (units > 0) tc::bar_wait(&sh.kv_full, (units - 1) & 1, 1u << 16);
+      for (int i = max(0, sent_q - C::QR); i < sent_q; ++i) tc::bar_wait(&sh.q_full[i % C::QR], i / C::QR & 1, 1u << 16);
+      for (int i = max(0, sent_o - C::OR); i < sent_o; ++i) tc::bar_wait(&sh.o_full[i % C::OR], i / C::OR & 1, 1u << 16);
+    }
     __syncwarp();
-  } else if (warp == 8) {
-    // ---- products
-    if (lane == 0) {
-      bool ok = tc_wait(&sh.kv_full, 0, &sh.dead);
-      const uint64_t kd = tc::sdesc(tc::smem_u32(kbuf)), vd = tc::sdesc(tc::smem_u32(vbuf));
-      const uint64_t q_s = tc::sdesc(tc::smem_u32(qslots)), o_s = tc::sdesc(tc::smem_u32(oslots));
-      const uint64_t q_r = tc::sdesc_mn(tc::smem_u32(qslots), PT_HALF), o_r = tc::sdesc_mn(tc::smem_u32(oslots), PT_HALF);
-      constexpr int STEP = C::SLOT / 16;
-      TcRing<C::QR> q_next, q_now;   // of the scores to form next, and of the gradients'
-      TcRing<C::OR> o_next, o_now;
-      auto form_s = [&]() {
-        ok = ok && tc_wait(&sh.q_ready[q_next.at], q_next.parity, &sh.dead);
-        if (!ok) return;
-        tc::fence_after_sync();
+  } else if (warp == PG_W) {
+    // ---- products: the warp waits and counts as one, one lane issues
+    fewer_registers();
+    bool ok = true;
+    const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem), t_s = tm, t_dp = tm + 128, t_dv = tm + 256, t_dk = tm + 384;
+    const uint64_t kd = tc::sdesc(tc::smem_u32(kbuf)), vd = tc::sdesc(tc::smem_u32(vbuf));
+    const uint64_t q_s = tc::sdesc(tc::smem_u32(qslots)), o_s = tc::sdesc(tc::smem_u32(oslots));
+    const uint64_t q_r = tc::sdesc_mn(tc::smem_u32(qslots), PT_HALF), o_r = tc::sdesc_mn(tc::smem_u32(oslots), PT_HALF);
+    constexpr int STEP = C::SLOT / 16;
+    TcRing<2> un;
+    TcRing<C::QR> q_next, q_now;  // of the scores to form next, and of the gradients'
+    TcRing<C::OR> o_next, o_now;
+    uint32_t p_parity = 0, ds_parity = 0;
+    auto form_s = [&]() {
+      ok = ok && tc_wait_warp(&sh.q_ready[q_next.at], q_next.parity, &sh.dead);
+      if (!ok) return;
+      tc::fence_after_sync();
+      if (tc::elect_one()) {
         scores_mma<D>(t_s, kd, q_s + q_next.at * STEP);
         tc::commit(&sh.s_full);
-        q_next.step();
-      };
-      auto form_dp = [&]() {
-        ok = ok && tc_wait(&sh.o_ready[o_next.at], o_next.parity, &sh.dead);
-        if (!ok) return;
-        tc::fence_after_sync();
+      }
+      q_next.step();
+    };
+    auto form_dp = [&](bool last) {
+      ok = ok && tc_wait_warp(&sh.o_ready[o_next.at], o_next.parity, &sh.dead);
+      if (!ok) return;
+      tc::fence_after_sync();
+      if (tc::elect_one()) {
         scores_mma<D>(t_dp, vd, o_s + o_next.at * STEP);
         tc::commit(&sh.dp_full);
-        o_next.step();
-      };
+        if (last) tc::commit(&sh.kv_empty);
+      }
+      o_next.step();
+    };
+    for (uint32_t kv_parity = 0;; kv_parity ^= 1, un.step()) {
+      ok = tc_wait_warp(&sh.feed.full[un.at], un.parity, &sh.dead);
+      if (!ok) break;
+      const PgKeysUnit& u = sh.unit[un.at];
+      // numbers that are known to be the same for all lanes
+      const int end = __reduce_max_sync(0xffffffffu, u.len), n = __reduce_max_sync(0xffffffffu, u.blocks * (u.h1 - u.h0));
+      if (lane == 0) tc::bar_arrive(&sh.feed.empty[un.at]);
+      __syncwarp();
+      if (end == 0) break;
+      ok = tc_wait_warp(&sh.kv_full, kv_parity, &sh.dead);
       form_s();
-      form_dp();
+      form_dp(n == 1);
       for (int i = 0; ok && i < n; ++i) {
-        ok = tc_wait(&sh.p_full, i & 1, &sh.dead);
+        ok = tc_wait_warp(&sh.p_full, p_parity, &sh.dead);
         if (!ok) break;
+        p_parity ^= 1;
         tc::fence_after_sync();
-        rows_mma<D>(t_dv, t_s, o_r + o_now.at * STEP, i == 0);
-        tc::commit(&sh.o_empty[o_now.at]);
+        if (tc::elect_one()) {
+          rows_mma<D>(t_dv, t_s, o_r + o_now.at * STEP, i == 0);
+          tc::commit(&sh.o_empty[o_now.at]);
+        }
         o_now.step();
         // the next scores go where these probabilities lie: products run in the order of their issue
         if (i + 1 < n) form_s();
-        ok = ok && tc_wait(&sh.ds_full, i & 1, &sh.dead);
+        ok = ok && tc_wait_warp(&sh.ds_full, ds_parity, &sh.dead);
         if (!ok) break;
+        ds_parity ^= 1;
         tc::fence_after_sync();
-        rows_mma<D>(t_dk, t_dp, q_r + q_now.at * STEP, i == 0);
-        tc::commit(&sh.q_empty[q_now.at]);
+        if (tc::elect_one()) {
+          rows_mma<D>(t_dk, t_dp, q_r + q_now.at * STEP, i == 0);
+          tc::commit(&sh.q_empty[q_now.at]);
+          if (i + 1 == n) tc::commit(&sh.out_full);
+        }
         q_now.step();
-        if (i + 1 < n) form_dp();
+        if (i + 1 < n) form_dp(i + 2 == n);
       }
-      // nothing of this thread's is on its way when the CTA ends
-      if (ok) tc::commit(&sh.out_full);
-      else flag_status(a.status, KDA_DEV_TIMEOUT);
-      tc::commit(&sh.drain);
-      tc::bar_wait(&sh.drain, 0);
+      if (!ok) break;
     }
+    // nothing of this warp's is on its way when the CTA ends
+    if (!ok && lane == 0) flag_status(a.status, KDA_DEV_TIMEOUT);
     __syncwarp();
-  } else if (warp >= 10) {
+    if (tc::elect_one()) tc::commit(&sh.drain);
+    tc::bar_wait(&sh.drain, 0);
+    __syncwarp();
+  } else if (warp >= PG_W + 2) {
     // ---- statistics, and rows behind the sequence
-    const int t = tid - 320;
+    fewer_registers();
+    const int t = tid - PG_SOFT - 64;
+    if (blockIdx.x == 0 && t < 32) pf_check_offsets(a);
     TcRing<C::QR> qr;
     TcRing<C::OR> orr;
-    TcRing<2> st;
+    TcRing<2> st, un;
     bool ok = true;
-    int h = h0, block = tile;
-    float2 next[2];
-    auto fetch = [&]() {
+    for (;; un.step()) {
+      ok = tc_wait_warp(&sh.feed.full[un.at], un.parity, &sh.dead);
+      if (!ok) break;
+      const PgKeysUnit u = sh.unit[un.at];
+      __syncwarp();
+      if (lane == 0) tc::bar_arrive(&sh.feed.empty[un.at]);
+      if (u.len == 0) break;
+      const int n = u.blocks * (u.h1 - u.h0);
+      int h = u.h0, block = u.tile;
+      float2 next[2];
+      auto fetch = [&]() {
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int row = block * PT_B + t + 64 * r;
-        next[r] = row < b.len ? __ldg(stats + (int64_t)h * a.T + b.t0 + row) : make_float2(0.f, 0.f);
+        for (int r = 0; r < 2; ++r) {
+          const int row = block * PT_B + t + 64 * r;
+          next[r] = row < u.len ? __ldg(stats + (int64_t)h * a.T + u.t0 + row) : make_float2(0.f, 0.f);
+        }
+      };
+      fetch();
+      for (int i = 0; i < n; ++i) {
+        const int rows = u.len - block * PT_B;  // of the sequence, from the block on
+        ok = tc_wait_warp(&sh.st_empty[st.at], st.parity ^ 1, &sh.dead);
+        if (!ok) break;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) sh.minus_lse[st.at][t + 64 * r] = -next[r].x, sh.minus_d[st.at][t + 64 * r] = -next[r].y;
+        __syncwarp();
+        if (lane == 0) tc::bar_arrive(&sh.st_full[st.at]);
+        st.step();
+        if (++block == u.tile + u.blocks) block = u.tile, ++h;
+        if (i + 1 < n) fetch();
+        ok = tc_wait_warp(&sh.q_full[qr.at], qr.parity, &sh.dead);
+        if (!ok) break;
+        if (rows < PT_B) clear_behind<D>(qslots + qr.at * C::SLOT, rows, t);
+        __syncwarp();
+        if (lane == 0) tc::bar_arrive(&sh.q_ready[qr.at]);
+        qr.step();
+        ok = tc_wait_warp(&sh.o_full[orr.at], orr.parity, &sh.dead);
+        if (!ok) break;
+        if (rows < PT_B) clear_behind<D>(oslots + orr.at * C::SLOT, rows, t);
+        __syncwarp();
+        if (lane == 0) tc::bar_arrive(&sh.o_ready[orr.at]);
+        orr.step();
       }
-    };
-    fetch();
-    for (int i = 0; i < n; ++i) {
-      const int rows = b.len - block * PT_B;  // of the sequence, from the block on
-      ok = ok && tc_wait(&sh.st_empty[st.at], st.parity ^ 1, &sh.dead);
-      ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-#pragma unroll
-      for (int r = 0; r < 2; ++r) sh.minus_lse[st.at][t + 64 * r] = -next[r].x, sh.minus_d[st.at][t + 64 * r] = -next[r].y;
-      __syncwarp();
-      if (lane == 0) tc::bar_arrive(&sh.st_full[st.at]);
-      st.step();
-      if (++block == tile + blocks) block = tile, ++h;
-      if (i + 1 < n) fetch();
-      ok = tc_wait(&sh.q_full[qr.at], qr.parity, &sh.dead);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      if (rows < PT_B) clear_behind<D>(qslots + qr.at * C::SLOT, rows, t);
-      __syncwarp();
-      if (lane == 0) tc::bar_arrive(&sh.q_ready[qr.at]);
-      qr.step();
-      ok = tc_wait(&sh.o_full[orr.at], orr.parity, &sh.dead);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      if (rows < PT_B) clear_behind<D>(oslots + orr.at * C::SLOT, rows, t);
-      __syncwarp();
-      if (lane == 0) tc::bar_arrive(&sh.o_ready[orr.at]);
-      orr.step();
     }
     if (!ok && lane == 0) flag_status(a.status, KDA_DEV_TIMEOUT);
   } else {
-    // ---- arithmetic: thread = key, and 64 of a block's queries
-    const int half = warp >> 2, key = k0 + (tid & 127);
-    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16, own_s = t_s + half * 64 + lanes, own_dp = t_dp + half * 64 + lanes;
-    const float cap2 = a.softcap * PA_LOG2E, factor = a.scale * (CAP ? 2.f * PA_LOG2E / a.softcap : PA_LOG2E);
+    // ---- arithmetic: thread = key, and PG_COLS of a block's queries
+    more_registers();
+    const int part = warp >> 2;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16, t_s = tmem, t_dp = tmem + 128, t_dv = tmem + 256, t_dk = tmem + 384;
+    const uint32_t own_s = t_s + part * PG_COLS + lanes, own_dp = t_dp + part * PG_COLS + lanes;
+    const float cap2 = a.softcap * PA_LOG2E, factor = a.scale * (CAP ? 2.f * PA_LOG2E / a.softcap : PA_LOG2E), over_cap2 = 1.f / cap2;
     bool ok = true;
-    TcRing<2> st;
-    int block = tile;
-    for (int i = 0; i < n; ++i) {
-      const int row0 = block * PT_B + half * 64;
-      const bool masked = block == tile || (block + 1) * PT_B > b.len || (block + 1) * PT_B - k0 > window;
-      if (++block == tile + blocks) block = tile;
-      ok = ok && tc_wait(&sh.st_full[st.at], st.parity, &sh.dead) && tc_wait(&sh.s_full, i & 1, &sh.dead);
-      ok = __all_sync(0xffffffffu, ok);
+    TcRing<2> st, un;
+    uint32_t s_parity = 0, dp_parity = 0, out_parity = 0;
+    for (;; un.step()) {
+      ok = tc_wait_warp(&sh.feed.full[un.at], un.parity, &sh.dead);
       if (!ok) break;
-      tc::fence_after_sync();
-      float2 x[32];
-      tc::tmem_ld64(own_s, reinterpret_cast<float*>(x));
-      if constexpr (CAP) pt_cap(x, factor, cap2);
-      const float4* lse = reinterpret_cast<const float4*>(sh.minus_lse[st.at] + half * 64);
-      const float4* dd = reinterpret_cast<const float4*>(sh.minus_d[st.at] + half * 64);
-      // the key is seen by queries from .. to - 1 of the 64
-      const int from = masked ? key - row0 : 0, to = masked ? (int)min((int64_t)b.len, (int64_t)key + window) - row0 : 64;
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t w[16];
-#pragma unroll
-        for (int j = 0; j < 16; j += 2) {
-          const float4 minus = lse[(16 * c + j) / 2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int at = 16 * c + j + e;
-            const float2 ml = e == 0 ? make_float2(minus.x, minus.y) : make_float2(minus.z, minus.w);
-            float2 p = CAP ? add2(x[at], ml) : fma2(x[at], both(factor), ml);
-            p = make_float2(ex2(p.x), ex2(p.y));
-            if (masked) {
-              if (2 * at < from || 2 * at >= to) p.x = 0.f;
-              if (2 * at + 1 < from || 2 * at + 1 >= to) p.y = 0.f;
-            }
-            w[j + e] = pack_bf16(p.x, p.y);
-            if constexpr (CAP) {  // times the cap's slope from here on
-              const float2 y = mul2(x[at], both(1.f / cap2));
-              p = mul2(p, fma2(mul2(y, both(-1.f)), y, both(1.f)));
-              if (masked) {
-                if (2 * at < from || 2 * at >= to) p.x = 0.f;
-                if (2 * at + 1 < from || 2 * at + 1 >= to) p.y = 0.f;
-              }
-            }
-            x[at] = p;
-          }
-        }
-        tc::tmem_st16(own_s + 16 * c, w);
-      }
-      tc::tmem_wait_st();
-      tc::fence_before_sync();
+      const PgKeysUnit u = sh.unit[un.at];
       __syncwarp();
-      if (lane == 0) tc::bar_arrive(&sh.p_full);
-      ok = tc_wait(&sh.dp_full, i & 1, &sh.dead);
-      ok = __all_sync(0xffffffffu, ok);
+      if (lane == 0) tc::bar_arrive(&sh.feed.empty[un.at]);
+      if (u.len == 0) break;
+      const int key = u.k0 + (tid & 127), n = u.blocks * (u.h1 - u.h0);
+      int block = u.tile;
+      for (int i = 0; i < n; ++i) {
+        const int row0 = block * PT_B + part * PG_COLS;
+        const bool masked = block == u.tile || (block + 1) * PT_B > u.len || (block + 1) * PT_B - u.k0 > window;
+        // of the thread's queries the key is seen by from .. to - 1
+        const int from = key - row0, to = (int)min((int64_t)u.len, (int64_t)key + window) - row0;
+        if (++block == u.tile + u.blocks) block = u.tile;
+        ok = tc_wait(&sh.st_full[st.at], st.parity, &sh.dead) && tc_wait(&sh.s_full, s_parity, &sh.dead);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        s_parity ^= 1;
+        tc::fence_after_sync();
+        float2 x[PG_COLS / 2];
+        const float4* lse = reinterpret_cast<const float4*>(sh.minus_lse[st.at] + part * PG_COLS);
+        const float4* dd = reinterpret_cast<const float4*>(sh.minus_d[st.at] + part * PG_COLS);
+        ld_columns(own_s, x);
+        if constexpr (CAP) pt_cap(x, factor, cap2);
+        // x becomes the probabilities, times the cap's slope
+        auto probabilities = [&](auto some) {
+          uint32_t w[PG_COLS / 2];
+#pragma unroll
+          for (int j = 0; j < PG_COLS / 2; j += 2) {
+            const float4 minus = lse[j / 2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float2 ml = e == 0 ? make_float2(minus.x, minus.y) : make_float2(minus.z, minus.w);
+              float2 p = CAP ? add2(x[j + e], ml) : fma2(x[j + e], both(factor), ml);
+              p = make_float2(ex2(p.x), ex2(p.y));
+              if (decltype(some)::value) p = only(p, 2 * (j + e), from, to);
+              w[j + e] = pack_bf16(p.x, p.y);
+              x[j + e] = CAP ? mul2(p, cap_slope(x[j + e], over_cap2)) : p;
+            }
+          }
+          st_columns(own_s, w);
+        };
+        if (masked) probabilities(Yes());
+        else probabilities(No());
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::bar_arrive(&sh.p_full);
+        ok = tc_wait_warp(&sh.dp_full, dp_parity, &sh.dead);
+        if (!ok) break;
+        dp_parity ^= 1;
+        tc::fence_after_sync();
+        float2 dp[PG_COLS / 2];
+        ld_columns(own_dp, dp);
+        auto slopes = [&](auto some) {
+          uint32_t w[PG_COLS / 2];
+#pragma unroll
+          for (int j = 0; j < PG_COLS / 2; j += 2) {
+            const float4 minus = dd[j / 2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float2 md = e == 0 ? make_float2(minus.x, minus.y) : make_float2(minus.z, minus.w);
+              float2 ds = mul2(x[j + e], add2(dp[j + e], md));
+              if (decltype(some)::value) ds = only(ds, 2 * (j + e), from, to);
+              w[j + e] = pack_bf16(ds.x, ds.y);
+            }
+          }
+          st_columns(own_dp, w);
+        };
+        if (masked) slopes(Yes());
+        else slopes(No());
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::bar_arrive(&sh.ds_full), tc::bar_arrive(&sh.st_empty[st.at]);
+        st.step();
+      }
       if (!ok) break;
+      ok = tc_wait_warp(&sh.out_full, out_parity, &sh.dead);
+      if (!ok) break;
+      out_parity ^= 1;
       tc::fence_after_sync();
-      float2 dp[32];
-      tc::tmem_ld64(own_dp, reinterpret_cast<float*>(dp));
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t w[16];
-#pragma unroll
-        for (int j = 0; j < 16; j += 2) {
-          const float4 minus = dd[(16 * c + j) / 2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int at = 16 * c + j + e;
-            const float2 md = e == 0 ? make_float2(minus.x, minus.y) : make_float2(minus.z, minus.w);
-            float2 ds = mul2(x[at], add2(dp[at], md));
-            if (masked) {
-              if (2 * at < from || 2 * at >= to) ds.x = 0.f;
-              if (2 * at + 1 < from || 2 * at + 1 >= to) ds.y = 0.f;
-            }
-            w[j + e] = pack_bf16(ds.x, ds.y);
-          }
-        }
-        tc::tmem_st16(own_dp + 16 * c, w);
-      }
-      tc::tmem_wait_st();
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) tc::bar_arrive(&sh.ds_full), tc::bar_arrive(&sh.st_empty[st.at]);
-      st.step();
-    }
-    ok = ok && tc_wait(&sh.out_full, 0, &sh.dead);
-    ok = __all_sync(0xffffffffu, ok);
-    tc::fence_after_sync();
-    if (ok) {
-      // the first half of the warps has dv, the second dk
-      const bool mine = key - k0 < keys;
-      const int64_t t = b.t0 + key;
-      const uint32_t from = (half ? t_dk : t_dv) + lanes;
-      const float by = half ? a.scale : 1.f;
+      // the first half of the parts has dv, the second dk, each its channels
+      constexpr int N = D * 2 / PG_GROUPS;
+      const int of_k = part / (PG_GROUPS / 2), c0 = part % (PG_GROUPS / 2) * N;
+      const bool mine = key < u.len;
+      const int64_t t = u.t0 + key;
+      const uint32_t from = (of_k ? t_dk : t_dv) + lanes;
+      const float by = of_k ? a.scale : 1.f;
       if (nparts > 1) {
-        float* to = parts + (int64_t)(part * 2 + half) * a.T * a.Hkv * a.d;
-        store_rows<D>(to, false, (t * a.Hkv + kh) * a.d, from, by, a.d, mine);
+        float* to = parts + (int64_t)(u.part * 2 + of_k) * a.T * a.Hkv * a.d;
+        store_rows<N>(to, false, (t * a.Hkv + u.kh) * a.d, from, c0, by, a.d, mine);
       } else {
-        store_rows<D>(half ? g.dk : g.dv, g.bf16, t * (half ? g.dk_stride : g.dv_stride) + (int64_t)kh * a.d, from, by, a.d, mine);
+        store_rows<N>(of_k ? g.dk : g.dv, g.bf16, t * (of_k ? g.dk_stride : g.dv_stride) + (int64_t)u.kh * a.d, from, c0, by, a.d, mine);
       }
     }
     if (!ok && lane == 0) flag_status(a.status, KDA_DEV_TIMEOUT);
@@ -387,11 +512,11 @@ __global__ void __launch_bounds__(PT_NT, 1)
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  if (warp == 8) tc::tmem_dealloc(tmem, PT_TMEM);
+  if (warp == PG_W) tc::tmem_dealloc(tmem, PT_TMEM);
 }
 
 template <int D, bool CAP>
-__global__ void __launch_bounds__(PT_NT, 1)
+__global__ void __launch_bounds__(PG_NT, 1)
     prefill_attention_grad_queries_kernel(const __grid_constant__ PgMaps maps, const PromptAttnArgs a, const PromptGradArgs g,
                                           const float2* __restrict__ stats, const int64_t places) {
   using C = PgCfg<D>;
@@ -399,201 +524,271 @@ __global__ void __launch_bounds__(PT_NT, 1)
   unsigned char* qbuf = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   unsigned char *obuf = qbuf + C::SLOT, *kslots = obuf + C::SLOT, *vslots = kslots + C::KR * C::SLOT;
   PgQueriesShared& sh = *reinterpret_cast<PgQueriesShared*>(vslots + C::VR * C::SLOT);
-  pdl_begin();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int window = a.window > 0 ? a.window : 0x7fffffff;
-  const int h = blockIdx.x % a.Hq, kh = h / (a.Hq / a.Hkv);
-  const PfBlock b = pf_block<7>(a, places - 1 - blockIdx.x / a.Hq);  // the longest rows first
-  if (b.len == 0) return;
-  const int rows = min(PT_B, b.len - b.row0);
-  const int lo = max(0, b.row0 - window + 1) / PT_B, n = b.row0 / PT_B - lo + 1;
 
   if (tid == 0) {
-    tc::bar_init(&sh.q_full, 1);
+    sh.feed.init(PG_W + 1 + 2);
+    tc::bar_init(&sh.q_full, 1), tc::bar_init(&sh.q_empty, 1);
     for (int i = 0; i < C::KR; ++i) tc::bar_init(&sh.k_full[i], 1), tc::bar_init(&sh.k_ready[i], 2), tc::bar_init(&sh.k_empty[i], 1);
     for (int i = 0; i < C::VR; ++i) tc::bar_init(&sh.v_full[i], 1), tc::bar_init(&sh.v_empty[i], 1);
-    tc::bar_init(&sh.s_full, 1), tc::bar_init(&sh.s_read, 8);
-    for (int i = 0; i < 2; ++i) tc::bar_init(&sh.dp_full[i], 1), tc::bar_init(&sh.ds_full[i], 8);
+    tc::bar_init(&sh.s_full, 1), tc::bar_init(&sh.s_read, PG_W);
+    for (int i = 0; i < 2; ++i) tc::bar_init(&sh.dp_full[i], 1), tc::bar_init(&sh.ds_full[i], PG_W);
     tc::bar_init(&sh.out_full, 1), tc::bar_init(&sh.drain, 1);
     tc::bar_fence_init();
     sh.dead = 0;
   }
-  if (warp == 8) tc::tmem_alloc(&sh.tmem, PT_TMEM);
+  if (tid == PG_SOFT + 32)
+    tc::prefetch_map(&maps.q), tc::prefetch_map(&maps.k), tc::prefetch_map(&maps.v), tc::prefetch_map(&maps.d_out);
+  if (warp == PG_W) tc::tmem_alloc(&sh.tmem, PT_TMEM);
+  pdl_begin();
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tmem = sh.tmem, t_s = tmem, t_dp = tmem + 128, t_dq = tmem + 384;  // two buffers of dp
+  const uint32_t tmem = sh.tmem;
 
-  if (warp == 9) {
-    // ---- loads
-    if (lane == 0) {
-      bool ok = true;
-      int sent_k = 0, sent_v = 0;
-      tc::bar_arrive_expect_tx(&sh.q_full, 2 * C::SLOT);
-      pt_load<D>(qbuf, &maps.q, h, b.t0 + b.row0, &sh.q_full);
-      pt_load<D>(obuf, &maps.d_out, h, b.t0 + b.row0, &sh.q_full);
-      TcRing<C::KR> kr;
-      TcRing<C::VR> vr;
-      for (int i = 0; i < n; ++i) {
-        const int tok = b.t0 + (lo + i) * PT_B;
-        ok = tc_wait(&sh.k_empty[kr.at], kr.parity ^ 1, &sh.dead);
+  if (warp == PG_W + 1) {
+    // ---- units, and their loads
+    fewer_registers();
+    const PfRanks<7> ranks(a);
+    bool ok = true, more = true;
+    int sent_k = 0, sent_v = 0, units = 0, id = blockIdx.x;
+    TcRing<2> un;
+    TcRing<C::KR> kr;
+    TcRing<C::VR> vr;
+    while (more) {
+      const PfBlock b = pf_ranked(a, ranks, id / a.Hq, places, false);  // the longest rows first
+      if (b.len > 0) {
+        PgQueriesUnit u;
+        u.t0 = b.t0, u.len = b.len, u.row0 = b.row0, u.h = id % a.Hq;
+        u.lo = max(0, b.row0 - window + 1) / PT_B, u.n = b.row0 / PT_B - u.lo + 1;
+        ok = tc_wait_warp(&sh.feed.empty[un.at], un.parity ^ 1, &sh.dead);
         if (!ok) break;
-        tc::bar_arrive_expect_tx(&sh.k_full[kr.at], C::SLOT);
-        pt_load<D>(kslots + kr.at * C::SLOT, &maps.k, kh, tok, &sh.k_full[kr.at]);
-        ++sent_k;
-        kr.step();
-        if (a.test_stall && i == PT_STALL_AT) ok = tc_give_up(&sh.dead);
-        ok = ok && tc_wait(&sh.v_empty[vr.at], vr.parity ^ 1, &sh.dead);
+        if (lane == 0) {
+          sh.unit[un.at] = u;
+          tc::bar_arrive(&sh.feed.full[un.at]);
+          const int kh = u.h / (a.Hq / a.Hkv);
+          for (int i = 0; i < u.n; ++i) {
+            const int tok = u.t0 + (u.lo + i) * PT_B;
+            ok = tc_wait(&sh.k_empty[kr.at], kr.parity ^ 1, &sh.dead);
+            if (!ok) break;
+            tc::bar_arrive_expect_tx(&sh.k_full[kr.at], C::SLOT);
+            pt_load<D>(kslots + kr.at * C::SLOT, &maps.k, kh, tok, &sh.k_full[kr.at]);
+            ++sent_k;
+            kr.step();
+            if (i == 0) {
+              ok = tc_wait(&sh.q_empty, (units & 1) ^ 1, &sh.dead);
+              if (!ok) break;
+              tc::bar_arrive_expect_tx(&sh.q_full, 2 * C::SLOT);
+              pt_load<D>(qbuf, &maps.q, u.h, u.t0 + u.row0, &sh.q_full);
+              pt_load<D>(obuf, &maps.d_out, u.h, u.t0 + u.row0, &sh.q_full);
+              ++units;
+            }
+            if (i + 1 == u.n) sh.feed.ask();
+            if (a.test_stall && i == PT_STALL_AT) ok = tc_give_up(&sh.dead);
+            ok = ok && tc_wait(&sh.v_empty[vr.at], vr.parity ^ 1, &sh.dead);
+            if (!ok) break;
+            tc::bar_arrive_expect_tx(&sh.v_full[vr.at], C::SLOT);
+            pt_load<D>(vslots + vr.at * C::SLOT, &maps.v, kh, tok, &sh.v_full[vr.at]);
+            ++sent_v;
+            vr.step();
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
-        tc::bar_arrive_expect_tx(&sh.v_full[vr.at], C::SLOT);
-        pt_load<D>(vslots + vr.at * C::SLOT, &maps.v, kh, tok, &sh.v_full[vr.at]);
-        ++sent_v;
-        vr.step();
+        un.step();
+      } else if (lane == 0) {
+        sh.feed.ask();
       }
-      if (!ok) {
-        flag_status(a.status, KDA_DEV_TIMEOUT);
-        tc::bar_wait(&sh.q_full, 0, 1u << 16);
-        for (int i = max(0, sent_k - C::KR); i < sent_k; ++i) tc::bar_wait(&sh.k_full[i % C::KR], i / C::KR & 1, 1u << 16);
-        for (int i = max(0, sent_v - C::VR); i < sent_v; ++i) tc::bar_wait(&sh.v_full[i % C::VR], i / C::VR & 1, 1u << 16);
+      ok = sh.feed.answered(&sh.dead, id);
+      if (!ok) break;
+      more = id >= 0;
+    }
+    if (ok) {
+      ok = tc_wait_warp(&sh.feed.empty[un.at], un.parity ^ 1, &sh.dead);
+      if (lane == 0 && ok) {
+        sh.unit[un.at].len = 0;
+        tc::bar_arrive(&sh.feed.full[un.at]);
       }
     }
+    if (!ok && lane == 0) {
+      flag_status(a.status, KDA_DEV_TIMEOUT);
+      sh.feed.drain();
+      if (units > 0) tc::bar_wait(&sh.q_full, (units - 1) & 1, 1u << 16);
+      for (int i = max(0, sent_k - C::KR); i < sent_k; ++i) tc::bar_wait(&sh.k_full[i % C::KR], i / C::KR & 1, 1u << 16);
+      for (int i = max(0, sent_v - C::VR); i < sent_v; ++i) tc::bar_wait(&sh.v_full[i % C::VR], i / C::VR & 1, 1u << 16);
+    }
     __syncwarp();
-  } else if (warp == 8) {
-    // ---- products
-    if (lane == 0) {
-      bool ok = tc_wait(&sh.q_full, 0, &sh.dead);
-      const uint64_t qd = tc::sdesc(tc::smem_u32(qbuf)), od = tc::sdesc(tc::smem_u32(obuf));
-      const uint64_t k_s = tc::sdesc(tc::smem_u32(kslots)), v_s = tc::sdesc(tc::smem_u32(vslots));
-      const uint64_t k_r = tc::sdesc_mn(tc::smem_u32(kslots), PT_HALF);
-      constexpr int STEP = C::SLOT / 16;
-      TcRing<C::KR> k_next, k_now;
-      TcRing<C::VR> vr;
-      TcRing<2> dp_next, dp_now;
-      auto form = [&]() {  // scores and dp of the next tile
-        ok = ok && tc_wait(&sh.k_ready[k_next.at], k_next.parity, &sh.dead);
-        if (!ok) return;
-        tc::fence_after_sync();
+  } else if (warp == PG_W) {
+    // ---- products: the warp waits and counts as one, one lane issues
+    fewer_registers();
+    bool ok = true;
+    const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem), t_s = tm, t_dp = tm + 128, t_dq = tm + 384;  // two buffers of dp
+    const uint64_t qd = tc::sdesc(tc::smem_u32(qbuf)), od = tc::sdesc(tc::smem_u32(obuf));
+    const uint64_t k_s = tc::sdesc(tc::smem_u32(kslots)), v_s = tc::sdesc(tc::smem_u32(vslots));
+    const uint64_t k_r = tc::sdesc_mn(tc::smem_u32(kslots), PT_HALF);
+    constexpr int STEP = C::SLOT / 16;
+    TcRing<2> un, dp_next, dp_now;
+    TcRing<C::KR> k_next, k_now;
+    TcRing<C::VR> vr;
+    uint32_t read_parity = 0;
+    auto form = [&](bool last) {  // scores and dp of the next tile
+      ok = ok && tc_wait_warp(&sh.k_ready[k_next.at], k_next.parity, &sh.dead);
+      if (!ok) return;
+      tc::fence_after_sync();
+      if (tc::elect_one()) {
         scores_mma<D>(t_s, qd, k_s + k_next.at * STEP);
         tc::commit(&sh.s_full);
-        k_next.step();
-        ok = tc_wait(&sh.v_full[vr.at], vr.parity, &sh.dead);
-        if (!ok) return;
-        tc::fence_after_sync();
+      }
+      k_next.step();
+      ok = tc_wait_warp(&sh.v_full[vr.at], vr.parity, &sh.dead);
+      if (!ok) return;
+      tc::fence_after_sync();
+      if (tc::elect_one()) {
         scores_mma<D>(t_dp + dp_next.at * 128, od, v_s + vr.at * STEP);
         tc::commit(&sh.dp_full[dp_next.at]);
         tc::commit(&sh.v_empty[vr.at]);
-        vr.step();
-        dp_next.step();
-      };
-      form();
+        if (last) tc::commit(&sh.q_empty);
+      }
+      vr.step();
+      dp_next.step();
+    };
+    for (uint32_t q_parity = 0;; q_parity ^= 1, un.step()) {
+      ok = tc_wait_warp(&sh.feed.full[un.at], un.parity, &sh.dead);
+      if (!ok) break;
+      const int end = __reduce_max_sync(0xffffffffu, sh.unit[un.at].len), n = __reduce_max_sync(0xffffffffu, sh.unit[un.at].n);
+      if (lane == 0) tc::bar_arrive(&sh.feed.empty[un.at]);
+      __syncwarp();
+      if (end == 0) break;
+      ok = tc_wait_warp(&sh.q_full, q_parity, &sh.dead);
+      form(n == 1);
       for (int i = 0; ok && i < n; ++i) {
-        if (i + 1 < n) {
-          ok = tc_wait(&sh.s_read, i & 1, &sh.dead);
-          if (ok) form();
-        }
-        ok = ok && tc_wait(&sh.ds_full[dp_now.at], dp_now.parity, &sh.dead);
+        ok = tc_wait_warp(&sh.s_read, read_parity, &sh.dead);
+        read_parity ^= 1;
+        if (ok && i + 1 < n) form(i + 2 == n);
+        ok = ok && tc_wait_warp(&sh.ds_full[dp_now.at], dp_now.parity, &sh.dead);
         if (!ok) break;
         tc::fence_after_sync();
-        rows_mma<D>(t_dq, t_dp + dp_now.at * 128, k_r + k_now.at * STEP, i == 0);
-        tc::commit(&sh.k_empty[k_now.at]);
+        if (tc::elect_one()) {
+          rows_mma<D>(t_dq, t_dp + dp_now.at * 128, k_r + k_now.at * STEP, i == 0);
+          tc::commit(&sh.k_empty[k_now.at]);
+          if (i + 1 == n) tc::commit(&sh.out_full);
+        }
         k_now.step();
         dp_now.step();
       }
-      if (ok) tc::commit(&sh.out_full);
-      else flag_status(a.status, KDA_DEV_TIMEOUT);
-      tc::commit(&sh.drain);
-      tc::bar_wait(&sh.drain, 0);
+      if (!ok) break;
     }
+    if (!ok && lane == 0) flag_status(a.status, KDA_DEV_TIMEOUT);
     __syncwarp();
-  } else if (warp >= 10) {
+    if (tc::elect_one()) tc::commit(&sh.drain);
+    tc::bar_wait(&sh.drain, 0);
+    __syncwarp();
+  } else if (warp >= PG_W + 2) {
     // ---- keys behind the sequence
+    fewer_registers();
+    TcRing<2> un;
     TcRing<C::KR> kr;
     bool ok = true;
-    for (int i = 0; i < n; ++i, kr.step()) {
-      ok = tc_wait(&sh.k_full[kr.at], kr.parity, &sh.dead);
-      ok = __all_sync(0xffffffffu, ok);
+    for (;; un.step()) {
+      ok = tc_wait_warp(&sh.feed.full[un.at], un.parity, &sh.dead);
       if (!ok) break;
-      const int left = b.len - (lo + i) * PT_B;
-      if (left < PT_B) clear_behind<D>(kslots + kr.at * C::SLOT, left, tid - 320);
+      const PgQueriesUnit u = sh.unit[un.at];
       __syncwarp();
-      if (lane == 0) tc::bar_arrive(&sh.k_ready[kr.at]);
+      if (lane == 0) tc::bar_arrive(&sh.feed.empty[un.at]);
+      if (u.len == 0) break;
+      for (int i = 0; i < u.n; ++i, kr.step()) {
+        ok = tc_wait_warp(&sh.k_full[kr.at], kr.parity, &sh.dead);
+        if (!ok) break;
+        const int left = u.len - (u.lo + i) * PT_B;
+        if (left < PT_B) clear_behind<D>(kslots + kr.at * C::SLOT, left, tid - PG_SOFT - 64);
+        __syncwarp();
+        if (lane == 0) tc::bar_arrive(&sh.k_ready[kr.at]);
+      }
+      if (!ok) break;
     }
     if (!ok && lane == 0) flag_status(a.status, KDA_DEV_TIMEOUT);
   } else {
-    // ---- arithmetic: thread = query, and 64 of a tile's keys
-    const int half = warp >> 2, row = b.row0 + (tid & 127);
-    const bool mine = row - b.row0 < rows;
-    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16, own_s = t_s + half * 64 + lanes;
-    const float cap2 = a.softcap * PA_LOG2E, factor = a.scale * (CAP ? 2.f * PA_LOG2E / a.softcap : PA_LOG2E);
-    const float2 stat = mine ? __ldg(stats + (int64_t)h * a.T + b.t0 + row) : make_float2(0.f, 0.f);
-    const float2 minus_lse = both(-stat.x), minus_d = both(-stat.y);
+    // ---- arithmetic: thread = query, and PG_COLS of a tile's keys
+    more_registers();
+    const int part = warp >> 2;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16, t_s = tmem, t_dp = tmem + 128, t_dq = tmem + 384;
+    const uint32_t own_s = t_s + part * PG_COLS + lanes;
+    const float cap2 = a.softcap * PA_LOG2E, factor = a.scale * (CAP ? 2.f * PA_LOG2E / a.softcap : PA_LOG2E), over_cap2 = 1.f / cap2;
     bool ok = true;
-    TcRing<2> buf;
-    for (int i = 0; i < n; ++i, buf.step()) {
-      const int k0 = (lo + i) * PT_B, first = k0 + half * 64;
-      const bool masked = k0 + PT_B - 1 > b.row0 || k0 <= b.row0 + PT_B - 1 - window;
-      // of the 64 the row sees keys from .. to - 1; a row behind the sequence none
-      const int to = !masked ? 64 : mine ? row + 1 - first : 0, from = masked && row - first >= window ? row - first - window + 1 : 0;
-      ok = ok && tc_wait(&sh.s_full, i & 1, &sh.dead);
-      ok = __all_sync(0xffffffffu, ok);
+    TcRing<2> un, buf;
+    uint32_t s_parity = 0, out_parity = 0;
+    int rows_done = 0;
+    for (;; un.step()) {
+      ok = tc_wait_warp(&sh.feed.full[un.at], un.parity, &sh.dead);
       if (!ok) break;
-      tc::fence_after_sync();
-      float2 x[32];
-      tc::tmem_ld64(own_s, reinterpret_cast<float*>(x));
-      tc::fence_before_sync();
+      const PgQueriesUnit u = sh.unit[un.at];
       __syncwarp();
-      if (lane == 0) tc::bar_arrive(&sh.s_read);
-      if constexpr (CAP) pt_cap(x, factor, cap2);
+      if (lane == 0) tc::bar_arrive(&sh.feed.empty[un.at]);
+      if (u.len == 0) break;
+      const int row = u.row0 + (tid & 127);
+      const bool mine = row < u.len;
+      const float2 stat = mine ? __ldg(stats + (int64_t)u.h * a.T + u.t0 + row) : make_float2(0.f, 0.f);
+      const float2 minus_lse = both(-stat.x), minus_d = both(-stat.y);
+      for (int i = 0; i < u.n; ++i, buf.step()) {
+        const int k0 = (u.lo + i) * PT_B, first = k0 + part * PG_COLS;
+        const bool masked = k0 + PT_B - 1 > u.row0 || k0 <= u.row0 + PT_B - 1 - window;
+        // of the thread's keys the row sees from .. to - 1; a row behind the sequence none
+        const int to = mine ? row + 1 - first : 0, from = row - first >= window ? row - first - window + 1 : 0;
+        ok = tc_wait_warp(&sh.s_full, s_parity, &sh.dead);
+        if (!ok) break;
+        s_parity ^= 1;
+        tc::fence_after_sync();
+        float2 x[PG_COLS / 2];
+        ld_columns(own_s, x);
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::bar_arrive(&sh.s_read);
+        if constexpr (CAP) pt_cap(x, factor, cap2);
 #pragma unroll
-      for (int at = 0; at < 32; ++at) {
-        float2 p = CAP ? add2(x[at], minus_lse) : fma2(x[at], both(factor), minus_lse);
-        p = make_float2(ex2(p.x), ex2(p.y));
-        if constexpr (CAP) {
-          const float2 y = mul2(x[at], both(1.f / cap2));
-          p = mul2(p, fma2(mul2(y, both(-1.f)), y, both(1.f)));
+        for (int j = 0; j < PG_COLS / 2; ++j) {
+          float2 p = CAP ? add2(x[j], minus_lse) : fma2(x[j], both(factor), minus_lse);
+          p = make_float2(ex2(p.x), ex2(p.y));
+          x[j] = CAP ? mul2(p, cap_slope(x[j], over_cap2)) : p;
         }
-        x[at] = p;
-      }
-      ok = tc_wait(&sh.dp_full[buf.at], buf.parity, &sh.dead);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      tc::fence_after_sync();
-      const uint32_t own_dp = t_dp + buf.at * 128 + half * 64 + lanes;
-      float2 dp[32];
-      tc::tmem_ld64(own_dp, reinterpret_cast<float*>(dp));
+        ok = tc_wait_warp(&sh.dp_full[buf.at], buf.parity, &sh.dead);
+        if (!ok) break;
+        tc::fence_after_sync();
+        const uint32_t own_dp = t_dp + buf.at * 128 + part * PG_COLS + lanes;
+        float2 dp[PG_COLS / 2];
+        ld_columns(own_dp, dp);
+        auto slopes = [&](auto some) {
+          uint32_t w[PG_COLS / 2];
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t w[16];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const int at = 16 * c + j;
-          float2 ds = mul2(x[at], add2(dp[at], minus_d));
-          if (masked) {
-            if (2 * at < from || 2 * at >= to) ds.x = 0.f;
-            if (2 * at + 1 < from || 2 * at + 1 >= to) ds.y = 0.f;
+          for (int j = 0; j < PG_COLS / 2; ++j) {
+            float2 ds = mul2(x[j], add2(dp[j], minus_d));
+            if (decltype(some)::value) ds = only(ds, 2 * j, from, to);
+            w[j] = pack_bf16(ds.x, ds.y);
           }
-          w[j] = pack_bf16(ds.x, ds.y);
-        }
-        tc::tmem_st16(own_dp + 16 * c, w);
+          st_columns(own_dp, w);
+        };
+        if (masked) slopes(Yes());
+        else slopes(No());
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::bar_arrive(&sh.ds_full[buf.at]);
       }
-      tc::tmem_wait_st();
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) tc::bar_arrive(&sh.ds_full[buf.at]);
-    }
-    ok = ok && tc_wait(&sh.out_full, 0, &sh.dead);
-    ok = __all_sync(0xffffffffu, ok);
-    tc::fence_after_sync();
-    if (ok && half == 0) {
-      store_rows<D>(g.dq, g.bf16, (b.t0 + (int64_t)row) * g.dq_stride + (int64_t)h * a.d, t_dq + lanes, a.scale, a.d, mine);
-      if (tid == 0) add_work(a.status, rows);
+      if (!ok) break;
+      ok = tc_wait_warp(&sh.out_full, out_parity, &sh.dead);
+      if (!ok) break;
+      out_parity ^= 1;
+      tc::fence_after_sync();
+      constexpr int N = D / PG_GROUPS;
+      store_rows<N>(g.dq, g.bf16, (u.t0 + (int64_t)row) * g.dq_stride + (int64_t)u.h * a.d, t_dq + lanes, part * N, a.scale, a.d, mine);
+      rows_done += min(PT_B, u.len - u.row0);
     }
     if (!ok && lane == 0) flag_status(a.status, KDA_DEV_TIMEOUT);
+    if (tid == 0) add_work(a.status, rows_done);
   }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  if (warp == 8) tc::tmem_dealloc(tmem, PT_TMEM);
+  if (warp == PG_W) tc::tmem_dealloc(tmem, PT_TMEM);
 }
 
 // dv and dk of a block's keys: the parts' sum, in order.  A thread has 4 channels of a row.
@@ -635,13 +830,13 @@ cudaError_t grad_launch(const PromptAttnArgs& a, const PromptGradArgs& g, const 
     return cudaErrorInvalidValue;
   const int64_t places = pf_places(a.T, a.N, PT_B);
   if (places * a.Hq > 0x7fffffff) return cudaErrorInvalidValue;
-  e = launch_pdl(keys, dim3((unsigned)(places * a.Hkv * nparts)), dim3(PT_NT), pg_keys_smem<D>(), s, maps, a, g, stats, parts, nparts);
+  e = launch_pdl(keys, dim3((unsigned)(places * a.Hkv * nparts)), dim3(PG_NT), pg_keys_smem<D>(), s, maps, a, g, stats, parts, nparts, places);
   if (e != cudaSuccess) return e;
   if (nparts > 1) {
     e = launch_pdl(pg_join_kernel, dim3((unsigned)places, 2 * a.Hkv), dim3(256), 0, s, a, g, parts, nparts);
     if (e != cudaSuccess) return e;
   }
-  return launch_pdl(queries, dim3((unsigned)(places * a.Hq)), dim3(PT_NT), pg_queries_smem<D>(), s, maps, a, g, stats, places);
+  return launch_pdl(queries, dim3((unsigned)(places * a.Hq)), dim3(PG_NT), pg_queries_smem<D>(), s, maps, a, g, stats, places);
 }
 
 }  // namespace
