@@ -541,7 +541,9 @@ __global__ void __launch_bounds__(PG_NT, 1)
   if (tid == PG_SOFT + 32)
     tc::prefetch_map(&maps.q), tc::prefetch_map(&maps.k), tc::prefetch_map(&maps.v), tc::prefetch_map(&maps.d_out);
   if (warp == PG_W) tc::tmem_alloc(&sh.tmem, PT_TMEM);
-  pdl_begin();
+  // No wait for the kernel before, the keys': nothing of it is read here.  That one's blocks let this start only when each had
+  // waited for the statistics itself, and the statistics are read past L1.
+  tc::pdl_launch_dependents();
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -728,7 +730,7 @@ __global__ void __launch_bounds__(PG_NT, 1)
       if (u.len == 0) break;
       const int row = u.row0 + (tid & 127);
       const bool mine = row < u.len;
-      const float2 stat = mine ? __ldg(stats + (int64_t)u.h * a.T + u.t0 + row) : make_float2(0.f, 0.f);
+      const float2 stat = mine ? __ldcg(stats + (int64_t)u.h * a.T + u.t0 + row) : make_float2(0.f, 0.f);
       const float2 minus_lse = both(-stat.x), minus_d = both(-stat.y);
       for (int i = 0; i < u.n; ++i, buf.step()) {
         const int k0 = (u.lo + i) * PT_B, first = k0 + part * PG_COLS;
@@ -789,6 +791,7 @@ __global__ void __launch_bounds__(PG_NT, 1)
   __syncthreads();
   tc::fence_after_sync();
   if (warp == PG_W) tc::tmem_dealloc(tmem, PT_TMEM);
+  tc::pdl_wait();  // what comes after this kernel comes after the keys' too
 }
 
 // dv and dk of a block's keys: the parts' sum, in order.  A thread has 4 channels of a row.
@@ -832,11 +835,9 @@ cudaError_t grad_launch(const PromptAttnArgs& a, const PromptGradArgs& g, const 
   if (places * a.Hq > 0x7fffffff) return cudaErrorInvalidValue;
   e = launch_pdl(keys, dim3((unsigned)(places * a.Hkv * nparts)), dim3(PG_NT), pg_keys_smem<D>(), s, maps, a, g, stats, parts, nparts, places);
   if (e != cudaSuccess) return e;
-  if (nparts > 1) {
-    e = launch_pdl(pg_join_kernel, dim3((unsigned)places, 2 * a.Hkv), dim3(256), 0, s, a, g, parts, nparts);
-    if (e != cudaSuccess) return e;
-  }
-  return launch_pdl(queries, dim3((unsigned)(places * a.Hq)), dim3(PG_NT), pg_queries_smem<D>(), s, maps, a, g, stats, places);
+  e = launch_pdl(queries, dim3((unsigned)(places * a.Hq)), dim3(PG_NT), pg_queries_smem<D>(), s, maps, a, g, stats, places);
+  if (e != cudaSuccess || nparts == 1) return e;
+  return launch_pdl(pg_join_kernel, dim3((unsigned)places, 2 * a.Hkv), dim3(256), 0, s, a, g, parts, nparts);
 }
 
 }  // namespace
