@@ -69,6 +69,10 @@ struct PfRanks {
         if (!(c0 < 0 || c1 < c0 || c1 > a.T || c1 - c0 > a.max_seqlen)) t0[r] = c0, len[r] = c1 - c0;
       }
     }
+    int most = 1;
+#pragma unroll
+    for (int r = 0; r < PF_RANKED; ++r) most = max(most, blocks(r));
+    level = __reduce_max_sync(0xffffffffu, most) - 1, above = 0;
   }
   __device__ __forceinline__ int blocks(int r) const { return (int)(((unsigned)len[r] + (1u << SHIFT) - 1) >> SHIFT); }
   __device__ __forceinline__ int64_t count(int level, int N) const {  // below 2^31 / 128 + N
@@ -78,21 +82,25 @@ struct PfRanks {
       if (32 * r < N) n += max(0, blocks(r) - level);
     return __reduce_add_sync(0xffffffffu, n);
   }
-  // level: the block's distance from the sequence's start (its number) in `from_start` order; the caller may count from the end.
-  __device__ __forceinline__ PfBlock find(int64_t rank, int N, int& level) const {
+  // Ranks are asked for in ascending order, so the search starts at the level that the last one found: steps that double, then halve.
+  int level, above;  // above = count(level + 1)
+  __device__ __forceinline__ PfBlock find(int64_t rank, int N) {
     PfBlock b{0, 0, 0};
-    int lo = 0, hi = 1;
-#pragma unroll
-    for (int r = 0; r < PF_RANKED; ++r) hi = max(hi, blocks(r));
-    hi = __reduce_max_sync(0xffffffffu, hi);
-    if (count(0, N) <= rank) return b;
+    int hi = level + 1, lo = level, step = 1, n_hi = above, n;
+    while ((n = (int)count(lo, N)) <= rank) {
+      if (lo == 0) return b;
+      hi = lo, n_hi = n;
+      lo = max(0, lo - step);
+      step *= 2;
+    }
     while (hi - lo > 1) {  // count(lo) > rank >= count(hi)
       const int mid = (lo + hi) >> 1;
-      if (count(mid, N) > rank) lo = mid;
-      else hi = mid;
+      n = (int)count(mid, N);
+      if (n > rank) lo = mid;
+      else hi = mid, n_hi = n;
     }
-    int k = (int)(rank - count(lo + 1, N));
-    level = lo;
+    level = lo, above = n_hi;
+    int k = (int)(rank - n_hi);
     bool found = false;
 #pragma unroll
     for (int r = 0; r < PF_RANKED; ++r) {
@@ -114,11 +122,10 @@ struct PfRanks {
 };
 // Block number `rank`, the longest rows first (the farthest from their sequence's start), or, `reversed`, the farthest from its end.
 template <int SHIFT>
-__device__ __forceinline__ PfBlock pf_ranked(const PromptAttnArgs& a, const PfRanks<SHIFT>& ranks, int64_t rank, int64_t places, bool reversed) {
+__device__ __forceinline__ PfBlock pf_ranked(const PromptAttnArgs& a, PfRanks<SHIFT>& ranks, int64_t rank, int64_t places, bool reversed) {
   if (!PfRanks<SHIFT>::serves(a.N)) return pf_block<SHIFT>(a, reversed ? rank : places - 1 - rank);
-  int level = 0;
-  PfBlock b = ranks.find(rank, a.N, level);
-  if (b.len > 0) b.row0 = (reversed ? (int)(((unsigned)b.len + (1u << SHIFT) - 1) >> SHIFT) - 1 - level : level) << SHIFT;
+  PfBlock b = ranks.find(rank, a.N);
+  if (b.len > 0) b.row0 = (reversed ? (int)(((unsigned)b.len + (1u << SHIFT) - 1) >> SHIFT) - 1 - ranks.level : ranks.level) << SHIFT;
   return b;
 }
 

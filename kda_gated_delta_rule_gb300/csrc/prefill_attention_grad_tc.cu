@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(PG_NT, 1)
   if (warp == PG_W + 1) {
     // ---- units, and their loads
     fewer_registers();
-    const PfRanks<7> ranks(a);
+    PfRanks<7> ranks(a);
     bool ok = true, more = true;
     int sent_q = 0, sent_o = 0, units = 0, id = blockIdx.x;
     TcRing<2> un;
@@ -552,7 +552,7 @@ __global__ void __launch_bounds__(PG_NT, 1)
   if (warp == PG_W + 1) {
     // ---- units, and their loads
     fewer_registers();
-    const PfRanks<7> ranks(a);
+    PfRanks<7> ranks(a);
     bool ok = true, more = true;
     int sent_k = 0, sent_v = 0, units = 0, id = blockIdx.x;
     TcRing<2> un;

@@ -62,7 +62,7 @@ constexpr int pt_smem() {
 static_assert(pt_smem<128>() <= 227 * 1024, "shared memory of one SM");
 
 template <bool BY_HEADS>
-__device__ __forceinline__ PtUnit pt_unit(const PromptAttnArgs& a, const PfRanks<BY_HEADS ? 7 : 8>& ranks, int64_t places, int pairs, int id,
+__device__ __forceinline__ PtUnit pt_unit(const PromptAttnArgs& a, PfRanks<BY_HEADS ? 7 : 8>& ranks, int64_t places, int pairs, int id,
                                           int window) {
   const int pair = id % pairs;
   const PfBlock b = pf_ranked(a, ranks, id / pairs, places, false);
@@ -92,30 +92,54 @@ template <int D>
 __device__ __forceinline__ bool pt_clean(unsigned char* tile, int keys, int t) {
   constexpr int N = PT_B * 8 * (D / 64);  // pieces of 16 bytes: eight lie in a row's 128 bytes, in some order
   bool odd = false;
+  uint4* pieces = reinterpret_cast<uint4*>(tile);
 #pragma unroll 1
   for (int i0 = t; i0 < N; i0 += 64 * 8) {
-    uint4 x[8];
-#pragma unroll
-    for (int n = 0; n < 8; ++n) x[n] = *(reinterpret_cast<uint4*>(tile) + i0 + 64 * n);
+    uint32_t carry[8], any = 0;
 #pragma unroll
     for (int n = 0; n < 8; ++n) {
-      uint4* at = reinterpret_cast<uint4*>(tile) + i0 + 64 * n;
-      const int row = ((i0 + 64 * n) >> 3) & (PT_B - 1);
+      const uint4 x = pieces[i0 + 64 * n];
       // an exponent of all ones carries into the next bit
-      const uint32_t carry = ((x[n].x & 0x7f807f80u) + 0x00800080u) | ((x[n].y & 0x7f807f80u) + 0x00800080u) |
-                             ((x[n].z & 0x7f807f80u) + 0x00800080u) | ((x[n].w & 0x7f807f80u) + 0x00800080u);
-      if (row >= keys) {
-        *at = make_uint4(0, 0, 0, 0);
-      } else if (carry & 0x80008000u) {
-        odd = true;
-        uint16_t* e = reinterpret_cast<uint16_t*>(at);
-        for (int c = 0; c < 8; ++c)
-          if ((e[c] & 0x7f80) == 0x7f80) e[c] = 0;
+      carry[n] = ((x.x & 0x7f807f80u) + 0x00800080u) | ((x.y & 0x7f807f80u) + 0x00800080u) | ((x.z & 0x7f807f80u) + 0x00800080u) |
+                 ((x.w & 0x7f807f80u) + 0x00800080u);
+      if ((((i0 + 64 * n) >> 3) & (PT_B - 1)) >= keys) carry[n] = 0x80008000u;
+      any |= carry[n];
+    }
+    if (!(any & 0x80008000u)) continue;
+#pragma unroll 1
+    for (int n = 0; n < 8; ++n) {
+      const bool behind = (((i0 + 64 * n) >> 3) & (PT_B - 1)) >= keys;
+      uint32_t* w = reinterpret_cast<uint32_t*>(pieces + i0 + 64 * n);
+      for (int c = 0; c < 4; ++c) {
+        const uint32_t x = w[c], low = (x & 0x7f80u) == 0x7f80u, high = (x & 0x7f800000u) == 0x7f800000u;
+        if (behind) w[c] = 0;
+        else if (low || high) odd = true, w[c] = (low ? 0u : x & 0xffffu) | (high ? 0u : x & 0xffff0000u);
       }
     }
   }
   tc::fence_proxy_async();
   return odd;
+}
+
+// Which of 32 keys, from number `first` on, a row sees that sees from .. to - 1.
+__device__ __forceinline__ uint32_t pt_seen(int first, int from, int to) {
+  const int n = max(0, min(32, to - first)), skip = max(0, min(32, from - first));
+  return (n < 32 ? (1u << n) - 1 : 0xffffffffu) & (skip < 32 ? 0xffffffffu << skip : 0u);
+}
+// `none` in the place of the scores of unseen keys.  A loop over 32 keys at a time: instructions that run once or twice in a unit are
+// fetched for it, and most of the four have nothing to do.
+__device__ __forceinline__ void pt_mask(uint32_t own_s, int from, int to, float none) {
+#pragma unroll 1
+  for (int c = 0; c < PT_B; c += 32) {
+    const uint32_t seen = pt_seen(c, from, to);
+    if (__all_sync(0xffffffffu, seen == 0xffffffffu)) continue;
+    float x[32];
+    tc::tmem_ld32(own_s + c, x);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] = seen >> i & 1 ? x[i] : none;
+    tc::tmem_st32f(own_s + c, x);
+  }
+  tc::tmem_wait_st();
 }
 
 // A tile's capped scores: the row's largest.  Half by half they are left in tensor memory as products where all rows of the warp see
@@ -144,10 +168,11 @@ __device__ __forceinline__ float pt_capped_top(uint32_t own_s, bool masked, int 
       uint32_t w[16];
       tc::tmem_ld16(own_s + c, reinterpret_cast<float*>(y));
       pt_cap(y, factor, cap2);
+      const uint32_t seen = masked ? pt_seen(c, from, to) : 0xffffffffu;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        if (masked && (c + 2 * i >= to || c + 2 * i < from)) y[i].x = -INFINITY;
-        if (masked && (c + 2 * i + 1 >= to || c + 2 * i + 1 < from)) y[i].y = -INFINITY;
+        y[i].x = seen >> (2 * i) & 1 ? y[i].x : -INFINITY;
+        y[i].y = seen >> (2 * i + 1) & 1 ? y[i].y : -INFINITY;
         top = fmaxf(top, fmaxf(y[i].x, y[i].y));
         w[2 * i] = __float_as_uint(y[i].x), w[2 * i + 1] = __float_as_uint(y[i].y);
       }
@@ -156,6 +181,20 @@ __device__ __forceinline__ float pt_capped_top(uint32_t own_s, bool masked, int 
     tc::tmem_wait_st();  // read back below
   }
   return top;
+}
+
+// The sum of a channel's values that are no numbers, and so were left out of the tiles with unseen keys, over the keys that a row sees.
+__device__ __noinline__ float pt_odd(const PromptAttnArgs& a, const PtUnit& u, int row, int hi, int window, int channel) {
+  const bf16* v = static_cast<const bf16*>(a.v) + (int64_t)u.kv_head * a.d + channel;
+  float sum = 0.f;
+  for (int j = u.lo; j <= hi; ++j) {
+    if (!pt_masked(u, j, window)) continue;
+    for (int k = max(j * PT_B, row >= window ? row - window + 1 : 0); k <= min(j * PT_B + PT_B - 1, row); ++k) {
+      const float x = to_f32(v[(int64_t)(u.t0 + k) * a.v_stride]);
+      if (!(fabsf(x) <= 3.4e38f)) sum += x;
+    }
+  }
+  return sum;
 }
 
 template <int D, bool CAP, bool BY_HEADS>
@@ -194,7 +233,7 @@ __global__ void __launch_bounds__(PT_NT, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     if (warp == 9) {
       // ---- units, and their loads
-      const PfRanks<BY_HEADS ? 7 : 8> ranks(a);
+      PfRanks<BY_HEADS ? 7 : 8> ranks(a);
       bool ok = true, more = true;
       int sent_k = 0, sent_v = 0, units = 0, id = blockIdx.x;
       TcRing<2> un;
@@ -411,17 +450,11 @@ __global__ void __launch_bounds__(PT_NT, 1)
         if constexpr (CAP) {
           top = pt_capped_top(own_s, masked, from, to, factor, cap2, nearer, products);
         } else {
+          if (masked) pt_mask(own_s, from, to, negative ? INFINITY : -INFINITY);
           tc::tmem_ld128(own_s, reinterpret_cast<float*>(x));
           if (negative) {
 #pragma unroll
             for (int i = 0; i < PT_B / 2; ++i) x[i] = make_float2(-x[i].x, -x[i].y);
-          }
-          if (masked) {
-#pragma unroll
-            for (int i = 0; i < PT_B / 2; ++i) {
-              if (2 * i >= to || 2 * i < from) x[i].x = -INFINITY;
-              if (2 * i + 1 >= to || 2 * i + 1 < from) x[i].y = -INFINITY;
-            }
           }
           float t[4];
 #pragma unroll
@@ -496,20 +529,8 @@ __global__ void __launch_bounds__(PT_NT, 1)
         tc::fence_after_sync();
         const bool mine = row - row0 < u.rows[s], odd = *const_cast<volatile int*>(&sh.odd_v[un.at]) != 0;
         const int64_t t = u.t0 + row;
-        const float by = 1.f / l;
-        const bf16* v = static_cast<const bf16*>(a.v) + (int64_t)u.kv_head * a.d;
-        // values that are no numbers were left out of the tiles with unseen keys
-        auto add_odd = [&](int c, float (&o)[32]) {
-          for (int j = u.lo; j <= hi; ++j) {
-            if (!pt_masked(u, j, window)) continue;
-            for (int k = max(j * PT_B, row >= window ? row - window + 1 : 0); k <= min(j * PT_B + PT_B - 1, row); ++k)
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const float x = c + i < a.d ? to_f32(v[(int64_t)(u.t0 + k) * a.v_stride + c + i]) : 0.f;
-                if (!(fabsf(x) <= 3.4e38f)) o[i] += x;
-              }
-          }
-        };
+        float by;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(by) : "f"(l));  // to 2^-23
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           float o[32];
@@ -517,7 +538,11 @@ __global__ void __launch_bounds__(PT_NT, 1)
           if (mine && c < a.d) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] *= by;
-            if (odd) add_odd(c, o);
+            if (odd) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (c + i < a.d) o[i] += pt_odd(a, u, row, hi, window, c + i);
+            }
             pt_store32(a.out, a.out_bf16, t * a.out_stride + (int64_t)u.head[s] * a.d + c, o, a.d - c);
           }
           __syncwarp();  // the next load is the whole warp's
