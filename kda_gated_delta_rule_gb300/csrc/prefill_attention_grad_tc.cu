@@ -115,19 +115,17 @@ __device__ __forceinline__ void rows_mma(uint32_t to, uint32_t a, uint64_t b, bo
                !(first && kk == 0));
 }
 
-// N channels from c0 on of a row of a block's result in tensor memory, times `by`.
+// Channels c0 .. c0 + N - 1 of a warp's 32 rows of a block's result in tensor memory, times `by`; `at`: the first row's first channel.
 template <int N>
-__device__ __forceinline__ void store_rows(void* base, bool is_bf16, int64_t at, uint32_t from, int c0, float by, int d, bool mine) {
+__device__ __forceinline__ void store_rows(void* base, bool is_bf16, int64_t at, int64_t stride, int rows, uint32_t from, int c0, float by, int d) {
+  static_assert(N % 32 == 0, "32 at a time");
 #pragma unroll 1
-  for (int c = c0; c < c0 + N; c += 16) {
-    float o[16];
-    tc::tmem_ld16(from + c, o);
-    if (mine && c < d) {
+  for (int c = c0; c < min(c0 + N, d); c += 32) {
+    float o[32];
+    tc::tmem_ld32(from + c, o);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) o[i] *= by;
-      pt_store16(base, is_bf16, at + c, o);
-    }
-    __syncwarp();  // the next load is the whole warp's
+    for (int i = 0; i < 32; ++i) o[i] *= by;
+    pt_store32(base, is_bf16, at + c, stride, rows, d - c, o);
   }
 }
 
@@ -496,15 +494,16 @@ __global__ void __launch_bounds__(PG_NT, 1)
       // the first half of the parts has dv, the second dk, each its channels
       constexpr int N = D * 2 / PG_GROUPS;
       const int of_k = part / (PG_GROUPS / 2), c0 = part % (PG_GROUPS / 2) * N;
-      const bool mine = key < u.len;
-      const int64_t t = u.t0 + key;
+      const int warp_row = (warp & 3) * 32, rows = u.len - u.k0 - warp_row;  // of the sequence, from the warp's first on
+      const int64_t t = u.t0 + u.k0 + warp_row;
       const uint32_t from = (of_k ? t_dk : t_dv) + lanes;
       const float by = of_k ? a.scale : 1.f;
       if (nparts > 1) {
         float* to = parts + (int64_t)(u.part * 2 + of_k) * a.T * a.Hkv * a.d;
-        store_rows<N>(to, false, (t * a.Hkv + u.kh) * a.d, from, c0, by, a.d, mine);
+        store_rows<N>(to, false, (t * a.Hkv + u.kh) * a.d, (int64_t)a.Hkv * a.d, rows, from, c0, by, a.d);
       } else {
-        store_rows<N>(of_k ? g.dk : g.dv, g.bf16, t * (of_k ? g.dk_stride : g.dv_stride) + (int64_t)u.kh * a.d, from, c0, by, a.d, mine);
+        const int64_t stride = of_k ? g.dk_stride : g.dv_stride;
+        store_rows<N>(of_k ? g.dk : g.dv, g.bf16, t * stride + (int64_t)u.kh * a.d, stride, rows, from, c0, by, a.d);
       }
     }
     if (!ok && lane == 0) flag_status(a.status, KDA_DEV_TIMEOUT);
@@ -780,8 +779,11 @@ __global__ void __launch_bounds__(PG_NT, 1)
       if (!ok) break;
       out_parity ^= 1;
       tc::fence_after_sync();
-      constexpr int N = D / PG_GROUPS;
-      store_rows<N>(g.dq, g.bf16, (u.t0 + (int64_t)row) * g.dq_stride + (int64_t)u.h * a.d, t_dq + lanes, part * N, a.scale, a.d, mine);
+      constexpr int N = D / PG_GROUPS < 32 ? 32 : D / PG_GROUPS;
+      const int warp_row = (warp & 3) * 32;
+      if (part * N < D)
+        store_rows<N>(g.dq, g.bf16, (u.t0 + (int64_t)u.row0 + warp_row) * g.dq_stride + (int64_t)u.h * a.d, g.dq_stride,
+                      u.len - u.row0 - warp_row, t_dq + lanes, part * N, a.scale, a.d);
       rows_done += min(PT_B, u.len - u.row0);
     }
     if (!ok && lane == 0) flag_status(a.status, KDA_DEV_TIMEOUT);

@@ -528,30 +528,32 @@ __global__ void __launch_bounds__(PT_NT, 1)
         o_parity ^= 1;
         tc::fence_after_sync();
         const bool mine = row - row0 < u.rows[s], odd = *const_cast<volatile int*>(&sh.odd_v[un.at]) != 0;
-        const int64_t t = u.t0 + row;
+        __syncwarp();
+        if (lane == 0) tc::bar_arrive(&sh.feed.empty[un.at]);  // before the stores, which an arrival behind them would wait for
         float by;
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(by) : "f"(l));  // to 2^-23
+        const int warp_row = (warp & 3) * 32;
+        const int64_t at = (int64_t)(u.t0 + row0 + warp_row) * a.out_stride + (int64_t)u.head[s] * a.d;
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
+        for (int c = 0; c < a.d; c += 32) {
           float o[32];
           tc::tmem_ld32(own_o + c, o);
-          if (mine && c < a.d) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] *= by;
-            if (odd) {
+          for (int i = 0; i < 32; ++i) o[i] *= by;
+          if (odd && mine) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (c + i < a.d) o[i] += pt_odd(a, u, row, hi, window, c + i);
-            }
-            pt_store32(a.out, a.out_bf16, t * a.out_stride + (int64_t)u.head[s] * a.d + c, o, a.d - c);
+            for (int i = 0; i < 32; ++i)
+              if (c + i < a.d) o[i] += pt_odd(a, u, row, hi, window, c + i);
           }
-          __syncwarp();  // the next load is the whole warp's
+          __syncwarp();
+          pt_store32(a.out, a.out_bf16, at + c, a.out_stride, u.rows[s] - warp_row, a.d - c, o);
         }
-        if (mine && a.lse) a.lse[t * a.Hq + u.head[s]] = (m + log2f(l)) * PA_LN2;
+        if (mine && a.lse) a.lse[(int64_t)(u.t0 + row) * a.Hq + u.head[s]] = (m + log2f(l)) * PA_LN2;
         rows_done += u.rows[s];
+      } else if (lane == 0) {
+        tc::bar_arrive(&sh.feed.empty[un.at]);
       }
       __syncwarp();
-      if (lane == 0) tc::bar_arrive(&sh.feed.empty[un.at]);
     }
     if (!ok && lane == 0) flag_status(a.status, KDA_DEV_TIMEOUT);
     if ((tid & 127) == 0) add_work(a.status, rows_done);

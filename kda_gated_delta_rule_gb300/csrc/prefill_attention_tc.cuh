@@ -60,23 +60,51 @@ struct PtFeed {
   }
 };
 
-// 16 results of a row, from channel c on.
-__device__ __forceinline__ void pt_store16(void* base, bool is_bf16, int64_t at, const float (&o)[16]) {
-  if (is_bf16) {
-    uint4* y = reinterpret_cast<uint4*>(static_cast<bf16*>(base) + at);
-    y[0] = make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]), pack_bf16(o[6], o[7]));
-    y[1] = make_uint4(pack_bf16(o[8], o[9]), pack_bf16(o[10], o[11]), pack_bf16(o[12], o[13]), pack_bf16(o[14], o[15]));
-  } else {
-    float4* y = reinterpret_cast<float4*>(static_cast<float*>(base) + at);
+// 64 bytes of each of a warp's 32 rows, of which the lane has one row's in w: lanes exchange pieces in fours, so that a store's
+// lanes have 64 bytes of eight rows instead of 16 of 32 (a store takes time by the 128-byte lines that it touches: with one row a
+// lane the ends of a unit's 256 rows of 64 channels took 2000 cycles of it).  `to`: the first row's place; `rows`, `bytes`: how
+// many of the 32 and of the 64 there are.  The whole warp calls.
+__device__ __forceinline__ void pt_store64(char* to, int64_t row_bytes, int rows, int bytes, uint32_t (&w)[16]) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+  for (int b = 1; b < 4; b <<= 1) {
+    const bool odd = (lane & b) != 0;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      if (c & b) continue;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t &low = w[4 * c + i], &high = w[4 * (c | b) + i];
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? low : high, b);
+        if (odd) low = got;
+        else high = got;
+      }
+    }
   }
+  // now w[4 i ..] is piece lane % 4 of row i of the lane's four
+  const int row = lane & ~3, at = (lane & 3) * 16;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (row + i < rows && at < bytes)
+      *reinterpret_cast<uint4*>(to + (row + i) * row_bytes + at) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
 }
 
-// The same with 32, of which there are `left` (a multiple of 16).
-__device__ __forceinline__ void pt_store32(void* base, bool is_bf16, int64_t at, const float (&o)[32], int left) {
-  pt_store16(base, is_bf16, at, reinterpret_cast<const float(&)[16]>(o[0]));
-  if (left > 16) pt_store16(base, is_bf16, at + 16, reinterpret_cast<const float(&)[16]>(o[16]));
+// 32 results of each of a warp's 32 rows, the first at element `at` of `base`, rows `stride` elements apart; `rows` and `left`: how many
+// rows and channels there are.
+__device__ __forceinline__ void pt_store32(void* base, bool is_bf16, int64_t at, int64_t stride, int rows, int left, const float (&o)[32]) {
+  uint32_t w[16];
+  if (is_bf16) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = pack_bf16(o[2 * i], o[2 * i + 1]);
+    pt_store64(static_cast<char*>(base) + at * 2, stride * 2, rows, left * 2, w);
+  } else {
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[16 * half + i]);
+      pt_store64(static_cast<char*>(base) + (at + 16 * half) * 4, stride * 4, rows, (left - 16 * half) * 4, w);
+    }
+  }
 }
 
 // Scores in powers of two, capped; `factor` takes a product to the cap's argument.
