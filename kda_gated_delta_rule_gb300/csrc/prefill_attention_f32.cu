@@ -29,16 +29,23 @@ struct PfShape {
   static constexpr int PLD = PB + 4;
 };
 
-// Rows 0 .. 63 of `base` (tokens `stride` apart); those from `valid` on are zeros.
+// Rows 0 .. 63 of `base` (tokens `stride` apart) on their way; those from `valid` on are zeros.
 template <int D>
 __device__ __forceinline__ void load_block(float* dst, const float* base, int64_t stride, int valid) {
   constexpr int C4 = D / 4;
+#pragma unroll 4
   for (int i = threadIdx.x; i < PB * C4; i += PNT) {
     const int r = i / C4, c = (i - r * C4) * 4;
-    const float4 x = r < valid ? __ldg(reinterpret_cast<const float4*>(base + r * stride + c)) : make_float4(0.f, 0.f, 0.f, 0.f);
-    *reinterpret_cast<float4*>(dst + r * PfShape<D>::LD + c) = x;
+    const bool there = r < valid;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst + r * PfShape<D>::LD + c)),
+                 "l"(base + (there ? r : 0) * stride + c), "r"(there ? 16 : 0)
+                 : "memory");
   }
 }
+__device__ __forceinline__ void loads_sent() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// all but the last `N` groups of this thread's loads are there
+template <int N>
+__device__ __forceinline__ void loads_there() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 // s[i][j] = row (ty + 16 i) of a times row (tx + 16 j) of b
 template <int D>
@@ -91,6 +98,20 @@ __device__ __forceinline__ void ld_channels(const float* row, float (&v)[PfShape
   }
 }
 
+// acc += p v, two channels at once
+template <int N>
+__device__ __forceinline__ void axpy(float (&acc)[N], float p, const float (&v)[N]) {
+  if constexpr (N >= 2) {
+#pragma unroll
+    for (int c = 0; c < N; c += 2) {
+      const float2 r = fma2(both(p), make_float2(v[c], v[c + 1]), make_float2(acc[c], acc[c + 1]));
+      acc[c] = r.x, acc[c + 1] = r.y;
+    }
+  } else {
+    acc[0] = fmaf(p, v[0], acc[0]);
+  }
+}
+
 // acc[i] += sum_j w(i, j) row_j over 4 rows of b at j0, w given per output row
 template <int D>
 __device__ __forceinline__ void add_rows(float (&acc)[4][PfShape<D>::CPT], const float4 (&w)[4], const float* b) {
@@ -102,15 +123,7 @@ __device__ __forceinline__ void add_rows(float (&acc)[4][PfShape<D>::CPT], const
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float p = j == 0 ? w[i].x : j == 1 ? w[i].y : j == 2 ? w[i].z : w[i].w;
-      if constexpr (CPT >= 2) {
-#pragma unroll
-        for (int c = 0; c < CPT; c += 2) {
-          const float2 r = fma2(both(p), make_float2(v[c], v[c + 1]), make_float2(acc[i][c], acc[i][c + 1]));
-          acc[i][c] = r.x, acc[i][c + 1] = r.y;
-        }
-      } else {
-        acc[i][0] = fmaf(p, v[0], acc[i][0]);
-      }
+      axpy(acc[i], p, v);
     }
   }
 }
@@ -152,12 +165,13 @@ template <int D>
 __global__ void __launch_bounds__(PNT) pf_f32_kernel(const PromptAttnArgs a, const int64_t places) {
   using S = PfShape<D>;
   extern __shared__ __align__(16) float sm[];
-  float *sq = sm, *sk = sq + PB * S::LD, *sv = sk + PB * S::LD, *sp = sv + PB * S::LD;
+  constexpr int BLOCK = PB * S::LD;
+  float *sq = sm, *kv = sq + BLOCK, *sp = kv + 4 * BLOCK;  // kv: two tiles of K and V
   pdl_begin();
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, h = blockIdx.y, kh = h / (a.Hq / a.Hkv);
-  if (blockIdx.x == 0 && h == 0 && tid < 32) pf_check_offsets(a);
-  // the longest rows first: a sequence's last blocks see most keys
-  const PfBlock b = pf_block<6>(a, places - 1 - blockIdx.x);
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, h = blockIdx.x % a.Hq, kh = h / (a.Hq / a.Hkv);
+  if (blockIdx.x == 0 && tid < 32) pf_check_offsets(a);
+  PfRanks<6> ranks(a);
+  const PfBlock b = pf_ranked(a, ranks, blockIdx.x / a.Hq, places, false);
   if (b.len == 0) return;
   const int rows = min(PB, b.len - b.row0), window = a.window > 0 ? a.window : 0x7fffffff;
   load_block<D>(sq, static_cast<const float*>(a.q) + (int64_t)(b.t0 + b.row0) * a.q_stride + h * D, a.q_stride, rows);
@@ -168,12 +182,20 @@ __global__ void __launch_bounds__(PNT) pf_f32_kernel(const PromptAttnArgs a, con
 #pragma unroll
     for (int c = 0; c < S::CPT; ++c) o[i][c] = 0.f;
   }
-  const int last = b.row0 + rows - 1, first = max(0, b.row0 - window + 1);
-  for (int k0 = first / PB * PB; k0 <= last; k0 += PB) {
+  const int last = b.row0 + rows - 1, first = max(0, b.row0 - window + 1) / PB * PB;
+  auto load = [&](int k0) {
+    float* to = kv + (k0 / PB & 1) * 2 * BLOCK;
     const int64_t tok = b.t0 + k0;
-    __syncthreads();
-    load_block<D>(sk, static_cast<const float*>(a.k) + tok * a.k_stride + kh * D, a.k_stride, b.len - k0);
-    load_block<D>(sv, static_cast<const float*>(a.v) + tok * a.v_stride + kh * D, a.v_stride, b.len - k0);
+    load_block<D>(to, static_cast<const float*>(a.k) + tok * a.k_stride + kh * D, a.k_stride, b.len - k0);
+    load_block<D>(to + BLOCK, static_cast<const float*>(a.v) + tok * a.v_stride + kh * D, a.v_stride, b.len - k0);
+  };
+  load(first);
+  loads_sent();
+  for (int k0 = first; k0 <= last; k0 += PB) {
+    const float *sk = kv + (k0 / PB & 1) * 2 * BLOCK, *sv = sk + BLOCK;
+    if (k0 + PB <= last) load(k0 + PB);  // over the tile before, which all have left
+    loads_sent();
+    loads_there<1>();
     __syncthreads();
     float s[4][4];
     dots<D>(sq, sk, s);
@@ -231,7 +253,7 @@ __global__ void __launch_bounds__(PNT) pf_f32_kernel(const PromptAttnArgs a, con
         }
       }
     }
-    __syncwarp();
+    __syncthreads();
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -273,17 +295,20 @@ __device__ __forceinline__ void tile_grads(const PromptAttnArgs& a, const float2
   }
 }
 
+__host__ __device__ constexpr int kv_buffers(int d) { return d == 128 ? 1 : 2; }  // of Q and dO: what shared memory holds
+
 template <int D>
 __global__ void __launch_bounds__(PNT)
     pf_f32_grad_kv_kernel(const PromptAttnArgs a, const PromptGradArgs g, const float2* __restrict__ stats, const int64_t places) {
   using S = PfShape<D>;
   extern __shared__ __align__(16) float sm[];
-  float *sk = sm, *sv = sk + PB * S::LD, *sq = sv + PB * S::LD, *sdo = sq + PB * S::LD, *sp = sdo + PB * S::LD,
-        *sds = sp + PB * S::PLD;
+  constexpr int BLOCK = PB * S::LD, BUF = kv_buffers(D);
+  float *sk = sm, *sv = sk + BLOCK, *qo = sv + BLOCK, *sp = qo + 2 * BUF * BLOCK, *sds = sp + PB * S::PLD;  // qo: Q and dO
   pdl_begin();
-  const int tid = threadIdx.x, ty = tid >> 4, kh = blockIdx.y, group = a.Hq / a.Hkv;
-  if (blockIdx.x == 0 && kh == 0 && tid < 32) pf_check_offsets(a);
-  const PfBlock b = pf_block<6>(a, blockIdx.x);
+  const int tid = threadIdx.x, ty = tid >> 4, kh = blockIdx.x % a.Hkv, group = a.Hq / a.Hkv;
+  if (blockIdx.x == 0 && tid < 32) pf_check_offsets(a);
+  PfRanks<6> ranks(a);
+  const PfBlock b = pf_ranked(a, ranks, blockIdx.x / a.Hkv, places, true);
   if (b.len == 0) return;
   const int k0 = b.row0, keys = min(PB, b.len - k0), window = a.window > 0 ? a.window : 0x7fffffff;
   const int64_t tok = b.t0 + k0;
@@ -295,35 +320,44 @@ __global__ void __launch_bounds__(PNT)
 #pragma unroll
     for (int c = 0; c < S::CPT; ++c) dk[i][c] = dv[i][c] = 0.f;
   const int64_t last = min((int64_t)b.len - 1, (int64_t)k0 + keys - 1 + window - 1);  // the last row that sees one of the keys
-  for (int h = kh * group; h < (kh + 1) * group; ++h)
-    for (int row0 = k0; row0 <= last; row0 += PB) {
-      const int64_t t = b.t0 + row0;
-      const int rows = min(PB, b.len - row0);
-      __syncthreads();
-      load_block<D>(sq, static_cast<const float*>(a.q) + t * a.q_stride + h * D, a.q_stride, rows);
-      load_block<D>(sdo, static_cast<const float*>(g.d_out) + t * g.d_out_stride + h * D, g.d_out_stride, rows);
-      __syncthreads();
-      tile_grads<D>(a, stats + h * a.T + t, sq, sk, sdo, sv, row0, k0, rows, b.len, window, sp, sds);
-      __syncthreads();
+  const int blocks = (int)(last / PB) - k0 / PB + 1, n = blocks * group;  // a round: a block of one head
+  auto load = [&](int i) {
+    const int h = kh * group + i / blocks, row0 = k0 + i % blocks * PB;
+    const int64_t t = b.t0 + row0;
+    float* to = qo + (i % BUF) * 2 * BLOCK;
+    load_block<D>(to, static_cast<const float*>(a.q) + t * a.q_stride + h * D, a.q_stride, b.len - row0);
+    load_block<D>(to + BLOCK, static_cast<const float*>(g.d_out) + t * g.d_out_stride + h * D, g.d_out_stride, b.len - row0);
+  };
+  load(0);
+  loads_sent();
+  for (int i = 0; i < n; ++i) {
+    const int h = kh * group + i / blocks, row0 = k0 + i % blocks * PB;
+    const float *sq = qo + (i % BUF) * 2 * BLOCK, *sdo = sq + BLOCK;
+    const int64_t t = b.t0 + row0;
+    if (BUF == 2 && i + 1 < n) load(i + 1);  // over the round before, which all have left
+    loads_sent();
+    loads_there<BUF - 1>();
+    __syncthreads();
+    tile_grads<D>(a, stats + h * a.T + t, sq, sk, sdo, sv, row0, k0, min(PB, b.len - row0), b.len, window, sp, sds);
+    __syncthreads();
 #pragma unroll 2
-      for (int q = 0; q < PB; q += 1) {
-        const float4 p = *reinterpret_cast<const float4*>(sp + q * S::PLD + ty * 4);
-        const float4 ds = *reinterpret_cast<const float4*>(sds + q * S::PLD + ty * 4);
-        float x[S::CPT], y[S::CPT];
-        ld_channels<D>(sdo + q * S::LD, x);
-        ld_channels<D>(sq + q * S::LD, y);
+    for (int q = 0; q < PB; ++q) {
+      const float4 p = *reinterpret_cast<const float4*>(sp + q * S::PLD + ty * 4);
+      const float4 ds = *reinterpret_cast<const float4*>(sds + q * S::PLD + ty * 4);
+      float x[S::CPT], y[S::CPT];
+      ld_channels<D>(sdo + q * S::LD, x);
+      ld_channels<D>(sq + q * S::LD, y);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float pi = i == 0 ? p.x : i == 1 ? p.y : i == 2 ? p.z : p.w;
-          const float di = i == 0 ? ds.x : i == 1 ? ds.y : i == 2 ? ds.z : ds.w;
-#pragma unroll
-          for (int c = 0; c < S::CPT; ++c) {
-            dv[i][c] = fmaf(pi, x[c], dv[i][c]);
-            dk[i][c] = fmaf(di, y[c], dk[i][c]);
-          }
-        }
+      for (int r = 0; r < 4; ++r) {
+        const float pr = r == 0 ? p.x : r == 1 ? p.y : r == 2 ? p.z : p.w;
+        const float dr = r == 0 ? ds.x : r == 1 ? ds.y : r == 2 ? ds.z : ds.w;
+        axpy(dv[r], pr, x);
+        axpy(dk[r], dr, y);
       }
     }
+    __syncthreads();
+    if (BUF == 1 && i + 1 < n) load(i + 1);
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = ty * 4 + i;
@@ -340,10 +374,12 @@ __global__ void __launch_bounds__(PNT)
     pf_f32_grad_q_kernel(const PromptAttnArgs a, const PromptGradArgs g, const float2* __restrict__ stats, const int64_t places) {
   using S = PfShape<D>;
   extern __shared__ __align__(16) float sm[];
-  float *sq = sm, *sdo = sq + PB * S::LD, *sk = sdo + PB * S::LD, *sv = sk + PB * S::LD, *sds = sv + PB * S::LD;
+  constexpr int BLOCK = PB * S::LD;
+  float *sq = sm, *sdo = sq + BLOCK, *kv = sdo + BLOCK, *sds = kv + 4 * BLOCK;
   pdl_begin();
-  const int tid = threadIdx.x, ty = tid >> 4, h = blockIdx.y, kh = h / (a.Hq / a.Hkv);
-  const PfBlock b = pf_block<6>(a, places - 1 - blockIdx.x);
+  const int tid = threadIdx.x, ty = tid >> 4, h = blockIdx.x % a.Hq, kh = h / (a.Hq / a.Hkv);
+  PfRanks<6> ranks(a);
+  const PfBlock b = pf_ranked(a, ranks, blockIdx.x / a.Hq, places, false);
   if (b.len == 0) return;
   const int rows = min(PB, b.len - b.row0), window = a.window > 0 ? a.window : 0x7fffffff;
   const int64_t t = b.t0 + b.row0;
@@ -354,12 +390,20 @@ __global__ void __launch_bounds__(PNT)
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int c = 0; c < S::CPT; ++c) dq[i][c] = 0.f;
-  const int last = b.row0 + rows - 1, first = max(0, b.row0 - window + 1);
-  for (int k0 = first / PB * PB; k0 <= last; k0 += PB) {
+  const int last = b.row0 + rows - 1, first = max(0, b.row0 - window + 1) / PB * PB;
+  auto load = [&](int k0) {
+    float* to = kv + (k0 / PB & 1) * 2 * BLOCK;
     const int64_t tok = b.t0 + k0;
-    __syncthreads();
-    load_block<D>(sk, static_cast<const float*>(a.k) + tok * a.k_stride + kh * D, a.k_stride, b.len - k0);
-    load_block<D>(sv, static_cast<const float*>(a.v) + tok * a.v_stride + kh * D, a.v_stride, b.len - k0);
+    load_block<D>(to, static_cast<const float*>(a.k) + tok * a.k_stride + kh * D, a.k_stride, b.len - k0);
+    load_block<D>(to + BLOCK, static_cast<const float*>(a.v) + tok * a.v_stride + kh * D, a.v_stride, b.len - k0);
+  };
+  load(first);
+  loads_sent();
+  for (int k0 = first; k0 <= last; k0 += PB) {
+    const float *sk = kv + (k0 / PB & 1) * 2 * BLOCK, *sv = sk + BLOCK;
+    if (k0 + PB <= last) load(k0 + PB);
+    loads_sent();
+    loads_there<1>();
     __syncthreads();
     tile_grads<D>(a, stats + h * a.T + t, sq, sk, sdo, sv, b.row0, k0, rows, b.len, window, nullptr, sds);
     __syncwarp();
@@ -370,7 +414,7 @@ __global__ void __launch_bounds__(PNT)
       for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float4*>(sds + (ty + 16 * i) * S::PLD + j);
       add_rows<D>(dq, w, sk + j * S::LD);
     }
-    __syncwarp();
+    __syncthreads();
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -386,27 +430,29 @@ __global__ void __launch_bounds__(PNT)
 template <int D>
 cudaError_t forward_launch(const PromptAttnArgs& a, cudaStream_t s) {
   using S = PfShape<D>;
-  const int smem = (3 * PB * S::LD + PB * S::PLD) * 4;
+  const int smem = (5 * PB * S::LD + PB * S::PLD) * 4;
   auto kernel = pf_f32_kernel<D>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int64_t places = pf_places(a.T, a.N, PB);
-  return launch_pdl(kernel, dim3((unsigned)places, a.Hq), dim3(PNT), smem, s, a, places);
+  if (places * a.Hq > 0x7fffffff) return cudaErrorInvalidValue;
+  return launch_pdl(kernel, dim3((unsigned)(places * a.Hq)), dim3(PNT), smem, s, a, places);
 }
 
 template <int D>
 cudaError_t grad_launch(const PromptAttnArgs& a, const PromptGradArgs& g, const float2* stats, cudaStream_t s) {
   using S = PfShape<D>;
-  const int smem_kv = (4 * PB * S::LD + 2 * PB * S::PLD) * 4, smem_q = (4 * PB * S::LD + PB * S::PLD) * 4;
+  const int smem_kv = ((2 + 2 * kv_buffers(D)) * PB * S::LD + 2 * PB * S::PLD) * 4, smem_q = (6 * PB * S::LD + PB * S::PLD) * 4;
   auto kv = pf_f32_grad_kv_kernel<D>;
   auto q = pf_f32_grad_q_kernel<D>;
   cudaError_t e = cudaFuncSetAttribute(kv, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_kv);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(q, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_q);
   if (e != cudaSuccess) return e;
   const int64_t places = pf_places(a.T, a.N, PB);
-  e = launch_pdl(kv, dim3((unsigned)places, a.Hkv), dim3(PNT), smem_kv, s, a, g, stats, places);
+  if (places * a.Hq > 0x7fffffff) return cudaErrorInvalidValue;
+  e = launch_pdl(kv, dim3((unsigned)(places * a.Hkv)), dim3(PNT), smem_kv, s, a, g, stats, places);
   if (e != cudaSuccess) return e;
-  return launch_pdl(q, dim3((unsigned)places, a.Hq), dim3(PNT), smem_q, s, a, g, stats, places);
+  return launch_pdl(q, dim3((unsigned)(places * a.Hq)), dim3(PNT), smem_q, s, a, g, stats, places);
 }
 
 }  // namespace
