@@ -93,27 +93,32 @@ __device__ __forceinline__ bool pt_clean(unsigned char* tile, int keys, int t) {
   constexpr int N = PT_B * 8 * (D / 64);  // pieces of 16 bytes: eight lie in a row's 128 bytes, in some order
   bool odd = false;
   uint4* pieces = reinterpret_cast<uint4*>(tile);
+  const int whole = max(0, min(PT_B, keys)) * 8;  // pieces of a half that are rows of the sequence
+#pragma unroll 1
+  for (int i = whole + t; i < PT_B * 8; i += 64)
+#pragma unroll
+    for (int h = 0; h < D / 64; ++h) pieces[h * PT_B * 8 + i] = make_uint4(0, 0, 0, 0);
 #pragma unroll 1
   for (int i0 = t; i0 < N; i0 += 64 * 8) {
-    uint32_t carry[8], any = 0;
+    uint32_t any = 0;
 #pragma unroll
     for (int n = 0; n < 8; ++n) {
-      const uint4 x = pieces[i0 + 64 * n];
+      const int i = i0 + 64 * n;
+      const uint4 x = pieces[i];
       // an exponent of all ones carries into the next bit
-      carry[n] = ((x.x & 0x7f807f80u) + 0x00800080u) | ((x.y & 0x7f807f80u) + 0x00800080u) | ((x.z & 0x7f807f80u) + 0x00800080u) |
-                 ((x.w & 0x7f807f80u) + 0x00800080u);
-      if ((((i0 + 64 * n) >> 3) & (PT_B - 1)) >= keys) carry[n] = 0x80008000u;
-      any |= carry[n];
+      const uint32_t carry = ((x.x & 0x7f807f80u) + 0x00800080u) | ((x.y & 0x7f807f80u) + 0x00800080u) |
+                             ((x.z & 0x7f807f80u) + 0x00800080u) | ((x.w & 0x7f807f80u) + 0x00800080u);
+      any |= (i & (PT_B * 8 - 1)) < whole ? carry : 0u;
     }
     if (!(any & 0x80008000u)) continue;
 #pragma unroll 1
     for (int n = 0; n < 8; ++n) {
-      const bool behind = (((i0 + 64 * n) >> 3) & (PT_B - 1)) >= keys;
-      uint32_t* w = reinterpret_cast<uint32_t*>(pieces + i0 + 64 * n);
+      const int i = i0 + 64 * n;
+      if ((i & (PT_B * 8 - 1)) >= whole) continue;
+      uint32_t* w = reinterpret_cast<uint32_t*>(pieces + i);
       for (int c = 0; c < 4; ++c) {
         const uint32_t x = w[c], low = (x & 0x7f80u) == 0x7f80u, high = (x & 0x7f800000u) == 0x7f800000u;
-        if (behind) w[c] = 0;
-        else if (low || high) odd = true, w[c] = (low ? 0u : x & 0xffffu) | (high ? 0u : x & 0xffff0000u);
+        if (low || high) odd = true, w[c] = (low ? 0u : x & 0xffffu) | (high ? 0u : x & 0xffff0000u);
       }
     }
   }
