@@ -5,7 +5,7 @@ import math
 import pytest
 import torch
 
-import _prompt as P
+from tests import _prompt as P
 
 pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
@@ -234,3 +234,47 @@ def test_gradients_against_differences(cuda, softcap, window):
         slope = (loss(*up) - loss(*down)) / (2 * h)
         want = (got[name].double() * step.double()).sum().item()
         assert abs(slope - want) <= 0.01, (name, slope, want)
+
+
+def test_a_layer_trained(cuda):
+    """The norm with rotation, the attention and both gradients in one chain over a fused projection's columns, fp32: the chain's
+    gradient along a random direction of the projection and of the norm's weights against the loss's central difference.  Noise and
+    third-order term as in the test above, with the norm's curvature (rows of length near sqrt(32), steps of 2^-7)."""
+    T, Hq, Hkv, d, eps = 60, 4, 2, 32, 1e-6
+    lengths = [45, 15]
+    offsets = P.cu(lengths)
+    g = torch.Generator(device="cuda").manual_seed(21)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    rows, d_out, wq, wk = r(T, Hq + 2 * Hkv, d), r(T, Hq, d), 1 + 0.1 * r(d), 1 + 0.1 * r(d)
+    angle = torch.arange(45, device="cuda")[:, None] * 100.0 ** (-torch.arange(d // 2, device="cuda") / (d // 2))
+    pos = torch.cat([torch.arange(n, device="cuda") for n in lengths]).int()
+    rope = dict(cos=angle.cos().contiguous(), sin=angle.sin().contiguous(), positions=pos, eps=eps)
+    cut = lambda x: (x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:])  # noqa: E731
+
+    def forward(rows, wq, wk):
+        q, k, v = cut(rows)
+        yq, yk = torch.empty(T, Hq, d, device="cuda"), torch.empty(T, Hkv, d, device="cuda")
+        cuda.kda_qk_norm_rope(q, k, wq, wk, yq, yk, **rope)
+        out, lse = torch.empty(T, Hq, d, device="cuda"), torch.empty(T, Hq, device="cuda")
+        cuda.kda_prefill_attention(yq, yk, v, offsets, 45, out, lse=lse)
+        return yq, yk, out, lse
+
+    yq, yk, out, lse = forward(rows, wq, wk)
+    grads = torch.empty_like(rows)
+    dq, dk, dv = cut(grads)
+    gq, gk = torch.empty_like(yq), torch.empty_like(yk)
+    ws = torch.empty(cuda.kda_prefill_attention_backward_workspace_size(T, 2, Hq, Hkv, d), dtype=torch.uint8, device="cuda")
+    cuda.kda_prefill_attention_backward(d_out, yq, yk, cut(rows)[2], out, lse, offsets, 45, gq, gk, dv, ws)
+    dw = torch.empty(2, d, device="cuda")
+    ws = torch.empty(cuda.kda_qk_norm_rope_backward_workspace_size(T, Hq, Hkv, d), dtype=torch.uint8, device="cuda")
+    cuda.kda_qk_norm_rope_backward(gq, gk, *cut(rows)[:2], wq, wk, dq, dk, dw[0], dw[1], ws, **rope)
+    loss = lambda *x: (forward(*x)[2].double() * d_out.double()).sum().item()  # noqa: E731
+    for i, grad in enumerate((grads, dw[0], dw[1])):
+        x = [rows, wq, wk]
+        step = r(*x[i].shape)
+        step /= step.norm()
+        h = 2.0 ** -7
+        up, down = list(x), list(x)
+        up[i], down[i] = x[i] + h * step, x[i] - h * step
+        slope, want = (loss(*up) - loss(*down)) / (2 * h), (grad.double() * step.double()).sum().item()
+        assert abs(slope - want) <= 0.02, (i, slope, want)

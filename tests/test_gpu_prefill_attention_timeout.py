@@ -4,7 +4,7 @@ counted, and the next calls are right."""
 import pytest
 import torch
 
-import _prompt as P
+from tests import _prompt as P
 
 pytestmark = pytest.mark.gpu
 
