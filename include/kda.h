@@ -675,7 +675,7 @@ kda_status kda_paged_attention(const kda_paged_attention_args* a, kda_stream_t s
  * The head layout is kda_qk_norm_rope's (its q_out, k_out and the projection's values go in as they are), the result that of
  * kda_paged_attention over a cache that holds the sequence, to rounding.  Sums and softmax statistics are fp32; with bf16 inputs
  * the probabilities are rounded to bf16 for their product with the values.
- * Rows outside every sequence are neither read into a result nor written.  What a query does not see does not matter to its row,
+ * `out` overlaps no input.  Rows outside every sequence are neither read into a result nor written.  What a query does not see does not matter to its row,
  * NaN included.
  */
 typedef struct {
@@ -685,7 +685,7 @@ typedef struct {
   int64_t q_stride, k_stride, v_stride;
   kda_dtype in_dtype;
   int64_t T;                 /* total packed tokens, at most 2^31 - 1024 */
-  int Hq, Hkv, d;            /* Hq a multiple of Hkv, at most 65535 */
+  int Hq, Hkv, d;            /* Hq a multiple of Hkv, at most 65535; T * Hq below 2^34, (T / 64 + N) * Hq below 2^31 */
   int N;                     /* sequences, <= 65535 */
   const int32_t* cu_seqlens; /* int32[N + 1] device, non-decreasing within [0, T] */
   int32_t max_seqlen;        /* host: an upper bound on every sequence length */
@@ -714,7 +714,8 @@ kda_status kda_prefill_attention(const kda_prefill_attention_args* a, kda_stream
  *   dv_j = sum_i p_ij d_out_i,   dx_ij = p_ij (d_out_i . v_j - D_i) c_ij scale,   dq_i = sum_j dx_ij k_j,
  *   dk_j = sum_i dx_ij q_i,   dk and dv summed over the query heads that share a key/value head.
  * Every sum has one owner and a fixed order: the same call gives the same bits.  With bf16 inputs p and dx are rounded to bf16
- * for the products that take them in.  Rows outside every sequence are not written.  A token that holds a NaN or an infinity
+ * for the products that take them in.  The gradients overlap neither inputs nor one another (columns of one buffer may be theirs).
+ * Rows outside every sequence are not written.  A token that holds a NaN or an infinity
  * (in q, k, v or d_out) may spread it to all gradients of its own sequence, never to another's.
  */
 typedef struct {

@@ -822,7 +822,8 @@ kda_status check_prompt(const kda_prefill_attention_args* a) {
   if (a->T < 0 || a->N < 0 || a->N > 65535 || a->Hq <= 0 || a->Hkv <= 0 || a->Hq > 65535 || a->Hq % a->Hkv != 0 ||
       a->max_seqlen < 0 || a->window < 0)
     return KDA_ERR_INVALID_ARG;
-  if (a->T > 0x7fffffff - 1023 || a->T * a->Hq > 0x3ffffffffLL) return KDA_ERR_INVALID_ARG;
+  if (a->T > 0x7fffffff - 1023 || a->T * a->Hq > 0x3ffffffffLL || (a->T / 64 + a->N) * a->Hq > 0x7fffffff)
+    return KDA_ERR_INVALID_ARG;  // the grids
   if (!(a->softcap >= 0.f) || a->softcap > 3e38f || !(a->scale >= -3e38f && a->scale <= 3e38f)) return KDA_ERR_INVALID_ARG;
   if (!d_ok(a->d)) return KDA_ERR_UNSUPPORTED;
   return KDA_OK;

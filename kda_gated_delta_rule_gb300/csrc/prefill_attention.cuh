@@ -30,7 +30,7 @@ __device__ __forceinline__ PfBlock pf_block(const PromptAttnArgs& a, int64_t pla
   PfBlock b{0, 0, 0};
   while (hi > lo) {
     const int step = (hi - lo + 31) >> 5, i = lo + lane * step;
-    if (i < hi) c0 = __ldg(a.cu + i), c1 = __ldg(a.cu + i + 1);
+    if (i < hi) c0 = __ldcg(a.cu + i), c1 = __ldcg(a.cu + i + 1);
     const bool ok = i < hi && (int64_t)(max(0, min(T, c0)) >> SHIFT) + i <= place;
     const int n = __popc(__ballot_sync(0xffffffffu, ok));
     if (n == 0) return b;
@@ -65,7 +65,7 @@ struct PfRanks {
       const int i = 32 * r + (int)(threadIdx.x & 31);
       t0[r] = len[r] = 0;
       if (32 * r < a.N && i < a.N) {
-        const int c0 = __ldg(a.cu + i), c1 = __ldg(a.cu + i + 1);
+        const int c0 = __ldcg(a.cu + i), c1 = __ldcg(a.cu + i + 1);
         if (!(c0 < 0 || c1 < c0 || c1 > a.T || c1 - c0 > a.max_seqlen)) t0[r] = c0, len[r] = c1 - c0;
       }
     }
@@ -129,11 +129,12 @@ __device__ __forceinline__ PfBlock pf_ranked(const PromptAttnArgs& a, PfRanks<SH
   return b;
 }
 
+// (Offsets are read past L1: the gradient's second kernel starts without a wait for the one before.)
 // Reports offsets that are out of order or out of range, and sequences beyond max_seqlen; one warp asks.
 __device__ __forceinline__ void pf_check_offsets(const PromptAttnArgs& a) {
   bool bad = false;
   for (int i = threadIdx.x & 31; i < a.N; i += 32) {
-    const int c0 = __ldg(a.cu + i), c1 = __ldg(a.cu + i + 1);
+    const int c0 = __ldcg(a.cu + i), c1 = __ldcg(a.cu + i + 1);
     bad |= c0 < 0 || c1 < c0 || c1 > a.T || c1 - c0 > a.max_seqlen;
   }
   if (__any_sync(0xffffffffu, bad) && (threadIdx.x & 31) == 0) flag_status(a.status, KDA_DEV_SEQ_OOB);
@@ -146,7 +147,7 @@ __device__ __forceinline__ void pf_check_offsets(const PromptAttnArgs& a) {
 cudaError_t pf_tc(const PromptAttnArgs& a, cudaStream_t s);
 // How many fp32 parts of dk and dv a gradient on the tensor cores adds up (1: none are written), and the gradient.
 int pg_parts(int64_t T, int Hq, int Hkv);
-cudaError_t pf_tc_grad(const PromptAttnArgs& a, const PromptGradArgs& g, const float2* stats, float* parts, cudaStream_t s);
+cudaError_t pf_tc_grad(const PromptAttnArgs& a, const PromptGradArgs& g, float2* stats, float* parts, cudaStream_t s);
 cudaError_t pf_f32(const PromptAttnArgs& a, cudaStream_t s);
 cudaError_t pf_f32_grad(const PromptAttnArgs& a, const PromptGradArgs& g, const float2* stats, cudaStream_t s);
 

@@ -10,6 +10,10 @@
 //            (over the S^T and V dO^T they come from) of dV += P^T dO and dK += dX^T Q.
 //   queries: 128 queries of a head against the tiles of 128 keys that they see: S = Q K^T, dO V^T, dQ += dX K, with two buffers for
 //            dO V^T (dX in its place), so that the next tile's products run under a tile's arithmetic.
+// D_i from the forward's output carries that output's rounding, d_out . (o rounded - o): against dx's own size it matters in rows that see
+// few keys (over many, o and its rounding shrink with the mean, and what is wrong in D meets the keys' mean).  So before both,
+//   means:   in blocks of queries that walk up to PG_FEW tiles, D_i = sum_j p_ij (do_i . v_j) in fp32, by the queries' kernel without
+//            its third product.
 // Where keys' blocks are too few for the SMs (one key/value head for all queries), the group's heads are dealt to several CTAs, whose
 // fp32 parts a third kernel adds up in order.
 // As in the forward, one CTA per SM walks units and takes over those that have not started, the most work first.  Its warps: the
@@ -24,6 +28,7 @@ namespace kda {
 namespace {
 
 constexpr int PG_MOST_PARTS = 16;
+constexpr int PG_FEW = 3;  // tiles
 constexpr int PG_GROUPS = 4;               // (2 with twice the columns: backward of 8192 tokens, 12 heads of 128, 566 us against 548)
 constexpr int PG_COLS = PT_B / PG_GROUPS;  // columns of a thread
 constexpr int PG_SOFT = 128 * PG_GROUPS, PG_NT = PG_SOFT + 128, PG_W = PG_SOFT / 32;
@@ -154,6 +159,17 @@ struct Yes {
 struct No {
   static constexpr bool value = false;
 };
+
+// Block id % PG_FEW of sequence id / PG_FEW.
+__device__ __forceinline__ PfBlock pg_first_block(const PromptAttnArgs& a, int id) {
+  PfBlock b{0, 0, 0};
+  const int i = id / PG_FEW, row0 = (id - i * PG_FEW) * PT_B;
+  if (i >= a.N) return b;
+  const int c0 = __ldcg(a.cu + i), c1 = __ldcg(a.cu + i + 1);
+  if (c0 < 0 || c1 < c0 || c1 > a.T || c1 - c0 > a.max_seqlen || row0 >= c1 - c0) return b;
+  b.t0 = c0, b.len = c1 - c0, b.row0 = row0;
+  return b;
+}
 
 template <int D, bool CAP>
 __global__ void __launch_bounds__(PG_NT, 1)
@@ -514,10 +530,10 @@ __global__ void __launch_bounds__(PG_NT, 1)
   if (warp == PG_W) tc::tmem_dealloc(tmem, PT_TMEM);
 }
 
-template <int D, bool CAP>
+template <int D, bool CAP, bool MEANS>
 __global__ void __launch_bounds__(PG_NT, 1)
     prefill_attention_grad_queries_kernel(const __grid_constant__ PgMaps maps, const PromptAttnArgs a, const PromptGradArgs g,
-                                          const float2* __restrict__ stats, const int64_t places) {
+                                          float2* __restrict__ stats, const int64_t places, const bool firsts) {
   using C = PgCfg<D>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* qbuf = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -540,9 +556,13 @@ __global__ void __launch_bounds__(PG_NT, 1)
   if (tid == PG_SOFT + 32)
     tc::prefetch_map(&maps.q), tc::prefetch_map(&maps.k), tc::prefetch_map(&maps.v), tc::prefetch_map(&maps.d_out);
   if (warp == PG_W) tc::tmem_alloc(&sh.tmem, PT_TMEM);
-  // No wait for the kernel before, the keys': nothing of it is read here.  That one's blocks let this start only when each had
-  // waited for the statistics itself, and the statistics are read past L1.
-  tc::pdl_launch_dependents();
+  if constexpr (MEANS) {
+    pdl_begin();
+  } else {
+    // No wait for the kernel before, the keys': nothing of it is read here.  That one's blocks let this start only when each had
+    // waited for the statistics itself, and the statistics are read past L1.
+    tc::pdl_launch_dependents();
+  }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -558,11 +578,12 @@ __global__ void __launch_bounds__(PG_NT, 1)
     TcRing<C::KR> kr;
     TcRing<C::VR> vr;
     while (more) {
-      const PfBlock b = pf_ranked(a, ranks, id / a.Hq, places, false);  // the longest rows first
-      if (b.len > 0) {
-        PgQueriesUnit u;
-        u.t0 = b.t0, u.len = b.len, u.row0 = b.row0, u.h = id % a.Hq;
-        u.lo = max(0, b.row0 - window + 1) / PT_B, u.n = b.row0 / PT_B - u.lo + 1;
+      // the longest rows first; of the sequences' first blocks in their own order
+      const PfBlock b = MEANS && firsts ? pg_first_block(a, id / a.Hq) : pf_ranked(a, ranks, id / a.Hq, places, false);
+      PgQueriesUnit u;
+      u.t0 = b.t0, u.len = b.len, u.row0 = b.row0, u.h = id % a.Hq;
+      u.lo = max(0, b.row0 - window + 1) / PT_B, u.n = b.row0 / PT_B - u.lo + 1;
+      if (b.len > 0 && (!MEANS || u.n <= PG_FEW)) {
         ok = tc_wait_warp(&sh.feed.empty[un.at], un.parity ^ 1, &sh.dead);
         if (!ok) break;
         if (lane == 0) {
@@ -671,9 +692,9 @@ __global__ void __launch_bounds__(PG_NT, 1)
         if (!ok) break;
         tc::fence_after_sync();
         if (tc::elect_one()) {
-          rows_mma<D>(t_dq, t_dp + dp_now.at * 128, k_r + k_now.at * STEP, i == 0);
+          if (!MEANS) rows_mma<D>(t_dq, t_dp + dp_now.at * 128, k_r + k_now.at * STEP, i == 0);
           tc::commit(&sh.k_empty[k_now.at]);
-          if (i + 1 == n) tc::commit(&sh.out_full);
+          if (!MEANS && i + 1 == n) tc::commit(&sh.out_full);
         }
         k_now.step();
         dp_now.step();
@@ -720,8 +741,11 @@ __global__ void __launch_bounds__(PG_NT, 1)
     TcRing<2> un, buf;
     uint32_t s_parity = 0, out_parity = 0;
     int rows_done = 0;
+    // The warps of the mean's sum meet at a unit's start and end: a wait that ran out in one ends all, so that none waits in vain.
+    auto meet = [&]() { ok = !tc::named_bar_or(1, PG_SOFT, !ok); };
     for (;; un.step()) {
       ok = tc_wait_warp(&sh.feed.full[un.at], un.parity, &sh.dead);
+      if (MEANS) meet();
       if (!ok) break;
       const PgQueriesUnit u = sh.unit[un.at];
       __syncwarp();
@@ -731,6 +755,7 @@ __global__ void __launch_bounds__(PG_NT, 1)
       const bool mine = row < u.len;
       const float2 stat = mine ? __ldcg(stats + (int64_t)u.h * a.T + u.t0 + row) : make_float2(0.f, 0.f);
       const float2 minus_lse = both(-stat.x), minus_d = both(-stat.y);
+      float2 mean = both(0.f);
       for (int i = 0; i < u.n; ++i, buf.step()) {
         const int k0 = (u.lo + i) * PT_B, first = k0 + part * PG_COLS;
         const bool masked = k0 + PT_B - 1 > u.row0 || k0 <= u.row0 + PT_B - 1 - window;
@@ -750,7 +775,7 @@ __global__ void __launch_bounds__(PG_NT, 1)
         for (int j = 0; j < PG_COLS / 2; ++j) {
           float2 p = CAP ? add2(x[j], minus_lse) : fma2(x[j], both(factor), minus_lse);
           p = make_float2(ex2(p.x), ex2(p.y));
-          x[j] = CAP ? mul2(p, cap_slope(x[j], over_cap2)) : p;
+          x[j] = CAP && !MEANS ? mul2(p, cap_slope(x[j], over_cap2)) : p;
         }
         ok = tc_wait_warp(&sh.dp_full[buf.at], buf.parity, &sh.dead);
         if (!ok) break;
@@ -762,17 +787,41 @@ __global__ void __launch_bounds__(PG_NT, 1)
           uint32_t w[PG_COLS / 2];
 #pragma unroll
           for (int j = 0; j < PG_COLS / 2; ++j) {
-            float2 ds = mul2(x[j], add2(dp[j], minus_d));
+            float2 ds = mul2(x[j], MEANS ? dp[j] : add2(dp[j], minus_d));
             if (decltype(some)::value) ds = only(ds, 2 * j, from, to);
-            w[j] = pack_bf16(ds.x, ds.y);
+            if (MEANS) mean = add2(mean, ds);
+            else w[j] = pack_bf16(ds.x, ds.y);
           }
-          st_columns(own_dp, w);
+          if (!MEANS) st_columns(own_dp, w);
         };
         if (masked) slopes(Yes());
         else slopes(No());
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) tc::bar_arrive(&sh.ds_full[buf.at]);
+      }
+      if constexpr (MEANS) {
+        // the parts' sums of a row meet in tensor memory, in places that take turns
+        float sums[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sums[i] = mean.x + mean.y;
+        const uint32_t at = t_dq + lanes + un.at * 32;
+        tc::tmem_st8f(at + part * 8, sums);
+        tc::tmem_wait_st();
+        tc::fence_before_sync();
+        meet();
+        if (!ok) break;
+        tc::fence_after_sync();
+        if (part == 0) {
+          float sum = 0.f;
+#pragma unroll
+          for (int i = 0; i < PG_GROUPS; ++i) {
+            tc::tmem_ld8(at + i * 8, sums);
+            sum += sums[0];
+          }
+          if (mine) stats[(int64_t)u.h * a.T + u.t0 + row].y = sum;
+        }
+        continue;
       }
       if (!ok) break;
       ok = tc_wait_warp(&sh.out_full, out_parity, &sh.dead);
@@ -787,13 +836,13 @@ __global__ void __launch_bounds__(PG_NT, 1)
       rows_done += min(PT_B, u.len - u.row0);
     }
     if (!ok && lane == 0) flag_status(a.status, KDA_DEV_TIMEOUT);
-    if (tid == 0) add_work(a.status, rows_done);
+    if (!MEANS && tid == 0) add_work(a.status, rows_done);
   }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   if (warp == PG_W) tc::tmem_dealloc(tmem, PT_TMEM);
-  tc::pdl_wait();  // what comes after this kernel comes after the keys' too
+  if (!MEANS) tc::pdl_wait();  // what comes after this kernel comes after the keys' too
 }
 
 // dv and dk of a block's keys: the parts' sum, in order.  A thread has 4 channels of a row.
@@ -821,10 +870,12 @@ __global__ void __launch_bounds__(256) pg_join_kernel(const PromptAttnArgs a, co
 }
 
 template <int D, bool CAP>
-cudaError_t grad_launch(const PromptAttnArgs& a, const PromptGradArgs& g, const float2* stats, float* parts, int nparts, cudaStream_t s) {
+cudaError_t grad_launch(const PromptAttnArgs& a, const PromptGradArgs& g, float2* stats, float* parts, int nparts, cudaStream_t s) {
   auto keys = prefill_attention_grad_keys_kernel<D, CAP>;
-  auto queries = prefill_attention_grad_queries_kernel<D, CAP>;
+  auto queries = prefill_attention_grad_queries_kernel<D, CAP, false>;
+  auto means = prefill_attention_grad_queries_kernel<D, CAP, true>;
   cudaError_t e = cudaFuncSetAttribute(keys, cudaFuncAttributeMaxDynamicSharedMemorySize, pg_keys_smem<D>());
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(means, cudaFuncAttributeMaxDynamicSharedMemorySize, pg_queries_smem<D>());
   if (e == cudaSuccess) e = cudaFuncSetAttribute(queries, cudaFuncAttributeMaxDynamicSharedMemorySize, pg_queries_smem<D>());
   if (e != cudaSuccess) return e;
   PgMaps maps;
@@ -835,9 +886,13 @@ cudaError_t grad_launch(const PromptAttnArgs& a, const PromptGradArgs& g, const 
     return cudaErrorInvalidValue;
   const int64_t places = pf_places(a.T, a.N, PT_B);
   if (places * a.Hq > 0x7fffffff) return cudaErrorInvalidValue;
+  const bool firsts = !(a.window > 0 && a.window <= (PG_FEW - 1) * PT_B + 1) && (int64_t)PG_FEW * a.N <= places;
+  e = launch_pdl(means, dim3((unsigned)((firsts ? (int64_t)PG_FEW * a.N : places) * a.Hq)), dim3(PG_NT), pg_queries_smem<D>(), s, maps, a, g,
+                 stats, places, firsts);
+  if (e != cudaSuccess) return e;
   e = launch_pdl(keys, dim3((unsigned)(places * a.Hkv * nparts)), dim3(PG_NT), pg_keys_smem<D>(), s, maps, a, g, stats, parts, nparts, places);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(queries, dim3((unsigned)(places * a.Hq)), dim3(PG_NT), pg_queries_smem<D>(), s, maps, a, g, stats, places);
+  e = launch_pdl(queries, dim3((unsigned)(places * a.Hq)), dim3(PG_NT), pg_queries_smem<D>(), s, maps, a, g, stats, places, false);
   if (e != cudaSuccess || nparts == 1) return e;
   return launch_pdl(pg_join_kernel, dim3((unsigned)places, 2 * a.Hkv), dim3(256), 0, s, a, g, parts, nparts);
 }
@@ -853,7 +908,7 @@ int pg_parts(int64_t T, int Hq, int Hkv) {
   return (int)(want < 1 ? 1 : want > most ? most : want);
 }
 
-cudaError_t pf_tc_grad(const PromptAttnArgs& a, const PromptGradArgs& g, const float2* stats, float* parts, cudaStream_t s) {
+cudaError_t pf_tc_grad(const PromptAttnArgs& a, const PromptGradArgs& g, float2* stats, float* parts, cudaStream_t s) {
   const bool cap = a.softcap > 0.f;
   const int n = pg_parts(a.T, a.Hq, a.Hkv);
   if (a.d == 128) return cap ? grad_launch<128, true>(a, g, stats, parts, n, s) : grad_launch<128, false>(a, g, stats, parts, n, s);

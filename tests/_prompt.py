@@ -5,6 +5,7 @@ The bounds count, with u the half step of the type that is rounded to (bf16 2^-8
                add 2^-20 of the score's size and 2^-21; e_ij is the bound on a probability's relative error that follows (a
                score's error twice: in itself and in the log-sum-exp)
   p            rounded to bf16 for its product when the inputs are bf16 (u_p, else 0)
+  D            the gradient's mean <d_out, out> from the rounded output, or (bf16, rows that see few keys) from p and d_out . v
   sums         over n rows in fp32: n 2^-24 of the terms' magnitudes, 2^-23 counted; rescaled sums stay within it
   results      rounded once to their type.
 """
@@ -65,6 +66,9 @@ def attention(q, k, v, d_out, lengths, start=0, scale=None, softcap=0.0, window=
             D = (dO * o).sum(1, keepdim=True)
             b_D = (dO.abs() * b_out).sum(1, keepdim=True) + d * 2.0 ** -23 * (dO.abs() * o.abs()).sum(1, keepdim=True)
             b_dp = d * 2.0 ** -23 * (dO.abs() @ V.abs().T)
+            if dt == torch.bfloat16:  # rows whose block of 128 walks up to three tiles have it from their own p and dp
+                own = ((e + n * 2.0 ** -23) * p * dp.abs() + p * b_dp).sum(1, keepdim=True)
+                b_D = torch.where((i < 384)[:, None] | bool(window and window <= 257), own, b_D)
             e_slope = 4 * (e_score / softcap + 2.0 ** -20) if softcap else 0.0
             dx = p * (dp - D) * slope
             b_dx = (u_in + e) * dx.abs() + p * ((b_dp + b_D) * slope + (dp - D).abs() * e_slope)

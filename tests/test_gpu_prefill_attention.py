@@ -71,6 +71,39 @@ def test_many_sequences(cuda, dtype, d):
     P.compare(cuda, lengths, 2, 1, d, dtype, seed=4)
 
 
+@pytest.mark.parametrize("dtype,d,heads", [(BF, 128, (2, 1)), (BF, 64, (3, 3)), (F32, 64, (2, 1))])
+@pytest.mark.parametrize("n", [256, 257, 1500])
+def test_more_sequences_than_a_warp_keeps(cuda, dtype, d, heads, n):
+    lengths = [(5 * i * i + 1) % 23 for i in range(n - 2)] + [200, 131]
+    P.compare(cuda, lengths, *heads, d, dtype, seed=n, start=3, tail=9)
+
+
+@pytest.mark.parametrize("softcap", [1e-25, 1e-12, 1e12, 1e35])
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 32), (F32, 64)])
+def test_caps_of_any_size(cuda, softcap, dtype, d):
+    """A tiny cap leaves equal scores and no gradient of them; a huge one is none."""
+    q, k, v, d_out = P.inputs(150, 2, 1, d, dtype, 22)
+    got = P.run(cuda, q, k, v, P.cu([150]), 150, d_out, softcap=softcap)
+    if softcap > 1:
+        want = P.attention(q, k, v, d_out, [150])
+    else:
+        want = P.attention(q, k, v, d_out, [150], scale=0.0)
+    for n, (value, bound) in want.items():
+        # |x| is at most 1e-12 of a score's 1 here, and the slope's: both far below the bounds' 2^-21 of P's
+        slack = 1e-9 * (d_out.abs().sum().double() if n in ("dq", "dk") else 1)
+        assert ((got[n].double() - value).abs() <= bound + slack).all(), n
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (F32, 64)])
+def test_offsets_out_of_order_are_flagged(cuda, dtype, d):
+    # which rows are written is not defined, that the call returns and says so is
+    q, k, v, d_out = P.inputs(340, 4, 2, d, dtype, 23)
+    for offsets in ([0, 200, 100, 340], [340, 0], [0, 50, 20, 20, 300, 299, 340] + [5, 340] * 200):
+        status = torch.zeros(2, dtype=torch.int32, device="cuda")
+        P.run(cuda, q, k, v, torch.tensor(offsets, dtype=torch.int32, device="cuda"), 340, d_out, dev_status=status)
+        assert status[0].item() == cuda.KDA_DEV_SEQ_OOB
+
+
 @pytest.mark.parametrize("dtype,d,heads", [(BF, 128, (4, 1)), (BF, 64, (3, 3)), (F32, 32, (2, 2))])
 @pytest.mark.parametrize("window", [0, 700])
 def test_longer_prompts(cuda, dtype, d, heads, window):

@@ -100,7 +100,7 @@ BAD_PROMPTS = [dict(in_dtype=7), dict(out_dtype=-1), dict(T=-1), dict(T=2 ** 31 
                dict(softcap=float("nan")), dict(softcap=float("inf")), dict(scale=float("nan")), dict(scale=float("inf")),
                dict(q=0), dict(k=0), dict(v=0), dict(out=0), dict(cu_seqlens=0), dict(q=(1 << 20) + 8), dict(cu_seqlens=(1 << 20) + 2),
                dict(lse=(1 << 20) + 2), dict(q_stride=HQ * D - 8), dict(k_stride=HKV * D + 4), dict(out_stride=0),
-               dict(T=2 ** 30, Hq=65535, Hkv=1)]
+               dict(T=2 ** 30, Hq=65535, Hkv=1), dict(N=65535, Hq=65534, Hkv=2, q_stride=65534 * D, out_stride=65534 * D)]
 
 
 @pytest.mark.parametrize("bad", BAD_PROMPTS, ids=str)
