@@ -19,7 +19,8 @@
 // As in the forward, one CTA per SM walks units and takes over those that have not started, the most work first.  Its warps: the
 // arithmetic's, thread = row and one of PG_GROUPS parts of the tile's columns; one for the products; one for units and loads (TMA);
 // and two that clear what lies behind the sequence in tiles that are column operands (0 * NaN), and bring the queries' statistics.
-// p and dx are rounded to bf16 (2^-8) for their products; everything else is fp32.
+// p and dx are rounded to bf16 (2^-8) for their products, as the results are, but dx for dq, where that rounding left 1.5 times the
+// results' own error: it goes in as two bf16.  Everything else is fp32.
 #include "device.h"
 #include "prefill_attention_tc.cuh"
 
@@ -111,13 +112,16 @@ __device__ __forceinline__ void scores_mma(uint32_t to, uint64_t a, uint64_t b) 
     tc::mma_ss(to, a + at, b + at, pt_idesc(PT_B), kk > 0);
   }
 }
-// to (128 x D) += the 128 x 128 bf16 in tensor memory at `a` (each thread's columns over its own scores) times rows of b
-template <int D>
+// to (128 x D) += the 128 x 128 bf16 in tensor memory at `a` (each thread's columns over its own scores; TWO: with what that rounding
+// left beside them) times rows of b
+template <int D, bool TWO = false>
 __device__ __forceinline__ void rows_mma(uint32_t to, uint32_t a, uint64_t b, bool first) {
 #pragma unroll
-  for (int kk = 0; kk < PT_B / 16; ++kk)  // 16 rows per step
-    tc::mma_ts(to, a + kk * 16 / PG_COLS * PG_COLS + kk * 16 % PG_COLS / 2, b + kk * (2048 / 16), pt_idesc(D) | tc::IDESC_B_MN,
-               !(first && kk == 0));
+  for (int kk = 0; kk < PT_B / 16; ++kk) {  // 16 rows per step
+    const uint32_t at = a + kk * 16 / PG_COLS * PG_COLS + kk * 16 % PG_COLS / 2;
+    tc::mma_ts(to, at, b + kk * (2048 / 16), pt_idesc(D) | tc::IDESC_B_MN, !(first && kk == 0));
+    if (TWO) tc::mma_ts(to, at + PG_COLS / 2, b + kk * (2048 / 16), pt_idesc(D) | tc::IDESC_B_MN, 1);
+  }
 }
 
 // Channels c0 .. c0 + N - 1 of a warp's 32 rows of a block's result in tensor memory, times `by`; `at`: the first row's first channel.
@@ -692,7 +696,7 @@ __global__ void __launch_bounds__(PG_NT, 1)
         if (!ok) break;
         tc::fence_after_sync();
         if (tc::elect_one()) {
-          if (!MEANS) rows_mma<D>(t_dq, t_dp + dp_now.at * 128, k_r + k_now.at * STEP, i == 0);
+          if (!MEANS) rows_mma<D, true>(t_dq, t_dp + dp_now.at * 128, k_r + k_now.at * STEP, i == 0);
           tc::commit(&sh.k_empty[k_now.at]);
           if (!MEANS && i + 1 == n) tc::commit(&sh.out_full);
         }
@@ -784,15 +788,18 @@ __global__ void __launch_bounds__(PG_NT, 1)
         float2 dp[PG_COLS / 2];
         ld_columns(own_dp, dp);
         auto slopes = [&](auto some) {
-          uint32_t w[PG_COLS / 2];
+          uint32_t w[PG_COLS / 2], rest[PG_COLS / 2];
 #pragma unroll
           for (int j = 0; j < PG_COLS / 2; ++j) {
             float2 ds = mul2(x[j], MEANS ? dp[j] : add2(dp[j], minus_d));
             if (decltype(some)::value) ds = only(ds, 2 * j, from, to);
             if (MEANS) mean = add2(mean, ds);
-            else w[j] = pack_bf16(ds.x, ds.y);
+            else tc::split_pair(ds.x, ds.y, w[j], rest[j]);
           }
-          if (!MEANS) st_columns(own_dp, w);
+          if (!MEANS) {
+            tc::tmem_st16(own_dp + PG_COLS / 2, rest);
+            st_columns(own_dp, w);
+          }
         };
         if (masked) slopes(Yes());
         else slopes(No());
