@@ -72,7 +72,7 @@ struct PfRanks {
     int most = 1;
 #pragma unroll
     for (int r = 0; r < PF_RANKED; ++r) most = max(most, blocks(r));
-    level = __reduce_max_sync(0xffffffffu, most) - 1, above = 0;
+    level = top = __reduce_max_sync(0xffffffffu, most) - 1, above = 0;
   }
   __device__ __forceinline__ int blocks(int r) const { return (int)(((unsigned)len[r] + (1u << SHIFT) - 1) >> SHIFT); }
   __device__ __forceinline__ int64_t count(int level, int N) const {  // below 2^31 / 128 + N
@@ -82,10 +82,12 @@ struct PfRanks {
       if (32 * r < N) n += max(0, blocks(r) - level);
     return __reduce_add_sync(0xffffffffu, n);
   }
-  // Ranks are asked for in ascending order, so the search starts at the level that the last one found: steps that double, then halve.
-  int level, above;  // above = count(level + 1)
+  // Ranks mostly ascend, so the search starts at the level that the last one found (or at the top, where a rank lies above it): steps
+  // that double, then halve.
+  int level, above, top;  // above = count(level + 1)
   __device__ __forceinline__ PfBlock find(int64_t rank, int N) {
     PfBlock b{0, 0, 0};
+    if (rank < above) level = top, above = 0;
     int hi = level + 1, lo = level, step = 1, n_hi = above, n;
     while ((n = (int)count(lo, N)) <= rank) {
       if (lo == 0) return b;

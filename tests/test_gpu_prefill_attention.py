@@ -41,8 +41,81 @@ def test_capped_scores(cuda, softcap, size, dtype, d, window):
 
 @pytest.mark.parametrize("scale", [1.0, -0.2, 0.0, 0.01])
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
-def test_scales(cuda, scale, dtype):
-    P.compare(cuda, [200], 2, 1, 64, dtype, seed=2, scale=scale)
+@pytest.mark.parametrize("softcap,window", [(0.0, 0), (4.0, 70)])
+def test_scales(cuda, scale, dtype, softcap, window):
+    P.compare(cuda, [200], 2, 1, 64, dtype, seed=2, scale=scale, softcap=softcap, window=window)
+
+
+@pytest.mark.parametrize("tokens,heads", [(7700, (12, 1)), (4100, (13, 1)), (1000, (34, 2)), (9900, (10, 2))], ids=str)
+def test_shared_heads_dealt_to_several_blocks(cuda, tokens, heads):
+    # 5 of 12 heads' parts, 9 of 13, 16 of 17, 1 of 5: uneven shares too
+    lengths = [tokens // 30 + (i % 3) * 7 - 7 for i in range(30)]
+    P.compare(cuda, lengths, *heads, 32, BF, seed=tokens)
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 16), (F32, 32)])
+def test_results_and_gradients_in_columns_of_larger_buffers(cuda, dtype, d):
+    T, Hq, Hkv = 190, 4, 2
+    q, k, v, d_out = P.inputs(T, Hq, Hkv, d, dtype, 24)
+    offsets = P.cu([150, 40])
+    want = P.run(cuda, q, k, v, offsets, 150, d_out)
+    wide = torch.full((T, 3 * Hq + 2 * Hkv + 1, d), 7.0, device="cuda").to(dtype)
+    out, dq, dk, dv = wide[:, 1:1 + Hq], wide[:, 5:5 + Hq], wide[:, 10:10 + Hkv], wide[:, 12:12 + Hkv]
+    grad = torch.full((T, Hq + 3, d), 9.0, device="cuda").to(dtype)
+    grad[:, 2:2 + Hq] = d_out
+    lse = torch.empty(T, Hq, device="cuda")
+    ws = torch.empty(cuda.kda_prefill_attention_backward_workspace_size(T, 2, Hq, Hkv, d), dtype=torch.uint8, device="cuda")
+    cuda.kda_prefill_attention(q, k, v, offsets, 150, out, lse=lse)
+    cuda.kda_prefill_attention_backward(grad[:, 2:2 + Hq], q, k, v, out, lse, offsets, 150, dq, dk, dv, ws)
+    for n, x in zip(("out", "dq", "dk", "dv"), (out, dq, dk, dv)):
+        assert torch.equal(x, want[n]), n
+    assert (wide[:, [0, 9, 14, 15, 16]] == 7.0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_offsets_beyond_32_bits(cuda, dtype):
+    """The last sequence of a batch whose elements number more than 2^31 gives what it gives alone."""
+    T, Hq, Hkv, d, n = 700001, 16, 4, 128, 300
+    rows = torch.empty(T, Hq + 2 * Hkv, d, dtype=dtype, device="cuda")
+    rows[:2 * n].normal_()
+    rows[-2 * n:].normal_()
+    assert rows.numel() > 2 ** 31
+    d_out, out, dq = (torch.empty(T, Hq, d, dtype=dtype, device="cuda") for _ in range(3))
+    d_out[-n:].normal_()
+    dk, dv = (torch.empty(T, Hkv, d, dtype=dtype, device="cuda") for _ in range(2))
+    lse = torch.empty(T, Hq, device="cuda")
+    q, k, v = rows[:, :Hq], rows[:, Hq:Hq + Hkv], rows[:, Hq + Hkv:]
+    offsets = P.cu([n], T - n)
+    ws = torch.empty(cuda.kda_prefill_attention_backward_workspace_size(T, 1, Hq, Hkv, d), dtype=torch.uint8, device="cuda")
+    cuda.kda_prefill_attention(q, k, v, offsets, n, out, lse=lse)
+    cuda.kda_prefill_attention_backward(d_out, q, k, v, out, lse, offsets, n, dq, dk, dv, ws)
+    at = slice(T - n, T)
+    alone = P.run(cuda, q[at], k[at], v[at], P.cu([n]), n, d_out[at])
+    for name, x in zip(("out", "lse", "dq", "dk", "dv"), (out, lse, dq, dk, dv)):
+        # dk and dv of the alone call may come in parts; out, lse and dq do not
+        if name in ("dk", "dv") and dtype == BF:
+            assert ((x[at].float() - alone[name].float()).norm() / alone[name].float().norm()).item() <= 2 ** -8, name
+        else:
+            assert torch.equal(x[at], alone[name]), name
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (F32, 64)])
+def test_calls_on_two_streams_at_once(cuda, dtype, d):
+    sets = [P.inputs(900, 8, 2, d, dtype, 30 + i) for i in range(2)]
+    offsets = P.cu([500, 400])
+    want = [P.run(cuda, *s[:3], offsets, 500, s[3]) for s in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(4):
+        for i, (s, stream) in enumerate(zip(sets, streams)):
+            with torch.cuda.stream(stream):
+                got[i].append(P.run(cuda, *s[:3], offsets, 500, s[3]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for res in got[i]:
+            for n in res:
+                assert torch.equal(res[n], want[i][n]), n
 
 
 @pytest.mark.parametrize("dtype,out_type,grad_type", [(BF, F32, F32), (BF, BF, F32), (F32, BF, BF), (BF, F32, BF)])

@@ -111,6 +111,14 @@ def test_fewer_drafts(cuda, proposal):
     assert call(cuda, target, guess, drafts, uniform, device_num) == expected(target, guess, drafts, uniform, num)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("size", [0.01, 3.0, 25.0])
+def test_rows_that_are_not_normalised(cuda, dtype, size):
+    target, guess, drafts, uniform = make(30, 3, 60, F32, True, 8, spread=4.0)
+    target, guess = (size * target).to(dtype), (size * 0.9 * guess).to(dtype)
+    assert call(cuda, target, guess, drafts, uniform) == expected(target, guess, drafts, uniform)
+
+
 def test_flags(cuda):
     target, guess, drafts, uniform = make(8, 3, 40, F32, True, 3)
     uniform[:, :2] = 0.0  # every draft with weight is accepted
