@@ -43,7 +43,7 @@ __device__ __forceinline__ PfBlock pf_block(const PromptAttnArgs& a, int64_t pla
   }
   if (c0 < 0 || c1 < c0 || c1 > T || c1 - c0 > a.max_seqlen) return b;
   const int64_t row0 = (place - ((int64_t)(c0 >> SHIFT) + lo)) << SHIFT;
-  if (row0 >= c1 - c0) return b;
+  if (row0 < 0 || row0 >= c1 - c0) return b;  // (below zero only with offsets out of order, where the search may end anywhere)
   b.t0 = c0;
   b.len = c1 - c0;
   b.row0 = (int)row0;
@@ -128,6 +128,7 @@ __device__ __forceinline__ PfBlock pf_ranked(const PromptAttnArgs& a, PfRanks<SH
   if (!PfRanks<SHIFT>::serves(a.N)) return pf_block<SHIFT>(a, reversed ? rank : places - 1 - rank);
   PfBlock b = ranks.find(rank, a.N);
   if (b.len > 0) b.row0 = (reversed ? (int)(((unsigned)b.len + (1u << SHIFT) - 1) >> SHIFT) - 1 - ranks.level : ranks.level) << SHIFT;
+  if ((unsigned)b.row0 >= (unsigned)b.len) b.len = 0;  // (offsets out of order: their blocks' number may pass 32 bits)
   return b;
 }
 

@@ -177,6 +177,34 @@ def test_offsets_out_of_order_are_flagged(cuda, dtype, d):
         assert status[0].item() == cuda.KDA_DEV_SEQ_OOB
 
 
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (F32, 64)])
+def test_offsets_out_of_order_write_only_the_batch(cuda, dtype, d):
+    T, Hq, Hkv, guard = 340, 4, 2, 512
+    q, k, v, d_out = P.inputs(T, Hq, Hkv, d, dtype, 24)
+    at = slice(guard, guard + T)
+
+    def inside(x):  # a copy between rows of ones
+        y = torch.ones(T + 2 * guard, *x.shape[1:], dtype=x.dtype, device="cuda")
+        y[at] = x
+        return y[at]
+    q, k, v, d_out = map(inside, (q, k, v, d_out))
+    rng = torch.Generator().manual_seed(25)
+    for offsets in ([0, 50, 20, 20, 300, 299, 340] + [5, 340] * 200, torch.randint(-3, 345, (300,), generator=rng).tolist(),
+                    torch.randint(-3, 345, (200,), generator=rng).tolist()):
+        N = len(offsets) - 1
+        bufs = [torch.full((T + 2 * guard, h, d), 7.0, dtype=dtype, device="cuda") for h in (Hq, Hq, Hkv, Hkv)]
+        lse = torch.full((T + 2 * guard, Hq), 7.0, device="cuda")
+        out, dq, dk, dv = (b[at] for b in bufs)
+        size = cuda.kda_prefill_attention_backward_workspace_size(T, N, Hq, Hkv, d)
+        ws = torch.full((size + 2 * (1 << 20),), 7, dtype=torch.uint8, device="cuda")
+        cu = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+        cuda.kda_prefill_attention(q, k, v, cu, T, out, lse=lse[at])
+        cuda.kda_prefill_attention_backward(d_out, q, k, v, out, lse[at], cu, T, dq, dk, dv, ws[1 << 20:(1 << 20) + size])
+        for b in (*bufs, lse):
+            assert (b[:guard] == 7.0).all() and (b[guard + T:] == 7.0).all()
+        assert (ws[:1 << 20] == 7).all() and (ws[(1 << 20) + size:] == 7).all()
+
+
 @pytest.mark.parametrize("dtype,d,heads", [(BF, 128, (4, 1)), (BF, 64, (3, 3)), (F32, 32, (2, 2))])
 @pytest.mark.parametrize("window", [0, 700])
 def test_longer_prompts(cuda, dtype, d, heads, window):
