@@ -10,6 +10,8 @@
 // query blocks of all its query heads (dk, dv), one per 64 query rows walks the keys (dq).  Both form the scores again
 // from the log-sum-exp.  Bound by the fp32 pipe and the shared-memory loads that feed it (8 loads of 16 bytes for 32
 // two-wide multiply-adds in the scores).
+#include <cooperative_groups.h>
+
 #include "f32x2.cuh"
 #include "prefill_attention.cuh"
 
@@ -19,6 +21,43 @@ namespace {
 
 constexpr int PB = 64;  // rows and keys of a block (1 << 6)
 constexpr int PNT = 256;
+
+namespace cg = cooperative_groups;
+
+// What the CTAs of a cluster hand one another at the end: `N` floats for each of a thread's 4 rows.  Row i of all threads is finished by CTA
+// i * parts / 4, which adds the others' up in order.
+__device__ __forceinline__ int row_owner(int i, int parts) { return i * parts / 4; }
+template <int N>
+__device__ __forceinline__ void hand_over(float* slots, int i, const float (&x)[N]) {
+#pragma unroll
+  for (int c = 0; c < N; ++c) slots[(i * N + c) * PNT + threadIdx.x] = x[c];
+}
+template <int N>
+__device__ __forceinline__ void take_over(cg::cluster_group& cluster, float* slots, int part, int i, float (&x)[N]) {
+  const float* from = cluster.map_shared_rank(slots, part);
+#pragma unroll
+  for (int c = 0; c < N; ++c) x[c] = from[(i * N + c) * PNT + threadIdx.x];
+}
+// The sums of the cluster's CTAs, in order, at each row's owner.
+template <int N>
+__device__ __forceinline__ void add_parts(cg::cluster_group& cluster, float* slots, float (&acc)[4][N]) {
+  const int parts = cluster.num_blocks(), part = cluster.block_rank();
+  if (parts == 1) return;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) hand_over(slots, i, acc[i]);
+  cluster.sync();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (row_owner(i, parts) != part) continue;
+    take_over(cluster, slots, 0, i, acc[i]);
+    for (int n = 1; n < parts; ++n) {
+      float x[N];
+      take_over(cluster, slots, n, i, x);
+#pragma unroll
+      for (int c = 0; c < N; ++c) acc[i][c] += x[c];
+    }
+  }
+}
 
 template <int D>
 struct PfShape {
@@ -161,6 +200,21 @@ __device__ __forceinline__ float score2(float dot, float scale, float cap, float
   return x * PA_LOG2E;
 }
 
+// Whether a thread's share of a tile's values are numbers.
+template <int D>
+__device__ __forceinline__ bool numbers(const float* sv) {
+  constexpr int C4 = D / 4;
+  bool ok = true;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < PB * C4; i += PNT) {
+    const int r = i / C4, c = (i - r * C4) * 4;
+    const float4 x = *reinterpret_cast<const float4*>(sv + r * PfShape<D>::LD + c);
+    const float most = 3.402823466e38f;
+    ok = ok && fabsf(x.x) <= most && fabsf(x.y) <= most && fabsf(x.z) <= most && fabsf(x.w) <= most;
+  }
+  return ok;
+}
+
 template <int D>
 __global__ void __launch_bounds__(PNT) pf_f32_kernel(const PromptAttnArgs a, const int64_t places) {
   using S = PfShape<D>;
@@ -168,10 +222,12 @@ __global__ void __launch_bounds__(PNT) pf_f32_kernel(const PromptAttnArgs a, con
   constexpr int BLOCK = PB * S::LD;
   float *sq = sm, *kv = sq + BLOCK, *sp = kv + 4 * BLOCK;  // kv: two tiles of K and V
   pdl_begin();
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, h = blockIdx.x % a.Hq, kh = h / (a.Hq / a.Hkv);
+  cg::cluster_group cluster = cg::this_cluster();
+  const int parts = cluster.num_blocks(), part = cluster.block_rank(), unit = blockIdx.x / parts;
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, h = unit % a.Hq, kh = h / (a.Hq / a.Hkv);
   if (blockIdx.x == 0 && tid < 32) pf_check_offsets(a);
   PfRanks<6> ranks(a);
-  const PfBlock b = pf_ranked(a, ranks, blockIdx.x / a.Hq, places, false);
+  const PfBlock b = pf_ranked(a, ranks, unit / a.Hq, places, false);
   if (b.len == 0) return;
   const int rows = min(PB, b.len - b.row0), window = a.window > 0 ? a.window : 0x7fffffff;
   load_block<D>(sq, static_cast<const float*>(a.q) + (int64_t)(b.t0 + b.row0) * a.q_stride + h * D, a.q_stride, rows);
@@ -182,24 +238,27 @@ __global__ void __launch_bounds__(PNT) pf_f32_kernel(const PromptAttnArgs a, con
 #pragma unroll
     for (int c = 0; c < S::CPT; ++c) o[i][c] = 0.f;
   }
-  const int last = b.row0 + rows - 1, first = max(0, b.row0 - window + 1) / PB * PB;
+  const int last = b.row0 + rows - 1, step = parts * PB;
+  const int lowest = max(0, b.row0 - window + 1) / PB, first = (lowest + ((part - lowest) & (parts - 1))) * PB;
   auto load = [&](int k0) {
-    float* to = kv + (k0 / PB & 1) * 2 * BLOCK;
+    float* to = kv + (k0 / step & 1) * 2 * BLOCK;
     const int64_t tok = b.t0 + k0;
     load_block<D>(to, static_cast<const float*>(a.k) + tok * a.k_stride + kh * D, a.k_stride, b.len - k0);
     load_block<D>(to + BLOCK, static_cast<const float*>(a.v) + tok * a.v_stride + kh * D, a.v_stride, b.len - k0);
   };
-  load(first);
+  if (first <= last) load(first);
   loads_sent();
-  for (int k0 = first; k0 <= last; k0 += PB) {
-    const float *sk = kv + (k0 / PB & 1) * 2 * BLOCK, *sv = sk + BLOCK;
-    if (k0 + PB <= last) load(k0 + PB);  // over the tile before, which all have left
+  for (int k0 = first; k0 <= last; k0 += step) {
+    const float *sk = kv + (k0 / step & 1) * 2 * BLOCK, *sv = sk + BLOCK;
+    if (k0 + step <= last) load(k0 + step);  // over the tile before, which all have left
     loads_sent();
     loads_there<1>();
     __syncthreads();
     float s[4][4];
     dots<D>(sq, sk, s);
     const bool masked = k0 + PB - 1 > b.row0 || k0 <= last - window;
+    // what unseen keys' values hold does not matter, NaN included (0 * NaN): a tile with such values takes the long way
+    const bool careful = masked && !__syncthreads_and(numbers<D>(sv));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int row = b.row0 + ty + 16 * i;
@@ -222,14 +281,12 @@ __global__ void __launch_bounds__(PNT) pf_f32_kernel(const PromptAttnArgs a, con
         sum += p;
         sp[(ty + 16 * i) * S::PLD + tx + 16 * j] = p;
       }
-#pragma unroll
-      for (int n = 1; n < 16; n <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, n);
       l[i] = l[i] * by + sum;
 #pragma unroll
       for (int c = 0; c < S::CPT; ++c) o[i][c] *= by;
     }
     __syncwarp();  // a row's probabilities come from its own half-warp
-    if (!masked) {
+    if (!careful) {
 #pragma unroll 2
       for (int j = 0; j < PB; j += 4) {
         float4 w[4];
@@ -238,7 +295,6 @@ __global__ void __launch_bounds__(PNT) pf_f32_kernel(const PromptAttnArgs a, con
         add_rows<D>(o, w, sv + j * S::LD);
       }
     } else {
-      // what unseen keys' values hold does not matter, NaN included
 #pragma unroll 1
       for (int j = 0; j < PB; ++j) {
         float v[S::CPT];
@@ -255,17 +311,53 @@ __global__ void __launch_bounds__(PNT) pf_f32_kernel(const PromptAttnArgs a, con
     }
     __syncthreads();
   }
+  loads_there<0>();
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int n = 1; n < 16; n <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], n);
+  if (parts > 1) {
+    constexpr int N = S::CPT + 2;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float x[N] = {m[i], l[i]};
+#pragma unroll
+      for (int c = 0; c < S::CPT; ++c) x[2 + c] = o[i][c];
+      hand_over(kv, i, x);
+    }
+    cluster.sync();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (row_owner(i, parts) != part) continue;
+      float x[N];
+      for (int n = 0; n < parts; ++n) {
+        take_over(cluster, kv, n, i, x);
+        const float top = n == 0 ? x[0] : fmaxf(m[i], x[0]), by = n == 0 ? 0.f : ex2(m[i] - top), w = ex2(x[0] - top);
+        if (n == 0) {
+          l[i] = x[1];
+#pragma unroll
+          for (int c = 0; c < S::CPT; ++c) o[i][c] = x[2 + c];
+        } else {
+          l[i] = l[i] * by + x[1] * w;
+#pragma unroll
+          for (int c = 0; c < S::CPT; ++c) o[i][c] = o[i][c] * by + x[2 + c] * w;
+        }
+        m[i] = top;
+      }
+    }
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = ty + 16 * i;
-    if (r >= rows) continue;
+    if (r >= rows || row_owner(i, parts) != part) continue;
     const int64_t t = b.t0 + b.row0 + r;
 #pragma unroll
     for (int c = 0; c < S::CPT; ++c) o[i][c] /= l[i];
     store_row<D>(a.out, a.out_bf16, t * a.out_stride + h * D, o[i]);
     if (tx == 0 && a.lse) a.lse[t * a.Hq + h] = m[i] * PA_LN2 + logf(l[i]);
   }
-  if (tid == 0) add_work(a.status, rows);
+  if (tid == 0 && part == 0) add_work(a.status, rows);
+  if (parts > 1) cluster.sync();  // the others have read what is here
 }
 
 // Probabilities and dy of the tile (rows: queries, columns: keys) from the scores, with the masks; also in shared memory.
@@ -275,22 +367,24 @@ __device__ __forceinline__ void tile_grads(const PromptAttnArgs& a, const float2
                                            float* sp, float* sds) {
   using S = PfShape<D>;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  float2 st[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) st[i] = ty + 16 * i < rows ? __ldg(stats + ty + 16 * i) : make_float2(0.f, 0.f);
   float s[4][4], dp[4][4];
   dots<D>(sq, sk, s);
   dots<D>(sdo, sv, dp);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = ty + 16 * i, row = row0 + r;
-    const float2 st = r < rows ? __ldg(stats + r) : make_float2(0.f, 0.f);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int key = k0 + tx + 16 * j;
       const bool seen = r < rows && key < len && key <= row && key > row - window;
       float slope;
       const float y = score2(s[i][j], a.scale, a.softcap, slope);
-      const float p = seen ? ex2(y - st.x) : 0.f;
+      const float p = seen ? ex2(y - st[i].x) : 0.f;
       if (sp) sp[r * S::PLD + tx + 16 * j] = p;
-      sds[r * S::PLD + tx + 16 * j] = seen ? p * (dp[i][j] - st.y) * slope : 0.f;
+      sds[r * S::PLD + tx + 16 * j] = seen ? p * (dp[i][j] - st[i].y) * slope : 0.f;
     }
   }
 }
@@ -305,10 +399,12 @@ __global__ void __launch_bounds__(PNT)
   constexpr int BLOCK = PB * S::LD, BUF = kv_buffers(D);
   float *sk = sm, *sv = sk + BLOCK, *qo = sv + BLOCK, *sp = qo + 2 * BUF * BLOCK, *sds = sp + PB * S::PLD;  // qo: Q and dO
   pdl_begin();
-  const int tid = threadIdx.x, ty = tid >> 4, kh = blockIdx.x % a.Hkv, group = a.Hq / a.Hkv;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int parts = cluster.num_blocks(), part = cluster.block_rank(), unit = blockIdx.x / parts;
+  const int tid = threadIdx.x, ty = tid >> 4, kh = unit % a.Hkv, group = a.Hq / a.Hkv;
   if (blockIdx.x == 0 && tid < 32) pf_check_offsets(a);
   PfRanks<6> ranks(a);
-  const PfBlock b = pf_ranked(a, ranks, blockIdx.x / a.Hkv, places, true);
+  const PfBlock b = pf_ranked(a, ranks, unit / a.Hkv, places, true);
   if (b.len == 0) return;
   const int k0 = b.row0, keys = min(PB, b.len - k0), window = a.window > 0 ? a.window : 0x7fffffff;
   const int64_t tok = b.t0 + k0;
@@ -320,18 +416,19 @@ __global__ void __launch_bounds__(PNT)
 #pragma unroll
     for (int c = 0; c < S::CPT; ++c) dk[i][c] = dv[i][c] = 0.f;
   const int64_t last = min((int64_t)b.len - 1, (int64_t)k0 + keys - 1 + window - 1);  // the last row that sees one of the keys
-  const int blocks = (int)(last / PB) - k0 / PB + 1, n = blocks * group;  // a round: a block of one head
+  // a round: a block of one head; this CTA's blocks are `part`, `part` + parts, ..
+  const int blocks = max(0, ((int)(last / PB) - k0 / PB + parts - part) / parts), n = blocks * group;
   auto load = [&](int i) {
-    const int h = kh * group + i / blocks, row0 = k0 + i % blocks * PB;
+    const int h = kh * group + i / blocks, row0 = k0 + (part + i % blocks * parts) * PB;
     const int64_t t = b.t0 + row0;
     float* to = qo + (i % BUF) * 2 * BLOCK;
     load_block<D>(to, static_cast<const float*>(a.q) + t * a.q_stride + h * D, a.q_stride, b.len - row0);
     load_block<D>(to + BLOCK, static_cast<const float*>(g.d_out) + t * g.d_out_stride + h * D, g.d_out_stride, b.len - row0);
   };
-  load(0);
+  if (n > 0) load(0);
   loads_sent();
   for (int i = 0; i < n; ++i) {
-    const int h = kh * group + i / blocks, row0 = k0 + i % blocks * PB;
+    const int h = kh * group + i / blocks, row0 = k0 + (part + i % blocks * parts) * PB;
     const float *sq = qo + (i % BUF) * 2 * BLOCK, *sdo = sq + BLOCK;
     const int64_t t = b.t0 + row0;
     if (BUF == 2 && i + 1 < n) load(i + 1);  // over the round before, which all have left
@@ -358,15 +455,19 @@ __global__ void __launch_bounds__(PNT)
     __syncthreads();
     if (BUF == 1 && i + 1 < n) load(i + 1);
   }
+  loads_there<0>();
+  add_parts(cluster, qo, dk);
+  add_parts(cluster, qo + 4 * S::CPT * PNT, dv);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = ty * 4 + i;
-    if (r >= keys) continue;
+    if (r >= keys || row_owner(i, parts) != part) continue;
 #pragma unroll
     for (int c = 0; c < S::CPT; ++c) dk[i][c] *= a.scale;
     store_row<D>(g.dk, g.bf16, (tok + r) * g.dk_stride + kh * D, dk[i]);
     store_row<D>(g.dv, g.bf16, (tok + r) * g.dv_stride + kh * D, dv[i]);
   }
+  if (parts > 1) cluster.sync();
 }
 
 template <int D>
@@ -377,9 +478,11 @@ __global__ void __launch_bounds__(PNT)
   constexpr int BLOCK = PB * S::LD;
   float *sq = sm, *sdo = sq + BLOCK, *kv = sdo + BLOCK, *sds = kv + 4 * BLOCK;
   pdl_begin();
-  const int tid = threadIdx.x, ty = tid >> 4, h = blockIdx.x % a.Hq, kh = h / (a.Hq / a.Hkv);
+  cg::cluster_group cluster = cg::this_cluster();
+  const int parts = cluster.num_blocks(), part = cluster.block_rank(), unit = blockIdx.x / parts;
+  const int tid = threadIdx.x, ty = tid >> 4, h = unit % a.Hq, kh = h / (a.Hq / a.Hkv);
   PfRanks<6> ranks(a);
-  const PfBlock b = pf_ranked(a, ranks, blockIdx.x / a.Hq, places, false);
+  const PfBlock b = pf_ranked(a, ranks, unit / a.Hq, places, false);
   if (b.len == 0) return;
   const int rows = min(PB, b.len - b.row0), window = a.window > 0 ? a.window : 0x7fffffff;
   const int64_t t = b.t0 + b.row0;
@@ -390,18 +493,19 @@ __global__ void __launch_bounds__(PNT)
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int c = 0; c < S::CPT; ++c) dq[i][c] = 0.f;
-  const int last = b.row0 + rows - 1, first = max(0, b.row0 - window + 1) / PB * PB;
+  const int last = b.row0 + rows - 1, step = parts * PB;
+  const int lowest = max(0, b.row0 - window + 1) / PB, first = (lowest + ((part - lowest) & (parts - 1))) * PB;
   auto load = [&](int k0) {
-    float* to = kv + (k0 / PB & 1) * 2 * BLOCK;
+    float* to = kv + (k0 / step & 1) * 2 * BLOCK;
     const int64_t tok = b.t0 + k0;
     load_block<D>(to, static_cast<const float*>(a.k) + tok * a.k_stride + kh * D, a.k_stride, b.len - k0);
     load_block<D>(to + BLOCK, static_cast<const float*>(a.v) + tok * a.v_stride + kh * D, a.v_stride, b.len - k0);
   };
-  load(first);
+  if (first <= last) load(first);
   loads_sent();
-  for (int k0 = first; k0 <= last; k0 += PB) {
-    const float *sk = kv + (k0 / PB & 1) * 2 * BLOCK, *sv = sk + BLOCK;
-    if (k0 + PB <= last) load(k0 + PB);
+  for (int k0 = first; k0 <= last; k0 += step) {
+    const float *sk = kv + (k0 / step & 1) * 2 * BLOCK, *sv = sk + BLOCK;
+    if (k0 + step <= last) load(k0 + step);
     loads_sent();
     loads_there<1>();
     __syncthreads();
@@ -416,43 +520,65 @@ __global__ void __launch_bounds__(PNT)
     }
     __syncthreads();
   }
+  loads_there<0>();
+  add_parts(cluster, kv, dq);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = ty + 16 * i;
-    if (r >= rows) continue;
+    if (r >= rows || row_owner(i, parts) != part) continue;
 #pragma unroll
     for (int c = 0; c < S::CPT; ++c) dq[i][c] *= a.scale;
     store_row<D>(g.dq, g.bf16, (t + r) * g.dq_stride + h * D, dq[i]);
   }
-  if (tid == 0) add_work(a.status, rows);
+  if (tid == 0 && part == 0) add_work(a.status, rows);
+  if (parts > 1) cluster.sync();
+}
+
+// CTAs for a unit (a cluster), up to `most`: twice as many as long as there are tiles for them and all run within `rounds` fillings of
+// the GPU (shared memory holds one CTA of 128 channels an SM, two of fewer).
+inline int parts_of(const PromptAttnArgs& a, int64_t units, int most, int rounds) {
+  const int64_t slots = 152 * (a.d == 128 ? 1 : 2);
+  int parts = 1;
+  while (parts < most && parts * PB < a.max_seqlen && units * parts * 2 <= rounds * slots) parts *= 2;
+  return parts;
+}
+template <typename Kernel, typename... Args>
+cudaError_t launch_parts(Kernel* kernel, int64_t units, int parts, int smem, cudaStream_t s, const Args&... args) {
+  if (units > 0x7fffffff) return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(units * parts));
+  cfg.blockDim = dim3(PNT);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)parts;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = parts > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 template <int D>
 cudaError_t forward_launch(const PromptAttnArgs& a, cudaStream_t s) {
   using S = PfShape<D>;
   const int smem = (5 * PB * S::LD + PB * S::PLD) * 4;
-  auto kernel = pf_f32_kernel<D>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
   const int64_t places = pf_places(a.T, a.N, PB);
-  if (places * a.Hq > 0x7fffffff) return cudaErrorInvalidValue;
-  return launch_pdl(kernel, dim3((unsigned)(places * a.Hq)), dim3(PNT), smem, s, a, places);
+  return launch_parts(pf_f32_kernel<D>, places * a.Hq, parts_of(a, places * a.Hq, 2, 3), smem, s, a, places);
 }
 
 template <int D>
 cudaError_t grad_launch(const PromptAttnArgs& a, const PromptGradArgs& g, const float2* stats, cudaStream_t s) {
   using S = PfShape<D>;
   const int smem_kv = ((2 + 2 * kv_buffers(D)) * PB * S::LD + 2 * PB * S::PLD) * 4, smem_q = (6 * PB * S::LD + PB * S::PLD) * 4;
-  auto kv = pf_f32_grad_kv_kernel<D>;
-  auto q = pf_f32_grad_q_kernel<D>;
-  cudaError_t e = cudaFuncSetAttribute(kv, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_kv);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(q, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_q);
-  if (e != cudaSuccess) return e;
   const int64_t places = pf_places(a.T, a.N, PB);
-  if (places * a.Hq > 0x7fffffff) return cudaErrorInvalidValue;
-  e = launch_pdl(kv, dim3((unsigned)(places * a.Hkv)), dim3(PNT), smem_kv, s, a, g, stats, places);
+  const cudaError_t e = launch_parts(pf_f32_grad_kv_kernel<D>, places * a.Hkv, parts_of(a, places * a.Hkv, 4, 1), smem_kv, s, a, g, stats, places);
   if (e != cudaSuccess) return e;
-  return launch_pdl(q, dim3((unsigned)(places * a.Hq)), dim3(PNT), smem_q, s, a, g, stats, places);
+  return launch_parts(pf_f32_grad_q_kernel<D>, places * a.Hq, parts_of(a, places * a.Hq, 4, 1), smem_q, s, a, g, stats, places);
 }
 
 }  // namespace

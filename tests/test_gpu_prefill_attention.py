@@ -90,11 +90,12 @@ def test_offsets_beyond_32_bits(cuda, dtype):
     cuda.kda_prefill_attention(q, k, v, offsets, n, out, lse=lse)
     cuda.kda_prefill_attention_backward(d_out, q, k, v, out, lse, offsets, n, dq, dk, dv, ws)
     at = slice(T - n, T)
+    # the alone call is of so few rows that its sums come in parts: all in fp32, dk and dv in bf16
     alone = P.run(cuda, q[at], k[at], v[at], P.cu([n]), n, d_out[at])
     for name, x in zip(("out", "lse", "dq", "dk", "dv"), (out, lse, dq, dk, dv)):
-        # dk and dv of the alone call may come in parts; out, lse and dq do not
-        if name in ("dk", "dv") and dtype == BF:
-            assert ((x[at].float() - alone[name].float()).norm() / alone[name].float().norm()).item() <= 2 ** -8, name
+        if dtype == F32 or name in ("dk", "dv"):
+            ratio = ((x[at].double() - alone[name].double()).norm() / alone[name].double().norm()).item()
+            assert ratio <= (2 ** -8 if dtype == BF else 2 ** -20), name
         else:
             assert torch.equal(x[at], alone[name]), name
 
