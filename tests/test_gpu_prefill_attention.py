@@ -212,6 +212,13 @@ def test_longer_prompts(cuda, dtype, d, heads, window):
     P.compare(cuda, [2500, 1100], *heads, d, dtype, seed=6, window=window)
 
 
+@pytest.mark.parametrize("d", [16, 64, 128])
+@pytest.mark.parametrize("window", [0, 100])
+def test_many_heads_in_fp32(cuda, d, window):
+    """So many rows' blocks that each has one CTA, and so few keys' that each has several."""
+    P.compare(cuda, [300, 200], 64, 8, d, F32, seed=8, window=window)
+
+
 def test_nothing_to_do(cuda):
     e = lambda *s: torch.zeros(*s, device="cuda")  # noqa: E731
     cuda.kda_prefill_attention(e(0, 2, 16), e(0, 1, 16), e(0, 1, 16), P.cu([0, 0]), 0, e(0, 2, 16))
