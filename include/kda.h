@@ -674,7 +674,8 @@ kda_status kda_paged_attention(const kda_paged_attention_args* a, kda_stream_t s
  *   out = sum_j exp(x_j - m) v_j / sum_j exp(x_j - m),   lse = m + log sum_j exp(x_j - m).
  * The head layout is kda_qk_norm_rope's (its q_out, k_out and the projection's values go in as they are), the result that of
  * kda_paged_attention over a cache that holds the sequence, to rounding.  Sums and softmax statistics are fp32; with bf16 inputs
- * the probabilities are rounded to bf16 for their product with the values.
+ * the probabilities are rounded to bf16 for their product with the values.  The same call gives the same bits; with fp32 inputs calls
+ * of few rows split their sums, so that the batch around a sequence may change its last bits.
  * `out` overlaps no input.  Rows outside every sequence are neither read into a result nor written.  What a query does not see does not matter to its row,
  * NaN included.
  */
@@ -713,7 +714,8 @@ kda_status kda_prefill_attention(const kda_prefill_attention_args* a, kda_stream
  * p = exp(x - lse), D = <d_out, out> and the cap's slope c = 1 - (x / softcap)^2 (1 without a cap):
  *   dv_j = sum_i p_ij d_out_i,   dx_ij = p_ij (d_out_i . v_j - D_i) c_ij scale,   dq_i = sum_j dx_ij k_j,
  *   dk_j = sum_i dx_ij q_i,   dk and dv summed over the query heads that share a key/value head.
- * Every sum has one owner and a fixed order: the same call gives the same bits.  With bf16 inputs p and dx are rounded to bf16
+ * Every sum has one owner and a fixed order: the same call gives the same bits.  Calls of few rows split sums (all with fp32 inputs, dk
+ * and dv with bf16), so that the batch around a sequence may change its last bits.  With bf16 inputs p and dx are rounded to bf16
  * for the products that take them in.  The gradients overlap neither inputs nor one another (columns of one buffer may be theirs).
  * Rows outside every sequence are not written.  A token that holds a NaN or an infinity
  * (in q, k, v or d_out) may spread it to all gradients of its own sequence, never to another's.
