@@ -141,8 +141,9 @@ __global__ void __launch_bounds__(VA_NT) verify_accept_kernel(const VerifyAccept
   __shared__ unsigned long long totals[2][VA_MOST];  // of the cluster's CTAs, by pass
   __shared__ float rough_totals[2][VA_MOST];
   __shared__ int accepted, odd;
-  pdl_begin();
   cg::cluster_group cluster = cg::this_cluster();
+  cluster.barrier_arrive();  // this CTA has started; waited for before the first store into another's shared memory
+  pdl_begin();
   const int C = cluster.num_blocks(), rank = cluster.block_rank(), b = blockIdx.x / C;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const In* target = static_cast<const In*>(a.target) + (int64_t)b * a.W * a.V;
@@ -200,6 +201,7 @@ __global__ void __launch_bounds__(VA_NT) verify_accept_kernel(const VerifyAccept
     const unsigned long long s = w.q ? warp_sum<In, true>(w, v0, v1, f) : warp_sum<In, false>(w, v0, v1, f);
     if (lane == 0) sums[warp] = s, roughs[warp] = f;
     __syncthreads();
+    if (!again) cluster.barrier_wait();  // all have started
     if (tid < C) {  // this CTA's sums to each of the others
       unsigned long long t = 0;
       float r = 0.f;

@@ -185,6 +185,20 @@ def test_captured_and_on_another_stream(cuda):
     assert (accepted.tolist(), tokens.tolist()) == call(cuda, *data)
 
 
+@pytest.mark.parametrize("B,V", [(76, 3), (300, 40), (152, 2049)])
+def test_clusters_with_little_to_read(cuda, B, V):
+    """Most of a cluster's CTAs have no token of so small a vocabulary and come to the sums at once, in calls close behind one
+    another: they store into CTAs that may have only just started."""
+    sets = [make(B, 2, V, F32, i % 2 == 0, seed=20 + i) for i in range(4)]
+    accepted, tokens = torch.full((200, B), 77, dtype=I32, device="cuda"), torch.full((200, B, 2), 77, dtype=I32, device="cuda")
+    for i in range(200):
+        target, guess, drafts, uniform = sets[i % 4]
+        cuda.kda_verify_accept(target, drafts, uniform, accepted[i], tokens[i], draft_probs=guess)
+    for i, data in enumerate(sets):
+        a, t = expected(*data)
+        assert (accepted[i::4].cpu() == torch.tensor(a, dtype=I32)).all() and (tokens[i::4].cpu() == torch.tensor(t, dtype=I32)).all()
+
+
 def test_unaligned_rows(cuda):
     # probabilities and drafts one element into their storage
     target, guess, drafts, uniform = make(4, 3, 77, BF, True, 7)
