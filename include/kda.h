@@ -752,7 +752,7 @@ kda_status kda_prefill_attention_backward(const kda_prefill_attention_args* a, c
  *   w = max(target_probs[b][n] - draft_probs[b][n], 0) where draft n was refused (drafts certain: target_probs[b][n] without
  *       that token), or target_probs[b][n] itself where that holds no weight or all drafts were accepted.
  * Tokens so drawn have the target's distribution.  The sums are integers in units of 2^-58, so they depend on no order.
- * NaN and negative probabilities count as zero; rows need not be normalised.
+ * NaN and negative probabilities count as zero, at a draft too; rows need not be normalised.
  *   accepted[b] = n + 1: window tokens to commit, as kda_verify_replay takes it.
  *   tokens[b] = the n accepted drafts, the drawn token, then -1.
  * num_drafts[b] (NULL: W - 1) is how many drafts request b has; the others are not read.  A number outside [0, W - 1] sets
@@ -766,7 +766,7 @@ typedef struct {
   int B, W, V;                 /* W >= 1; 1 <= V <= 2^30 */
   const int32_t* draft_tokens; /* int32[B][W - 1]; NULL when W = 1 */
   const int32_t* num_drafts;   /* int32[B], or NULL */
-  const float* uniform;        /* [B][W] in [0, 1); other values count as the nearest within, NaN as 0 (in the draw) */
+  const float* uniform;        /* [B][W] in [0, 1); other values count as the nearest within, NaN as 0 */
   int32_t* accepted;           /* int32[B] */
   int32_t* tokens;             /* int32[B][W] */
   int32_t* dev_status;         /* optional int32[2]; the work counter counts accepted (n + 1 per request) */

@@ -44,6 +44,9 @@ __device__ __forceinline__ unsigned long long units(float p) {
   return (unsigned long long)high << 32 | low;
 }
 
+// A random number, brought into [0, 1).
+__device__ __forceinline__ double within(float u) { return u > 0.f ? fmin((double)u, 1.0 - 0x1p-53) : 0.0; }
+
 // What a token weighs.
 template <typename In>
 struct Weights {
@@ -166,8 +169,9 @@ __global__ void __launch_bounds__(VA_NT) verify_accept_kernel(const VerifyAccept
         out = (unsigned)x >= (unsigned)a.V;
         if (!out) {
           const int64_t at = (int64_t)i * a.V + x;
-          const double p = to_f32(target[at]), q = a.proposal ? to_f32(proposal[at]) : 1.f;
-          ok = (double)__ldg(u + i) * q < p;  // a product of two fp32 is exact in fp64
+          // NaN and negative values count as zero, as in the weights
+          const double p = fmaxf(to_f32(target[at]), 0.f), q = a.proposal ? fmaxf(to_f32(proposal[at]), 0.f) : 1.f;
+          ok = within(__ldg(u + i)) * q < p;  // a product of two fp32 is exact in fp64; the largest number's is q or just below: p >= q decides
         }
       }
       const unsigned not_ok = ~__ballot_sync(0xffffffffu, ok);
@@ -237,9 +241,7 @@ __global__ void __launch_bounds__(VA_NT) verify_accept_kernel(const VerifyAccept
   if (!usable) return;
 
   // the last random number in units of 2^-64, within [0, 1)
-  const float r = __ldg(u + a.W - 1);
-  const double r1 = r > 0.f ? fmin((double)r, 1.0 - 0x1p-53) : 0.0;
-  const unsigned long long threshold = __umul64hi((unsigned long long)(r1 * 0x1p64), total);
+  const unsigned long long threshold = __umul64hi((unsigned long long)(within(__ldg(u + a.W - 1)) * 0x1p64), total);
   if (threshold < before || threshold - before >= total_here) return;
   // of this CTA's pieces the one that goes beyond it
   int at = 0;

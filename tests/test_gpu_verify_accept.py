@@ -151,6 +151,29 @@ def test_random_numbers_outside_the_range(cuda, r, v):
     assert call(cuda, p, None, torch.zeros(1, 0, dtype=I32, device="cuda"), torch.tensor([[r]], device="cuda")) == ([1], [[v]])
 
 
+NAN, INF = float("nan"), float("inf")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("p,q,u,taken", [(0.0, -1.0, 0.5, False), (-0.25, -1.0, 0.5, False), (0.25, NAN, 0.5, True), (NAN, 0.25, 0.5, False),
+                                         (NAN, NAN, 0.5, False), (-0.25, 0.25, -2.0, False), (0.0, 0.5, -0.5, False), (0.25, 0.5, -0.5, True),
+                                         (0.25, 0.25, 1.0, True), (0.25, 0.5, 1.0, False), (0.25, 0.25, 2.0, True), (0.25, 0.5, 2.0, False),
+                                         (0.25, 0.0, INF, True), (0.25, 0.5, NAN, True), (0.0, 0.5, NAN, False),
+                                         (0.0, None, -1.0, False), (1.0, None, 1.0, True), (0.5, None, NAN, True), (0.0, None, NAN, False)])
+def test_values_outside_their_range_at_a_draft(cuda, dtype, p, q, u, taken):
+    """Probabilities that are negative or NaN count as zero and random numbers as the nearest in [0, 1), NaN as 0, in the
+    test of a draft as in the draw."""
+    W, V, at = 3, 600, 300
+    target, guess = torch.full((2, W, V), 0.0625, device="cuda"), torch.full((2, W - 1, V), 0.0625, device="cuda")
+    target[:, :, 10:] = 0.0
+    target[:, 1, at], guess[:, 1, at] = p, 0.5 if q is None else q
+    drafts = torch.tensor([[3, at]] * 2, dtype=I32, device="cuda")
+    uniform = torch.tensor([[0.0, u, 0.0]] * 2, device="cuda")
+    accepted, tokens = call(cuda, target.to(dtype), None if q is None else guess.to(dtype), drafts, uniform)
+    assert accepted == [3 if taken else 2] * 2
+    assert [t[:2] for t in tokens] == [[3, at] if taken else [3, tokens[0][1]]] * 2 and (taken or tokens[0][2] == -1)
+
+
 def test_the_draw_has_the_target_distribution(cuda):
     """Drafts from q, 40000 windows of one draft: token counts against p.  A count's standard deviation is at most
     sqrt(40000 / 4) = 100; five of them."""
