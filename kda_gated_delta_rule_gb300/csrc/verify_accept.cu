@@ -57,10 +57,7 @@ struct Weights {
     // p - q is d + e exactly, d its rounding: where d > 0, p is the larger and (p - d) - q has no rounding.  |e| is at most 2^-25 for
     // probabilities, so that it fits 32 bits in units of 2^-55.
     const float a = fmaxf(pv, 0.f), b = fmaxf(qv, 0.f), d = fmaxf(__fsub_rn(a, b), 0.f);
-    if (a >= 1.f) {  // not a probability, but rows need not be normalised
-      const unsigned long long x = units(a), y = units(b);
-      return x > y ? x - y : 0ull;
-    }
+    if (a >= 1.f) return a > b ? units(a) - units(b) : 0ull;  // not a probability, but rows need not be normalised
     const float e = d > 0.f ? __fsub_rn(__fsub_rn(a, d), b) : 0.f;
     return units(d) + (unsigned long long)((long long)__float2int_rz(__fmul_rn(e, 0x1p55f)) * 16);
   }

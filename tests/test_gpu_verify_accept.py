@@ -174,6 +174,21 @@ def test_values_outside_their_range_at_a_draft(cuda, dtype, p, q, u, taken):
     assert [t[:2] for t in tokens] == [[3, at] if taken else [3, tokens[0][1]]] * 2 and (taken or tokens[0][2] == -1)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("q", [2.0, 31.5, 32.0, 40.0, 1e10, 3e38, INF])
+@pytest.mark.parametrize("p", [0.5, 1.0, 3.0, 20.0])
+def test_proposals_far_from_normalised(cuda, dtype, p, q):
+    # whatever the proposal holds too much of, its tokens weigh nothing
+    target, guess = torch.full((3, 2, 500), 0.0078125, device="cuda"), torch.full((3, 1, 500), 0.00390625, device="cuda")
+    target[:, 0, [5, 70, 400]] = p if p < 10 else p / 4
+    guess[:, 0, [5, 70, 400]] = q
+    drafts = torch.tensor([[5]] * 3, dtype=I32, device="cuda")
+    target[:, 0, 5] = 0.0  # refused
+    uniform = torch.tensor([[0.5, 0.01], [0.5, 0.2], [0.5, 0.99]], device="cuda")
+    target, guess = target.to(dtype), guess.to(dtype)
+    assert call(cuda, target, guess, drafts, uniform) == expected(target, guess.clamp(max=1e30), drafts, uniform)
+
+
 def test_the_draw_has_the_target_distribution(cuda):
     """Drafts from q, 40000 windows of one draft: token counts against p.  A count's standard deviation is at most
     sqrt(40000 / 4) = 100; five of them."""
