@@ -751,7 +751,8 @@ kda_status kda_prefill_attention_backward(const kda_prefill_attention_args* a, c
  * them are.  Then one token is drawn with r = uniform[b][W - 1]: the least v for which w(0) + .. + w(v) > r * sum w, with
  *   w = max(target_probs[b][n] - draft_probs[b][n], 0) where draft n was refused (drafts certain: target_probs[b][n] without
  *       that token), or target_probs[b][n] itself where that holds no weight or all drafts were accepted.
- * Tokens so drawn have the target's distribution.  The sums are integers in units of 2^-58, so they depend on no order.
+ * Tokens so drawn have the target's distribution.  The sums are integers in units of 2^-59, so they depend on no order; each w is
+ * within two units of its value.
  * NaN and negative probabilities count as zero, at a draft too; rows need not be normalised.
  *   accepted[b] = n + 1: window tokens to commit, as kda_verify_replay takes it.
  *   tokens[b] = the n accepted drafts, the drawn token, then -1.

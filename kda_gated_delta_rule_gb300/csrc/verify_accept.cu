@@ -5,9 +5,9 @@
 // at a refused draft's place (p without x for a certain draft; p where nothing is left of it) and p behind the last accepted.
 //
 // The sums decide a whole number, so they must not depend on their order, and a place that fp32 rounds by 2^-24 would move past
-// neighbouring tokens of a large vocabulary.  Probabilities are summed as 64-bit integers, in units of 2^-59: a difference
-// p - q is exact down to that unit (truncated below it: in all V 2^-59, 3e-13 for 150001 tokens), sums up to 31 stay
-// within 64 bits, and any split gives the same result.
+// neighbouring tokens of a large vocabulary.  Probabilities are summed as 64-bit integers, in units of 2^-59: p is cut to whole units, and
+// p - q, whose two fp32 terms are cut one by one, is less than two units off (2^-58 a token, 5.2e-13 for 150001; exact where p and
+// q are whole units themselves).  Sums up to 31 stay within 64 bits, and any split gives the same result.
 //
 // One request per cluster of C CTAs of 8 warps, each warp a contiguous piece of the vocabulary.  It reads one row of p and of q
 // once, for the sums; then the CTA in whose part the threshold falls reads one warp's piece again (from L2) to find the token.
@@ -54,12 +54,12 @@ struct Weights {
   int without;      // with no q: a token that weighs nothing, or -1
   // NaN and negative values count as zero
   __device__ __forceinline__ unsigned long long operator()(float pv, float qv) const {
-    // p - q is d + e exactly, d its rounding: where d > 0, p is the larger and (p - d) - q has no rounding.  |e| is at most 2^-25 for
-    // probabilities, so that it fits 32 bits in units of 2^-55.
+    // p - q is d + e exactly, d its rounding: where d > 0, p is the larger and (p - d) - q has no rounding.  Below 2^-4 e is at most
+    // half of d's last place, 2^-29, so that it fits 32 bits in the sums' unit; few tokens of a row are above.
     const float a = fmaxf(pv, 0.f), b = fmaxf(qv, 0.f), d = fmaxf(__fsub_rn(a, b), 0.f);
-    if (a >= 1.f) return a > b ? units(a) - units(b) : 0ull;  // not a probability, but rows need not be normalised
+    if (a >= 0x1p-4f) return a > b ? units(a) - units(b) : 0ull;
     const float e = d > 0.f ? __fsub_rn(__fsub_rn(a, d), b) : 0.f;
-    return units(d) + (unsigned long long)((long long)__float2int_rz(__fmul_rn(e, 0x1p55f)) * 16);
+    return units(d) + (unsigned long long)(long long)__float2int_rz(__fmul_rn(e, 0x1p59f));
   }
   __device__ __forceinline__ unsigned long long alone(float pv, int v) const { return v != without ? units(fmaxf(pv, 0.f)) : 0ull; }
   __device__ __forceinline__ unsigned long long at(int v) const {

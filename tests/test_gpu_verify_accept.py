@@ -174,6 +174,44 @@ def test_values_outside_their_range_at_a_draft(cuda, dtype, p, q, u, taken):
     assert [t[:2] for t in tokens] == [[3, at] if taken else [3, tokens[0][1]]] * 2 and (taken or tokens[0][2] == -1)
 
 
+def pieces(x):
+    """Fractions that fp32 holds, with the sum x."""
+    out = []
+    while x:
+        e = 0
+        while x * 2 ** e < 2 ** 23:
+            e += 1
+        while x * Fraction(2) ** e >= 2 ** 24:
+            e -= 1
+        out.append(Fraction(int(x * Fraction(2) ** e)) / Fraction(2) ** e)
+        x -= out[-1]
+    return out
+
+
+@pytest.mark.parametrize("first", [True, False])
+@pytest.mark.parametrize("p,q", [(1.37 * 2.0 ** -20, 2.0 ** -34 + 2.0 ** -57), (1.37 * 2.0 ** -20, 2.0 ** -34 - 2.0 ** -58),
+                                 (0.0624, 2.0 ** -34 + 2.0 ** -57), (0.137, 2.0 ** -34 + 2.0 ** -57), (0.137, 2.0 ** -34 - 2.0 ** -58),
+                                 (0.9, 2.0 ** -33 - 2.0 ** -57), (2.5, 2.0 ** -34 + 2.0 ** -57), (1.1 * 2.0 ** -30, 2.0 ** -36 + 2.0 ** -59)])
+def test_differences_keep_what_fp32_cannot_hold(cuda, p, q, first):
+    """A token of weight p - q against others that weigh the same together, all multiples of 2^-59: half of the sum is exactly where
+    the one ends and the others begin, so one unit more or less of any would move the token."""
+    f32 = lambda x: Fraction(float(torch.tensor(x, dtype=F32)))  # noqa: E731
+    p, q = f32(p), f32(q)
+    rest = pieces(p - q)
+    assert len(rest) > 1 and (p - q) * 2 ** 59 % 1 == 0
+    row, guess = ([p] + rest, [q] + [0] * len(rest)) if first else (rest + [p], [0] * len(rest) + [q])
+    target = torch.zeros(1, 2, 300, device="cuda")
+    proposal = torch.zeros(1, 1, 300, device="cuda")
+    target[0, 0, 7:7 + len(row)] = torch.tensor([float(x) for x in row], device="cuda")
+    proposal[0, 0, 7:7 + len(row)] = torch.tensor([float(x) for x in guess], device="cuda")
+    proposal[0, 0, 299] = 0.5  # the draft, refused
+    target[0, 1, 0] = 1.0
+    data = target, proposal, torch.tensor([[299]], dtype=I32, device="cuda"), torch.tensor([[0.5, 0.5]], device="cuda")
+    want = expected(*data)
+    assert want[1][0][0] == (8 if first else 7 + len(rest))
+    assert call(cuda, *data) == want
+
+
 @pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
 @pytest.mark.parametrize("q", [2.0, 31.5, 32.0, 40.0, 1e10, 3e38, INF])
 @pytest.mark.parametrize("p", [0.5, 1.0, 3.0, 20.0])
