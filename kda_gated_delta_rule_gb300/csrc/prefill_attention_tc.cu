@@ -43,6 +43,11 @@ struct PtMaps {
   CUtensorMap q, k, v;
 };
 
+template <int N>
+struct Count {
+  static constexpr int value = N;
+};
+
 // The two blocks of a unit, and the key tiles that they walk.
 struct PtUnit {
   int t0, len;  // len = 0: no more units
@@ -154,45 +159,79 @@ __device__ __forceinline__ void pt_mask(uint32_t own_s, int from, int to, float 
   tc::tmem_wait_st();
 }
 
-// A tile's capped scores: the row's largest.  Half by half they are left in tensor memory as products where all rows of the warp see
-// all keys and the short polynomial serves, else written there as scores in powers of two, -infinity for unseen keys.
-__device__ __forceinline__ float pt_capped_top(uint32_t own_s, bool masked, int from, int to, float factor, float cap2,
-                                               const CapNearer& nearer, int& products) {
-  float top = -INFINITY;
-#pragma unroll 1
-  for (int half = 0; half < 2; ++half) {
-    float x[64], far[4], most[4];
-    tc::tmem_ld64(own_s + 64 * half, x);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) far[i] = fabsf(x[i]), most[i] = x[i];
-#pragma unroll
-    for (int i = 4; i < 64; ++i) far[i & 3] = fmaxf(far[i & 3], fabsf(x[i])), most[i & 3] = fmaxf(most[i & 3], x[i]);
-    const float all = fmaxf(fmaxf(far[0], far[1]), fmaxf(far[2], far[3]));
-    if (!masked && factor > 0.f && __all_sync(0xffffffffu, all * factor <= 2.f * PA_LOG2E * PA_NEARER)) {
-      const float s = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
-      top = fmaxf(top, s * nearer(s));
-      products |= 1 << half;
-      continue;
-    }
-#pragma unroll 1
-    for (int c = 64 * half; c < 64 * half + 64; c += 16) {
-      float2 y[8];
-      uint32_t w[16];
-      tc::tmem_ld16(own_s + c, reinterpret_cast<float*>(y));
-      pt_cap(y, factor, cap2);
-      const uint32_t seen = masked ? pt_seen(c, from, to) : 0xffffffffu;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        y[i].x = seen >> (2 * i) & 1 ? y[i].x : -INFINITY;
-        y[i].y = seen >> (2 * i + 1) & 1 ? y[i].y : -INFINITY;
-        top = fmaxf(top, fmaxf(y[i].x, y[i].y));
-        w[2 * i] = __float_as_uint(y[i].x), w[2 * i + 1] = __float_as_uint(y[i].y);
-      }
-      tc::tmem_st16(own_s + c, w);
-    }
-    tc::tmem_wait_st();  // read back below
+// Capped scores.  Which formula a score takes goes by its own product alone: the short polynomial up to `limit`, beyond it that of
+// pt_cap.  A warp's votes only leave out what none of its scores takes, so that a row's bits do not depend on the other rows (and the
+// next sequence's, which come along at a sequence's end) nor on keys that it does not see.
+struct PtCap {
+  CapNearer nearer;
+  float factor, cap2;  // of a product, to the cap's argument; the cap in powers of two
+  float limit;
+  __device__ __forceinline__ PtCap(float factor, float cap2) : nearer(cap2, factor * (0.5f * PA_LN2)), factor(factor), cap2(cap2) {
+    limit = factor > 0.f ? __fdividef(2.f * PA_LOG2E * PA_NEARER, factor) : -1.f;
   }
-  return top;
+  // 16 scores in powers of two, less m
+  __device__ __forceinline__ void less(const float2 (&x)[8], float m, float2 (&y)[8]) const {
+    float far = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      y[i] = fma2(x[i], nearer(x[i]), both(-m));
+      far = fmaxf(far, fmaxf(fabsf(x[i].x), fabsf(x[i].y)));
+    }
+    if (__all_sync(0xffffffffu, far <= limit)) return;
+    float2 z[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] = x[i];
+    pt_cap(z, factor, cap2);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      z[i] = add2(z[i], both(-m));
+      if (!(fabsf(x[i].x) <= limit)) y[i].x = z[i].x;
+      if (!(fabsf(x[i].y) <= limit)) y[i].y = z[i].y;
+    }
+  }
+  __device__ __forceinline__ float score(float s) const {
+    if (fabsf(s) <= limit) return __fmul_rn(s, nearer(s));
+    const float z = s * factor;
+    return fabsf(z) <= PA_NEAR ? capped_near(z, cap2) : capped_far(z, cap2);
+  }
+};
+
+// The largest capped score that a row sees of a tile, whose products stay in tensor memory.  `all_near`: halves of the keys that every row of
+// the warp sees, within the short polynomial.
+__device__ __forceinline__ float pt_capped_top(uint32_t own_s, bool masked, int from, int to, const PtCap& cap, int& all_near) {
+  const bool falls = cap.factor < 0.f;  // the smallest product has the largest score
+  float best = -INFINITY;
+  if (masked) {
+#pragma unroll 1
+    for (int c = 0; c < PT_B; c += 32) {
+      const uint32_t seen = pt_seen(c, from, to);
+      if (__all_sync(0xffffffffu, seen == 0)) continue;
+      float x[32];
+      tc::tmem_ld32(own_s + c, x);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) best = fmaxf(best, seen >> i & 1 ? (falls ? -x[i] : x[i]) : -INFINITY);
+    }
+    if (to <= 0 || from >= PT_B) return -INFINITY;
+  } else {
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {
+      float x[64], most[4], far[4];
+      tc::tmem_ld64(own_s + 64 * half, x);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) far[i] = fabsf(x[i]), most[i] = x[i];
+#pragma unroll
+      for (int i = 4; i < 64; ++i) far[i & 3] = fmaxf(far[i & 3], fabsf(x[i])), most[i & 3] = fmaxf(most[i & 3], x[i]);
+      if (falls) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) most[i] = -x[i];
+#pragma unroll
+        for (int i = 4; i < 64; ++i) most[i & 3] = fmaxf(most[i & 3], -x[i]);
+      }
+      best = fmaxf(best, fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3])));
+      if (__all_sync(0xffffffffu, fmaxf(fmaxf(far[0], far[1]), fmaxf(far[2], far[3])) <= cap.limit)) all_near |= 1 << half;
+    }
+  }
+  return cap.score(falls ? -best : best);
 }
 
 // The sum of a channel's values that are no numbers, and so were left out of the tiles with unseen keys, over the keys that a row sees.
@@ -433,7 +472,7 @@ __global__ void __launch_bounds__(PT_NT, 1)
     float factor = a.scale * (CAP ? 2.f * PA_LOG2E / a.softcap : PA_LOG2E);
     const bool negative = !CAP && factor < 0.f;
     if (!CAP) factor = fmaxf(fabsf(factor), 1.2e-38f);
-    const CapNearer nearer(cap2, factor * (0.5f * PA_LN2));
+    const PtCap cap(factor, cap2);
     bool ok = true;
     uint32_t s_parity = 0, o_parity = 0;
     int rows_done = 0;
@@ -458,9 +497,9 @@ __global__ void __launch_bounds__(PT_NT, 1)
         // the largest score in powers of two
         float top;
         float2 x[CAP ? 1 : PT_B / 2];
-        int products = 0;  // halves of the keys whose scores are left as products, for the short polynomial
+        int all_near = 0;  // halves of the keys for the short polynomial alone
         if constexpr (CAP) {
-          top = pt_capped_top(own_s, masked, from, to, factor, cap2, nearer, products);
+          top = pt_capped_top(own_s, masked, from, to, cap, all_near);
         } else {
           if (masked) pt_mask(own_s, from, to, negative ? INFINITY : -INFINITY);
           tc::tmem_ld128(own_s, reinterpret_cast<float*>(x));
@@ -493,35 +532,47 @@ __global__ void __launch_bounds__(PT_NT, 1)
           }
         }
         float2 sum0 = make_float2(l, 0.f), sum1 = both(0.f);
-        // 32 probabilities, to the columns of the scores that `at` counts in keys
-        auto probabilities = [&](int at, const float2* x, auto argument) {
-          uint32_t w[16];
+        // N probabilities, to the columns of the scores that `at` counts in keys
+        auto probabilities = [&](auto n, int at, const float2* x, auto argument) {
+          constexpr int N = decltype(n)::value;
+          uint32_t w[N / 2];
 #pragma unroll
-          for (int i = 0; i < 16; i += 2) {
+          for (int i = 0; i < N / 2; i += 2) {
             float2 e0 = argument(x[i]), e1 = argument(x[i + 1]);
             e0 = make_float2(ex2(e0.x), ex2(e0.y)), e1 = make_float2(ex2(e1.x), ex2(e1.y));
             sum0 = add2(sum0, e0), sum1 = add2(sum1, e1);
             w[i] = pack_bf16(e0.x, e0.y), w[i + 1] = pack_bf16(e1.x, e1.y);
           }
-          tc::tmem_st16(own_s + at / 2, w);
+          if constexpr (N == 32) tc::tmem_st16(own_s + at / 2, w);
+          else tc::tmem_st8f(own_s + at / 2, reinterpret_cast<const float*>(w));
         };
         if constexpr (CAP) {
           // by halves, over scores that have been read (a shorter body than the whole row's: instructions are fetched for each tile)
 #pragma unroll 1
           for (int half = 0; half < 2; ++half) {
-            float2 y[32];
-            tc::tmem_ld64(own_s + 64 * half, reinterpret_cast<float*>(y));
-            if (products >> half & 1) {
+            if (all_near >> half & 1) {
+              float2 y[32];
+              tc::tmem_ld64(own_s + 64 * half, reinterpret_cast<float*>(y));
 #pragma unroll
-              for (int c = 0; c < 2; ++c) probabilities(64 * half + 32 * c, y + 16 * c, [&](float2 s) { return fma2(s, nearer(s), both(-m)); });
-            } else {
+              for (int c = 0; c < 2; ++c)
+                probabilities(Count<32>(), 64 * half + 32 * c, y + 16 * c, [&](float2 s) { return fma2(s, cap.nearer(s), both(-m)); });
+              continue;
+            }
+#pragma unroll 1
+            for (int c = 64 * half; c < 64 * half + 64; c += 16) {
+              float2 x[8], y[8];
+              tc::tmem_ld16(own_s + c, reinterpret_cast<float*>(x));
+              cap.less(x, m, y);
+              const uint32_t seen = masked ? pt_seen(c, from, to) : 0xffffffffu;
 #pragma unroll
-              for (int c = 0; c < 2; ++c) probabilities(64 * half + 32 * c, y + 16 * c, [&](float2 s) { return add2(s, both(-m)); });
+              for (int i = 0; i < 8; ++i)
+                y[i] = make_float2(seen >> (2 * i) & 1 ? y[i].x : -INFINITY, seen >> (2 * i + 1) & 1 ? y[i].y : -INFINITY);
+              probabilities(Count<16>(), c, y, [](float2 s) { return s; });
             }
           }
         } else {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) probabilities(32 * c, x + 16 * c, [&](float2 s) { return fma2(s, both(factor), both(-m)); });
+          for (int c = 0; c < 4; ++c) probabilities(Count<32>(), 32 * c, x + 16 * c, [&](float2 s) { return fma2(s, both(factor), both(-m)); });
         }
         sum0 = add2(sum0, sum1);
         l = sum0.x + sum0.y;

@@ -107,7 +107,8 @@ __device__ __forceinline__ void pt_store32(void* base, bool is_bf16, int64_t at,
   }
 }
 
-// Scores in powers of two, capped; `factor` takes a product to the cap's argument.
+// Scores in powers of two, capped; `factor` takes a product to the cap's argument.  Each takes its formula by its own argument; the vote only
+// leaves the exponential out where no score of the warp needs it, so that none depends on what the other lanes hold.
 template <int N>
 __device__ __forceinline__ void pt_cap(float2 (&x)[N], float factor, float cap2) {
   const CapPoly near(cap2);
@@ -122,7 +123,10 @@ __device__ __forceinline__ void pt_cap(float2 (&x)[N], float factor, float cap2)
     for (int i = 0; i < N; ++i) x[i] = near(x[i]);
   } else {
 #pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = make_float2(capped(x[i].x, cap2), capped(x[i].y, cap2));
+    for (int i = 0; i < N; ++i) {
+      const float2 y = near(x[i]);
+      x[i] = make_float2(fabsf(x[i].x) <= PA_NEAR ? y.x : capped_far(x[i].x, cap2), fabsf(x[i].y) <= PA_NEAR ? y.y : capped_far(x[i].y, cap2));
+    }
   }
 }
 

@@ -15,7 +15,8 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
-// cap2 * tanh(y) given z = 2 log2(e) y, with cap2 = cap * log2(e).  Where all of a warp's |y| are up to 0.75 (|z| <= PA_NEAR) it is y
+// cap2 * tanh(y) given z = 2 log2(e) y, with cap2 = cap * log2(e).  Where all of a warp's |y| are up to 0.75 (|z| <= PA_NEAR; the prompt's
+// forms choose score by score) it is y
 // times a polynomial in y^2 for tanh(y) / y (a weighted least-squares fit that levels the relative error, 1.3e-7 in fp32):
 // no cancellation for small scores, and no use of the exponential's unit, which the exponentials fill already (256 ragged
 // requests, e4m3 cache, cap 30: 103 us without it, 101 with).  Else 1 - 2 / (1 + 2^z), within 1.2e-7 absolutely, and below |y| = 0.15
@@ -32,12 +33,16 @@ __device__ __forceinline__ float capped_near(float z, float cap2) {
   for (int i = 4; i >= 0; --i) t = fmaf(t, u, pa_tanh(i));
   return cap2 * y * t;
 }
-__device__ __forceinline__ float capped(float z, float cap2) {
+// The form with the exponential alone: for |z| beyond PA_NEAR, 2e-7 relatively there.
+__device__ __forceinline__ float capped_far(float z, float cap2) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(z)));
+  return fmaf(-2.f * cap2, r, cap2);
+}
+__device__ __forceinline__ float capped(float z, float cap2) {
   const float y = z * (0.5f * PA_LN2), u = y * y;
   const float small = cap2 * y * fmaf(u, fmaf(u, fmaf(u, -17.f / 315.f, 2.f / 15.f), -1.f / 3.f), 1.f);
-  return fabsf(z) < 0.3f * PA_LOG2E ? small : fmaf(-2.f * cap2, r, cap2);
+  return fabsf(z) < 0.3f * PA_LOG2E ? small : capped_far(z, cap2);
 }
 
 // capped_near for two scores, its coefficients multiplied out to powers of z.  Seven multiplications and
