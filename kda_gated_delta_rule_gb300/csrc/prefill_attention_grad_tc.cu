@@ -432,7 +432,7 @@ __global__ void __launch_bounds__(PG_NT, 1)
     const int part = warp >> 2;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16, t_s = tmem, t_dp = tmem + 128, t_dv = tmem + 256, t_dk = tmem + 384;
     const uint32_t own_s = t_s + part * PG_COLS + lanes, own_dp = t_dp + part * PG_COLS + lanes;
-    const float cap2 = a.softcap * PA_LOG2E, factor = a.scale * (CAP ? 2.f * PA_LOG2E / a.softcap : PA_LOG2E), over_cap2 = 1.f / cap2;
+    const float cap2 = a.softcap * PA_LOG2E, factor = pt_factor(a.scale, CAP ? 2.f * PA_LOG2E / a.softcap : PA_LOG2E), over_cap2 = 1.f / cap2;
     bool ok = true;
     TcRing<2> st, un;
     uint32_t s_parity = 0, dp_parity = 0, out_parity = 0;
@@ -746,7 +746,7 @@ __global__ void __launch_bounds__(PG_NT, 1)
     const int part = warp >> 2;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16, t_s = tmem, t_dp = tmem + 128, t_dq = tmem + 384;
     const uint32_t own_s = t_s + part * PG_COLS + lanes;
-    const float cap2 = a.softcap * PA_LOG2E, factor = a.scale * (CAP ? 2.f * PA_LOG2E / a.softcap : PA_LOG2E), over_cap2 = 1.f / cap2;
+    const float cap2 = a.softcap * PA_LOG2E, factor = pt_factor(a.scale, CAP ? 2.f * PA_LOG2E / a.softcap : PA_LOG2E), over_cap2 = 1.f / cap2;
     bool ok = true;
     TcRing<2> un, buf;
     uint32_t s_parity = 0, out_parity = 0;

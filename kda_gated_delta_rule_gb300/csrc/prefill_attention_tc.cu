@@ -167,7 +167,7 @@ struct PtCap {
   float factor, cap2;  // of a product, to the cap's argument; the cap in powers of two
   float limit;
   __device__ __forceinline__ PtCap(float factor, float cap2) : nearer(cap2, factor * (0.5f * PA_LN2)), factor(factor), cap2(cap2) {
-    limit = factor > 0.f ? __fdividef(2.f * PA_LOG2E * PA_NEARER, factor) : -1.f;
+    limit = factor > 0.f && nearer.usable() ? __fdividef(2.f * PA_LOG2E * PA_NEARER, factor) : -1.f;
   }
   // 16 scores in powers of two, less m
   __device__ __forceinline__ void less(const float2 (&x)[8], float m, float2 (&y)[8]) const {
@@ -469,7 +469,7 @@ __global__ void __launch_bounds__(PT_NT, 1)
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16, own_s = tmem + s * PT_B + lanes, own_o = tmem + PT_O + s * 128 + lanes;
     const float cap2 = a.softcap * PA_LOG2E;
     // of a product, to powers of two (or the cap's argument); not 0, which would turn an unseen key's -infinity into a NaN
-    float factor = a.scale * (CAP ? 2.f * PA_LOG2E / a.softcap : PA_LOG2E);
+    float factor = pt_factor(a.scale, CAP ? 2.f * PA_LOG2E / a.softcap : PA_LOG2E);
     const bool negative = !CAP && factor < 0.f;
     if (!CAP) factor = fmaxf(fabsf(factor), 1.2e-38f);
     const PtCap cap(factor, cap2);

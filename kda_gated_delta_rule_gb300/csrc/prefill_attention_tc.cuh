@@ -107,6 +107,12 @@ __device__ __forceinline__ void pt_store32(void* base, bool is_bf16, int64_t at,
   }
 }
 
+// What takes a product to the softmax's or the cap's argument; finite, so that a product of zero stays one.
+__device__ __forceinline__ float pt_factor(float scale, float per) {
+  constexpr float most = 3.402823466e38f;
+  return fminf(fmaxf(scale * per, -most), most);
+}
+
 // Scores in powers of two, capped; `factor` takes a product to the cap's argument.  Each takes its formula by its own argument; the vote only
 // leaves the exponential out where no score of the warp needs it, so that none depends on what the other lanes hold.
 template <int N>

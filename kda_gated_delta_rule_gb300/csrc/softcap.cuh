@@ -76,6 +76,13 @@ struct CapNearer {
 #pragma unroll
     for (int i = 0; i < 4; ++i) k[i] = c[i] * w, w *= per * per;
   }
+  // The coefficients go with per, per^3, .. per^7: caps far below or above the scale leave fp32's range, and so may s^2 under the latter.
+  __device__ __forceinline__ bool usable() const {
+    bool ok = true;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ok = ok && fabsf(k[i]) >= 1.175494351e-38f && fabsf(k[i]) <= 3.402823466e38f;
+    return ok;
+  }
   __device__ __forceinline__ float2 operator()(float2 s) const {
     const float2 u = mul2(s, s);
     return fma2(fma2(fma2(both(k[3]), u, both(k[2])), u, both(k[1])), u, both(k[0]));

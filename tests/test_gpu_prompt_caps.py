@@ -73,3 +73,38 @@ def test_scores_of_every_part_of_the_cap(cuda, dtype, d, heads, softcap, size, w
     # products from far below the cap to far above it within a tile
     P.compare(cuda, [600, 131], *heads, d, dtype, seed=43, softcap=softcap, size=size, window=window)
     P.compare(cuda, [300], *heads, d, dtype, seed=44, softcap=softcap, size=size, window=window, scale=-0.3)
+
+
+@pytest.mark.parametrize("dtype,d,heads", FORMS, ids=str)
+@pytest.mark.parametrize("softcap", [1e-30, 1e-20, 1e-12, 1e-8, 1e-4, 1.0])
+def test_products_of_zero_are_scores_of_zero(cuda, dtype, d, heads, softcap):
+    """Padded queries or keys: every key weighs the same, whatever the cap."""
+    q, k, v, d_out = P.inputs(500, *heads, d, dtype, 45)
+    q[100:], k[:50] = 0, 0
+    got = P.run(cuda, q, k, v, P.cu([500]), 500, d_out, softcap=softcap)
+    want = P.attention(q, k, v, d_out, [500], softcap=softcap)
+    rows = torch.arange(500, device="cuda") >= 100
+    # a product of zero has no error, so neither have these rows' scores: p = 1 / n and lse = log n to what sums, exponentials and logarithms round
+    for n in ("out", "lse"):
+        value, bound = want[n]
+        assert P.worst(got[n], value, bound, rows) <= 1, n
+    assert all(torch.isfinite(x).all() for x in got.values())
+
+
+@pytest.mark.parametrize("dtype,d,heads", FORMS, ids=str)
+@pytest.mark.parametrize("softcap", [1.0, 30.0])
+def test_products_whose_squares_overflow(cuda, dtype, d, heads, softcap):
+    # products of 1e20 and more, scores of 1
+    P.compare(cuda, [400], *heads, d, dtype, seed=46, size=1e10, scale=1e-20 * d ** -0.5, softcap=softcap)
+
+
+@pytest.mark.parametrize("dtype,d,heads", FORMS, ids=str)
+@pytest.mark.parametrize("softcap", [0.0, 1e-20, 5.0])
+@pytest.mark.parametrize("scale", [3e38, -3e38])
+def test_products_of_zero_under_the_largest_scale(cuda, dtype, d, heads, softcap, scale):
+    q, k, v, _ = P.inputs(300, *heads, d, dtype, 48)
+    q[:] = 0
+    got = P.run(cuda, q, k, v, P.cu([300]), 300, softcap=softcap, scale=scale)
+    want = P.attention(q, k, v, None, [300])
+    for n, (value, bound) in want.items():
+        assert P.worst(got[n], value, bound, slice(None)) <= 1, n
