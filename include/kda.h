@@ -677,7 +677,8 @@ kda_status kda_paged_attention(const kda_paged_attention_args* a, kda_stream_t s
  * the probabilities are rounded to bf16 for their product with the values.  The same call gives the same bits; with fp32 inputs calls
  * of few rows split their sums, so that the batch around a sequence may change its last bits.
  * `out` overlaps no input.  Rows outside every sequence are neither read into a result nor written.  What a query does not see does not matter to its row,
- * NaN included.
+ * to the last bit, NaN included.  With bf16 inputs finite scores x are within 2^28 in size (fp32 holds them to 16 there); a row with larger
+ * ones may come out as no numbers.
  */
 typedef struct {
   const void* q;             /* [T][Hq][d] in_dtype, tokens q_stride elements apart */
