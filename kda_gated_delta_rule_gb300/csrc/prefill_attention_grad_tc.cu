@@ -274,6 +274,7 @@ __global__ void __launch_bounds__(PG_NT, 1)
       } else if (lane == 0) {
         sh.feed.ask();
       }
+      if (id == 0) pf_check_offsets(a);  // once in a call: whichever CTA walks the unit
       ok = sh.feed.answered(&sh.dead, id);
       if (!ok) break;
       more = id >= 0;
@@ -376,7 +377,6 @@ __global__ void __launch_bounds__(PG_NT, 1)
     // ---- statistics, and rows behind the sequence
     fewer_registers();
     const int t = tid - PG_SOFT - 64;
-    if (blockIdx.x == 0 && t < 32) pf_check_offsets(a);
     TcRing<C::QR> qr;
     TcRing<C::OR> orr;
     TcRing<2> st, un;

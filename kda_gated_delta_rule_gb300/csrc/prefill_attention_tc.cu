@@ -331,6 +331,7 @@ __global__ void __launch_bounds__(PT_NT, 1)
         } else if (lane == 0) {
           sh.feed.ask();
         }
+        if (id == 0) pf_check_offsets(a);  // once in a call: whichever CTA walks the unit
         ok = sh.feed.answered(&sh.dead, id);
         if (!ok) break;
         more = id >= 0;
@@ -438,7 +439,6 @@ __global__ void __launch_bounds__(PT_NT, 1)
       TcRing<2> un;
       TcRing<C::VR> vr;
       bool ok = true;
-      if (blockIdx.x == 0 && warp == 10) pf_check_offsets(a);
       for (;; un.step()) {
         ok = tc_wait(&sh.feed.full[un.at], un.parity, &sh.dead);
         ok = __all_sync(0xffffffffu, ok);
