@@ -542,10 +542,12 @@ __global__ void __launch_bounds__(pf_threads(RI), D == 128 ? 1 : 2)
   if (parts > 1) cluster.sync();
 }
 
-// CTAs for a unit (a cluster), up to `most`: twice as many as long as there are tiles for them and all run within `rounds` fillings of
-// the GPU (shared memory holds one CTA of 128 channels an SM, two of fewer).  Both sides: 408 units of up to 23 tiles 194 -> 144 us with
+// CTAs for a unit (a cluster), up to `most`: twice as many as long as there are tiles for them and all run within `rounds` times 152 CTAs
+// of 128 channels, 304 of fewer.  (Shared memory holds one CTA of 128 channels an SM and two of fewer, but one in the gradients of 64: those
+// run in up to two fillings, which took less than half as many CTAs in one: 509 tokens, 12 heads, forward and gradients 114 us for 159;
+// 2000 tokens, 4 / 2 heads, 360 for 569.)  Both sides: 408 units of up to 23 tiles 194 -> 144 us with
 // two CTAs, 420 of 11 tiles as before; 64 prompts of 512 tokens, 12 heads, 776 -> 963.  Gradients of 36 units of 8 query
-// heads 1062 -> 347 us with four; 420 units 255 -> 305 with two, hence one filling there.
+// heads 1062 -> 347 us with four; 420 units 255 -> 305 with two, hence `rounds` of 1 there.
 inline int parts_of(const PromptAttnArgs& a, int64_t units, int most, int rounds) {
   const int64_t slots = 152 * (a.d == 128 ? 1 : 2);
   int parts = 1;
