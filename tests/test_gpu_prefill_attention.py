@@ -212,6 +212,12 @@ def test_longer_prompts(cuda, dtype, d, heads, window):
     P.compare(cuda, [2500, 1100], *heads, d, dtype, seed=6, window=window)
 
 
+@pytest.mark.parametrize("dtype,d,heads,softcap,window", [(BF, 128, (2, 1), 0.0, 0), (BF, 128, (1, 1), 30.0, 3000), (BF, 64, (3, 3), 30.0, 0),
+                                                          (BF, 16, (2, 1), 0.0, 1000), (F32, 64, (2, 1), 0.0, 0), (F32, 128, (1, 1), 30.0, 3000)])
+def test_prompts_of_thousands_of_tokens(cuda, dtype, d, heads, softcap, window):
+    P.compare(cuda, [9001, 5000], *heads, d, dtype, seed=50, softcap=softcap, window=window)
+
+
 @pytest.mark.parametrize("d", [16, 64, 128])
 @pytest.mark.parametrize("window", [0, 100])
 def test_many_heads_in_fp32(cuda, d, window):
