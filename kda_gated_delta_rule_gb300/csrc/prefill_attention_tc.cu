@@ -16,12 +16,12 @@
 // it, after the products that the scores' barrier already covers.  Probabilities are rounded to bf16 (2^-8) for the second
 // product, half a step like the output's own rounding; their sum is taken before that, in fp32.
 //
-// Measured: 16384 tokens, 32 / 8 heads of 128: 1300 to 1340 us, 1640 to 1690 TFLOP/s of cuBLAS' 1921; 16 prompts of 32771 tokens, 12 / 4 heads:
-// 309 us (1290); window 1024 and cap 30, 16 / 2 heads of 64: 213 to 230 us; one of 137 tokens 12 us.  Bound by the chain of scores,
+// Measured: 16384 tokens, 32 / 8 heads of 128: 1300 to 1410 us by the clocks, 1560 to 1690 TFLOP/s of cuBLAS' 1921; 16 prompts of 32771 tokens, 12 / 4
+// heads: 309 to 317 us (1260 to 1290); window 1024 and cap 30, 16 / 2 heads of 64: 209 to 231 us; one of 137 tokens 11 to 12.  Bound by the chain of scores,
 // softmax, products of each block (the products' pipe 57 to 62 % busy, no other fuller): two blocks per CTA because one alone leaves the pipe
 // idle half the time, a whole row per thread because halves (sixteen warps) took 1432 us for 1425, tiles of 128 keys because 64 take as
 // much of shared memory's bandwidth per product (1756).  Registers are shared out anew among the roles (setmaxnreg): without that 2
-// to 5 % longer.  Heads of 64 halve the products and not the softmax: 897 TFLOP/s without window or cap.
+// to 5 % longer.  Heads of 64 halve the products and not the softmax: 897 to 912 TFLOP/s without window or cap.
 #include "device.h"
 #include "prefill_attention_tc.cuh"
 
@@ -161,7 +161,8 @@ __device__ __forceinline__ void pt_mask(uint32_t own_s, int from, int to, float 
 
 // Capped scores.  Which formula a score takes goes by its own product alone: the short polynomial up to `limit`, beyond it that of
 // pt_cap.  A warp's votes only leave out what none of its scores takes, so that a row's bits do not depend on the other rows (and the
-// next sequence's, which come along at a sequence's end) nor on keys that it does not see.
+// next sequence's, which come along at a sequence's end) nor on keys that it does not see.  Where a warp has both kinds, both are worked out:
+// window 1024, 16 / 2 heads of 64, 24001 tokens 209 us with cap 30, 408 with cap 6, 498 with cap 1 (318 and 402 when the warp chose one for all).
 struct PtCap {
   CapNearer nearer;
   float factor, cap2;  // of a product, to the cap's argument; the cap in powers of two

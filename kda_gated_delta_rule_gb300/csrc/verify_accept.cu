@@ -11,8 +11,8 @@
 //
 // One request per cluster of C CTAs of 8 warps, each warp a contiguous piece of the vocabulary.  It reads one row of p and of q
 // once, for the sums; then the CTA in whose part the threshold falls reads one warp's piece again (from L2) to find the token.
-// Measured: 64 windows of 7 drafts over 150001 tokens 28 us, where reading the rows takes 11 (odd rows: a token a load); 192 of 3 certain drafts over
-// 65536 tokens, bf16, 20 to 24; one of 4 over 32768 tokens 6.3.  Bound by the instructions that make integers of probabilities,
+// Measured: 64 windows of 7 drafts over 150001 tokens 26 to 28 us, where reading the rows takes 11 (odd rows: a token a load); 192 of 3 certain drafts over
+// 65536 tokens, bf16, 20 to 24; one of 4 over 32768 tokens 5.7 to 6.3.  Bound by the instructions that make integers of probabilities,
 // and in small calls by the chain draft, its probabilities, row, the cluster's sums, token.  Clusters because one CTA a
 // request reads a row at its own latency, and partial sums in memory would need a second launch.
 #include <cooperative_groups.h>
