@@ -10,6 +10,7 @@
 //            (over the S^T and V dO^T they come from) of dV += P^T dO and dK += dX^T Q.
 //   queries: 128 queries of a head against the tiles of 128 keys that they see: S = Q K^T, dO V^T, dQ += dX K, with two buffers for
 //            dO V^T (dX in its place), so that the next tile's products run under a tile's arithmetic.
+// A query that sees one key has p = 1 and dx = 0 exactly, whatever p (from the rounded log-sum-exp) and D come out as.
 // D_i from the forward's output carries that output's rounding, d_out . (o rounded - o): against dx's own size it matters in rows that see
 // few keys (over many, o and its rounding shrink with the mean, and what is wrong in D meets the keys' mean).  So before both,
 //   means:   in blocks of queries that walk up to PG_FEW tiles, D_i = sum_j p_ij (do_i . v_j) in fp32, by the queries' kernel without
@@ -451,6 +452,7 @@ __global__ void __launch_bounds__(PG_NT, 1)
         const bool masked = block == u.tile || (block + 1) * PT_B > u.len || (block + 1) * PT_B - u.k0 > window;
         // of the thread's queries the key is seen by from .. to - 1
         const int from = key - row0, to = (int)min((int64_t)u.len, (int64_t)key + window) - row0;
+        const int several = window > 1 ? max(from, 1 - row0) : PG_COLS;  // by a query that sees other keys too (else p = 1 and dx = 0)
         if (++block == u.tile + u.blocks) block = u.tile;
         ok = tc_wait(&sh.st_full[st.at], st.parity, &sh.dead) && tc_wait(&sh.s_full, s_parity, &sh.dead);
         ok = __all_sync(0xffffffffu, ok);
@@ -500,7 +502,7 @@ __global__ void __launch_bounds__(PG_NT, 1)
             for (int e = 0; e < 2; ++e) {
               const float2 md = e == 0 ? make_float2(minus.x, minus.y) : make_float2(minus.z, minus.w);
               float2 ds = mul2(x[j + e], add2(dp[j + e], md));
-              if (decltype(some)::value) ds = only(ds, 2 * (j + e), from, to);
+              if (decltype(some)::value) ds = only(ds, 2 * (j + e), several, to);
               w[j + e] = pack_bf16(ds.x, ds.y);
             }
           }
@@ -770,8 +772,8 @@ __global__ void __launch_bounds__(PG_NT, 1)
       for (int i = 0; i < u.n; ++i, buf.step()) {
         const int k0 = (u.lo + i) * PT_B, first = k0 + part * PG_COLS;
         const bool masked = k0 + PT_B - 1 > u.row0 || k0 <= u.row0 + PT_B - 1 - window;
-        // of the thread's keys the row sees from .. to - 1; a row behind the sequence none
-        const int to = mine ? row + 1 - first : 0, from = row - first >= window ? row - first - window + 1 : 0;
+        // of the thread's keys the row sees from .. to - 1; a row behind the sequence none, nor for dx one that sees a single key
+        const int to = mine && (MEANS || (row > 0 && window > 1)) ? row + 1 - first : 0, from = row - first >= window ? row - first - window + 1 : 0;
         ok = tc_wait_warp(&sh.s_full, s_parity, &sh.dead);
         if (!ok) break;
         s_parity ^= 1;

@@ -46,6 +46,21 @@ def test_scales(cuda, scale, dtype, softcap, window):
     P.compare(cuda, [200], 2, 1, 64, dtype, seed=2, scale=scale, softcap=softcap, window=window)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("d,heads", [(128, (8, 8)), (64, (6, 2)), (16, (12, 1))], ids=str)
+@pytest.mark.parametrize("softcap", [0.0, 5.0])
+def test_a_query_that_sees_one_key_has_no_gradient(cuda, dtype, d, heads, softcap):
+    """A softmax over one key is 1 whatever the scores are: dq and what dk has of such a query are zero, exactly."""
+    for lengths, window in (([1], 0), ([1, 0, 1, 1], 0), ([1], 1000), ([300, 41, 1], 1)):
+        q, k, v, d_out = P.inputs(sum(lengths), *heads, d, dtype, 51, size=3.0)
+        got = P.run(cuda, q, k, v, P.cu(lengths), max(lengths), d_out, softcap=softcap, window=window)
+        assert not got["dq"].any() and not got["dk"].any(), (lengths, window)
+    lengths = [200, 130]
+    q, k, v, d_out = P.inputs(330, *heads, d, dtype, 52)
+    got = P.run(cuda, q, k, v, P.cu(lengths), 200, d_out, softcap=softcap)
+    assert not got["dq"][[0, 200]].any() and got["dq"][[1, 201]].any()
+
+
 @pytest.mark.parametrize("tokens,heads", [(7700, (12, 1)), (4100, (13, 1)), (1000, (34, 2)), (9900, (10, 2))], ids=str)
 def test_shared_heads_dealt_to_several_blocks(cuda, tokens, heads):
     # 5 of 12 heads' parts, 9 of 13, 16 of 17, 1 of 5: uneven shares too
