@@ -389,9 +389,17 @@ __device__ __forceinline__ void tile_grads(const PromptAttnArgs& a, const float2
       const float y = score2(s[i][j], a.scale, a.softcap, slope);
       const float p = seen ? ex2(y - st[i].x) : 0.f;
       if (sp) sp[r * S::PLD + tx + 16 * j] = p;
-      // (a query that sees one key has p = 1 and dx = 0, whatever p and D are rounded to)
-      sds[r * S::PLD + tx + 16 * j] = seen && row > 0 && window > 1 ? p * (dp[i][j] - st[i].y) * slope : 0.f;
+      sds[r * S::PLD + tx + 16 * j] = seen ? p * (dp[i][j] - st[i].y) * slope : 0.f;
     }
+  }
+  // a query that sees one key has p = 1 and dx = 0, whatever p and D are rounded to
+  const int single = window == 1 ? PB : row0 == 0 ? 1 : 0;  // the block's first queries
+  if (single > ty) {
+#pragma unroll
+    for (int i = 0; i < RI; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (ty + PB / RI * i < single) sds[(ty + PB / RI * i) * S::PLD + tx + 16 * j] = 0.f;
   }
 }
 

@@ -10,7 +10,8 @@
 //            (over the S^T and V dO^T they come from) of dV += P^T dO and dK += dX^T Q.
 //   queries: 128 queries of a head against the tiles of 128 keys that they see: S = Q K^T, dO V^T, dQ += dX K, with two buffers for
 //            dO V^T (dX in its place), so that the next tile's products run under a tile's arithmetic.
-// A query that sees one key has p = 1 and dx = 0 exactly, whatever p (from the rounded log-sum-exp) and D come out as.
+// A query that sees one key has p = 1 and dx = 0 exactly, whatever p (from the rounded log-sum-exp) and D come out as: the keys' kernel takes
+// it as a row of zeros with a log-sum-exp of 0, the queries' as one that sees nothing.
 // D_i from the forward's output carries that output's rounding, d_out . (o rounded - o): against dx's own size it matters in rows that see
 // few keys (over many, o and its rounding shrink with the mean, and what is wrong in D meets the keys' mean).  So before both,
 //   means:   in blocks of queries that walk up to PG_FEW tiles, D_i = sum_j p_ij (do_i . v_j) in fp32, by the queries' kernel without
@@ -107,6 +108,16 @@ __device__ __forceinline__ void clear_behind(unsigned char* tile, int rows, int 
   for (int i = t; i < n * (D / 64); i += 64) {
     const int half = i / n;
     *reinterpret_cast<uint4*>(tile + half * PT_HALF + (first + i - half * n) * 16) = make_uint4(0, 0, 0, 0);
+  }
+  tc::fence_proxy_async();
+}
+
+// The first `rows` rows become zeros.
+template <int D>
+__device__ __forceinline__ void clear_first(unsigned char* tile, int rows, int t) {
+  for (int i = t; i < rows * 8 * (D / 64); i += 64) {
+    const int half = i / (rows * 8);
+    *reinterpret_cast<uint4*>(tile + half * PT_HALF + (i - half * rows * 8) * 16) = make_uint4(0, 0, 0, 0);
   }
   tc::fence_proxy_async();
 }
@@ -392,17 +403,19 @@ __global__ void __launch_bounds__(PG_NT, 1)
       if (u.len == 0) break;
       const int n = u.blocks * (u.h1 - u.h0);
       int h = u.h0, block = u.tile;
+      const int single = window == 1 ? 0x7fffffff : 1;  // queries at positions below see one key
       float2 next[2];
       auto fetch = [&]() {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const int row = block * PT_B + t + 64 * r;
           next[r] = row < u.len ? __ldg(stats + (int64_t)h * a.T + u.t0 + row) : make_float2(0.f, 0.f);
+          if (row < single) next[r].x = 0.f;
         }
       };
       fetch();
       for (int i = 0; i < n; ++i) {
-        const int rows = u.len - block * PT_B;  // of the sequence, from the block on
+        const int rows = u.len - block * PT_B, alone = min(PT_B, single - block * PT_B);  // of the sequence, from the block on; that see one key
         ok = tc_wait_warp(&sh.st_empty[st.at], st.parity ^ 1, &sh.dead);
         if (!ok) break;
 #pragma unroll
@@ -415,6 +428,7 @@ __global__ void __launch_bounds__(PG_NT, 1)
         ok = tc_wait_warp(&sh.q_full[qr.at], qr.parity, &sh.dead);
         if (!ok) break;
         if (rows < PT_B) clear_behind<D>(qslots + qr.at * C::SLOT, rows, t);
+        if (alone > 0) clear_first<D>(qslots + qr.at * C::SLOT, alone, t);
         __syncwarp();
         if (lane == 0) tc::bar_arrive(&sh.q_ready[qr.at]);
         qr.step();
@@ -452,7 +466,6 @@ __global__ void __launch_bounds__(PG_NT, 1)
         const bool masked = block == u.tile || (block + 1) * PT_B > u.len || (block + 1) * PT_B - u.k0 > window;
         // of the thread's queries the key is seen by from .. to - 1
         const int from = key - row0, to = (int)min((int64_t)u.len, (int64_t)key + window) - row0;
-        const int several = window > 1 ? max(from, 1 - row0) : PG_COLS;  // by a query that sees other keys too (else p = 1 and dx = 0)
         if (++block == u.tile + u.blocks) block = u.tile;
         ok = tc_wait(&sh.st_full[st.at], st.parity, &sh.dead) && tc_wait(&sh.s_full, s_parity, &sh.dead);
         ok = __all_sync(0xffffffffu, ok);
@@ -502,7 +515,7 @@ __global__ void __launch_bounds__(PG_NT, 1)
             for (int e = 0; e < 2; ++e) {
               const float2 md = e == 0 ? make_float2(minus.x, minus.y) : make_float2(minus.z, minus.w);
               float2 ds = mul2(x[j + e], add2(dp[j + e], md));
-              if (decltype(some)::value) ds = only(ds, 2 * (j + e), several, to);
+              if (decltype(some)::value) ds = only(ds, 2 * (j + e), from, to);
               w[j + e] = pack_bf16(ds.x, ds.y);
             }
           }
@@ -765,7 +778,7 @@ __global__ void __launch_bounds__(PG_NT, 1)
       if (lane == 0) tc::bar_arrive(&sh.feed.empty[un.at]);
       if (u.len == 0) break;
       const int row = u.row0 + (tid & 127);
-      const bool mine = row < u.len;
+      const bool mine = row < u.len, sees = mine && (MEANS || (row > 0 && window > 1));
       const float2 stat = mine ? __ldcg(stats + (int64_t)u.h * a.T + u.t0 + row) : make_float2(0.f, 0.f);
       const float2 minus_lse = both(-stat.x), minus_d = both(-stat.y);
       float2 mean = both(0.f);
@@ -773,7 +786,7 @@ __global__ void __launch_bounds__(PG_NT, 1)
         const int k0 = (u.lo + i) * PT_B, first = k0 + part * PG_COLS;
         const bool masked = k0 + PT_B - 1 > u.row0 || k0 <= u.row0 + PT_B - 1 - window;
         // of the thread's keys the row sees from .. to - 1; a row behind the sequence none, nor for dx one that sees a single key
-        const int to = mine && (MEANS || (row > 0 && window > 1)) ? row + 1 - first : 0, from = row - first >= window ? row - first - window + 1 : 0;
+        const int to = sees ? row + 1 - first : 0, from = row - first >= window ? row - first - window + 1 : 0;
         ok = tc_wait_warp(&sh.s_full, s_parity, &sh.dead);
         if (!ok) break;
         s_parity ^= 1;
