@@ -717,7 +717,8 @@ kda_status kda_prefill_attention(const kda_prefill_attention_args* a, kda_stream
  *   dk_j = sum_i dx_ij q_i,   dk and dv summed over the query heads that share a key/value head.
  * Every sum has one owner and a fixed order: the same call gives the same bits.  Calls of few rows split sums (all with fp32 inputs, dk
  * and dv with bf16), so that the batch around a sequence may change its last bits.  With bf16 inputs p and dx are rounded to bf16
- * for the products that take them in.  The gradients overlap neither inputs nor one another (columns of one buffer may be theirs).
+ * for the products that take them in (dx for dq as two bf16, and both so in sequences of up to 128 tokens).  The gradients overlap
+ * neither inputs nor one another (columns of one buffer may be theirs).
  * Rows outside every sequence are not written.  A token that holds a NaN or an infinity
  * (in q, k, v or d_out) may spread it to all gradients of its own sequence, never to another's.
  */

@@ -22,7 +22,7 @@
 // arithmetic's, thread = row and one of PG_GROUPS parts of the tile's columns; one for the products; one for units and loads (TMA);
 // and two that clear what lies behind the sequence in tiles that are column operands (0 * NaN), and bring the queries' statistics.
 // p and dx are rounded to bf16 (2^-8) for their products, as the results are, but dx for dq, where that rounding left 1.5 times the
-// results' own error: it goes in as two bf16.  Everything else is fp32.
+// results' own error: it goes in as two bf16, as both do in sequences of one block.  Everything else is fp32.
 //
 // Measured (backward alone): 8 documents of 8192 tokens, 32 / 8 heads of 128: 522 us, keys 262, queries 238, means 25, statistics 37 (their starts
 // and ends overlap); 8192 tokens, 12 heads: 593 us and, when it goes on, up to 615, 840 to 870 TFLOP/s of the five products, 1340 to 1390 with those
@@ -182,6 +182,12 @@ struct Yes {
 struct No {
   static constexpr bool value = false;
 };
+
+// Whether p and dx go into dv's and dk's products as two bf16: in sequences of one block.  Few terms average little of a rounding out: dk's
+// error against 64 bits, relative to its size, was 0.0023 to 0.0034 for two tokens, up to twice that of the formula in fp32 rounded once, and
+// 0.0025 for 39, 1.5 times; now it is 0.0017 to 0.0019 in both, as the formula's.  Longer sequences keep 1.4 times; two products more for
+// all would cost them a fifth.  That the kernel can do both costs 655 -> 672 us (forward and gradients, 8 documents).
+__device__ __forceinline__ bool pg_twice(int len) { return len <= PT_B; }
 
 // Block id % PG_FEW of sequence id / PG_FEW.
 __device__ __forceinline__ PfBlock pg_first_block(const PromptAttnArgs& a, int id) {
@@ -351,6 +357,7 @@ __global__ void __launch_bounds__(PG_NT, 1)
       if (lane == 0) tc::bar_arrive(&sh.feed.empty[un.at]);
       __syncwarp();
       if (end == 0) break;
+      const bool twice = pg_twice(end);
       ok = tc_wait_warp(&sh.kv_full, kv_parity, &sh.dead);
       form_s();
       form_dp(n == 1);
@@ -361,6 +368,7 @@ __global__ void __launch_bounds__(PG_NT, 1)
         tc::fence_after_sync();
         if (tc::elect_one()) {
           rows_mma<D>(t_dv, t_s, o_r + o_now.at * STEP, i == 0);
+          if (twice) rows_mma<D>(t_dv, t_s + PG_COLS / 2, o_r + o_now.at * STEP, false);
           tc::commit(&sh.o_empty[o_now.at]);
         }
         o_now.step();
@@ -372,6 +380,7 @@ __global__ void __launch_bounds__(PG_NT, 1)
         tc::fence_after_sync();
         if (tc::elect_one()) {
           rows_mma<D>(t_dk, t_dp, q_r + q_now.at * STEP, i == 0);
+          if (twice) rows_mma<D>(t_dk, t_dp + PG_COLS / 2, q_r + q_now.at * STEP, false);
           tc::commit(&sh.q_empty[q_now.at]);
           if (i + 1 == n) tc::commit(&sh.out_full);
         }
@@ -460,6 +469,7 @@ __global__ void __launch_bounds__(PG_NT, 1)
       if (lane == 0) tc::bar_arrive(&sh.feed.empty[un.at]);
       if (u.len == 0) break;
       const int key = u.k0 + (tid & 127), n = u.blocks * (u.h1 - u.h0);
+      const bool twice = pg_twice(u.len);
       int block = u.tile;
       for (int i = 0; i < n; ++i) {
         const int row0 = block * PT_B + part * PG_COLS;
@@ -478,8 +488,8 @@ __global__ void __launch_bounds__(PG_NT, 1)
         ld_columns(own_s, x);
         if constexpr (CAP) pt_cap(x, factor, cap2);
         // x becomes the probabilities, times the cap's slope
-        auto probabilities = [&](auto some) {
-          uint32_t w[PG_COLS / 2];
+        auto probabilities = [&](auto some, auto two) {
+          uint32_t w[PG_COLS / 2], rest[PG_COLS / 2];
 #pragma unroll
           for (int j = 0; j < PG_COLS / 2; j += 2) {
             const float4 minus = lse[j / 2];
@@ -489,14 +499,17 @@ __global__ void __launch_bounds__(PG_NT, 1)
               float2 p = CAP ? add2(x[j + e], ml) : fma2(x[j + e], both(factor), ml);
               p = make_float2(ex2(p.x), ex2(p.y));
               if (decltype(some)::value) p = only(p, 2 * (j + e), from, to);
-              w[j + e] = pack_bf16(p.x, p.y);
+              if (decltype(two)::value) tc::split_pair(p.x, p.y, w[j + e], rest[j + e]);
+              else w[j + e] = pack_bf16(p.x, p.y);
               x[j + e] = CAP ? mul2(p, cap_slope(x[j + e], over_cap2)) : p;
             }
           }
+          if (decltype(two)::value) tc::tmem_st16(own_s + PG_COLS / 2, rest);
           st_columns(own_s, w);
         };
-        if (masked) probabilities(Yes());
-        else probabilities(No());
+        if (twice) probabilities(Yes(), Yes());
+        else if (masked) probabilities(Yes(), No());
+        else probabilities(No(), No());
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) tc::bar_arrive(&sh.p_full);
@@ -506,8 +519,8 @@ __global__ void __launch_bounds__(PG_NT, 1)
         tc::fence_after_sync();
         float2 dp[PG_COLS / 2];
         ld_columns(own_dp, dp);
-        auto slopes = [&](auto some) {
-          uint32_t w[PG_COLS / 2];
+        auto slopes = [&](auto some, auto two) {
+          uint32_t w[PG_COLS / 2], rest[PG_COLS / 2];
 #pragma unroll
           for (int j = 0; j < PG_COLS / 2; j += 2) {
             const float4 minus = dd[j / 2];
@@ -516,13 +529,16 @@ __global__ void __launch_bounds__(PG_NT, 1)
               const float2 md = e == 0 ? make_float2(minus.x, minus.y) : make_float2(minus.z, minus.w);
               float2 ds = mul2(x[j + e], add2(dp[j + e], md));
               if (decltype(some)::value) ds = only(ds, 2 * (j + e), from, to);
-              w[j + e] = pack_bf16(ds.x, ds.y);
+              if (decltype(two)::value) tc::split_pair(ds.x, ds.y, w[j + e], rest[j + e]);
+              else w[j + e] = pack_bf16(ds.x, ds.y);
             }
           }
+          if (decltype(two)::value) tc::tmem_st16(own_dp + PG_COLS / 2, rest);
           st_columns(own_dp, w);
         };
-        if (masked) slopes(Yes());
-        else slopes(No());
+        if (twice) slopes(Yes(), Yes());
+        else if (masked) slopes(Yes(), No());
+        else slopes(No(), No());
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) tc::bar_arrive(&sh.ds_full), tc::bar_arrive(&sh.st_empty[st.at]);

@@ -61,6 +61,26 @@ def test_a_query_that_sees_one_key_has_no_gradient(cuda, dtype, d, heads, softca
     assert not got["dq"][[0, 200]].any() and got["dq"][[1, 201]].any()
 
 
+@pytest.mark.parametrize("d,heads", [(128, (8, 8)), (64, (12, 1)), (32, (6, 2))], ids=str)
+@pytest.mark.parametrize("softcap", [0.0, 30.0])
+@pytest.mark.parametrize("lengths", [[2], [1, 2], [39], [128], [127, 300, 5]], ids=str)
+def test_gradients_of_short_sequences_keep_their_bits(cuda, d, heads, softcap, lengths):
+    """Sequences of up to 128 tokens, bf16: p and dx as two bf16 are off by 2^-16, the scores' fp32 products by d 2^-24 of their magnitudes (a few,
+    so 2^-14): 2^-12 of the results' size, where one bf16 would leave 2^-9.  Gradients in fp32, so that no rounding of theirs covers it."""
+    q, k, v, d_out = P.inputs(sum(lengths), *heads, d, BF, 53)
+    got = P.run(cuda, q, k, v, P.cu(lengths), max(lengths), d_out, out_type=F32, grad_type=F32, softcap=softcap)
+    want = P.attention(q, k, v, d_out, lengths, softcap=softcap)
+    at = 0
+    for n in lengths:
+        rows = slice(at, at + n)
+        at += n
+        for name in ("dq", "dk", "dv") if n > 1 else ("dv",):
+            value = want[name][0][rows]
+            if n <= 128 or name == "dq":
+                ratio = ((got[name][rows].double() - value).norm() / value.norm()).item()
+                assert ratio <= 2.0 ** -12, (name, n, ratio)
+
+
 @pytest.mark.parametrize("tokens,heads", [(7700, (12, 1)), (4100, (13, 1)), (1000, (34, 2)), (9900, (10, 2))], ids=str)
 def test_shared_heads_dealt_to_several_blocks(cuda, tokens, heads):
     # 5 of 12 heads' parts, 9 of 13, 16 of 17, 1 of 5: uneven shares too
