@@ -185,8 +185,9 @@ struct No {
 
 // Whether p and dx go into dv's and dk's products as two bf16: in sequences of one block.  Few terms average little of a rounding out: dk's
 // error against 64 bits, relative to its size, was 0.0023 to 0.0034 for two tokens, up to twice that of the formula in fp32 rounded once, and
-// 0.0025 for 39, 1.5 times; now it is 0.0017 to 0.0019 in both, as the formula's.  Longer sequences keep 1.4 times; two products more for
-// all would cost them a fifth.  That the kernel can do both costs 655 -> 672 us (forward and gradients, 8 documents).
+// 0.0025 for 39, 1.5 times; now it is 0.0017 to 0.0019 in both, as the formula's.  Longer sequences keep 1.4 times, and four
+// products instead of six.  The roles take such units in loops of their own: where both kinds shared one, its instructions cost the others
+// (forward and gradients, 8 documents: 658 us without, 673 in one loop, 661 so).
 __device__ __forceinline__ bool pg_twice(int len) { return len <= PT_B; }
 
 // Block id % PG_FEW of sequence id / PG_FEW.
@@ -357,36 +358,37 @@ __global__ void __launch_bounds__(PG_NT, 1)
       if (lane == 0) tc::bar_arrive(&sh.feed.empty[un.at]);
       __syncwarp();
       if (end == 0) break;
-      const bool twice = pg_twice(end);
       ok = tc_wait_warp(&sh.kv_full, kv_parity, &sh.dead);
       form_s();
       form_dp(n == 1);
-      for (int i = 0; ok && i < n; ++i) {
-        ok = tc_wait_warp(&sh.p_full, p_parity, &sh.dead);
-        if (!ok) break;
-        p_parity ^= 1;
-        tc::fence_after_sync();
-        if (tc::elect_one()) {
-          rows_mma<D>(t_dv, t_s, o_r + o_now.at * STEP, i == 0);
-          if (twice) rows_mma<D>(t_dv, t_s + PG_COLS / 2, o_r + o_now.at * STEP, false);
-          tc::commit(&sh.o_empty[o_now.at]);
+      auto walk = [&](auto two) {
+        for (int i = 0; ok && i < n; ++i) {
+          ok = tc_wait_warp(&sh.p_full, p_parity, &sh.dead);
+          if (!ok) break;
+          p_parity ^= 1;
+          tc::fence_after_sync();
+          if (tc::elect_one()) {
+            rows_mma<D, decltype(two)::value>(t_dv, t_s, o_r + o_now.at * STEP, i == 0);
+            tc::commit(&sh.o_empty[o_now.at]);
+          }
+          o_now.step();
+          // the next scores go where these probabilities lie: products run in the order of their issue
+          if (i + 1 < n) form_s();
+          ok = ok && tc_wait_warp(&sh.ds_full, ds_parity, &sh.dead);
+          if (!ok) break;
+          ds_parity ^= 1;
+          tc::fence_after_sync();
+          if (tc::elect_one()) {
+            rows_mma<D, decltype(two)::value>(t_dk, t_dp, q_r + q_now.at * STEP, i == 0);
+            tc::commit(&sh.q_empty[q_now.at]);
+            if (i + 1 == n) tc::commit(&sh.out_full);
+          }
+          q_now.step();
+          if (i + 1 < n) form_dp(i + 2 == n);
         }
-        o_now.step();
-        // the next scores go where these probabilities lie: products run in the order of their issue
-        if (i + 1 < n) form_s();
-        ok = ok && tc_wait_warp(&sh.ds_full, ds_parity, &sh.dead);
-        if (!ok) break;
-        ds_parity ^= 1;
-        tc::fence_after_sync();
-        if (tc::elect_one()) {
-          rows_mma<D>(t_dk, t_dp, q_r + q_now.at * STEP, i == 0);
-          if (twice) rows_mma<D>(t_dk, t_dp + PG_COLS / 2, q_r + q_now.at * STEP, false);
-          tc::commit(&sh.q_empty[q_now.at]);
-          if (i + 1 == n) tc::commit(&sh.out_full);
-        }
-        q_now.step();
-        if (i + 1 < n) form_dp(i + 2 == n);
-      }
+      };
+      if (pg_twice(end)) walk(Yes());
+      else walk(No());
       if (!ok) break;
     }
     // nothing of this warp's is on its way when the CTA ends
@@ -469,81 +471,82 @@ __global__ void __launch_bounds__(PG_NT, 1)
       if (lane == 0) tc::bar_arrive(&sh.feed.empty[un.at]);
       if (u.len == 0) break;
       const int key = u.k0 + (tid & 127), n = u.blocks * (u.h1 - u.h0);
-      const bool twice = pg_twice(u.len);
       int block = u.tile;
-      for (int i = 0; i < n; ++i) {
-        const int row0 = block * PT_B + part * PG_COLS;
-        const bool masked = block == u.tile || (block + 1) * PT_B > u.len || (block + 1) * PT_B - u.k0 > window;
-        // of the thread's queries the key is seen by from .. to - 1
-        const int from = key - row0, to = (int)min((int64_t)u.len, (int64_t)key + window) - row0;
-        if (++block == u.tile + u.blocks) block = u.tile;
-        ok = tc_wait(&sh.st_full[st.at], st.parity, &sh.dead) && tc_wait(&sh.s_full, s_parity, &sh.dead);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        s_parity ^= 1;
-        tc::fence_after_sync();
-        float2 x[PG_COLS / 2];
-        const float4* lse = reinterpret_cast<const float4*>(sh.minus_lse[st.at] + part * PG_COLS);
-        const float4* dd = reinterpret_cast<const float4*>(sh.minus_d[st.at] + part * PG_COLS);
-        ld_columns(own_s, x);
-        if constexpr (CAP) pt_cap(x, factor, cap2);
-        // x becomes the probabilities, times the cap's slope
-        auto probabilities = [&](auto some, auto two) {
-          uint32_t w[PG_COLS / 2], rest[PG_COLS / 2];
+      auto rounds = [&](auto two) {
+        for (int i = 0; i < n; ++i) {
+          const int row0 = block * PT_B + part * PG_COLS;
+          const bool masked = block == u.tile || (block + 1) * PT_B > u.len || (block + 1) * PT_B - u.k0 > window;
+          // of the thread's queries the key is seen by from .. to - 1
+          const int from = key - row0, to = (int)min((int64_t)u.len, (int64_t)key + window) - row0;
+          if (++block == u.tile + u.blocks) block = u.tile;
+          ok = tc_wait(&sh.st_full[st.at], st.parity, &sh.dead) && tc_wait(&sh.s_full, s_parity, &sh.dead);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          s_parity ^= 1;
+          tc::fence_after_sync();
+          float2 x[PG_COLS / 2];
+          const float4* lse = reinterpret_cast<const float4*>(sh.minus_lse[st.at] + part * PG_COLS);
+          const float4* dd = reinterpret_cast<const float4*>(sh.minus_d[st.at] + part * PG_COLS);
+          ld_columns(own_s, x);
+          if constexpr (CAP) pt_cap(x, factor, cap2);
+          // x becomes the probabilities, times the cap's slope
+          auto probabilities = [&](auto some) {
+            uint32_t w[PG_COLS / 2], rest[PG_COLS / 2];
 #pragma unroll
-          for (int j = 0; j < PG_COLS / 2; j += 2) {
-            const float4 minus = lse[j / 2];
+            for (int j = 0; j < PG_COLS / 2; j += 2) {
+              const float4 minus = lse[j / 2];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float2 ml = e == 0 ? make_float2(minus.x, minus.y) : make_float2(minus.z, minus.w);
-              float2 p = CAP ? add2(x[j + e], ml) : fma2(x[j + e], both(factor), ml);
-              p = make_float2(ex2(p.x), ex2(p.y));
-              if (decltype(some)::value) p = only(p, 2 * (j + e), from, to);
-              if (decltype(two)::value) tc::split_pair(p.x, p.y, w[j + e], rest[j + e]);
-              else w[j + e] = pack_bf16(p.x, p.y);
-              x[j + e] = CAP ? mul2(p, cap_slope(x[j + e], over_cap2)) : p;
+              for (int e = 0; e < 2; ++e) {
+                const float2 ml = e == 0 ? make_float2(minus.x, minus.y) : make_float2(minus.z, minus.w);
+                float2 p = CAP ? add2(x[j + e], ml) : fma2(x[j + e], both(factor), ml);
+                p = make_float2(ex2(p.x), ex2(p.y));
+                if (decltype(some)::value) p = only(p, 2 * (j + e), from, to);
+                if (decltype(two)::value) tc::split_pair(p.x, p.y, w[j + e], rest[j + e]);
+                else w[j + e] = pack_bf16(p.x, p.y);
+                x[j + e] = CAP ? mul2(p, cap_slope(x[j + e], over_cap2)) : p;
+              }
             }
-          }
-          if (decltype(two)::value) tc::tmem_st16(own_s + PG_COLS / 2, rest);
-          st_columns(own_s, w);
-        };
-        if (twice) probabilities(Yes(), Yes());
-        else if (masked) probabilities(Yes(), No());
-        else probabilities(No(), No());
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) tc::bar_arrive(&sh.p_full);
-        ok = tc_wait_warp(&sh.dp_full, dp_parity, &sh.dead);
-        if (!ok) break;
-        dp_parity ^= 1;
-        tc::fence_after_sync();
-        float2 dp[PG_COLS / 2];
-        ld_columns(own_dp, dp);
-        auto slopes = [&](auto some, auto two) {
-          uint32_t w[PG_COLS / 2], rest[PG_COLS / 2];
+            if (decltype(two)::value) tc::tmem_st16(own_s + PG_COLS / 2, rest);
+            st_columns(own_s, w);
+          };
+          if (decltype(two)::value || masked) probabilities(Yes());
+          else probabilities(No());
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) tc::bar_arrive(&sh.p_full);
+          ok = tc_wait_warp(&sh.dp_full, dp_parity, &sh.dead);
+          if (!ok) break;
+          dp_parity ^= 1;
+          tc::fence_after_sync();
+          float2 dp[PG_COLS / 2];
+          ld_columns(own_dp, dp);
+          auto slopes = [&](auto some) {
+            uint32_t w[PG_COLS / 2], rest[PG_COLS / 2];
 #pragma unroll
-          for (int j = 0; j < PG_COLS / 2; j += 2) {
-            const float4 minus = dd[j / 2];
+            for (int j = 0; j < PG_COLS / 2; j += 2) {
+              const float4 minus = dd[j / 2];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float2 md = e == 0 ? make_float2(minus.x, minus.y) : make_float2(minus.z, minus.w);
-              float2 ds = mul2(x[j + e], add2(dp[j + e], md));
-              if (decltype(some)::value) ds = only(ds, 2 * (j + e), from, to);
-              if (decltype(two)::value) tc::split_pair(ds.x, ds.y, w[j + e], rest[j + e]);
-              else w[j + e] = pack_bf16(ds.x, ds.y);
+              for (int e = 0; e < 2; ++e) {
+                const float2 md = e == 0 ? make_float2(minus.x, minus.y) : make_float2(minus.z, minus.w);
+                float2 ds = mul2(x[j + e], add2(dp[j + e], md));
+                if (decltype(some)::value) ds = only(ds, 2 * (j + e), from, to);
+                if (decltype(two)::value) tc::split_pair(ds.x, ds.y, w[j + e], rest[j + e]);
+                else w[j + e] = pack_bf16(ds.x, ds.y);
+              }
             }
-          }
-          if (decltype(two)::value) tc::tmem_st16(own_dp + PG_COLS / 2, rest);
-          st_columns(own_dp, w);
-        };
-        if (twice) slopes(Yes(), Yes());
-        else if (masked) slopes(Yes(), No());
-        else slopes(No(), No());
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) tc::bar_arrive(&sh.ds_full), tc::bar_arrive(&sh.st_empty[st.at]);
-        st.step();
-      }
+            if (decltype(two)::value) tc::tmem_st16(own_dp + PG_COLS / 2, rest);
+            st_columns(own_dp, w);
+          };
+          if (decltype(two)::value || masked) slopes(Yes());
+          else slopes(No());
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) tc::bar_arrive(&sh.ds_full), tc::bar_arrive(&sh.st_empty[st.at]);
+          st.step();
+        }
+      };
+      if (pg_twice(u.len)) rounds(Yes());
+      else rounds(No());
       if (!ok) break;
       ok = tc_wait_warp(&sh.out_full, out_parity, &sh.dead);
       if (!ok) break;
