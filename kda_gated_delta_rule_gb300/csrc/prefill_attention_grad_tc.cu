@@ -27,7 +27,7 @@
 // Measured (backward alone): 8 documents of 8192 tokens, 32 / 8 heads of 128: 522 to 542 us, keys some 262, queries 238, means 25, statistics 37 (their
 // starts and ends overlap); 8192 tokens, 12 heads: 591 us and, when it goes on, up to 626, 820 to 870 TFLOP/s of the five products, 1310 to 1390
 // with those formed twice.  Bound by
-// the chain of products and arithmetic, and by shared memory's bandwidth: 61 % of the products' pipe, in the keys' kernel 81 % of
+// the chain of products and arithmetic, and by shared memory's bandwidth: 61 % of the products' pipe, in the keys' kernel 79 % of
 // shared memory's, half of that the queries' statistics that all threads read.  Handing those to the products instead, as
 // six more channels, came out the same (522 -> 520 us), so they stay here.
 #include "device.h"
